@@ -429,6 +429,165 @@ TP_API tp_status tp_combine(tp_combine_mode mode, const void* const* partials, i
                      void* out, tp_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* 8-bit projections                                                         */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The block-scaled 8-bit format of the calls below: e4m3 codes (1 byte) with
+ * one power-of-two scale per group of 128, held as an e8m0 byte (scale =
+ * 2^(byte - 127), 255 = NaN).  An activation's groups are 128 consecutive
+ * features of one token: scales [T, ceil(K/128)].  A weight's groups are its
+ * 128 x 128 blocks: scales [ceil(rows/128), ceil(K/128)].  The last group of a
+ * row or column may be shorter.  The pages have no counterpart of these calls:
+ * they load and run the model in bf16; here the same shards, projections and
+ * joins run with half the weight bytes and twice the tensor-core rate.
+ *
+ * A weight is quantised shard by shard (after tp_plan_shard), so that a
+ * shard's blocks start at its own first row and column.
+ */
+
+/*
+ * tp_quantize_fp8 -- codes and scales of a bf16 matrix:
+ *     e = ceil(log2(max|x| / 448)) over a group, clamped to [-127, 127]
+ *         (0 for a group of zeros),  scale byte = e + 127,
+ *     q = e4m3(x / 2^e), rounded once, to nearest even.
+ * A group that holds a NaN or an infinity becomes NaN: byte 255 and NaN codes.
+ *
+ * x:      device bf16 [rows, cols], row stride ldx elements (0 = cols).
+ * block_rows: 1 (groups of 128 features of one row: activations) or 128
+ *         (128 x 128 blocks: weights).
+ * q:      device e4m3 [rows, cols], row stride ldq (0 = cols).
+ * scales: device e8m0 [ceil(rows/block_rows), ceil(cols/128)], row stride lds
+ *         (0 = dense).  Any alignment; 4-byte aligned rows are read faster by
+ *         the projections.
+ * Alignment (TP_ERR_ALIGNMENT): cols % 16 == 0, ldx % 8 == 0, ldq % 16 == 0,
+ * x and q 16-byte aligned.  q and scales must not overlap x.
+ * rows == 0 or cols == 0 enqueues nothing and returns TP_OK.
+ */
+TP_API tp_status tp_quantize_fp8(const void* x, int64_t ldx, int64_t rows, int64_t cols, int block_rows, void* q,
+                                 int64_t ldq, void* scales, int64_t lds, tp_stream_t stream);
+
+/*
+ * tp_linear_colwise_fp8 -- tp_linear_colwise on the 8-bit format, every rank
+ * in one launch:  Y_r = act(X . W_r^T + b_r), X and W_r the values their codes
+ * and scales stand for.
+ *
+ * x, x_scales: device e4m3 [T, K] with row stride ldx (0 = K) and e8m0
+ *              [T, ceil(K/128)] with row stride ld_xs (0 = dense), shared by
+ *              every rank.
+ * w_shards, w_scales: host arrays of tp_degree device pointers, each e4m3
+ *              [N_r, K] and e8m0 [ceil(N_r/128), ceil(K/128)], dense.
+ * bias_shards: NULL, or host array of tp_degree device pointers (each NULL or
+ *              bf16 [N_r]).
+ * act:         as tp_linear_colwise (SwiGLU shards are [gate_r; up_r]; N_r/2
+ *              need not be a multiple of 128), applied to the fp32 sum.
+ * y_shards:    host array of tp_degree device pointers, row stride ldy
+ *              elements (0 = N_out).  With y_scales NULL each is bf16
+ *              [T, N_out] (and the gathered layout of tp_linear_colwise works).
+ * y_scales:    NULL, or host array of tp_degree device pointers: Y_r then
+ *              leaves as e4m3 [T, N_out] with e8m0 [T, ceil(N_out/128)] (row
+ *              stride ld_ys, 0 = dense), quantised from the unrounded fp32
+ *              values as tp_quantize_fp8 does with block_rows 1 -- the input
+ *              tp_linear_rowwise_fp8 takes.
+ * The sum over K is one fp32 accumulator of the tensor core, scales applied
+ * inside; with few tokens K may be split over up to 8 accumulators that are
+ * added in fp32 in K order.  The same call gives the same bits every time.
+ * Alignment (TP_ERR_ALIGNMENT): K and ldx % 16 == 0; N_out and ldy % 8 == 0
+ * (% 16 with y_scales); x, w_shards, y_shards 16-byte aligned.
+ * T == 0 or N_r == 0 enqueues nothing and returns TP_OK.  No output may overlap an input.
+ */
+TP_API tp_status tp_linear_colwise_fp8(const void* x, int64_t ldx, const void* x_scales, int64_t ld_xs,
+                                       const void* const* w_shards, const void* const* w_scales,
+                                       const void* const* bias_shards, tp_act act, int tp_degree, int64_t T, int64_t K,
+                                       int64_t N_r, void* const* y_shards, int64_t ldy, void* const* y_scales,
+                                       int64_t ld_ys, tp_stream_t stream);
+
+/*
+ * tp_linear_rowwise_fp8 -- tp_linear_rowwise (its on-chip sum) on the 8-bit
+ * format:  Z = sum_r X_r . W_r^T (+ bias, once), in rank order, in fp32.
+ *
+ * x_shards, x_scales: host arrays of tp_degree device pointers, each e4m3
+ *         [T, K_r] with row stride ldx (0 = K_r) and e8m0 [T, ceil(K_r/128)]
+ *         with row stride ld_xs (0 = dense) -- what tp_linear_colwise_fp8
+ *         writes with y_scales.  A replicated input [T, p*K_r] is passed as p
+ *         pointers into it (with K_r % 128 == 0, so that no group is shared).
+ * w_shards, w_scales: host arrays of tp_degree device pointers, each e4m3
+ *         [N, K_r] and e8m0 [ceil(N/128), ceil(K_r/128)], dense.
+ * bias:   NULL or device bf16 [N]; added once, after the sum.
+ * out:    device bf16 [T, N], row stride ldo elements (0 = N).
+ * Alignment (TP_ERR_ALIGNMENT): K_r and ldx % 16 == 0, N and ldo % 8 == 0,
+ * x_shards, w_shards and out 16-byte aligned.  Accumulation as tp_linear_colwise_fp8.
+ * T == 0 or N == 0 enqueues nothing and returns TP_OK.  No output may overlap an input.
+ */
+TP_API tp_status tp_linear_rowwise_fp8(const void* const* x_shards, int64_t ldx, const void* const* x_scales,
+                                       int64_t ld_xs, const void* const* w_shards, const void* const* w_scales,
+                                       const void* bias, int tp_degree, int64_t T, int64_t K_r, int64_t N, void* out,
+                                       int64_t ldo, tp_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Between sharded blocks                                                    */
+/* ------------------------------------------------------------------------ */
+
+typedef enum { TP_NORM_NONE = 0, TP_NORM_RMS = 1, TP_NORM_LAYER = 2 } tp_norm;
+
+#define TP_NORM_MAX_D 32768 /* widest row tp_residual_norm accepts */
+
+/*
+ * tp_residual_norm -- what stands between one sharded block and the next,
+ * each row read once:
+ *     h = alpha * x + gate * post_norm(y)          (the residual stream)
+ *     u = norm(h) * (1 + scale) + shift            (the next block's input)
+ * Norms and modulations are replicated modules of the model, outside the
+ * sharding plan ("Tensor parallelism" page, §What to leave out): every rank
+ * computes the same rows, so one call serves them all.
+ *
+ *     rms(v)   = v / sqrt(mean(v^2) + eps) * weight + bias
+ *     layer(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias
+ * (weight and bias optional), over the D elements of a row.  Everything is
+ * fp32 until an output is stored; u is computed from the unrounded h.
+ *
+ * Without a branch (y NULL; h, gate and post_norm unset) u = norm(alpha * x) *
+ * (1 + scale) + shift.  Without u (u NULL; norm, scale, shift and u_scales
+ * unset) only h is written.  h may be x itself with the same row stride (the
+ * residual updated in place); no other overlap of an output with an input.
+ *
+ * gate, scale and shift (each optional) are [mod_rows, D] tables with the row
+ * stride ld_mod: row t of the call uses table row t / rows_per_mod.
+ * mod_rows = 1 with rows_per_mod = T is one vector for every row;
+ * rows_per_mod = 1 is a row per token.
+ * u_scales set: u is e4m3 with e8m0 scales [T, ceil(D/128)], quantised from
+ * the unrounded fp32 values as tp_quantize_fp8 does with block_rows 1.
+ * Row strides of 0 mean dense rows.
+ * Errors: TP_ERR_INVALID_ARG for sizes, strides and combinations outside the
+ * above (and mod_rows * rows_per_mod < T); TP_ERR_ALIGNMENT unless D and every
+ * row stride are multiples of 8 (D and ldu of 16 with u_scales) and every
+ * pointer but u_scales is 16-byte aligned; TP_ERR_UNSUPPORTED above
+ * TP_NORM_MAX_D.  T == 0 or D == 0 enqueues nothing and returns TP_OK.
+ */
+typedef struct {
+  int64_t T, D;
+  const void* x;            /* bf16 [T, D] */
+  int64_t ldx;
+  const void* y;            /* NULL, or bf16 [T, D]: the block's output */
+  int64_t ldy;
+  tp_norm post_norm;
+  const void *post_weight, *post_bias; /* NULL, or bf16 [D] */
+  float alpha;
+  float eps;                /* of both norms */
+  const void *gate, *scale, *shift;    /* NULL, or bf16 [mod_rows, D] */
+  int64_t ld_mod, mod_rows, rows_per_mod;
+  void* h;                  /* NULL, or bf16 [T, D] */
+  int64_t ldh;
+  tp_norm norm;
+  const void *weight, *bias;           /* NULL, or bf16 [D] */
+  void* u;                  /* NULL, or bf16 [T, D] (e4m3 with u_scales) */
+  int64_t ldu;
+  void* u_scales;           /* NULL, or e8m0 [T, ceil(D/128)] */
+  int64_t ld_u_scales;
+} tp_residual_norm_args;
+TP_API tp_status tp_residual_norm(const tp_residual_norm_args* args, tp_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics                                                               */
 /* ------------------------------------------------------------------------ */
 

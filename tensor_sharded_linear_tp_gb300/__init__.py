@@ -40,6 +40,9 @@ ACTS = {"none": 0, "gelu_tanh": 1, "swiglu": 2}
 ACCUM_CHUNKED = 0x100   # TP_ACCUM_CHUNKED (include/tp.h): OR'd into the colwise act argument
 REDUCE_MODES = {"none": 0, "workspace": 1, "accum": 2}
 COMBINE_MODES = {"gather": 0, "reduce": 1}
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+FP8_GROUP = 128         # features (or weight rows) that share a scale
+NORM_MAX_D = 32768      # TP_NORM_MAX_D
 MAX_DEGREE = 16
 MAX_SPLITS = 16
 
@@ -67,6 +70,12 @@ _SIGS = {
                                            _vp, ctypes.c_size_t, ctypes.POINTER(_vp), _i64, _vp]),
     "tp_attention_ranks_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, _i64, ctypes.c_int, ctypes.c_int]),
     "tp_combine": (_status, [ctypes.c_int, ctypes.POINTER(_vp), ctypes.c_int, _i64, _i64, _vp, _vp]),
+    "tp_quantize_fp8": (_status, [_vp, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _i64, _vp]),
+    "tp_linear_colwise_fp8": (_status, [_vp, _i64, _vp, _i64, ctypes.POINTER(_vp), ctypes.POINTER(_vp),
+                                        ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, _i64, _i64, _i64,
+                                        ctypes.POINTER(_vp), _i64, ctypes.POINTER(_vp), _i64, _vp]),
+    "tp_linear_rowwise_fp8": (_status, [ctypes.POINTER(_vp), _i64, ctypes.POINTER(_vp), _i64, ctypes.POINTER(_vp),
+                                        ctypes.POINTER(_vp), _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp]),
     "tp_last_error": (ctypes.c_char_p, []),
     "tp_status_name": (ctypes.c_char_p, [ctypes.c_int]),
     "tp_device_status": (_status, [_vp]),
@@ -95,7 +104,17 @@ class ShardRequest(ctypes.Structure):
                 ("dev_outs", ctypes.POINTER(_vp))]
 
 
+class ResidualNormArgs(ctypes.Structure):
+    """Mirror of tp_residual_norm_args (include/tp.h)."""
+    _fields_ = [("T", _i64), ("D", _i64), ("x", _vp), ("ldx", _i64), ("y", _vp), ("ldy", _i64),
+                ("post_norm", ctypes.c_int), ("post_weight", _vp), ("post_bias", _vp), ("alpha", ctypes.c_float),
+                ("eps", ctypes.c_float), ("gate", _vp), ("scale", _vp), ("shift", _vp), ("ld_mod", _i64),
+                ("mod_rows", _i64), ("rows_per_mod", _i64), ("h", _vp), ("ldh", _i64), ("norm", ctypes.c_int),
+                ("weight", _vp), ("bias", _vp), ("u", _vp), ("ldu", _i64), ("u_scales", _vp), ("ld_u_scales", _i64)]
+
+
 _SIGS["tp_plan_shard_many"] = (_status, [ctypes.POINTER(ShardRequest), ctypes.c_int, _vp])
+_SIGS["tp_residual_norm"] = (_status, [ctypes.POINTER(ResidualNormArgs), _vp])
 
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -436,6 +455,252 @@ def tp_combine(mode: str, partials: Sequence[torch.Tensor], out: torch.Tensor | 
         out = torch.empty((T, cols), dtype=torch.bfloat16, device=partials[0].device)
     _check(lib.tp_combine(COMBINE_MODES[mode], _ptrs(partials), p, T, N_each, _ptr(out), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# 8-bit projections and the residual norm
+#
+# The block-scaled format (include/tp.h): float8_e4m3fn codes with one power-of-two scale per
+# group of 128, a float8_e8m0fnu (or uint8) byte.  These calls check every tensor's type, shape,
+# strides and device before the library is called, so a refused call touches no device memory.
+# ---------------------------------------------------------------------------
+
+_E4M3, _E8M0, _BF16 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.bfloat16
+
+
+def _groups(n: int) -> int:
+    return -(-n // FP8_GROUP)
+
+
+def _need(name, t, dtype, shape, device=None):
+    """A tensor of `dtype` (a scale: e8m0 or uint8) and `shape` on the current GPU, its last dimension contiguous.
+
+    Returns the row stride (0 for a single row, whose stride means nothing)."""
+    if t.dtype is not dtype and not (dtype is _E8M0 and t.dtype is torch.uint8):
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != (torch.cuda.current_device() if device is None else device):
+        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+    if t.dim() == 1:
+        if t.numel() > 1 and t.stride(0) != 1:
+            raise ValueError(f"{name} must be contiguous")
+        return 0
+    rows, cols = shape
+    step, inner = t.stride()
+    if cols > 1 and inner != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        return 0
+    if step < cols:
+        raise ValueError(f"{name}: a row stride of {step} overlaps rows of {cols} elements")
+    return step
+
+
+def _one_stride(name, strides, cols, rows):
+    """The row stride every rank's tensor shares (a single row's is taken as dense)."""
+    first = strides[0]
+    for s in strides:
+        if s != first:
+            raise ValueError(f"every rank's {name} must have the same row stride")
+    return first if rows > 1 else 0
+
+
+def _alloc(stream, dev, dtype, *shapes):
+    """Outputs for a call on `stream`, from that stream's memory."""
+    def make():
+        if dtype is _E8M0:
+            return [torch.empty(s, dtype=torch.uint8, device=dev).view(_E8M0) for s in shapes]
+        return [torch.empty(s, dtype=dtype, device=dev) for s in shapes]
+    if stream is None:
+        return make()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _launch_stream(stream, dev) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _device_of(name, t) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a tensor on the current CUDA device")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
+    return t.get_device()
+
+
+def _same_count(p, **lists):
+    for name, ts in lists.items():
+        if ts is not None and len(ts) != p:
+            raise ValueError(f"{name} must have one entry for each of the {p} ranks, got {len(ts)}")
+
+
+def tp_quantize_fp8(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | None = None,
+                    scales: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(codes, scales) of a bf16 [rows, cols]: groups of 1 x 128 (activations) or 128 x 128 (weights)."""
+    dev = _device_of("x", x)
+    if block_rows not in (1, FP8_GROUP):
+        raise ValueError(f"block_rows must be 1 or {FP8_GROUP}, got {block_rows}")
+    rows, cols = x.shape
+    ldx = _need("x", x, _BF16, (rows, cols), dev)
+    s_shape = (-(-rows // block_rows), _groups(cols))
+    if q is None:
+        q, = _alloc(stream, dev, _E4M3, (rows, cols))
+    if scales is None:
+        scales, = _alloc(stream, dev, _E8M0, s_shape)
+    ldq, lds = _need("q", q, _E4M3, (rows, cols), dev), _need("scales", scales, _E8M0, s_shape, dev)
+    _check(lib.tp_quantize_fp8(x.data_ptr(), ldx, rows, cols, block_rows, q.data_ptr(), ldq, scales.data_ptr(), lds,
+                               _launch_stream(stream, dev)))
+    return q, scales
+
+
+def _fp8_weights(w_shards, w_scales, K, dev):
+    N = w_shards[0].shape[0]
+    s_shape = (_groups(N), _groups(K))
+    for i, (w, s) in enumerate(zip(w_shards, w_scales)):
+        if _need(f"w_shards[{i}]", w, _E4M3, (N, K), dev) not in (0, K):
+            raise ValueError(f"w_shards[{i}] must be contiguous")
+        if _need(f"w_scales[{i}]", s, _E8M0, s_shape, dev) not in (0, s_shape[1]):
+            raise ValueError(f"w_scales[{i}] must be contiguous")
+    return N
+
+
+def tp_linear_colwise_fp8(x: torch.Tensor, x_scales: torch.Tensor, w_shards: Sequence[torch.Tensor],
+                          w_scales: Sequence[torch.Tensor], act: str = "none",
+                          bias_shards: Sequence[torch.Tensor | None] | None = None, out: str = "bf16",
+                          y_shards: Sequence[torch.Tensor] | None = None,
+                          y_scales: Sequence[torch.Tensor] | None = None, stream=None):
+    """Y_r = act(X W_r^T + b_r) for every rank r on the 8-bit format, one launch.
+
+    x and x_scales as tp_quantize_fp8 writes them (block_rows 1), each w_shards[r] and
+    w_scales[r] with block_rows 128.  out="bf16" returns the list of Y_r; out="fp8" returns
+    (codes, scales), two lists, ready for tp_linear_rowwise_fp8."""
+    dev = _device_of("x", x)
+    if out not in ("bf16", "fp8"):
+        raise ValueError(f'out must be "bf16" or "fp8", got {out!r}')
+    p = len(w_shards)
+    if p < 1:
+        raise ValueError("w_shards is empty")
+    _same_count(p, w_scales=w_scales, bias_shards=bias_shards, y_shards=y_shards, y_scales=y_scales)
+    T, K = x.shape
+    ldx = _need("x", x, _E4M3, (T, K), dev)
+    ld_xs = _need("x_scales", x_scales, _E8M0, (T, _groups(K)), dev)
+    N = _fp8_weights(w_shards, w_scales, K, dev)
+    if bias_shards is not None:
+        for i, b in enumerate(bias_shards):
+            if b is not None:
+                _need(f"bias_shards[{i}]", b, _BF16, (N,), dev)
+    n = N // 2 if act == "swiglu" else N
+    fp8 = out == "fp8"
+    if not fp8 and y_scales is not None:
+        raise ValueError('y_scales belongs to out="fp8"')
+    y_type, s_shape = (_E4M3 if fp8 else _BF16), (T, _groups(n))
+    if y_shards is None:
+        y_shards = _alloc(stream, dev, y_type, *[(T, n)] * p)
+    if fp8 and y_scales is None:
+        y_scales = _alloc(stream, dev, _E8M0, *[s_shape] * p)
+    ldy = _one_stride("output", [_need("y_shards[r]", y, y_type, (T, n), dev) for y in y_shards], n, T)
+    ld_ys = _one_stride("output scales", [_need("y_scales[r]", s, _E8M0, s_shape, dev) for s in y_scales], s_shape[1],
+                        T) if fp8 else 0
+    _check(lib.tp_linear_colwise_fp8(x.data_ptr(), ldx, x_scales.data_ptr(), ld_xs, _ptrs(w_shards), _ptrs(w_scales),
+                                     _ptrs(bias_shards) if bias_shards is not None else None, ACTS[act], p, T, K, N,
+                                     _ptrs(y_shards), ldy, _ptrs(y_scales) if fp8 else None, ld_ys,
+                                     _launch_stream(stream, dev)))
+    return (list(y_shards), list(y_scales)) if fp8 else list(y_shards)
+
+
+def tp_linear_rowwise_fp8(x_shards: Sequence[torch.Tensor], x_scales: Sequence[torch.Tensor],
+                          w_shards: Sequence[torch.Tensor], w_scales: Sequence[torch.Tensor],
+                          bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """Z = sum_r X_r W_r^T (+ bias once) on the 8-bit format, one launch; bf16 [T, N]."""
+    p = len(w_shards)
+    if p < 1:
+        raise ValueError("w_shards is empty")
+    _same_count(p, w_scales=w_scales, x_shards=x_shards, x_scales=x_scales)
+    dev = _device_of("x_shards[0]", x_shards[0])
+    T, K = x_shards[0].shape
+    N = _fp8_weights(w_shards, w_scales, K, dev)
+    s_shape = (T, _groups(K))
+    ldx = _one_stride("input", [_need("x_shards[r]", x, _E4M3, (T, K), dev) for x in x_shards], K, T)
+    ld_xs = _one_stride("input scales", [_need("x_scales[r]", s, _E8M0, s_shape, dev) for s in x_scales], s_shape[1], T)
+    if bias is not None:
+        _need("bias", bias, _BF16, (N,), dev)
+    if out is None:
+        out, = _alloc(stream, dev, _BF16, (T, N))
+    ldo = _need("out", out, _BF16, (T, N), dev)
+    _check(lib.tp_linear_rowwise_fp8(_ptrs(x_shards), ldx, _ptrs(x_scales), ld_xs, _ptrs(w_shards), _ptrs(w_scales),
+                                     bias.data_ptr() if bias is not None else None, p, T, K, N, out.data_ptr(), ldo,
+                                     _launch_stream(stream, dev)))
+    return out
+
+
+def tp_residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, norm: str = "rms",
+                     weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                     scale: torch.Tensor | None = None, shift: torch.Tensor | None = None, post_norm: str = "none",
+                     post_weight: torch.Tensor | None = None, post_bias: torch.Tensor | None = None,
+                     gate: torch.Tensor | None = None, alpha: float = 1.0, eps: float = 1e-6,
+                     rows_per_mod: int | None = None, out: str | None = "bf16", h: torch.Tensor | None = None,
+                     u: torch.Tensor | None = None, u_scales: torch.Tensor | None = None, stream=None):
+    """h = alpha x + gate post_norm(y); u = norm(h) (1 + scale) + shift.  Returns (h, u, u_scales).
+
+    gate, scale and shift are [D] vectors or [mod_rows, D] tables (row t uses table row
+    t // rows_per_mod; default: one row for every row of x).  out: "bf16" or "fp8" (codes and
+    scales), or None for h alone; what a call does not compute is returned as None.  Without a
+    branch y there is no h."""
+    dev = _device_of("x", x)
+    if out not in ("bf16", "fp8", None):
+        raise ValueError(f'out must be "bf16", "fp8" or None, got {out!r}')
+    T, D = x.shape
+    a = ResidualNormArgs()
+    a.T, a.D, a.alpha, a.eps = T, D, alpha, eps
+    a.x, a.ldx = x.data_ptr(), _need("x", x, _BF16, (T, D), dev)
+    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight), ("post_bias", post_bias)):
+        if t is not None:
+            _need(name, t, _BF16, (D,), dev)
+            setattr(a, name, t.data_ptr())
+    a.post_norm = NORMS[post_norm]
+    ld_mod, mod_rows = None, None
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is not None:
+            rows = 1 if t.dim() == 1 else t.shape[0]
+            step = _need(name, t, _BF16, (D,) if t.dim() == 1 else (rows, D), dev)
+            if mod_rows is None:
+                ld_mod, mod_rows = step, rows
+            elif mod_rows != rows or ld_mod != step:
+                raise ValueError("gate, scale and shift must have the same rows and row stride")
+            setattr(a, name, t.data_ptr())
+    if mod_rows is not None:
+        a.ld_mod, a.mod_rows = ld_mod, mod_rows
+        a.rows_per_mod = max(T, 1) if rows_per_mod is None else rows_per_mod
+    if y is not None:
+        a.y, a.ldy = y.data_ptr(), _need("y", y, _BF16, (T, D), dev)
+        if h is None:
+            h, = _alloc(stream, dev, _BF16, (T, D))
+    if h is not None:
+        a.h, a.ldh = h.data_ptr(), _need("h", h, _BF16, (T, D), dev)
+    if out is None:
+        if u is not None or u_scales is not None:
+            raise ValueError("u and u_scales belong to an output type")
+    else:
+        a.norm = NORMS[norm]
+        u_type = _E4M3 if out == "fp8" else _BF16
+        if u is None:
+            u, = _alloc(stream, dev, u_type, (T, D))
+        a.u, a.ldu = u.data_ptr(), _need("u", u, u_type, (T, D), dev)
+        if out == "fp8":
+            if u_scales is None:
+                u_scales, = _alloc(stream, dev, _E8M0, (T, _groups(D)))
+            a.u_scales, a.ld_u_scales = u_scales.data_ptr(), _need("u_scales", u_scales, _E8M0, (T, _groups(D)), dev)
+        elif u_scales is not None:
+            raise ValueError('u_scales belongs to out="fp8"')
+    _check(lib.tp_residual_norm(ctypes.byref(a), _launch_stream(stream, dev)))
+    return h, u, u_scales
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,680 @@
+// Block-scaled 8-bit projections on the 5th-generation tensor cores.
+//
+//   colwise  Y_r = act(X . W_r^T + b_r),  rowwise  Z = sum_r X_r . W_r^T + b
+//
+// with e4m3 operands that carry one e8m0 scale per token and 128 features (X) and per 128 x 128
+// block (W).  A scale is a power of two, so the tensor core applies it itself: tcgen05.mma
+// kind::mxf8f6f4 takes a scale byte per operand row and 32 features from tensor memory, and the
+// four K=32 steps of a group name the same byte.  Nothing is rescaled outside the MMA, the sum
+// over K (and over the ranks of a rowwise call, in rank order) stays in one fp32 accumulator.
+//
+// Scale bytes reach tensor memory as 32-bit words of four consecutive groups (a "chunk", K = 512):
+// operand row r's word lies in lane r % 32 of column r / 32, the same in each 32-lane quarter.
+// Four warps load the bytes of a chunk and store the words while the MMAs of the previous chunk
+// run (two buffers).
+//
+// fp8_tokens_kernel: the weight rows are the MMA's M (128 lanes), the tokens its N.  A launch is
+// bound by the bytes of W, each read once: a ring of 128-byte-wide TMA boxes, and, when there are
+// fewer 128-row tiles than SMs, the chunks of K split over the CTAs of a cluster.  Every CTA
+// leaves its fp32 partial tile in its shared memory, and after a cluster barrier each CTA sums
+// its share of the tokens over the CTAs in K order through distributed shared memory, applies
+// bias and activation and stores (or quantises: a tile's 128 columns are one scale group).
+//
+// Every mbarrier wait is bounded (about 2 s); a CTA that gives up records it in the library's
+// status word, lets its copies and MMAs drain, frees tensor memory and exits.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "tp_e4m3.cuh"
+#include "tp_internal.h"
+#include "tp_ptx.cuh"
+
+namespace tp {
+namespace {
+
+constexpr int BM = 128;                // accumulator rows per CTA (TMEM lanes)
+constexpr int KB = kFp8Group;          // K per stage: one 128-byte swizzled row, one scale group
+constexpr int kChunk = 4;              // scale groups in one 32-bit word
+constexpr uint32_t kBoxA = BM * KB;    // bytes of one operand box of 128 rows
+constexpr int kMaxStages = 12;
+constexpr int kMaxSplits = 8;          // CTAs of a cluster (portable limit)
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+struct Fp8Params {
+  CUtensorMap map_x[TP_MAX_DEGREE];    // [0] only when the tokens are shared (colwise)
+  CUtensorMap map_w[TP_MAX_DEGREE];
+  const uint8_t* sx[TP_MAX_DEGREE];    // [T, k_groups], row stride ld_sx
+  const uint8_t* sw[TP_MAX_DEGREE];    // [ceil(w_rows / 128), k_groups], dense
+  const __nv_bfloat16* bias[TP_MAX_DEGREE];  // per output, nullable
+  void* out[TP_MAX_DEGREE];                  // per output: bf16, or e4m3 when out_scales is set
+  uint8_t* out_scales[TP_MAX_DEGREE];
+  unsigned int* status;
+  int64_t ld_sx, ldo, ld_os;
+  int T;
+  int w_rows;      // rows of each W
+  int n_out;       // output columns of each output
+  int up_row;      // SwiGLU: first row of the up block
+  int n_groups;    // outputs (ranks of a colwise call; 1 for rowwise)
+  int n_segs;      // K segments of an output (ranks of a rowwise call; 1 for colwise)
+  int k_groups;    // scale groups (128 features) per segment
+  int n_tiles, t_tiles;
+  int splits;      // cluster CTAs that share a tile's K
+  int act;
+};
+
+// ---------------------------------------------------------------- instructions
+// D[tmem] (+)= (A * 2^sfa)[smem] . (B * 2^sfb)[smem]^T, e4m3 operands, scale bytes in tensor memory.
+__device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::mxf8f6f4: e4m3 A and B (both K-major), fp32 D, e8m0 scales, M x N tile.
+__host__ __device__ constexpr uint32_t idesc_mx(int m, int n) {
+  return (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+// The byte of its scale words that an instruction uses, for A and B alike.
+__device__ __forceinline__ uint32_t idesc_scale_byte(uint32_t k) { return (k << 4) | (k << 29); }
+
+__device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Bounded wait: true when the phase completed, false when this CTA is giving up.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                             unsigned int* status, bool ignore_abort = false) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (!ignore_abort && *abort_flag) return false;
+      if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(status, TP_DEVSTATUS_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- scale words
+// Bytes [0, n) of p as a little-endian word (n <= 4, warp-uniform); one load where p allows it.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int n) {
+  if (n == kChunk && (reinterpret_cast<uintptr_t>(p) & 3u) == 0) return *reinterpret_cast<const uint32_t*>(p);
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i)
+    if (i < n) w |= static_cast<uint32_t>(p[i]) << (8 * i);
+  return w;
+}
+constexpr uint32_t kScaleOne = 0x7F7F7F7Fu;  // 2^0 for rows past the operand (their products are not stored)
+
+// Four columns of words for 128 weight rows from row `row0`; this lane's rows are row0 + 32 c + lane.
+__device__ __forceinline__ void weight_words(const Fp8Params& p, const uint8_t* sw, int row0, int kg, int n, int lane,
+                                             uint32_t (&w)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int row = row0 + 32 * c + lane;
+    w[c] = row < p.w_rows
+               ? scale_word(sw + static_cast<int64_t>(row / kFp8Group) * p.k_groups + kg, n)
+               : kScaleOne;
+  }
+}
+// The same for 32 * kCols tokens.
+template <int kCols>
+__device__ __forceinline__ void token_words(const Fp8Params& p, const uint8_t* sx, int t0, int kg, int n, int lane,
+                                            uint32_t (&w)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int t = t0 + 32 * c + lane;
+    w[c] = (c < kCols && t < p.T) ? scale_word(sx + static_cast<int64_t>(t) * p.ld_sx + kg, n) : kScaleOne;
+  }
+}
+
+// ---------------------------------------------------------------- activation
+// GELU(tanh) as x / (1 + e^(-2u)), u = sqrt(2/pi) (x + 0.044715 x^3); SiLU as x / (1 + e^(-x)).
+__device__ __forceinline__ float gelu_tanh_f(float x) {
+  const float u = 0.7978845608028654f * (x + 0.044715f * x * x * x);
+  return __fdividef(x, 1.0f + __expf(-2.0f * u));
+}
+__device__ __forceinline__ float silu_f(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// ---------------------------------------------------------------- few tokens
+template <int TN, bool kGlu>
+struct TokensCfg {
+  static constexpr int W_TILES = kGlu ? 2 : 1;                  // gate rows and up rows
+  static constexpr uint32_t W_BYTES = W_TILES * kBoxA;
+  static constexpr uint32_t X_BYTES = TN * KB;
+  static constexpr uint32_t STAGE_BYTES = W_BYTES + X_BYTES;
+  static constexpr int STAGES = 196608 / STAGE_BYTES < kMaxStages ? 196608 / STAGE_BYTES : kMaxStages;
+  static constexpr uint32_t RING = STAGES * STAGE_BYTES;
+  static constexpr uint32_t PARTIAL = W_TILES * TN * BM * 4;    // fp32 [tile][token][128], over the ring
+  static_assert(PARTIAL <= RING, "the partial tile reuses the ring");
+  // One CTA per SM, and none beside another kernel's CTA that may still be about to allocate
+  // tensor memory: the smallest of those holds 97 KB.
+  static_assert(RING >= 135168, "fewer than 132 KB would let two kernels' CTAs share an SM");
+  static constexpr int ACC_COLS = W_TILES * TN;
+  static constexpr int SF_COLS = 16;                            // per buffer: W (4 or 8), then tokens (4)
+  static constexpr uint32_t TMEM_COLS = ACC_COLS + 2 * SF_COLS <= 64    ? 64
+                                        : ACC_COLS + 2 * SF_COLS <= 128 ? 128
+                                        : ACC_COLS + 2 * SF_COLS <= 256 ? 256
+                                                                        : 512;
+  static constexpr size_t SMEM = 1024 + RING;
+};
+
+struct alignas(8) TokensCtrl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t sf_full[2], sf_empty[2];
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+constexpr int kTokensThreads = 192;  // producer, MMA issuer, four scale / accumulator warps
+
+template <int TN, bool kGlu>
+__global__ void __launch_bounds__(kTokensThreads, 1) fp8_tokens_kernel(const __grid_constant__ Fp8Params p) {
+  using C = TokensCfg<TN, kGlu>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TokensCtrl ctl_mem;
+  TokensCtrl* ctl = &ctl_mem;
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  volatile int* abort_flag = &ctl->abort;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(ptx::smem_addr(&ctl->sf_full[b]), 128);
+      ptx::mbar_init(ptx::smem_addr(&ctl->sf_empty[b]), 1);
+    }
+    ptx::mbar_init(ptx::smem_addr(&ctl->done), 1);
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == 0) {
+    ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), C::TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  // Only now may a dependent kernel's CTAs be scheduled: one that took tensor memory before this
+  // CTA had its own would wait for this kernel while this CTA waits for it.
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // This CTA's tile and its share of the tile's chunks of K.
+  const int splits = p.splits;
+  const int part = static_cast<int>(blockIdx.x) % splits;
+  const int tile = static_cast<int>(blockIdx.x) / splits;
+  const int tt = tile % p.t_tiles;
+  const int nt = tile / p.t_tiles % p.n_tiles;
+  const int g = tile / p.t_tiles / p.n_tiles;
+  const int seg_chunks = (p.k_groups + kChunk - 1) / kChunk;
+  const int chunks = p.n_segs * seg_chunks;
+  const int c0 = static_cast<int>(static_cast<int64_t>(chunks) * part / splits);
+  const int c1 = static_cast<int>(static_cast<int64_t>(chunks) * (part + 1) / splits);
+  const int t0 = tt * TN;
+  const int w_row0 = nt * BM;
+  // An output's operands: its rank's (colwise), or every rank's in turn (rowwise).
+  auto w_of = [&](int seg) { return p.n_segs > 1 ? seg : g; };
+  auto x_of = [&](int seg) { return p.n_segs > 1 ? seg : 0; };
+  bool gave_up = false;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      uint32_t it = 0;
+      bool ok = true;
+      for (int c = c0; c < c1 && ok; ++c) {
+        const int seg = c / seg_chunks;
+        const int kg0 = (c - seg * seg_chunks) * kChunk;
+        const int n = min(kChunk, p.k_groups - kg0);
+        const CUtensorMap* mw = &p.map_w[w_of(seg)];
+        const CUtensorMap* mx = &p.map_x[x_of(seg)];
+        for (int k = 0; k < n; ++k, ++it) {
+          const uint32_t s = it % C::STAGES;
+          if (!wait_bounded(ptx::smem_addr(&ctl->empty[s]), ((it / C::STAGES) & 1u) ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = ptx::smem_addr(&ctl->full[s]);
+          const uint32_t sw = ptx::smem_addr(base + s * C::STAGE_BYTES);
+          const int kx = (kg0 + k) * (KB / 2);  // the maps count 2-byte elements
+          ptx::mbar_arrive_expect_tx(full, C::STAGE_BYTES);
+          ptx::tma_load_2d(sw, mw, full, kx, w_row0);
+          if constexpr (kGlu) ptx::tma_load_2d(sw + kBoxA, mw, full, kx, p.up_row + w_row0);
+          ptx::tma_load_2d(sw + C::W_BYTES, mx, full, kx, t0);
+        }
+      }
+      // Every copy this thread issued lands before the CTA can exit.
+      const uint32_t first = it > C::STAGES ? it - C::STAGES : 0;
+      for (uint32_t j = first; j < it; ++j)
+        wait_bounded(ptx::smem_addr(&ctl->full[j % C::STAGES]), (j / C::STAGES) & 1u, abort_flag, p.status, true);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t idesc = idesc_mx(BM, TN);
+      uint32_t it = 0, accumulate = 0;
+      bool ok = true;
+      for (int c = c0; c < c1 && ok; ++c) {
+        const int i = c - c0;
+        const int seg = c / seg_chunks;
+        const int n = min(kChunk, p.k_groups - (c - seg * seg_chunks) * kChunk);
+        const uint32_t buf = i & 1u;
+        if (!wait_bounded(ptx::smem_addr(&ctl->sf_full[buf]), (i >> 1) & 1u, abort_flag, p.status)) break;
+        const uint32_t sf = tmem + C::ACC_COLS + buf * C::SF_COLS;
+        for (int k = 0; k < n; ++k, ++it) {
+          const uint32_t s = it % C::STAGES;
+          if (!wait_bounded(ptx::smem_addr(&ctl->full[s]), (it / C::STAGES) & 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sw = ptx::smem_addr(base + s * C::STAGE_BYTES);
+          const uint64_t wdesc = ptx::sw128_kmajor_desc(sw);
+          const uint64_t xdesc = ptx::sw128_kmajor_desc(sw + C::W_BYTES);
+          const uint32_t id = idesc | idesc_scale_byte(static_cast<uint32_t>(k));
+#pragma unroll
+          for (int j = 0; j < KB / 32; ++j) {  // +32 bytes along K = +2 in the descriptor's 16-byte units
+            umma_mx(tmem, wdesc + 2 * j, xdesc + 2 * j, id, sf, sf + 4 * C::W_TILES, accumulate);
+            if constexpr (kGlu) {
+              const uint64_t udesc = ptx::sw128_kmajor_desc(sw + kBoxA);
+              umma_mx(tmem + TN, udesc + 2 * j, xdesc + 2 * j, id, sf + 4, sf + 4 * C::W_TILES, accumulate);
+            }
+            accumulate = 1;
+          }
+          ptx::umma_commit(ptx::smem_addr(&ctl->empty[s]));
+        }
+        ptx::umma_commit(ptx::smem_addr(&ctl->sf_empty[buf]));
+      }
+      ptx::umma_commit(ptx::smem_addr(&ctl->done));
+      wait_bounded(ptx::smem_addr(&ctl->done), 0, abort_flag, p.status, true);
+    }
+  } else {
+    // -------------------------------------------------------------- scales, then the partial tile
+    const int q = warp & 3;  // TMEM lane quarter this warp may access
+    const uint32_t quarter = static_cast<uint32_t>(q * 32) << 16;
+    for (int c = c0; c < c1; ++c) {
+      const int i = c - c0;
+      const int seg = c / seg_chunks;
+      const int kg = (c - seg * seg_chunks) * kChunk;
+      const int n = min(kChunk, p.k_groups - kg);
+      const uint32_t buf = i & 1u;
+      uint32_t w[4], u[4], x[4];
+      const uint8_t* sw = p.sw[w_of(seg)];
+      weight_words(p, sw, w_row0, kg, n, lane, w);
+      if constexpr (kGlu) weight_words(p, sw, p.up_row + w_row0, kg, n, lane, u);
+      token_words<(TN + 31) / 32>(p, p.sx[x_of(seg)], t0, kg, n, lane, x);
+      if (!__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&ctl->sf_empty[buf]), ((i >> 1) & 1u) ^ 1u, abort_flag,
+                                                p.status))) {
+        gave_up = true;
+        break;
+      }
+      const uint32_t sf = tmem + quarter + C::ACC_COLS + buf * C::SF_COLS;
+      tmem_st_x4(sf, w);
+      if constexpr (kGlu) tmem_st_x4(sf + 4, u);
+      tmem_st_x4(sf + 4 * C::W_TILES, x);
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(ptx::smem_addr(&ctl->sf_full[buf]));
+    }
+    if (!gave_up)
+      gave_up = !__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&ctl->done), 0, abort_flag, p.status));
+    if (!gave_up) {
+      // Every MMA is done, so every copy has landed and the ring is free: it takes the partial
+      // tile as [W tile][token][128 weight rows].
+      ptx::tc_fence_after();
+      float* partial = reinterpret_cast<float*>(base);
+#pragma unroll
+      for (int j = 0; j < C::ACC_COLS; j += 16) {
+        uint32_t v[16];
+        ptx::tmem_ld_32x32b_x16(tmem + quarter + j, v);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) partial[(j + e) * BM + q * 32 + lane] = __uint_as_float(v[e]);
+      }
+    }
+    ptx::tc_fence_before();
+  }
+  __syncwarp();
+  ptx::cluster_sync();  // every CTA's partial tile is in its shared memory
+
+  // ---------------------------------------------------------------- join, activation, store
+  // This CTA's share of the tile's tokens, a warp to a token, four columns to a lane.
+  if (!*abort_flag) {
+    const int tokens = min(TN, p.T - t0);
+    const int n0 = w_row0 + lane * 4;
+    const bool on = n0 < p.n_out;  // n_out is a multiple of 8
+    const __nv_bfloat16* bias = p.bias[g];
+    const uint32_t local = ptx::smem_addr(base) + static_cast<uint32_t>(lane) * 16;
+    for (int t = tokens * part / splits + warp; t < tokens * (part + 1) / splits; t += kTokensThreads / 32) {
+      float v[C::W_TILES][4];
+#pragma unroll
+      for (int a = 0; a < C::W_TILES; ++a) {
+        const uint32_t at = local + static_cast<uint32_t>(a * TN + t) * (BM * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[a][e] = 0.0f;
+        for (int s = 0; s < splits; ++s) {
+          const float4 f = ld_cluster_f4(ptx::mapa_shared(at, static_cast<uint32_t>(s)));
+          v[a][0] += f.x, v[a][1] += f.y, v[a][2] += f.z, v[a][3] += f.w;
+        }
+        if (bias != nullptr && on)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[a][e] += __bfloat162float(bias[n0 + e + (a ? p.up_row : 0)]);
+      }
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (kGlu)
+          y[e] = silu_f(v[0][e]) * v[1][e];
+        else
+          y[e] = p.act == TP_ACT_GELU_TANH ? gelu_tanh_f(v[0][e]) : v[0][e];
+      }
+      const int64_t row = static_cast<int64_t>(t0 + t);
+      if (p.out_scales[g] != nullptr) {  // the tile's 128 columns are one group of the output
+        uint32_t m = 0;
+        if (on)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m = max(m, abs_bits(y[e]));
+        const uint32_t byte = e8m0_of_amax(__reduce_max_sync(0xffffffffu, m));
+        const float inv = e8m0_inverse(byte);
+        if (on)
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out[g]) + row * p.ldo + n0) =
+              e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+        if (lane == 0) p.out_scales[g][row * p.ld_os + nt] = static_cast<uint8_t>(byte);
+      } else if (on) {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out[g]) + row * p.ldo + n0) =
+            make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+      }
+    }
+  }
+  ptx::cluster_sync();  // no CTA's shared memory goes away while another reads it
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+inline int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// Operand map over a row-major [rows, K] matrix of bytes: boxes of 128 bytes x box_rows, 128-byte
+// swizzle, zeros outside.  Encoded as 2-byte elements (K and the stride are multiples of 16).
+tp_status operand_map(CUtensorMap* m, const void* ptr, int64_t K, int64_t rows, int64_t ld, int box_rows) {
+  return encode_bf16_2d(m, ptr, K / 2, rows, ld / 2, KB / 2, static_cast<uint32_t>(box_rows), true);
+}
+
+// Clusters of `splits` CTAs that can be resident at once (cached per device and kernel).
+template <int TN, bool kGlu>
+tp_status resident_clusters(int splits, int* n) {
+  static std::mutex mu;
+  static int cached[64][kMaxSplits + 1];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  std::lock_guard<std::mutex> lock(mu);
+  int& c = cached[dev & 63][splits];
+  if (c == 0) {
+    e = cudaFuncSetAttribute(fp8_tokens_kernel<TN, kGlu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(TokensCfg<TN, kGlu>::SMEM));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(splits) * 64, 1, 1);
+    cfg.blockDim = dim3(kTokensThreads, 1, 1);
+    cfg.dynamicSmemBytes = TokensCfg<TN, kGlu>::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int k = 0;
+    if (cudaOccupancyMaxActiveClusters(&k, fp8_tokens_kernel<TN, kGlu>, &cfg) != cudaSuccess || k <= 0) {
+      cudaGetLastError();
+      k = -1;  // no such cluster on this device
+    }
+    c = k;
+  }
+  *n = c;
+  return TP_OK;
+}
+
+template <int TN, bool kGlu>
+tp_status launch_tokens(Fp8Params& p, cudaStream_t stream) {
+  const int64_t tiles = static_cast<int64_t>(p.n_groups) * p.n_tiles * p.t_tiles;
+  const int chunks = p.n_segs * ceil_div(p.k_groups, kChunk);
+  // The split of K whose longest CTA column is shortest: waves x (its chunks + the fixed part of
+  // a CTA's life, about one chunk's time).  Ties go to the smaller cluster.
+  int best = 0;
+  int64_t best_cost = 0;
+  for (int s = 1; s <= kMaxSplits && s <= chunks; ++s) {
+    int n = 0;
+    tp_status st = resident_clusters<TN, kGlu>(s, &n);
+    if (st != TP_OK) return st;
+    if (n < 1) continue;
+    const int64_t cost = ((tiles + n - 1) / n) * (ceil_div(chunks, s) + 1);
+    if (best == 0 || cost < best_cost) best = s, best_cost = cost;
+  }
+  if (best == 0) return fail(TP_ERR_UNSUPPORTED, "the kernel does not fit on this device");
+  if (tiles * best > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many tiles (%lld)", (long long)tiles);
+  p.splits = best;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * best), 1, 1);
+  cfg.blockDim = dim3(kTokensThreads, 1, 1);
+  cfg.dynamicSmemBytes = TokensCfg<TN, kGlu>::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(best);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_tokens_kernel<TN, kGlu>, p);
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 projection launch");
+  return TP_OK;
+}
+
+// The operands of a call, checked.
+struct Fp8Call {
+  const void* const* x;         // one (shared) or tp_degree
+  const void* const* sx;
+  bool x_shared;
+  int64_t ldx, ld_sx;
+  const void* const* w;
+  const void* const* sw;
+  int p;
+  int64_t T, K, w_rows, n_out;
+};
+
+tp_status run_fp8(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
+  p.status = status_word();
+  if (p.status == nullptr) return fail(TP_ERR_CUDA, "cannot locate the kernel status word");
+  const bool glu = p.act == TP_ACT_SWIGLU;
+  const int tn = c.T <= 16 ? 16 : c.T <= 32 ? 32 : c.T <= 64 ? 64 : 128;
+  for (int r = 0; r < c.p; ++r) {
+    tp_status st = operand_map(&p.map_w[r], c.w[r], c.K, c.w_rows, c.K, BM);
+    if (st != TP_OK) return st;
+    p.sw[r] = static_cast<const uint8_t*>(c.sw[r]);
+    if (r == 0 || !c.x_shared) {
+      st = operand_map(&p.map_x[r], c.x[r], c.K, c.T, c.ldx, tn);
+      if (st != TP_OK) return st;
+      p.sx[r] = static_cast<const uint8_t*>(c.sx[r]);
+    }
+  }
+  p.ld_sx = c.ld_sx;
+  p.T = static_cast<int>(c.T);
+  p.w_rows = static_cast<int>(c.w_rows);
+  p.n_out = static_cast<int>(c.n_out);
+  p.up_row = static_cast<int>(c.w_rows / 2);
+  p.k_groups = ceil_div(c.K, KB);
+  p.n_tiles = ceil_div(c.n_out, BM);
+  p.t_tiles = ceil_div(c.T, tn);
+  switch (tn) {
+    case 16: return glu ? launch_tokens<16, true>(p, stream) : launch_tokens<16, false>(p, stream);
+    case 32: return glu ? launch_tokens<32, true>(p, stream) : launch_tokens<32, false>(p, stream);
+    case 64: return glu ? launch_tokens<64, true>(p, stream) : launch_tokens<64, false>(p, stream);
+    default: return glu ? launch_tokens<128, true>(p, stream) : launch_tokens<128, false>(p, stream);
+  }
+}
+
+// What both entry points check of their operands.
+tp_status check_fp8(const Fp8Call& c) {
+  if (c.x == nullptr || c.sx == nullptr || c.w == nullptr || c.sw == nullptr)
+    return fail(TP_ERR_INVALID_ARG, "an operand array or its scales is NULL");
+  if (c.K % 16 != 0 || c.ldx % 16 != 0)
+    return fail(TP_ERR_ALIGNMENT, "in_features (%lld) and the input's row stride (%lld) must be multiples of 16",
+                (long long)c.K, (long long)c.ldx);
+  for (int r = 0; r < c.p; ++r) {
+    const int xr = c.x_shared ? 0 : r;
+    if (c.x[xr] == nullptr || c.sx[xr] == nullptr || c.w[r] == nullptr || c.sw[r] == nullptr)
+      return fail(TP_ERR_INVALID_ARG, "rank %d: an operand or its scales is NULL", r);
+    if (!aligned16(c.x[xr]) || !aligned16(c.w[r]))
+      return fail(TP_ERR_ALIGNMENT, "rank %d: the input or the weight is not 16-byte aligned", r);
+  }
+  return TP_OK;
+}
+
+tp_status check_sizes(int tp_degree, int64_t T, int64_t K, int64_t N) {
+  if (tp_degree < 1) return fail(TP_ERR_INVALID_ARG, "tp_degree must be >= 1, got %d", tp_degree);
+  if (tp_degree > TP_MAX_DEGREE)
+    return fail(TP_ERR_UNSUPPORTED, "tp_degree=%d above TP_MAX_DEGREE=%d", tp_degree, TP_MAX_DEGREE);
+  if (T < 0 || K < 0 || N < 0) return fail(TP_ERR_INVALID_ARG, "negative size");
+  if (T > 0x7FFFFF00 || N > 0x7FFFFF00 || K > 0x7FFFFF00)
+    return fail(TP_ERR_UNSUPPORTED, "sizes above 2^31-256 are not supported");
+  return TP_OK;
+}
+
+}  // namespace
+}  // namespace tp
+
+extern "C" {
+
+tp_status tp_linear_colwise_fp8(const void* x, int64_t ldx, const void* x_scales, int64_t ld_xs,
+                                const void* const* w_shards, const void* const* w_scales,
+                                const void* const* bias_shards, tp_act act, int tp_degree, int64_t T, int64_t K,
+                                int64_t N_r, void* const* y_shards, int64_t ldy, void* const* y_scales, int64_t ld_ys,
+                                tp_stream_t stream) {
+  using namespace tp;
+  clear_error();
+  tp_status st = check_sizes(tp_degree, T, K, N_r);
+  if (st != TP_OK) return st;
+  if (act != TP_ACT_NONE && act != TP_ACT_GELU_TANH && act != TP_ACT_SWIGLU)
+    return fail(TP_ERR_INVALID_ARG, "unknown activation %d", (int)act);
+  if (act == TP_ACT_SWIGLU && (N_r % 2) != 0)
+    return fail(TP_ERR_INVALID_ARG, "SwiGLU needs an even shard width ([gate_r; up_r]), got N_r=%lld", (long long)N_r);
+  const int64_t n_out = (act == TP_ACT_SWIGLU) ? N_r / 2 : N_r;
+  const int64_t k_groups = ceil_div(K, KB), out_groups = ceil_div(n_out, KB);
+  if (ldx == 0) ldx = K;
+  if (ld_xs == 0) ld_xs = k_groups;
+  if (ldy == 0) ldy = n_out;
+  if (ld_ys == 0) ld_ys = out_groups;
+  if (ldx < K || ld_xs < k_groups || ldy < n_out || ld_ys < out_groups)
+    return fail(TP_ERR_INVALID_ARG, "a row stride (ldx %lld, ld_xs %lld, ldy %lld, ld_ys %lld) is smaller than its row",
+                (long long)ldx, (long long)ld_xs, (long long)ldy, (long long)ld_ys);
+  if (T == 0 || N_r == 0) return TP_OK;
+  if (K == 0) return fail(TP_ERR_INVALID_ARG, "K (in_features) must be positive");
+  const void* xs[1] = {x};
+  const void* sxs[1] = {x_scales};
+  Fp8Call c{xs, sxs, true, ldx, ld_xs, w_shards, w_scales, tp_degree, T, K, N_r, n_out};
+  st = check_fp8(c);
+  if (st != TP_OK) return st;
+  if (y_shards == nullptr) return fail(TP_ERR_INVALID_ARG, "y_shards is NULL");
+  const int64_t step = y_scales != nullptr ? 16 : 8;
+  if (n_out % step != 0 || ldy % step != 0)
+    return fail(TP_ERR_ALIGNMENT, "output width (%lld) and ldy (%lld) must be multiples of %lld", (long long)n_out,
+                (long long)ldy, (long long)step);
+  Fp8Params p{};
+  for (int r = 0; r < tp_degree; ++r) {
+    if (y_shards[r] == nullptr || (y_scales != nullptr && y_scales[r] == nullptr))
+      return fail(TP_ERR_INVALID_ARG, "y_shards[%d] or y_scales[%d] is NULL", r, r);
+    if (!aligned16(y_shards[r])) return fail(TP_ERR_ALIGNMENT, "y_shards[%d] is not 16-byte aligned", r);
+    p.out[r] = y_shards[r];
+    p.out_scales[r] = y_scales != nullptr ? static_cast<uint8_t*>(y_scales[r]) : nullptr;
+    p.bias[r] = bias_shards != nullptr ? static_cast<const __nv_bfloat16*>(bias_shards[r]) : nullptr;
+  }
+  p.act = act;
+  p.n_groups = tp_degree;
+  p.n_segs = 1;
+  p.ldo = ldy;
+  p.ld_os = ld_ys;
+  return run_fp8(c, p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tp_status tp_linear_rowwise_fp8(const void* const* x_shards, int64_t ldx, const void* const* x_scales, int64_t ld_xs,
+                                const void* const* w_shards, const void* const* w_scales, const void* bias,
+                                int tp_degree, int64_t T, int64_t K_r, int64_t N, void* out, int64_t ldo,
+                                tp_stream_t stream) {
+  using namespace tp;
+  clear_error();
+  tp_status st = check_sizes(tp_degree, T, K_r, N);
+  if (st != TP_OK) return st;
+  const int64_t k_groups = ceil_div(K_r, KB);
+  if (ldx == 0) ldx = K_r;
+  if (ld_xs == 0) ld_xs = k_groups;
+  if (ldo == 0) ldo = N;
+  if (ldx < K_r || ld_xs < k_groups || ldo < N)
+    return fail(TP_ERR_INVALID_ARG, "a row stride (ldx %lld, ld_xs %lld, ldo %lld) is smaller than its row",
+                (long long)ldx, (long long)ld_xs, (long long)ldo);
+  if (T == 0 || N == 0) return TP_OK;
+  if (K_r == 0) return fail(TP_ERR_INVALID_ARG, "K_r (in_features per rank) must be positive");
+  if (static_cast<int64_t>(tp_degree) * k_groups > 0x7FFFFFFF)
+    return fail(TP_ERR_UNSUPPORTED, "too many K groups (%d ranks of %lld)", tp_degree, (long long)k_groups);
+  Fp8Call c{x_shards, x_scales, false, ldx, ld_xs, w_shards, w_scales, tp_degree, T, K_r, N, N};
+  st = check_fp8(c);
+  if (st != TP_OK) return st;
+  if (out == nullptr) return fail(TP_ERR_INVALID_ARG, "out is NULL");
+  if (N % 8 != 0 || ldo % 8 != 0)
+    return fail(TP_ERR_ALIGNMENT, "N (%lld) and ldo (%lld) must be multiples of 8", (long long)N, (long long)ldo);
+  if (!aligned16(out)) return fail(TP_ERR_ALIGNMENT, "out is not 16-byte aligned");
+  Fp8Params p{};
+  p.out[0] = out;
+  p.bias[0] = static_cast<const __nv_bfloat16*>(bias);
+  p.act = TP_ACT_NONE;
+  p.n_groups = 1;
+  p.n_segs = tp_degree;
+  p.ldo = ldo;
+  return run_fp8(c, p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

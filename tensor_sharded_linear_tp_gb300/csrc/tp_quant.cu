@@ -1,0 +1,438 @@
+// What stands around the 8-bit projections: the quantiser and the residual norm.  Both read and
+// write every element once and are bound by HBM.
+//
+// tp_quantize_fp8: a thread holds 16 consecutive elements (two 16-byte loads, one 16-byte store
+// of codes).  By token (1 x 128): 8 lanes share a group and join their maxima by three shuffles.
+// By weight block (128 x 128): a CTA of 256 threads holds the block in registers, four rows'
+// chunks a thread, so the block is read once although its scale needs all of it.
+//
+// tp_residual_norm: one row is held in registers as fp32 by one warp (short rows) or one CTA; the
+// statistics are sums over those registers (the variance about the mean, in a second sum), and
+// the normed, modulated row leaves as bf16 or as codes with their scales.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "tp_e4m3.cuh"
+#include "tp_internal.h"
+
+namespace tp {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Quantiser
+// ---------------------------------------------------------------------------
+
+struct QuantParams {
+  const uint8_t* x;  // bf16 [rows, cols], row stride ldx bytes
+  uint8_t* q;        // e4m3 [rows, cols], row stride ldq
+  uint8_t* scales;   // e8m0, row stride lds
+  int64_t ldx, ldq, lds;
+  int64_t rows;
+  int cols;
+  int col_groups;    // ceil(cols / 128)
+};
+
+// The largest |x| of 16 bf16 elements, as bf16 bits (integer maximum: a NaN wins).
+__device__ __forceinline__ uint32_t amax16(const uint4& a, const uint4& b) {
+  const uint32_t m = 0x7FFF7FFFu;
+  const uint32_t v = __vmaxu2(__vmaxu2(__vmaxu2(a.x & m, a.y & m), __vmaxu2(a.z & m, a.w & m)),
+                              __vmaxu2(__vmaxu2(b.x & m, b.y & m), __vmaxu2(b.z & m, b.w & m)));
+  return max(v & 0xFFFFu, v >> 16);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint4 codes16(const uint4& a, const uint4& b, float inv) {
+  auto four = [&](uint32_t u, uint32_t v) {
+    return e4m3x4(bf16_lo(u) * inv, bf16_hi(u) * inv, bf16_lo(v) * inv, bf16_hi(v) * inv);
+  };
+  return make_uint4(four(a.x, a.y), four(a.z, a.w), four(b.x, b.y), four(b.z, b.w));
+}
+
+constexpr int kQuantThreads = 256;
+
+__global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const QuantParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t group = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 8) + (threadIdx.x >> 3);
+  const int64_t row = group / p.col_groups;
+  const int kg = static_cast<int>(group - row * p.col_groups);
+  const int col = kg * kFp8Group + static_cast<int>(threadIdx.x & 7) * 16;
+  const bool on = row < p.rows && col < p.cols;  // cols is a multiple of 16: a chunk is whole or absent
+  uint4 a = make_uint4(0, 0, 0, 0), b = a;
+  if (on) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.x + row * p.ldx + static_cast<int64_t>(col) * 2);
+    a = src[0];
+    b = src[1];
+  }
+  uint32_t m = amax16(a, b);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const uint32_t byte = e8m0_of_amax(m << 16);
+  if (!on) return;
+  *reinterpret_cast<uint4*>(p.q + row * p.ldq + col) = codes16(a, b, e8m0_inverse(byte));
+  if ((threadIdx.x & 7) == 0) p.scales[row * p.lds + kg] = static_cast<uint8_t>(byte);
+}
+
+__global__ void __launch_bounds__(kQuantThreads) quantize_blocks_kernel(const QuantParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ uint32_t warp_max[kQuantThreads / 32];
+  const int64_t rg = blockIdx.x / p.col_groups;
+  const int kg = static_cast<int>(blockIdx.x - rg * p.col_groups);
+  const int col = kg * kFp8Group + static_cast<int>(threadIdx.x & 7) * 16;
+  const int64_t row0 = rg * kFp8Group + (threadIdx.x >> 3);
+  uint4 a[4], b[4];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + 32 * i;
+    a[i] = b[i] = make_uint4(0, 0, 0, 0);
+    if (row < p.rows && col < p.cols) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.x + row * p.ldx + static_cast<int64_t>(col) * 2);
+      a[i] = src[0];
+      b[i] = src[1];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, amax16(a[i], b[i]));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kQuantThreads / 32; ++w) m = max(m, warp_max[w]);
+  const uint32_t byte = e8m0_of_amax(m << 16);
+  const float inv = e8m0_inverse(byte);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + 32 * i;
+    if (row < p.rows && col < p.cols)
+      *reinterpret_cast<uint4*>(p.q + row * p.ldq + col) = codes16(a[i], b[i], inv);
+  }
+  if (threadIdx.x == 0) p.scales[rg * p.lds + kg] = static_cast<uint8_t>(byte);
+}
+
+// ---------------------------------------------------------------------------
+// Residual norm
+// ---------------------------------------------------------------------------
+
+struct NormParams {
+  const __nv_bfloat16 *x, *y;
+  const __nv_bfloat16 *post_weight, *post_bias, *weight, *bias;  // [D], nullable
+  const __nv_bfloat16 *gate, *scale, *shift;                     // [mod_rows, D], row stride ld_mod, nullable
+  __nv_bfloat16 *h, *u;
+  uint8_t *u8, *u_scales;
+  int64_t ldx, ldy, ldh, ldu, ld_us, ld_mod, rows_per_mod;
+  int64_t T;
+  int D;
+  int post_norm, norm;
+  float alpha, eps;
+};
+
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
+  v[4] = bf16_lo(a.z), v[5] = bf16_hi(a.z), v[6] = bf16_lo(a.w), v[7] = bf16_hi(a.w);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  auto two = [](float a, float b) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&t);
+  };
+  *reinterpret_cast<uint4*>(p) = make_uint4(two(v[0], v[1]), two(v[2], v[3]), two(v[4], v[5]), two(v[6], v[7]));
+}
+
+// Sum over the threads that hold one row: a warp, or the CTA (a fixed order either way).
+template <int kThreads>
+__device__ __forceinline__ float row_sum(float v, float* scratch) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (kThreads > 32) {
+    __syncthreads();  // the previous sum's readers are done with the scratch
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) v += scratch[w];
+  }
+  return v;
+}
+
+// v <- norm(v) over one row of D elements; elements past D are not part of the sums.
+template <int kThreads, int kVecs>
+__device__ __forceinline__ void normalise(float (&v)[kVecs][8], int kind, int D, float eps, int lane, float* scratch,
+                                          const __nv_bfloat16* weight, const __nv_bfloat16* bias) {
+  if (kind == TP_NORM_NONE) return;
+  const float inv_d = 1.0f / static_cast<float>(D);
+  if (kind == TP_NORM_LAYER) {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+      if ((j * kThreads + lane) * 8 < D)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += v[j][i];
+    const float mean = row_sum<kThreads>(s, scratch) * inv_d;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] -= mean;
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j)
+    if ((j * kThreads + lane) * 8 < D)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(v[j][i], v[j][i], s);
+  const float r = 1.0f / sqrtf(row_sum<kThreads>(s, scratch) * inv_d + eps);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int col = (j * kThreads + lane) * 8;
+    float w[8], b[8];
+    if (weight != nullptr && col < D) load8(weight + col, w);
+    if (bias != nullptr && col < D) load8(bias + col, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[j][i] *= r;
+      if (weight != nullptr) v[j][i] *= w[i];
+      if (bias != nullptr) v[j][i] += b[i];
+    }
+  }
+}
+
+// kThreads threads hold a row (32: one warp, four rows a CTA), kVecs vectors of 8 elements each.
+template <int kThreads, int kVecs>
+__global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128) residual_norm_kernel(const NormParams p) {
+  __shared__ float scratch[32];
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kRows = kThreads > 32 ? 1 : 4;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (kRows > 1 ? threadIdx.x >> 5 : 0);
+  if (row >= p.T) return;  // warp-uniform; with one row a CTA the grid is exact
+  const int lane = kRows > 1 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
+  const int64_t mod = p.rows_per_mod > 0 ? row / p.rows_per_mod * p.ld_mod : 0;
+  float v[kVecs][8];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int col = (j * kThreads + lane) * 8;
+    if (p.y != nullptr && col < p.D) {
+      load8(p.y + row * p.ldy + col, v[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+    }
+  }
+  if (p.y != nullptr)
+    normalise<kThreads, kVecs>(v, p.post_norm, p.D, p.eps, lane, scratch, p.post_weight, p.post_bias);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int col = (j * kThreads + lane) * 8;
+    if (col < p.D) {
+      float x[8];
+      load8(p.x + row * p.ldx + col, x);
+      if (p.gate != nullptr) {
+        float g[8];
+        load8(p.gate + mod + col, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] *= g[i];
+      }
+      if (p.y != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = fmaf(p.alpha, x[i], v[j][i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = p.alpha * x[i];
+      }
+      if (p.h != nullptr) store8(p.h + row * p.ldh + col, v[j]);
+    }
+  }
+  if (p.u == nullptr && p.u8 == nullptr) return;  // uniform over the grid
+  normalise<kThreads, kVecs>(v, p.norm, p.D, p.eps, lane, scratch, p.weight, p.bias);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int col = (j * kThreads + lane) * 8;
+    const bool on = col < p.D;
+    if (on && p.scale != nullptr) {
+      float s[8];
+      load8(p.scale + mod + col, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] *= 1.0f + s[i];
+    }
+    if (on && p.shift != nullptr) {
+      float s[8];
+      load8(p.shift + mod + col, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] += s[i];
+    }
+    if (p.u != nullptr) {
+      if (on) store8(p.u + row * p.ldu + col, v[j]);
+    } else {
+      // 16 lanes hold a group of 128.
+      uint32_t m = 0;
+      if (on)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[j][i]));
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const uint32_t byte = e8m0_of_amax(m);
+      const float inv = e8m0_inverse(byte);
+      if (on) {
+        const uint2 c = make_uint2(e4m3x4(v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv),
+                                   e4m3x4(v[j][4] * inv, v[j][5] * inv, v[j][6] * inv, v[j][7] * inv));
+        *reinterpret_cast<uint2*>(p.u8 + row * p.ldu + col) = c;
+        if ((lane & 15) == 0) p.u_scales[row * p.ld_us + col / kFp8Group] = static_cast<uint8_t>(byte);
+      }
+    }
+  }
+}
+
+template <int kThreads, int kVecs>
+tp_status launch_norm(const NormParams& p, cudaStream_t stream) {
+  constexpr int kRows = kThreads > 32 ? 1 : 4;
+  const int64_t blocks = (p.T + kRows - 1) / kRows;
+  if (blocks > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many rows (%lld)", (long long)p.T);
+  cudaError_t e = launch_pdl(residual_norm_kernel<kThreads, kVecs>, dim3(static_cast<unsigned>(blocks)),
+                             dim3(kThreads > 32 ? kThreads : 128), 0, stream, p);
+  if (e != cudaSuccess) return cuda_fail(e, "residual norm launch");
+  return TP_OK;
+}
+
+// Rows up to 1024 wide take a warp, longer ones the smallest CTA whose threads hold four vectors or fewer.
+tp_status dispatch_norm(const NormParams& p, cudaStream_t s) {
+  const int vecs = (p.D + 7) / 8;
+  if (vecs <= 32) return launch_norm<32, 1>(p, s);
+  if (vecs <= 64) return launch_norm<32, 2>(p, s);
+  if (vecs <= 128) return launch_norm<32, 4>(p, s);
+  if (vecs <= 256) return launch_norm<256, 1>(p, s);
+  if (vecs <= 512) return launch_norm<256, 2>(p, s);
+  if (vecs <= 768) return launch_norm<256, 3>(p, s);
+  if (vecs <= 1024) return launch_norm<256, 4>(p, s);
+  if (vecs <= 2048) return launch_norm<512, 4>(p, s);
+  return launch_norm<1024, 4>(p, s);
+}
+
+}  // namespace
+}  // namespace tp
+
+extern "C" {
+
+tp_status tp_quantize_fp8(const void* x, int64_t ldx, int64_t rows, int64_t cols, int block_rows, void* q, int64_t ldq,
+                          void* scales, int64_t lds, tp_stream_t stream) {
+  using namespace tp;
+  clear_error();
+  if (rows < 0 || cols < 0) return fail(TP_ERR_INVALID_ARG, "negative size");
+  if (block_rows != 1 && block_rows != kFp8Group)
+    return fail(TP_ERR_INVALID_ARG, "block_rows must be 1 or %d, got %d", kFp8Group, block_rows);
+  if (cols > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "sizes above 2^31-1 are not supported");
+  const int64_t col_groups = (cols + kFp8Group - 1) / kFp8Group;
+  if (ldx == 0) ldx = cols;
+  if (ldq == 0) ldq = cols;
+  if (lds == 0) lds = col_groups;
+  if (ldx < cols || ldq < cols || lds < col_groups)
+    return fail(TP_ERR_INVALID_ARG, "a row stride (ldx %lld, ldq %lld, lds %lld) is smaller than its row",
+                (long long)ldx, (long long)ldq, (long long)lds);
+  if (rows == 0 || cols == 0) return TP_OK;
+  if (x == nullptr || q == nullptr || scales == nullptr)
+    return fail(TP_ERR_INVALID_ARG, "x, q or scales is NULL");
+  if (cols % 16 != 0 || ldx % 8 != 0 || ldq % 16 != 0)
+    return fail(TP_ERR_ALIGNMENT, "cols (%lld) and ldq (%lld) must be multiples of 16, ldx (%lld) of 8",
+                (long long)cols, (long long)ldq, (long long)ldx);
+  if (!aligned16(x) || !aligned16(q)) return fail(TP_ERR_ALIGNMENT, "x or q is not 16-byte aligned");
+  const int64_t row_groups = (rows + block_rows - 1) / block_rows;
+  const int64_t per_cta = block_rows == 1 ? kQuantThreads / 8 : 1;
+  if (row_groups > 0x7FFFFFFFll * per_cta / col_groups) return fail(TP_ERR_UNSUPPORTED, "too many groups");
+  const int64_t blocks = (row_groups * col_groups + per_cta - 1) / per_cta;
+  QuantParams p{};
+  p.x = static_cast<const uint8_t*>(x);
+  p.q = static_cast<uint8_t*>(q);
+  p.scales = static_cast<uint8_t*>(scales);
+  p.ldx = ldx * 2;
+  p.ldq = ldq;
+  p.lds = lds;
+  p.rows = rows;
+  p.cols = static_cast<int>(cols);
+  p.col_groups = static_cast<int>(col_groups);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_pdl(block_rows == 1 ? quantize_rows_kernel : quantize_blocks_kernel,
+                             dim3(static_cast<unsigned>(blocks)), dim3(kQuantThreads), 0, s, p);
+  if (e != cudaSuccess) return cuda_fail(e, "quantiser launch");
+  return TP_OK;
+}
+
+tp_status tp_residual_norm(const tp_residual_norm_args* a, tp_stream_t stream) {
+  using namespace tp;
+  clear_error();
+  if (a == nullptr) return fail(TP_ERR_INVALID_ARG, "args is NULL");
+  if (a->T < 0 || a->D < 0) return fail(TP_ERR_INVALID_ARG, "negative size");
+  auto known = [](int k) { return k == TP_NORM_NONE || k == TP_NORM_RMS || k == TP_NORM_LAYER; };
+  if (!known(a->norm) || !known(a->post_norm))
+    return fail(TP_ERR_INVALID_ARG, "unknown norm %d or post_norm %d", (int)a->norm, (int)a->post_norm);
+  if (!(a->eps >= 0.0f) || std::isinf(a->eps)) return fail(TP_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (a->D > TP_NORM_MAX_D)
+    return fail(TP_ERR_UNSUPPORTED, "rows wider than %d are not supported, got %lld", TP_NORM_MAX_D, (long long)a->D);
+  NormParams p{};
+  p.ldx = a->ldx == 0 ? a->D : a->ldx;
+  p.ldy = a->ldy == 0 ? a->D : a->ldy;
+  p.ldh = a->ldh == 0 ? a->D : a->ldh;
+  p.ldu = a->ldu == 0 ? a->D : a->ldu;
+  const int64_t groups = (a->D + kFp8Group - 1) / kFp8Group;
+  p.ld_us = a->ld_u_scales == 0 ? groups : a->ld_u_scales;
+  p.ld_mod = a->ld_mod == 0 ? a->D : a->ld_mod;
+  if (p.ldx < a->D || p.ldy < a->D || p.ldh < a->D || p.ldu < a->D || p.ld_mod < a->D || p.ld_us < groups)
+    return fail(TP_ERR_INVALID_ARG, "a row stride is smaller than its row");
+  if (a->T == 0 || a->D == 0) return TP_OK;
+  if (a->x == nullptr) return fail(TP_ERR_INVALID_ARG, "x is NULL");
+  if (a->h == nullptr && a->u == nullptr) return fail(TP_ERR_INVALID_ARG, "neither h nor u is wanted");
+  if (a->y == nullptr && (a->h != nullptr || a->gate != nullptr || a->post_norm != TP_NORM_NONE))
+    return fail(TP_ERR_INVALID_ARG, "h, gate and post_norm belong to a branch y, which is NULL");
+  if ((a->post_weight != nullptr || a->post_bias != nullptr) && a->post_norm == TP_NORM_NONE)
+    return fail(TP_ERR_INVALID_ARG, "post_weight or post_bias without a post_norm");
+  if ((a->weight != nullptr || a->bias != nullptr) && a->norm == TP_NORM_NONE)
+    return fail(TP_ERR_INVALID_ARG, "weight or bias without a norm");
+  const bool fp8 = a->u != nullptr && a->u_scales != nullptr;
+  if (a->u == nullptr && (a->u_scales != nullptr || a->scale != nullptr || a->shift != nullptr ||
+                          a->norm != TP_NORM_NONE))
+    return fail(TP_ERR_INVALID_ARG, "norm, scale, shift and u_scales belong to u, which is NULL");
+  if (a->gate != nullptr || a->scale != nullptr || a->shift != nullptr) {
+    if (a->rows_per_mod < 1 || a->mod_rows < 1)
+      return fail(TP_ERR_INVALID_ARG, "rows_per_mod and mod_rows must be positive with a gate, scale or shift");
+    if ((a->T - 1) / a->rows_per_mod >= a->mod_rows)
+      return fail(TP_ERR_INVALID_ARG, "%lld rows, %lld to a modulation row, need more than %lld modulation rows",
+                  (long long)a->T, (long long)a->rows_per_mod, (long long)a->mod_rows);
+    p.rows_per_mod = a->rows_per_mod;
+  }
+  const int64_t step = fp8 ? 16 : 8;
+  if (a->D % step != 0 || p.ldu % step != 0)
+    return fail(TP_ERR_ALIGNMENT, "D (%lld) and ldu (%lld) must be multiples of %lld", (long long)a->D,
+                (long long)p.ldu, (long long)step);
+  if (p.ldx % 8 != 0 || p.ldy % 8 != 0 || p.ldh % 8 != 0 || p.ld_mod % 8 != 0)
+    return fail(TP_ERR_ALIGNMENT, "ldx, ldy, ldh and ld_mod must be multiples of 8");
+  const void* ptrs[] = {a->x, a->y, a->post_weight, a->post_bias, a->gate, a->weight, a->bias,
+                        a->scale, a->shift, a->h, a->u};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return fail(TP_ERR_ALIGNMENT, "a pointer is not 16-byte aligned");
+  p.x = static_cast<const __nv_bfloat16*>(a->x);
+  p.y = static_cast<const __nv_bfloat16*>(a->y);
+  p.post_weight = static_cast<const __nv_bfloat16*>(a->post_weight);
+  p.post_bias = static_cast<const __nv_bfloat16*>(a->post_bias);
+  p.weight = static_cast<const __nv_bfloat16*>(a->weight);
+  p.bias = static_cast<const __nv_bfloat16*>(a->bias);
+  p.gate = static_cast<const __nv_bfloat16*>(a->gate);
+  p.scale = static_cast<const __nv_bfloat16*>(a->scale);
+  p.shift = static_cast<const __nv_bfloat16*>(a->shift);
+  p.h = static_cast<__nv_bfloat16*>(a->h);
+  p.u = fp8 ? nullptr : static_cast<__nv_bfloat16*>(a->u);
+  p.u8 = fp8 ? static_cast<uint8_t*>(a->u) : nullptr;
+  p.u_scales = static_cast<uint8_t*>(a->u_scales);
+  p.T = a->T;
+  p.D = static_cast<int>(a->D);
+  p.post_norm = a->post_norm;
+  p.norm = a->norm;
+  p.alpha = a->alpha;
+  p.eps = a->eps;
+  return dispatch_norm(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
