@@ -20,13 +20,21 @@
 // its share of the tokens over the CTAs in K order through distributed shared memory, applies
 // bias and activation and stores (or quantises: a tile's 128 columns are one scale group).
 //
+// fp8_prompt_kernel: the tokens are M, 256 of them to a persistent CTA pair (cta_group::2), 256
+// weight rows (SwiGLU: 128 gate and 128 up rows) are N.  Bound by the tensor core.  Two
+// accumulators of 256 columns and the scale words do not fit tensor memory's 512 columns side by
+// side, so the accumulators overlap by 32 columns: the epilogue reads those first and hands them
+// back, and the next tile's MMAs start while it works through the rest.
+//
 // Every mbarrier wait is bounded (about 2 s); a CTA that gives up records it in the library's
 // status word, lets its copies and MMAs drain, frees tensor memory and exits.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cstdlib>
 #include <mutex>
+#include <type_traits>
 
 #include "tp_e4m3.cuh"
 #include "tp_internal.h"
@@ -61,7 +69,8 @@ struct Fp8Params {
   int n_segs;      // K segments of an output (ranks of a rowwise call; 1 for colwise)
   int k_groups;    // scale groups (128 features) per segment
   int n_tiles, t_tiles;
-  int splits;      // cluster CTAs that share a tile's K
+  int splits;      // tokens kernel: cluster CTAs that share a tile's K
+  int group_m;     // prompt kernel: token tiles that sweep the weight tiles together
   int act;
 };
 
@@ -73,6 +82,17 @@ __device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b, uint
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// The same over a CTA pair: 128 rows of A and half of B's rows from each CTA, issued by the leader.
+__device__ __forceinline__ void umma_mx_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
@@ -100,12 +120,17 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 }
 
 // Bounded wait: true when the phase completed, false when this CTA is giving up.
+// kCluster: the phase's arrivals may come from the other CTA of a pair.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                              unsigned int* status, bool ignore_abort = false) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+  auto probe = [&]() {
+    return kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
+  };
+  if (probe()) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (probe()) return true;
     if ((i & 63u) == 0) {
       if (!ignore_abort && *abort_flag) return false;
       if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -429,6 +454,357 @@ __global__ void __launch_bounds__(kTokensThreads, 1) fp8_tokens_kernel(const __g
   }
 }
 
+// ---------------------------------------------------------------- prompts
+constexpr int PM = 256;                              // tokens per pair tile
+constexpr int PN = 256;                              // accumulator columns (weight rows) per tile
+constexpr int kPromptStages = 6;
+constexpr uint32_t kPromptStage = 2 * kBoxA;         // a CTA's 128 tokens and its 128 weight rows
+constexpr uint32_t kShared = 32;                     // columns the two accumulators share
+constexpr uint32_t kPromptSf = 2 * PN - kShared;     // scale words: two buffers of 16 columns (X 4, W 8)
+constexpr uint32_t kStagingRow = 256;                // epilogue staging: 32 rows a warp, 128 bf16 each
+constexpr uint32_t kStagingWarp = 32 * kStagingRow;
+constexpr int kPromptThreads = 320;                  // producer, MMA issuer, 4 epilogue and 4 scale warps
+constexpr size_t kPromptSmem = 1024 + kPromptStages * kPromptStage + 4 * kStagingWarp;
+static_assert(kPromptSf + 32 <= 512, "accumulators and scale words fill tensor memory");
+
+struct alignas(8) PromptCtrl {
+  uint64_t full[kPromptStages], empty[kPromptStages];
+  uint64_t sf_full[2], sf_empty[2];
+  uint64_t tfull[2], tempty;
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ void decode_tile(const Fp8Params& p, int t, int& g, int& mt, int& nt) {
+  // group_m token tiles sweep the weight tiles together, so that CTAs that run at the same time
+  // share both operands through L2.
+  const int per_out = p.t_tiles * p.n_tiles;
+  g = t / per_out;
+  const int in_out = t - g * per_out;
+  const int span = p.group_m * p.n_tiles;
+  const int first = in_out / span * p.group_m;
+  const int m = min(p.group_m, p.t_tiles - first);
+  const int in_span = in_out % span;
+  mt = first + in_span % m;
+  nt = in_span / m;
+}
+
+// One group of 128 output columns of this thread's row, from the accumulator's columns at
+// `taddr` (SwiGLU: gate there, up at `uaddr`), rows and columns past the output included.
+// kAcc: which accumulator; `release` is called once its shared columns are in registers.
+template <bool kGlu, int kAcc, typename Release>
+__device__ __forceinline__ void output_group(const Fp8Params& p, const __nv_bfloat16* bias, uint32_t taddr, int col0,
+                                             float (&y)[128], bool holds_shared, Release release) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // Accumulator 0 shares its last 32 columns, accumulator 1 its first.
+    const int j = (i + (kAcc == 0 ? 6 : 0)) & 7;
+    uint32_t v[16], u[16];
+    ptx::tmem_ld_32x32b_x16(taddr + 16 * j, v);
+    if constexpr (kGlu) ptx::tmem_ld_32x32b_x16(taddr + 128 + 16 * j, u);
+    ptx::tmem_ld_wait();
+    if (i == 1 && holds_shared) release();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int col = col0 + 16 * j + e;
+      float a = __uint_as_float(v[e]);
+      if (bias != nullptr && col < p.n_out) a += __bfloat162float(bias[col]);
+      if constexpr (kGlu) {
+        float b = __uint_as_float(u[e]);
+        if (bias != nullptr && col < p.n_out) b += __bfloat162float(bias[p.up_row + col]);
+        y[16 * j + e] = silu_f(a) * b;
+      } else {
+        y[16 * j + e] = a;
+      }
+    }
+  }
+  if (!kGlu && p.act == TP_ACT_GELU_TANH)
+#pragma unroll
+    for (int i = 0; i < 128; ++i) y[i] = gelu_tanh_f(y[i]);
+}
+
+// Store a warp's 32 rows x 128 columns: rows leave their threads through swizzled 16-byte pieces
+// of shared memory, so that a global store instruction writes whole 128- or 256-byte row segments.
+__device__ __forceinline__ void store_group(const Fp8Params& p, int g, const float (&y)[128], uint32_t staging,
+                                            int row0, int col0, int lane) {
+  const bool fp8 = p.out_scales[g] != nullptr;  // uniform
+  uint32_t byte = 0;
+  __syncwarp();  // the previous group has left the buffer
+  if (fp8) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 128; ++i)
+      if (col0 + (i & ~15) < p.n_out) m = max(m, abs_bits(y[i]));  // n_out is a multiple of 16
+    byte = e8m0_of_amax(m);
+    const float inv = e8m0_inverse(byte);
+    const uint32_t row = staging + static_cast<uint32_t>(lane) * 128;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = e4m3x4(y[16 * c + 4 * e] * inv, y[16 * c + 4 * e + 1] * inv, y[16 * c + 4 * e + 2] * inv,
+                      y[16 * c + 4 * e + 3] * inv);
+      ptx::st_shared_v4(row + (static_cast<uint32_t>(c ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    const uint32_t row = staging + static_cast<uint32_t>(lane) * 256;
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      ptx::st_shared_v4(row + (static_cast<uint32_t>(c ^ (lane & 7)) << 4), pack_bf16(y[8 * c], y[8 * c + 1]),
+                        pack_bf16(y[8 * c + 2], y[8 * c + 3]), pack_bf16(y[8 * c + 4], y[8 * c + 5]),
+                        pack_bf16(y[8 * c + 6], y[8 * c + 7]));
+  }
+  __syncwarp();
+  const int pieces = fp8 ? 8 : 16;                    // 16-byte pieces of a row
+  const int per_piece = fp8 ? 16 : 8;                 // columns
+  const int rows_at_once = 32 / pieces;
+  const int c = lane % pieces;
+  const int64_t esize = fp8 ? 1 : 2;
+  uint8_t* out = static_cast<uint8_t*>(p.out[g]) + static_cast<int64_t>(col0 + c * per_piece) * esize;
+  const bool col_on = col0 + c * per_piece < p.n_out;
+  for (int i = lane / pieces; i < 32; i += rows_at_once) {
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(staging + static_cast<uint32_t>(i * pieces * 16) + (static_cast<uint32_t>(c ^ (i & 7)) << 4)));
+    if (col_on && row0 + i < p.T)
+      *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + i) * p.ldo * esize) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (fp8 && row0 + lane < p.T)
+    p.out_scales[g][static_cast<int64_t>(row0 + lane) * p.ld_os + col0 / kFp8Group] = static_cast<uint8_t>(byte);
+}
+
+template <bool kGlu>
+__global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __grid_constant__ Fp8Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ PromptCtrl ctl_mem;
+  PromptCtrl* ctl = &ctl_mem;
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  volatile int* abort_flag = &ctl->abort;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t cta = ptx::cluster_ctarank();  // 0 = leader
+  const int unit = static_cast<int>(blockIdx.x) / 2;
+  const int units = static_cast<int>(gridDim.x) / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPromptStages; ++s) {
+      ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(ptx::smem_addr(&ctl->sf_full[b]), 256);
+      ptx::mbar_init(ptx::smem_addr(&ctl->sf_empty[b]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl->tfull[b]), 1);
+    }
+    ptx::mbar_init(ptx::smem_addr(&ctl->tempty), 256);
+    ptx::mbar_init(ptx::smem_addr(&ctl->drain), 1);
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == 0) {
+    ptx::tmem_alloc_pair(ptx::smem_addr(&ctl->tmem_base), 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int total = p.n_groups * p.t_tiles * p.n_tiles;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units) {
+        int g, mt, nt;
+        decode_tile(p, t, g, mt, nt);
+        const int x_row = mt * PM + static_cast<int>(cta) * BM;
+        const int w_row = kGlu ? (cta == 0 ? 0 : p.up_row) + nt * BM : nt * PN + static_cast<int>(cta) * BM;
+        for (int seg = 0; seg < p.n_segs && ok; ++seg) {
+          const CUtensorMap* mx = &p.map_x[p.n_segs > 1 ? seg : 0];
+          const CUtensorMap* mw = &p.map_w[p.n_segs > 1 ? seg : g];
+          for (int k = 0; k < p.k_groups; ++k, ++it) {
+            const uint32_t s = it % kPromptStages;
+            if (!wait_bounded<true>(ptx::smem_addr(&ctl->empty[s]), ((it / kPromptStages) & 1u) ^ 1u, abort_flag,
+                                    p.status)) {
+              ok = false;
+              break;
+            }
+            // Both CTAs' copies complete on the leader's barrier.
+            const uint32_t full = ptx::smem_addr(&ctl->full[s]);
+            const uint32_t full_leader = ptx::mapa_shared(full, 0);
+            const uint32_t sx = ptx::smem_addr(base + s * kPromptStage);
+            if (cta == 0) ptx::mbar_arrive_expect_tx(full, 2 * kPromptStage);
+            ptx::tma_load_2d_pair(sx, mx, full_leader, k * (KB / 2), x_row);
+            ptx::tma_load_2d_pair(sx + kBoxA, mw, full_leader, k * (KB / 2), w_row);
+          }
+        }
+      }
+      // Every copy lands before the CTAs can exit; the leader's barriers count both CTAs' copies.
+      if (cta == 0) {
+        const uint32_t first = it > kPromptStages ? it - kPromptStages : 0;
+        for (uint32_t j = first; j < it; ++j)
+          wait_bounded(ptx::smem_addr(&ctl->full[j % kPromptStages]), (j / kPromptStages) & 1u, abort_flag, p.status,
+                       true);
+      } else if (*abort_flag) {
+        // The peer cannot observe its own copies; give any in flight time to land (give-up path only).
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (ptx::globaltimer_ns() - t0 < 100000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && cta == 0) {
+      // ------------------------------------------------------------ MMA issuer (leader)
+      constexpr uint32_t idesc = idesc_mx(PM, PN);
+      uint32_t it = 0, chunk = 0, tile = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units, ++tile) {
+        // The shared columns are back from the tile before; the rest of this accumulator was read
+        // before that, by the same threads.
+        if (tile > 0 &&
+            !wait_bounded<true>(ptx::smem_addr(&ctl->tempty), (tile - 1) & 1u, abort_flag, p.status))
+          break;
+        ptx::tc_fence_after();
+        const uint32_t acc = tmem + (tile & 1u) * (PN - kShared);
+        uint32_t accumulate = 0;
+        for (int seg = 0; seg < p.n_segs && ok; ++seg) {
+          for (int k0 = 0; k0 < p.k_groups && ok; k0 += kChunk, ++chunk) {
+            const uint32_t buf = chunk & 1u;
+            if (!wait_bounded<true>(ptx::smem_addr(&ctl->sf_full[buf]), (chunk >> 1) & 1u, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            const uint32_t sf = tmem + kPromptSf + buf * 16;
+            const int n = min(kChunk, p.k_groups - k0);
+            for (int k = 0; k < n; ++k, ++it) {
+              const uint32_t s = it % kPromptStages;
+              if (!wait_bounded(ptx::smem_addr(&ctl->full[s]), (it / kPromptStages) & 1u, abort_flag, p.status)) {
+                ok = false;
+                break;
+              }
+              ptx::tc_fence_after();
+              const uint32_t sx = ptx::smem_addr(base + s * kPromptStage);
+              const uint64_t xdesc = ptx::sw128_kmajor_desc(sx);
+              const uint64_t wdesc = ptx::sw128_kmajor_desc(sx + kBoxA);
+              const uint32_t id = idesc | idesc_scale_byte(static_cast<uint32_t>(k));
+#pragma unroll
+              for (int j = 0; j < KB / 32; ++j) {
+                umma_mx_pair(acc, xdesc + 2 * j, wdesc + 2 * j, id, sf, sf + 4, accumulate);
+                accumulate = 1;
+              }
+              ptx::umma_commit_pair(ptx::smem_addr(&ctl->empty[s]), 0x3);
+            }
+            ptx::umma_commit_pair(ptx::smem_addr(&ctl->sf_empty[buf]), 0x3);
+          }
+        }
+        if (!ok) break;
+        ptx::umma_commit_pair(ptx::smem_addr(&ctl->tfull[tile & 1u]), 0x3);
+      }
+      ptx::umma_commit_pair(ptx::smem_addr(&ctl->drain), 0x3);
+      wait_bounded<true>(ptx::smem_addr(&ctl->drain), 0, abort_flag, p.status, true);
+    } else if (lane == 0) {
+      // The peer's shared memory feeds the leader's MMAs until the drain arrives.
+      wait_bounded<true>(ptx::smem_addr(&ctl->drain), 0, abort_flag, p.status, true);
+    }
+  } else if (warp < 6) {
+    // -------------------------------------------------------------- epilogue: a row to a thread
+    const int q = warp & 3;
+    const uint32_t quarter = static_cast<uint32_t>(q * 32) << 16;
+    const uint32_t staging = ptx::smem_addr(base) + kPromptStages * kPromptStage +
+                             static_cast<uint32_t>(warp - 2) * kStagingWarp;
+    const uint32_t tempty = ptx::mapa_shared(ptx::smem_addr(&ctl->tempty), 0);
+    auto release = [&]() {
+      ptx::tc_fence_before();
+      ptx::mbar_arrive_cluster(tempty);
+    };
+    uint32_t tile = 0;
+    for (int t = unit; t < total; t += units, ++tile) {
+      int g, mt, nt;
+      decode_tile(p, t, g, mt, nt);
+      if (!__all_sync(0xffffffffu, wait_bounded<true>(ptx::smem_addr(&ctl->tfull[tile & 1u]), (tile >> 1) & 1u,
+                                                      abort_flag, p.status)))
+        break;
+      ptx::tc_fence_after();
+      const int row0 = mt * PM + static_cast<int>(cta) * BM + q * 32;
+      const __nv_bfloat16* bias = p.bias[g];
+      auto drain = [&](auto acc_tag) {
+        constexpr int kAcc = decltype(acc_tag)::value;
+        const uint32_t taddr = tmem + quarter + kAcc * (PN - kShared);
+        float y[128];
+        if constexpr (kGlu) {
+          output_group<true, kAcc>(p, bias, taddr, nt * BM, y, true, release);
+          store_group(p, g, y, staging, row0, nt * BM, lane);
+        } else {
+          // The group with the shared columns first: the upper one of accumulator 0, the lower of 1.
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            const int h = kAcc == 0 ? 1 - i : i;
+            const int col0 = nt * PN + h * 128;
+            output_group<false, kAcc>(p, bias, taddr + h * 128, col0, y, i == 0, release);
+            if (col0 < p.n_out) store_group(p, g, y, staging, row0, col0, lane);
+          }
+        }
+      };
+      if ((tile & 1u) == 0)
+        drain(std::integral_constant<int, 0>{});
+      else
+        drain(std::integral_constant<int, 1>{});
+    }
+  } else {
+    // -------------------------------------------------------------- scale words
+    const int q = warp & 3;
+    const uint32_t quarter = static_cast<uint32_t>(q * 32) << 16;
+    uint32_t chunk = 0;
+    bool ok = true;
+    for (int t = unit; t < total && ok; t += units) {
+      int g, mt, nt;
+      decode_tile(p, t, g, mt, nt);
+      const int x_row = mt * PM + static_cast<int>(cta) * BM;
+      for (int seg = 0; seg < p.n_segs && ok; ++seg) {
+        const uint8_t* sx = p.sx[p.n_segs > 1 ? seg : 0];
+        const uint8_t* sw = p.sw[p.n_segs > 1 ? seg : g];
+        for (int k0 = 0; k0 < p.k_groups; k0 += kChunk, ++chunk) {
+          const int n = min(kChunk, p.k_groups - k0);
+          const uint32_t buf = chunk & 1u;
+          uint32_t x[4], w0[4], w1[4];
+          token_words<4>(p, sx, x_row, k0, n, lane, x);
+          weight_words(p, sw, kGlu ? nt * BM : nt * PN, k0, n, lane, w0);
+          weight_words(p, sw, kGlu ? p.up_row + nt * BM : nt * PN + BM, k0, n, lane, w1);
+          if (!__all_sync(0xffffffffu, wait_bounded<true>(ptx::smem_addr(&ctl->sf_empty[buf]),
+                                                          ((chunk >> 1) & 1u) ^ 1u, abort_flag, p.status))) {
+            ok = false;
+            break;
+          }
+          const uint32_t sf = tmem + quarter + kPromptSf + buf * 16;
+          tmem_st_x4(sf, x);
+          tmem_st_x4(sf + 4, w0);
+          tmem_st_x4(sf + 8, w1);
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&ctl->sf_full[buf]), 0));
+        }
+      }
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
@@ -515,6 +891,76 @@ tp_status launch_tokens(Fp8Params& p, cudaStream_t stream) {
   return TP_OK;
 }
 
+// CTA pairs of the prompt kernel that can be resident at once (cached per device).
+template <bool kGlu>
+tp_status resident_pairs(int* n) {
+  static std::mutex mu;
+  static int cached[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  std::lock_guard<std::mutex> lock(mu);
+  int& c = cached[dev & 63];
+  if (c == 0) {
+    e = cudaFuncSetAttribute(fp8_prompt_kernel<kGlu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kPromptSmem));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(256, 1, 1);
+    cfg.blockDim = dim3(kPromptThreads, 1, 1);
+    cfg.dynamicSmemBytes = kPromptSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int k = 0;
+    e = cudaOccupancyMaxActiveClusters(&k, fp8_prompt_kernel<kGlu>, &cfg);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+    if (k < 1) return fail(TP_ERR_UNSUPPORTED, "no CTA pair of the kernel fits on this device");
+    c = k;
+  }
+  *n = c;
+  return TP_OK;
+}
+
+template <bool kGlu>
+tp_status launch_prompt(const Fp8Params& p, cudaStream_t stream) {
+  int pairs = 0;
+  tp_status st = resident_pairs<kGlu>(&pairs);
+  if (st != TP_OK) return st;
+  const int64_t tiles = static_cast<int64_t>(p.n_groups) * p.n_tiles * p.t_tiles;
+  if (tiles > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many tiles (%lld)", (long long)tiles);
+  if (tiles < pairs) pairs = static_cast<int>(tiles);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(pairs), 1, 1);
+  cfg.blockDim = dim3(kPromptThreads, 1, 1);
+  cfg.dynamicSmemBytes = kPromptSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_prompt_kernel<kGlu>, p);
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 projection launch");
+  return TP_OK;
+}
+
+// Token tiles that sweep the weight tiles together: all of them while their operand fits L2
+// comfortably (each weight tile is then read from HBM once), else groups of about 16, evenly sized.
+int choose_group_m(int t_tiles, int64_t x_bytes) {
+  if (x_bytes <= (64ll << 20)) return t_tiles;
+  const int groups = ceil_div(t_tiles, 16);
+  return ceil_div(t_tiles, groups);
+}
+
 // The operands of a call, checked.
 struct Fp8Call {
   const void* const* x;         // one (shared) or tp_degree
@@ -531,7 +977,9 @@ tp_status run_fp8(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   p.status = status_word();
   if (p.status == nullptr) return fail(TP_ERR_CUDA, "cannot locate the kernel status word");
   const bool glu = p.act == TP_ACT_SWIGLU;
-  const int tn = c.T <= 16 ? 16 : c.T <= 32 ? 32 : c.T <= 64 ? 64 : 128;
+  const char* force = getenv("TP_FP8_FORCE");
+  const bool prompt = force ? force[0] == 'p' : c.T > 128;
+  const int tn = prompt ? BM : c.T <= 16 ? 16 : c.T <= 32 ? 32 : c.T <= 64 ? 64 : 128;  // rows of an X box
   for (int r = 0; r < c.p; ++r) {
     tp_status st = operand_map(&p.map_w[r], c.w[r], c.K, c.w_rows, c.K, BM);
     if (st != TP_OK) return st;
@@ -548,6 +996,12 @@ tp_status run_fp8(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   p.n_out = static_cast<int>(c.n_out);
   p.up_row = static_cast<int>(c.w_rows / 2);
   p.k_groups = ceil_div(c.K, KB);
+  if (prompt) {
+    p.n_tiles = ceil_div(c.n_out, glu ? BM : PN);
+    p.t_tiles = ceil_div(c.T, PM);
+    p.group_m = choose_group_m(p.t_tiles, c.T * c.K * p.n_segs);
+    return glu ? launch_prompt<true>(p, stream) : launch_prompt<false>(p, stream);
+  }
   p.n_tiles = ceil_div(c.n_out, BM);
   p.t_tiles = ceil_div(c.T, tn);
   switch (tn) {
