@@ -10,8 +10,10 @@
 //
 // Scale bytes reach tensor memory as 32-bit words of four consecutive groups (a "chunk", K = 512):
 // operand row r's word lies in lane r % 32 of column r / 32, the same in each 32-lane quarter.
-// Four warps load the bytes of a chunk and store the words while the MMAs of the previous chunk
-// run (two buffers).
+// Four warps load a chunk's words, a row to a lane, and leave them in shared memory in that order;
+// the MMA thread copies them (tcgen05.cp) in front of the chunk's MMAs, which it stays in order
+// with.  (Stored to tensor memory by the warps themselves, tcgen05.st waited for the MMAs in
+// flight: 200 ns without work for the tensor core in each chunk of 1.4 us.)
 //
 // fp8_tokens_kernel: the weight rows are the MMA's M (128 lanes), the tokens its N.  A launch is
 // bound by the bytes of W, each read once: a ring of 128-byte-wide TMA boxes, and, when there are
@@ -70,7 +72,11 @@ struct Fp8Params {
   int k_groups;    // scale groups (128 features) per segment
   int n_tiles, t_tiles;
   int splits;      // tokens kernel: cluster CTAs that share a tile's K
-  int group_m;     // prompt kernel: token tiles that sweep the weight tiles together
+  int t_items, n_items;  // prompt kernel: work items (pairs of tiles along the dimension a cluster shares)
+  int group_m;           // prompt kernel: token items that sweep the weight items together
+  bool share_x;          // prompt kernel, clusters of two pairs: n-adjacent tiles share X (else m-adjacent, W)
+  bool x_words, w_words;  // scale chunks can be read as aligned 32-bit words
+  bool bias_vec;          // every bias is 16-byte aligned
   int act;
 };
 
@@ -104,10 +110,18 @@ __host__ __device__ constexpr uint32_t idesc_mx(int m, int n) {
 // The byte of its scale words that an instruction uses, for A and B alike.
 __device__ __forceinline__ uint32_t idesc_scale_byte(uint32_t k) { return (k << 4) | (k << 29); }
 
-__device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint32_t (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3])
-               : "memory");
+// Scale words of 128 rows from shared memory (32 x 16 bytes, dense) to four columns of tensor
+// memory, the same in every 32-lane quarter; in order with the MMAs of the issuing thread.
+// kPair: in both CTAs of a pair, each from its own shared memory.
+template <bool kPair>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+  const uint64_t desc = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu)     // start address
+                        | (static_cast<uint64_t>(128 >> 4) << 32)         // stride of 8-row groups
+                        | (static_cast<uint64_t>(1) << 46);               // descriptor version; no swizzle
+  if constexpr (kPair)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -121,16 +135,12 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 
 // Bounded wait: true when the phase completed, false when this CTA is giving up.
 // kCluster: the phase's arrivals may come from the other CTA of a pair.
-template <bool kCluster = false>
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                             unsigned int* status, bool ignore_abort = false) {
-  auto probe = [&]() {
-    return kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
-  };
-  if (probe()) return true;
+template <bool kCluster>
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* status,
+                                       bool ignore_abort) {
   const uint64_t t0 = ptx::globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (probe()) return true;
+    if (kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
     if ((i & 63u) == 0) {
       if (!ignore_abort && *abort_flag) return false;
       if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -141,40 +151,50 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
     }
   }
 }
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                             unsigned int* status, bool ignore_abort = false) {
+  if (kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+  return wait_slow<kCluster>(bar, parity, abort_flag, status, ignore_abort);
+}
 
 // ---------------------------------------------------------------- scale words
-// Bytes [0, n) of p as a little-endian word (n <= 4, warp-uniform); one load where p allows it.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int n) {
-  if (n == kChunk && (reinterpret_cast<uintptr_t>(p) & 3u) == 0) return *reinterpret_cast<const uint32_t*>(p);
+constexpr uint32_t kScaleOne = 0x7F7F7F7Fu;  // 2^0 for rows past the operand (their products are not stored)
+
+// One row's word: scale bytes [kg, kg + n) of scale row (row >> kShift).  `words` (host: every
+// row's chunks are aligned whole words) keeps the load free of branches, so that a thread's loads
+// are in flight together.
+template <int kShift>
+__device__ __forceinline__ uint32_t load_word(const uint8_t* s, int64_t ld, int rows, int row, int kg, int n,
+                                              bool words) {
+  const uint8_t* at = s + static_cast<int64_t>(row >> kShift) * ld + kg;
+  if (words) return row < rows ? __ldg(reinterpret_cast<const uint32_t*>(at)) : kScaleOne;
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < kChunk; ++i)
-    if (i < n) w |= static_cast<uint32_t>(p[i]) << (8 * i);
+    w |= (row < rows && i < n ? static_cast<uint32_t>(__ldg(at + i)) : 0x7Fu) << (8 * i);
   return w;
 }
-constexpr uint32_t kScaleOne = 0x7F7F7F7Fu;  // 2^0 for rows past the operand (their products are not stored)
 
-// Four columns of words for 128 weight rows from row `row0`; this lane's rows are row0 + 32 c + lane.
-__device__ __forceinline__ void weight_words(const Fp8Params& p, const uint8_t* sw, int row0, int kg, int n, int lane,
-                                             uint32_t (&w)[4]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int row = row0 + 32 * c + lane;
-    w[c] = row < p.w_rows
-               ? scale_word(sw + static_cast<int64_t>(row / kFp8Group) * p.k_groups + kg, n)
-               : kScaleOne;
-  }
+constexpr int kSfBufs = 4;               // chunks of scale words in shared memory
+constexpr uint32_t kSfRows = 32 * 16;    // bytes of 128 rows' words
+__device__ __forceinline__ void store_word(uint32_t rows_at, int row, uint32_t w) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(rows_at + static_cast<uint32_t>((row & 31) * 16 + (row >> 5) * 4)), "r"(w)
+               : "memory");
 }
-// The same for 32 * kCols tokens.
-template <int kCols>
-__device__ __forceinline__ void token_words(const Fp8Params& p, const uint8_t* sx, int t0, int kg, int n, int lane,
-                                            uint32_t (&w)[4]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int t = t0 + 32 * c + lane;
-    w[c] = (c < kCols && t < p.T) ? scale_word(sx + static_cast<int64_t>(t) * p.ld_sx + kg, n) : kScaleOne;
+
+// The chunks of K in the order every role of a kernel walks them.
+struct ChunkWalk {
+  int seg, kg;  // segment and first scale group
+  __device__ __forceinline__ void start(int chunk, int seg_chunks) {
+    seg = chunk / seg_chunks;
+    kg = (chunk - seg * seg_chunks) * kChunk;
   }
-}
+  __device__ __forceinline__ void next(int k_groups) {
+    kg += kChunk;
+    if (kg >= k_groups) kg = 0, ++seg;
+  }
+};
 
 // ---------------------------------------------------------------- activation
 // GELU(tanh) as x / (1 + e^(-2u)), u = sqrt(2/pi) (x + 0.044715 x^3); SiLU as x / (1 + e^(-x)).
@@ -183,6 +203,29 @@ __device__ __forceinline__ float gelu_tanh_f(float x) {
   return __fdividef(x, 1.0f + __expf(-2.0f * u));
 }
 __device__ __forceinline__ float silu_f(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
+
+// v[e] += bias[col + e] for columns inside the output (n_out is a multiple of 8).
+template <int kN>
+__device__ __forceinline__ void add_bias(float (&v)[kN], const __nv_bfloat16* bias, int col, int n_out, bool vec) {
+  static_assert(kN % 8 == 0, "read eight at a time");
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 8) {
+      uint4 b = make_uint4(0, 0, 0, 0);
+      if (col + i < n_out) b = __ldg(reinterpret_cast<const uint4*>(bias + col + i));
+      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[i + 2 * e] += __uint_as_float(w[e] << 16);
+        v[i + 2 * e + 1] += __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (col + i < n_out) v[i] += __bfloat162float(bias[col + i]);
+  }
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
@@ -209,12 +252,13 @@ struct TokensCfg {
                                         : ACC_COLS + 2 * SF_COLS <= 128 ? 128
                                         : ACC_COLS + 2 * SF_COLS <= 256 ? 256
                                                                         : 512;
-  static constexpr size_t SMEM = 1024 + RING;
+  static constexpr uint32_t SF_BYTES = (W_TILES + 1) * kSfRows;   // one chunk's words: W, then tokens
+  static constexpr size_t SMEM = 1024 + RING + kSfBufs * SF_BYTES;
 };
 
 struct alignas(8) TokensCtrl {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t sf_full[2], sf_empty[2];
+  uint64_t sf_full[kSfBufs], sf_empty[kSfBufs];
   uint64_t done;
   uint32_t tmem_base;
   int abort;
@@ -238,7 +282,7 @@ __global__ void __launch_bounds__(kTokensThreads, 1) fp8_tokens_kernel(const __g
       ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kSfBufs; ++b) {
       ptx::mbar_init(ptx::smem_addr(&ctl->sf_full[b]), 128);
       ptx::mbar_init(ptx::smem_addr(&ctl->sf_empty[b]), 1);
     }
@@ -276,6 +320,7 @@ __global__ void __launch_bounds__(kTokensThreads, 1) fp8_tokens_kernel(const __g
   // An output's operands: its rank's (colwise), or every rank's in turn (rowwise).
   auto w_of = [&](int seg) { return p.n_segs > 1 ? seg : g; };
   auto x_of = [&](int seg) { return p.n_segs > 1 ? seg : 0; };
+  const uint32_t sf_base = ptx::smem_addr(base) + C::RING;
   bool gave_up = false;
 
   if (warp == 0) {
@@ -319,9 +364,12 @@ __global__ void __launch_bounds__(kTokensThreads, 1) fp8_tokens_kernel(const __g
         const int i = c - c0;
         const int seg = c / seg_chunks;
         const int n = min(kChunk, p.k_groups - (c - seg * seg_chunks) * kChunk);
-        const uint32_t buf = i & 1u;
-        if (!wait_bounded(ptx::smem_addr(&ctl->sf_full[buf]), (i >> 1) & 1u, abort_flag, p.status)) break;
-        const uint32_t sf = tmem + C::ACC_COLS + buf * C::SF_COLS;
+        const uint32_t buf = i % kSfBufs;
+        if (!wait_bounded(ptx::smem_addr(&ctl->sf_full[buf]), (i / kSfBufs) & 1u, abort_flag, p.status)) break;
+        const uint32_t sf = tmem + C::ACC_COLS + (i & 1) * C::SF_COLS;
+        const uint32_t words = sf_base + buf * C::SF_BYTES;
+#pragma unroll
+        for (int a = 0; a <= C::W_TILES; ++a) copy_scales<false>(sf + 4 * a, words + a * kSfRows);
         for (int k = 0; k < n; ++k, ++it) {
           const uint32_t s = it % C::STAGES;
           if (!wait_bounded(ptx::smem_addr(&ctl->full[s]), (it / C::STAGES) & 1u, abort_flag, p.status)) {
@@ -353,28 +401,35 @@ __global__ void __launch_bounds__(kTokensThreads, 1) fp8_tokens_kernel(const __g
     // -------------------------------------------------------------- scales, then the partial tile
     const int q = warp & 3;  // TMEM lane quarter this warp may access
     const uint32_t quarter = static_cast<uint32_t>(q * 32) << 16;
-    for (int c = c0; c < c1; ++c) {
-      const int i = c - c0;
-      const int seg = c / seg_chunks;
-      const int kg = (c - seg * seg_chunks) * kChunk;
-      const int n = min(kChunk, p.k_groups - kg);
-      const uint32_t buf = i & 1u;
-      uint32_t w[4], u[4], x[4];
-      const uint8_t* sw = p.sw[w_of(seg)];
-      weight_words(p, sw, w_row0, kg, n, lane, w);
-      if constexpr (kGlu) weight_words(p, sw, p.up_row + w_row0, kg, n, lane, u);
-      token_words<(TN + 31) / 32>(p, p.sx[x_of(seg)], t0, kg, n, lane, x);
-      if (!__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&ctl->sf_empty[buf]), ((i >> 1) & 1u) ^ 1u, abort_flag,
-                                                p.status))) {
+    const int row = q * 32 + lane;
+    uint32_t w_next, u_next = 0, x_next;
+    auto load = [&](const ChunkWalk& at) {
+      const int n = min(kChunk, p.k_groups - at.kg);
+      const uint8_t* sw = p.sw[w_of(at.seg)];
+      w_next = load_word<7>(sw, p.k_groups, p.w_rows, w_row0 + row, at.kg, n, p.w_words);
+      if constexpr (kGlu) u_next = load_word<7>(sw, p.k_groups, p.w_rows, p.up_row + w_row0 + row, at.kg, n, p.w_words);
+      x_next = load_word<0>(p.sx[x_of(at.seg)], p.ld_sx, row < TN ? p.T : 0, t0 + row, at.kg, n, p.x_words);
+    };
+    ChunkWalk at;
+    at.start(c0, seg_chunks);
+    load(at);
+    for (int i = 0; i < c1 - c0; ++i) {
+      const uint32_t buf = i % kSfBufs;
+      const uint32_t w = w_next, u = u_next, x = x_next;
+      if (i + 1 < c1 - c0) {
+        at.next(p.k_groups);
+        load(at);
+      }
+      if (!__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&ctl->sf_empty[buf]), ((i / kSfBufs) & 1u) ^ 1u,
+                                                abort_flag, p.status))) {
         gave_up = true;
         break;
       }
-      const uint32_t sf = tmem + quarter + C::ACC_COLS + buf * C::SF_COLS;
-      tmem_st_x4(sf, w);
-      if constexpr (kGlu) tmem_st_x4(sf + 4, u);
-      tmem_st_x4(sf + 4 * C::W_TILES, x);
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before();
+      const uint32_t words = sf_base + buf * C::SF_BYTES;
+      store_word(words, row, w);
+      if constexpr (kGlu) store_word(words + kSfRows, row, u);
+      store_word(words + C::W_TILES * kSfRows, row, x);
+      ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(ptx::smem_addr(&ctl->sf_full[buf]));
     }
     if (!gave_up)
@@ -461,84 +516,105 @@ constexpr int kPromptStages = 6;
 constexpr uint32_t kPromptStage = 2 * kBoxA;         // a CTA's 128 tokens and its 128 weight rows
 constexpr uint32_t kShared = 32;                     // columns the two accumulators share
 constexpr uint32_t kPromptSf = 2 * PN - kShared;     // scale words: two buffers of 16 columns (X 4, W 8)
-constexpr uint32_t kStagingRow = 256;                // epilogue staging: 32 rows a warp, 128 bf16 each
-constexpr uint32_t kStagingWarp = 32 * kStagingRow;
+constexpr uint32_t kStagingWarp = 32 * 128;          // epilogue staging: 32 rows a warp, 128 codes or 64 bf16 each
+constexpr uint32_t kPromptSfBytes = 3 * kSfRows;     // one chunk's words: X, W rows 0..127, W rows 128..255
 constexpr int kPromptThreads = 320;                  // producer, MMA issuer, 4 epilogue and 4 scale warps
-constexpr size_t kPromptSmem = 1024 + kPromptStages * kPromptStage + 4 * kStagingWarp;
+constexpr size_t kPromptSmem = 1024 + kPromptStages * kPromptStage + 4 * kStagingWarp + kSfBufs * kPromptSfBytes;
 static_assert(kPromptSf + 32 <= 512, "accumulators and scale words fill tensor memory");
 
 struct alignas(8) PromptCtrl {
   uint64_t full[kPromptStages], empty[kPromptStages];
-  uint64_t sf_full[2], sf_empty[2];
+  uint64_t sf_full[kSfBufs], sf_empty[kSfBufs];
   uint64_t tfull[2], tempty;
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
 
-__device__ __forceinline__ void decode_tile(const Fp8Params& p, int t, int& g, int& mt, int& nt) {
-  // group_m token tiles sweep the weight tiles together, so that CTAs that run at the same time
+// A work item is a tile, or with clusters of two pairs two adjacent tiles.
+__device__ __forceinline__ void decode_item(const Fp8Params& p, int t, int& g, int& mt, int& nt) {
+  // group_m token items sweep the weight items together, so that CTAs that run at the same time
   // share both operands through L2.
-  const int per_out = p.t_tiles * p.n_tiles;
+  const int per_out = p.t_items * p.n_items;
   g = t / per_out;
   const int in_out = t - g * per_out;
-  const int span = p.group_m * p.n_tiles;
+  const int span = p.group_m * p.n_items;
   const int first = in_out / span * p.group_m;
-  const int m = min(p.group_m, p.t_tiles - first);
+  const int m = min(p.group_m, p.t_items - first);
   const int in_span = in_out % span;
   mt = first + in_span % m;
   nt = in_span / m;
 }
 
-// One group of 128 output columns of this thread's row, from the accumulator's columns at
-// `taddr` (SwiGLU: gate there, up at `uaddr`), rows and columns past the output included.
-// kAcc: which accumulator; `release` is called once its shared columns are in registers.
-template <bool kGlu, int kAcc, typename Release>
+// One group of 128 output columns of this thread's row, from the accumulator's columns at `taddr`
+// (SwiGLU: gate there, up 128 columns on), rows and columns past the output included.  `early`
+// holds the accumulator's shared columns, already read: those of accumulator 0 are its last 32 (up
+// columns 96..127, or the upper group's), those of accumulator 1 its first 32.
+// kHeld: this group has them.
+template <bool kGlu, int kAcc, bool kHeld>
 __device__ __forceinline__ void output_group(const Fp8Params& p, const __nv_bfloat16* bias, uint32_t taddr, int col0,
-                                             float (&y)[128], bool holds_shared, Release release) {
+                                             float (&y)[128], const uint32_t (&early)[32]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    // Accumulator 0 shares its last 32 columns, accumulator 1 its first.
-    const int j = (i + (kAcc == 0 ? 6 : 0)) & 7;
+    const int j = (i + (kAcc == 0 ? 6 : 0)) & 7;  // the shared columns' part first: it frees their registers
     uint32_t v[16], u[16];
-    ptx::tmem_ld_32x32b_x16(taddr + 16 * j, v);
-    if constexpr (kGlu) ptx::tmem_ld_32x32b_x16(taddr + 128 + 16 * j, u);
+    const bool held = i < 2 && kHeld;
+    if (!held || (kGlu && kAcc == 0)) ptx::tmem_ld_32x32b_x16(taddr + 16 * j, v);
+    if (kGlu && (!held || kAcc == 1)) ptx::tmem_ld_32x32b_x16(taddr + 128 + 16 * j, u);
     ptx::tmem_ld_wait();
-    if (i == 1 && holds_shared) release();
+    if (held)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) (kGlu && kAcc == 0 ? u : v)[e] = early[16 * (i & 1) + e];
+    const int col = col0 + 16 * j;
+    float a[16], b[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const int col = col0 + 16 * j + e;
-      float a = __uint_as_float(v[e]);
-      if (bias != nullptr && col < p.n_out) a += __bfloat162float(bias[col]);
-      if constexpr (kGlu) {
-        float b = __uint_as_float(u[e]);
-        if (bias != nullptr && col < p.n_out) b += __bfloat162float(bias[p.up_row + col]);
-        y[16 * j + e] = silu_f(a) * b;
-      } else {
-        y[16 * j + e] = a;
-      }
+      a[e] = __uint_as_float(v[e]);
+      if constexpr (kGlu) b[e] = __uint_as_float(u[e]);
     }
+    if (bias != nullptr) {  // uniform
+      add_bias(a, bias, col, p.n_out, p.bias_vec);
+      if constexpr (kGlu) add_bias(b, bias + p.up_row, col, p.n_out, p.bias_vec && p.up_row % 8 == 0);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[16 * j + e] = kGlu ? silu_f(a[e]) * b[e] : a[e];
   }
   if (!kGlu && p.act == TP_ACT_GELU_TANH)
 #pragma unroll
     for (int i = 0; i < 128; ++i) y[i] = gelu_tanh_f(y[i]);
 }
 
-// Store a warp's 32 rows x 128 columns: rows leave their threads through swizzled 16-byte pieces
-// of shared memory, so that a global store instruction writes whole 128- or 256-byte row segments.
+// Copy a warp's 32 staged rows of 128 bytes (swizzled 16-byte pieces) out, eight lanes to a row, so
+// that a store instruction writes whole row segments.  `out` is row 0's first byte.
+__device__ __forceinline__ void store_rows(uint8_t* out, int64_t row_bytes, uint32_t staging, int rows, int bytes,
+                                           int lane) {
+  __syncwarp();
+  const int c = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const int r = i + (lane >> 3);
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(staging + static_cast<uint32_t>(r * 128) + (static_cast<uint32_t>(c ^ (r & 7)) << 4)));
+    if (r < rows && 16 * c < bytes)
+      *reinterpret_cast<uint4*>(out + r * row_bytes + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();  // the buffer may be written again
+}
+
+// Store a warp's 32 rows x 128 columns of values, a row to a thread.
 __device__ __forceinline__ void store_group(const Fp8Params& p, int g, const float (&y)[128], uint32_t staging,
                                             int row0, int col0, int lane) {
-  const bool fp8 = p.out_scales[g] != nullptr;  // uniform
-  uint32_t byte = 0;
-  __syncwarp();  // the previous group has left the buffer
-  if (fp8) {
+  const int rows = p.T - row0, cols = p.n_out - col0;
+  const uint32_t row = staging + static_cast<uint32_t>(lane) * 128;
+  if (p.out_scales[g] != nullptr) {  // uniform
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 128; ++i)
-      if (col0 + (i & ~15) < p.n_out) m = max(m, abs_bits(y[i]));  // n_out is a multiple of 16
-    byte = e8m0_of_amax(m);
+      if ((i & ~15) < cols) m = max(m, abs_bits(y[i]));  // n_out is a multiple of 16
+    const uint32_t byte = e8m0_of_amax(m);
     const float inv = e8m0_inverse(byte);
-    const uint32_t row = staging + static_cast<uint32_t>(lane) * 128;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       uint32_t w[4];
@@ -548,36 +624,28 @@ __device__ __forceinline__ void store_group(const Fp8Params& p, int g, const flo
                       y[16 * c + 4 * e + 3] * inv);
       ptx::st_shared_v4(row + (static_cast<uint32_t>(c ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
     }
+    store_rows(static_cast<uint8_t*>(p.out[g]) + row0 * p.ldo + col0, p.ldo, staging, rows, cols, lane);
+    if (lane < rows)
+      p.out_scales[g][(row0 + lane) * p.ld_os + col0 / kFp8Group] = static_cast<uint8_t>(byte);
   } else {
-    const uint32_t row = staging + static_cast<uint32_t>(lane) * 256;
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-      ptx::st_shared_v4(row + (static_cast<uint32_t>(c ^ (lane & 7)) << 4), pack_bf16(y[8 * c], y[8 * c + 1]),
-                        pack_bf16(y[8 * c + 2], y[8 * c + 3]), pack_bf16(y[8 * c + 4], y[8 * c + 5]),
-                        pack_bf16(y[8 * c + 6], y[8 * c + 7]));
+    for (int h = 0; h < 128; h += 64) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int i = h + 8 * c;
+        ptx::st_shared_v4(row + (static_cast<uint32_t>(c ^ (lane & 7)) << 4), pack_bf16(y[i], y[i + 1]),
+                          pack_bf16(y[i + 2], y[i + 3]), pack_bf16(y[i + 4], y[i + 5]), pack_bf16(y[i + 6], y[i + 7]));
+      }
+      store_rows(static_cast<uint8_t*>(p.out[g]) + 2 * (row0 * p.ldo + col0 + h), 2 * p.ldo, staging, rows,
+                 2 * (cols - h), lane);
+    }
   }
-  __syncwarp();
-  const int pieces = fp8 ? 8 : 16;                    // 16-byte pieces of a row
-  const int per_piece = fp8 ? 16 : 8;                 // columns
-  const int rows_at_once = 32 / pieces;
-  const int c = lane % pieces;
-  const int64_t esize = fp8 ? 1 : 2;
-  uint8_t* out = static_cast<uint8_t*>(p.out[g]) + static_cast<int64_t>(col0 + c * per_piece) * esize;
-  const bool col_on = col0 + c * per_piece < p.n_out;
-  for (int i = lane / pieces; i < 32; i += rows_at_once) {
-    uint32_t w[4];
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(staging + static_cast<uint32_t>(i * pieces * 16) + (static_cast<uint32_t>(c ^ (i & 7)) << 4)));
-    if (col_on && row0 + i < p.T)
-      *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + i) * p.ldo * esize) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  if (fp8 && row0 + lane < p.T)
-    p.out_scales[g][static_cast<int64_t>(row0 + lane) * p.ld_os + col0 / kFp8Group] = static_cast<uint8_t>(byte);
 }
 
-template <bool kGlu>
+// kQuad: clusters of two pairs on adjacent tiles that share an operand.  Each CTA loads half of its
+// rows of that operand and multicasts them to the CTA in its place in the other pair: a quarter
+// less is read from L2.  A stage is then free once both pairs' MMAs are done with it.
+template <bool kGlu, bool kQuad>
 __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __grid_constant__ Fp8Params p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ PromptCtrl ctl_mem;
@@ -586,20 +654,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
   volatile int* abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t cta = ptx::cluster_ctarank();  // 0 = leader
-  const int unit = static_cast<int>(blockIdx.x) / 2;
-  const int units = static_cast<int>(gridDim.x) / 2;
+  const uint32_t crank = ptx::cluster_ctarank();
+  const uint32_t cta = crank & 1u;                  // 0 = the pair's leader
+  const uint32_t leader = crank & ~1u;              // its cluster rank
+  const uint32_t pair = kQuad ? crank >> 1 : 0u;
+  const uint16_t pair_mask = static_cast<uint16_t>(0x3u << (2 * pair));
+  constexpr int kCtas = kQuad ? 4 : 2;
+  const int unit = static_cast<int>(blockIdx.x) / kCtas;
+  const int units = static_cast<int>(gridDim.x) / kCtas;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPromptStages; ++s) {
       ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
-      ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), kQuad ? 2 : 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kSfBufs; ++b) {
       ptx::mbar_init(ptx::smem_addr(&ctl->sf_full[b]), 256);
       ptx::mbar_init(ptx::smem_addr(&ctl->sf_empty[b]), 1);
-      ptx::mbar_init(ptx::smem_addr(&ctl->tfull[b]), 1);
     }
+    ptx::mbar_init(ptx::smem_addr(&ctl->tfull[0]), 1);
+    ptx::mbar_init(ptx::smem_addr(&ctl->tfull[1]), 1);
     ptx::mbar_init(ptx::smem_addr(&ctl->tempty), 256);
     ptx::mbar_init(ptx::smem_addr(&ctl->drain), 1);
     ctl->abort = 0;
@@ -617,7 +691,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
   pdl_launch_dependents();
   pdl_wait();
 
-  const int total = p.n_groups * p.t_tiles * p.n_tiles;
+  const uint32_t sf_base = ptx::smem_addr(base) + kPromptStages * kPromptStage + 4 * kStagingWarp;
+  const int total = p.n_groups * p.t_items * p.n_items;
+  // Work item t's output and this pair's tile.
+  auto tile_of = [&](int t, int& g, int& mt, int& nt) {
+    decode_item(p, t, g, mt, nt);
+    if (kQuad && p.share_x) nt = 2 * nt + static_cast<int>(pair);
+    if (kQuad && !p.share_x) mt = 2 * mt + static_cast<int>(pair);
+  };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -626,7 +707,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
         int g, mt, nt;
-        decode_tile(p, t, g, mt, nt);
+        tile_of(t, g, mt, nt);
         const int x_row = mt * PM + static_cast<int>(cta) * BM;
         const int w_row = kGlu ? (cta == 0 ? 0 : p.up_row) + nt * BM : nt * PN + static_cast<int>(cta) * BM;
         for (int seg = 0; seg < p.n_segs && ok; ++seg) {
@@ -641,11 +722,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
             }
             // Both CTAs' copies complete on the leader's barrier.
             const uint32_t full = ptx::smem_addr(&ctl->full[s]);
-            const uint32_t full_leader = ptx::mapa_shared(full, 0);
+            const uint32_t full_leader = ptx::mapa_shared(full, leader);
             const uint32_t sx = ptx::smem_addr(base + s * kPromptStage);
             if (cta == 0) ptx::mbar_arrive_expect_tx(full, 2 * kPromptStage);
-            ptx::tma_load_2d_pair(sx, mx, full_leader, k * (KB / 2), x_row);
-            ptx::tma_load_2d_pair(sx + kBoxA, mw, full_leader, k * (KB / 2), w_row);
+            const int kx = k * (KB / 2);
+            if constexpr (kQuad) {
+              const uint32_t half = pair * (kBoxA / 2);
+              const int row = static_cast<int>(pair) * (BM / 2);
+              const uint16_t both = static_cast<uint16_t>(0x5u << cta);  // this CTA's place in both pairs
+              if (p.share_x) {
+                ptx::tma_load_2d_pair_mc(sx + half, mx, full_leader, kx, x_row + row, both);
+                ptx::tma_load_2d_pair(sx + kBoxA, mw, full_leader, kx, w_row);
+              } else {
+                ptx::tma_load_2d_pair(sx, mx, full_leader, kx, x_row);
+                ptx::tma_load_2d_pair_mc(sx + kBoxA + half, mw, full_leader, kx, w_row + row, both);
+              }
+            } else {
+              ptx::tma_load_2d_pair(sx, mx, full_leader, kx, x_row);
+              ptx::tma_load_2d_pair(sx + kBoxA, mw, full_leader, kx, w_row);
+            }
           }
         }
       }
@@ -665,8 +760,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
   } else if (warp == 1) {
     if (lane == 0 && cta == 0) {
       // ------------------------------------------------------------ MMA issuer (leader)
+      // One thread issues a group's four MMAs in the time they run, 512 cycles, so the loop carries
+      // its addresses along instead of computing them (with them computed from the stage number
+      // it took 690 cycles a group and bounded the kernel).
       constexpr uint32_t idesc = idesc_mx(PM, PN);
-      uint32_t it = 0, chunk = 0, tile = 0;
+      const uint64_t x0 = ptx::sw128_kmajor_desc(ptx::smem_addr(base));
+      const uint32_t full0 = ptx::smem_addr(&ctl->full[0]), empty0 = ptx::smem_addr(&ctl->empty[0]);
+      const uint32_t sf_full0 = ptx::smem_addr(&ctl->sf_full[0]), sf_empty0 = ptx::smem_addr(&ctl->sf_empty[0]);
+      uint32_t stage = 0, phase = 0, chunk = 0, tile = 0;
+      uint64_t xdesc = x0;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units, ++tile) {
         // The shared columns are back from the tile before; the rest of this accumulator was read
@@ -678,39 +780,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
         const uint32_t acc = tmem + (tile & 1u) * (PN - kShared);
         uint32_t accumulate = 0;
         for (int seg = 0; seg < p.n_segs && ok; ++seg) {
-          for (int k0 = 0; k0 < p.k_groups && ok; k0 += kChunk, ++chunk) {
-            const uint32_t buf = chunk & 1u;
-            if (!wait_bounded<true>(ptx::smem_addr(&ctl->sf_full[buf]), (chunk >> 1) & 1u, abort_flag, p.status)) {
+          for (int left = p.k_groups; left > 0; left -= kChunk, ++chunk) {
+            const uint32_t buf = chunk % kSfBufs;
+            if (!wait_bounded<true>(sf_full0 + 8 * buf, (chunk / kSfBufs) & 1u, abort_flag, p.status)) {
               ok = false;
               break;
             }
-            const uint32_t sf = tmem + kPromptSf + buf * 16;
-            const int n = min(kChunk, p.k_groups - k0);
-            for (int k = 0; k < n; ++k, ++it) {
-              const uint32_t s = it % kPromptStages;
-              if (!wait_bounded(ptx::smem_addr(&ctl->full[s]), (it / kPromptStages) & 1u, abort_flag, p.status)) {
-                ok = false;
-                break;
-              }
-              ptx::tc_fence_after();
-              const uint32_t sx = ptx::smem_addr(base + s * kPromptStage);
-              const uint64_t xdesc = ptx::sw128_kmajor_desc(sx);
-              const uint64_t wdesc = ptx::sw128_kmajor_desc(sx + kBoxA);
-              const uint32_t id = idesc | idesc_scale_byte(static_cast<uint32_t>(k));
+            const uint32_t sf = tmem + kPromptSf + (chunk & 1u) * 16;
 #pragma unroll
-              for (int j = 0; j < KB / 32; ++j) {
-                umma_mx_pair(acc, xdesc + 2 * j, wdesc + 2 * j, id, sf, sf + 4, accumulate);
-                accumulate = 1;
+            for (int a = 0; a < 3; ++a)
+              copy_scales<true>(sf + 4 * a, sf_base + buf * kPromptSfBytes + a * kSfRows);
+#pragma unroll
+            for (int k = 0; k < kChunk; ++k) {
+              if (k < left) {
+                if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, p.status)) {
+                  ok = false;
+                  break;
+                }
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < KB / 32; ++j) {
+                  umma_mx_pair(acc, xdesc + 2 * j, xdesc + (kBoxA >> 4) + 2 * j,
+                               idesc | idesc_scale_byte(static_cast<uint32_t>(k)), sf, sf + 4, accumulate);
+                  accumulate = 1;
+                }
+                ptx::umma_commit_pair(empty0 + 8 * stage, kQuad ? 0xF : 0x3);
+                xdesc += kPromptStage >> 4;
+                if (++stage == kPromptStages) stage = 0, phase ^= 1u, xdesc = x0;
               }
-              ptx::umma_commit_pair(ptx::smem_addr(&ctl->empty[s]), 0x3);
             }
-            ptx::umma_commit_pair(ptx::smem_addr(&ctl->sf_empty[buf]), 0x3);
+            if (!ok) break;
+            ptx::umma_commit_pair(sf_empty0 + 8 * buf, pair_mask);
           }
         }
         if (!ok) break;
-        ptx::umma_commit_pair(ptx::smem_addr(&ctl->tfull[tile & 1u]), 0x3);
+        ptx::umma_commit_pair(ptx::smem_addr(&ctl->tfull[tile & 1u]), pair_mask);
       }
-      ptx::umma_commit_pair(ptx::smem_addr(&ctl->drain), 0x3);
+      ptx::umma_commit_pair(ptx::smem_addr(&ctl->drain), pair_mask);
       wait_bounded<true>(ptx::smem_addr(&ctl->drain), 0, abort_flag, p.status, true);
     } else if (lane == 0) {
       // The peer's shared memory feeds the leader's MMAs until the drain arrives.
@@ -722,15 +828,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
     const uint32_t quarter = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t staging = ptx::smem_addr(base) + kPromptStages * kPromptStage +
                              static_cast<uint32_t>(warp - 2) * kStagingWarp;
-    const uint32_t tempty = ptx::mapa_shared(ptx::smem_addr(&ctl->tempty), 0);
-    auto release = [&]() {
-      ptx::tc_fence_before();
-      ptx::mbar_arrive_cluster(tempty);
-    };
+    const uint32_t tempty = ptx::mapa_shared(ptx::smem_addr(&ctl->tempty), leader);
     uint32_t tile = 0;
     for (int t = unit; t < total; t += units, ++tile) {
       int g, mt, nt;
-      decode_tile(p, t, g, mt, nt);
+      tile_of(t, g, mt, nt);
       if (!__all_sync(0xffffffffu, wait_bounded<true>(ptx::smem_addr(&ctl->tfull[tile & 1u]), (tile >> 1) & 1u,
                                                       abort_flag, p.status)))
         break;
@@ -740,18 +842,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       auto drain = [&](auto acc_tag) {
         constexpr int kAcc = decltype(acc_tag)::value;
         const uint32_t taddr = tmem + quarter + kAcc * (PN - kShared);
+        // The shared columns first: the next tile's MMAs wait for them.
+        uint32_t early[32];
+        ptx::tmem_ld_32x32b_x32(tmem + quarter + PN - kShared, early);
+        ptx::tmem_ld_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive_cluster(tempty);
         float y[128];
         if constexpr (kGlu) {
-          output_group<true, kAcc>(p, bias, taddr, nt * BM, y, true, release);
+          output_group<true, kAcc, true>(p, bias, taddr, nt * BM, y, early);
           store_group(p, g, y, staging, row0, nt * BM, lane);
         } else {
           // The group with the shared columns first: the upper one of accumulator 0, the lower of 1.
-#pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            const int h = kAcc == 0 ? 1 - i : i;
-            const int col0 = nt * PN + h * 128;
-            output_group<false, kAcc>(p, bias, taddr + h * 128, col0, y, i == 0, release);
-            if (col0 < p.n_out) store_group(p, g, y, staging, row0, col0, lane);
+          constexpr int kFirst = kAcc == 0 ? 128 : 0;
+          const int first = nt * PN + kFirst, second = nt * PN + 128 - kFirst;
+          output_group<false, kAcc, true>(p, bias, taddr + kFirst, first, y, early);
+          if (first < p.n_out) store_group(p, g, y, staging, row0, first, lane);
+          if (second < p.n_out) {
+            output_group<false, kAcc, false>(p, bias, taddr + 128 - kFirst, second, y, early);
+            store_group(p, g, y, staging, row0, second, lane);
           }
         }
       };
@@ -762,38 +871,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
     }
   } else {
     // -------------------------------------------------------------- scale words
-    const int q = warp & 3;
-    const uint32_t quarter = static_cast<uint32_t>(q * 32) << 16;
-    uint32_t chunk = 0;
-    bool ok = true;
-    for (int t = unit; t < total && ok; t += units) {
-      int g, mt, nt;
-      decode_tile(p, t, g, mt, nt);
-      const int x_row = mt * PM + static_cast<int>(cta) * BM;
-      for (int seg = 0; seg < p.n_segs && ok; ++seg) {
-        const uint8_t* sx = p.sx[p.n_segs > 1 ? seg : 0];
-        const uint8_t* sw = p.sw[p.n_segs > 1 ? seg : g];
-        for (int k0 = 0; k0 < p.k_groups; k0 += kChunk, ++chunk) {
-          const int n = min(kChunk, p.k_groups - k0);
-          const uint32_t buf = chunk & 1u;
-          uint32_t x[4], w0[4], w1[4];
-          token_words<4>(p, sx, x_row, k0, n, lane, x);
-          weight_words(p, sw, kGlu ? nt * BM : nt * PN, k0, n, lane, w0);
-          weight_words(p, sw, kGlu ? p.up_row + nt * BM : nt * PN + BM, k0, n, lane, w1);
-          if (!__all_sync(0xffffffffu, wait_bounded<true>(ptx::smem_addr(&ctl->sf_empty[buf]),
-                                                          ((chunk >> 1) & 1u) ^ 1u, abort_flag, p.status))) {
-            ok = false;
-            break;
-          }
-          const uint32_t sf = tmem + quarter + kPromptSf + buf * 16;
-          tmem_st_x4(sf, x);
-          tmem_st_x4(sf + 4, w0);
-          tmem_st_x4(sf + 8, w1);
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-          ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&ctl->sf_full[buf]), 0));
-        }
+    const int row = (warp & 3) * 32 + lane;
+    uint32_t x_next = 0, w0_next = 0, w1_next = 0;
+    int t = unit, g = 0, mt = 0, nt = 0;
+    auto load = [&](const ChunkWalk& at) {
+      const int n = min(kChunk, p.k_groups - at.kg);
+      const uint8_t* sw = p.sw[p.n_segs > 1 ? at.seg : g];
+      const int w_row = kGlu ? nt * BM : nt * PN;
+      x_next = load_word<0>(p.sx[p.n_segs > 1 ? at.seg : 0], p.ld_sx, p.T, mt * PM + static_cast<int>(cta) * BM + row,
+                            at.kg, n, p.x_words);
+      w0_next = load_word<7>(sw, p.k_groups, p.w_rows, w_row + row, at.kg, n, p.w_words);
+      w1_next = load_word<7>(sw, p.k_groups, p.w_rows, w_row + (kGlu ? p.up_row : BM) + row, at.kg, n, p.w_words);
+    };
+    ChunkWalk at{0, 0};
+    if (t < total) {
+      tile_of(t, g, mt, nt);
+      load(at);
+    }
+    for (uint32_t chunk = 0; t < total; ++chunk) {
+      const uint32_t buf = chunk % kSfBufs;
+      const uint32_t x = x_next, w0 = w0_next, w1 = w1_next;
+      at.next(p.k_groups);
+      if (at.seg == p.n_segs) {  // on to the next tile
+        at = ChunkWalk{0, 0};
+        t += units;
+        if (t < total) tile_of(t, g, mt, nt);
       }
+      if (t < total) load(at);
+      if (!__all_sync(0xffffffffu, wait_bounded<true>(ptx::smem_addr(&ctl->sf_empty[buf]),
+                                                      ((chunk / kSfBufs) & 1u) ^ 1u, abort_flag, p.status)))
+        break;
+      const uint32_t words = sf_base + buf * kPromptSfBytes;
+      store_word(words, row, x);
+      store_word(words + kSfRows, row, w0);
+      store_word(words + 2 * kSfRows, row, w1);
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&ctl->sf_full[buf]), leader));
     }
   }
   __syncwarp();
@@ -891,9 +1004,9 @@ tp_status launch_tokens(Fp8Params& p, cudaStream_t stream) {
   return TP_OK;
 }
 
-// CTA pairs of the prompt kernel that can be resident at once (cached per device).
-template <bool kGlu>
-tp_status resident_pairs(int* n) {
+// Clusters of the prompt kernel that can be resident at once (cached per device).
+template <bool kGlu, bool kQuad>
+tp_status resident_prompt(int* n) {
   static std::mutex mu;
   static int cached[64];
   int dev = 0;
@@ -902,7 +1015,7 @@ tp_status resident_pairs(int* n) {
   std::lock_guard<std::mutex> lock(mu);
   int& c = cached[dev & 63];
   if (c == 0) {
-    e = cudaFuncSetAttribute(fp8_prompt_kernel<kGlu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(fp8_prompt_kernel<kGlu, kQuad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kPromptSmem));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
     cudaLaunchConfig_t cfg{};
@@ -911,31 +1024,30 @@ tp_status resident_pairs(int* n) {
     cfg.dynamicSmemBytes = kPromptSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = kQuad ? 4 : 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int k = 0;
-    e = cudaOccupancyMaxActiveClusters(&k, fp8_prompt_kernel<kGlu>, &cfg);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
-    if (k < 1) return fail(TP_ERR_UNSUPPORTED, "no CTA pair of the kernel fits on this device");
+    if (cudaOccupancyMaxActiveClusters(&k, fp8_prompt_kernel<kGlu, kQuad>, &cfg) != cudaSuccess || k <= 0) {
+      cudaGetLastError();
+      k = -1;  // no such cluster on this device
+    }
     c = k;
   }
   *n = c;
   return TP_OK;
 }
 
-template <bool kGlu>
-tp_status launch_prompt(const Fp8Params& p, cudaStream_t stream) {
-  int pairs = 0;
-  tp_status st = resident_pairs<kGlu>(&pairs);
-  if (st != TP_OK) return st;
-  const int64_t tiles = static_cast<int64_t>(p.n_groups) * p.n_tiles * p.t_tiles;
-  if (tiles > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many tiles (%lld)", (long long)tiles);
-  if (tiles < pairs) pairs = static_cast<int>(tiles);
+template <bool kGlu, bool kQuad>
+tp_status launch_prompt(Fp8Params& p, int clusters, cudaStream_t stream) {
+  const int64_t items = static_cast<int64_t>(p.n_groups) * p.t_items * p.n_items;
+  if (items > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many tiles (%lld)", (long long)items);
+  if (items < clusters) clusters = static_cast<int>(items);
+  constexpr unsigned kCtas = kQuad ? 4 : 2;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(pairs), 1, 1);
+  cfg.gridDim = dim3(kCtas * static_cast<unsigned>(clusters), 1, 1);
   cfg.blockDim = dim3(kPromptThreads, 1, 1);
   cfg.dynamicSmemBytes = kPromptSmem;
   cfg.stream = stream;
@@ -943,22 +1055,22 @@ tp_status launch_prompt(const Fp8Params& p, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = kCtas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_prompt_kernel<kGlu>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_prompt_kernel<kGlu, kQuad>, p);
   if (e != cudaSuccess) return cuda_fail(e, "fp8 projection launch");
   return TP_OK;
 }
 
-// Token tiles that sweep the weight tiles together: all of them while their operand fits L2
-// comfortably (each weight tile is then read from HBM once), else groups of about 16, evenly sized.
-int choose_group_m(int t_tiles, int64_t x_bytes) {
-  if (x_bytes <= (64ll << 20)) return t_tiles;
-  const int groups = ceil_div(t_tiles, 16);
-  return ceil_div(t_tiles, groups);
+// Token items that sweep the weight items together: all of them while their operand fits L2
+// comfortably (each weight tile is then read from HBM once), else groups of about 16 tiles, evenly sized.
+int choose_group_m(int t_items, int tiles_per_item, int64_t x_bytes) {
+  if (x_bytes <= (64ll << 20)) return t_items;
+  const int groups = ceil_div(static_cast<int64_t>(t_items) * tiles_per_item, 16);
+  return ceil_div(t_items, groups);
 }
 
 // The operands of a call, checked.
@@ -973,43 +1085,75 @@ struct Fp8Call {
   int64_t T, K, w_rows, n_out;
 };
 
+// The maps of X and W in boxes of x_box and w_box rows.
+tp_status set_maps(const Fp8Call& c, Fp8Params& p, int x_box, int w_box) {
+  for (int r = 0; r < c.p; ++r) {
+    tp_status st = operand_map(&p.map_w[r], c.w[r], c.K, c.w_rows, c.K, w_box);
+    if (st == TP_OK && (r == 0 || !c.x_shared)) st = operand_map(&p.map_x[r], c.x[r], c.K, c.T, c.ldx, x_box);
+    if (st != TP_OK) return st;
+  }
+  return TP_OK;
+}
+
+template <bool kGlu>
+tp_status run_prompt(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
+  p.n_tiles = ceil_div(c.n_out, kGlu ? BM : PN);
+  p.t_tiles = ceil_div(c.T, PM);
+  int pairs = 0, quads = 0;
+  tp_status st = resident_prompt<kGlu, false>(&pairs);
+  if (st == TP_OK) st = resident_prompt<kGlu, true>(&quads);
+  if (st != TP_OK) return st;
+  if (pairs < 1) return fail(TP_ERR_UNSUPPORTED, "no CTA pair of the kernel fits on this device");
+  p.share_x = p.n_tiles % 2 == 0;
+  bool quad = quads > 0 && (p.n_tiles % 2 == 0 || p.t_tiles % 2 == 0);
+  const char* force = getenv("TP_FP8_FORCE");
+  if (force && force[1] == '2') quad = false;
+  if (force && force[1] == 'm' && p.t_tiles % 2 == 0) p.share_x = false;
+  p.n_items = quad && p.share_x ? p.n_tiles / 2 : p.n_tiles;
+  p.t_items = quad && !p.share_x ? p.t_tiles / 2 : p.t_tiles;
+  p.group_m = choose_group_m(p.t_items, p.t_tiles / p.t_items, c.T * c.K * p.n_segs);
+  st = set_maps(c, p, quad && p.share_x ? BM / 2 : BM, quad && !p.share_x ? BM / 2 : BM);
+  if (st != TP_OK) return st;
+  return quad ? launch_prompt<kGlu, true>(p, quads, stream) : launch_prompt<kGlu, false>(p, pairs, stream);
+}
+
+template <int TN>
+tp_status run_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
+  p.n_tiles = ceil_div(c.n_out, BM);
+  p.t_tiles = ceil_div(c.T, TN);
+  tp_status st = set_maps(c, p, TN, BM);
+  if (st != TP_OK) return st;
+  return p.act == TP_ACT_SWIGLU ? launch_tokens<TN, true>(p, stream) : launch_tokens<TN, false>(p, stream);
+}
+
 tp_status run_fp8(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   p.status = status_word();
   if (p.status == nullptr) return fail(TP_ERR_CUDA, "cannot locate the kernel status word");
-  const bool glu = p.act == TP_ACT_SWIGLU;
-  const char* force = getenv("TP_FP8_FORCE");
-  const bool prompt = force ? force[0] == 'p' : c.T > 128;
-  const int tn = prompt ? BM : c.T <= 16 ? 16 : c.T <= 32 ? 32 : c.T <= 64 ? 64 : 128;  // rows of an X box
-  for (int r = 0; r < c.p; ++r) {
-    tp_status st = operand_map(&p.map_w[r], c.w[r], c.K, c.w_rows, c.K, BM);
-    if (st != TP_OK) return st;
-    p.sw[r] = static_cast<const uint8_t*>(c.sw[r]);
-    if (r == 0 || !c.x_shared) {
-      st = operand_map(&p.map_x[r], c.x[r], c.K, c.T, c.ldx, tn);
-      if (st != TP_OK) return st;
-      p.sx[r] = static_cast<const uint8_t*>(c.sx[r]);
-    }
-  }
   p.ld_sx = c.ld_sx;
   p.T = static_cast<int>(c.T);
   p.w_rows = static_cast<int>(c.w_rows);
   p.n_out = static_cast<int>(c.n_out);
   p.up_row = static_cast<int>(c.w_rows / 2);
   p.k_groups = ceil_div(c.K, KB);
-  if (prompt) {
-    p.n_tiles = ceil_div(c.n_out, glu ? BM : PN);
-    p.t_tiles = ceil_div(c.T, PM);
-    p.group_m = choose_group_m(p.t_tiles, c.T * c.K * p.n_segs);
-    return glu ? launch_prompt<true>(p, stream) : launch_prompt<false>(p, stream);
+  auto word_rows = [](const void* q, int64_t ld) { return (reinterpret_cast<uintptr_t>(q) & 3u) == 0 && ld % 4 == 0; };
+  p.x_words = p.w_words = p.k_groups % kChunk == 0;
+  p.bias_vec = true;
+  for (int r = 0; r < c.p; ++r) {
+    p.sw[r] = static_cast<const uint8_t*>(c.sw[r]);
+    p.w_words = p.w_words && word_rows(p.sw[r], p.k_groups);
+    if (r == 0 || !c.x_shared) {
+      p.sx[r] = static_cast<const uint8_t*>(c.sx[r]);
+      p.x_words = p.x_words && word_rows(p.sx[r], c.ld_sx);
+    }
+    p.bias_vec = p.bias_vec && aligned16(p.bias[r]);
   }
-  p.n_tiles = ceil_div(c.n_out, BM);
-  p.t_tiles = ceil_div(c.T, tn);
-  switch (tn) {
-    case 16: return glu ? launch_tokens<16, true>(p, stream) : launch_tokens<16, false>(p, stream);
-    case 32: return glu ? launch_tokens<32, true>(p, stream) : launch_tokens<32, false>(p, stream);
-    case 64: return glu ? launch_tokens<64, true>(p, stream) : launch_tokens<64, false>(p, stream);
-    default: return glu ? launch_tokens<128, true>(p, stream) : launch_tokens<128, false>(p, stream);
-  }
+  const char* force = getenv("TP_FP8_FORCE");
+  if (force ? force[0] == 'p' : c.T > 128)
+    return p.act == TP_ACT_SWIGLU ? run_prompt<true>(c, p, stream) : run_prompt<false>(c, p, stream);
+  if (c.T <= 16) return run_tokens<16>(c, p, stream);
+  if (c.T <= 32) return run_tokens<32>(c, p, stream);
+  if (c.T <= 64) return run_tokens<64>(c, p, stream);
+  return run_tokens<128>(c, p, stream);
 }
 
 // What both entry points check of their operands.
