@@ -158,6 +158,17 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
   return wait_slow<kCluster>(bar, parity, abort_flag, status, ignore_abort);
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+
 // ---------------------------------------------------------------- scale words
 constexpr uint32_t kScaleOne = 0x7F7F7F7Fu;  // 2^0 for rows past the operand (their products are not stored)
 
@@ -652,7 +663,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
   PromptCtrl* ctl = &ctl_mem;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort_flag = &ctl->abort;
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
   const int lane = threadIdx.x & 31;
   const uint32_t crank = ptx::cluster_ctarank();
   const uint32_t cta = crank & 1u;                  // 0 = the pair's leader
@@ -687,7 +698,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
   ptx::tc_fence_before();
   ptx::cluster_sync();
   ptx::tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
   pdl_launch_dependents();
   pdl_wait();
 
@@ -703,44 +714,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ producer
-      uint32_t it = 0;
+      const uint32_t full0 = ptx::smem_addr(&ctl->full[0]), empty0 = ptx::smem_addr(&ctl->empty[0]);
+      uint32_t it = 0;  // copies issued
+      const uint32_t full0_leader = ptx::mapa_shared(full0, leader);  // both CTAs' copies complete there
+      const uint32_t ring = ptx::smem_addr(base);
+      const uint32_t half = kQuad ? pair * (kBoxA / 2) : 0;           // the part of a shared box this CTA loads
+      const int half_row = static_cast<int>(pair) * (BM / 2);
+      const uint16_t both = static_cast<uint16_t>(0x5u << cta);       // this CTA's place in both pairs
+      const bool share_x = kQuad && p.share_x, share_w = kQuad && !p.share_x;
+      uint32_t stage = 0, phase = 1;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
         int g, mt, nt;
         tile_of(t, g, mt, nt);
-        const int x_row = mt * PM + static_cast<int>(cta) * BM;
-        const int w_row = kGlu ? (cta == 0 ? 0 : p.up_row) + nt * BM : nt * PN + static_cast<int>(cta) * BM;
+        const int x_row = mt * PM + static_cast<int>(cta) * BM + (share_x ? half_row : 0);
+        const int w_row = (kGlu ? (cta == 0 ? 0 : p.up_row) + nt * BM : nt * PN + static_cast<int>(cta) * BM) +
+                          (share_w ? half_row : 0);
         for (int seg = 0; seg < p.n_segs && ok; ++seg) {
           const CUtensorMap* mx = &p.map_x[p.n_segs > 1 ? seg : 0];
           const CUtensorMap* mw = &p.map_w[p.n_segs > 1 ? seg : g];
-          for (int k = 0; k < p.k_groups; ++k, ++it) {
-            const uint32_t s = it % kPromptStages;
-            if (!wait_bounded<true>(ptx::smem_addr(&ctl->empty[s]), ((it / kPromptStages) & 1u) ^ 1u, abort_flag,
-                                    p.status)) {
+          int kx = 0;
+          for (int k = p.k_groups; k > 0; --k, kx += KB / 2, ++it) {
+            if (!wait_bounded(empty0 + 8 * stage, phase, abort_flag, p.status)) {
               ok = false;
               break;
             }
-            // Both CTAs' copies complete on the leader's barrier.
-            const uint32_t full = ptx::smem_addr(&ctl->full[s]);
-            const uint32_t full_leader = ptx::mapa_shared(full, leader);
-            const uint32_t sx = ptx::smem_addr(base + s * kPromptStage);
-            if (cta == 0) ptx::mbar_arrive_expect_tx(full, 2 * kPromptStage);
-            const int kx = k * (KB / 2);
-            if constexpr (kQuad) {
-              const uint32_t half = pair * (kBoxA / 2);
-              const int row = static_cast<int>(pair) * (BM / 2);
-              const uint16_t both = static_cast<uint16_t>(0x5u << cta);  // this CTA's place in both pairs
-              if (p.share_x) {
-                ptx::tma_load_2d_pair_mc(sx + half, mx, full_leader, kx, x_row + row, both);
-                ptx::tma_load_2d_pair(sx + kBoxA, mw, full_leader, kx, w_row);
-              } else {
-                ptx::tma_load_2d_pair(sx, mx, full_leader, kx, x_row);
-                ptx::tma_load_2d_pair_mc(sx + kBoxA + half, mw, full_leader, kx, w_row + row, both);
-              }
-            } else {
-              ptx::tma_load_2d_pair(sx, mx, full_leader, kx, x_row);
-              ptx::tma_load_2d_pair(sx + kBoxA, mw, full_leader, kx, w_row);
-            }
+            const uint32_t full = full0_leader + 8 * stage;
+            const uint32_t sx = ring + stage * kPromptStage, sw = sx + kBoxA;
+            if (cta == 0) ptx::mbar_arrive_expect_tx(full0 + 8 * stage, 2 * kPromptStage);
+            if (share_x)
+              ptx::tma_load_2d_pair_mc(sx + half, mx, full, kx, x_row, both);
+            else
+              ptx::tma_load_2d_pair(sx, mx, full, kx, x_row);
+            if (share_w)
+              ptx::tma_load_2d_pair_mc(sw + half, mw, full, kx, w_row, both);
+            else
+              ptx::tma_load_2d_pair(sw, mw, full, kx, w_row);
+            if (++stage == kPromptStages) stage = 0, phase ^= 1u;
           }
         }
       }
@@ -758,11 +768,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && cta == 0) {
+    if (cta == 0) {
       // ------------------------------------------------------------ MMA issuer (leader)
-      // One thread issues a group's four MMAs in the time they run, 512 cycles, so the loop carries
-      // its addresses along instead of computing them (with them computed from the stage number
-      // it took 690 cycles a group and bounded the kernel).
+      // A group's four MMAs run in 512 cycles, and the loop has to issue them in less: it carries
+      // its addresses along (computed from the stage number, the loop took 690 cycles a group and
+      // bounded the kernel), and the whole warp runs it, so that they stay in uniform registers;
+      // one lane issues.
+      const bool issuer = elect_one();
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, p.status));
+      };
       constexpr uint32_t idesc = idesc_mx(PM, PN);
       const uint64_t x0 = ptx::sw128_kmajor_desc(ptx::smem_addr(base));
       const uint32_t full0 = ptx::smem_addr(&ctl->full[0]), empty0 = ptx::smem_addr(&ctl->empty[0]);
@@ -773,8 +788,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       for (int t = unit; t < total && ok; t += units, ++tile) {
         // The shared columns are back from the tile before; the rest of this accumulator was read
         // before that, by the same threads.
-        if (tile > 0 &&
-            !wait_bounded<true>(ptx::smem_addr(&ctl->tempty), (tile - 1) & 1u, abort_flag, p.status))
+        if (tile > 0 && !__all_sync(0xffffffffu, wait_bounded<true>(ptx::smem_addr(&ctl->tempty), (tile - 1) & 1u,
+                                                                    abort_flag, p.status)))
           break;
         ptx::tc_fence_after();
         const uint32_t acc = tmem + (tile & 1u) * (PN - kShared);
@@ -782,41 +797,44 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
         for (int seg = 0; seg < p.n_segs && ok; ++seg) {
           for (int left = p.k_groups; left > 0; left -= kChunk, ++chunk) {
             const uint32_t buf = chunk % kSfBufs;
-            if (!wait_bounded<true>(sf_full0 + 8 * buf, (chunk / kSfBufs) & 1u, abort_flag, p.status)) {
+            if (!__all_sync(0xffffffffu, wait_bounded<true>(sf_full0 + 8 * buf, (chunk / kSfBufs) & 1u, abort_flag,
+                                                            p.status))) {
               ok = false;
               break;
             }
             const uint32_t sf = tmem + kPromptSf + (chunk & 1u) * 16;
+            if (issuer)
 #pragma unroll
-            for (int a = 0; a < 3; ++a)
-              copy_scales<true>(sf + 4 * a, sf_base + buf * kPromptSfBytes + a * kSfRows);
+              for (int a = 0; a < 3; ++a)
+                copy_scales<true>(sf + 4 * a, sf_base + buf * kPromptSfBytes + a * kSfRows);
 #pragma unroll
             for (int k = 0; k < kChunk; ++k) {
               if (k < left) {
-                if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, p.status)) {
+                if (!wait(full0 + 8 * stage, phase)) {
                   ok = false;
                   break;
                 }
                 ptx::tc_fence_after();
+                if (issuer) {
 #pragma unroll
-                for (int j = 0; j < KB / 32; ++j) {
-                  umma_mx_pair(acc, xdesc + 2 * j, xdesc + (kBoxA >> 4) + 2 * j,
-                               idesc | idesc_scale_byte(static_cast<uint32_t>(k)), sf, sf + 4, accumulate);
-                  accumulate = 1;
+                  for (int j = 0; j < KB / 32; ++j)
+                    umma_mx_pair(acc, xdesc + 2 * j, xdesc + (kBoxA >> 4) + 2 * j,
+                                 idesc | idesc_scale_byte(static_cast<uint32_t>(k)), sf, sf + 4, j > 0 ? 1u : accumulate);
+                  ptx::umma_commit_pair(empty0 + 8 * stage, kQuad ? 0xF : 0x3);
                 }
-                ptx::umma_commit_pair(empty0 + 8 * stage, kQuad ? 0xF : 0x3);
+                accumulate = 1;
                 xdesc += kPromptStage >> 4;
                 if (++stage == kPromptStages) stage = 0, phase ^= 1u, xdesc = x0;
               }
             }
             if (!ok) break;
-            ptx::umma_commit_pair(sf_empty0 + 8 * buf, pair_mask);
+            if (issuer) ptx::umma_commit_pair(sf_empty0 + 8 * buf, pair_mask);
           }
         }
         if (!ok) break;
-        ptx::umma_commit_pair(ptx::smem_addr(&ctl->tfull[tile & 1u]), pair_mask);
+        if (issuer) ptx::umma_commit_pair(ptx::smem_addr(&ctl->tfull[tile & 1u]), pair_mask);
       }
-      ptx::umma_commit_pair(ptx::smem_addr(&ctl->drain), pair_mask);
+      if (issuer) ptx::umma_commit_pair(ptx::smem_addr(&ctl->drain), pair_mask);
       wait_bounded<true>(ptx::smem_addr(&ctl->drain), 0, abort_flag, p.status, true);
     } else if (lane == 0) {
       // The peer's shared memory feeds the leader's MMAs until the drain arrives.
