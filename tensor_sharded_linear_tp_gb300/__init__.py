@@ -10,6 +10,7 @@ been built, importing this package raises ImportError.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Optional, Sequence
 
@@ -465,79 +466,92 @@ def tp_combine(mode: str, partials: Sequence[torch.Tensor], out: torch.Tensor | 
 # strides and device before the library is called, so a refused call touches no device memory.
 # ---------------------------------------------------------------------------
 
-_E4M3, _E8M0, _BF16 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.bfloat16
+_E4M3, _E8M0, _BF16, _U8 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.bfloat16, torch.uint8
+_POINTERS = [_vp * n for n in range(MAX_DEGREE + 1)]
+_kind = operator.attrgetter("dtype", "shape")
+_data_ptr, _contiguous, _gpu = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
 
 
 def _groups(n: int) -> int:
     return -(-n // FP8_GROUP)
 
 
-def _need(name, t, dtype, shape, device=None):
+def _need(name, t, dtype, shape, dev):
     """A tensor of `dtype` (a scale: e8m0 or uint8) and `shape` on the current GPU, its last dimension contiguous.
 
-    Returns the row stride (0 for a single row, whose stride means nothing)."""
-    if t.dtype is not dtype and not (dtype is _E8M0 and t.dtype is torch.uint8):
+    Returns the row stride (0 where the rows are dense)."""
+    if _kind(t) == (dtype, shape) and t.get_device() == dev and t.is_contiguous():
+        return 0
+    if t.dtype is not dtype and not (dtype is _E8M0 and t.dtype is _U8):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != (torch.cuda.current_device() if device is None else device):
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
-    if t.dim() == 1:
-        if t.numel() > 1 and t.stride(0) != 1:
-            raise ValueError(f"{name} must be contiguous")
+    if t.is_contiguous():
         return 0
+    if len(shape) == 1:
+        raise ValueError(f"{name} must be contiguous")
     rows, cols = shape
     step, inner = t.stride()
     if cols > 1 and inner != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if rows <= 1:
-        return 0
-    if step < cols:
+    if rows > 1 and step < cols:
         raise ValueError(f"{name}: a row stride of {step} overlaps rows of {cols} elements")
-    return step
+    return step if rows > 1 else 0
 
 
-def _one_stride(name, strides, cols, rows):
-    """The row stride every rank's tensor shares (a single row's is taken as dense)."""
-    first = strides[0]
-    for s in strides:
-        if s != first:
+def _need_ranks(name, ts, dtype, shape, dev, dense=False):
+    """(pointer array, row stride) of one tensor for each rank, as _need; every rank has the same row stride."""
+    # The usual case, in as few steps as it takes: a call with few tokens is as long as its checks.
+    n = len(ts)
+    if list(map(_kind, ts)) == [(dtype, shape)] * n and all(map(_contiguous, ts)) and [dev] * n == list(map(_gpu, ts)):
+        return _POINTERS[n](*map(_data_ptr, ts)), 0
+    steps = [_need(f"{name}[{i}]", t, dtype, shape, dev) for i, t in enumerate(ts)]
+    if any(s not in (0, shape[1]) for s in steps):
+        if dense:
+            raise ValueError(f"every rank's {name} must be contiguous")
+        if any(s != steps[0] for s in steps):
             raise ValueError(f"every rank's {name} must have the same row stride")
-    return first if rows > 1 else 0
+    return _POINTERS[n](*map(_data_ptr, ts)), steps[0]
 
 
-def _alloc(stream, dev, dtype, *shapes):
-    """Outputs for a call on `stream`, from that stream's memory."""
-    def make():
-        if dtype is _E8M0:
-            return [torch.empty(s, dtype=torch.uint8, device=dev).view(_E8M0) for s in shapes]
-        return [torch.empty(s, dtype=dtype, device=dev) for s in shapes]
-    if stream is None:
-        return make()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    with torch.cuda.stream(stream):
-        return make()
+def _alloc(stream, dev, dtype, shape, count=1):
+    """`count` outputs for a call on `stream`, from that stream's memory."""
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            return _alloc(None, dev, dtype, shape, count)
+    # (Scales are made as bytes: not every operation knows their type.)
+    out = torch.empty((count, *shape), dtype=_U8 if dtype is _E8M0 else dtype, device=f"cuda:{dev}").unbind(0)
+    return [t.view(_E8M0) for t in out] if dtype is _E8M0 else out
 
 
 def _launch_stream(stream, dev) -> int:
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _device_of(name, t) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be a tensor on the current CUDA device")
+    """The current device, which a 2-D tensor `t` has to be on."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
-    return t.get_device()
+    return dev
 
 
-def _same_count(p, **lists):
-    for name, ts in lists.items():
+def _ranks(w_shards, *lists) -> int:
+    p = len(w_shards)
+    if not 1 <= p <= MAX_DEGREE:
+        raise ValueError(f"w_shards must have one entry for each of 1 to {MAX_DEGREE} ranks, got {p}")
+    for ts in lists:
         if ts is not None and len(ts) != p:
-            raise ValueError(f"{name} must have one entry for each of the {p} ranks, got {len(ts)}")
+            raise ValueError(f"every list must have one entry for each of the {p} ranks, got {len(ts)}")
+    return p
 
 
 def tp_quantize_fp8(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | None = None,
@@ -546,28 +560,18 @@ def tp_quantize_fp8(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | None
     dev = _device_of("x", x)
     if block_rows not in (1, FP8_GROUP):
         raise ValueError(f"block_rows must be 1 or {FP8_GROUP}, got {block_rows}")
-    rows, cols = x.shape
-    ldx = _need("x", x, _BF16, (rows, cols), dev)
+    shape = x.shape
+    rows, cols = shape
+    ldx = _need("x", x, _BF16, shape, dev)
     s_shape = (-(-rows // block_rows), _groups(cols))
     if q is None:
-        q, = _alloc(stream, dev, _E4M3, (rows, cols))
+        q, = _alloc(stream, dev, _E4M3, shape)
     if scales is None:
         scales, = _alloc(stream, dev, _E8M0, s_shape)
-    ldq, lds = _need("q", q, _E4M3, (rows, cols), dev), _need("scales", scales, _E8M0, s_shape, dev)
+    ldq, lds = _need("q", q, _E4M3, shape, dev), _need("scales", scales, _E8M0, s_shape, dev)
     _check(lib.tp_quantize_fp8(x.data_ptr(), ldx, rows, cols, block_rows, q.data_ptr(), ldq, scales.data_ptr(), lds,
                                _launch_stream(stream, dev)))
     return q, scales
-
-
-def _fp8_weights(w_shards, w_scales, K, dev):
-    N = w_shards[0].shape[0]
-    s_shape = (_groups(N), _groups(K))
-    for i, (w, s) in enumerate(zip(w_shards, w_scales)):
-        if _need(f"w_shards[{i}]", w, _E4M3, (N, K), dev) not in (0, K):
-            raise ValueError(f"w_shards[{i}] must be contiguous")
-        if _need(f"w_scales[{i}]", s, _E8M0, s_shape, dev) not in (0, s_shape[1]):
-            raise ValueError(f"w_scales[{i}] must be contiguous")
-    return N
 
 
 def tp_linear_colwise_fp8(x: torch.Tensor, x_scales: torch.Tensor, w_shards: Sequence[torch.Tensor],
@@ -581,36 +585,36 @@ def tp_linear_colwise_fp8(x: torch.Tensor, x_scales: torch.Tensor, w_shards: Seq
     w_scales[r] with block_rows 128.  out="bf16" returns the list of Y_r; out="fp8" returns
     (codes, scales), two lists, ready for tp_linear_rowwise_fp8."""
     dev = _device_of("x", x)
-    if out not in ("bf16", "fp8"):
+    if out != "bf16" and out != "fp8":
         raise ValueError(f'out must be "bf16" or "fp8", got {out!r}')
-    p = len(w_shards)
-    if p < 1:
-        raise ValueError("w_shards is empty")
-    _same_count(p, w_scales=w_scales, bias_shards=bias_shards, y_shards=y_shards, y_scales=y_scales)
+    fp8 = out == "fp8"
+    if not fp8 and y_scales is not None:
+        raise ValueError('y_scales belongs to out="fp8"')
+    p = _ranks(w_shards, w_scales, bias_shards, y_shards, y_scales)
     T, K = x.shape
-    ldx = _need("x", x, _E4M3, (T, K), dev)
-    ld_xs = _need("x_scales", x_scales, _E8M0, (T, _groups(K)), dev)
-    N = _fp8_weights(w_shards, w_scales, K, dev)
+    N = w_shards[0].shape[0]
+    kg = _groups(K)
+    ldx, ld_xs = _need("x", x, _E4M3, (T, K), dev), _need("x_scales", x_scales, _E8M0, (T, kg), dev)
+    w, _ = _need_ranks("w_shards", w_shards, _E4M3, (N, K), dev, dense=True)
+    ws, _ = _need_ranks("w_scales", w_scales, _E8M0, (_groups(N), kg), dev, dense=True)
+    bias = None
     if bias_shards is not None:
         for i, b in enumerate(bias_shards):
             if b is not None:
                 _need(f"bias_shards[{i}]", b, _BF16, (N,), dev)
+        bias = _POINTERS[p](*[None if b is None else b.data_ptr() for b in bias_shards])
     n = N // 2 if act == "swiglu" else N
-    fp8 = out == "fp8"
-    if not fp8 and y_scales is not None:
-        raise ValueError('y_scales belongs to out="fp8"')
-    y_type, s_shape = (_E4M3 if fp8 else _BF16), (T, _groups(n))
     if y_shards is None:
-        y_shards = _alloc(stream, dev, y_type, *[(T, n)] * p)
-    if fp8 and y_scales is None:
-        y_scales = _alloc(stream, dev, _E8M0, *[s_shape] * p)
-    ldy = _one_stride("output", [_need("y_shards[r]", y, y_type, (T, n), dev) for y in y_shards], n, T)
-    ld_ys = _one_stride("output scales", [_need("y_scales[r]", s, _E8M0, s_shape, dev) for s in y_scales], s_shape[1],
-                        T) if fp8 else 0
-    _check(lib.tp_linear_colwise_fp8(x.data_ptr(), ldx, x_scales.data_ptr(), ld_xs, _ptrs(w_shards), _ptrs(w_scales),
-                                     _ptrs(bias_shards) if bias_shards is not None else None, ACTS[act], p, T, K, N,
-                                     _ptrs(y_shards), ldy, _ptrs(y_scales) if fp8 else None, ld_ys,
-                                     _launch_stream(stream, dev)))
+        y_shards = _alloc(stream, dev, _E4M3 if fp8 else _BF16, (T, n), p)
+    y, ldy = _need_ranks("y_shards", y_shards, _E4M3 if fp8 else _BF16, (T, n), dev)
+    ys, ld_ys = None, 0
+    if fp8:
+        s_shape = (T, _groups(n))
+        if y_scales is None:
+            y_scales = _alloc(stream, dev, _E8M0, s_shape, p)
+        ys, ld_ys = _need_ranks("y_scales", y_scales, _E8M0, s_shape, dev)
+    _check(lib.tp_linear_colwise_fp8(x.data_ptr(), ldx, x_scales.data_ptr(), ld_xs, w, ws, bias, ACTS[act], p, T, K, N,
+                                     y, ldy, ys, ld_ys, _launch_stream(stream, dev)))
     return (list(y_shards), list(y_scales)) if fp8 else list(y_shards)
 
 
@@ -619,24 +623,22 @@ def tp_linear_rowwise_fp8(x_shards: Sequence[torch.Tensor], x_scales: Sequence[t
                           bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
                           stream=None) -> torch.Tensor:
     """Z = sum_r X_r W_r^T (+ bias once) on the 8-bit format, one launch; bf16 [T, N]."""
-    p = len(w_shards)
-    if p < 1:
-        raise ValueError("w_shards is empty")
-    _same_count(p, w_scales=w_scales, x_shards=x_shards, x_scales=x_scales)
+    p = _ranks(w_shards, w_scales, x_shards, x_scales)
     dev = _device_of("x_shards[0]", x_shards[0])
     T, K = x_shards[0].shape
-    N = _fp8_weights(w_shards, w_scales, K, dev)
-    s_shape = (T, _groups(K))
-    ldx = _one_stride("input", [_need("x_shards[r]", x, _E4M3, (T, K), dev) for x in x_shards], K, T)
-    ld_xs = _one_stride("input scales", [_need("x_scales[r]", s, _E8M0, s_shape, dev) for s in x_scales], s_shape[1], T)
+    N = w_shards[0].shape[0]
+    kg = _groups(K)
+    w, _ = _need_ranks("w_shards", w_shards, _E4M3, (N, K), dev, dense=True)
+    ws, _ = _need_ranks("w_scales", w_scales, _E8M0, (_groups(N), kg), dev, dense=True)
+    x, ldx = _need_ranks("x_shards", x_shards, _E4M3, (T, K), dev)
+    xs, ld_xs = _need_ranks("x_scales", x_scales, _E8M0, (T, kg), dev)
     if bias is not None:
         _need("bias", bias, _BF16, (N,), dev)
     if out is None:
         out, = _alloc(stream, dev, _BF16, (T, N))
     ldo = _need("out", out, _BF16, (T, N), dev)
-    _check(lib.tp_linear_rowwise_fp8(_ptrs(x_shards), ldx, _ptrs(x_scales), ld_xs, _ptrs(w_shards), _ptrs(w_scales),
-                                     bias.data_ptr() if bias is not None else None, p, T, K, N, out.data_ptr(), ldo,
-                                     _launch_stream(stream, dev)))
+    _check(lib.tp_linear_rowwise_fp8(x, ldx, xs, ld_xs, w, ws, None if bias is None else bias.data_ptr(), p, T, K, N,
+                                     out.data_ptr(), ldo, _launch_stream(stream, dev)))
     return out
 
 
@@ -655,50 +657,60 @@ def tp_residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, norm: str =
     branch y there is no h."""
     dev = _device_of("x", x)
     if out not in ("bf16", "fp8", None):
-        raise ValueError(f'out must be "bf16", "fp8" or None, got {out!r}')
-    T, D = x.shape
-    a = ResidualNormArgs()
-    a.T, a.D, a.alpha, a.eps = T, D, alpha, eps
-    a.x, a.ldx = x.data_ptr(), _need("x", x, _BF16, (T, D), dev)
-    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight), ("post_bias", post_bias)):
-        if t is not None:
-            _need(name, t, _BF16, (D,), dev)
-            setattr(a, name, t.data_ptr())
-    a.post_norm = NORMS[post_norm]
-    ld_mod, mod_rows = None, None
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if t is not None:
-            rows = 1 if t.dim() == 1 else t.shape[0]
-            step = _need(name, t, _BF16, (D,) if t.dim() == 1 else (rows, D), dev)
-            if mod_rows is None:
-                ld_mod, mod_rows = step, rows
-            elif mod_rows != rows or ld_mod != step:
-                raise ValueError("gate, scale and shift must have the same rows and row stride")
-            setattr(a, name, t.data_ptr())
-    if mod_rows is not None:
-        a.ld_mod, a.mod_rows = ld_mod, mod_rows
-        a.rows_per_mod = max(T, 1) if rows_per_mod is None else rows_per_mod
+        raise ValueError(f'out must be "bf16" or "fp8", got {out!r}')
+    fp8 = out == "fp8"
+    if u_scales is not None and not fp8:
+        raise ValueError('u_scales belongs to out="fp8"')
+    if u is not None and out is None:
+        raise ValueError("u belongs to an output type")
+    shape = x.shape
+    T, D = shape
+    ldx = _need("x", x, _BF16, shape, dev)
+
+    def vec(name, t):
+        if t is None:
+            return None
+        _need(name, t, _BF16, (D,), dev)
+        return t.data_ptr()
+
+    mod = None  # (row stride, rows) of the tables
+
+    def table(name, t):
+        nonlocal mod
+        if t is None:
+            return None
+        rows = 1 if t.dim() == 1 else t.shape[0]
+        step = _need(name, t, _BF16, (D,) if t.dim() == 1 else (rows, D), dev)
+        if mod is None:
+            mod = step, rows
+        elif mod != (step, rows):
+            raise ValueError("gate, scale and shift must have the same rows and row stride")
+        return t.data_ptr()
+
+    gate_at, scale_at, shift_at = table("gate", gate), table("scale", scale), table("shift", shift)
+    y_at, ldy = None, 0
     if y is not None:
-        a.y, a.ldy = y.data_ptr(), _need("y", y, _BF16, (T, D), dev)
+        y_at, ldy = y.data_ptr(), _need("y", y, _BF16, shape, dev)
         if h is None:
-            h, = _alloc(stream, dev, _BF16, (T, D))
-    if h is not None:
-        a.h, a.ldh = h.data_ptr(), _need("h", h, _BF16, (T, D), dev)
-    if out is None:
-        if u is not None or u_scales is not None:
-            raise ValueError("u and u_scales belong to an output type")
-    else:
-        a.norm = NORMS[norm]
-        u_type = _E4M3 if out == "fp8" else _BF16
+            h, = _alloc(stream, dev, _BF16, shape)
+    h_at, ldh = (None, 0) if h is None else (h.data_ptr(), _need("h", h, _BF16, shape, dev))
+    u_at, ldu, s_at, ld_us = None, 0, None, 0
+    if out is not None:
+        u_type = _E4M3 if fp8 else _BF16
         if u is None:
-            u, = _alloc(stream, dev, u_type, (T, D))
-        a.u, a.ldu = u.data_ptr(), _need("u", u, u_type, (T, D), dev)
-        if out == "fp8":
+            u, = _alloc(stream, dev, u_type, shape)
+        u_at, ldu = u.data_ptr(), _need("u", u, u_type, shape, dev)
+        if fp8:
             if u_scales is None:
                 u_scales, = _alloc(stream, dev, _E8M0, (T, _groups(D)))
-            a.u_scales, a.ld_u_scales = u_scales.data_ptr(), _need("u_scales", u_scales, _E8M0, (T, _groups(D)), dev)
-        elif u_scales is not None:
-            raise ValueError('u_scales belongs to out="fp8"')
+            s_at, ld_us = u_scales.data_ptr(), _need("u_scales", u_scales, _E8M0, (T, _groups(D)), dev)
+    ld_mod, mod_rows = mod or (0, 0)
+    if mod and rows_per_mod is None:
+        rows_per_mod = max(T, 1)
+    a = ResidualNormArgs(T, D, x.data_ptr(), ldx, y_at, ldy, NORMS[post_norm], vec("post_weight", post_weight),
+                         vec("post_bias", post_bias), alpha, eps, gate_at, scale_at, shift_at, ld_mod, mod_rows,
+                         rows_per_mod if mod else 0, h_at, ldh, 0 if out is None else NORMS[norm],
+                         vec("weight", weight), vec("bias", bias), u_at, ldu, s_at, ld_us)
     _check(lib.tp_residual_norm(ctypes.byref(a), _launch_stream(stream, dev)))
     return h, u, u_scales
 
