@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cstdio>
 #include <cstdlib>
 #include <mutex>
 #include <type_traits>
@@ -250,13 +251,14 @@ struct TokensCfg {
   static constexpr uint32_t W_BYTES = W_TILES * kBoxA;
   static constexpr uint32_t X_BYTES = TN * KB;
   static constexpr uint32_t STAGE_BYTES = W_BYTES + X_BYTES;
-  static constexpr int STAGES = 196608 / STAGE_BYTES < kMaxStages ? 196608 / STAGE_BYTES : kMaxStages;
+  // Up to 32 tokens two CTAs fit an SM (so that a kernel's prologue runs beside its predecessor),
+  // with 90 to 108 KB in flight each; more tokens take one CTA with twice that.
+  static constexpr bool SMALL = TN <= 32;
+  static constexpr uint32_t RING_MAX = SMALL ? 110592 : 196608;
+  static constexpr int STAGES = RING_MAX / STAGE_BYTES;
   static constexpr uint32_t RING = STAGES * STAGE_BYTES;
   static constexpr uint32_t PARTIAL = W_TILES * TN * BM * 4;    // fp32 [tile][token][128], over the ring
-  static_assert(PARTIAL <= RING, "the partial tile reuses the ring");
-  // One CTA per SM, and none beside another kernel's CTA that may still be about to allocate
-  // tensor memory: the smallest of those holds 97 KB.
-  static_assert(RING >= 135168, "fewer than 132 KB would let two kernels' CTAs share an SM");
+  static_assert(STAGES <= kMaxStages && PARTIAL <= RING, "the partial tile reuses the ring");
   static constexpr int ACC_COLS = W_TILES * TN;
   static constexpr int SF_COLS = 16;                            // per buffer: W (4 or 8), then tokens (4)
   static constexpr uint32_t TMEM_COLS = ACC_COLS + 2 * SF_COLS <= 64    ? 64
@@ -264,12 +266,17 @@ struct TokensCfg {
                                         : ACC_COLS + 2 * SF_COLS <= 256 ? 256
                                                                         : 512;
   static constexpr uint32_t SF_BYTES = (W_TILES + 1) * kSfRows;   // one chunk's words: W, then tokens
-  static constexpr size_t SMEM = 1024 + RING + kSfBufs * SF_BYTES;
+  static constexpr int SF_BUFS = 2;
+  static constexpr size_t SMEM = 1024 + RING + SF_BUFS * SF_BYTES;
+  // CTAs that can share an SM never ask for more tensor memory than it has, so that none waits for
+  // another's: with clusters, whose CTAs wait for each other, that could close a circle.
+  static constexpr int CTAS_PER_SM = static_cast<int>((228 * 1024) / (SMEM + 1024));
+  static_assert(CTAS_PER_SM * TMEM_COLS <= 512, "tensor memory for every CTA an SM can hold");
 };
 
 struct alignas(8) TokensCtrl {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t sf_full[kSfBufs], sf_empty[kSfBufs];
+  uint64_t sf_full[2], sf_empty[2];
   uint64_t done;
   uint32_t tmem_base;
   int abort;
@@ -278,22 +285,25 @@ struct alignas(8) TokensCtrl {
 constexpr int kTokensThreads = 192;  // producer, MMA issuer, four scale / accumulator warps
 
 template <int TN, bool kGlu>
-__global__ void __launch_bounds__(kTokensThreads, 1) fp8_tokens_kernel(const __grid_constant__ Fp8Params p) {
+__global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2 : 1) fp8_tokens_kernel(const __grid_constant__ Fp8Params p) {
   using C = TokensCfg<TN, kGlu>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TokensCtrl ctl_mem;
   TokensCtrl* ctl = &ctl_mem;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abort_flag = &ctl->abort;
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    // The maps are launch parameters, so their descriptors can be fetched before the wait below.
+    for (int r = 0; r < max(p.n_groups, p.n_segs); ++r) ptx::prefetch_tensormap(&p.map_w[r]);
+    for (int r = 0; r < p.n_segs; ++r) ptx::prefetch_tensormap(&p.map_x[r]);
     for (int s = 0; s < C::STAGES; ++s) {
       ptx::mbar_init(ptx::smem_addr(&ctl->full[s]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->empty[s]), 1);
     }
-    for (int b = 0; b < kSfBufs; ++b) {
+    for (int b = 0; b < C::SF_BUFS; ++b) {
       ptx::mbar_init(ptx::smem_addr(&ctl->sf_full[b]), 128);
       ptx::mbar_init(ptx::smem_addr(&ctl->sf_empty[b]), 1);
     }
@@ -302,6 +312,10 @@ __global__ void __launch_bounds__(kTokensThreads, 1) fp8_tokens_kernel(const __g
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
+  // Tensor memory is taken once the kernel before has ended, and only then may a dependent
+  // kernel's CTAs be scheduled: CTAs of two kernels of a stream on one SM could otherwise wait for
+  // each other's.
+  pdl_wait();
   if (warp == 0) {
     ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), C::TMEM_COLS);
     ptx::tmem_relinquish();
@@ -309,11 +323,8 @@ __global__ void __launch_bounds__(kTokensThreads, 1) fp8_tokens_kernel(const __g
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
-  // Only now may a dependent kernel's CTAs be scheduled: one that took tensor memory before this
-  // CTA had its own would wait for this kernel while this CTA waits for it.
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
   pdl_launch_dependents();
-  pdl_wait();
 
   // This CTA's tile and its share of the tile's chunks of K.
   const int splits = p.splits;
@@ -334,80 +345,98 @@ __global__ void __launch_bounds__(kTokensThreads, 1) fp8_tokens_kernel(const __g
   const uint32_t sf_base = ptx::smem_addr(base) + C::RING;
   bool gave_up = false;
 
+  // The producer and the MMA issuer spend a group's 16 KB, at an SM's share of the memory rate
+  // some 350 ns, in loops that have to be shorter: addresses are carried along, and the whole
+  // warp runs each loop, so that they stay in uniform registers; one lane issues.
+  const uint32_t ring = ptx::smem_addr(base);
+  const uint32_t full0 = ptx::smem_addr(&ctl->full[0]), empty0 = ptx::smem_addr(&ctl->empty[0]);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, p.status));
+  };
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ producer
-      uint32_t it = 0;
-      bool ok = true;
-      for (int c = c0; c < c1 && ok; ++c) {
-        const int seg = c / seg_chunks;
-        const int kg0 = (c - seg * seg_chunks) * kChunk;
-        const int n = min(kChunk, p.k_groups - kg0);
-        const CUtensorMap* mw = &p.map_w[w_of(seg)];
-        const CUtensorMap* mx = &p.map_x[x_of(seg)];
-        for (int k = 0; k < n; ++k, ++it) {
-          const uint32_t s = it % C::STAGES;
-          if (!wait_bounded(ptx::smem_addr(&ctl->empty[s]), ((it / C::STAGES) & 1u) ^ 1u, abort_flag, p.status)) {
+    // -------------------------------------------------------------- producer
+    const bool issuer = elect_one();
+    uint32_t stage = 0, phase = 1, issued = 0;
+    ChunkWalk at;
+    at.start(c0, seg_chunks);
+    bool ok = true;
+    for (int c = c0; c < c1 && ok; ++c, at.next(p.k_groups)) {
+      const int n = min(kChunk, p.k_groups - at.kg);
+      const CUtensorMap* mw = &p.map_w[w_of(at.seg)];
+      const CUtensorMap* mx = &p.map_x[x_of(at.seg)];
+      const int kx = at.kg * (KB / 2);  // the maps count 2-byte elements
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) {
+        if (k < n) {
+          if (!wait(empty0 + 8 * stage, phase)) {
             ok = false;
             break;
           }
-          const uint32_t full = ptx::smem_addr(&ctl->full[s]);
-          const uint32_t sw = ptx::smem_addr(base + s * C::STAGE_BYTES);
-          const int kx = (kg0 + k) * (KB / 2);  // the maps count 2-byte elements
-          ptx::mbar_arrive_expect_tx(full, C::STAGE_BYTES);
-          ptx::tma_load_2d(sw, mw, full, kx, w_row0);
-          if constexpr (kGlu) ptx::tma_load_2d(sw + kBoxA, mw, full, kx, p.up_row + w_row0);
-          ptx::tma_load_2d(sw + C::W_BYTES, mx, full, kx, t0);
+          if (issuer) {
+            const uint32_t full = full0 + 8 * stage, sw = ring + stage * C::STAGE_BYTES;
+            ptx::mbar_arrive_expect_tx(full, C::STAGE_BYTES);
+            ptx::tma_load_2d(sw, mw, full, kx + k * (KB / 2), w_row0);
+            if constexpr (kGlu) ptx::tma_load_2d(sw + kBoxA, mw, full, kx + k * (KB / 2), p.up_row + w_row0);
+            ptx::tma_load_2d(sw + C::W_BYTES, mx, full, kx + k * (KB / 2), t0);
+          }
+          ++issued;
+          if (++stage == C::STAGES) stage = 0, phase ^= 1u;
         }
       }
-      // Every copy this thread issued lands before the CTA can exit.
-      const uint32_t first = it > C::STAGES ? it - C::STAGES : 0;
-      for (uint32_t j = first; j < it; ++j)
-        wait_bounded(ptx::smem_addr(&ctl->full[j % C::STAGES]), (j / C::STAGES) & 1u, abort_flag, p.status, true);
     }
+    // Every copy lands before the CTA can exit.
+    const uint32_t first = issued > C::STAGES ? issued - C::STAGES : 0;
+    for (uint32_t i = first; i < issued; ++i)
+      wait_bounded(full0 + 8 * (i % C::STAGES), (i / C::STAGES) & 1u, abort_flag, p.status, true);
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issuer
-      constexpr uint32_t idesc = idesc_mx(BM, TN);
-      uint32_t it = 0, accumulate = 0;
-      bool ok = true;
-      for (int c = c0; c < c1 && ok; ++c) {
-        const int i = c - c0;
-        const int seg = c / seg_chunks;
-        const int n = min(kChunk, p.k_groups - (c - seg * seg_chunks) * kChunk);
-        const uint32_t buf = i % kSfBufs;
-        if (!wait_bounded(ptx::smem_addr(&ctl->sf_full[buf]), (i / kSfBufs) & 1u, abort_flag, p.status)) break;
-        const uint32_t sf = tmem + C::ACC_COLS + (i & 1) * C::SF_COLS;
-        const uint32_t words = sf_base + buf * C::SF_BYTES;
+    // -------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc = idesc_mx(BM, TN);
+    const bool issuer = elect_one();
+    const uint64_t w0 = ptx::sw128_kmajor_desc(ring);
+    const uint32_t sf_full0 = ptx::smem_addr(&ctl->sf_full[0]), sf_empty0 = ptx::smem_addr(&ctl->sf_empty[0]);
+    uint64_t wdesc = w0;
+    uint32_t stage = 0, phase = 0, accumulate = 0;
+    ChunkWalk at;
+    at.start(c0, seg_chunks);
+    bool ok = true;
+    for (int i = 0; i < c1 - c0 && ok; ++i, at.next(p.k_groups)) {
+      const int n = min(kChunk, p.k_groups - at.kg);
+      const uint32_t buf = i % C::SF_BUFS;
+      if (!wait(sf_full0 + 8 * buf, (i / C::SF_BUFS) & 1u)) break;
+      const uint32_t sf = tmem + C::ACC_COLS + (i & 1) * C::SF_COLS;
+      if (issuer)
 #pragma unroll
-        for (int a = 0; a <= C::W_TILES; ++a) copy_scales<false>(sf + 4 * a, words + a * kSfRows);
-        for (int k = 0; k < n; ++k, ++it) {
-          const uint32_t s = it % C::STAGES;
-          if (!wait_bounded(ptx::smem_addr(&ctl->full[s]), (it / C::STAGES) & 1u, abort_flag, p.status)) {
+        for (int a = 0; a <= C::W_TILES; ++a)
+          copy_scales<false>(sf + 4 * a, sf_base + buf * C::SF_BYTES + a * kSfRows);
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) {
+        if (k < n) {
+          if (!wait(full0 + 8 * stage, phase)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t sw = ptx::smem_addr(base + s * C::STAGE_BYTES);
-          const uint64_t wdesc = ptx::sw128_kmajor_desc(sw);
-          const uint64_t xdesc = ptx::sw128_kmajor_desc(sw + C::W_BYTES);
-          const uint32_t id = idesc | idesc_scale_byte(static_cast<uint32_t>(k));
+          if (issuer) {
+            const uint64_t xdesc = wdesc + (C::W_BYTES >> 4);
+            const uint32_t id = idesc | idesc_scale_byte(static_cast<uint32_t>(k));
 #pragma unroll
-          for (int j = 0; j < KB / 32; ++j) {  // +32 bytes along K = +2 in the descriptor's 16-byte units
-            umma_mx(tmem, wdesc + 2 * j, xdesc + 2 * j, id, sf, sf + 4 * C::W_TILES, accumulate);
-            if constexpr (kGlu) {
-              const uint64_t udesc = ptx::sw128_kmajor_desc(sw + kBoxA);
-              umma_mx(tmem + TN, udesc + 2 * j, xdesc + 2 * j, id, sf + 4, sf + 4 * C::W_TILES, accumulate);
+            for (int j = 0; j < KB / 32; ++j) {  // +32 bytes along K = +2 in the descriptor's 16-byte units
+              umma_mx(tmem, wdesc + 2 * j, xdesc + 2 * j, id, sf, sf + 4 * C::W_TILES, j > 0 ? 1u : accumulate);
+              if constexpr (kGlu)
+                umma_mx(tmem + TN, wdesc + (kBoxA >> 4) + 2 * j, xdesc + 2 * j, id, sf + 4, sf + 4 * C::W_TILES,
+                        j > 0 ? 1u : accumulate);
             }
-            accumulate = 1;
+            ptx::umma_commit(empty0 + 8 * stage);
           }
-          ptx::umma_commit(ptx::smem_addr(&ctl->empty[s]));
+          accumulate = 1;
+          wdesc += C::STAGE_BYTES >> 4;
+          if (++stage == C::STAGES) stage = 0, phase ^= 1u, wdesc = w0;
         }
-        ptx::umma_commit(ptx::smem_addr(&ctl->sf_empty[buf]));
       }
-      ptx::umma_commit(ptx::smem_addr(&ctl->done));
-      wait_bounded(ptx::smem_addr(&ctl->done), 0, abort_flag, p.status, true);
+      if (issuer && ok) ptx::umma_commit(sf_empty0 + 8 * buf);
     }
+    if (issuer) ptx::umma_commit(ptx::smem_addr(&ctl->done));
+    wait_bounded(ptx::smem_addr(&ctl->done), 0, abort_flag, p.status, true);
   } else {
     // -------------------------------------------------------------- scales, then the partial tile
     const int q = warp & 3;  // TMEM lane quarter this warp may access
@@ -425,13 +454,13 @@ __global__ void __launch_bounds__(kTokensThreads, 1) fp8_tokens_kernel(const __g
     at.start(c0, seg_chunks);
     load(at);
     for (int i = 0; i < c1 - c0; ++i) {
-      const uint32_t buf = i % kSfBufs;
+      const uint32_t buf = i % C::SF_BUFS;
       const uint32_t w = w_next, u = u_next, x = x_next;
       if (i + 1 < c1 - c0) {
         at.next(p.k_groups);
         load(at);
       }
-      if (!__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&ctl->sf_empty[buf]), ((i / kSfBufs) & 1u) ^ 1u,
+      if (!__all_sync(0xffffffffu, wait_bounded(ptx::smem_addr(&ctl->sf_empty[buf]), ((i / C::SF_BUFS) & 1u) ^ 1u,
                                                 abort_flag, p.status))) {
         gave_up = true;
         break;
@@ -948,6 +977,28 @@ tp_status operand_map(CUtensorMap* m, const void* ptr, int64_t K, int64_t rows, 
   return encode_bf16_2d(m, ptr, K / 2, rows, ld / 2, KB / 2, static_cast<uint32_t>(box_rows), true);
 }
 
+// The operands of a call, checked.
+struct Fp8Call {
+  const void* const* x;         // one (shared) or tp_degree
+  const void* const* sx;
+  bool x_shared;
+  int64_t ldx, ld_sx;
+  const void* const* w;
+  const void* const* sw;
+  int p;
+  int64_t T, K, w_rows, n_out;
+};
+
+// The maps of X and W in boxes of x_box and w_box rows.
+tp_status set_maps(const Fp8Call& c, Fp8Params& p, int x_box, int w_box) {
+  for (int r = 0; r < c.p; ++r) {
+    tp_status st = operand_map(&p.map_w[r], c.w[r], c.K, c.w_rows, c.K, w_box);
+    if (st == TP_OK && (r == 0 || !c.x_shared)) st = operand_map(&p.map_x[r], c.x[r], c.K, c.T, c.ldx, x_box);
+    if (st != TP_OK) return st;
+  }
+  return TP_OK;
+}
+
 // Clusters of `splits` CTAs that can be resident at once (cached per device and kernel).
 template <int TN, bool kGlu>
 tp_status resident_clusters(int splits, int* n) {
@@ -985,14 +1036,15 @@ tp_status resident_clusters(int splits, int* n) {
 }
 
 template <int TN, bool kGlu>
-tp_status launch_tokens(Fp8Params& p, cudaStream_t stream) {
-  const int64_t tiles = static_cast<int64_t>(p.n_groups) * p.n_tiles * p.t_tiles;
+tp_status launch_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   const int chunks = p.n_segs * ceil_div(p.k_groups, kChunk);
-  // The split of K whose longest CTA column is shortest: waves x (its chunks + the fixed part of
-  // a CTA's life, about one chunk's time).  Ties go to the smaller cluster.
+  p.n_tiles = ceil_div(p.n_out, BM);
+  const int64_t tiles = static_cast<int64_t>(p.n_groups) * p.n_tiles * p.t_tiles;
   int best = 0;
   int64_t best_cost = 0;
+  const char* fs = getenv("TP_FP8_S");
   for (int s = 1; s <= kMaxSplits && s <= chunks; ++s) {
+    if (fs && atoi(fs) != s) continue;
     int n = 0;
     tp_status st = resident_clusters<TN, kGlu>(s, &n);
     if (st != TP_OK) return st;
@@ -1001,8 +1053,11 @@ tp_status launch_tokens(Fp8Params& p, cudaStream_t stream) {
     if (best == 0 || cost < best_cost) best = s, best_cost = cost;
   }
   if (best == 0) return fail(TP_ERR_UNSUPPORTED, "the kernel does not fit on this device");
+  if (getenv("TP_FP8_DBG")) fprintf(stderr, "TN %d glu %d: split %d tiles %d\n", TN, kGlu, best, (int)tiles);
   if (tiles * best > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many tiles (%lld)", (long long)tiles);
   p.splits = best;
+  tp_status st = set_maps(c, p, TN, BM);
+  if (st != TP_OK) return st;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * best), 1, 1);
   cfg.blockDim = dim3(kTokensThreads, 1, 1);
@@ -1091,27 +1146,6 @@ int choose_group_m(int t_items, int tiles_per_item, int64_t x_bytes) {
   return ceil_div(t_items, groups);
 }
 
-// The operands of a call, checked.
-struct Fp8Call {
-  const void* const* x;         // one (shared) or tp_degree
-  const void* const* sx;
-  bool x_shared;
-  int64_t ldx, ld_sx;
-  const void* const* w;
-  const void* const* sw;
-  int p;
-  int64_t T, K, w_rows, n_out;
-};
-
-// The maps of X and W in boxes of x_box and w_box rows.
-tp_status set_maps(const Fp8Call& c, Fp8Params& p, int x_box, int w_box) {
-  for (int r = 0; r < c.p; ++r) {
-    tp_status st = operand_map(&p.map_w[r], c.w[r], c.K, c.w_rows, c.K, w_box);
-    if (st == TP_OK && (r == 0 || !c.x_shared)) st = operand_map(&p.map_x[r], c.x[r], c.K, c.T, c.ldx, x_box);
-    if (st != TP_OK) return st;
-  }
-  return TP_OK;
-}
 
 template <bool kGlu>
 tp_status run_prompt(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
@@ -1137,11 +1171,8 @@ tp_status run_prompt(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
 
 template <int TN>
 tp_status run_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
-  p.n_tiles = ceil_div(c.n_out, BM);
   p.t_tiles = ceil_div(c.T, TN);
-  tp_status st = set_maps(c, p, TN, BM);
-  if (st != TP_OK) return st;
-  return p.act == TP_ACT_SWIGLU ? launch_tokens<TN, true>(p, stream) : launch_tokens<TN, false>(p, stream);
+  return p.act == TP_ACT_SWIGLU ? launch_tokens<TN, true>(c, p, stream) : launch_tokens<TN, false>(c, p, stream);
 }
 
 tp_status run_fp8(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
