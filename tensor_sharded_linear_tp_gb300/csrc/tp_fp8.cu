@@ -134,6 +134,11 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+// Cluster barrier that orders no memory (what has been read is in registers).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // Bounded wait: true when the phase completed, false when this CTA is giving up.
 // kCluster: the phase's arrivals may come from the other CTA of a pair.
 template <bool kCluster>
@@ -508,10 +513,13 @@ __global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2
         const uint32_t at = local + static_cast<uint32_t>(a * TN + t) * (BM * 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[a][e] = 0.0f;
-        for (int s = 0; s < splits; ++s) {
-          const float4 f = ld_cluster_f4(ptx::mapa_shared(at, static_cast<uint32_t>(s)));
-          v[a][0] += f.x, v[a][1] += f.y, v[a][2] += f.z, v[a][3] += f.w;
-        }
+        float4 f[kMaxSplits];  // all in flight together
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+          if (s < splits) f[s] = ld_cluster_f4(ptx::mapa_shared(at, static_cast<uint32_t>(s)));
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+          if (s < splits) v[a][0] += f[s].x, v[a][1] += f[s].y, v[a][2] += f[s].z, v[a][3] += f[s].w;
         if (bias != nullptr && on)
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[a][e] += __bfloat162float(bias[n0 + e + (a ? p.up_row : 0)]);
@@ -542,7 +550,7 @@ __global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2
       }
     }
   }
-  ptx::cluster_sync();  // no CTA's shared memory goes away while another reads it
+  cluster_sync_relaxed();  // no CTA's shared memory goes away while another reads it
   if (warp == 0) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::TMEM_COLS);
