@@ -10,8 +10,8 @@ been built, importing this package raises ImportError.
 from __future__ import annotations
 
 import ctypes
-import operator
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -72,11 +72,11 @@ _SIGS = {
     "tp_attention_ranks_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, _i64, ctypes.c_int, ctypes.c_int]),
     "tp_combine": (_status, [ctypes.c_int, ctypes.POINTER(_vp), ctypes.c_int, _i64, _i64, _vp, _vp]),
     "tp_quantize_fp8": (_status, [_vp, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp, _i64, _vp]),
-    "tp_linear_colwise_fp8": (_status, [_vp, _i64, _vp, _i64, ctypes.POINTER(_vp), ctypes.POINTER(_vp),
-                                        ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, _i64, _i64, _i64,
-                                        ctypes.POINTER(_vp), _i64, ctypes.POINTER(_vp), _i64, _vp]),
-    "tp_linear_rowwise_fp8": (_status, [ctypes.POINTER(_vp), _i64, ctypes.POINTER(_vp), _i64, ctypes.POINTER(_vp),
-                                        ctypes.POINTER(_vp), _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp]),
+    # (their arrays of pointers are passed as bytes, see _pointers)
+    "tp_linear_colwise_fp8": (_status, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, ctypes.c_int, ctypes.c_int, _i64, _i64,
+                                        _i64, _vp, _i64, _vp, _i64, _vp]),
+    "tp_linear_rowwise_fp8": (_status, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp,
+                                        _i64, _vp]),
     "tp_last_error": (ctypes.c_char_p, []),
     "tp_status_name": (ctypes.c_char_p, [ctypes.c_int]),
     "tp_device_status": (_status, [_vp]),
@@ -115,7 +115,9 @@ class ResidualNormArgs(ctypes.Structure):
 
 
 _SIGS["tp_plan_shard_many"] = (_status, [ctypes.POINTER(ShardRequest), ctypes.c_int, _vp])
-_SIGS["tp_residual_norm"] = (_status, [ctypes.POINTER(ResidualNormArgs), _vp])
+_SIGS["tp_residual_norm"] = (_status, [_vp, _vp])
+# The same structure as bytes, in native alignment (q: int64, P: pointer, i: enum).
+_residual_norm_args = struct.Struct("@qq PqPq iPP ff PPP qqq Pq iPP PqPq").pack
 
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -467,9 +469,8 @@ def tp_combine(mode: str, partials: Sequence[torch.Tensor], out: torch.Tensor | 
 # ---------------------------------------------------------------------------
 
 _E4M3, _E8M0, _BF16, _U8 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.bfloat16, torch.uint8
-_POINTERS = [_vp * n for n in range(MAX_DEGREE + 1)]
-_kind = operator.attrgetter("dtype", "shape")
-_data_ptr, _contiguous, _gpu = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
+# A host array of n device pointers, as the bytes of one (made in a fifth of the time of a ctypes array).
+_pointers = [struct.Struct(f"{n}P").pack for n in range(MAX_DEGREE + 1)]
 
 
 def _groups(n: int) -> int:
@@ -480,7 +481,7 @@ def _need(name, t, dtype, shape, dev):
     """A tensor of `dtype` (a scale: e8m0 or uint8) and `shape` on the current GPU, its last dimension contiguous.
 
     Returns the row stride (0 where the rows are dense)."""
-    if _kind(t) == (dtype, shape) and t.get_device() == dev and t.is_contiguous():
+    if t.dtype is dtype and t.is_contiguous() and t.shape == shape and t.get_device() == dev:
         return 0
     if t.dtype is not dtype and not (dtype is _E8M0 and t.dtype is _U8):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -503,17 +504,20 @@ def _need(name, t, dtype, shape, dev):
 
 def _need_ranks(name, ts, dtype, shape, dev, dense=False):
     """(pointer array, row stride) of one tensor for each rank, as _need; every rank has the same row stride."""
-    # The usual case, in as few steps as it takes: a call with few tokens is as long as its checks.
-    n = len(ts)
-    if list(map(_kind, ts)) == [(dtype, shape)] * n and all(map(_contiguous, ts)) and [dev] * n == list(map(_gpu, ts)):
-        return _POINTERS[n](*map(_data_ptr, ts)), 0
+    at = []
+    for t in ts:   # the usual case, in as few steps as it takes: a call with few tokens is as long as its checks
+        if t.dtype is not dtype or not t.is_contiguous() or t.shape != shape or t.get_device() != dev:
+            break
+        at.append(t.data_ptr())
+    else:
+        return _pointers[len(at)](*at), 0
     steps = [_need(f"{name}[{i}]", t, dtype, shape, dev) for i, t in enumerate(ts)]
     if any(s not in (0, shape[1]) for s in steps):
         if dense:
             raise ValueError(f"every rank's {name} must be contiguous")
         if any(s != steps[0] for s in steps):
             raise ValueError(f"every rank's {name} must have the same row stride")
-    return _POINTERS[n](*map(_data_ptr, ts)), steps[0]
+    return _pointers[len(ts)](*[t.data_ptr() for t in ts]), steps[0]
 
 
 def _alloc(stream, dev, dtype, shape, count=1):
@@ -602,7 +606,7 @@ def tp_linear_colwise_fp8(x: torch.Tensor, x_scales: torch.Tensor, w_shards: Seq
         for i, b in enumerate(bias_shards):
             if b is not None:
                 _need(f"bias_shards[{i}]", b, _BF16, (N,), dev)
-        bias = _POINTERS[p](*[None if b is None else b.data_ptr() for b in bias_shards])
+        bias = _pointers[p](*[0 if b is None else b.data_ptr() for b in bias_shards])
     n = N // 2 if act == "swiglu" else N
     if y_shards is None:
         y_shards = _alloc(stream, dev, _E4M3 if fp8 else _BF16, (T, n), p)
@@ -667,51 +671,48 @@ def tp_residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, norm: str =
     T, D = shape
     ldx = _need("x", x, _BF16, shape, dev)
 
-    def vec(name, t):
-        if t is None:
-            return None
-        _need(name, t, _BF16, (D,), dev)
-        return t.data_ptr()
-
-    mod = None  # (row stride, rows) of the tables
-
-    def table(name, t):
-        nonlocal mod
-        if t is None:
-            return None
-        rows = 1 if t.dim() == 1 else t.shape[0]
-        step = _need(name, t, _BF16, (D,) if t.dim() == 1 else (rows, D), dev)
-        if mod is None:
-            mod = step, rows
-        elif mod != (step, rows):
-            raise ValueError("gate, scale and shift must have the same rows and row stride")
-        return t.data_ptr()
-
-    gate_at, scale_at, shift_at = table("gate", gate), table("scale", scale), table("shift", shift)
-    y_at, ldy = None, 0
+    vectors = [0, 0, 0, 0]
+    if weight is not None or bias is not None or post_weight is not None or post_bias is not None:
+        for i, (name, t) in enumerate((("weight", weight), ("bias", bias), ("post_weight", post_weight),
+                                       ("post_bias", post_bias))):
+            if t is not None:
+                _need(name, t, _BF16, (D,), dev)
+                vectors[i] = t.data_ptr()
+    tables, mod = [0, 0, 0], None   # mod: (row stride, rows) of the tables
+    if gate is not None or scale is not None or shift is not None:
+        for i, (name, t) in enumerate((("gate", gate), ("scale", scale), ("shift", shift))):
+            if t is not None:
+                rows = 1 if t.dim() == 1 else t.shape[0]
+                step = _need(name, t, _BF16, (D,) if t.dim() == 1 else (rows, D), dev)
+                if mod is None:
+                    mod = step, rows
+                elif mod != (step, rows):
+                    raise ValueError("gate, scale and shift must have the same rows and row stride")
+                tables[i] = t.data_ptr()
+    y_at, ldy = 0, 0
     if y is not None:
         y_at, ldy = y.data_ptr(), _need("y", y, _BF16, shape, dev)
         if h is None:
             h, = _alloc(stream, dev, _BF16, shape)
-    h_at, ldh = (None, 0) if h is None else (h.data_ptr(), _need("h", h, _BF16, shape, dev))
-    u_at, ldu, s_at, ld_us = None, 0, None, 0
+    h_at, ldh = (0, 0) if h is None else (h.data_ptr(), _need("h", h, _BF16, shape, dev))
+    u_at, ldu, s_at, ld_us = 0, 0, 0, 0
     if out is not None:
         u_type = _E4M3 if fp8 else _BF16
         if u is None:
             u, = _alloc(stream, dev, u_type, shape)
         u_at, ldu = u.data_ptr(), _need("u", u, u_type, shape, dev)
         if fp8:
+            s_shape = (T, _groups(D))
             if u_scales is None:
-                u_scales, = _alloc(stream, dev, _E8M0, (T, _groups(D)))
-            s_at, ld_us = u_scales.data_ptr(), _need("u_scales", u_scales, _E8M0, (T, _groups(D)), dev)
+                u_scales, = _alloc(stream, dev, _E8M0, s_shape)
+            s_at, ld_us = u_scales.data_ptr(), _need("u_scales", u_scales, _E8M0, s_shape, dev)
     ld_mod, mod_rows = mod or (0, 0)
     if mod and rows_per_mod is None:
         rows_per_mod = max(T, 1)
-    a = ResidualNormArgs(T, D, x.data_ptr(), ldx, y_at, ldy, NORMS[post_norm], vec("post_weight", post_weight),
-                         vec("post_bias", post_bias), alpha, eps, gate_at, scale_at, shift_at, ld_mod, mod_rows,
-                         rows_per_mod if mod else 0, h_at, ldh, 0 if out is None else NORMS[norm],
-                         vec("weight", weight), vec("bias", bias), u_at, ldu, s_at, ld_us)
-    _check(lib.tp_residual_norm(ctypes.byref(a), _launch_stream(stream, dev)))
+    args = _residual_norm_args(T, D, x.data_ptr(), ldx, y_at, ldy, NORMS[post_norm], vectors[2], vectors[3], alpha, eps,
+                               *tables, ld_mod, mod_rows, rows_per_mod if mod else 0, h_at, ldh,
+                               0 if out is None else NORMS[norm], vectors[0], vectors[1], u_at, ldu, s_at, ld_us)
+    _check(lib.tp_residual_norm(args, _launch_stream(stream, dev)))
     return h, u, u_scales
 
 

@@ -192,3 +192,8 @@ def test_struct_mirrors_header():
     body = re.sub(r"/\*.*?\*/", "", body[body.rindex("typedef struct {"):], flags=re.S)
     names = re.findall(r"[\*\s,](\w+)\s*(?=[;,])", body)
     assert names == [n for n, _ in tp.ResidualNormArgs._fields_]
+    values = [float(i + 1) if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(tp.ResidualNormArgs._fields_)]
+    packed = tp._residual_norm_args(*values)
+    assert len(packed) == ctypes.sizeof(tp.ResidualNormArgs)
+    a = tp.ResidualNormArgs.from_buffer_copy(packed)
+    assert [getattr(a, n) for n in names] == values
