@@ -130,82 +130,149 @@ struct NormParams {
   int D;
   int post_norm, norm;
   float alpha, eps;
+  bool prefetch;  // few rows: fetch the vectors and tables ahead of their use
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
-  v[4] = bf16_lo(a.z), v[5] = bf16_hi(a.z), v[6] = bf16_lo(a.w), v[7] = bf16_hi(a.w);
+// Two fp32 values in one 64-bit register, for the paired instructions: the row's arithmetic, not
+// its bytes, is what a scalar version of this kernel is bound by (51 instructions an element).
+using f2 = uint64_t;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  auto two = [](float a, float b) {
+__device__ __forceinline__ void unpair(f2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+  float a, b;
+  unpair(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ void unpack8(const uint4& a, f2 (&v)[4]) {
+  v[0] = pair(bf16_lo(a.x), bf16_hi(a.x)), v[1] = pair(bf16_lo(a.y), bf16_hi(a.y));
+  v[2] = pair(bf16_lo(a.z), bf16_hi(a.z)), v[3] = pair(bf16_lo(a.w), bf16_hi(a.w));
+}
+// Eight elements of a vector or table that many rows read: they stay in L1.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, f2 (&v)[4]) {
+  unpack8(__ldg(reinterpret_cast<const uint4*>(p)), v);
+}
+// Eight elements of a row that is read once: past L1, which keeps the tables.
+__device__ __forceinline__ uint4 load_row8(const __nv_bfloat16* p) {
+  uint4 a;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w)
+               : "l"(p));
+  return a;
+}
+__device__ __forceinline__ void prefetch_l2(const __nv_bfloat16* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const f2 (&v)[4]) {
+  auto two = [](f2 v) {
+    float a, b;
+    unpair(v, a, b);
     const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&t);
   };
-  *reinterpret_cast<uint4*>(p) = make_uint4(two(v[0], v[1]), two(v[2], v[3]), two(v[4], v[5]), two(v[6], v[7]));
+  *reinterpret_cast<uint4*>(p) = make_uint4(two(v[0]), two(v[1]), two(v[2]), two(v[3]));
+}
+// max(m, |v|), NaN if either is.
+__device__ __forceinline__ float max_abs(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
 }
 
-// Sum over the threads that hold one row: a warp, or the CTA (a fixed order either way).
+// Sum over the threads that hold one row: a warp, or the CTA (a fixed order either way).  Sums of
+// a row alternate between two parts of the scratch, so that one barrier each is enough: a part is
+// written again only after the barrier of the sum between, which every reader has passed.
 template <int kThreads>
-__device__ __forceinline__ float row_sum(float v, float* scratch) {
+__device__ __forceinline__ float row_sum(float v, float (&scratch)[2][32], int part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (kThreads > 32) {
-    __syncthreads();  // the previous sum's readers are done with the scratch
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) scratch[part][threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) v += scratch[w];
+    for (int w = 0; w < kThreads / 32; ++w) v += scratch[part][w];
   }
   return v;
 }
 
-// v <- norm(v) over one row of D elements; elements past D are not part of the sums.
+// v <- norm(v) over one row of D elements; elements past D are not part of the sums.  `part`: the
+// scratch part of the first sum, moved on past the last.
 template <int kThreads, int kVecs>
-__device__ __forceinline__ void normalise(float (&v)[kVecs][8], int kind, int D, float eps, int lane, float* scratch,
-                                          const __nv_bfloat16* weight, const __nv_bfloat16* bias) {
+__device__ __forceinline__ void normalise(f2 (&v)[kVecs][4], int kind, int D, float eps, int lane,
+                                          float (&scratch)[2][32], int& part, const __nv_bfloat16* weight,
+                                          const __nv_bfloat16* bias) {
   if (kind == TP_NORM_NONE) return;
   const float inv_d = 1.0f / static_cast<float>(D);
   if (kind == TP_NORM_LAYER) {
-    float s = 0.0f;
+    f2 s = 0;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)  // (a vector past D is zero here)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = add2(s, v[j][i]);
+    const float mean = row_sum<kThreads>(sum2(s), scratch, part) * inv_d;
+    part ^= 1;
+    const f2 minus = pair(-mean, -mean);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
       if ((j * kThreads + lane) * 8 < D)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += v[j][i];
-    const float mean = row_sum<kThreads>(s, scratch) * inv_d;
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] -= mean;
+        for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], minus);
   }
-  float s = 0.0f;
+  f2 s = 0;
 #pragma unroll
   for (int j = 0; j < kVecs; ++j)
-    if ((j * kThreads + lane) * 8 < D)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(v[j][i], v[j][i], s);
-  const float r = 1.0f / sqrtf(row_sum<kThreads>(s, scratch) * inv_d + eps);
+    for (int i = 0; i < 4; ++i) s = fma2(v[j][i], v[j][i], s);
+  const float r = 1.0f / sqrtf(row_sum<kThreads>(sum2(s), scratch, part) * inv_d + eps);
+  part ^= 1;
+  const f2 rr = pair(r, r);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     const int col = (j * kThreads + lane) * 8;
-    float w[8], b[8];
-    if (weight != nullptr && col < D) load8(weight + col, w);
-    if (bias != nullptr && col < D) load8(bias + col, b);
+    if (col >= D) continue;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[j][i] *= r;
-      if (weight != nullptr) v[j][i] *= w[i];
-      if (bias != nullptr) v[j][i] += b[i];
+    for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], rr);
+    if (weight != nullptr) {  // uniform, as the other optional vectors
+      f2 w[4];
+      load8(weight + col, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], w[i]);
+    }
+    if (bias != nullptr) {
+      f2 w[4];
+      load8(bias + col, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], w[i]);
     }
   }
 }
 
 // kThreads threads hold a row (32: one warp, four rows a CTA), kVecs vectors of 8 elements each.
 template <int kThreads, int kVecs>
-__global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128) residual_norm_kernel(const NormParams p) {
-  __shared__ float scratch[32];
+__global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 ? 1024 / kThreads : 8)
+    residual_norm_kernel(const NormParams p) {
+  __shared__ float scratch[2][32];
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kRows = kThreads > 32 ? 1 : 4;
@@ -213,75 +280,99 @@ __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128) residual_norm_
   if (row >= p.T) return;  // warp-uniform; with one row a CTA the grid is exact
   const int lane = kRows > 1 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int64_t mod = p.rows_per_mod > 0 ? row / p.rows_per_mod * p.ld_mod : 0;
-  float v[kVecs][8];
+  // Both rows are asked for at once, and with few rows, where the launch is as long as its chain
+  // of memory accesses, the vectors and tables as well.
+  uint4 xs[kVecs], ys[kVecs];
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     const int col = (j * kThreads + lane) * 8;
-    if (p.y != nullptr && col < p.D) {
-      load8(p.y + row * p.ldy + col, v[j]);
+    xs[j] = ys[j] = make_uint4(0, 0, 0, 0);
+    if (col < p.D) {
+      if (p.y != nullptr) ys[j] = load_row8(p.y + row * p.ldy + col);
+      xs[j] = load_row8(p.x + row * p.ldx + col);
+    }
+  }
+  if (p.prefetch) {
+    const __nv_bfloat16* const vectors[4] = {p.post_weight, p.post_bias, p.weight, p.bias};
+    const __nv_bfloat16* const tables[3] = {p.gate, p.scale, p.shift};
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int col = (j * kThreads + lane) * 8;
+      if (col < p.D) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (tables[i] != nullptr) prefetch_l2(tables[i] + mod + col);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (vectors[i] != nullptr) prefetch_l2(vectors[i] + col);
+      }
+    }
+  }
+  f2 v[kVecs][4];  // zero past D
+  int part = 0;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) unpack8(ys[j], v[j]);
+  if (p.y != nullptr)
+    normalise<kThreads, kVecs>(v, p.post_norm, p.D, p.eps, lane, scratch, part, p.post_weight, p.post_bias);
+  const f2 alpha = pair(p.alpha, p.alpha);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int col = (j * kThreads + lane) * 8;
+    if (col >= p.D) continue;
+    f2 x[4];
+    unpack8(xs[j], x);
+    if (p.gate != nullptr) {
+      f2 g[4];
+      load8(p.gate + mod + col, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], g[i]);
+    }
+    if (p.y != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = fma2(alpha, x[i], v[j][i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+      for (int i = 0; i < 4; ++i) v[j][i] = mul2(alpha, x[i]);
     }
-  }
-  if (p.y != nullptr)
-    normalise<kThreads, kVecs>(v, p.post_norm, p.D, p.eps, lane, scratch, p.post_weight, p.post_bias);
-#pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    const int col = (j * kThreads + lane) * 8;
-    if (col < p.D) {
-      float x[8];
-      load8(p.x + row * p.ldx + col, x);
-      if (p.gate != nullptr) {
-        float g[8];
-        load8(p.gate + mod + col, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] *= g[i];
-      }
-      if (p.y != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = fmaf(p.alpha, x[i], v[j][i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = p.alpha * x[i];
-      }
-      if (p.h != nullptr) store8(p.h + row * p.ldh + col, v[j]);
-    }
+    if (p.h != nullptr) store8(p.h + row * p.ldh + col, v[j]);
   }
   if (p.u == nullptr && p.u8 == nullptr) return;  // uniform over the grid
-  normalise<kThreads, kVecs>(v, p.norm, p.D, p.eps, lane, scratch, p.weight, p.bias);
+  normalise<kThreads, kVecs>(v, p.norm, p.D, p.eps, lane, scratch, part, p.weight, p.bias);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     const int col = (j * kThreads + lane) * 8;
     const bool on = col < p.D;
     if (on && p.scale != nullptr) {
-      float s[8];
+      f2 s[4];
       load8(p.scale + mod + col, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] *= 1.0f + s[i];
+      for (int i = 0; i < 4; ++i) v[j][i] = fma2(v[j][i], s[i], v[j][i]);
     }
     if (on && p.shift != nullptr) {
-      float s[8];
+      f2 s[4];
       load8(p.shift + mod + col, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] += s[i];
+      for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], s[i]);
     }
     if (p.u != nullptr) {
       if (on) store8(p.u + row * p.ldu + col, v[j]);
     } else {
       // 16 lanes hold a group of 128.
-      uint32_t m = 0;
-      if (on)
+      float e[8], m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[j][i]));
+      for (int i = 0; i < 4; ++i) unpair(v[j][i], e[2 * i], e[2 * i + 1]);
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const uint32_t byte = e8m0_of_amax(m);
+      for (int i = 0; i < 8; ++i) m = max_abs(m, e[i]);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const uint32_t byte = e8m0_of_amax(__float_as_uint(m));
       const float inv = e8m0_inverse(byte);
       if (on) {
-        const uint2 c = make_uint2(e4m3x4(v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv),
-                                   e4m3x4(v[j][4] * inv, v[j][5] * inv, v[j][6] * inv, v[j][7] * inv));
-        *reinterpret_cast<uint2*>(p.u8 + row * p.ldu + col) = c;
+        const f2 ii = pair(inv, inv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpair(mul2(v[j][i], ii), e[2 * i], e[2 * i + 1]);
+        *reinterpret_cast<uint2*>(p.u8 + row * p.ldu + col) =
+            make_uint2(e4m3x4(e[0], e[1], e[2], e[3]), e4m3x4(e[4], e[5], e[6], e[7]));
         if ((lane & 15) == 0) p.u_scales[row * p.ld_us + col / kFp8Group] = static_cast<uint8_t>(byte);
       }
     }
@@ -299,16 +390,24 @@ tp_status launch_norm(const NormParams& p, cudaStream_t stream) {
   return TP_OK;
 }
 
-// Rows up to 1024 wide take a warp, longer ones the smallest CTA whose threads hold four vectors or fewer.
+// Rows up to 1024 wide take a warp, longer ones the smallest CTA whose threads hold four vectors or
+// fewer.  With fewer rows than SMs a launch is one row's latency, and a row gets more threads.
 tp_status dispatch_norm(const NormParams& p, cudaStream_t s) {
   const int vecs = (p.D + 7) / 8;
-  if (vecs <= 32) return launch_norm<32, 1>(p, s);
-  if (vecs <= 64) return launch_norm<32, 2>(p, s);
-  if (vecs <= 128) return launch_norm<32, 4>(p, s);
-  if (vecs <= 256) return launch_norm<256, 1>(p, s);
-  if (vecs <= 512) return launch_norm<256, 2>(p, s);
-  if (vecs <= 768) return launch_norm<256, 3>(p, s);
-  if (vecs <= 1024) return launch_norm<256, 4>(p, s);
+  if (p.prefetch) {
+    if (vecs <= 128) return launch_norm<128, 1>(p, s);
+    if (vecs <= 256) return launch_norm<256, 1>(p, s);
+    if (vecs <= 512) return launch_norm<512, 1>(p, s);
+    if (vecs <= 1024) return launch_norm<1024, 1>(p, s);
+  } else {
+    if (vecs <= 32) return launch_norm<32, 1>(p, s);
+    if (vecs <= 64) return launch_norm<32, 2>(p, s);
+    if (vecs <= 128) return launch_norm<32, 4>(p, s);
+    if (vecs <= 256) return launch_norm<256, 1>(p, s);
+    if (vecs <= 512) return launch_norm<256, 2>(p, s);
+    if (vecs <= 768) return launch_norm<256, 3>(p, s);
+    if (vecs <= 1024) return launch_norm<256, 4>(p, s);
+  }
   if (vecs <= 2048) return launch_norm<512, 4>(p, s);
   return launch_norm<1024, 4>(p, s);
 }
@@ -432,6 +531,7 @@ tp_status tp_residual_norm(const tp_residual_norm_args* a, tp_stream_t stream) {
   p.norm = a->norm;
   p.alpha = a->alpha;
   p.eps = a->eps;
+  p.prefetch = a->T <= sm_count();
   return dispatch_norm(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
