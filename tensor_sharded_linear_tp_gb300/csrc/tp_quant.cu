@@ -125,11 +125,11 @@ struct NormParams {
   const __nv_bfloat16 *gate, *scale, *shift;                     // [mod_rows, D], row stride ld_mod, nullable
   __nv_bfloat16 *h, *u;
   uint8_t *u8, *u_scales;
-  int64_t ldx, ldy, ldh, ldu, ld_us, ld_mod, rows_per_mod;
-  int64_t T;
-  int D;
+  int64_t ldx, ldy, ldh, ldu, ld_us, ld_mod;
+  uint32_t rows_per_mod;
+  int T, D;
   int post_norm, norm;
-  float alpha, eps;
+  float alpha, eps, inv_d;
   bool prefetch;  // few rows: fetch the vectors and tables ahead of their use
 };
 
@@ -203,39 +203,41 @@ __device__ __forceinline__ float max_abs(float m, float v) {
 // a row alternate between two parts of the scratch, so that one barrier each is enough: a part is
 // written again only after the barrier of the sum between, which every reader has passed.
 template <int kThreads>
-__device__ __forceinline__ float row_sum(float v, float (&scratch)[2][32], int part) {
+__device__ __forceinline__ float row_sum(float v, float4 (&scratch)[2][8], int part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (kThreads > 32) {
-    if ((threadIdx.x & 31) == 0) scratch[part][threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<float*>(scratch[part])[threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) v += scratch[part][w];
+    for (int w = 0; w < kThreads / 128; ++w) {
+      const float4 f = scratch[part][w];
+      v += (f.x + f.y) + (f.z + f.w);
+    }
   }
   return v;
 }
 
 // v <- norm(v) over one row of D elements; elements past D are not part of the sums.  `part`: the
 // scratch part of the first sum, moved on past the last.
-template <int kThreads, int kVecs>
-__device__ __forceinline__ void normalise(f2 (&v)[kVecs][4], int kind, int D, float eps, int lane,
-                                          float (&scratch)[2][32], int& part, const __nv_bfloat16* weight,
+template <int kThreads, int kVecs, bool kFull>
+__device__ __forceinline__ void normalise(f2 (&v)[kVecs][4], int kind, const NormParams& p, int lane,
+                                          float4 (&scratch)[2][8], int& part, const __nv_bfloat16* weight,
                                           const __nv_bfloat16* bias) {
   if (kind == TP_NORM_NONE) return;
-  const float inv_d = 1.0f / static_cast<float>(D);
   if (kind == TP_NORM_LAYER) {
     f2 s = 0;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)  // (a vector past D is zero here)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = add2(s, v[j][i]);
-    const float mean = row_sum<kThreads>(sum2(s), scratch, part) * inv_d;
+    const float mean = row_sum<kThreads>(sum2(s), scratch, part) * p.inv_d;
     part ^= 1;
     const f2 minus = pair(-mean, -mean);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
-      if ((j * kThreads + lane) * 8 < D)
+      if (kFull || (j * kThreads + lane) * 8 < p.D)
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], minus);
   }
@@ -244,13 +246,13 @@ __device__ __forceinline__ void normalise(f2 (&v)[kVecs][4], int kind, int D, fl
   for (int j = 0; j < kVecs; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) s = fma2(v[j][i], v[j][i], s);
-  const float r = 1.0f / sqrtf(row_sum<kThreads>(sum2(s), scratch, part) * inv_d + eps);
+  const float r = rsqrtf(row_sum<kThreads>(sum2(s), scratch, part) * p.inv_d + p.eps);  // within 2 ulp
   part ^= 1;
   const f2 rr = pair(r, r);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     const int col = (j * kThreads + lane) * 8;
-    if (col >= D) continue;
+    if (!kFull && col >= p.D) continue;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], rr);
     if (weight != nullptr) {  // uniform, as the other optional vectors
@@ -268,18 +270,20 @@ __device__ __forceinline__ void normalise(f2 (&v)[kVecs][4], int kind, int D, fl
   }
 }
 
-// kThreads threads hold a row (32: one warp, four rows a CTA), kVecs vectors of 8 elements each.
-template <int kThreads, int kVecs>
+// kThreads threads hold a row (32: one warp, four rows a CTA), kVecs vectors of 8 elements each;
+// kFull: every one of them, so that nothing is tested against D.
+template <int kThreads, int kVecs, bool kFull>
 __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 ? 1024 / kThreads : 8)
     residual_norm_kernel(const NormParams p) {
-  __shared__ float scratch[2][32];
+  __shared__ float4 scratch[2][8];
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kRows = kThreads > 32 ? 1 : 4;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (kRows > 1 ? threadIdx.x >> 5 : 0);
-  if (row >= p.T) return;  // warp-uniform; with one row a CTA the grid is exact
+  const int t = static_cast<int>(blockIdx.x) * kRows + (kRows > 1 ? static_cast<int>(threadIdx.x >> 5) : 0);
+  if (t >= p.T) return;  // warp-uniform; with one row a CTA the grid is exact
   const int lane = kRows > 1 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
-  const int64_t mod = p.rows_per_mod > 0 ? row / p.rows_per_mod * p.ld_mod : 0;
+  const int64_t row = t;
+  const int64_t mod = p.rows_per_mod > 0 ? static_cast<uint32_t>(t) / p.rows_per_mod * p.ld_mod : 0;
   // Both rows are asked for at once, and with few rows, where the launch is as long as its chain
   // of memory accesses, the vectors and tables as well.
   uint4 xs[kVecs], ys[kVecs];
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 
   for (int j = 0; j < kVecs; ++j) {
     const int col = (j * kThreads + lane) * 8;
     xs[j] = ys[j] = make_uint4(0, 0, 0, 0);
-    if (col < p.D) {
+    if (kFull || col < p.D) {
       if (p.y != nullptr) ys[j] = load_row8(p.y + row * p.ldy + col);
       xs[j] = load_row8(p.x + row * p.ldx + col);
     }
@@ -298,7 +302,7 @@ __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       const int col = (j * kThreads + lane) * 8;
-      if (col < p.D) {
+      if (kFull || col < p.D) {
 #pragma unroll
         for (int i = 0; i < 3; ++i)
           if (tables[i] != nullptr) prefetch_l2(tables[i] + mod + col);
@@ -313,12 +317,12 @@ __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) unpack8(ys[j], v[j]);
   if (p.y != nullptr)
-    normalise<kThreads, kVecs>(v, p.post_norm, p.D, p.eps, lane, scratch, part, p.post_weight, p.post_bias);
+    normalise<kThreads, kVecs, kFull>(v, p.post_norm, p, lane, scratch, part, p.post_weight, p.post_bias);
   const f2 alpha = pair(p.alpha, p.alpha);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     const int col = (j * kThreads + lane) * 8;
-    if (col >= p.D) continue;
+    if (!kFull && col >= p.D) continue;
     f2 x[4];
     unpack8(xs[j], x);
     if (p.gate != nullptr) {
@@ -337,11 +341,11 @@ __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 
     if (p.h != nullptr) store8(p.h + row * p.ldh + col, v[j]);
   }
   if (p.u == nullptr && p.u8 == nullptr) return;  // uniform over the grid
-  normalise<kThreads, kVecs>(v, p.norm, p.D, p.eps, lane, scratch, part, p.weight, p.bias);
+  normalise<kThreads, kVecs, kFull>(v, p.norm, p, lane, scratch, part, p.weight, p.bias);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     const int col = (j * kThreads + lane) * 8;
-    const bool on = col < p.D;
+    const bool on = kFull || col < p.D;
     if (on && p.scale != nullptr) {
       f2 s[4];
       load8(p.scale + mod + col, s);
@@ -382,9 +386,9 @@ __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 
 template <int kThreads, int kVecs>
 tp_status launch_norm(const NormParams& p, cudaStream_t stream) {
   constexpr int kRows = kThreads > 32 ? 1 : 4;
-  const int64_t blocks = (p.T + kRows - 1) / kRows;
-  if (blocks > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many rows (%lld)", (long long)p.T);
-  cudaError_t e = launch_pdl(residual_norm_kernel<kThreads, kVecs>, dim3(static_cast<unsigned>(blocks)),
+  auto kernel = p.D == kThreads * kVecs * 8 ? residual_norm_kernel<kThreads, kVecs, true>
+                                            : residual_norm_kernel<kThreads, kVecs, false>;
+  cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>((p.T + kRows - 1) / kRows)),
                              dim3(kThreads > 32 ? kThreads : 128), 0, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "residual norm launch");
   return TP_OK;
@@ -471,6 +475,7 @@ tp_status tp_residual_norm(const tp_residual_norm_args* a, tp_stream_t stream) {
   if (!(a->eps >= 0.0f) || std::isinf(a->eps)) return fail(TP_ERR_INVALID_ARG, "eps must be finite and not negative");
   if (a->D > TP_NORM_MAX_D)
     return fail(TP_ERR_UNSUPPORTED, "rows wider than %d are not supported, got %lld", TP_NORM_MAX_D, (long long)a->D);
+  if (a->T > 0x7FFFFFF0) return fail(TP_ERR_UNSUPPORTED, "too many rows (%lld)", (long long)a->T);
   NormParams p{};
   p.ldx = a->ldx == 0 ? a->D : a->ldx;
   p.ldy = a->ldy == 0 ? a->D : a->ldy;
@@ -500,7 +505,7 @@ tp_status tp_residual_norm(const tp_residual_norm_args* a, tp_stream_t stream) {
     if ((a->T - 1) / a->rows_per_mod >= a->mod_rows)
       return fail(TP_ERR_INVALID_ARG, "%lld rows, %lld to a modulation row, need more than %lld modulation rows",
                   (long long)a->T, (long long)a->rows_per_mod, (long long)a->mod_rows);
-    p.rows_per_mod = a->rows_per_mod;
+    p.rows_per_mod = static_cast<uint32_t>(a->rows_per_mod < a->T ? a->rows_per_mod : a->T);
   }
   const int64_t step = fp8 ? 16 : 8;
   if (a->D % step != 0 || p.ldu % step != 0)
@@ -525,8 +530,9 @@ tp_status tp_residual_norm(const tp_residual_norm_args* a, tp_stream_t stream) {
   p.u = fp8 ? nullptr : static_cast<__nv_bfloat16*>(a->u);
   p.u8 = fp8 ? static_cast<uint8_t*>(a->u) : nullptr;
   p.u_scales = static_cast<uint8_t*>(a->u_scales);
-  p.T = a->T;
+  p.T = static_cast<int>(a->T);
   p.D = static_cast<int>(a->D);
+  p.inv_d = 1.0f / static_cast<float>(p.D);
   p.post_norm = a->post_norm;
   p.norm = a->norm;
   p.alpha = a->alpha;
