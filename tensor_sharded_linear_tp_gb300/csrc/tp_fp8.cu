@@ -34,8 +34,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <cstdio>
-#include <cstdlib>
 #include <mutex>
 #include <type_traits>
 
@@ -73,9 +71,8 @@ struct Fp8Params {
   int k_groups;    // scale groups (128 features) per segment
   int n_tiles, t_tiles;
   int splits;      // tokens kernel: cluster CTAs that share a tile's K
-  int t_items, n_items;  // prompt kernel: work items (pairs of tiles along the dimension a cluster shares)
-  int group_m;           // prompt kernel: token items that sweep the weight items together
-  bool share_x;          // prompt kernel, clusters of two pairs: n-adjacent tiles share X (else m-adjacent, W)
+  int n_items;           // prompt kernel: n_tiles, or pairs of them (clusters of two CTA pairs)
+  int group_m;           // prompt kernel: token tiles that sweep the weight tiles together
   bool x_words, w_words;  // scale chunks can be read as aligned 32-bit words
   bool bias_vec;          // every bias is 16-byte aligned
   int act;
@@ -581,14 +578,14 @@ struct alignas(8) PromptCtrl {
 
 // A work item is a tile, or with clusters of two pairs two adjacent tiles.
 __device__ __forceinline__ void decode_item(const Fp8Params& p, int t, int& g, int& mt, int& nt) {
-  // group_m token items sweep the weight items together, so that CTAs that run at the same time
+  // group_m token tiles sweep the weight tiles together, so that CTAs that run at the same time
   // share both operands through L2.
-  const int per_out = p.t_items * p.n_items;
+  const int per_out = p.t_tiles * p.n_items;
   g = t / per_out;
   const int in_out = t - g * per_out;
   const int span = p.group_m * p.n_items;
   const int first = in_out / span * p.group_m;
-  const int m = min(p.group_m, p.t_items - first);
+  const int m = min(p.group_m, p.t_tiles - first);
   const int in_span = in_out % span;
   mt = first + in_span % m;
   nt = in_span / m;
@@ -690,9 +687,9 @@ __device__ __forceinline__ void store_group(const Fp8Params& p, int g, const flo
   }
 }
 
-// kQuad: clusters of two pairs on adjacent tiles that share an operand.  Each CTA loads half of its
-// rows of that operand and multicasts them to the CTA in its place in the other pair: a quarter
-// less is read from L2.  A stage is then free once both pairs' MMAs are done with it.
+// kQuad: clusters of two pairs on n-adjacent tiles, which share X.  Each CTA loads half of its
+// tokens and multicasts them to the CTA in its place in the other pair: a quarter less is read
+// from L2.  A stage is then free once both pairs' MMAs are done with it.
 template <bool kGlu, bool kQuad>
 __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __grid_constant__ Fp8Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -740,12 +737,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
   pdl_wait();
 
   const uint32_t sf_base = ptx::smem_addr(base) + kPromptStages * kPromptStage + 4 * kStagingWarp;
-  const int total = p.n_groups * p.t_items * p.n_items;
+  const int total = p.n_groups * p.t_tiles * p.n_items;
   // Work item t's output and this pair's tile.
   auto tile_of = [&](int t, int& g, int& mt, int& nt) {
     decode_item(p, t, g, mt, nt);
-    if (kQuad && p.share_x) nt = 2 * nt + static_cast<int>(pair);
-    if (kQuad && !p.share_x) mt = 2 * mt + static_cast<int>(pair);
+    if (kQuad) nt = 2 * nt + static_cast<int>(pair);
   };
 
   if (warp == 0) {
@@ -755,18 +751,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       uint32_t it = 0;  // copies issued
       const uint32_t full0_leader = ptx::mapa_shared(full0, leader);  // both CTAs' copies complete there
       const uint32_t ring = ptx::smem_addr(base);
-      const uint32_t half = kQuad ? pair * (kBoxA / 2) : 0;           // the part of a shared box this CTA loads
+      const uint32_t half = pair * (kBoxA / 2);                       // the part of a shared box this CTA loads
       const int half_row = static_cast<int>(pair) * (BM / 2);
       const uint16_t both = static_cast<uint16_t>(0x5u << cta);       // this CTA's place in both pairs
-      const bool share_x = kQuad && p.share_x, share_w = kQuad && !p.share_x;
       uint32_t stage = 0, phase = 1;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
         int g, mt, nt;
         tile_of(t, g, mt, nt);
-        const int x_row = mt * PM + static_cast<int>(cta) * BM + (share_x ? half_row : 0);
-        const int w_row = (kGlu ? (cta == 0 ? 0 : p.up_row) + nt * BM : nt * PN + static_cast<int>(cta) * BM) +
-                          (share_w ? half_row : 0);
+        const int x_row = mt * PM + static_cast<int>(cta) * BM + half_row;
+        const int w_row = kGlu ? (cta == 0 ? 0 : p.up_row) + nt * BM : nt * PN + static_cast<int>(cta) * BM;
         for (int seg = 0; seg < p.n_segs && ok; ++seg) {
           const CUtensorMap* mx = &p.map_x[p.n_segs > 1 ? seg : 0];
           const CUtensorMap* mw = &p.map_w[p.n_segs > 1 ? seg : g];
@@ -777,16 +771,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
               break;
             }
             const uint32_t full = full0_leader + 8 * stage;
-            const uint32_t sx = ring + stage * kPromptStage, sw = sx + kBoxA;
+            const uint32_t sx = ring + stage * kPromptStage;
             if (cta == 0) ptx::mbar_arrive_expect_tx(full0 + 8 * stage, 2 * kPromptStage);
-            if (share_x)
+            if constexpr (kQuad)
               ptx::tma_load_2d_pair_mc(sx + half, mx, full, kx, x_row, both);
             else
               ptx::tma_load_2d_pair(sx, mx, full, kx, x_row);
-            if (share_w)
-              ptx::tma_load_2d_pair_mc(sw + half, mw, full, kx, w_row, both);
-            else
-              ptx::tma_load_2d_pair(sw, mw, full, kx, w_row);
+            ptx::tma_load_2d_pair(sx + kBoxA, mw, full, kx, w_row);
             if (++stage == kPromptStages) stage = 0, phase ^= 1u;
           }
         }
@@ -1048,20 +1039,21 @@ tp_status launch_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   const int chunks = p.n_segs * ceil_div(p.k_groups, kChunk);
   p.n_tiles = ceil_div(p.n_out, BM);
   const int64_t tiles = static_cast<int64_t>(p.n_groups) * p.n_tiles * p.t_tiles;
+  // The split of K whose longest SM is shortest: waves x (a CTA's chunks + the fixed part of its
+  // life, about 4 us or three chunks).  Ties go to the smaller cluster.  Measured, down projection
+  // of one token (4 x 6144 x 4608, 36 chunks, 48 tiles): splits 1 / 2 / 3 / 4 / 5 / 6 / 8 take
+  // 29.9 / 22.0 / 21.2 / 20.6 / 20.7 / 26.3 / 24.7 us (from 6 on the clusters need a second wave).
   int best = 0;
   int64_t best_cost = 0;
-  const char* fs = getenv("TP_FP8_S");
   for (int s = 1; s <= kMaxSplits && s <= chunks; ++s) {
-    if (fs && atoi(fs) != s) continue;
     int n = 0;
     tp_status st = resident_clusters<TN, kGlu>(s, &n);
     if (st != TP_OK) return st;
     if (n < 1) continue;
-    const int64_t cost = ((tiles + n - 1) / n) * (ceil_div(chunks, s) + 1);
+    const int64_t cost = ((tiles + n - 1) / n) * (ceil_div(chunks, s) + 3);
     if (best == 0 || cost < best_cost) best = s, best_cost = cost;
   }
   if (best == 0) return fail(TP_ERR_UNSUPPORTED, "the kernel does not fit on this device");
-  if (getenv("TP_FP8_DBG")) fprintf(stderr, "TN %d glu %d: split %d tiles %d\n", TN, kGlu, best, (int)tiles);
   if (tiles * best > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many tiles (%lld)", (long long)tiles);
   p.splits = best;
   tp_status st = set_maps(c, p, TN, BM);
@@ -1123,7 +1115,7 @@ tp_status resident_prompt(int* n) {
 
 template <bool kGlu, bool kQuad>
 tp_status launch_prompt(Fp8Params& p, int clusters, cudaStream_t stream) {
-  const int64_t items = static_cast<int64_t>(p.n_groups) * p.t_items * p.n_items;
+  const int64_t items = static_cast<int64_t>(p.n_groups) * p.t_tiles * p.n_items;
   if (items > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many tiles (%lld)", (long long)items);
   if (items < clusters) clusters = static_cast<int>(items);
   constexpr unsigned kCtas = kQuad ? 4 : 2;
@@ -1146,14 +1138,13 @@ tp_status launch_prompt(Fp8Params& p, int clusters, cudaStream_t stream) {
   return TP_OK;
 }
 
-// Token items that sweep the weight items together: all of them while their operand fits L2
-// comfortably (each weight tile is then read from HBM once), else groups of about 16 tiles, evenly sized.
-int choose_group_m(int t_items, int tiles_per_item, int64_t x_bytes) {
-  if (x_bytes <= (64ll << 20)) return t_items;
-  const int groups = ceil_div(static_cast<int64_t>(t_items) * tiles_per_item, 16);
-  return ceil_div(t_items, groups);
+// Token tiles that sweep the weight tiles together: all of them while their operand fits L2
+// comfortably (each weight tile is then read from HBM once), else groups of about 16, evenly sized.
+int choose_group_m(int t_tiles, int64_t x_bytes) {
+  if (x_bytes <= (64ll << 20)) return t_tiles;
+  const int groups = ceil_div(t_tiles, 16);
+  return ceil_div(t_tiles, groups);
 }
-
 
 template <bool kGlu>
 tp_status run_prompt(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
@@ -1164,15 +1155,19 @@ tp_status run_prompt(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   if (st == TP_OK) st = resident_prompt<kGlu, true>(&quads);
   if (st != TP_OK) return st;
   if (pairs < 1) return fail(TP_ERR_UNSUPPORTED, "no CTA pair of the kernel fits on this device");
-  p.share_x = p.n_tiles % 2 == 0;
-  bool quad = quads > 0 && (p.n_tiles % 2 == 0 || p.t_tiles % 2 == 0);
-  const char* force = getenv("TP_FP8_FORCE");
-  if (force && force[1] == '2') quad = false;
-  if (force && force[1] == 'm' && p.t_tiles % 2 == 0) p.share_x = false;
-  p.n_items = quad && p.share_x ? p.n_tiles / 2 : p.n_tiles;
-  p.t_items = quad && !p.share_x ? p.t_tiles / 2 : p.t_tiles;
-  p.group_m = choose_group_m(p.t_items, p.t_tiles / p.t_items, c.T * c.K * p.n_segs);
-  st = set_maps(c, p, quad && p.share_x ? BM / 2 : BM, quad && !p.share_x ? BM / 2 : BM);
+  // Clusters of two pairs, on n-adjacent tiles that share X, where the tiles pair up and the
+  // clusters' waves, each about 4 % shorter, take no longer than the pairs' (fewer clusters of
+  // four CTAs than pairs fit: 36 x 4 against 76 x 2).  Measured at 4608 tokens: gate/up 659 us
+  // against 667 (36 waves, 35 of pairs), down 354 against 357 (6 waves either way).
+  const int64_t tiles = static_cast<int64_t>(p.n_groups) * p.n_tiles * p.t_tiles;
+  bool quad = quads > 0 && p.n_tiles % 2 == 0;
+  if (quad) {
+    const int64_t waves_quad = (tiles / 2 + quads - 1) / quads, waves_pair = (tiles + pairs - 1) / pairs;
+    quad = waves_quad * 24 <= waves_pair * 25;
+  }
+  p.n_items = quad ? p.n_tiles / 2 : p.n_tiles;
+  p.group_m = choose_group_m(p.t_tiles, c.T * c.K * p.n_segs);
+  st = set_maps(c, p, quad ? BM / 2 : BM, BM);
   if (st != TP_OK) return st;
   return quad ? launch_prompt<kGlu, true>(p, quads, stream) : launch_prompt<kGlu, false>(p, pairs, stream);
 }
@@ -1181,6 +1176,22 @@ template <int TN>
 tp_status run_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   p.t_tiles = ceil_div(c.T, TN);
   return p.act == TP_ACT_SWIGLU ? launch_tokens<TN, true>(c, p, stream) : launch_tokens<TN, false>(c, p, stream);
+}
+
+// Whether 256 x 256 tiles on CTA pairs beat 128 x 128 tiles on single CTAs, by what both took (ns):
+// a single CTA 4000 and 300 a scale group (SwiGLU 600), a launch of pairs 8000 and 380 a group.
+// Measured (us, single against pairs): Q/K/V of 128 / 256 / 384 tokens 26.8 / 40 / 57 against 29.7 /
+// 30.6 / 48; down of 384 / 512 tokens 40 / 66 against 61 / 61; 2 x 2048 x 1024 of 384 / 768 tokens
+// 9.6 / 18.3 against 9.0 / 9.5.
+bool prompt_is_faster(const Fp8Params& p, const Fp8Call& c) {
+  const bool glu = p.act == TP_ACT_SWIGLU;
+  const int64_t sms = sm_count(), groups = static_cast<int64_t>(p.n_segs) * p.k_groups;
+  if (sms < 2) return false;
+  const int64_t single = static_cast<int64_t>(p.n_groups) * ceil_div(c.n_out, BM) * ceil_div(c.T, 128);
+  const int64_t paired = static_cast<int64_t>(p.n_groups) * ceil_div(c.n_out, glu ? BM : PN) * ceil_div(c.T, PM);
+  const int64_t t_single = (single + sms - 1) / sms * (4000 + groups * (glu ? 600 : 300));
+  const int64_t t_paired = 8000 + (paired + sms / 2 - 1) / (sms / 2) * groups * 380;
+  return t_paired < t_single;
 }
 
 tp_status run_fp8(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
@@ -1204,8 +1215,7 @@ tp_status run_fp8(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
     }
     p.bias_vec = p.bias_vec && aligned16(p.bias[r]);
   }
-  const char* force = getenv("TP_FP8_FORCE");
-  if (force ? force[0] == 'p' : c.T > 128)
+  if (c.T > 64 && prompt_is_faster(p, c))
     return p.act == TP_ACT_SWIGLU ? run_prompt<true>(c, p, stream) : run_prompt<false>(c, p, stream);
   if (c.T <= 16) return run_tokens<16>(c, p, stream);
   if (c.T <= 32) return run_tokens<32>(c, p, stream);

@@ -192,10 +192,10 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const f2 (&v)[4]) {
   };
   *reinterpret_cast<uint4*>(p) = make_uint4(two(v[0]), two(v[1]), two(v[2]), two(v[3]));
 }
-// max(m, |v|), NaN if either is.
-__device__ __forceinline__ float max_abs(float m, float v) {
+// The larger magnitude of two values, NaN if either is, with a sign that means nothing.
+__device__ __forceinline__ float max_abs(float a, float b) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
@@ -362,14 +362,14 @@ __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 
       if (on) store8(p.u + row * p.ldu + col, v[j]);
     } else {
       // 16 lanes hold a group of 128.
-      float e[8], m = 0.0f;
+      float e[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) unpair(v[j][i], e[2 * i], e[2 * i + 1]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max_abs(m, e[i]);
+      float m = max_abs(max_abs(max_abs(e[0], e[1]), max_abs(e[2], e[3])),
+                        max_abs(max_abs(e[4], e[5]), max_abs(e[6], e[7])));
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const uint32_t byte = e8m0_of_amax(__float_as_uint(m));
+      const uint32_t byte = e8m0_of_amax(abs_bits(m));
       const float inv = e8m0_inverse(byte);
       if (on) {
         const f2 ii = pair(inv, inv);

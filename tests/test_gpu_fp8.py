@@ -227,26 +227,75 @@ def test_rowwise_exact_integers(T, K, N, p):
     np.testing.assert_array_equal(f64(z), bf16_round(sum(x[2] @ w[2].T for x, w in zip(xs, ws))))
 
 
-@pytest.mark.parametrize("T", [1, 70, 300])
-def test_one_scale_at_a_time(T):
+@pytest.mark.parametrize("T, N", [(1, 384), (70, 384), (300, 384), (1300, 2176)])
+def test_one_scale_at_a_time(T, N):
     """Every scale in turn is the only one that is not 1: each group of each operand has its own."""
     rng = np.random.default_rng(T)
-    K, N = 1152, 384
+    K = 1152
     x, sx, _ = integers(rng, T, K, 1)
     w, sw, _ = integers(rng, N, K, 128)
     for kg in range(9):
-        bx, bw = np.full((T, 9), 127, np.uint8), np.full((3, 9), 127, np.uint8)
+        bx, bw = np.full((T, 9), 127, np.uint8), np.full((N // 128, 9), 127, np.uint8)
         bx[T // 2, kg], bw[kg % 3, kg] = 130, 125
         y = tp.tp_linear_colwise_fp8(x, to_scales(bx), [w], [to_scales(bw)])[0]
         want = F.dequantize(codes(x), bx, 1) @ F.dequantize(codes(w), bw, 128).T
         np.testing.assert_array_equal(f64(y), bf16_round(want), err_msg=f"group {kg}")
 
 
-@pytest.mark.parametrize("T", [5, 300])
+# Prompts: sizes that take the 256 x 256 tiles of CTA pairs -- pairs alone (odd numbers of weight
+# tiles) and clusters of two pairs (even), one tile a pair and several (both accumulators), ragged
+# rows and columns, chunks of K that end early.
+PROMPTS = [(1300, 144, 2064, 1), (2600, 272, 2064, 1), (1300, 640, 2300, 1), (2600, 528, 1160, 2), (4500, 1040, 1032, 2)]
+
+
+@pytest.mark.parametrize("T, K, N, p", PROMPTS, ids=lambda v: str(v))
+def test_colwise_prompt_exact_integers(T, K, N, p):
+    rng = np.random.default_rng(T * 7 + K)
+    N -= N % 8
+    x, sx, xv = integers(rng, T, K, 1)
+    ws = [integers(rng, N, K, 128) for _ in range(p)]
+    y = tp.tp_linear_colwise_fp8(x, sx, [w[0] for w in ws], [w[1] for w in ws])
+    for r in range(p):
+        np.testing.assert_array_equal(f64(y[r]), bf16_round(xv @ ws[r][2].T), err_msg=f"rank {r}")
+
+
+@pytest.mark.parametrize("T, K, N, p", PROMPTS, ids=lambda v: str(v))
+def test_rowwise_prompt_exact_integers(T, K, N, p):
+    rng = np.random.default_rng(T * 11 + K)
+    N = p * N - p * N % 8
+    xs = [integers(rng, T, K, 1) for _ in range(p)]
+    ws = [integers(rng, N, K, 128) for _ in range(p)]
+    z = tp.tp_linear_rowwise_fp8([x[0] for x in xs], [x[1] for x in xs], [w[0] for w in ws], [w[1] for w in ws])
+    np.testing.assert_array_equal(f64(z), bf16_round(sum(x[2] @ w[2].T for x, w in zip(xs, ws))))
+
+
+@pytest.mark.parametrize("T, K, N", [(1300, 272, 2304), (2600, 144, 2320)], ids=lambda v: str(v))
+@pytest.mark.parametrize("out", ["bf16", "fp8"])
+@pytest.mark.parametrize("act", ["none", "gelu_tanh", "swiglu"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_colwise_prompt(T, K, N, out, act, bias):
+    rng = np.random.default_rng(T + K)
+    rows = 2 * N if act == "swiglu" else N     # 2320 rows on, the up block starts inside a scale block
+    x, sx, xv = quantized(rng, T, K, 1, 1.5)
+    w, sw, wv = quantized(rng, rows, K, 128, 1.5 / np.sqrt(K))
+    b = to_bf16(rng.normal(size=rows + 1))[1 if act == "none" else 0:][:rows] if bias else None   # also not 16-byte aligned
+    y = tp.tp_linear_colwise_fp8(x, sx, [w], [sw], act=act, bias_shards=[b] if bias else None, out=out)
+    pre, mag = F.linear_terms(xv, wv)
+    if bias:
+        pre, mag = pre + f64(b), mag + np.abs(f64(b))
+    err = accumulated(mag, K)
+    if act == "swiglu":
+        want, err = swiglu_bound(pre[:, :N], pre[:, N:], err[:, :N], err[:, N:])
+    else:
+        want, err = act_bound(pre, err, act)
+    check_bf16(y[0], want, err) if out == "bf16" else check_fp8(y[0][0], y[1][0], want, err)
+
+
+@pytest.mark.parametrize("T", [5, 300, 1300])
 def test_views_and_gathered_output(T):
     """Row strides of every tensor: a replicated input read slice by slice, one gathered output."""
     rng = np.random.default_rng(3)
-    K, N, p = 256, 136, 3
+    K, N, p = 256, 136 if T < 1000 else 1160, 3
     x, sx, xv = integers(rng, T, p * K + 128, 1)
     ws = [integers(rng, N, K, 128) for _ in range(p)]
     wt, st = [w[0] for w in ws], [w[1] for w in ws]
@@ -312,13 +361,13 @@ def test_rowwise(T, K, N, p, bias):
     check_bf16(z, want, accumulated(mag, p * (K + 31)))
 
 
-@pytest.mark.parametrize("T", [3, 300])
+@pytest.mark.parametrize("T, N", [(3, 272), (300, 272), (1300, 2064)])
 @pytest.mark.parametrize("out", ["bf16", "fp8"])
-def test_nan_stays_in_its_token(T, out):
+def test_nan_stays_in_its_token(T, N, out):
     """A token with a NaN group is NaN in every output it has; the other tokens are as without it."""
     rng = np.random.default_rng(1)
     x = to_bf16(rng.normal(size=(T, 384)))
-    w, sw, _ = quantized(rng, 264 if out == "bf16" else 272, 384, 128, 0.05)
+    w, sw, _ = quantized(rng, N - 8 if out == "bf16" else N, 384, 128, 0.05)
     clean = tp.tp_linear_colwise_fp8(*tp.tp_quantize_fp8(x), [w], [sw], out=out)
     x[1, 200] = float("nan")
     x[2, 3] = float("inf")
@@ -338,23 +387,23 @@ def test_zero_weights_and_padding_tokens():
     assert np.all(codes(y[0]) == 0) and np.all(codes(ys[0]) == 127)
 
 
-@pytest.mark.parametrize("T", [1, 48, 300])
-def test_extreme_scales(T):
+@pytest.mark.parametrize("T, N", [(1, 136), (48, 136), (300, 136), (1300, 2056)])
+def test_extreme_scales(T, N):
     """Scales at both ends of the format: 2^-127 on one operand against 2^120 on the other."""
     rng = np.random.default_rng(2)
     x = F.f64_to_e4m3(rng.integers(-4, 5, (T, 256)).astype(float))
-    w = F.f64_to_e4m3(rng.integers(-4, 5, (136, 256)).astype(float))
-    bx, bw = np.zeros((T, 2), np.uint8), np.full((2, 2), 247, np.uint8)
+    w = F.f64_to_e4m3(rng.integers(-4, 5, (N, 256)).astype(float))
+    bx, bw = np.zeros((T, 2), np.uint8), np.full((-(-N // 128), 2), 247, np.uint8)
     y = tp.tp_linear_colwise_fp8(to_codes(x), to_scales(bx), [to_codes(w)], [to_scales(bw)])[0]
     want = F.e4m3_to_f64(x) @ F.e4m3_to_f64(w).T * 2.0 ** -7
     np.testing.assert_array_equal(f64(y), bf16_round(want))
 
 
-@pytest.mark.parametrize("T", [1, 30, 300])
+@pytest.mark.parametrize("T", [1, 30, 300, 2600])
 def test_same_bits_every_time_and_on_another_stream(T):
     rng = np.random.default_rng(4)
     x, sx, _ = quantized(rng, T, 2064, 1)
-    ws = [quantized(rng, 544, 2064, 128, 0.03) for _ in range(2)]
+    ws = [quantized(rng, 1056, 2064, 128, 0.03) for _ in range(2)]
     wt, st = [w[0] for w in ws], [w[1] for w in ws]
     torch.cuda.synchronize()
     first = tp.tp_linear_colwise_fp8(x, sx, wt, st, act="swiglu", out="fp8")
@@ -514,7 +563,7 @@ def forward(x, gate, gu, dn, stream=None):
     return u, su, h, hs, z, x2, u2
 
 
-@pytest.mark.parametrize("T", [1, 19, 300])
+@pytest.mark.parametrize("T", [1, 19, 300, 3000])
 @pytest.mark.parametrize("p", [1, 2, 4])
 def test_block_of_all_operators(T, p):
     """Each step from the stored output of the step before, against the oracle."""
@@ -541,7 +590,7 @@ def test_block_of_all_operators(T, p):
     check_bf16(u2, uv, eu, "next input")
 
 
-@pytest.mark.parametrize("T", [1, 300])
+@pytest.mark.parametrize("T", [1, 300, 3000])
 def test_block_captured_and_replayed(T):
     """The block in a CUDA graph, replayed on new inputs, gives the eager calls' bits; two graphs at once too."""
     args = [sharded_block(T, 512, 1024, 2, seed) for seed in (1, 2)]
@@ -572,7 +621,7 @@ def test_block_captured_and_replayed(T):
 
 
 def test_calls_on_several_streams_at_once():
-    args = [sharded_block(T, 512, 1024, 2, T) for T in (1, 40, 200, 300)]
+    args = [sharded_block(T, 512, 1024, 2, T) for T in (1, 40, 200, 3000)]
     want = [forward(*a) for a in args]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in args]
