@@ -129,8 +129,9 @@ struct NormParams {
   uint32_t rows_per_mod;
   int T, D;
   int post_norm, norm;
+  int sms, ahead;  // ahead: a row asks for the one that many rows on
   float alpha, eps, inv_d;
-  bool prefetch;  // few rows: fetch the vectors and tables ahead of their use
+  bool few_rows;   // fewer than SMs
 };
 
 // Two fp32 values in one 64-bit register, for the paired instructions: the row's arithmetic, not
@@ -180,6 +181,10 @@ __device__ __forceinline__ uint4 load_row8(const __nv_bfloat16* p) {
                : "l"(p));
   return a;
 }
+// A whole row of n bytes (a multiple of 16) into L2.
+__device__ __forceinline__ void prefetch_row_l2(const __nv_bfloat16* p, uint32_t n) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(n) : "memory");
+}
 __device__ __forceinline__ void prefetch_l2(const __nv_bfloat16* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
@@ -199,41 +204,41 @@ __device__ __forceinline__ float max_abs(float a, float b) {
   return r;
 }
 
-// Sum over the threads that hold one row: a warp, or the CTA (a fixed order either way).  Sums of
-// a row alternate between two parts of the scratch, so that one barrier each is enough: a part is
+// Sum over the threads that hold one row: a warp, or the CTA (a fixed order either way).  Sums
+// alternate between two parts of the scratch, so that one barrier each is enough: a part is
 // written again only after the barrier of the sum between, which every reader has passed.
 template <int kThreads>
-__device__ __forceinline__ float row_sum(float v, float4 (&scratch)[2][8], int part) {
+__device__ __forceinline__ float row_sum(f2 v2, float (*scratch)[32], int& part) {
+  float v = sum2(v2);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (kThreads > 32) {
-    if ((threadIdx.x & 31) == 0) reinterpret_cast<float*>(scratch[part])[threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) scratch[part][threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 128; ++w) {
-      const float4 f = scratch[part][w];
+    for (int w = 0; w < kThreads / 32; w += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(&scratch[part][w]);
       v += (f.x + f.y) + (f.z + f.w);
     }
+    part ^= 1;
   }
   return v;
 }
 
-// v <- norm(v) over one row of D elements; elements past D are not part of the sums.  `part`: the
-// scratch part of the first sum, moved on past the last.
+// v <- norm(v) over one row of D elements; elements past D (zero) are not part of the sums.
 template <int kThreads, int kVecs, bool kFull>
 __device__ __forceinline__ void normalise(f2 (&v)[kVecs][4], int kind, const NormParams& p, int lane,
-                                          float4 (&scratch)[2][8], int& part, const __nv_bfloat16* weight,
+                                          float (*scratch)[32], int& part, const __nv_bfloat16* weight,
                                           const __nv_bfloat16* bias) {
   if (kind == TP_NORM_NONE) return;
   if (kind == TP_NORM_LAYER) {
     f2 s = 0;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)  // (a vector past D is zero here)
+    for (int j = 0; j < kVecs; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = add2(s, v[j][i]);
-    const float mean = row_sum<kThreads>(sum2(s), scratch, part) * p.inv_d;
-    part ^= 1;
+    const float mean = row_sum<kThreads>(s, scratch, part) * p.inv_d;
     const f2 minus = pair(-mean, -mean);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
@@ -246,23 +251,24 @@ __device__ __forceinline__ void normalise(f2 (&v)[kVecs][4], int kind, const Nor
   for (int j = 0; j < kVecs; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) s = fma2(v[j][i], v[j][i], s);
-  const float r = rsqrtf(row_sum<kThreads>(sum2(s), scratch, part) * p.inv_d + p.eps);  // within 2 ulp
-  part ^= 1;
+  const float r = rsqrtf(row_sum<kThreads>(s, scratch, part) * p.inv_d + p.eps);  // within 2 ulp
   const f2 rr = pair(r, r);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], rr);
+  if (weight == nullptr && bias == nullptr) return;  // uniform, as every optional vector
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     const int col = (j * kThreads + lane) * 8;
     if (!kFull && col >= p.D) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], rr);
-    if (weight != nullptr) {  // uniform, as the other optional vectors
-      f2 w[4];
+    f2 w[4];
+    if (weight != nullptr) {
       load8(weight + col, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], w[i]);
     }
     if (bias != nullptr) {
-      f2 w[4];
       load8(bias + col, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], w[i]);
@@ -271,20 +277,20 @@ __device__ __forceinline__ void normalise(f2 (&v)[kVecs][4], int kind, const Nor
 }
 
 // kThreads threads hold a row (32: one warp, four rows a CTA), kVecs vectors of 8 elements each;
-// kFull: every one of them, so that nothing is tested against D.
+// kFull: every vector is inside D, so that nothing is tested against it.
 template <int kThreads, int kVecs, bool kFull>
 __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 ? 1024 / kThreads : 8)
     residual_norm_kernel(const NormParams p) {
-  __shared__ float4 scratch[2][8];
+  __shared__ __align__(16) float scratch[2][32];
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kRows = kThreads > 32 ? 1 : 4;
   const int t = static_cast<int>(blockIdx.x) * kRows + (kRows > 1 ? static_cast<int>(threadIdx.x >> 5) : 0);
-  if (t >= p.T) return;  // warp-uniform; with one row a CTA the grid is exact
+  if (t >= p.T) return;  // uniform over a row's threads
   const int lane = kRows > 1 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int64_t row = t;
   const int64_t mod = p.rows_per_mod > 0 ? static_cast<uint32_t>(t) / p.rows_per_mod * p.ld_mod : 0;
-  // Both rows are asked for at once, and with few rows, where the launch is as long as its chain
+  // Both inputs are asked for at once, and with few rows, where the launch is as long as its chain
   // of memory accesses, the vectors and tables as well.
   uint4 xs[kVecs], ys[kVecs];
 #pragma unroll
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 
       xs[j] = load_row8(p.x + row * p.ldx + col);
     }
   }
-  if (p.prefetch) {
+  if (p.few_rows) {
     const __nv_bfloat16* const vectors[4] = {p.post_weight, p.post_bias, p.weight, p.bias};
     const __nv_bfloat16* const tables[3] = {p.gate, p.scale, p.shift};
 #pragma unroll
@@ -311,6 +317,11 @@ __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 
           if (vectors[i] != nullptr) prefetch_l2(vectors[i] + col);
       }
     }
+  } else if (lane == 0 && t < p.T - p.ahead) {
+    // A row's threads wait for it and then work on it with no other row in flight, so each asks for
+    // a row that is not far from its turn to be in L2 by then (42.7 -> 40.3 us at 4608 x 6144).
+    if (p.y != nullptr) prefetch_row_l2(p.y + (row + p.ahead) * p.ldy, 2 * static_cast<uint32_t>(p.D));
+    prefetch_row_l2(p.x + (row + p.ahead) * p.ldx, 2 * static_cast<uint32_t>(p.D));
   }
   f2 v[kVecs][4];  // zero past D
   int part = 0;
@@ -346,46 +357,47 @@ __global__ void __launch_bounds__(kThreads > 32 ? kThreads : 128, kThreads > 32 
   for (int j = 0; j < kVecs; ++j) {
     const int col = (j * kThreads + lane) * 8;
     const bool on = kFull || col < p.D;
+    f2 s[4];
     if (on && p.scale != nullptr) {
-      f2 s[4];
       load8(p.scale + mod + col, s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[j][i] = fma2(v[j][i], s[i], v[j][i]);
     }
     if (on && p.shift != nullptr) {
-      f2 s[4];
       load8(p.shift + mod + col, s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], s[i]);
     }
     if (p.u != nullptr) {
       if (on) store8(p.u + row * p.ldu + col, v[j]);
-    } else {
-      // 16 lanes hold a group of 128.
-      float e[8];
+      continue;
+    }
+    // 16 lanes hold a group of 128.
+    float e[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) unpair(v[j][i], e[2 * i], e[2 * i + 1]);
-      float m = max_abs(max_abs(max_abs(e[0], e[1]), max_abs(e[2], e[3])),
-                        max_abs(max_abs(e[4], e[5]), max_abs(e[6], e[7])));
+    for (int i = 0; i < 4; ++i) unpair(v[j][i], e[2 * i], e[2 * i + 1]);
+    float m = max_abs(max_abs(max_abs(e[0], e[1]), max_abs(e[2], e[3])),
+                      max_abs(max_abs(e[4], e[5]), max_abs(e[6], e[7])));
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const uint32_t byte = e8m0_of_amax(abs_bits(m));
-      const float inv = e8m0_inverse(byte);
-      if (on) {
-        const f2 ii = pair(inv, inv);
+    for (int o = 1; o < 16; o <<= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const uint32_t byte = e8m0_of_amax(abs_bits(m));
+    const float inv = e8m0_inverse(byte);
+    if (on) {
+      const f2 ii = pair(inv, inv);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) unpair(mul2(v[j][i], ii), e[2 * i], e[2 * i + 1]);
-        *reinterpret_cast<uint2*>(p.u8 + row * p.ldu + col) =
-            make_uint2(e4m3x4(e[0], e[1], e[2], e[3]), e4m3x4(e[4], e[5], e[6], e[7]));
-        if ((lane & 15) == 0) p.u_scales[row * p.ld_us + col / kFp8Group] = static_cast<uint8_t>(byte);
-      }
+      for (int i = 0; i < 4; ++i) unpair(mul2(v[j][i], ii), e[2 * i], e[2 * i + 1]);
+      *reinterpret_cast<uint2*>(p.u8 + row * p.ldu + col) =
+          make_uint2(e4m3x4(e[0], e[1], e[2], e[3]), e4m3x4(e[4], e[5], e[6], e[7]));
+      if ((lane & 15) == 0) p.u_scales[row * p.ld_us + col / kFp8Group] = static_cast<uint8_t>(byte);
     }
   }
 }
 
 template <int kThreads, int kVecs>
-tp_status launch_norm(const NormParams& p, cudaStream_t stream) {
+tp_status launch_norm(NormParams& p, cudaStream_t stream) {
   constexpr int kRows = kThreads > 32 ? 1 : 4;
+  // Half of the rows the GPU works on at a time (a quarter to one and a half times them: 44.7 to 46.5 us).
+  p.ahead = p.sms * (kThreads > 32 ? 1024 / kThreads : 8) * kRows / 2;
   auto kernel = p.D == kThreads * kVecs * 8 ? residual_norm_kernel<kThreads, kVecs, true>
                                             : residual_norm_kernel<kThreads, kVecs, false>;
   cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>((p.T + kRows - 1) / kRows)),
@@ -394,24 +406,23 @@ tp_status launch_norm(const NormParams& p, cudaStream_t stream) {
   return TP_OK;
 }
 
-// Rows up to 1024 wide take a warp, longer ones the smallest CTA whose threads hold four vectors or
-// fewer.  With fewer rows than SMs a launch is one row's latency, and a row gets more threads.
-tp_status dispatch_norm(const NormParams& p, cudaStream_t s) {
+// Threads and vectors for a row of D: rows up to 512 wide take a warp, longer ones a CTA whose
+// threads hold few vectors (4608 x 1024: 8.3 us with a warp of four vectors, 7.9 with four of
+// one; 4608 x 6144: 42.6 us with 192 threads of four, 40.3 with 256 of three, 43.2 with 384 of two,
+// 60 with 768 of one).  With fewer rows than SMs a launch is one row's latency, and a thread gets
+// one vector where that fits.
+tp_status dispatch_norm(NormParams& p, cudaStream_t s) {
   const int vecs = (p.D + 7) / 8;
-  if (p.prefetch) {
-    if (vecs <= 128) return launch_norm<128, 1>(p, s);
-    if (vecs <= 256) return launch_norm<256, 1>(p, s);
-    if (vecs <= 512) return launch_norm<512, 1>(p, s);
-    if (vecs <= 1024) return launch_norm<1024, 1>(p, s);
-  } else {
-    if (vecs <= 32) return launch_norm<32, 1>(p, s);
-    if (vecs <= 64) return launch_norm<32, 2>(p, s);
-    if (vecs <= 128) return launch_norm<32, 4>(p, s);
-    if (vecs <= 256) return launch_norm<256, 1>(p, s);
-    if (vecs <= 512) return launch_norm<256, 2>(p, s);
-    if (vecs <= 768) return launch_norm<256, 3>(p, s);
-    if (vecs <= 1024) return launch_norm<256, 4>(p, s);
-  }
+  if (!p.few_rows && vecs <= 32) return launch_norm<32, 1>(p, s);
+  if (!p.few_rows && vecs <= 64) return launch_norm<32, 2>(p, s);
+  if (vecs <= 128) return launch_norm<128, 1>(p, s);
+  if (vecs <= 256) return launch_norm<256, 1>(p, s);
+  if (p.few_rows && vecs <= 512) return launch_norm<512, 1>(p, s);
+  if (p.few_rows && vecs <= 1024) return launch_norm<1024, 1>(p, s);
+  if (vecs <= 512) return launch_norm<256, 2>(p, s);
+  if (vecs <= 768) return launch_norm<256, 3>(p, s);
+  if (vecs <= 1024) return launch_norm<256, 4>(p, s);
+  if (vecs <= 1536) return launch_norm<512, 3>(p, s);
   if (vecs <= 2048) return launch_norm<512, 4>(p, s);
   return launch_norm<1024, 4>(p, s);
 }
@@ -537,7 +548,9 @@ tp_status tp_residual_norm(const tp_residual_norm_args* a, tp_stream_t stream) {
   p.norm = a->norm;
   p.alpha = a->alpha;
   p.eps = a->eps;
-  p.prefetch = a->T <= sm_count();
+  p.sms = sm_count();
+  if (p.sms <= 0) return fail(TP_ERR_CUDA, "cannot query the SM count of the current device");
+  p.few_rows = a->T <= p.sms;
   return dispatch_norm(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
