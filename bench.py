@@ -995,6 +995,88 @@ class StackWorkload:
             return O.f64_to_bf16(z)
 
 
+class Fp8StackWorkload:
+    """The stack of eight SwiGLU MLP blocks with the norms that stand between them, on 8-bit shards.
+
+    Each block is x <- x + gate * rms(W_down . swiglu(W_gate_up . rms(x))): the shards are quantised
+    one by one (tp_quantize_fp8, 128 x 128 blocks) after their extraction, a block's input and hidden
+    state leave the norm and the gate/up projection as fp8 with their scales, and one residual norm
+    joins a block's output to the stream and norms it for the next.  Unlike the bare bf16 stack,
+    whose activations leave the bf16 range after a few blocks, it stays finite.
+    """
+
+    name = "stack8_fp8_tp4"
+    dtype = "fp8 (e4m3 codes, one e8m0 scale for each 128), fp32 accumulation, bf16 residual stream"
+
+    def __init__(self, tp, torch, device):
+        cfg = tp_inputs.WORKLOADS[WORKLOAD]
+        self.tp, self.torch, self.device = tp, torch, device
+        self.p, self.nb, self.T, self.H, self.F = cfg["tp"], cfg["blocks"], cfg["tokens"], cfg["hidden"], cfg["ffn"]
+        self.heads, seed = cfg["heads"], cfg["seed"]
+        p, H, F, T = self.p, self.H, self.F, self.T
+        self.shards = []
+        for b in range(self.nb):
+            with ThreadPoolExecutor(max_workers=2) as ex:
+                gu, dn = ex.map(lambda w: tp_inputs.stack_weight(seed, b, w, H, F), ("gate_up", "down"))
+            sh = [tp.tp_plan_shard_ranks(tp.bf16_from_bits(gu, device), "colwise", p, 0, p, [F, F], self.heads),
+                  tp.tp_plan_shard_ranks(tp.bf16_from_bits(dn, device), "rowwise", p, 0, p, None, self.heads)]
+            q = [[tp.tp_quantize_fp8(w, tp.FP8_GROUP) for w in ws] for ws in sh]
+            self.shards.append([[list(v) for v in zip(*ws)] for ws in q])     # [codes, scales] of gate/up, of down
+        x_bits = tp_inputs.stack_input(seed, self.nb, T, H)
+        self.x = tp.bf16_from_bits(x_bits, device)
+        gen = torch.Generator(device="cpu").manual_seed(seed)
+        self.gate = torch.randn(H, generator=gen).mul_(0.5).to(torch.bfloat16).to(device)
+        e = lambda *sh: torch.empty(sh, dtype=torch.bfloat16, device=device)  # noqa: E731
+        q = lambda *sh: torch.empty(sh, dtype=torch.uint8, device=device)  # noqa: E731
+        e4m3, e8m0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+        self.stream = [e(T, H), e(T, H)]
+        self.u, self.us = q(T, H).view(e4m3), q(T, H // 128).view(e8m0)
+        self.h = [q(T, F // p).view(e4m3) for _ in range(p)]
+        self.hs = [q(T, F // p // 128).view(e8m0) for _ in range(p)]
+        self.y = e(T, H)
+        self.z = self.stream[(self.nb - 1) % 2]
+        self.fl_gu, self.fl_dn = 2.0 * T * H * 2 * F, 2.0 * T * F * H
+        self.flops = self.nb * (self.fl_gu + self.fl_dn)
+        self.launches_per_step = 3 * self.nb + 1
+
+    def config(self):
+        return {"workload": self.name, "blocks": self.nb, "tokens": self.T, "hidden": self.H, "ffn": self.F,
+                "heads": self.heads, "tp_degree": self.p,
+                "step": "tp_residual_norm (fp8), then 8 x (tp_linear_colwise_fp8 SwiGLU to fp8 + tp_linear_rowwise_fp8 "
+                        "+ tp_residual_norm), shards resident in HBM",
+                "output_finite": bool(self.torch.isfinite(self.z.float()).all())}
+
+    def first_norm(self, stream):
+        self.tp.tp_residual_norm(self.x, norm="rms", out="fp8", u=self.u, u_scales=self.us, stream=stream)
+
+    def gate_up(self, b, stream):
+        w, s = self.shards[b][0]
+        self.tp.tp_linear_colwise_fp8(self.u, self.us, w, s, act="swiglu", out="fp8", y_shards=self.h,
+                                      y_scales=self.hs, stream=stream)
+
+    def down(self, b, stream):
+        w, s = self.shards[b][1]
+        self.tp.tp_linear_rowwise_fp8(self.h, self.hs, w, s, out=self.y, stream=stream)
+
+    def norm(self, b, stream):
+        """The block's output joins the residual stream; the last block has no next one to norm for."""
+        x = self.x if b == 0 else self.stream[(b - 1) % 2]
+        last = b == self.nb - 1
+        self.tp.tp_residual_norm(x, self.y, norm="rms", post_norm="rms", gate=self.gate, h=self.stream[b % 2],
+                                 out=None if last else "fp8", u=None if last else self.u,
+                                 u_scales=None if last else self.us, stream=stream)
+
+    def phases(self):
+        TH = self.T * self.H
+        out = [("norm_first", self.first_norm, "hbm", 3.0 * TH)]
+        for b in range(self.nb):
+            last = b == self.nb - 1
+            out += [("colwise_swiglu_fp8", lambda st, b=b: self.gate_up(b, st), "tensor", self.fl_gu),
+                    ("rowwise_down_fp8", lambda st, b=b: self.down(b, st), "tensor", self.fl_dn),
+                    ("norm_last" if last else "norm", lambda st, b=b: self.norm(b, st), "hbm", (6.0 if last else 7.0) * TH)]
+        return out
+
+
 # ----------------------------------------------------------------------------- CPU oracle timing
 
 def stack_cpu_baseline(wl, n_rows=512):
@@ -1065,6 +1147,8 @@ def make_workload(name, args, tp, torch, device):
         return BlockWorkload(tp, torch, device, args.tp)
     if name == "single_stream_tp4":
         return SingleStreamWorkload(tp, torch, device, args.tp)
+    if name == Fp8StackWorkload.name:
+        return Fp8StackWorkload(tp, torch, device)
     raise ValueError(name)
 
 
@@ -1247,6 +1331,11 @@ def roofline_of(res, workload, peaks, sustained):
     k = res["kernels"][label]
     if "TFLOP/s" in k:
         peak = peaks["bf16_tflops_sustained"] if sustained else peaks["bf16_tflops"]
+        if label.endswith("_fp8"):   # the tensor core's 8-bit rate is twice its bf16 rate
+            return {"bound": "tensor", "achieved": k["TFLOP/s"], "peak": 2 * peak, "unit": "TFLOP/s",
+                    "frac": k["TFLOP/s"] / (2 * peak), "kernel": f"fp8_prompt_kernel ({label})",
+                    "peak_source": "2 x " + peaks["source"] + (" sustained" if sustained else " burst"),
+                    "launch_ms": k["ms"], "traffic": None}
         return {"bound": "tensor", "achieved": k["TFLOP/s"], "peak": peak, "unit": "TFLOP/s",
                 "frac": k["TFLOP/s"] / peak, "frac_of_burst": k["TFLOP/s"] / peaks["bf16_tflops"],
                 "kernel": f"tp_gemm_kernel ({label})" if label != "attention" else "tp_flash_kernel",
@@ -1352,13 +1441,14 @@ def run_ours(args):
     wl = make_workload(args.workload, args, tp, torch, device)
     res = measure(wl, args, tp, torch, device, stream, peaks, flush=flush, sampler=ClockSampler(0))
     add_attention_issued(res, peaks)
-    cpu = None if args.no_cpu_baseline else generic_cpu_baseline(wl)
+    cpu = None if args.no_cpu_baseline or not hasattr(wl, "oracle_step") else generic_cpu_baseline(wl)
     cfg = wl.config()
     cfg.update({"parallelism": f"tp{wl.p} simulated on one GPU", "l2": "flushed between steps "
                 "(256 MiB write, then 256 MiB read)", "sms": torch.cuda.get_device_properties(device).multi_processor_count})
     line = {"metric": METRIC, "value": res["value"], "unit": UNIT, "n_gpus": 1, "steps": args.steps,
             "warmup": args.warmup, "ms_per_step": res["ms_per_step"], "higher_is_better": True, "scaling": "weak",
-            "vs_baseline": None, "dtype": "bf16", "data": "synthetic (seeded N(0,0.02) weights, N(0,1) activations)",
+            "vs_baseline": None, "dtype": getattr(wl, "dtype", "bf16"),
+            "data": "synthetic (seeded N(0,0.02) weights, N(0,1) activations)",
             "config": cfg, "roofline": roofline_of(res, args.workload, peaks, sustained=False),
             "cpu_baseline": cpu, "gpu_launches": wl.launches_per_step * args.steps, "peaks": peaks}
     line.update({k: v for k, v in res.items() if k not in ("value", "ms_per_step")})
@@ -1675,10 +1765,10 @@ def main(argv=None):
                          "of writing the gathered layout from the colwise GEMM")
     ap.add_argument("--workload", default=WORKLOAD,
                     choices=[WORKLOAD, ATTN_PROJ, "tiny_mlp_tp2", "swiglu_mlp_tp4", "block_sweep",
-                             "single_stream_tp4", "st_load_single_stream"],
+                             "single_stream_tp4", "st_load_single_stream", Fp8StackWorkload.name],
                     help="the 8-block stack loaded shard-on-read (default), the attention projections, the tiny "
-                         "or SwiGLU MLP block, the full block (with --tp), the single-stream block, or "
-                         "shard-on-read from a safetensors file")
+                         "or SwiGLU MLP block, the full block (with --tp), the single-stream block, "
+                         "shard-on-read from a safetensors file, or the 8-block stack with its norms on 8-bit shards")
     ap.add_argument("--tp", type=int, default=4, help="tp_degree of --workload block_sweep / single_stream_tp4")
     args = ap.parse_args(argv)
     args.warmup = max(3, args.warmup)   # at least three untimed warm-up steps, whatever was asked
