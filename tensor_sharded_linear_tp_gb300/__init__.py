@@ -512,7 +512,7 @@ def _need_ranks(name, ts, dtype, shape, dev, dense=False):
     else:
         return _pointers[len(at)](*at), 0
     steps = [_need(f"{name}[{i}]", t, dtype, shape, dev) for i, t in enumerate(ts)]
-    if any(s not in (0, shape[1]) for s in steps):
+    if any(s not in (0, shape[-1]) for s in steps):
         if dense:
             raise ValueError(f"every rank's {name} must be contiguous")
         if any(s != steps[0] for s in steps):
@@ -541,7 +541,7 @@ def _launch_stream(stream, dev) -> int:
 def _device_of(name, t) -> int:
     """The current device, which a 2-D tensor `t` has to be on."""
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
@@ -550,7 +550,7 @@ def _device_of(name, t) -> int:
 
 def _ranks(w_shards, *lists) -> int:
     p = len(w_shards)
-    if not 1 <= p <= MAX_DEGREE:
+    if p < 1 or p > MAX_DEGREE:
         raise ValueError(f"w_shards must have one entry for each of 1 to {MAX_DEGREE} ranks, got {p}")
     for ts in lists:
         if ts is not None and len(ts) != p:
@@ -603,10 +603,10 @@ def tp_linear_colwise_fp8(x: torch.Tensor, x_scales: torch.Tensor, w_shards: Seq
     ws, _ = _need_ranks("w_scales", w_scales, _E8M0, (_groups(N), kg), dev, dense=True)
     bias = None
     if bias_shards is not None:
-        for i, b in enumerate(bias_shards):
-            if b is not None:
-                _need(f"bias_shards[{i}]", b, _BF16, (N,), dev)
-        bias = _pointers[p](*[0 if b is None else b.data_ptr() for b in bias_shards])
+        given = [b for b in bias_shards if b is not None]
+        bias, _ = _need_ranks("bias_shards", given, _BF16, (N,), dev, dense=True)
+        if len(given) != p:
+            bias = _pointers[p](*[0 if b is None else b.data_ptr() for b in bias_shards])
     n = N // 2 if act == "swiglu" else N
     if y_shards is None:
         y_shards = _alloc(stream, dev, _E4M3 if fp8 else _BF16, (T, n), p)

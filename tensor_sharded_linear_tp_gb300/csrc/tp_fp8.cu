@@ -35,7 +35,6 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
-#include <type_traits>
 
 #include "tp_e4m3.cuh"
 #include "tp_internal.h"
@@ -129,6 +128,14 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+// Arrival on a barrier of the cluster without release semantics: what it announces is that tensor
+// memory has been read, and tcgen05.wait::ld has seen to that.  (A release at cluster scope first
+// waits for the thread's earlier memory operations: 1300 to 1700 cycles here, in which the tensor
+// core had no work between two tiles.)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Cluster barrier that orders no memory (what has been read is in registers).
@@ -561,7 +568,7 @@ constexpr int kPromptStages = 6;
 constexpr uint32_t kPromptStage = 2 * kBoxA;         // a CTA's 128 tokens and its 128 weight rows
 constexpr uint32_t kShared = 32;                     // columns the two accumulators share
 constexpr uint32_t kPromptSf = 2 * PN - kShared;     // scale words: two buffers of 16 columns (X 4, W 8)
-constexpr uint32_t kStagingWarp = 32 * 128;          // epilogue staging: 32 rows a warp, 128 codes or 64 bf16 each
+constexpr uint32_t kStagingWarp = 32 * 128;          // epilogue staging: 32 rows a warp, 128 codes or 32 bf16 each
 constexpr uint32_t kPromptSfBytes = 3 * kSfRows;     // one chunk's words: X, W rows 0..127, W rows 128..255
 constexpr int kPromptThreads = 320;                  // producer, MMA issuer, 4 epilogue and 4 scale warps
 constexpr size_t kPromptSmem = 1024 + kPromptStages * kPromptStage + 4 * kStagingWarp + kSfBufs * kPromptSfBytes;
@@ -591,99 +598,147 @@ __device__ __forceinline__ void decode_item(const Fp8Params& p, int t, int& g, i
   nt = in_span / m;
 }
 
-// One group of 128 output columns of this thread's row, from the accumulator's columns at `taddr`
-// (SwiGLU: gate there, up 128 columns on), rows and columns past the output included.  `early`
-// holds the accumulator's shared columns, already read: those of accumulator 0 are its last 32 (up
-// columns 96..127, or the upper group's), those of accumulator 1 its first 32.
-// kHeld: this group has them.
-template <bool kGlu, int kAcc, bool kHeld>
-__device__ __forceinline__ void output_group(const Fp8Params& p, const __nv_bfloat16* bias, uint32_t taddr, int col0,
-                                             float (&y)[128], const uint32_t (&early)[32]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int j = (i + (kAcc == 0 ? 6 : 0)) & 7;  // the shared columns' part first: it frees their registers
-    uint32_t v[16], u[16];
-    const bool held = i < 2 && kHeld;
-    if (!held || (kGlu && kAcc == 0)) ptx::tmem_ld_32x32b_x16(taddr + 16 * j, v);
-    if (kGlu && (!held || kAcc == 1)) ptx::tmem_ld_32x32b_x16(taddr + 128 + 16 * j, u);
-    ptx::tmem_ld_wait();
-    if (held)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) (kGlu && kAcc == 0 ? u : v)[e] = early[16 * (i & 1) + e];
-    const int col = col0 + 16 * j;
-    float a[16], b[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      a[e] = __uint_as_float(v[e]);
-      if constexpr (kGlu) b[e] = __uint_as_float(u[e]);
-    }
-    if (bias != nullptr) {  // uniform
-      add_bias(a, bias, col, p.n_out, p.bias_vec);
-      if constexpr (kGlu) add_bias(b, bias + p.up_row, col, p.n_out, p.bias_vec && p.up_row % 8 == 0);
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) y[16 * j + e] = kGlu ? silu_f(a[e]) * b[e] : a[e];
-  }
-  if (!kGlu && p.act == TP_ACT_GELU_TANH)
-#pragma unroll
-    for (int i = 0; i < 128; ++i) y[i] = gelu_tanh_f(y[i]);
+// Copy a warp's 32 staged rows of kPieces 16-byte pieces out, so that a store instruction writes
+// whole row segments.  `out` is row 0's first byte, `bytes` what the output has of a row.  A piece
+// lies at a place of its 128-byte line that the row turns, so that neither the threads that wrote a
+// row each nor these reads meet in a bank.
+template <int kPieces>
+__device__ __forceinline__ uint32_t staged(uint32_t staging, int row, int piece) {
+  const int line = row * kPieces / 8, in_line = row % (8 / kPieces) * kPieces;
+  return staging + static_cast<uint32_t>(line * 128 + ((in_line + (piece ^ (line & (kPieces - 1)))) << 4));
 }
-
-// Copy a warp's 32 staged rows of 128 bytes (swizzled 16-byte pieces) out, eight lanes to a row, so
-// that a store instruction writes whole row segments.  `out` is row 0's first byte.
+template <int kPieces>
 __device__ __forceinline__ void store_rows(uint8_t* out, int64_t row_bytes, uint32_t staging, int rows, int bytes,
                                            int lane) {
   __syncwarp();
-  const int c = lane & 7;
+  const int c = lane % kPieces;
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const int r = i + (lane >> 3);
+  for (int i = 0; i < 32; i += 32 / kPieces) {
+    const int r = i + lane / kPieces;
     uint32_t w[4];
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(staging + static_cast<uint32_t>(r * 128) + (static_cast<uint32_t>(c ^ (r & 7)) << 4)));
+                 : "r"(staged<kPieces>(staging, r, c)));
     if (r < rows && 16 * c < bytes)
       *reinterpret_cast<uint4*>(out + r * row_bytes + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncwarp();  // the buffer may be written again
 }
 
-// Store a warp's 32 rows x 128 columns of values, a row to a thread.
-__device__ __forceinline__ void store_group(const Fp8Params& p, int g, const float (&y)[128], uint32_t staging,
-                                            int row0, int col0, int lane) {
-  const int rows = p.T - row0, cols = p.n_out - col0;
-  const uint32_t row = staging + static_cast<uint32_t>(lane) * 128;
-  if (p.out_scales[g] != nullptr) {  // uniform
-    uint32_t m = 0;
+// One accumulator tile: this thread's row of it, in groups of 128 output columns (SwiGLU: one, from
+// 128 gate and 128 up columns; else two), each in four chunks of 32.  The accumulator's columns that
+// the other one shares come first (accumulator 0: its last 32, accumulator 1: its first): once they
+// are in registers, the next tile's MMAs may start.  A group that leaves as codes needs its largest
+// value before the first of them: its activated chunks wait in the accumulator's own columns (the
+// first one, whose columns may be gone, in registers).  The loops stay rolled: unrolled over 128
+// columns and both accumulators, the code was fetched from memory once per tile (SwiGLU, K 1024:
+// 11 us a tile).
+template <bool kGlu>
+__device__ __forceinline__ void epilogue_tile(const Fp8Params& p, int g, int acc, uint32_t taddr, int nt, int row0,
+                                              uint32_t staging, uint32_t tempty, int lane) {
+  uint32_t v[32], keep[32];
+  ptx::tmem_ld_32x32b_x32(taddr + (acc == 0 ? PN - kShared : 0), keep);
+  ptx::tmem_ld_wait();
+  ptx::tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive_cluster_relaxed(tempty);
+
+  const __nv_bfloat16* bias = p.bias[g];
+  const bool fp8 = p.out_scales[g] != nullptr;
+  const int rows = p.T - row0;
+#pragma unroll 1
+  for (int i = 0; i < (kGlu ? 1 : 2); ++i) {
+    const int half = kGlu ? 0 : (acc == 0 ? 1 - i : i);
+    const int col0 = kGlu ? nt * BM : nt * PN + 128 * half;
+    const uint32_t columns = taddr + 128 * half;
+    const uint32_t stash = columns + (kGlu && acc == 1 ? 128 : 0);  // not the shared columns
+    const int first = acc == 0 ? 3 : 0;
+    if (col0 >= p.n_out) continue;  // uniform
+    float largest = 0.0f;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      const int c = (first + k) & 3;
+      const int col = col0 + 32 * c;
+      float y[32];
+      ptx::tmem_ld_32x32b_x32(columns + 32 * c, v);
+      if constexpr (kGlu) {
+        uint32_t u[32];
+        ptx::tmem_ld_32x32b_x32(columns + 128 + 32 * c, u);
+        ptx::tmem_ld_wait();
+        if (k == 0) {  // one of the two is what was read before
+          if (acc == 0)
 #pragma unroll
-    for (int i = 0; i < 128; ++i)
-      if ((i & ~15) < cols) m = max(m, abs_bits(y[i]));  // n_out is a multiple of 16
-    const uint32_t byte = e8m0_of_amax(m);
-    const float inv = e8m0_inverse(byte);
+            for (int e = 0; e < 32; ++e) u[e] = keep[e];
+          else
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      uint32_t w[4];
+            for (int e = 0; e < 32; ++e) v[e] = keep[e];
+        }
+        float up[32];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = e4m3x4(y[16 * c + 4 * e] * inv, y[16 * c + 4 * e + 1] * inv, y[16 * c + 4 * e + 2] * inv,
-                      y[16 * c + 4 * e + 3] * inv);
-      ptx::st_shared_v4(row + (static_cast<uint32_t>(c ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
-    }
-    store_rows(static_cast<uint8_t*>(p.out[g]) + row0 * p.ldo + col0, p.ldo, staging, rows, cols, lane);
-    if (lane < rows)
-      p.out_scales[g][(row0 + lane) * p.ld_os + col0 / kFp8Group] = static_cast<uint8_t>(byte);
-  } else {
+        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(v[e]), up[e] = __uint_as_float(u[e]);
+        if (bias != nullptr) {  // uniform
+          add_bias(y, bias, col, p.n_out, p.bias_vec);
+          add_bias(up, bias + p.up_row, col, p.n_out, p.bias_vec && p.up_row % 8 == 0);
+        }
 #pragma unroll
-    for (int h = 0; h < 128; h += 64) {
+        for (int e = 0; e < 32; ++e) y[e] = silu_f(y[e]) * up[e];
+      } else {
+        ptx::tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int i = h + 8 * c;
-        ptx::st_shared_v4(row + (static_cast<uint32_t>(c ^ (lane & 7)) << 4), pack_bf16(y[i], y[i + 1]),
-                          pack_bf16(y[i + 2], y[i + 3]), pack_bf16(y[i + 4], y[i + 5]), pack_bf16(y[i + 6], y[i + 7]));
+        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(i == 0 && k == 0 ? keep[e] : v[e]);
+        if (bias != nullptr) add_bias(y, bias, col, p.n_out, p.bias_vec);
+        if (p.act == TP_ACT_GELU_TANH)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = gelu_tanh_f(y[e]);
       }
-      store_rows(static_cast<uint8_t*>(p.out[g]) + 2 * (row0 * p.ldo + col0 + h), 2 * p.ldo, staging, rows,
-                 2 * (cols - h), lane);
+      if (!fp8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          ptx::st_shared_v4(staged<4>(staging, lane, e), pack_bf16(y[8 * e], y[8 * e + 1]),
+                            pack_bf16(y[8 * e + 2], y[8 * e + 3]), pack_bf16(y[8 * e + 4], y[8 * e + 5]),
+                            pack_bf16(y[8 * e + 6], y[8 * e + 7]));
+        store_rows<4>(static_cast<uint8_t*>(p.out[g]) + 2 * (row0 * p.ldo + col), 2 * p.ldo, staging, rows,
+                      2 * (p.n_out - col), lane);
+        continue;
+      }
+#pragma unroll
+      for (int h = 0; h < 32; h += 16)
+        if (col + h < p.n_out)  // n_out is a multiple of 16
+#pragma unroll
+          for (int e = h; e < h + 16; ++e) largest = max_abs(largest, y[e]);
+      if (k == 0) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) keep[e] = __float_as_uint(y[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(y[e]);
+        ptx::tmem_st_32x32b_x32(stash + 32 * c, v);
+      }
     }
+    if (!fp8) continue;
+    ptx::tmem_st_wait();
+    const uint32_t byte = e8m0_of_amax(abs_bits(largest));
+    const float inv = e8m0_inverse(byte);
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      const int c = (first + k) & 3;
+      if (k > 0) {
+        ptx::tmem_ld_32x32b_x32(stash + 32 * c, v);
+        ptx::tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = keep[e];
+      }
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        w[e] = e4m3x4(__uint_as_float(v[4 * e]) * inv, __uint_as_float(v[4 * e + 1]) * inv,
+                      __uint_as_float(v[4 * e + 2]) * inv, __uint_as_float(v[4 * e + 3]) * inv);
+      ptx::st_shared_v4(staged<8>(staging, lane, 2 * c), w[0], w[1], w[2], w[3]);
+      ptx::st_shared_v4(staged<8>(staging, lane, 2 * c + 1), w[4], w[5], w[6], w[7]);
+    }
+    store_rows<8>(static_cast<uint8_t*>(p.out[g]) + row0 * p.ldo + col0, p.ldo, staging, rows, p.n_out - col0, lane);
+    if (lane < rows) p.out_scales[g][(row0 + lane) * p.ld_os + col0 / kFp8Group] = static_cast<uint8_t>(byte);
   }
 }
 
@@ -719,7 +774,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
     }
     ptx::mbar_init(ptx::smem_addr(&ctl->tfull[0]), 1);
     ptx::mbar_init(ptx::smem_addr(&ctl->tfull[1]), 1);
-    ptx::mbar_init(ptx::smem_addr(&ctl->tempty), 256);
+    ptx::mbar_init(ptx::smem_addr(&ctl->tempty), 8);  // four epilogue warps of each CTA
     ptx::mbar_init(ptx::smem_addr(&ctl->drain), 1);
     ctl->abort = 0;
     ptx::fence_mbar_init();
@@ -884,36 +939,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
         break;
       ptx::tc_fence_after();
       const int row0 = mt * PM + static_cast<int>(cta) * BM + q * 32;
-      const __nv_bfloat16* bias = p.bias[g];
-      auto drain = [&](auto acc_tag) {
-        constexpr int kAcc = decltype(acc_tag)::value;
-        const uint32_t taddr = tmem + quarter + kAcc * (PN - kShared);
-        // The shared columns first: the next tile's MMAs wait for them.
-        uint32_t early[32];
-        ptx::tmem_ld_32x32b_x32(tmem + quarter + PN - kShared, early);
-        ptx::tmem_ld_wait();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive_cluster(tempty);
-        float y[128];
-        if constexpr (kGlu) {
-          output_group<true, kAcc, true>(p, bias, taddr, nt * BM, y, early);
-          store_group(p, g, y, staging, row0, nt * BM, lane);
-        } else {
-          // The group with the shared columns first: the upper one of accumulator 0, the lower of 1.
-          constexpr int kFirst = kAcc == 0 ? 128 : 0;
-          const int first = nt * PN + kFirst, second = nt * PN + 128 - kFirst;
-          output_group<false, kAcc, true>(p, bias, taddr + kFirst, first, y, early);
-          if (first < p.n_out) store_group(p, g, y, staging, row0, first, lane);
-          if (second < p.n_out) {
-            output_group<false, kAcc, false>(p, bias, taddr + 128 - kFirst, second, y, early);
-            store_group(p, g, y, staging, row0, second, lane);
-          }
-        }
-      };
-      if ((tile & 1u) == 0)
-        drain(std::integral_constant<int, 0>{});
-      else
-        drain(std::integral_constant<int, 1>{});
+      const int acc = static_cast<int>(tile & 1u);
+      epilogue_tile<kGlu>(p, g, acc, tmem + quarter + static_cast<uint32_t>(acc) * (PN - kShared), nt, row0, staging,
+                          tempty, lane);
     }
   } else {
     // -------------------------------------------------------------- scale words
@@ -998,39 +1026,58 @@ tp_status set_maps(const Fp8Call& c, Fp8Params& p, int x_box, int w_box) {
   return TP_OK;
 }
 
-// Clusters of `splits` CTAs that can be resident at once (cached per device and kernel).
-template <int TN, bool kGlu>
-tp_status resident_clusters(int splits, int* n) {
-  static std::mutex mu;
-  static int cached[64][kMaxSplits + 1];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  std::lock_guard<std::mutex> lock(mu);
-  int& c = cached[dev & 63][splits];
-  if (c == 0) {
-    e = cudaFuncSetAttribute(fp8_tokens_kernel<TN, kGlu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(TokensCfg<TN, kGlu>::SMEM));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(splits) * 64, 1, 1);
-    cfg.blockDim = dim3(kTokensThreads, 1, 1);
-    cfg.dynamicSmemBytes = TokensCfg<TN, kGlu>::SMEM;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int k = 0;
-    if (cudaOccupancyMaxActiveClusters(&k, fp8_tokens_kernel<TN, kGlu>, &cfg) != cudaSuccess || k <= 0) {
-      cudaGetLastError();
-      k = -1;  // no such cluster on this device
-    }
-    c = k;
+// Clusters of `size` CTAs of a kernel that can be resident at once (0: no such cluster on this device).
+template <typename Kernel>
+int resident_clusters(Kernel kernel, int size, int threads, size_t smem) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(size) * 64, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) {
+    cudaGetLastError();
+    return 0;
   }
-  *n = c;
+  return n;
+}
+
+// What a kernel's first call on a device finds out, for the later ones.
+struct Residency {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+  int clusters[kMaxSplits + 1] = {0};  // by cluster size
+};
+tp_status current_device_index(int* dev) {
+  const cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (*dev < 0 || *dev >= 64) return fail(TP_ERR_UNSUPPORTED, "device index %d", *dev);
+  return TP_OK;
+}
+
+// The tokens kernel's resident clusters by size.
+template <int TN, bool kGlu>
+tp_status tokens_residency(const int** clusters) {
+  static Residency found[64];
+  int dev = 0;
+  tp_status st = current_device_index(&dev);
+  if (st != TP_OK) return st;
+  Residency& r = found[dev];
+  std::call_once(r.once, [&] {
+    r.err = cudaFuncSetAttribute(fp8_tokens_kernel<TN, kGlu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(TokensCfg<TN, kGlu>::SMEM));
+    for (int s = 1; s <= kMaxSplits && r.err == cudaSuccess; ++s)
+      r.clusters[s] =
+          resident_clusters(fp8_tokens_kernel<TN, kGlu>, s, kTokensThreads, TokensCfg<TN, kGlu>::SMEM);
+  });
+  if (r.err != cudaSuccess) return cuda_fail(r.err, "cudaFuncSetAttribute(max dynamic shared memory)");
+  *clusters = r.clusters;
   return TP_OK;
 }
 
@@ -1043,12 +1090,13 @@ tp_status launch_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   // life, about 4 us or three chunks).  Ties go to the smaller cluster.  Measured, down projection
   // of one token (4 x 6144 x 4608, 36 chunks, 48 tiles): splits 1 / 2 / 3 / 4 / 5 / 6 / 8 take
   // 29.9 / 22.0 / 21.2 / 20.6 / 20.7 / 26.3 / 24.7 us (from 6 on the clusters need a second wave).
+  const int* resident = nullptr;
+  tp_status st = tokens_residency<TN, kGlu>(&resident);
+  if (st != TP_OK) return st;
   int best = 0;
   int64_t best_cost = 0;
   for (int s = 1; s <= kMaxSplits && s <= chunks; ++s) {
-    int n = 0;
-    tp_status st = resident_clusters<TN, kGlu>(s, &n);
-    if (st != TP_OK) return st;
+    const int n = resident[s];
     if (n < 1) continue;
     const int64_t cost = ((tiles + n - 1) / n) * (ceil_div(chunks, s) + 3);
     if (best == 0 || cost < best_cost) best = s, best_cost = cost;
@@ -1056,7 +1104,7 @@ tp_status launch_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   if (best == 0) return fail(TP_ERR_UNSUPPORTED, "the kernel does not fit on this device");
   if (tiles * best > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many tiles (%lld)", (long long)tiles);
   p.splits = best;
-  tp_status st = set_maps(c, p, TN, BM);
+  st = set_maps(c, p, TN, BM);
   if (st != TP_OK) return st;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * best), 1, 1);
@@ -1077,39 +1125,22 @@ tp_status launch_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   return TP_OK;
 }
 
-// Clusters of the prompt kernel that can be resident at once (cached per device).
+// The prompt kernel's resident pairs, or clusters of two pairs.
 template <bool kGlu, bool kQuad>
 tp_status resident_prompt(int* n) {
-  static std::mutex mu;
-  static int cached[64];
+  static Residency found[64];
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  std::lock_guard<std::mutex> lock(mu);
-  int& c = cached[dev & 63];
-  if (c == 0) {
-    e = cudaFuncSetAttribute(fp8_prompt_kernel<kGlu, kQuad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kPromptSmem));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(256, 1, 1);
-    cfg.blockDim = dim3(kPromptThreads, 1, 1);
-    cfg.dynamicSmemBytes = kPromptSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kQuad ? 4 : 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int k = 0;
-    if (cudaOccupancyMaxActiveClusters(&k, fp8_prompt_kernel<kGlu, kQuad>, &cfg) != cudaSuccess || k <= 0) {
-      cudaGetLastError();
-      k = -1;  // no such cluster on this device
-    }
-    c = k;
-  }
-  *n = c;
+  tp_status st = current_device_index(&dev);
+  if (st != TP_OK) return st;
+  Residency& r = found[dev];
+  std::call_once(r.once, [&] {
+    r.err = cudaFuncSetAttribute(fp8_prompt_kernel<kGlu, kQuad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kPromptSmem));
+    if (r.err == cudaSuccess)
+      r.clusters[0] = resident_clusters(fp8_prompt_kernel<kGlu, kQuad>, kQuad ? 4 : 2, kPromptThreads, kPromptSmem);
+  });
+  if (r.err != cudaSuccess) return cuda_fail(r.err, "cudaFuncSetAttribute(max dynamic shared memory)");
+  *n = r.clusters[0];
   return TP_OK;
 }
 

@@ -197,13 +197,6 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const f2 (&v)[4]) {
   };
   *reinterpret_cast<uint4*>(p) = make_uint4(two(v[0]), two(v[1]), two(v[2]), two(v[3]));
 }
-// The larger magnitude of two values, NaN if either is, with a sign that means nothing.
-__device__ __forceinline__ float max_abs(float a, float b) {
-  float r;
-  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Sum over the threads that hold one row: a warp, or the CTA (a fixed order either way).  Sums
 // alternate between two parts of the scratch, so that one barrier each is enough: a part is
 // written again only after the barrier of the sum between, which every reader has passed.
