@@ -73,7 +73,6 @@ struct Fp8Params {
   int n_items;           // prompt kernel: n_tiles, or pairs of them (clusters of two CTA pairs)
   int group_m;           // prompt kernel: token tiles that sweep the weight tiles together
   bool x_words, w_words;  // scale chunks can be read as aligned 32-bit words
-  bool bias_vec;          // every bias is 16-byte aligned
   int act;
 };
 
@@ -224,29 +223,6 @@ __device__ __forceinline__ float gelu_tanh_f(float x) {
   return __fdividef(x, 1.0f + __expf(-2.0f * u));
 }
 __device__ __forceinline__ float silu_f(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
-
-// v[e] += bias[col + e] for columns inside the output (n_out is a multiple of 8).
-template <int kN>
-__device__ __forceinline__ void add_bias(float (&v)[kN], const __nv_bfloat16* bias, int col, int n_out, bool vec) {
-  static_assert(kN % 8 == 0, "read eight at a time");
-  if (vec) {
-#pragma unroll
-    for (int i = 0; i < kN; i += 8) {
-      uint4 b = make_uint4(0, 0, 0, 0);
-      if (col + i < n_out) b = __ldg(reinterpret_cast<const uint4*>(bias + col + i));
-      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[i + 2 * e] += __uint_as_float(w[e] << 16);
-        v[i + 2 * e + 1] += __uint_as_float(w[e] & 0xFFFF0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (col + i < n_out) v[i] += __bfloat162float(bias[col + i]);
-  }
-}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
@@ -571,7 +547,9 @@ constexpr uint32_t kPromptSf = 2 * PN - kShared;     // scale words: two buffers
 constexpr uint32_t kStagingWarp = 32 * 128;          // epilogue staging: 32 rows a warp, 128 codes or 32 bf16 each
 constexpr uint32_t kPromptSfBytes = 3 * kSfRows;     // one chunk's words: X, W rows 0..127, W rows 128..255
 constexpr int kPromptThreads = 320;                  // producer, MMA issuer, 4 epilogue and 4 scale warps
-constexpr size_t kPromptSmem = 1024 + kPromptStages * kPromptStage + 4 * kStagingWarp + kSfBufs * kPromptSfBytes;
+constexpr uint32_t kPromptBias = PN * 4;             // a tile's bias, in each epilogue warp's own copy
+constexpr size_t kPromptSmem =
+    1024 + kPromptStages * kPromptStage + 4 * kStagingWarp + kSfBufs * kPromptSfBytes + 4 * kPromptBias;
 static_assert(kPromptSf + 32 <= 512, "accumulators and scale words fill tensor memory");
 
 struct alignas(8) PromptCtrl {
@@ -625,6 +603,35 @@ __device__ __forceinline__ void store_rows(uint8_t* out, int64_t row_bytes, uint
   __syncwarp();  // the buffer may be written again
 }
 
+// A tile's bias as fp32 in a warp's own shared memory, eight columns to a lane (SwiGLU: gate, then
+// up); read before the tile's MMAs are done, so that its latency is not the epilogue's.
+template <bool kGlu>
+__device__ __forceinline__ void stage_bias(const Fp8Params& p, const __nv_bfloat16* bias, int nt, uint32_t bias_at,
+                                           int lane) {
+  const bool up = kGlu && lane >= 16;
+  const int col = kGlu ? nt * BM + (lane & 15) * 8 : nt * PN + lane * 8;
+  const __nv_bfloat16* from = bias + (up ? p.up_row : 0) + col;
+  float b[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) b[e] = col + e < p.n_out ? __bfloat162float(from[e]) : 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; e += 4)
+    ptx::st_shared_v4(bias_at + static_cast<uint32_t>(lane * 8 + e) * 4, __float_as_uint(b[e]), __float_as_uint(b[e + 1]),
+                      __float_as_uint(b[e + 2]), __float_as_uint(b[e + 3]));
+  __syncwarp();
+}
+__device__ __forceinline__ void add_bias(float (&v)[32], uint32_t at) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    float b[4];
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3])
+                 : "r"(at + 4 * e));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[e + i] += b[i];
+  }
+}
+
 // One accumulator tile: this thread's row of it, in groups of 128 output columns (SwiGLU: one, from
 // 128 gate and 128 up columns; else two), each in four chunks of 32.  The accumulator's columns that
 // the other one shares come first (accumulator 0: its last 32, accumulator 1: its first): once they
@@ -635,7 +642,7 @@ __device__ __forceinline__ void store_rows(uint8_t* out, int64_t row_bytes, uint
 // 11 us a tile).
 template <bool kGlu>
 __device__ __forceinline__ void epilogue_tile(const Fp8Params& p, int g, int acc, uint32_t taddr, int nt, int row0,
-                                              uint32_t staging, uint32_t tempty, int lane) {
+                                              uint32_t staging, uint32_t bias_at, uint32_t tempty, int lane) {
   uint32_t v[32], keep[32];
   ptx::tmem_ld_32x32b_x32(taddr + (acc == 0 ? PN - kShared : 0), keep);
   ptx::tmem_ld_wait();
@@ -643,8 +650,7 @@ __device__ __forceinline__ void epilogue_tile(const Fp8Params& p, int g, int acc
   __syncwarp();
   if (lane == 0) mbar_arrive_cluster_relaxed(tempty);
 
-  const __nv_bfloat16* bias = p.bias[g];
-  const bool fp8 = p.out_scales[g] != nullptr;
+  const bool biased = p.bias[g] != nullptr, fp8 = p.out_scales[g] != nullptr;
   const int rows = p.T - row0;
 #pragma unroll 1
   for (int i = 0; i < (kGlu ? 1 : 2); ++i) {
@@ -676,9 +682,9 @@ __device__ __forceinline__ void epilogue_tile(const Fp8Params& p, int g, int acc
         float up[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(v[e]), up[e] = __uint_as_float(u[e]);
-        if (bias != nullptr) {  // uniform
-          add_bias(y, bias, col, p.n_out, p.bias_vec);
-          add_bias(up, bias + p.up_row, col, p.n_out, p.bias_vec && p.up_row % 8 == 0);
+        if (biased) {  // uniform
+          add_bias(y, bias_at + 4 * (32 * c));
+          add_bias(up, bias_at + 4 * (128 + 32 * c));
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) y[e] = silu_f(y[e]) * up[e];
@@ -686,7 +692,7 @@ __device__ __forceinline__ void epilogue_tile(const Fp8Params& p, int g, int acc
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(i == 0 && k == 0 ? keep[e] : v[e]);
-        if (bias != nullptr) add_bias(y, bias, col, p.n_out, p.bias_vec);
+        if (biased) add_bias(y, bias_at + 4 * (128 * half + 32 * c));
         if (p.act == TP_ACT_GELU_TANH)
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = gelu_tanh_f(y[e]);
@@ -929,11 +935,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
     const uint32_t quarter = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t staging = ptx::smem_addr(base) + kPromptStages * kPromptStage +
                              static_cast<uint32_t>(warp - 2) * kStagingWarp;
+    const uint32_t bias_at = sf_base + kSfBufs * kPromptSfBytes + static_cast<uint32_t>(warp - 2) * kPromptBias;
     const uint32_t tempty = ptx::mapa_shared(ptx::smem_addr(&ctl->tempty), leader);
     uint32_t tile = 0;
     for (int t = unit; t < total; t += units, ++tile) {
       int g, mt, nt;
       tile_of(t, g, mt, nt);
+      if (p.bias[g] != nullptr) stage_bias<kGlu>(p, p.bias[g], nt, bias_at, lane);
       if (!__all_sync(0xffffffffu, wait_bounded<true>(ptx::smem_addr(&ctl->tfull[tile & 1u]), (tile >> 1) & 1u,
                                                       abort_flag, p.status)))
         break;
@@ -941,7 +949,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       const int row0 = mt * PM + static_cast<int>(cta) * BM + q * 32;
       const int acc = static_cast<int>(tile & 1u);
       epilogue_tile<kGlu>(p, g, acc, tmem + quarter + static_cast<uint32_t>(acc) * (PN - kShared), nt, row0, staging,
-                          tempty, lane);
+                          bias_at, tempty, lane);
     }
   } else {
     // -------------------------------------------------------------- scale words
@@ -1236,7 +1244,6 @@ tp_status run_fp8(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   p.k_groups = ceil_div(c.K, KB);
   auto word_rows = [](const void* q, int64_t ld) { return (reinterpret_cast<uintptr_t>(q) & 3u) == 0 && ld % 4 == 0; };
   p.x_words = p.w_words = p.k_groups % kChunk == 0;
-  p.bias_vec = true;
   for (int r = 0; r < c.p; ++r) {
     p.sw[r] = static_cast<const uint8_t*>(c.sw[r]);
     p.w_words = p.w_words && word_rows(p.sw[r], p.k_groups);
@@ -1244,7 +1251,6 @@ tp_status run_fp8(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
       p.sx[r] = static_cast<const uint8_t*>(c.sx[r]);
       p.x_words = p.x_words && word_rows(p.sx[r], c.ld_sx);
     }
-    p.bias_vec = p.bias_vec && aligned16(p.bias[r]);
   }
   if (c.T > 64 && prompt_is_faster(p, c))
     return p.act == TP_ACT_SWIGLU ? run_prompt<true>(c, p, stream) : run_prompt<false>(c, p, stream);
