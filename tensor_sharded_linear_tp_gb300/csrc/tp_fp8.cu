@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "tp_e4m3.cuh"
 #include "tp_internal.h"
@@ -479,55 +480,91 @@ __global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2
   ptx::cluster_sync();  // every CTA's partial tile is in its shared memory
 
   // ---------------------------------------------------------------- join, activation, store
-  // This CTA's share of the tile's tokens, a warp to a token, four columns to a lane.
+  // This CTA's share of the tile's tokens, a warp to a token, four columns to a lane.  A token's
+  // reads, sums and store take half a microsecond one after the other, so what can be is in flight
+  // together: the reads from all the CTAs that share K, or, with one, those of four tokens (gate/up
+  // of 256 tokens in this kernel 72 -> 64 us).
   if (!*abort_flag) {
     const int tokens = min(TN, p.T - t0);
     const int n0 = w_row0 + lane * 4;
     const bool on = n0 < p.n_out;  // n_out is a multiple of 8
-    const __nv_bfloat16* bias = p.bias[g];
+    const bool fp8 = p.out_scales[g] != nullptr;
+    float bias[C::W_TILES][4];
+#pragma unroll
+    for (int a = 0; a < C::W_TILES; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        bias[a][e] = p.bias[g] != nullptr && on ? __bfloat162float(p.bias[g][n0 + e + (a ? p.up_row : 0)]) : 0.0f;
     const uint32_t local = ptx::smem_addr(base) + static_cast<uint32_t>(lane) * 16;
-    for (int t = tokens * part / splits + warp; t < tokens * (part + 1) / splits; t += kTokensThreads / 32) {
-      float v[C::W_TILES][4];
+    const int t_begin = tokens * part / splits, t_end = tokens * (part + 1) / splits;
+    constexpr int kWarps = kTokensThreads / 32;
+    auto join = [&](auto several, int t) {
+      constexpr int U = decltype(several)::value;  // tokens t, t + kWarps, ...
+      float v[U][C::W_TILES][4];
+      auto at = [&](int j, int a, int s) {  // a token past the share: the first one's, not stored
+        const int tj = t + j * kWarps < t_end ? t + j * kWarps : t;
+        return ptx::mapa_shared(local + static_cast<uint32_t>(a * TN + tj) * (BM * 4), static_cast<uint32_t>(s));
+      };
 #pragma unroll
-      for (int a = 0; a < C::W_TILES; ++a) {
-        const uint32_t at = local + static_cast<uint32_t>(a * TN + t) * (BM * 4);
+      for (int j = 0; j < U; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[a][e] = 0.0f;
-        float4 f[kMaxSplits];  // all in flight together
+        for (int a = 0; a < C::W_TILES; ++a)
 #pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s)
-          if (s < splits) f[s] = ld_cluster_f4(ptx::mapa_shared(at, static_cast<uint32_t>(s)));
+          for (int e = 0; e < 4; ++e) v[j][a][e] = 0.0f;
+      auto add = [](float (&to)[4], const float4& f) { to[0] += f.x, to[1] += f.y, to[2] += f.z, to[3] += f.w; };
+      constexpr int kFrom = U == 1 ? kMaxSplits : 1;
+      float4 f[U][C::W_TILES][kFrom];
 #pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s)
-          if (s < splits) v[a][0] += f[s].x, v[a][1] += f[s].y, v[a][2] += f[s].z, v[a][3] += f[s].w;
-        if (bias != nullptr && on)
+      for (int j = 0; j < U; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[a][e] += __bfloat162float(bias[n0 + e + (a ? p.up_row : 0)]);
+        for (int a = 0; a < C::W_TILES; ++a)
+#pragma unroll
+          for (int s = 0; s < kFrom; ++s)
+            if (s < splits) f[j][a][s] = ld_cluster_f4(at(j, a, s));
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int a = 0; a < C::W_TILES; ++a)
+#pragma unroll
+          for (int s = 0; s < kFrom; ++s)
+            if (s < splits) add(v[j][a], f[j][a][s]);
+      float y[U][4];
+      uint32_t byte[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = v[j][0][e] + bias[0][e];
+          if constexpr (kGlu)
+            y[j][e] = silu_f(x) * (v[j][1][e] + bias[1][e]);
+          else
+            y[j][e] = p.act == TP_ACT_GELU_TANH ? gelu_tanh_f(x) : x;
+        }
+        if (fp8) {  // the tile's 128 columns are one group of the output
+          const float m = max_abs(max_abs(y[j][0], y[j][1]), max_abs(y[j][2], y[j][3]));
+          byte[j] = e8m0_of_amax(__reduce_max_sync(0xffffffffu, on ? abs_bits(m) : 0u));
+        }
       }
-      float y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (kGlu)
-          y[e] = silu_f(v[0][e]) * v[1][e];
-        else
-          y[e] = p.act == TP_ACT_GELU_TANH ? gelu_tanh_f(v[0][e]) : v[0][e];
+      for (int j = 0; j < U; ++j) {
+        if (t + j * kWarps >= t_end) break;
+        const int64_t row = static_cast<int64_t>(t0 + t + j * kWarps);
+        if (fp8) {
+          const float inv = e8m0_inverse(byte[j]);
+          if (on)
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out[g]) + row * p.ldo + n0) =
+                e4m3x4(y[j][0] * inv, y[j][1] * inv, y[j][2] * inv, y[j][3] * inv);
+          if (lane == 0) p.out_scales[g][row * p.ld_os + nt] = static_cast<uint8_t>(byte[j]);
+        } else if (on) {
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out[g]) + row * p.ldo + n0) =
+              make_uint2(pack_bf16(y[j][0], y[j][1]), pack_bf16(y[j][2], y[j][3]));
+        }
       }
-      const int64_t row = static_cast<int64_t>(t0 + t);
-      if (p.out_scales[g] != nullptr) {  // the tile's 128 columns are one group of the output
-        uint32_t m = 0;
-        if (on)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) m = max(m, abs_bits(y[e]));
-        const uint32_t byte = e8m0_of_amax(__reduce_max_sync(0xffffffffu, m));
-        const float inv = e8m0_inverse(byte);
-        if (on)
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out[g]) + row * p.ldo + n0) =
-              e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-        if (lane == 0) p.out_scales[g][row * p.ld_os + nt] = static_cast<uint8_t>(byte);
-      } else if (on) {
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out[g]) + row * p.ldo + n0) =
-            make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-      }
+    };
+    if (splits == 1 && tokens > kWarps) {
+      for (int t = t_begin + warp; t < t_end; t += 4 * kWarps) join(std::integral_constant<int, 4>{}, t);
+    } else {
+      for (int t = t_begin + warp; t < t_end; t += kWarps) join(std::integral_constant<int, 1>{}, t);
     }
   }
   cluster_sync_relaxed();  // no CTA's shared memory goes away while another reads it
@@ -1218,18 +1255,19 @@ tp_status run_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
 }
 
 // Whether 256 x 256 tiles on CTA pairs beat 128 x 128 tiles on single CTAs, by what both took (ns):
-// a single CTA 4000 and 300 a scale group (SwiGLU 600), a launch of pairs 8000 and 380 a group.
-// Measured (us, single against pairs): Q/K/V of 128 / 256 / 384 tokens 26.8 / 40 / 57 against 29.7 /
-// 30.6 / 48; down of 384 / 512 tokens 40 / 66 against 61 / 61; 2 x 2048 x 1024 of 384 / 768 tokens
-// 9.6 / 18.3 against 9.0 / 9.5.
+// a wave of single CTAs 6000 (SwiGLU 9000) and 230 (400) a scale group, a launch of pairs 6500 and
+// 380 a group and wave.  Measured (us, single against pairs): Q/K/V of 128 / 256 / 384 tokens 25.4 /
+// 37.6 / 52.5 against 29.4 / 30.3 / 45.1; down of 384 / 512 tokens 38 / 66 against 60 / 60; 2 x 2048 x
+// 1024 of 256 / 384 / 640 tokens 8.0 / 8.8 / 15.9 against 8.5 / 8.7 / 9.2; SwiGLU 4096 x 512 of 64 / 128
+// tokens 8.2 / 11.9 against 8.2 / 8.0.
 bool prompt_is_faster(const Fp8Params& p, const Fp8Call& c) {
   const bool glu = p.act == TP_ACT_SWIGLU;
   const int64_t sms = sm_count(), groups = static_cast<int64_t>(p.n_segs) * p.k_groups;
   if (sms < 2) return false;
   const int64_t single = static_cast<int64_t>(p.n_groups) * ceil_div(c.n_out, BM) * ceil_div(c.T, 128);
   const int64_t paired = static_cast<int64_t>(p.n_groups) * ceil_div(c.n_out, glu ? BM : PN) * ceil_div(c.T, PM);
-  const int64_t t_single = (single + sms - 1) / sms * (4000 + groups * (glu ? 600 : 300));
-  const int64_t t_paired = 8000 + (paired + sms / 2 - 1) / (sms / 2) * groups * 380;
+  const int64_t t_single = (single + sms - 1) / sms * (glu ? 9000 + groups * 400 : 6000 + groups * 230);
+  const int64_t t_paired = 6500 + (paired + sms / 2 - 1) / (sms / 2) * groups * 380;
   return t_paired < t_single;
 }
 
