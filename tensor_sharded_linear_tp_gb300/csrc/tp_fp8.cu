@@ -1336,49 +1336,51 @@ tp_status tp_linear_colwise_fp8(const void* x, int64_t ldx, const void* x_scales
                                 int64_t N_r, void* const* y_shards, int64_t ldy, void* const* y_scales, int64_t ld_ys,
                                 tp_stream_t stream) {
   using namespace tp;
-  clear_error();
-  tp_status st = check_sizes(tp_degree, T, K, N_r);
-  if (st != TP_OK) return st;
-  if (act != TP_ACT_NONE && act != TP_ACT_GELU_TANH && act != TP_ACT_SWIGLU)
-    return fail(TP_ERR_INVALID_ARG, "unknown activation %d", (int)act);
-  if (act == TP_ACT_SWIGLU && (N_r % 2) != 0)
-    return fail(TP_ERR_INVALID_ARG, "SwiGLU needs an even shard width ([gate_r; up_r]), got N_r=%lld", (long long)N_r);
-  const int64_t n_out = (act == TP_ACT_SWIGLU) ? N_r / 2 : N_r;
-  const int64_t k_groups = ceil_div(K, KB), out_groups = ceil_div(n_out, KB);
-  if (ldx == 0) ldx = K;
-  if (ld_xs == 0) ld_xs = k_groups;
-  if (ldy == 0) ldy = n_out;
-  if (ld_ys == 0) ld_ys = out_groups;
-  if (ldx < K || ld_xs < k_groups || ldy < n_out || ld_ys < out_groups)
-    return fail(TP_ERR_INVALID_ARG, "a row stride (ldx %lld, ld_xs %lld, ldy %lld, ld_ys %lld) is smaller than its row",
-                (long long)ldx, (long long)ld_xs, (long long)ldy, (long long)ld_ys);
-  if (T == 0 || N_r == 0) return TP_OK;
-  if (K == 0) return fail(TP_ERR_INVALID_ARG, "K (in_features) must be positive");
-  const void* xs[1] = {x};
-  const void* sxs[1] = {x_scales};
-  Fp8Call c{xs, sxs, true, ldx, ld_xs, w_shards, w_scales, tp_degree, T, K, N_r, n_out};
-  st = check_fp8(c);
-  if (st != TP_OK) return st;
-  if (y_shards == nullptr) return fail(TP_ERR_INVALID_ARG, "y_shards is NULL");
-  const int64_t step = y_scales != nullptr ? 16 : 8;
-  if (n_out % step != 0 || ldy % step != 0)
-    return fail(TP_ERR_ALIGNMENT, "output width (%lld) and ldy (%lld) must be multiples of %lld", (long long)n_out,
-                (long long)ldy, (long long)step);
-  Fp8Params p{};
-  for (int r = 0; r < tp_degree; ++r) {
-    if (y_shards[r] == nullptr || (y_scales != nullptr && y_scales[r] == nullptr))
-      return fail(TP_ERR_INVALID_ARG, "y_shards[%d] or y_scales[%d] is NULL", r, r);
-    if (!aligned16(y_shards[r])) return fail(TP_ERR_ALIGNMENT, "y_shards[%d] is not 16-byte aligned", r);
-    p.out[r] = y_shards[r];
-    p.out_scales[r] = y_scales != nullptr ? static_cast<uint8_t*>(y_scales[r]) : nullptr;
-    p.bias[r] = bias_shards != nullptr ? static_cast<const __nv_bfloat16*>(bias_shards[r]) : nullptr;
-  }
-  p.act = act;
-  p.n_groups = tp_degree;
-  p.n_segs = 1;
-  p.ldo = ldy;
-  p.ld_os = ld_ys;
-  return run_fp8(c, p, reinterpret_cast<cudaStream_t>(stream));
+  return guarded([&]() -> tp_status {
+    clear_error();
+    tp_status st = check_sizes(tp_degree, T, K, N_r);
+    if (st != TP_OK) return st;
+    if (act != TP_ACT_NONE && act != TP_ACT_GELU_TANH && act != TP_ACT_SWIGLU)
+      return fail(TP_ERR_INVALID_ARG, "unknown activation %d", (int)act);
+    if (act == TP_ACT_SWIGLU && (N_r % 2) != 0)
+      return fail(TP_ERR_INVALID_ARG, "SwiGLU needs an even shard width ([gate_r; up_r]), got N_r=%lld", (long long)N_r);
+    const int64_t n_out = (act == TP_ACT_SWIGLU) ? N_r / 2 : N_r;
+    const int64_t k_groups = ceil_div(K, KB), out_groups = ceil_div(n_out, KB);
+    if (ldx == 0) ldx = K;
+    if (ld_xs == 0) ld_xs = k_groups;
+    if (ldy == 0) ldy = n_out;
+    if (ld_ys == 0) ld_ys = out_groups;
+    if (ldx < K || ld_xs < k_groups || ldy < n_out || ld_ys < out_groups)
+      return fail(TP_ERR_INVALID_ARG, "a row stride (ldx %lld, ld_xs %lld, ldy %lld, ld_ys %lld) is smaller than its row",
+                  (long long)ldx, (long long)ld_xs, (long long)ldy, (long long)ld_ys);
+    if (T == 0 || N_r == 0) return TP_OK;
+    if (K == 0) return fail(TP_ERR_INVALID_ARG, "K (in_features) must be positive");
+    const void* xs[1] = {x};
+    const void* sxs[1] = {x_scales};
+    Fp8Call c{xs, sxs, true, ldx, ld_xs, w_shards, w_scales, tp_degree, T, K, N_r, n_out};
+    st = check_fp8(c);
+    if (st != TP_OK) return st;
+    if (y_shards == nullptr) return fail(TP_ERR_INVALID_ARG, "y_shards is NULL");
+    const int64_t step = y_scales != nullptr ? 16 : 8;
+    if (n_out % step != 0 || ldy % step != 0)
+      return fail(TP_ERR_ALIGNMENT, "output width (%lld) and ldy (%lld) must be multiples of %lld", (long long)n_out,
+                  (long long)ldy, (long long)step);
+    Fp8Params p{};
+    for (int r = 0; r < tp_degree; ++r) {
+      if (y_shards[r] == nullptr || (y_scales != nullptr && y_scales[r] == nullptr))
+        return fail(TP_ERR_INVALID_ARG, "y_shards[%d] or y_scales[%d] is NULL", r, r);
+      if (!aligned16(y_shards[r])) return fail(TP_ERR_ALIGNMENT, "y_shards[%d] is not 16-byte aligned", r);
+      p.out[r] = y_shards[r];
+      p.out_scales[r] = y_scales != nullptr ? static_cast<uint8_t*>(y_scales[r]) : nullptr;
+      p.bias[r] = bias_shards != nullptr ? static_cast<const __nv_bfloat16*>(bias_shards[r]) : nullptr;
+    }
+    p.act = act;
+    p.n_groups = tp_degree;
+    p.n_segs = 1;
+    p.ldo = ldy;
+    p.ld_os = ld_ys;
+    return run_fp8(c, p, reinterpret_cast<cudaStream_t>(stream));
+  });
 }
 
 tp_status tp_linear_rowwise_fp8(const void* const* x_shards, int64_t ldx, const void* const* x_scales, int64_t ld_xs,
@@ -1386,35 +1388,37 @@ tp_status tp_linear_rowwise_fp8(const void* const* x_shards, int64_t ldx, const 
                                 int tp_degree, int64_t T, int64_t K_r, int64_t N, void* out, int64_t ldo,
                                 tp_stream_t stream) {
   using namespace tp;
-  clear_error();
-  tp_status st = check_sizes(tp_degree, T, K_r, N);
-  if (st != TP_OK) return st;
-  const int64_t k_groups = ceil_div(K_r, KB);
-  if (ldx == 0) ldx = K_r;
-  if (ld_xs == 0) ld_xs = k_groups;
-  if (ldo == 0) ldo = N;
-  if (ldx < K_r || ld_xs < k_groups || ldo < N)
-    return fail(TP_ERR_INVALID_ARG, "a row stride (ldx %lld, ld_xs %lld, ldo %lld) is smaller than its row",
-                (long long)ldx, (long long)ld_xs, (long long)ldo);
-  if (T == 0 || N == 0) return TP_OK;
-  if (K_r == 0) return fail(TP_ERR_INVALID_ARG, "K_r (in_features per rank) must be positive");
-  if (static_cast<int64_t>(tp_degree) * k_groups > 0x7FFFFFFF)
-    return fail(TP_ERR_UNSUPPORTED, "too many K groups (%d ranks of %lld)", tp_degree, (long long)k_groups);
-  Fp8Call c{x_shards, x_scales, false, ldx, ld_xs, w_shards, w_scales, tp_degree, T, K_r, N, N};
-  st = check_fp8(c);
-  if (st != TP_OK) return st;
-  if (out == nullptr) return fail(TP_ERR_INVALID_ARG, "out is NULL");
-  if (N % 8 != 0 || ldo % 8 != 0)
-    return fail(TP_ERR_ALIGNMENT, "N (%lld) and ldo (%lld) must be multiples of 8", (long long)N, (long long)ldo);
-  if (!aligned16(out)) return fail(TP_ERR_ALIGNMENT, "out is not 16-byte aligned");
-  Fp8Params p{};
-  p.out[0] = out;
-  p.bias[0] = static_cast<const __nv_bfloat16*>(bias);
-  p.act = TP_ACT_NONE;
-  p.n_groups = 1;
-  p.n_segs = tp_degree;
-  p.ldo = ldo;
-  return run_fp8(c, p, reinterpret_cast<cudaStream_t>(stream));
+  return guarded([&]() -> tp_status {
+    clear_error();
+    tp_status st = check_sizes(tp_degree, T, K_r, N);
+    if (st != TP_OK) return st;
+    const int64_t k_groups = ceil_div(K_r, KB);
+    if (ldx == 0) ldx = K_r;
+    if (ld_xs == 0) ld_xs = k_groups;
+    if (ldo == 0) ldo = N;
+    if (ldx < K_r || ld_xs < k_groups || ldo < N)
+      return fail(TP_ERR_INVALID_ARG, "a row stride (ldx %lld, ld_xs %lld, ldo %lld) is smaller than its row",
+                  (long long)ldx, (long long)ld_xs, (long long)ldo);
+    if (T == 0 || N == 0) return TP_OK;
+    if (K_r == 0) return fail(TP_ERR_INVALID_ARG, "K_r (in_features per rank) must be positive");
+    if (static_cast<int64_t>(tp_degree) * k_groups > 0x7FFFFFFF)
+      return fail(TP_ERR_UNSUPPORTED, "too many K groups (%d ranks of %lld)", tp_degree, (long long)k_groups);
+    Fp8Call c{x_shards, x_scales, false, ldx, ld_xs, w_shards, w_scales, tp_degree, T, K_r, N, N};
+    st = check_fp8(c);
+    if (st != TP_OK) return st;
+    if (out == nullptr) return fail(TP_ERR_INVALID_ARG, "out is NULL");
+    if (N % 8 != 0 || ldo % 8 != 0)
+      return fail(TP_ERR_ALIGNMENT, "N (%lld) and ldo (%lld) must be multiples of 8", (long long)N, (long long)ldo);
+    if (!aligned16(out)) return fail(TP_ERR_ALIGNMENT, "out is not 16-byte aligned");
+    Fp8Params p{};
+    p.out[0] = out;
+    p.bias[0] = static_cast<const __nv_bfloat16*>(bias);
+    p.act = TP_ACT_NONE;
+    p.n_groups = 1;
+    p.n_segs = tp_degree;
+    p.ldo = ldo;
+    return run_fp8(c, p, reinterpret_cast<cudaStream_t>(stream));
+  });
 }
 
 }  // extern "C"

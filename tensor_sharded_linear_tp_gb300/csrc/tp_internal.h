@@ -20,6 +20,16 @@ void clear_error();
 // Convert a CUDA error into TP_ERR_CUDA with a message naming `what`.
 tp_status cuda_fail(cudaError_t err, const char* what);
 
+// The body of a C entry point: no C++ exception (of an allocation on the host, say) leaves it.
+template <typename Body>
+tp_status guarded(Body&& body) {
+  try {
+    return body();
+  } catch (...) {
+    return TP_ERR_CUDA;
+  }
+}
+
 // Number of SMs of the current device (cached per device).
 int sm_count();
 

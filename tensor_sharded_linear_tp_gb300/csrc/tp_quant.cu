@@ -428,123 +428,127 @@ extern "C" {
 tp_status tp_quantize_fp8(const void* x, int64_t ldx, int64_t rows, int64_t cols, int block_rows, void* q, int64_t ldq,
                           void* scales, int64_t lds, tp_stream_t stream) {
   using namespace tp;
-  clear_error();
-  if (rows < 0 || cols < 0) return fail(TP_ERR_INVALID_ARG, "negative size");
-  if (block_rows != 1 && block_rows != kFp8Group)
-    return fail(TP_ERR_INVALID_ARG, "block_rows must be 1 or %d, got %d", kFp8Group, block_rows);
-  if (cols > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "sizes above 2^31-1 are not supported");
-  const int64_t col_groups = (cols + kFp8Group - 1) / kFp8Group;
-  if (ldx == 0) ldx = cols;
-  if (ldq == 0) ldq = cols;
-  if (lds == 0) lds = col_groups;
-  if (ldx < cols || ldq < cols || lds < col_groups)
-    return fail(TP_ERR_INVALID_ARG, "a row stride (ldx %lld, ldq %lld, lds %lld) is smaller than its row",
-                (long long)ldx, (long long)ldq, (long long)lds);
-  if (rows == 0 || cols == 0) return TP_OK;
-  if (x == nullptr || q == nullptr || scales == nullptr)
-    return fail(TP_ERR_INVALID_ARG, "x, q or scales is NULL");
-  if (cols % 16 != 0 || ldx % 8 != 0 || ldq % 16 != 0)
-    return fail(TP_ERR_ALIGNMENT, "cols (%lld) and ldq (%lld) must be multiples of 16, ldx (%lld) of 8",
-                (long long)cols, (long long)ldq, (long long)ldx);
-  if (!aligned16(x) || !aligned16(q)) return fail(TP_ERR_ALIGNMENT, "x or q is not 16-byte aligned");
-  const int64_t row_groups = (rows + block_rows - 1) / block_rows;
-  const int64_t per_cta = block_rows == 1 ? kQuantThreads / 8 : 1;
-  if (row_groups > 0x7FFFFFFFll * per_cta / col_groups) return fail(TP_ERR_UNSUPPORTED, "too many groups");
-  const int64_t blocks = (row_groups * col_groups + per_cta - 1) / per_cta;
-  QuantParams p{};
-  p.x = static_cast<const uint8_t*>(x);
-  p.q = static_cast<uint8_t*>(q);
-  p.scales = static_cast<uint8_t*>(scales);
-  p.ldx = ldx * 2;
-  p.ldq = ldq;
-  p.lds = lds;
-  p.rows = rows;
-  p.cols = static_cast<int>(cols);
-  p.col_groups = static_cast<int>(col_groups);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(block_rows == 1 ? quantize_rows_kernel : quantize_blocks_kernel,
-                             dim3(static_cast<unsigned>(blocks)), dim3(kQuantThreads), 0, s, p);
-  if (e != cudaSuccess) return cuda_fail(e, "quantiser launch");
-  return TP_OK;
+  return guarded([&]() -> tp_status {
+    clear_error();
+    if (rows < 0 || cols < 0) return fail(TP_ERR_INVALID_ARG, "negative size");
+    if (block_rows != 1 && block_rows != kFp8Group)
+      return fail(TP_ERR_INVALID_ARG, "block_rows must be 1 or %d, got %d", kFp8Group, block_rows);
+    if (cols > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "sizes above 2^31-1 are not supported");
+    const int64_t col_groups = (cols + kFp8Group - 1) / kFp8Group;
+    if (ldx == 0) ldx = cols;
+    if (ldq == 0) ldq = cols;
+    if (lds == 0) lds = col_groups;
+    if (ldx < cols || ldq < cols || lds < col_groups)
+      return fail(TP_ERR_INVALID_ARG, "a row stride (ldx %lld, ldq %lld, lds %lld) is smaller than its row",
+                  (long long)ldx, (long long)ldq, (long long)lds);
+    if (rows == 0 || cols == 0) return TP_OK;
+    if (x == nullptr || q == nullptr || scales == nullptr)
+      return fail(TP_ERR_INVALID_ARG, "x, q or scales is NULL");
+    if (cols % 16 != 0 || ldx % 8 != 0 || ldq % 16 != 0)
+      return fail(TP_ERR_ALIGNMENT, "cols (%lld) and ldq (%lld) must be multiples of 16, ldx (%lld) of 8",
+                  (long long)cols, (long long)ldq, (long long)ldx);
+    if (!aligned16(x) || !aligned16(q)) return fail(TP_ERR_ALIGNMENT, "x or q is not 16-byte aligned");
+    const int64_t row_groups = (rows + block_rows - 1) / block_rows;
+    const int64_t per_cta = block_rows == 1 ? kQuantThreads / 8 : 1;
+    if (row_groups > 0x7FFFFFFFll * per_cta / col_groups) return fail(TP_ERR_UNSUPPORTED, "too many groups");
+    const int64_t blocks = (row_groups * col_groups + per_cta - 1) / per_cta;
+    QuantParams p{};
+    p.x = static_cast<const uint8_t*>(x);
+    p.q = static_cast<uint8_t*>(q);
+    p.scales = static_cast<uint8_t*>(scales);
+    p.ldx = ldx * 2;
+    p.ldq = ldq;
+    p.lds = lds;
+    p.rows = rows;
+    p.cols = static_cast<int>(cols);
+    p.col_groups = static_cast<int>(col_groups);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_pdl(block_rows == 1 ? quantize_rows_kernel : quantize_blocks_kernel,
+                               dim3(static_cast<unsigned>(blocks)), dim3(kQuantThreads), 0, s, p);
+    if (e != cudaSuccess) return cuda_fail(e, "quantiser launch");
+    return TP_OK;
+  });
 }
 
 tp_status tp_residual_norm(const tp_residual_norm_args* a, tp_stream_t stream) {
   using namespace tp;
-  clear_error();
-  if (a == nullptr) return fail(TP_ERR_INVALID_ARG, "args is NULL");
-  if (a->T < 0 || a->D < 0) return fail(TP_ERR_INVALID_ARG, "negative size");
-  auto known = [](int k) { return k == TP_NORM_NONE || k == TP_NORM_RMS || k == TP_NORM_LAYER; };
-  if (!known(a->norm) || !known(a->post_norm))
-    return fail(TP_ERR_INVALID_ARG, "unknown norm %d or post_norm %d", (int)a->norm, (int)a->post_norm);
-  if (!(a->eps >= 0.0f) || std::isinf(a->eps)) return fail(TP_ERR_INVALID_ARG, "eps must be finite and not negative");
-  if (a->D > TP_NORM_MAX_D)
-    return fail(TP_ERR_UNSUPPORTED, "rows wider than %d are not supported, got %lld", TP_NORM_MAX_D, (long long)a->D);
-  if (a->T > 0x7FFFFFF0) return fail(TP_ERR_UNSUPPORTED, "too many rows (%lld)", (long long)a->T);
-  NormParams p{};
-  p.ldx = a->ldx == 0 ? a->D : a->ldx;
-  p.ldy = a->ldy == 0 ? a->D : a->ldy;
-  p.ldh = a->ldh == 0 ? a->D : a->ldh;
-  p.ldu = a->ldu == 0 ? a->D : a->ldu;
-  const int64_t groups = (a->D + kFp8Group - 1) / kFp8Group;
-  p.ld_us = a->ld_u_scales == 0 ? groups : a->ld_u_scales;
-  p.ld_mod = a->ld_mod == 0 ? a->D : a->ld_mod;
-  if (p.ldx < a->D || p.ldy < a->D || p.ldh < a->D || p.ldu < a->D || p.ld_mod < a->D || p.ld_us < groups)
-    return fail(TP_ERR_INVALID_ARG, "a row stride is smaller than its row");
-  if (a->T == 0 || a->D == 0) return TP_OK;
-  if (a->x == nullptr) return fail(TP_ERR_INVALID_ARG, "x is NULL");
-  if (a->h == nullptr && a->u == nullptr) return fail(TP_ERR_INVALID_ARG, "neither h nor u is wanted");
-  if (a->y == nullptr && (a->h != nullptr || a->gate != nullptr || a->post_norm != TP_NORM_NONE))
-    return fail(TP_ERR_INVALID_ARG, "h, gate and post_norm belong to a branch y, which is NULL");
-  if ((a->post_weight != nullptr || a->post_bias != nullptr) && a->post_norm == TP_NORM_NONE)
-    return fail(TP_ERR_INVALID_ARG, "post_weight or post_bias without a post_norm");
-  if ((a->weight != nullptr || a->bias != nullptr) && a->norm == TP_NORM_NONE)
-    return fail(TP_ERR_INVALID_ARG, "weight or bias without a norm");
-  const bool fp8 = a->u != nullptr && a->u_scales != nullptr;
-  if (a->u == nullptr && (a->u_scales != nullptr || a->scale != nullptr || a->shift != nullptr ||
-                          a->norm != TP_NORM_NONE))
-    return fail(TP_ERR_INVALID_ARG, "norm, scale, shift and u_scales belong to u, which is NULL");
-  if (a->gate != nullptr || a->scale != nullptr || a->shift != nullptr) {
-    if (a->rows_per_mod < 1 || a->mod_rows < 1)
-      return fail(TP_ERR_INVALID_ARG, "rows_per_mod and mod_rows must be positive with a gate, scale or shift");
-    if ((a->T - 1) / a->rows_per_mod >= a->mod_rows)
-      return fail(TP_ERR_INVALID_ARG, "%lld rows, %lld to a modulation row, need more than %lld modulation rows",
-                  (long long)a->T, (long long)a->rows_per_mod, (long long)a->mod_rows);
-    p.rows_per_mod = static_cast<uint32_t>(a->rows_per_mod < a->T ? a->rows_per_mod : a->T);
-  }
-  const int64_t step = fp8 ? 16 : 8;
-  if (a->D % step != 0 || p.ldu % step != 0)
-    return fail(TP_ERR_ALIGNMENT, "D (%lld) and ldu (%lld) must be multiples of %lld", (long long)a->D,
-                (long long)p.ldu, (long long)step);
-  if (p.ldx % 8 != 0 || p.ldy % 8 != 0 || p.ldh % 8 != 0 || p.ld_mod % 8 != 0)
-    return fail(TP_ERR_ALIGNMENT, "ldx, ldy, ldh and ld_mod must be multiples of 8");
-  const void* ptrs[] = {a->x, a->y, a->post_weight, a->post_bias, a->gate, a->weight, a->bias,
-                        a->scale, a->shift, a->h, a->u};
-  for (const void* q : ptrs)
-    if (!aligned16(q)) return fail(TP_ERR_ALIGNMENT, "a pointer is not 16-byte aligned");
-  p.x = static_cast<const __nv_bfloat16*>(a->x);
-  p.y = static_cast<const __nv_bfloat16*>(a->y);
-  p.post_weight = static_cast<const __nv_bfloat16*>(a->post_weight);
-  p.post_bias = static_cast<const __nv_bfloat16*>(a->post_bias);
-  p.weight = static_cast<const __nv_bfloat16*>(a->weight);
-  p.bias = static_cast<const __nv_bfloat16*>(a->bias);
-  p.gate = static_cast<const __nv_bfloat16*>(a->gate);
-  p.scale = static_cast<const __nv_bfloat16*>(a->scale);
-  p.shift = static_cast<const __nv_bfloat16*>(a->shift);
-  p.h = static_cast<__nv_bfloat16*>(a->h);
-  p.u = fp8 ? nullptr : static_cast<__nv_bfloat16*>(a->u);
-  p.u8 = fp8 ? static_cast<uint8_t*>(a->u) : nullptr;
-  p.u_scales = static_cast<uint8_t*>(a->u_scales);
-  p.T = static_cast<int>(a->T);
-  p.D = static_cast<int>(a->D);
-  p.inv_d = 1.0f / static_cast<float>(p.D);
-  p.post_norm = a->post_norm;
-  p.norm = a->norm;
-  p.alpha = a->alpha;
-  p.eps = a->eps;
-  p.sms = sm_count();
-  if (p.sms <= 0) return fail(TP_ERR_CUDA, "cannot query the SM count of the current device");
-  p.few_rows = a->T <= p.sms;
-  return dispatch_norm(p, reinterpret_cast<cudaStream_t>(stream));
+  return guarded([&]() -> tp_status {
+    clear_error();
+    if (a == nullptr) return fail(TP_ERR_INVALID_ARG, "args is NULL");
+    if (a->T < 0 || a->D < 0) return fail(TP_ERR_INVALID_ARG, "negative size");
+    auto known = [](int k) { return k == TP_NORM_NONE || k == TP_NORM_RMS || k == TP_NORM_LAYER; };
+    if (!known(a->norm) || !known(a->post_norm))
+      return fail(TP_ERR_INVALID_ARG, "unknown norm %d or post_norm %d", (int)a->norm, (int)a->post_norm);
+    if (!(a->eps >= 0.0f) || std::isinf(a->eps)) return fail(TP_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (a->D > TP_NORM_MAX_D)
+      return fail(TP_ERR_UNSUPPORTED, "rows wider than %d are not supported, got %lld", TP_NORM_MAX_D, (long long)a->D);
+    if (a->T > 0x7FFFFFF0) return fail(TP_ERR_UNSUPPORTED, "too many rows (%lld)", (long long)a->T);
+    NormParams p{};
+    p.ldx = a->ldx == 0 ? a->D : a->ldx;
+    p.ldy = a->ldy == 0 ? a->D : a->ldy;
+    p.ldh = a->ldh == 0 ? a->D : a->ldh;
+    p.ldu = a->ldu == 0 ? a->D : a->ldu;
+    const int64_t groups = (a->D + kFp8Group - 1) / kFp8Group;
+    p.ld_us = a->ld_u_scales == 0 ? groups : a->ld_u_scales;
+    p.ld_mod = a->ld_mod == 0 ? a->D : a->ld_mod;
+    if (p.ldx < a->D || p.ldy < a->D || p.ldh < a->D || p.ldu < a->D || p.ld_mod < a->D || p.ld_us < groups)
+      return fail(TP_ERR_INVALID_ARG, "a row stride is smaller than its row");
+    if (a->T == 0 || a->D == 0) return TP_OK;
+    if (a->x == nullptr) return fail(TP_ERR_INVALID_ARG, "x is NULL");
+    if (a->h == nullptr && a->u == nullptr) return fail(TP_ERR_INVALID_ARG, "neither h nor u is wanted");
+    if (a->y == nullptr && (a->h != nullptr || a->gate != nullptr || a->post_norm != TP_NORM_NONE))
+      return fail(TP_ERR_INVALID_ARG, "h, gate and post_norm belong to a branch y, which is NULL");
+    if ((a->post_weight != nullptr || a->post_bias != nullptr) && a->post_norm == TP_NORM_NONE)
+      return fail(TP_ERR_INVALID_ARG, "post_weight or post_bias without a post_norm");
+    if ((a->weight != nullptr || a->bias != nullptr) && a->norm == TP_NORM_NONE)
+      return fail(TP_ERR_INVALID_ARG, "weight or bias without a norm");
+    const bool fp8 = a->u != nullptr && a->u_scales != nullptr;
+    if (a->u == nullptr && (a->u_scales != nullptr || a->scale != nullptr || a->shift != nullptr ||
+                            a->norm != TP_NORM_NONE))
+      return fail(TP_ERR_INVALID_ARG, "norm, scale, shift and u_scales belong to u, which is NULL");
+    if (a->gate != nullptr || a->scale != nullptr || a->shift != nullptr) {
+      if (a->rows_per_mod < 1 || a->mod_rows < 1)
+        return fail(TP_ERR_INVALID_ARG, "rows_per_mod and mod_rows must be positive with a gate, scale or shift");
+      if ((a->T - 1) / a->rows_per_mod >= a->mod_rows)
+        return fail(TP_ERR_INVALID_ARG, "%lld rows, %lld to a modulation row, need more than %lld modulation rows",
+                    (long long)a->T, (long long)a->rows_per_mod, (long long)a->mod_rows);
+      p.rows_per_mod = static_cast<uint32_t>(a->rows_per_mod < a->T ? a->rows_per_mod : a->T);
+    }
+    const int64_t step = fp8 ? 16 : 8;
+    if (a->D % step != 0 || p.ldu % step != 0)
+      return fail(TP_ERR_ALIGNMENT, "D (%lld) and ldu (%lld) must be multiples of %lld", (long long)a->D,
+                  (long long)p.ldu, (long long)step);
+    if (p.ldx % 8 != 0 || p.ldy % 8 != 0 || p.ldh % 8 != 0 || p.ld_mod % 8 != 0)
+      return fail(TP_ERR_ALIGNMENT, "ldx, ldy, ldh and ld_mod must be multiples of 8");
+    const void* ptrs[] = {a->x, a->y, a->post_weight, a->post_bias, a->gate, a->weight, a->bias,
+                          a->scale, a->shift, a->h, a->u};
+    for (const void* q : ptrs)
+      if (!aligned16(q)) return fail(TP_ERR_ALIGNMENT, "a pointer is not 16-byte aligned");
+    p.x = static_cast<const __nv_bfloat16*>(a->x);
+    p.y = static_cast<const __nv_bfloat16*>(a->y);
+    p.post_weight = static_cast<const __nv_bfloat16*>(a->post_weight);
+    p.post_bias = static_cast<const __nv_bfloat16*>(a->post_bias);
+    p.weight = static_cast<const __nv_bfloat16*>(a->weight);
+    p.bias = static_cast<const __nv_bfloat16*>(a->bias);
+    p.gate = static_cast<const __nv_bfloat16*>(a->gate);
+    p.scale = static_cast<const __nv_bfloat16*>(a->scale);
+    p.shift = static_cast<const __nv_bfloat16*>(a->shift);
+    p.h = static_cast<__nv_bfloat16*>(a->h);
+    p.u = fp8 ? nullptr : static_cast<__nv_bfloat16*>(a->u);
+    p.u8 = fp8 ? static_cast<uint8_t*>(a->u) : nullptr;
+    p.u_scales = static_cast<uint8_t*>(a->u_scales);
+    p.T = static_cast<int>(a->T);
+    p.D = static_cast<int>(a->D);
+    p.inv_d = 1.0f / static_cast<float>(p.D);
+    p.post_norm = a->post_norm;
+    p.norm = a->norm;
+    p.alpha = a->alpha;
+    p.eps = a->eps;
+    p.sms = sm_count();
+    if (p.sms <= 0) return fail(TP_ERR_CUDA, "cannot query the SM count of the current device");
+    p.few_rows = a->T <= p.sms;
+    return dispatch_norm(p, reinterpret_cast<cudaStream_t>(stream));
+  });
 }
 
 }  // extern "C"

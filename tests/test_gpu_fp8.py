@@ -632,6 +632,70 @@ def test_calls_on_several_streams_at_once():
             assert torch.equal(w[6], g[6]) and torch.equal(w[4], g[4])
 
 
+def test_offsets_past_32_bits():
+    """Rows whose bytes start beyond 4 GiB: a long quantised activation, outputs and inputs with a huge row stride."""
+    rng = np.random.default_rng(30)
+    T, K = 70016, 32768
+    x = torch.zeros((T, K), dtype=BF16, device=DEV)
+    last = to_bf16(rng.normal(size=(2, K)))
+    x[-2:] = last
+    q, s = tp.tp_quantize_fp8(x)
+    q2, s2 = tp.tp_quantize_fp8(last)
+    assert torch.equal(q[-2:].view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s[-2:].view(torch.uint8),
+                                                                                        s2.view(torch.uint8))
+    assert int(q[:-2].view(torch.uint8).count_nonzero()) == 0
+    _, u, _ = tp.tp_residual_norm(x, norm="rms")
+    assert torch.equal(u[-2:], tp.tp_residual_norm(last, norm="rms")[1])
+    w, sw, _ = quantized(rng, 2176, K, 128, 0.01)
+    few = tp.tp_linear_colwise_fp8(q2, s2, [w], [sw])[0]
+    long = tp.tp_linear_colwise_fp8(q, s, [w], [sw])[0]
+    assert float((long[-2:].float() - few.float()).abs().max()) <= 2.0 ** -6 * float(few.float().abs().max())
+    assert int(long[:-2].count_nonzero()) == 0
+    del x, q, u, long
+    for T, N in ((40, 136), (2600, 2064)):       # either kernel, rows 8 MiB apart and more
+        wide = torch.full((T, (1 << 32) // T // 64 * 64), -7.0, dtype=BF16, device=DEV)
+        a, sa, av = integers(rng, T, 256, 1)
+        b, sb, bv = integers(rng, N, 256, 128)
+        z = tp.tp_linear_rowwise_fp8([a], [sa], [b], [sb], out=wide[:, 64:64 + N])
+        np.testing.assert_array_equal(f64(z), bf16_round(av @ bv.T))
+        h, _, _ = tp.tp_residual_norm(z.contiguous(), z.contiguous(), out=None, h=wide[:, 8192:8192 + N])
+        assert torch.equal(h, (2 * z.float()).to(BF16))
+        assert int((wide[:, 64 + N:8192] != -7).count_nonzero()) == 0
+        del wide, z, h
+
+
+def test_first_call_may_be_captured():
+    """In a new process, whose first use of the library is inside a capture."""
+    import subprocess
+    import sys
+    code = """
+import sys, torch
+sys.path.insert(0, %r)
+import tensor_sharded_linear_tp_gb300 as tp
+mode = sys.argv[1]
+T = 4 if mode == "few" else 1300
+x = torch.randn(T, 512, device="cuda").to(torch.bfloat16)
+w8 = torch.zeros(2064, 512, device="cuda").to(torch.float8_e4m3fn)
+ws = torch.full((17, 4), 127, dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    _, u, su = tp.tp_residual_norm(x, norm="rms", out="fp8")
+    q, s = tp.tp_quantize_fp8(x)
+    y = tp.tp_linear_colwise_fp8(u, su, [w8], [ws])[0]
+    z = tp.tp_linear_rowwise_fp8([q], [s], [w8], [ws])
+y.fill_(1), z.fill_(1)
+g.replay()
+torch.cuda.synchronize()
+tp.tp_device_status()
+assert int(y.count_nonzero()) == 0 and int(z.count_nonzero()) == 0
+print("replayed")
+""" % tp.__file__.rsplit("/", 2)[0]
+    for mode in ("few", "many"):
+        r = subprocess.run([sys.executable, "-c", code, mode], capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0 and "replayed" in r.stdout, (mode, r.stdout[-500:], r.stderr[-2000:])
+
+
 # ----------------------------------------------------------------------------- refusals on the GPU's side
 
 def test_binding_refusals():
