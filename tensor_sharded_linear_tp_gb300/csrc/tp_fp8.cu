@@ -33,6 +33,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <mutex>
 #include <type_traits>
 
@@ -1270,18 +1271,21 @@ tp_status run_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
 }
 
 // Whether 256 x 256 tiles on CTA pairs beat 128 x 128 tiles on single CTAs, by what both took (ns):
-// a wave of single CTAs 6000 (SwiGLU 9000) and 230 (400) a scale group, a launch of pairs 6500 and
-// 380 a group and wave.  Measured (us, single against pairs): Q/K/V of 128 / 256 / 384 tokens 25.4 /
+// a wave of single CTAs 6000 (SwiGLU 10500) and 230 (400) a scale group of the CTAs' share, a launch
+// of pairs 6500 and 380 a group and wave.  Measured (us, single against pairs): Q/K/V of 128 / 256 / 384 tokens 25.4 /
 // 37.6 / 52.5 against 29.4 / 30.3 / 45.1; down of 384 / 512 tokens 38 / 66 against 60 / 60; 2 x 2048 x
 // 1024 of 256 / 384 / 640 tokens 8.0 / 8.8 / 15.9 against 8.5 / 8.7 / 9.2; SwiGLU 4096 x 512 of 64 / 128
-// tokens 8.2 / 11.9 against 8.2 / 8.0.
+// tokens 8.2 / 11.9 against 8.2 / 8.0, 2 x 2048 x 2048 of 100 tokens 9.8 against 11.5.
 bool prompt_is_faster(const Fp8Params& p, const Fp8Call& c) {
   const bool glu = p.act == TP_ACT_SWIGLU;
   const int64_t sms = sm_count(), groups = static_cast<int64_t>(p.n_segs) * p.k_groups;
   if (sms < 2) return false;
   const int64_t single = static_cast<int64_t>(p.n_groups) * ceil_div(c.n_out, BM) * ceil_div(c.T, 128);
   const int64_t paired = static_cast<int64_t>(p.n_groups) * ceil_div(c.n_out, glu ? BM : PN) * ceil_div(c.T, PM);
-  const int64_t t_single = (single + sms - 1) / sms * (glu ? 9000 + groups * 400 : 6000 + groups * 230);
+  const int64_t chunks = (groups + kChunk - 1) / kChunk;
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, chunks, sms / single}));
+  const int64_t share = (groups + splits - 1) / splits;
+  const int64_t t_single = (single + sms - 1) / sms * (glu ? 10500 + share * 400 : 6000 + share * 230);
   const int64_t t_paired = 6500 + (paired + sms / 2 - 1) / (sms / 2) * groups * 380;
   return t_paired < t_single;
 }
