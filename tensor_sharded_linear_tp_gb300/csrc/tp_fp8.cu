@@ -19,13 +19,18 @@
 // fewer 128-row tiles than SMs, the chunks of K split over the CTAs of a cluster.  Every CTA
 // leaves its fp32 partial tile in its shared memory, and after a cluster barrier each CTA sums
 // its share of the tokens over the CTAs in K order through distributed shared memory, applies
-// bias and activation and stores (or quantises: a tile's 128 columns are one scale group).
+// bias and activation and stores (or quantises: a tile's 128 columns are one scale group).  One
+// token's Q/K/V, 4 x 4608 x 6144, takes 21.2 us (5.3 TB/s; 16.7 us at the measured copy rate, the
+// rest is a launch's start and join), gate/up of 23 tokens, 3 x 12288 x 6144, 39.4 us (5.8 TB/s).
+// With 128 tokens a tile, shared memory bounds it: 32 KB in and 32 KB out for each 256 cycles of MMA.
 //
 // fp8_prompt_kernel: the tokens are M, 256 of them to a persistent CTA pair (cta_group::2), 256
 // weight rows (SwiGLU: 128 gate and 128 up rows) are N.  Bound by the tensor core.  Two
 // accumulators of 256 columns and the scale words do not fit tensor memory's 512 columns side by
 // side, so the accumulators overlap by 32 columns: the epilogue reads those first and hands them
-// back, and the next tile's MMAs start while it works through the rest.
+// back, and the next tile's MMAs start while it works through the rest.  Gate/up of 4608 tokens,
+// 4 x 9216 x 6144 with SwiGLU to fp8, takes 654 us at the power limit (3190 TFLOP/s; 600 us in the
+// first, unthrottled runs), the down projection 354 us; a scale group's MMAs run 512 cycles.
 //
 // Every mbarrier wait is bounded (about 2 s); a CTA that gives up records it in the library's
 // status word, lets its copies and MMAs drain, frees tensor memory and exits.

@@ -1,14 +1,18 @@
 // What stands around the 8-bit projections: the quantiser and the residual norm.  Both read and
-// write every element once and are bound by HBM.
+// write every element once.
 //
 // tp_quantize_fp8: a thread holds 16 consecutive elements (two 16-byte loads, one 16-byte store
 // of codes).  By token (1 x 128): 8 lanes share a group and join their maxima by three shuffles.
 // By weight block (128 x 128): a CTA of 256 threads holds the block in registers, four rows'
-// chunks a thread, so the block is read once although its scale needs all of it.
+// chunks a thread, so the block is read once although its scale needs all of it.  Both are bound by
+// HBM: 4608 x 18432 by token 37.5 us (6.8 TB/s, the measured copy rate), 9216 x 6144 by block 25.4 us
+// (6.7 TB/s).
 //
 // tp_residual_norm: one row is held in registers as fp32 by one warp (short rows) or one CTA; the
 // statistics are sums over those registers (the variance about the mean, in a second sum), and
-// the normed, modulated row leaves as bf16 or as codes with their scales.
+// the normed, modulated row leaves as bf16 or as codes with their scales.  4608 x 6144 with two
+// norms, gate and modulation, to fp8: 40.3 us (4.9 TB/s); bound by its instructions, some 130 a
+// thread for each 8 elements, and the three sums on the way through a row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
