@@ -566,7 +566,7 @@ def tp_quantize_fp8(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | None
         raise ValueError(f"block_rows must be 1 or {FP8_GROUP}, got {block_rows}")
     shape = x.shape
     rows, cols = shape
-    ldx = _need("x", x, _BF16, shape, dev)
+    ldx = 0 if x.dtype is _BF16 and x.is_contiguous() else _need("x", x, _BF16, shape, dev)
     s_shape = (-(-rows // block_rows), _groups(cols))
     if q is None:
         q, = _alloc(stream, dev, _E4M3, shape)
@@ -669,7 +669,7 @@ def tp_residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, norm: str =
         raise ValueError("u belongs to an output type")
     shape = x.shape
     T, D = shape
-    ldx = _need("x", x, _BF16, shape, dev)
+    ldx = 0 if x.dtype is _BF16 and x.is_contiguous() else _need("x", x, _BF16, shape, dev)
 
     vectors = [0, 0, 0, 0]
     if weight is not None or bias is not None or post_weight is not None or post_bias is not None:
