@@ -39,7 +39,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <memory>
 #include <mutex>
 #include <type_traits>
 
@@ -1066,31 +1065,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
 inline int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 // Operand map over a row-major [rows, K] matrix of bytes: boxes of 128 bytes x box_rows, 128-byte
-// swizzle, zeros outside.  Encoded as 2-byte elements (K and the stride are multiples of 16).  A call
-// makes one for each operand of each rank, so each thread keeps the maps of its last calls' operands
-// beside the library's own store (0.2 us a map there): the key is every argument of the encoding, and
-// the map a function of the key alone.
+// swizzle, zeros outside.  Encoded as 2-byte elements (K and the stride are multiples of 16).
 tp_status operand_map(CUtensorMap* m, const void* ptr, int64_t K, int64_t rows, int64_t ld, int box_rows) {
-  struct Entry {
-    const void* ptr;
-    int64_t K, rows, ld;
-    int box_rows;
-    CUtensorMap map;
-  };
-  constexpr size_t kEntries = 256;
-  thread_local std::unique_ptr<Entry[]> entries;
-  if (!entries) entries.reset(new Entry[kEntries]());
-  uint64_t h = reinterpret_cast<uint64_t>(ptr) >> 4;
-  h = (h ^ static_cast<uint64_t>(rows) << 40 ^ static_cast<uint64_t>(K) << 20) * 0x9E3779B97F4A7C15ull;
-  Entry& e = entries[h >> 56];
-  if (e.ptr != ptr || e.K != K || e.rows != rows || e.ld != ld || e.box_rows != box_rows) {
-    e.ptr = nullptr;
-    tp_status st = encode_bf16_2d(&e.map, ptr, K / 2, rows, ld / 2, KB / 2, static_cast<uint32_t>(box_rows), true);
-    if (st != TP_OK) return st;
-    e.ptr = ptr, e.K = K, e.rows = rows, e.ld = ld, e.box_rows = box_rows;
-  }
-  *m = e.map;
-  return TP_OK;
+  return encode_bf16_2d(m, ptr, K / 2, rows, ld / 2, KB / 2, static_cast<uint32_t>(box_rows), true);
 }
 
 // The operands of a call, checked.
