@@ -194,16 +194,17 @@ constexpr uint32_t kScaleOne = 0x7F7F7F7Fu;  // 2^0 for rows past the operand (t
 
 // One row's word: scale bytes [kg, kg + n) of scale row (row >> kShift).  `words` (host: every
 // row's chunks are aligned whole words) keeps the load free of branches, so that a thread's loads
-// are in flight together.
+// are in flight together.  (Not read-only loads: this CTA may have been resident while the kernel
+// before wrote X's scales, and only ordinary loads are sure to see that after the grid wait.)
 template <int kShift>
 __device__ __forceinline__ uint32_t load_word(const uint8_t* s, int64_t ld, int rows, int row, int kg, int n,
                                               bool words) {
   const uint8_t* at = s + static_cast<int64_t>(row >> kShift) * ld + kg;
-  if (words) return row < rows ? __ldg(reinterpret_cast<const uint32_t*>(at)) : kScaleOne;
+  if (words) return row < rows ? *reinterpret_cast<const uint32_t*>(at) : kScaleOne;
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < kChunk; ++i)
-    w |= (row < rows && i < n ? static_cast<uint32_t>(__ldg(at + i)) : 0x7Fu) << (8 * i);
+    w |= (row < rows && i < n ? static_cast<uint32_t>(at[i]) : 0x7Fu) << (8 * i);
   return w;
 }
 

@@ -11,7 +11,7 @@
 // tp_residual_norm: one row is held in registers as fp32 by one warp (short rows) or one CTA; the
 // statistics are sums over those registers (the variance about the mean, in a second sum), and
 // the normed, modulated row leaves as bf16 or as codes with their scales.  4608 x 6144 with two
-// norms, gate and modulation, to fp8: 40.3 us (4.9 TB/s); bound by its instructions, some 130 a
+// norms, gate and modulation, to fp8: 40.6 us (4.9 TB/s); bound by its instructions, some 130 a
 // thread for each 8 elements, and the three sums on the way through a row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -173,9 +173,11 @@ __device__ __forceinline__ void unpack8(const uint4& a, f2 (&v)[4]) {
   v[0] = pair(bf16_lo(a.x), bf16_hi(a.x)), v[1] = pair(bf16_lo(a.y), bf16_hi(a.y));
   v[2] = pair(bf16_lo(a.z), bf16_hi(a.z)), v[3] = pair(bf16_lo(a.w), bf16_hi(a.w));
 }
-// Eight elements of a vector or table that many rows read: they stay in L1.
+// Eight elements of a vector or table that many rows read: they stay in L1.  (Not a read-only load:
+// this CTA may have been resident while the kernel before wrote a table, and only an ordinary load
+// is sure to see that after the grid wait.)
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, f2 (&v)[4]) {
-  unpack8(__ldg(reinterpret_cast<const uint4*>(p)), v);
+  unpack8(*reinterpret_cast<const uint4*>(p), v);
 }
 // Eight elements of a row that is read once: past L1, which keeps the tables.
 __device__ __forceinline__ uint4 load_row8(const __nv_bfloat16* p) {

@@ -620,6 +620,43 @@ def test_block_captured_and_replayed(T):
                 assert torch.equal(got[i].view(torch.uint8), want[i].view(torch.uint8)), i
 
 
+@pytest.mark.parametrize("T", [1, 24, 260])
+def test_buffers_written_anew_between_launches(T):
+    """Calls queued without a pause, each reading what the one before wrote into the same buffers anew.
+
+    A launch's CTAs may be on their SMs while the launch before the last still reads the old
+    contents through the same L1: codes, scales, and the tables of the residual norm."""
+    rng = np.random.default_rng(31)
+    K, N, steps = 512, 512, 24
+    w, sw, _ = quantized(rng, N, K, 128, 0.05)
+    xs = [to_bf16(rng.normal(0, 10.0 ** (i % 5 - 2), size=(T, K))) for i in range(steps)]
+    q, s = tp.tp_quantize_fp8(xs[0])
+    table, hold = torch.empty_like(xs[0]), [torch.empty_like(xs[0]) for _ in range(steps)]
+    ys = [torch.empty((T, N), dtype=BF16, device=DEV) for _ in range(steps)]
+
+    def step(i):
+        tp.tp_residual_norm(xs[i], norm="layer", u=table)
+        tp.tp_residual_norm(xs[i - 1], xs[i], out="fp8", norm="rms", gate=table, scale=table, shift=table,
+                            rows_per_mod=1, h=hold[i], u=q, u_scales=s)
+        tp.tp_linear_colwise_fp8(q, s, [w], [sw], y_shards=[ys[i]])
+
+    for i in range(steps):
+        step(i)
+        torch.cuda.synchronize()
+    want = [(h.clone(), y.clone()) for h, y in zip(hold, ys)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for i in range(steps):
+            step(i)
+    for _ in range(10):
+        for t in hold + ys:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for i in range(steps):
+            assert torch.equal(hold[i], want[i][0]) and torch.equal(ys[i], want[i][1]), i
+
+
 def test_calls_on_several_streams_at_once():
     args = [sharded_block(T, 512, 1024, 2, T) for T in (1, 40, 200, 3000)]
     want = [forward(*a) for a in args]
