@@ -1068,7 +1068,7 @@ inline int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) 
 // Operand map over a row-major [rows, K] matrix of bytes: boxes of 128 bytes x box_rows, 128-byte
 // swizzle, zeros outside.  Encoded as 2-byte elements (K and the stride are multiples of 16).
 tp_status operand_map(CUtensorMap* m, const void* ptr, int64_t K, int64_t rows, int64_t ld, int box_rows) {
-  return encode_bf16_2d(m, ptr, K / 2, rows, ld / 2, KB / 2, static_cast<uint32_t>(box_rows), true);
+  return encode_bf16_2d_now(m, ptr, K / 2, rows, ld / 2, KB / 2, static_cast<uint32_t>(box_rows));
 }
 
 // The operands of a call, checked.

@@ -1043,6 +1043,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
+// The encode itself.
+tp_status encode_2d_now(CUtensorMap* m, const void* ptr, CUtensorMapDataType dtype, int esz, int64_t inner, int64_t outer,
+                        int64_t ld, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle,
+                        CUtensorMapL2promotion promo) {
+  auto enc = encoder();
+  if (enc == nullptr) return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * esz};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, dtype, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   swizzle, promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+  return TP_OK;
+}
+
 // Encoded tensor maps are cached: a call that reuses the buffers of an earlier
 // call (the usual case in a model's forward pass) skips the driver encode.  The
 // key is every argument of the encode, so a cached map is exactly what the
@@ -1085,15 +1101,8 @@ tp_status encode_2d(CUtensorMap* m, const void* ptr, CUtensorMapDataType dtype, 
       return TP_OK;
     }
   }
-  auto enc = encoder();
-  if (enc == nullptr) return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * esz};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(m, dtype, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   swizzle, promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+  tp_status st = encode_2d_now(m, ptr, dtype, esz, inner, outer, ld, box_inner, box_outer, swizzle, promo);
+  if (st != TP_OK) return st;
   std::lock_guard<std::mutex> lock(g_map_mutex);
   if (g_map_cache.size() >= kMapCacheMax) g_map_cache.clear();
   g_map_cache.emplace(key, *m);
@@ -1702,6 +1711,11 @@ tp_status encode_bf16_2d(CUtensorMap* m, const void* ptr, int64_t inner, int64_t
   return encode_2d(m, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, outer, ld, box_inner, box_outer,
                    swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+tp_status encode_bf16_2d_now(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int64_t ld,
+                             uint32_t box_inner, uint32_t box_outer) {
+  return encode_2d_now(m, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, outer, ld, box_inner, box_outer,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 }  // namespace tp
