@@ -249,9 +249,10 @@ struct TokensCfg {
   static constexpr uint32_t X_BYTES = TN * KB;
   static constexpr uint32_t STAGE_BYTES = W_BYTES + X_BYTES;
   // Up to 32 tokens two CTAs fit an SM (so that a kernel's prologue runs beside its predecessor),
-  // with 90 to 108 KB in flight each; more tokens take one CTA with twice that.
+  // with 90 to 108 KB in flight each; more tokens take one CTA with up to 216 KB (SwiGLU of 64 tokens:
+  // five stages 40.0 us, four 40.8).
   static constexpr bool SMALL = TN <= 32;
-  static constexpr uint32_t RING_MAX = SMALL ? 110592 : 196608;
+  static constexpr uint32_t RING_MAX = SMALL ? 110592 : 221184;
   static constexpr int STAGES = RING_MAX / STAGE_BYTES;
   static constexpr uint32_t RING = STAGES * STAGE_BYTES;
   static constexpr uint32_t PARTIAL = W_TILES * TN * BM * 4;    // fp32 [tile][token][128], over the ring
