@@ -1298,12 +1298,13 @@ tp_status run_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   return p.act == TP_ACT_SWIGLU ? launch_tokens<TN, true>(c, p, stream) : launch_tokens<TN, false>(c, p, stream);
 }
 
-// Whether 256 x 256 tiles on CTA pairs beat 128 x 128 tiles on single CTAs, by what both took (ns):
-// a wave of single CTAs 6000 (SwiGLU 10500) and 230 (400) a scale group of the CTAs' share, a launch
-// of pairs 6500 and 380 a group and wave.  Measured (us, single against pairs): Q/K/V of 128 / 256 / 384 tokens 25.4 /
-// 37.6 / 52.5 against 29.4 / 30.3 / 45.1; down of 384 / 512 tokens 38 / 66 against 60 / 60; 2 x 2048 x
-// 1024 of 256 / 384 / 640 tokens 8.0 / 8.8 / 15.9 against 8.5 / 8.7 / 9.2; SwiGLU 4096 x 512 of 64 / 128
-// tokens 8.2 / 11.9 against 8.2 / 8.0, 2 x 2048 x 2048 of 100 tokens 9.8 against 11.5.
+// Whether 256 x 256 tiles on CTA pairs beat 128 x 128 tiles on single CTAs, by what both took (ns): a
+// wave of single CTAs 6000 and 230 a scale group of the CTAs' share (SwiGLU 28 more a token of the
+// tile, and 400), a launch of pairs 6500 and 260 a group and wave.  Measured (us, single against
+// pairs): Q/K/V of 128 / 192 / 384 tokens 25.3 / 36.3 / 53.1 against 26.5 / 26.9 / 38.4; down of 384 /
+// 512 tokens 38 / 66 against 47 / 48; 2 x 2048 x 1024 of 256 / 512 / 768 tokens 7.9 / 8.7 / 16.4
+// against 8.5 / 8.8 / 9.3; SwiGLU 4096 x 512 of 65 / 128 tokens 8.6 / 11.6 against 8.3 / 8.2, 2 x 2048
+// x 2048 of 96 / 300 tokens 9.1 / 14.3 against 11.4 / 11.6.
 bool prompt_is_faster(const Fp8Params& p, const Fp8Call& c) {
   const bool glu = p.act == TP_ACT_SWIGLU;
   const int64_t sms = sm_count(), groups = static_cast<int64_t>(p.n_segs) * p.k_groups;
@@ -1313,8 +1314,9 @@ bool prompt_is_faster(const Fp8Params& p, const Fp8Call& c) {
   const int64_t chunks = (groups + kChunk - 1) / kChunk;
   const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, chunks, sms / single}));
   const int64_t share = (groups + splits - 1) / splits;
-  const int64_t t_single = (single + sms - 1) / sms * (glu ? 10500 + share * 400 : 6000 + share * 230);
-  const int64_t t_paired = 6500 + (paired + sms / 2 - 1) / (sms / 2) * groups * 380;
+  const int64_t wave = 6000 + (glu ? 28 * std::min<int64_t>(c.T, 128) + share * 400 : share * 230);
+  const int64_t t_single = (single + sms - 1) / sms * wave;
+  const int64_t t_paired = 6500 + (paired + sms / 2 - 1) / (sms / 2) * groups * 260;
   return t_paired < t_single;
 }
 
