@@ -513,8 +513,9 @@ __global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2
   // ---------------------------------------------------------------- join, activation, store
   // This CTA's share of the tile's tokens, a warp to a token, four columns to a lane.  A token's
   // reads, sums and store take half a microsecond one after the other, so what can be is in flight
-  // together: the reads from all the CTAs that share K, or, with one, those of four tokens (gate/up
-  // of 256 tokens in this kernel 72 -> 64 us).
+  // together: the reads from all the CTAs that share K, or, with one or two, those of four tokens (with
+  // one: gate/up of 256 tokens in this kernel 72 -> 64 us; with two: GELU of 333 tokens, 2 x 1096 x
+  // 2000, 10.8 -> 10.1 us; two tokens with three or four: 0.1 to 0.3 us slower).
   if (!*abort_flag) {
     const int tokens = min(TN, p.T - t0);
     const int n0 = w_row0 + lane * 4;
@@ -529,8 +530,9 @@ __global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2
     const uint32_t local = ptx::smem_addr(base) + static_cast<uint32_t>(lane) * 16;
     const int t_begin = tokens * part / splits, t_end = tokens * (part + 1) / splits;
     constexpr int kWarps = kTokensThreads / 32;
-    auto join = [&](auto several, int t) {
-      constexpr int U = decltype(several)::value;  // tokens t, t + kWarps, ...
+    auto join = [&](auto several, auto sources, int t) {
+      constexpr int U = decltype(several)::value;      // tokens t, t + kWarps, ...
+      constexpr int kFrom = decltype(sources)::value;  // at least `splits`
       float v[U][C::W_TILES][4];
       auto at = [&](int j, int a, int s) {  // a token past the share: the first one's, not stored
         const int tj = t + j * kWarps < t_end ? t + j * kWarps : t;
@@ -543,7 +545,6 @@ __global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[j][a][e] = 0.0f;
       auto add = [](float (&to)[4], const float4& f) { to[0] += f.x, to[1] += f.y, to[2] += f.z, to[3] += f.w; };
-      constexpr int kFrom = U == 1 ? kMaxSplits : 1;
       float4 f[U][C::W_TILES][kFrom];
 #pragma unroll
       for (int j = 0; j < U; ++j)
@@ -592,11 +593,15 @@ __global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2
         }
       }
     };
-    if (splits == 1 && tokens > kWarps) {
-      for (int t = t_begin + warp; t < t_end; t += 4 * kWarps) join(std::integral_constant<int, 4>{}, t);
-    } else {
-      for (int t = t_begin + warp; t < t_end; t += kWarps) join(std::integral_constant<int, 1>{}, t);
-    }
+    auto join_all = [&](auto several, auto sources) {
+      for (int t = t_begin + warp; t < t_end; t += decltype(several)::value * kWarps) join(several, sources, t);
+    };
+    if (t_end - t_begin <= kWarps || splits > 2)
+      join_all(std::integral_constant<int, 1>{}, std::integral_constant<int, kMaxSplits>{});
+    else if (splits == 1)
+      join_all(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+    else
+      join_all(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
   }
   cluster_sync_relaxed();  // no CTA's shared memory goes away while another reads it
   if (warp == 0) {
