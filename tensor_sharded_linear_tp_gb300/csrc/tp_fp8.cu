@@ -22,15 +22,17 @@
 // bias and activation and stores (or quantises: a tile's 128 columns are one scale group).  One
 // token's Q/K/V, 4 x 4608 x 6144, takes 21.2 us (5.3 TB/s; 16.7 us at the measured copy rate, the
 // rest is a launch's start and join), gate/up of 23 tokens, 3 x 12288 x 6144, 39.4 us (5.8 TB/s).
-// With 128 tokens a tile, shared memory bounds it: 32 KB in and 32 KB out for each 256 cycles of MMA.
+// With 128 tokens a tile it is bound by the operands' way from L2: 144 CTAs take 32 KB each for a
+// scale group, in 230 ns (20 TB/s; without three quarters of the MMAs a launch is 10 % shorter).
 //
 // fp8_prompt_kernel: the tokens are M, 256 of them to a persistent CTA pair (cta_group::2), 256
 // weight rows (SwiGLU: 128 gate and 128 up rows) are N.  Bound by the tensor core.  Two
 // accumulators of 256 columns and the scale words do not fit tensor memory's 512 columns side by
 // side, so the accumulators overlap by 32 columns: the epilogue reads those first and hands them
 // back, and the next tile's MMAs start while it works through the rest.  Gate/up of 4608 tokens,
-// 4 x 9216 x 6144 with SwiGLU to fp8, takes 654 us at the power limit (3190 TFLOP/s; 600 us in the
-// first, unthrottled runs), the down projection 354 us; a scale group's MMAs run 512 cycles.
+// 4 x 9216 x 6144 with SwiGLU to fp8, takes 620 us at the power limit (3370 TFLOP/s; 551 us in the
+// first, unthrottled runs), the down projection 318 us (282); a scale group's MMAs run 512 cycles
+// and a group takes 540 (1.43 GHz at the power limit).
 //
 // Every mbarrier wait is bounded (about 2 s); a CTA that gives up records it in the library's
 // status word, lets its copies and MMAs drain, frees tensor memory and exits.
@@ -1293,8 +1295,8 @@ tp_status run_prompt(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   if (pairs < 1) return fail(TP_ERR_UNSUPPORTED, "no CTA pair of the kernel fits on this device");
   // Clusters of two pairs, on n-adjacent tiles that share X, where the tiles pair up and the
   // clusters' waves, each about 4 % shorter, take no longer than the pairs' (fewer clusters of
-  // four CTAs than pairs fit: 36 x 4 against 76 x 2).  Measured at 4608 tokens: gate/up 659 us
-  // against 667 (36 waves, 35 of pairs), down 354 against 357 (6 waves either way).
+  // four CTAs than pairs fit: 36 x 4 against 76 x 2).  Measured at 4608 tokens: gate/up 652 us
+  // against 663 (36 waves, 35 of pairs), down 345 against 357 (6 waves either way).
   const int64_t tiles = static_cast<int64_t>(p.n_groups) * p.n_tiles * p.t_tiles;
   bool quad = quads > 0 && p.n_tiles % 2 == 0;
   if (quad) {
