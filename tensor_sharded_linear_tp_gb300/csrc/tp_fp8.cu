@@ -1194,9 +1194,12 @@ tp_status launch_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   p.n_tiles = ceil_div(p.n_out, BM);
   const int64_t tiles = static_cast<int64_t>(p.n_groups) * p.n_tiles * p.t_tiles;
   // The split of K whose longest SM is shortest: waves x (a CTA's chunks + the fixed part of its
-  // life, about 4 us or three chunks).  Ties go to the smaller cluster.  Measured, down projection
-  // of one token (4 x 6144 x 4608, 36 chunks, 48 tiles): splits 1 / 2 / 3 / 4 / 5 / 6 / 8 take
-  // 29.9 / 22.0 / 21.2 / 20.6 / 20.7 / 26.3 / 24.7 us (from 6 on the clusters need a second wave).
+  // life, about 4 us or three chunks; with 128 tokens to join, six).  Ties go to the smaller
+  // cluster.  Measured, down projection of one token (4 x 6144 x 4608, 36 chunks, 48 tiles): splits
+  // 1 / 2 / 3 / 4 / 5 / 6 / 8 take 29.9 / 22.0 / 21.2 / 20.6 / 20.7 / 26.3 / 24.7 us (from 6 on the
+  // clusters need a second wave); of 256 tokens (96 tiles): 36.4 / 43.7 / 50.1 / 44.1 / 52.0 / 56.4 /
+  // 72.0, of 512 (192 tiles): 70.1 / 64.8 / 81.8 / 81.9 and more.
+  constexpr int kFixed = TN > 64 ? 6 : 3;
   const int* resident = nullptr;
   tp_status st = tokens_residency<TN, kGlu>(&resident);
   if (st != TP_OK) return st;
@@ -1205,7 +1208,7 @@ tp_status launch_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   for (int s = 1; s <= kMaxSplits && s <= chunks; ++s) {
     const int n = resident[s];
     if (n < 1) continue;
-    const int64_t cost = ((tiles + n - 1) / n) * (ceil_div(chunks, s) + 3);
+    const int64_t cost = ((tiles + n - 1) / n) * (ceil_div(chunks, s) + kFixed);
     if (best == 0 || cost < best_cost) best = s, best_cost = cost;
   }
   if (best == 0) return fail(TP_ERR_UNSUPPORTED, "the kernel does not fit on this device");
