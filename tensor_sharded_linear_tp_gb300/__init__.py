@@ -520,16 +520,15 @@ def _need_ranks(name, ts, dtype, shape, dev, dense=False):
     return _pointers[len(ts)](*[t.data_ptr() for t in ts]), steps[0]
 
 
-def _alloc(stream, dev, dtype, shape, count=1):
+def _alloc(stream, device, dtype, shape, count=1):
     """`count` outputs for a call on `stream`, from that stream's memory."""
     if stream is not None:
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
         with torch.cuda.stream(stream):
-            return _alloc(None, dev, dtype, shape, count)
-    # (Scales are made as bytes: not every operation knows their type.)
-    out = torch.empty((count, *shape), dtype=_U8 if dtype is _E8M0 else dtype, device=f"cuda:{dev}").unbind(0)
-    return [t.view(_E8M0) for t in out] if dtype is _E8M0 else out
+            return _alloc(None, device, dtype, shape, count)
+    # (One by one: 1.5 us each on the host, where views of one allocation take 2 to 7.)
+    return [torch.empty(shape, dtype=dtype, device=device) for _ in range(count)]
 
 
 def _launch_stream(stream, dev) -> int:
@@ -569,9 +568,9 @@ def tp_quantize_fp8(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | None
     ldx = 0 if x.dtype is _BF16 and x.is_contiguous() else _need("x", x, _BF16, shape, dev)
     s_shape = (-(-rows // block_rows), _groups(cols))
     if q is None:
-        q, = _alloc(stream, dev, _E4M3, shape)
+        q, = _alloc(stream, x.device, _E4M3, shape)
     if scales is None:
-        scales, = _alloc(stream, dev, _E8M0, s_shape)
+        scales, = _alloc(stream, x.device, _E8M0, s_shape)
     ldq, lds = _need("q", q, _E4M3, shape, dev), _need("scales", scales, _E8M0, s_shape, dev)
     _check(lib.tp_quantize_fp8(x.data_ptr(), ldx, rows, cols, block_rows, q.data_ptr(), ldq, scales.data_ptr(), lds,
                                _launch_stream(stream, dev)))
@@ -609,13 +608,13 @@ def tp_linear_colwise_fp8(x: torch.Tensor, x_scales: torch.Tensor, w_shards: Seq
             bias = _pointers[p](*[0 if b is None else b.data_ptr() for b in bias_shards])
     n = N // 2 if act == "swiglu" else N
     if y_shards is None:
-        y_shards = _alloc(stream, dev, _E4M3 if fp8 else _BF16, (T, n), p)
+        y_shards = _alloc(stream, x.device, _E4M3 if fp8 else _BF16, (T, n), p)
     y, ldy = _need_ranks("y_shards", y_shards, _E4M3 if fp8 else _BF16, (T, n), dev)
     ys, ld_ys = None, 0
     if fp8:
         s_shape = (T, _groups(n))
         if y_scales is None:
-            y_scales = _alloc(stream, dev, _E8M0, s_shape, p)
+            y_scales = _alloc(stream, x.device, _E8M0, s_shape, p)
         ys, ld_ys = _need_ranks("y_scales", y_scales, _E8M0, s_shape, dev)
     _check(lib.tp_linear_colwise_fp8(x.data_ptr(), ldx, x_scales.data_ptr(), ld_xs, w, ws, bias, ACTS[act], p, T, K, N,
                                      y, ldy, ys, ld_ys, _launch_stream(stream, dev)))
@@ -639,7 +638,7 @@ def tp_linear_rowwise_fp8(x_shards: Sequence[torch.Tensor], x_scales: Sequence[t
     if bias is not None:
         _need("bias", bias, _BF16, (N,), dev)
     if out is None:
-        out, = _alloc(stream, dev, _BF16, (T, N))
+        out, = _alloc(stream, x_shards[0].device, _BF16, (T, N))
     ldo = _need("out", out, _BF16, (T, N), dev)
     _check(lib.tp_linear_rowwise_fp8(x, ldx, xs, ld_xs, w, ws, None if bias is None else bias.data_ptr(), p, T, K, N,
                                      out.data_ptr(), ldo, _launch_stream(stream, dev)))
@@ -693,18 +692,18 @@ def tp_residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, norm: str =
     if y is not None:
         y_at, ldy = y.data_ptr(), _need("y", y, _BF16, shape, dev)
         if h is None:
-            h, = _alloc(stream, dev, _BF16, shape)
+            h, = _alloc(stream, x.device, _BF16, shape)
     h_at, ldh = (0, 0) if h is None else (h.data_ptr(), _need("h", h, _BF16, shape, dev))
     u_at, ldu, s_at, ld_us = 0, 0, 0, 0
     if out is not None:
         u_type = _E4M3 if fp8 else _BF16
         if u is None:
-            u, = _alloc(stream, dev, u_type, shape)
+            u, = _alloc(stream, x.device, u_type, shape)
         u_at, ldu = u.data_ptr(), _need("u", u, u_type, shape, dev)
         if fp8:
             s_shape = (T, _groups(D))
             if u_scales is None:
-                u_scales, = _alloc(stream, dev, _E8M0, s_shape)
+                u_scales, = _alloc(stream, x.device, _E8M0, s_shape)
             s_at, ld_us = u_scales.data_ptr(), _need("u_scales", u_scales, _E8M0, s_shape, dev)
     ld_mod, mod_rows = mod or (0, 0)
     if mod and rows_per_mod is None:
