@@ -560,8 +560,8 @@ typedef enum { TP_NORM_NONE = 0, TP_NORM_RMS = 1, TP_NORM_LAYER = 2 } tp_norm;
  * Row strides of 0 mean dense rows.
  * Errors: TP_ERR_INVALID_ARG for sizes, strides and combinations outside the
  * above (and mod_rows * rows_per_mod < T); TP_ERR_ALIGNMENT unless D and every
- * row stride are multiples of 8 (D and ldu of 16 with u_scales) and every
- * pointer but u_scales is 16-byte aligned; TP_ERR_UNSUPPORTED above
+ * row stride but ld_u_scales are multiples of 8 (D and ldu of 16 with u_scales)
+ * and every pointer but u_scales is 16-byte aligned; TP_ERR_UNSUPPORTED above
  * TP_NORM_MAX_D.  T == 0 or D == 0 enqueues nothing and returns TP_OK.
  */
 typedef struct {

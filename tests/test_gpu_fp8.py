@@ -669,6 +669,46 @@ def test_calls_on_several_streams_at_once():
             assert torch.equal(w[6], g[6]) and torch.equal(w[4], g[4])
 
 
+def test_calls_from_several_threads():
+    import threading
+    args = [sharded_block(T, 512, 1024, 2, T) for T in (3, 70, 520)]
+    want = [forward(*a) for a in args]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(args), []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(20):
+                got[i] = forward(*args[i], stream=s)
+            s.synchronize()
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(args))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert torch.equal(w[6], g[6]) and torch.equal(w[4], g[4])
+
+
+@pytest.mark.parametrize("T", [5, 1300])
+def test_one_tensor_for_several_ranks(T):
+    """The same operands as every rank's: each colwise output alike, the rowwise sum p times one product."""
+    rng = np.random.default_rng(32)
+    x, sx, xv = integers(rng, T, 256, 1)
+    w, sw, wv = integers(rng, 2064, 256, 128)
+    ys = tp.tp_linear_colwise_fp8(x, sx, [w] * 3, [sw] * 3)
+    for y in ys:
+        np.testing.assert_array_equal(f64(y), bf16_round(xv @ wv.T))
+    z = tp.tp_linear_rowwise_fp8([x] * 4, [sx] * 4, [w] * 4, [sw] * 4)
+    np.testing.assert_array_equal(f64(z), bf16_round(4 * (xv @ wv.T)))
+
+
 def test_offsets_past_32_bits():
     """Rows whose bytes start beyond 4 GiB: a long quantised activation, outputs and inputs with a huge row stride."""
     rng = np.random.default_rng(30)
