@@ -153,7 +153,7 @@ __device__ __forceinline__ void store_async(uint32_t cluster_addr, uint32_t v, u
                : "memory");
 }
 
-// Cluster barrier that orders no memory (what has been read is in registers).
+// Cluster barrier that orders no memory: for threads that have used all they read from other CTAs.
 __device__ __forceinline__ void cluster_sync_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -536,9 +536,15 @@ __global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2
       constexpr int U = decltype(several)::value;      // tokens t, t + kWarps, ...
       constexpr int kFrom = decltype(sources)::value;  // at least `splits`
       float v[U][C::W_TILES][4];
-      auto at = [&](int j, int a, int s) {  // a token past the share: the first one's, not stored
-        const int tj = t + j * kWarps < t_end ? t + j * kWarps : t;
-        return ptx::mapa_shared(local + static_cast<uint32_t>(a * TN + tj) * (BM * 4), static_cast<uint32_t>(s));
+      // What is not stored (a token past the share, a column past the output) is read from this CTA's own
+      // partial tile, the share's first token in place of one past it.  A store waits for its reads, so
+      // that none is on its way to another CTA when this one comes to the last barrier, behind which
+      // the other's shared memory may be gone.
+      auto at = [&](int j, int a, int s) {
+        const bool inside = t + j * kWarps < t_end;
+        const int tj = inside ? t + j * kWarps : t;
+        return ptx::mapa_shared(local + static_cast<uint32_t>(a * TN + tj) * (BM * 4),
+                                static_cast<uint32_t>(inside && on ? s : part));
       };
 #pragma unroll
       for (int j = 0; j < U; ++j)
