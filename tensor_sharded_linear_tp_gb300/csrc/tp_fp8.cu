@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2
   // kernel's CTAs be scheduled: CTAs of two kernels of a stream on one SM could otherwise wait for
   // each other's.
   pdl_wait();
+  __syncwarp();  // (here and below: converged for the instructions that a whole warp has to run together)
   if (warp == 0) {
     ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), C::TMEM_COLS);
     ptx::tmem_relinquish();
@@ -496,6 +497,7 @@ __global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2
     if (!gave_up) {
       // Every MMA is done, so every copy has landed and the ring is free: it takes the partial
       // tile as [W tile][token][128 weight rows].
+      __syncwarp();
       ptx::tc_fence_after();
       float* partial = reinterpret_cast<float*>(base);
 #pragma unroll
@@ -611,6 +613,7 @@ __global__ void __launch_bounds__(kTokensThreads, TokensCfg<TN, kGlu>::SMALL ? 2
     else
       join_all(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
   }
+  __syncwarp();            // the stores above are some lanes' only
   cluster_sync_relaxed();  // no CTA's shared memory goes away while another reads it
   if (warp == 0) {
     ptx::tc_fence_after();
@@ -732,6 +735,7 @@ __device__ __forceinline__ void epilogue_tile(const Fp8Params& p, int g, int acc
   ptx::tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive_cluster_relaxed(tempty);
+  __syncwarp();
 
   const bool biased = p.bias[g] != nullptr, fp8 = p.out_scales[g] != nullptr;
   const int rows = p.T - row0;
@@ -828,6 +832,7 @@ __device__ __forceinline__ void epilogue_tile(const Fp8Params& p, int g, int acc
     }
     store_rows<8>(static_cast<uint8_t*>(p.out[g]) + row0 * p.ldo + col0, p.ldo, staging, rows, p.n_out - col0, lane);
     if (lane < rows) p.out_scales[g][(row0 + lane) * p.ld_os + col0 / kFp8Group] = static_cast<uint8_t>(byte);
+    __syncwarp();
   }
 }
 
@@ -870,6 +875,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
+  __syncwarp();  // (here and below: converged for the instructions that a whole warp has to run together)
   if (warp == 0) {
     ptx::tmem_alloc_pair(ptx::smem_addr(&ctl->tmem_base), 512);
     ptx::tmem_relinquish_pair();
@@ -1050,6 +1056,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       if (!__all_sync(0xffffffffu, wait_bounded<true>(ptx::smem_addr(&ctl->tfull[tile & 1u]), (tile >> 1) & 1u,
                                                       abort_flag, p.status)))
         break;
+      __syncwarp();
       ptx::tc_fence_after();
       const int row0 = mt * PM + static_cast<int>(cta) * BM + q * 32;
       const int acc = static_cast<int>(tile & 1u);
