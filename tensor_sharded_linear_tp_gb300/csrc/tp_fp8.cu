@@ -145,14 +145,6 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// One word to shared memory of another CTA of the cluster; its four bytes complete on a barrier
-// there, which orders what this thread knew to be done before.
-__device__ __forceinline__ void store_async(uint32_t cluster_addr, uint32_t v, uint32_t cluster_bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr), "r"(v),
-               "r"(cluster_bar)
-               : "memory");
-}
-
 // Cluster barrier that orders no memory: for threads that have used all they read from other CTAs.
 __device__ __forceinline__ void cluster_sync_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
@@ -640,7 +632,6 @@ struct alignas(8) PromptCtrl {
   uint64_t full[kPromptStages], empty[kPromptStages];
   uint64_t sf_full[kSfBufs], sf_empty[kSfBufs];
   uint64_t sf_peer[kSfBufs];  // the leader's: the other CTA's words are in its shared memory
-  uint32_t peer_note[kSfBufs];  // what the other CTA stores to say so
   uint64_t tfull[2], tempty;
   uint64_t drain;
   uint32_t tmem_base;
@@ -977,7 +968,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
         for (int seg = 0; seg < p.n_segs && ok; ++seg) {
           for (int left = p.k_groups; left > 0; left -= kChunk, ++chunk) {
             const uint32_t buf = chunk % kSfBufs;
-            if (issuer) ptx::mbar_arrive_expect_tx(sf_peer0 + 8 * buf, 4);
             if (!wait(sf_full0 + 8 * buf, (chunk / kSfBufs) & 1u) ||
                 !__all_sync(0xffffffffu, wait_bounded<true>(sf_peer0 + 8 * buf, (chunk / kSfBufs) & 1u, abort_flag,
                                                             p.status))) {
@@ -1019,11 +1009,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       if (issuer) ptx::umma_commit_pair(ptx::smem_addr(&ctl->drain), pair_mask);
       wait_bounded<true>(ptx::smem_addr(&ctl->drain), 0, abort_flag, p.status, true);
     } else if (lane == 0) {
-      // The peer tells the leader when its own scale words are there, by an asynchronous store: an
-      // arrival with release at cluster scope, from here or from the threads that store the words,
-      // takes 0.7 to 1.5 us, longer than a chunk's MMAs (down of 256 tokens 63 -> 45 us).
+      // The peer tells the leader when its own scale words are there.  The threads that store them
+      // release them to this lane in their own CTA, and this lane, which has seen that, releases
+      // them at cluster scope.  (From the threads themselves such a release first waits for their loads of
+      // the next words, 1.5 us, longer than a chunk's MMAs: down of 256 tokens 63 us, by way of this
+      // lane, which loads nothing, 47.  An asynchronous store whose bytes complete on the leader's
+      // barrier took 45, but releases no more than its own word.)
       const uint32_t to = ptx::mapa_shared(ptx::smem_addr(&ctl->sf_peer[0]), leader);
-      const uint32_t note = ptx::mapa_shared(ptx::smem_addr(&ctl->peer_note[0]), leader);
       const int tile_chunks = p.n_segs * ((p.k_groups + kChunk - 1) / kChunk);
       uint32_t buf = 0, phase = 0;
       bool ok = true;
@@ -1033,7 +1025,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
             ok = false;
             break;
           }
-          store_async(note + 4 * buf, 1, to + 8 * buf);
+          ptx::mbar_arrive_cluster(to + 8 * buf);
           if (++buf == kSfBufs) buf = 0, phase ^= 1u;
         }
       }
