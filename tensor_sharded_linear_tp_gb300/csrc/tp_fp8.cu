@@ -619,14 +619,15 @@ constexpr int PN = 256;                              // accumulator columns (wei
 constexpr int kPromptStages = 6;
 constexpr uint32_t kPromptStage = 2 * kBoxA;         // a CTA's 128 tokens and its 128 weight rows
 constexpr uint32_t kShared = 32;                     // columns the two accumulators share
-constexpr uint32_t kPromptSf = 2 * PN - kShared;     // scale words: two buffers of 16 columns (X 4, W 8)
+constexpr uint32_t kPromptSf = 2 * PN - kShared;     // scale words: buffers of 16 columns (X 4, W 8)
+constexpr uint32_t kSfTmem = 2;                      // of them, chunks that are in tensor memory at once
 constexpr uint32_t kStagingWarp = 32 * 128;          // epilogue staging: 32 rows a warp, 128 codes or 32 bf16 each
 constexpr uint32_t kPromptSfBytes = 3 * kSfRows;     // one chunk's words: X, W rows 0..127, W rows 128..255
 constexpr int kPromptThreads = 320;                  // producer, MMA issuer, 4 epilogue and 4 scale warps
 constexpr uint32_t kPromptBias = PN * 4;             // a tile's bias, in each epilogue warp's own copy
 constexpr size_t kPromptSmem =
     1024 + kPromptStages * kPromptStage + 4 * kStagingWarp + kSfBufs * kPromptSfBytes + 4 * kPromptBias;
-static_assert(kPromptSf + 32 <= 512, "accumulators and scale words fill tensor memory");
+static_assert(kPromptSf + kSfTmem * 16 <= 512 && kSfTmem <= kSfBufs, "accumulators and scale words fill tensor memory");
 
 struct alignas(8) PromptCtrl {
   uint64_t full[kPromptStages], empty[kPromptStages];
@@ -974,7 +975,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
               ok = false;
               break;
             }
-            const uint32_t sf = tmem + kPromptSf + (chunk & 1u) * 16;
+            // Copies are in order with the MMAs behind them, but nothing orders them with those before: the
+            // chunk whose words these replace has to be done (one chunk's MMAs are queued meanwhile).
+            if (chunk >= kSfTmem &&
+                !wait(sf_empty0 + 8 * ((chunk - kSfTmem) % kSfBufs), ((chunk - kSfTmem) / kSfBufs) & 1u)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t sf = tmem + kPromptSf + chunk % kSfTmem * 16;
             if (issuer)
 #pragma unroll
               for (int a = 0; a < 3; ++a)
