@@ -926,8 +926,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
         }
       }
       // Every copy lands before the CTAs can exit; the leader's barriers count both CTAs' copies.
+      const uint32_t first = it > kPromptStages ? it - kPromptStages : 0;
       if (cta == 0) {
-        const uint32_t first = it > kPromptStages ? it - kPromptStages : 0;
         for (uint32_t j = first; j < it; ++j)
           wait_bounded(ptx::smem_addr(&ctl->full[j % kPromptStages]), (j / kPromptStages) & 1u, abort_flag, p.status,
                        true);
@@ -937,6 +937,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
         while (ptx::globaltimer_ns() - t0 < 100000ull) {
         }
       }
+      // And so does every arrival that hands a stage back (from another CTA's MMA thread, kQuad: from both
+      // pairs'): none is on its way here when this CTA's shared memory goes.
+      for (uint32_t j = first; j < it; ++j)
+        if (!wait_bounded<true>(empty0 + 8 * (j % kPromptStages), (j / kPromptStages) & 1u, abort_flag, p.status)) break;
     }
   } else if (warp == 1) {
     if (cta == 0) {
@@ -1083,7 +1087,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       tile_of(t, g, mt, nt);
       load(at);
     }
-    for (uint32_t chunk = 0; t < total; ++chunk) {
+    uint32_t chunk = 0;
+    bool ok = true;
+    for (; t < total; ++chunk) {
       const uint32_t buf = chunk % kSfBufs;
       const uint32_t x = x_next, w0 = w0_next, w1 = w1_next;
       at.next(p.k_groups);
@@ -1094,8 +1100,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       }
       if (t < total) load(at);
       if (!__all_sync(0xffffffffu, wait_bounded<true>(ptx::smem_addr(&ctl->sf_empty[buf]),
-                                                      ((chunk / kSfBufs) & 1u) ^ 1u, abort_flag, p.status)))
+                                                      ((chunk / kSfBufs) & 1u) ^ 1u, abort_flag, p.status))) {
+        ok = false;
         break;
+      }
       const uint32_t words = sf_base + buf * kPromptSfBytes;
       store_word(words, row, x);
       store_word(words + kSfRows, row, w0);
@@ -1103,6 +1111,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(ptx::smem_addr(&ctl->sf_full[buf]));
     }
+    // The arrivals that hand the last buffers back, as the stages' above.
+    for (uint32_t j = chunk > kSfBufs ? chunk - kSfBufs : 0; j < chunk && ok; ++j)
+      ok = wait_bounded<true>(ptx::smem_addr(&ctl->sf_empty[j % kSfBufs]), (j / kSfBufs) & 1u, abort_flag, p.status);
   }
   __syncwarp();
   ptx::tc_fence_before();
