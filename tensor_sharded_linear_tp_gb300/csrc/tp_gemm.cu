@@ -883,8 +883,8 @@ __global__ void __launch_bounds__(threads_of(kEpi), 1) tp_gemm_kernel(const __gr
       }
       // Let every copy this thread issued land before the CTA can exit.  In a
       // pair, the leader's full barriers count both CTAs' copies.
+      const uint32_t first = it > C::STAGES ? it - C::STAGES : 0;
       if (!kPair || cta == 0) {
-        const uint32_t first = it > C::STAGES ? it - C::STAGES : 0;
         for (uint32_t j = first; j < it; ++j)
           wait_bounded(ptx::smem_addr(&ctl->full[j % C::STAGES]), (j / C::STAGES) & 1u, abort_flag, p.status, true);
       } else if (*abort_flag) {
@@ -892,6 +892,15 @@ __global__ void __launch_bounds__(threads_of(kEpi), 1) tp_gemm_kernel(const __gr
         const uint64_t t0 = ptx::globaltimer_ns();
         while (ptx::globaltimer_ns() - t0 < 100000ull) {
         }
+      }
+      // And so does every arrival that hands a box back, from another CTA's MMA thread (kQuad: from
+      // both pairs'): none is on its way here when this CTA's shared memory goes.
+      if constexpr (kPair) {
+        constexpr uint32_t boxes = C::BK / KBOX;
+        bool back = true;
+        for (uint32_t j = first * boxes; j < it * boxes && back; ++j)
+          back = wait_bounded<true>(ptx::smem_addr(&ctl->empty[j % (C::STAGES * boxes)]),
+                                    (j / (C::STAGES * boxes)) & 1u, abort_flag, p.status, false);
       }
     }
   } else if (warp == 1) {
