@@ -654,10 +654,10 @@ def tp_residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, norm: str =
                      u: torch.Tensor | None = None, u_scales: torch.Tensor | None = None, stream=None):
     """h = alpha x + gate post_norm(y); u = norm(h) (1 + scale) + shift.  Returns (h, u, u_scales).
 
-    gate, scale and shift are [D] vectors or [mod_rows, D] tables (row t uses table row
-    t // rows_per_mod; default: one row for every row of x).  out: "bf16" or "fp8" (codes and
-    scales), or None for h alone; what a call does not compute is returned as None.  Without a
-    branch y there is no h."""
+    gate, scale and shift are [D] vectors, used for every row of x, or [mod_rows, D] tables: row t
+    uses table row t // rows_per_mod, which has to be given with more than one.  out: "bf16" or
+    "fp8" (codes and scales), or None for h alone; what a call does not compute is returned as
+    None.  Without a branch y there is no h."""
     dev = _device_of("x", x)
     if out not in ("bf16", "fp8", None):
         raise ValueError(f'out must be "bf16" or "fp8", got {out!r}')
@@ -688,6 +688,8 @@ def tp_residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, norm: str =
                 elif mod != (step, rows):
                     raise ValueError("gate, scale and shift must have the same rows and row stride")
                 tables[i] = t.data_ptr()
+        if rows_per_mod is None and mod[1] > 1:
+            raise ValueError(f"tables of {mod[1]} rows need rows_per_mod, how many rows of x use each of them")
     y_at, ldy = 0, 0
     if y is not None:
         y_at, ldy = y.data_ptr(), _need("y", y, _BF16, shape, dev)

@@ -183,6 +183,23 @@ def test_binding_refuses_host_tensors():
         tp.tp_residual_norm(x, x)
 
 
+class _NoCalls:
+    """In the library's place where every call has to be refused before it."""
+
+    def __getattr__(self, name):
+        pytest.fail(f"{name} was called")
+
+
+@pytest.mark.parametrize("tables", [dict(gate=2), dict(scale=2), dict(scale=3, shift=3)], ids=str)
+def test_tables_of_several_rows_need_rows_per_mod(monkeypatch, tables):
+    """Without it every row of x would silently be modulated as the first sample's."""
+    monkeypatch.setattr(tp, "_device_of", lambda name, t: t.get_device())
+    monkeypatch.setattr(tp, "lib", _NoCalls())
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="rows_per_mod"):
+        tp.tp_residual_norm(x, x, **{k: torch.zeros(n, 256, dtype=torch.bfloat16) for k, n in tables.items()})
+
+
 def test_struct_mirrors_header():
     """The field order of the binding's structure is the header's."""
     import os
