@@ -493,7 +493,7 @@ TP_API tp_status tp_quantize_fp8(const void* x, int64_t ldx, int64_t rows, int64
  * inside; with few tokens K may be split over up to 8 accumulators that are
  * added in fp32 in K order.  The same call gives the same bits every time.
  * Alignment (TP_ERR_ALIGNMENT): K and ldx % 16 == 0; N_out and ldy % 8 == 0
- * (% 16 with y_scales); x, w_shards, y_shards 16-byte aligned.
+ * (% 16 with y_scales); x, w_shards, y_shards 16-byte aligned, bias_shards 2-byte.
  * T == 0 or N_r == 0 enqueues nothing and returns TP_OK.  No output may overlap an input.
  */
 TP_API tp_status tp_linear_colwise_fp8(const void* x, int64_t ldx, const void* x_scales, int64_t ld_xs,
@@ -516,7 +516,7 @@ TP_API tp_status tp_linear_colwise_fp8(const void* x, int64_t ldx, const void* x
  * bias:   NULL or device bf16 [N]; added once, after the sum.
  * out:    device bf16 [T, N], row stride ldo elements (0 = N).
  * Alignment (TP_ERR_ALIGNMENT): K_r and ldx % 16 == 0, N and ldo % 8 == 0,
- * x_shards, w_shards and out 16-byte aligned.  Accumulation as tp_linear_colwise_fp8.
+ * x_shards, w_shards and out 16-byte aligned, bias 2-byte.  Accumulation as tp_linear_colwise_fp8.
  * T == 0 or N == 0 enqueues nothing and returns TP_OK.  No output may overlap an input.
  */
 TP_API tp_status tp_linear_rowwise_fp8(const void* const* x_shards, int64_t ldx, const void* const* x_scales,

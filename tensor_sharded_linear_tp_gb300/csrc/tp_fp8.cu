@@ -1410,6 +1410,13 @@ tp_status check_fp8(const Fp8Call& c) {
   return TP_OK;
 }
 
+// bf16 elements one at a time, so that a bias may start at any of them (but not inside one).
+tp_status check_bias(const void* bias, int r) {
+  if ((reinterpret_cast<uintptr_t>(bias) & 1u) != 0)
+    return fail(TP_ERR_ALIGNMENT, "bias %d is not 2-byte aligned", r);
+  return TP_OK;
+}
+
 tp_status check_sizes(int tp_degree, int64_t T, int64_t K, int64_t N) {
   if (tp_degree < 1) return fail(TP_ERR_INVALID_ARG, "tp_degree must be >= 1, got %d", tp_degree);
   if (tp_degree > TP_MAX_DEGREE)
@@ -1468,6 +1475,8 @@ tp_status tp_linear_colwise_fp8(const void* x, int64_t ldx, const void* x_scales
       p.out[r] = y_shards[r];
       p.out_scales[r] = y_scales != nullptr ? static_cast<uint8_t*>(y_scales[r]) : nullptr;
       p.bias[r] = bias_shards != nullptr ? static_cast<const __nv_bfloat16*>(bias_shards[r]) : nullptr;
+      st = check_bias(p.bias[r], r);
+      if (st != TP_OK) return st;
     }
     p.act = act;
     p.n_groups = tp_degree;
@@ -1505,6 +1514,8 @@ tp_status tp_linear_rowwise_fp8(const void* const* x_shards, int64_t ldx, const 
     if (N % 8 != 0 || ldo % 8 != 0)
       return fail(TP_ERR_ALIGNMENT, "N (%lld) and ldo (%lld) must be multiples of 8", (long long)N, (long long)ldo);
     if (!aligned16(out)) return fail(TP_ERR_ALIGNMENT, "out is not 16-byte aligned");
+    st = check_bias(bias, 0);
+    if (st != TP_OK) return st;
     Fp8Params p{};
     p.out[0] = out;
     p.bias[0] = static_cast<const __nv_bfloat16*>(bias);

@@ -134,6 +134,16 @@ def test_rowwise_refusals(kw, want):
     assert _row(**kw) == want
 
 
+def test_bias_inside_an_element_is_refused():
+    lib, F16, S = tp.lib, FAKE, FAKE_SCALE
+    two = lambda v: _ptrs(v, v)  # noqa: E731
+    for bias in (_ptrs(FAKE + 1, 0), _ptrs(None, FAKE + 3)):
+        assert _name(lib.tp_linear_colwise_fp8(F16, 0, S, 0, two(F16), two(S), bias, 0, 2, 4, 256, 256, two(F16), 0, None,
+                                               0, None)) == "TP_ERR_ALIGNMENT"
+    assert _name(lib.tp_linear_rowwise_fp8(two(F16), 0, two(S), 0, two(F16), two(S), FAKE + 1, 2, 4, 256, 256, F16, 0,
+                                           None)) == "TP_ERR_ALIGNMENT"
+
+
 def _norm(**kw):
     a = tp.ResidualNormArgs()
     base = dict(T=4, D=256, x=FAKE, y=FAKE, h=FAKE, u=FAKE, norm=1, alpha=1.0, eps=1e-6)
