@@ -482,6 +482,66 @@ def test_residual_norm(T, D, norm, post, out):
     check_bf16(u, uv, eu, "u") if out == "bf16" else check_fp8(u, su, uv, eu, "u")
 
 
+# More rows than SMs: the kernels that hold a row in a warp or in 256 to 1024 threads of one to four
+# vectors, whose rows ask for rows ahead of them (from some 300 rows on with 256 threads, 2500 with a
+# warp a row), rows that fill their last vectors and rows that do not, tables whose rows are no whole
+# fraction of the tokens.
+NORM_MANY = [(2600, 256), (2500, 520), (161, 1024), (400, 1536), (400, 2064), (400, 2560), (310, 6144), (313, 6160),
+             (400, 8192), (200, 8208), (161, 12288), (160, 16384), (160, 16400), (200, 32768)]
+
+
+def norm_case(T, D, norm, post, out, mod_rows):
+    """One call with every vector and table, held to norm_bounds."""
+    rng = np.random.default_rng(T * 100003 + D)
+    per = -(-T // mod_rows)
+    x, y = to_bf16(rng.normal(0.5, 2, (T, D))), to_bf16(rng.normal(-0.2, 0.6, (T, D)))
+    vec = lambda c: to_bf16(rng.normal(c, 0.2, D))  # noqa: E731
+    table = to_bf16(rng.normal(0, 0.4, (mod_rows, 3 * D)))
+    t = dict(weight=vec(1), bias=vec(0)) if norm != "none" else {}
+    if post != "none":
+        t.update(post_weight=vec(1), post_bias=vec(0))
+    t.update(gate=table[:, :D], scale=table[:, D:2 * D], shift=table[:, 2 * D:])
+    h, u, su = tp.tp_residual_norm(x, y, norm=norm, post_norm=post, alpha=0.75, eps=1e-5, rows_per_mod=per, out=out, **t)
+    kw = dict(norm=norm, post_norm=post, alpha=0.75, eps=1e-5, rows_per_mod=per, **{k: f64(v) for k, v in t.items()})
+    hv, eh, uv, eu = norm_bounds(f64(x), f64(y), kw, (D + 16) * 2.0 ** -24)
+    check_bf16(h, hv, eh, "h")
+    check_bf16(u, uv, eu, "u") if out == "bf16" else check_fp8(u, su, uv, eu, "u")
+
+
+@pytest.mark.parametrize("T, D", NORM_MANY, ids=lambda v: str(v))
+@pytest.mark.parametrize("norm, post", [("rms", "none"), ("layer", "rms"), ("none", "layer")])
+@pytest.mark.parametrize("out", ["bf16", "fp8"])
+def test_residual_norm_many_rows(T, D, norm, post, out):
+    norm_case(T, D + 8 if out == "fp8" and D % 16 else D, norm, post, out, 3)
+
+
+def test_residual_norm_of_a_prompt():
+    norm_case(4608, 6144, "layer", "rms", "fp8", 5)
+
+
+@pytest.mark.parametrize("T, D", [(2600, 264), (400, 2064), (400, 6144), (200, 16384)], ids=lambda v: str(v))
+def test_residual_norm_forms_many_rows(T, D):
+    """Without a branch, without u, in place."""
+    rng = np.random.default_rng(T + D)
+    x, y = to_bf16(rng.normal(0.3, 1.5, (T, D))), to_bf16(rng.normal(-0.1, 0.8, (T, D)))
+    rel = (D + 16) * 2.0 ** -24
+    base = dict(alpha=1.0, eps=1e-6, rows_per_mod=T, post_norm="none", norm="none")
+    for norm in ("layer", "rms"):
+        h, u, su = tp.tp_residual_norm(x, norm=norm)
+        assert h is None and su is None
+        _, _, uv, eu = norm_bounds(f64(x), None, {**base, "norm": norm}, rel)
+        check_bf16(u, uv, eu, norm)
+    hv, eh, _, _ = norm_bounds(f64(x), f64(y), {**base, "post_norm": "layer"}, rel)
+    h, u, su = tp.tp_residual_norm(x, y, post_norm="layer", out=None)
+    assert u is None and su is None
+    check_bf16(h, hv, eh, "h")
+    inplace = x.clone()
+    h2, u2, _ = tp.tp_residual_norm(inplace, y, post_norm="layer", norm="rms", h=inplace)
+    assert h2 is inplace and torch.equal(inplace, h)
+    _, _, uv, eu = norm_bounds(f64(x), f64(y), {**base, "post_norm": "layer", "norm": "rms"}, rel)
+    check_bf16(u2, uv, eu, "u beside an h in place")
+
+
 def test_residual_norm_forms():
     """Without a branch, without an input for the next block, in place, and vectors as tables."""
     rng = np.random.default_rng(9)
