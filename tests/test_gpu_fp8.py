@@ -315,6 +315,29 @@ def test_views_and_gathered_output(T):
     assert np.all(got[T:] == -7) and np.all(got[:, p * N:] == -7)
 
 
+@pytest.mark.parametrize("T", [1, 5, 70, 300, 1300])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_quantised_outputs_in_views(T, act):
+    """Codes and scales written through row strides, ranks side by side: the dense call's bytes, and no others."""
+    rng = np.random.default_rng(T)
+    p, K, N = 2, 272, 272 if T < 1000 else 2064
+    g = -(-N // 128)
+    x, sx, _ = quantized(rng, T, K, 1)
+    ws = [quantized(rng, 2 * N if act == "swiglu" else N, K, 128, 0.05) for _ in range(p)]
+    wt, st = [w[0] for w in ws], [w[1] for w in ws]
+    want, want_s = tp.tp_linear_colwise_fp8(x, sx, wt, st, act=act, out="fp8")
+    qb = torch.full((T + 3, p * N + 48), 0x55, dtype=torch.uint8, device=DEV)
+    sb = torch.full((T + 3, p * g + 5), 0x55, dtype=torch.uint8, device=DEV)
+    at = [(slice(1, T + 1), slice(16 + r * N, 16 + (r + 1) * N)) for r in range(p)]
+    at_s = [(slice(1, T + 1), slice(3 + r * g, 3 + (r + 1) * g)) for r in range(p)]
+    tp.tp_linear_colwise_fp8(x, sx, wt, st, act=act, out="fp8", y_shards=[qb[a].view(E4M3) for a in at],
+                             y_scales=[sb[a].view(E8M0) for a in at_s])
+    for r in range(p):
+        assert torch.equal(qb[at[r]], want[r].view(torch.uint8)) and torch.equal(sb[at_s[r]], want_s[r].view(torch.uint8))
+        qb[at[r]], sb[at_s[r]] = 0x55, 0x55
+    assert bool((qb == 0x55).all()) and bool((sb == 0x55).all())
+
+
 # ----------------------------------------------------------------------------- projections, in general
 
 @pytest.mark.parametrize("T", [1, 9, 40, 100, 200, 333])
@@ -799,6 +822,29 @@ def test_offsets_past_32_bits():
         assert torch.equal(h, (2 * z.float()).to(BF16))
         assert int((wide[:, 64 + N:8192] != -7).count_nonzero()) == 0
         del wide, z, h
+
+
+@pytest.mark.parametrize("T", [40, 2600])
+def test_codes_past_four_gib(T):
+    """Codes, scales and quantised outputs whose last rows start beyond 2^32 bytes, through both projection kernels."""
+    rng = np.random.default_rng(T)
+    K, N = 256, 2064
+    step = (1 << 32) // (T - 4) // 64 * 64 + 64              # the last three rows start past 2^32
+    assert (T - 3) * step > 1 << 32
+    wide = [torch.full((T, step), 0x55, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    q, s = wide[0][:, 32:32 + K].view(E4M3), wide[1][:, 3:5]
+    x = to_bf16(rng.normal(size=(T, K)))
+    tp.tp_quantize_fp8(x, q=q, scales=s)
+    q2, s2 = tp.tp_quantize_fp8(x)
+    assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2.view(torch.uint8))
+    w, sw, _ = quantized(rng, N, K, 128, 0.05)
+    y, ys = wide[2][:, 16:16 + N].view(E4M3), wide[3][:, 5:5 + 17]
+    tp.tp_linear_colwise_fp8(q, s, [w], [sw], out="fp8", y_shards=[y], y_scales=[ys])
+    y2, ys2 = tp.tp_linear_colwise_fp8(q2, s2, [w], [sw], out="fp8")
+    assert torch.equal(y.view(torch.uint8), y2[0].view(torch.uint8)) and torch.equal(ys, ys2[0].view(torch.uint8))
+    wide[0][:, 32:32 + K], wide[1][:, 3:5], wide[2][:, 16:16 + N], wide[3][:, 5:5 + 17] = 0x55, 0x55, 0x55, 0x55
+    for b in wide:
+        assert int(b.min()) == int(b.max()) == 0x55
 
 
 def test_first_call_may_be_captured():
