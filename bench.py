@@ -1282,8 +1282,7 @@ def measure(wl, args, tp, torch, device, stream, peaks, flush=None, steps=None, 
             rec["launches_per_step"] = n
         if kind == "tensor":
             v = work / (ms * 1e-3) / 1e12
-            rec.update({"TFLOP/s": v, "frac_tensor": v / peaks["bf16_tflops"],
-                        "frac_tensor_sustained": v / peaks["bf16_tflops_sustained"]})
+            rec.update(tensor_record(label, v, peaks))
         else:
             v = work / (ms * 1e-3) / 1e9
             rec.update({"GB/s": v, "frac_hbm": v / peaks["hbm_gbs"]})
@@ -1325,16 +1324,28 @@ def measure(wl, args, tp, torch, device, stream, peaks, flush=None, steps=None, 
     return res
 
 
+def tensor_rate(label):
+    """The tensor core's rate for a phase, in units of its bf16 rate: twice it for 8-bit operands."""
+    return 2 if label.endswith("_fp8") else 1
+
+
+def tensor_record(label, v, peaks):
+    rate = tensor_rate(label)
+    return {"TFLOP/s": v, "frac_tensor": v / (rate * peaks["bf16_tflops"]),
+            "frac_tensor_sustained": v / (rate * peaks["bf16_tflops_sustained"])}
+
+
 def roofline_of(res, workload, peaks, sustained):
     """The roofline object for the dominant kernel of a measure() result."""
     label = res["dominant"]
     k = res["kernels"][label]
     if "TFLOP/s" in k:
         peak = peaks["bf16_tflops_sustained"] if sustained else peaks["bf16_tflops"]
-        if label.endswith("_fp8"):   # the tensor core's 8-bit rate is twice its bf16 rate
-            return {"bound": "tensor", "achieved": k["TFLOP/s"], "peak": 2 * peak, "unit": "TFLOP/s",
-                    "frac": k["TFLOP/s"] / (2 * peak), "kernel": f"fp8_prompt_kernel ({label})",
-                    "peak_source": "2 x " + peaks["source"] + (" sustained" if sustained else " burst"),
+        rate = tensor_rate(label)
+        if rate != 1:
+            return {"bound": "tensor", "achieved": k["TFLOP/s"], "peak": rate * peak, "unit": "TFLOP/s",
+                    "frac": k["TFLOP/s"] / (rate * peak), "kernel": f"fp8_prompt_kernel ({label})",
+                    "peak_source": f"{rate} x " + peaks["source"] + (" sustained" if sustained else " burst"),
                     "launch_ms": k["ms"], "traffic": None}
         return {"bound": "tensor", "achieved": k["TFLOP/s"], "peak": peak, "unit": "TFLOP/s",
                 "frac": k["TFLOP/s"] / peak, "frac_of_burst": k["TFLOP/s"] / peaks["bf16_tflops"],

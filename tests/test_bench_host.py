@@ -39,3 +39,15 @@ def test_reference_arm_other_ranks_exit_without_work():
     r = _bench(["--impl", "reference", "--steps", "3"], env={"WORLD_SIZE": "2", "RANK": "1"})
     assert r.returncode == 0
     assert r.stdout.strip() == ""
+
+
+def test_tensor_fractions_use_the_operands_rate():
+    """An 8-bit phase at the tensor core's full 8-bit rate is at 1 of it, not at 2 of the bf16 rate."""
+    sys.path.insert(0, ROOT)
+    import bench
+    peaks = {"bf16_tflops": 1000.0, "bf16_tflops_sustained": 900.0, "source": "test"}
+    for label, rate in (("colwise_swiglu_fp8", 2), ("rowwise_down_fp8", 2), ("colwise_swiglu", 1), ("attention", 1)):
+        rec = bench.tensor_record(label, rate * 1000.0, peaks)
+        assert rec == {"TFLOP/s": rate * 1000.0, "frac_tensor": 1.0, "frac_tensor_sustained": 1000.0 / 900.0}
+        res = {"dominant": label, "kernels": {label: {"ms": 1.0, **rec}}}
+        assert bench.roofline_of(res, "w", peaks, sustained=False)["frac"] == 1.0
