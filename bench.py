@@ -1066,6 +1066,40 @@ class Fp8StackWorkload:
                                  out=None if last else "fp8", u=None if last else self.u,
                                  u_scales=None if last else self.us, stream=stream)
 
+    def oracle_check(self, stream, n=8):
+        """The first block's steps on sampled tokens, each from the stored output of the one before, against
+        the float64 oracle: error over the output's rms.  A stored element is off by at most half a step of its
+        type (2^-8 of a bf16, 2^-4 of an e4m3 code); more in the rms is an error."""
+        from oracle import fp8_oracle as F
+        from oracle import tp_oracle as O
+        rows = tp_inputs.sample_rows(13, self.T, n)
+        at = self.torch.from_numpy(np.asarray(rows)).to(self.device)
+        byte = lambda t: t.view(self.torch.uint8).cpu().numpy()  # noqa: E731
+        bf16 = lambda t: O.bf16_to_f64(self.tp.bits_from_bf16(t[at]))  # noqa: E731
+        codes = lambda q, s: F.dequantize(byte(q.view(self.torch.uint8)[at]), byte(s.view(self.torch.uint8)[at]), 1)  # noqa: E731
+        weight = lambda q, s: F.dequantize(byte(q), byte(s), F.GROUP)  # noqa: E731
+        self.first_norm(stream), self.gate_up(0, stream), self.down(0, stream)
+        stream.synchronize()
+        x, u, y = bf16(self.x), codes(self.u, self.us), bf16(self.y)
+        hs = [codes(q, s) for q, s in zip(self.h, self.hs)]
+        self.norm(0, stream)
+        stream.synchronize()
+        out, u_next = bf16(self.stream[0]), codes(self.u, self.us)
+        gate = O.bf16_to_f64(self.tp.bits_from_bf16(self.gate))[None]
+        (gu, gus), (dn, dns) = self.shards[0]
+        want_out, want_next = F.residual_norm(x, y, norm="rms", post_norm="rms", gate=gate, rows_per_mod=n)
+        pairs = {"norm_first": (u, F.residual_norm(x, norm="rms")[1], 2.0 ** -4),
+                 "rowwise_down": (y, sum(h @ weight(q, s).T for h, q, s in zip(hs, dn, dns)), 2.0 ** -8),
+                 "residual": (out, want_out, 2.0 ** -8), "norm": (u_next, want_next, 2.0 ** -4)}
+        for r, (h, q, s) in enumerate(zip(hs, gu, gus)):
+            pairs[f"colwise_swiglu rank {r}"] = (h, F.colwise(u, weight(q, s), act="swiglu"), 2.0 ** -4)
+        errs = {}
+        for label, (got, want, bound) in pairs.items():
+            errs[label] = float(np.sqrt(np.mean((got - want) ** 2) / np.mean(want ** 2)))
+            if not errs[label] <= bound:
+                raise RuntimeError(f"{self.name}: {label} is off by {errs[label]:.3g} of its rms, bound {bound:.3g}")
+        return {"tokens": n, "rms_error_over_rms": errs}
+
     def phases(self):
         TH = self.T * self.H
         out = [("norm_first", self.first_norm, "hbm", 3.0 * TH)]
@@ -1454,6 +1488,8 @@ def run_ours(args):
     add_attention_issued(res, peaks)
     cpu = None if args.no_cpu_baseline or not hasattr(wl, "oracle_step") else generic_cpu_baseline(wl)
     cfg = wl.config()
+    if hasattr(wl, "oracle_check"):
+        cfg["oracle_check"] = wl.oracle_check(stream)
     cfg.update({"parallelism": f"tp{wl.p} simulated on one GPU", "l2": "flushed between steps "
                 "(256 MiB write, then 256 MiB read)", "sms": torch.cuda.get_device_properties(device).multi_processor_count})
     line = {"metric": METRIC, "value": res["value"], "unit": UNIT, "n_gpus": 1, "steps": args.steps,
