@@ -1322,14 +1322,15 @@ tp_status run_prompt(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   if (st != TP_OK) return st;
   if (pairs < 1) return fail(TP_ERR_UNSUPPORTED, "no CTA pair of the kernel fits on this device");
   // Clusters of two pairs, on n-adjacent tiles that share X, where the tiles pair up and the
-  // clusters' waves, each about 4 % shorter, take no longer than the pairs' (fewer clusters of
-  // four CTAs than pairs fit: 36 x 4 against 76 x 2).  Measured at 4608 tokens: gate/up 652 us
-  // against 663 (36 waves, 35 of pairs), down 345 against 357 (6 waves either way).
+  // clusters' waves, each about 3 % shorter, take no longer than the pairs' (fewer clusters of
+  // four CTAs than pairs fit: 36 x 4 against 76 x 2).  Measured in 3 s each at the power limit:
+  // gate/up of 4608 tokens 647 us against 655 (36 waves, 35 of pairs), down 338 against 343.5 (6
+  // waves either way), of 2048 tokens 158 against 161.5 (3 either way).
   const int64_t tiles = static_cast<int64_t>(p.n_groups) * p.n_tiles * p.t_tiles;
   bool quad = quads > 0 && p.n_tiles % 2 == 0;
   if (quad) {
     const int64_t waves_quad = (tiles / 2 + quads - 1) / quads, waves_pair = (tiles + pairs - 1) / pairs;
-    quad = waves_quad * 24 <= waves_pair * 25;
+    quad = waves_quad * 32 <= waves_pair * 33;
   }
   p.n_items = quad ? p.n_tiles / 2 : p.n_tiles;
   p.group_m = choose_group_m(p.t_tiles, c.T * c.K * p.n_segs);
