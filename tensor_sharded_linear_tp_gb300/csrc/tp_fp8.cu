@@ -1158,7 +1158,9 @@ tp_status set_maps(const Fp8Call& c, Fp8Params& p, int x_box, int w_box) {
   return TP_OK;
 }
 
-// Clusters of `size` CTAs of a kernel that can be resident at once (0: no such cluster on this device).
+// Clusters of `size` CTAs of a kernel that can be resident at once, as the runtime counts them (0: no such
+// cluster on this device).  It counts one CTA an SM for the small tokens kernels too, of which two fit:
+// 152 / 76 / 46 / 36 / 28 / 23 / 15 / 15 clusters of 1 to 8.
 template <typename Kernel>
 int resident_clusters(Kernel kernel, int size, int threads, size_t smem) {
   cudaLaunchConfig_t cfg{};
