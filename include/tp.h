@@ -461,7 +461,7 @@ TP_API tp_status tp_combine(tp_combine_mode mode, const void* const* partials, i
  *         (0 = dense).  Any alignment; 4-byte aligned rows are read faster by
  *         the projections.
  * Alignment (TP_ERR_ALIGNMENT): cols % 16 == 0, ldx % 8 == 0, ldq % 16 == 0,
- * x and q 16-byte aligned.  q and scales must not overlap x.
+ * x and q 16-byte aligned.  q and scales must overlap neither x nor each other.
  * rows == 0 or cols == 0 enqueues nothing and returns TP_OK.
  */
 TP_API tp_status tp_quantize_fp8(const void* x, int64_t ldx, int64_t rows, int64_t cols, int block_rows, void* q,
@@ -494,7 +494,8 @@ TP_API tp_status tp_quantize_fp8(const void* x, int64_t ldx, int64_t rows, int64
  * added in fp32 in K order.  The same call gives the same bits every time.
  * Alignment (TP_ERR_ALIGNMENT): K and ldx % 16 == 0; N_out and ldy % 8 == 0
  * (% 16 with y_scales); x, w_shards, y_shards 16-byte aligned, bias_shards 2-byte.
- * T == 0 or N_r == 0 enqueues nothing and returns TP_OK.  No output may overlap an input.
+ * T == 0 or N_r == 0 enqueues nothing and returns TP_OK.  No output may overlap an input
+ * or another output.
  */
 TP_API tp_status tp_linear_colwise_fp8(const void* x, int64_t ldx, const void* x_scales, int64_t ld_xs,
                                        const void* const* w_shards, const void* const* w_scales,
@@ -517,7 +518,8 @@ TP_API tp_status tp_linear_colwise_fp8(const void* x, int64_t ldx, const void* x
  * out:    device bf16 [T, N], row stride ldo elements (0 = N).
  * Alignment (TP_ERR_ALIGNMENT): K_r and ldx % 16 == 0, N and ldo % 8 == 0,
  * x_shards, w_shards and out 16-byte aligned, bias 2-byte.  Accumulation as tp_linear_colwise_fp8.
- * T == 0 or N == 0 enqueues nothing and returns TP_OK.  No output may overlap an input.
+ * T == 0 or N == 0 enqueues nothing and returns TP_OK.  No output may overlap an input
+ * or another output.
  */
 TP_API tp_status tp_linear_rowwise_fp8(const void* const* x_shards, int64_t ldx, const void* const* x_scales,
                                        int64_t ld_xs, const void* const* w_shards, const void* const* w_scales,
@@ -544,12 +546,15 @@ typedef enum { TP_NORM_NONE = 0, TP_NORM_RMS = 1, TP_NORM_LAYER = 2 } tp_norm;
  *     rms(v)   = v / sqrt(mean(v^2) + eps) * weight + bias
  *     layer(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias
  * (weight and bias optional), over the D elements of a row.  Everything is
- * fp32 until an output is stored; u is computed from the unrounded h.
+ * fp32 until an output is stored; u is computed from the unrounded h.  Squares
+ * are fp32 too: a row with values above about 1e19 norms to zeros (NaN where it
+ * holds an infinity), one below about 1e-19 as if its mean square were smaller.
  *
  * Without a branch (y NULL; h, gate and post_norm unset) u = norm(alpha * x) *
  * (1 + scale) + shift.  Without u (u NULL; norm, scale, shift and u_scales
  * unset) only h is written.  h may be x itself with the same row stride (the
- * residual updated in place); no other overlap of an output with an input.
+ * residual updated in place); no other overlap of an output with an input or
+ * another output.
  *
  * gate, scale and shift (each optional) are [mod_rows, D] tables with the row
  * stride ld_mod: row t of the call uses table row t / rows_per_mod.

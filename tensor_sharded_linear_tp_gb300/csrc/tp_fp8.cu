@@ -20,19 +20,21 @@
 // leaves its fp32 partial tile in its shared memory, and after a cluster barrier each CTA sums
 // its share of the tokens over the CTAs in K order through distributed shared memory, applies
 // bias and activation and stores (or quantises: a tile's 128 columns are one scale group).  One
-// token's Q/K/V, 4 x 4608 x 6144, takes 21.2 us (5.3 TB/s; 16.7 us at the measured copy rate, the
-// rest is a launch's start and join), gate/up of 23 tokens, 3 x 12288 x 6144, 39.4 us (5.8 TB/s).
-// With 128 tokens a tile it is bound by the operands' way from L2: 144 CTAs take 32 KB each for a
-// scale group, in 230 ns (20 TB/s; without three quarters of the MMAs a launch is 10 % shorter).
+// token's Q/K/V, 4 x 4608 x 6144, takes 21.4 us (5.3 TB/s; 16.7 us at the measured copy rate, the
+// rest is a launch's start and join), gate/up of 23 tokens, 3 x 12288 x 6144, 39.3 us (5.8 TB/s).
+// With 128 tokens a tile 144 CTAs take 32 KB each for a scale group, 227 MB from L2 in the 18 us of
+// an out-projection of 300 tokens (4 x 6144 x 1536; some 12 us of them between start and join: 19 TB/s);
+// the tensor pipe is 39 % busy, and without three quarters of the MMAs a launch is 10 % shorter.
 //
 // fp8_prompt_kernel: the tokens are M, 256 of them to a persistent CTA pair (cta_group::2), 256
 // weight rows (SwiGLU: 128 gate and 128 up rows) are N.  Bound by the tensor core.  Two
 // accumulators of 256 columns and the scale words do not fit tensor memory's 512 columns side by
 // side, so the accumulators overlap by 32 columns: the epilogue reads those first and hands them
 // back, and the next tile's MMAs start while it works through the rest.  Gate/up of 4608 tokens,
-// 4 x 9216 x 6144 with SwiGLU to fp8, takes 620 us at the power limit (3370 TFLOP/s; 551 us in the
-// first, unthrottled runs), the down projection 318 us (282); a scale group's MMAs run 512 cycles
-// and a group takes 540 (1.43 GHz at the power limit).
+// 4 x 9216 x 6144 with SwiGLU to fp8, takes 649 us at the power limit (3220 TFLOP/s; 561 us in the
+// first, unthrottled runs), the down projection 338 us (290).  A scale group's MMAs run 512 cycles; at
+// the clocks sampled in 3 s of launches (1515 and 1400 MHz) gate/up takes 567 cycles a group of its
+// 36 waves of 48, start and epilogues among them, down 548 of its 6 waves of 144.
 //
 // Every mbarrier wait is bounded (about 2 s); a CTA that gives up records it in the library's
 // status word, lets its copies and MMAs drain, frees tensor memory and exits.
@@ -1026,7 +1028,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) fp8_prompt_kernel(const __g
       // release them to this lane in their own CTA, and this lane, which has seen that, releases
       // them at cluster scope.  (From the threads themselves such a release first waits for their loads of
       // the next words, 1.5 us, longer than a chunk's MMAs: down of 256 tokens 63 us, by way of this
-      // lane, which loads nothing, 47.  An asynchronous store whose bytes complete on the leader's
+      // lane, which loads nothing, 48.  An asynchronous store whose bytes complete on the leader's
       // barrier took 45, but releases no more than its own word.)
       const uint32_t to = ptx::mapa_shared(ptx::smem_addr(&ctl->sf_peer[0]), leader);
       const int tile_chunks = p.n_segs * ((p.k_groups + kChunk - 1) / kChunk);
@@ -1224,7 +1226,7 @@ tp_status launch_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   // life, about 4 us or three chunks; with 128 tokens to join, six).  Ties go to the smaller
   // cluster.  Measured, down projection of one token (4 x 6144 x 4608, 36 chunks, 48 tiles): splits
   // 1 / 2 / 3 / 4 / 5 / 6 / 8 take 29.9 / 22.0 / 21.2 / 20.6 / 20.7 / 26.3 / 24.7 us (from 6 on the
-  // clusters need a second wave); of 256 tokens (96 tiles): 36.4 / 43.7 / 50.1 / 44.1 / 52.0 / 56.4 /
+  // clusters need a second wave; the rule, which counts one CTA an SM, takes 2); of 256 tokens (96 tiles): 36.4 / 43.7 / 50.1 / 44.1 / 52.0 / 56.4 /
   // 72.0, of 512 (192 tiles): 70.1 / 64.8 / 81.8 / 81.9 and more.
   constexpr int kFixed = TN > 64 ? 6 : 3;
   const int* resident = nullptr;
@@ -1350,10 +1352,10 @@ tp_status run_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
 // Whether 256 x 256 tiles on CTA pairs beat 128 x 128 tiles on single CTAs, by what both took (ns): a
 // wave of single CTAs 6000 and 230 a scale group of the CTAs' share (SwiGLU 28 more a token of the
 // tile, and 400), a launch of pairs 6500 and 260 a group and wave.  Measured (us, single against
-// pairs): Q/K/V of 128 / 192 / 384 tokens 25.3 / 36.3 / 53.1 against 26.5 / 26.9 / 38.4; down of 384 /
-// 512 tokens 38 / 66 against 47 / 48; 2 x 2048 x 1024 of 256 / 512 / 768 tokens 7.9 / 8.7 / 16.4
-// against 8.5 / 8.8 / 9.3; SwiGLU 4096 x 512 of 65 / 128 tokens 8.6 / 11.6 against 8.3 / 8.2, 2 x 2048
-// x 2048 of 96 / 300 tokens 9.1 / 14.3 against 11.4 / 11.6.
+// pairs): Q/K/V of 128 / 192 / 384 tokens 25.1 / 36.2 / 52.6 against 26.2 / 26.7 / 38.5; down of 256 /
+// 384 / 512 tokens 36.4 / 37.9 / 63.4 against 48.0 / 47.6 / 48.2; 2 x 2048 x 1024 of 256 / 512 / 768
+// tokens 7.1 / 8.8 / 16.4 against 8.6 / 8.7 / 9.2; SwiGLU 4096 x 512 of 65 / 128 tokens 8.5 / 11.5
+// against 8.2 / 8.1, 2 x 2048 x 2048 of 96 / 300 tokens 9.1 / 12.1 against 11.5 / 11.7.
 bool prompt_is_faster(const Fp8Params& p, const Fp8Call& c) {
   const bool glu = p.act == TP_ACT_SWIGLU;
   const int64_t sms = sm_count(), groups = static_cast<int64_t>(p.n_segs) * p.k_groups;
