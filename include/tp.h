@@ -547,8 +547,8 @@ typedef enum { TP_NORM_NONE = 0, TP_NORM_RMS = 1, TP_NORM_LAYER = 2 } tp_norm;
  *     layer(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * weight + bias
  * (weight and bias optional), over the D elements of a row.  Everything is
  * fp32 until an output is stored; u is computed from the unrounded h.  Squares
- * are fp32 too: a row with values above about 1e19 norms to zeros (NaN where it
- * holds an infinity), one below about 1e-19 as if its mean square were smaller.
+ * and their sums are fp32 too: a row whose squares add up past 3.4e38 norms to
+ * zeros (NaN where it holds an infinity).
  *
  * Without a branch (y NULL; h, gate and post_norm unset) u = norm(alpha * x) *
  * (1 + scale) + shift.  Without u (u NULL; norm, scale, shift and u_scales
