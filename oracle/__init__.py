@@ -1,7 +1,7 @@
 """CPU oracle (test infrastructure): plain float64 numpy definitions of the sharded projection.
 
-Only tests, the smoke check and the benchmark's CPU-baseline leg import this
-package.  The CUDA product path never does.
+Only tests, the smoke check and the benchmark (its CPU-baseline leg, its check of
+the 8-bit stack) import this package.  The CUDA product path never does.
 """
 from .tp_oracle import *  # noqa: F401,F403
 from .tp_oracle import (COLWISE, ROWWISE, PlanRejected, attention_core, bf16_to_f64,  # noqa: F401

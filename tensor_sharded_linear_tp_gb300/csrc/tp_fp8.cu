@@ -1226,8 +1226,9 @@ tp_status launch_tokens(const Fp8Call& c, Fp8Params& p, cudaStream_t stream) {
   // life, about 4 us or three chunks; with 128 tokens to join, six).  Ties go to the smaller
   // cluster.  Measured, down projection of one token (4 x 6144 x 4608, 36 chunks, 48 tiles): splits
   // 1 / 2 / 3 / 4 / 5 / 6 / 8 take 29.9 / 22.0 / 21.2 / 20.6 / 20.7 / 26.3 / 24.7 us (from 6 on the
-  // clusters need a second wave; the rule, which counts one CTA an SM, takes 2); of 256 tokens (96 tiles): 36.4 / 43.7 / 50.1 / 44.1 / 52.0 / 56.4 /
-  // 72.0, of 512 (192 tiles): 70.1 / 64.8 / 81.8 / 81.9 and more.
+  // clusters need a second wave; the rule, which counts one CTA an SM, takes 2); of 256 tokens (96
+  // tiles): 36.4 / 43.7 / 50.1 / 44.1 / 52.0 / 56.4 / 72.0, of 512 (192 tiles): 70.1 / 64.8 / 81.8 / 81.9
+  // and more.
   constexpr int kFixed = TN > 64 ? 6 : 3;
   const int* resident = nullptr;
   tp_status st = tokens_residency<TN, kGlu>(&resident);
