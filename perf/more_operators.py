@@ -6,9 +6,9 @@ tokens in the cache with them; its i-th of n new rows stands at position kv_len[
 page page_table[s][j // P].
 
 * append     Q and K are rotated (pairs (x[i], x[i + R/2]) or (x[2i], x[2i+1]); (x1 c - x2 s, x2 c + x1 s), c and s from a
-             table's row for the position).  A page's exponent e is the least with max|x| <= 448 * 2^e over its new values, and
-             not less than the one it has where older tokens of the sequence are in it; these tokens' codes q become
-             e4m3(q * 2^(e_old - e)), the new ones are e4m3(x / 2^e).
+             table's row for the position).  A page's exponent e is the least from -127 on with max|x| <= 448 * 2^e over its new
+             values, and not less than the one it has where older tokens of the sequence are in it; these tokens' codes q
+             become e4m3(q * 2^(e_old - e)), the new ones are e4m3(x / 2^e).
 * attention  out = softmax(scale q K^T) V over the visible keys j: j <= position where causal, j > position - window where
              there is a window; 0 where no key is visible.  Query head h reads KV head h // (heads / kv heads).
 
@@ -117,10 +117,10 @@ def _ceil(a, b):
 
 
 def _exponent(top):
-    """The least e with top <= 448 * 2^e, clamped; 0 for a group of zeros."""
+    """The least e >= -127 with top <= 448 * 2^e."""
     m, k = torch.frexp(top)                                            # 448 = 0.875 * 2^9
     e = torch.where(m > 0.875, k - 8, k - 9).clamp(-127, 127)
-    return torch.where(top > 0, e, torch.zeros_like(e))
+    return torch.where(top > 0, e, torch.full_like(e, -127))
 
 
 def _pages(g, n, kv, page, D, std):
@@ -342,7 +342,7 @@ def _exact_append(case, seed):
                     e = torch.ceil(torch.log2(top.clamp_min(1e-300) / 448.0)) - 1
                     for _ in range(2):
                         e = torch.where(top > 448.0 * torch.exp2(e), e + 1, e)
-                    power = torch.exp2(torch.where(top > 0, e.clamp(-127, 127), torch.zeros_like(e)))
+                    power = torch.exp2(e.clamp(-127, 127))
                     if lo:
                         power = torch.maximum(power, size[page])
                         value[page, :, :lo] *= (size[page] / power)[:, None, None]
