@@ -593,6 +593,151 @@ typedef struct {
 TP_API tp_status tp_residual_norm(const tp_residual_norm_args* args, tp_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Paged 8-bit cache of keys and values                                      */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Serving a sharded transformer: each rank keeps the keys and values of its
+ * own KV heads ("Tensor parallelism" page, §Colwise and rowwise: the colwise
+ * Q, K and V projections give each rank a subset of heads) in pages of
+ * page_size tokens, in the 8-bit format above with one scale for each page and
+ * head.  The pages have no counterpart of these calls (they describe no cache).
+ *
+ * One decoding step or prompt chunk of a rank is
+ *     tp_linear_colwise(_fp8) -> Q, K, V columns   (bf16)
+ *     tp_kv_append_fp8        -> Q rotated, K rotated and cached, V cached
+ *     tp_attention_paged_fp8  -> attention over the cache
+ *     tp_linear_rowwise       -> the out-projection.
+ *
+ * Cache.  k[r] and v[r] are rank r's codes, e4m3 [n_pages, n_kv_heads,
+ * page_size, head_dim] with ld_page elements from page to page (0 = dense);
+ * k_scales[r] and v_scales[r] are e8m0 [n_pages, n_kv_heads] with ld_scales
+ * from page to page (0 = n_kv_heads).  head_dim is 64 or 128, page_size 16, 32,
+ * 64 or 128 (TP_ERR_UNSUPPORTED otherwise).  Codes are 16-byte aligned and
+ * ld_page is a multiple of 16 (TP_ERR_ALIGNMENT); scales have any alignment.
+ * No initial value is needed: a page is only read where tokens were appended.
+ *
+ * Batch.  Every rank serves the same sequences.  seq_start (n_seqs + 1 entries,
+ * ascending from seq_start[0] >= 0 to at most T), kv_len (n_seqs) and
+ * page_table (n_seqs rows of max_pages, row stride ld_table, 0 = max_pages)
+ * are int32 in DEVICE memory, read when the kernels run, so that a captured
+ * CUDA graph takes the values of each replay.  Sequence s has the new rows
+ * [seq_start[s], seq_start[s+1]), at most max_new of them, and kv_len[s] tokens
+ * with the new ones; its row i of n stands at position kv_len[s] - n + i, and
+ * position j is slot j % page_size of page page_table[s][j / page_size].  Rows
+ * of T outside every sequence (padding) are neither read nor written.  A page
+ * may be in several sequences' tables (a shared prefix), but not be appended
+ * to by two in one call.
+ *
+ * What only the device can see is checked there: a token without a place (a
+ * negative position, a page outside the table or the cache) is not cached, a
+ * key in such a page is not seen, a token whose rotation is outside its table
+ * is NaN, and rows beyond max_new or T are left out.  Nothing is read or
+ * written out of bounds, and tp_device_status reports TP_ERR_INVALID_ARG.
+ */
+typedef struct {
+  int n_ranks;                  /* 1 .. TP_MAX_DEGREE */
+  int n_kv_heads;               /* of one rank */
+  int head_dim, page_size;
+  int64_t n_pages;
+  void* const* k;               /* host arrays of n_ranks device pointers */
+  void* const* v;
+  void* const* k_scales;
+  void* const* v_scales;
+  int64_t ld_page, ld_scales;
+} tp_paged_cache;
+
+typedef struct {
+  int n_seqs;
+  int max_new;                  /* at least the new rows of any sequence */
+  const int32_t* seq_start;     /* device [n_seqs + 1] */
+  const int32_t* kv_len;        /* device [n_seqs] */
+  const int32_t* page_table;    /* device [n_seqs, max_pages] */
+  int64_t ld_table, max_pages;
+} tp_paged_batch;
+
+/* Which elements of a head form a pair: x[i] and x[i + rot_dim/2], or x[2i] and x[2i + 1]. */
+typedef enum { TP_ROPE_HALF = 0, TP_ROPE_PAIRS = 1 } tp_rope_style;
+
+/*
+ * The position rotation of Q and K: pair i of a token becomes
+ * (x1 c_i - x2 s_i, x2 c_i + x1 s_i) with the row [c_0 .. c_{rot_dim/2 - 1},
+ * s_0 ..] of cos_sin that belongs to the token: row `position`, or row
+ * positions[t] of its row t.  Elements from rot_dim on stay as they are.  The
+ * table is the caller's (any base, scaling or number of axes; computed in
+ * double precision, far positions keep their angles).
+ */
+typedef struct {
+  tp_rope_style style;
+  int rot_dim;                  /* multiple of 16, at most head_dim */
+  const float* cos_sin;         /* device [n_positions, rot_dim], 16-byte aligned */
+  int64_t ld;                   /* row stride in elements, multiple of 4; 0 = rot_dim */
+  int64_t n_positions;
+  const int32_t* positions;     /* NULL, or device [T] */
+} tp_rope;
+
+/*
+ * tp_kv_append_fp8 -- every rank's new tokens into its cache, and their Q
+ * rotated, in one launch.
+ *
+ * qkv[r]: device bf16 [T, (n_heads + 2 n_kv_heads) head_dim], row stride
+ *         ld_qkv (0 = dense): rank r's Q, K and V columns.
+ * rope:   NULL (no rotation), or the rotation of Q and K.
+ * q_out:  NULL (Q is left alone), or host array of device pointers, each bf16
+ *         [T, n_heads head_dim] with row stride ld_q (0 = dense): Q rotated in
+ *         fp32 and rounded once.  q_out[r] may be qkv[r] with ld_q = ld_qkv (Q rotated
+ *         in place); no other output may overlap an input or another output.
+ *
+ * K (rotated in fp32, not rounded in between) and V are quantised by page and
+ * head: e is the least exponent >= -127 with max|x| <= 448 * 2^e over the new
+ * tokens of the page, and not less than the page's own where older tokens of
+ * the sequence are in it; the scale byte is e + 127 and a new code is
+ * e4m3(x / 2^e), rounded once to nearest even.  Where e grew, the older
+ * tokens' codes q become e4m3(q * 2^(e_old - e)) (exact but for codes that
+ * become subnormal).  A page with a NaN or an infinity becomes NaN for that
+ * head (byte 255, NaN codes).  Slots behind the last token are left as they
+ * were.  Appending the same tokens again changes nothing, and a token's
+ * cache does not depend on what else is in the batch.
+ * Alignment (TP_ERR_ALIGNMENT): ld_qkv and ld_q % 8 == 0, qkv and q_out 16-byte.
+ * T == 0, n_seqs == 0 or max_new == 0 enqueues nothing.
+ */
+TP_API tp_status tp_kv_append_fp8(const tp_paged_cache* cache, const tp_paged_batch* batch, const void* const* qkv,
+                                  int64_t ld_qkv, int64_t T, int n_heads, const tp_rope* rope, void* const* q_out,
+                                  int64_t ld_q, tp_stream_t stream);
+
+/*
+ * tp_attention_paged_fp8 -- attention of every rank's new tokens over its cache:
+ *     O_h = softmax(scale * Q_h K_g^T) V_g,  g = h / (n_heads / n_kv_heads)
+ * K and V the values their codes and scales stand for.  A token at position p
+ * sees the keys j < kv_len of its sequence with j <= p (causal) and
+ * j > p - window (window > 0, causal only); a row that sees no key is 0.
+ *
+ * q:    host array of device pointers, each bf16 [T, n_heads head_dim] with row
+ *       stride ld_q (0 = dense); n_heads is a multiple of n_kv_heads.
+ * out:  host array of device pointers, each bf16 [T, n_heads head_dim] with row
+ *       stride ldo (0 = dense); may not overlap q or another output.
+ * workspace: device buffer of tp_attention_paged_workspace_bytes(...) bytes,
+ *       16-byte aligned, owned by the caller, of any content.  Calls that share one must not
+ *       overlap on the GPU.
+ * Codes and Q enter the tensor cores exactly (as fp16, scaled by powers of
+ * two); products, softmax and sums are fp32, the probabilities enter P.V as
+ * fp16 (2^-12 relative, a sixteenth of the output's own rounding step).  A key or value
+ * page that is NaN makes the rows that see it NaN, and no others.  The same
+ * call gives the same bits every time.
+ * Alignment (TP_ERR_ALIGNMENT): ld_q and ldo % 8 == 0, q and out 16-byte.
+ * T == 0, n_seqs == 0 or max_new == 0 enqueues nothing.
+ */
+TP_API tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_batch* batch, const void* const* q,
+                                        int64_t ld_q, int64_t T, int n_heads, float scale, int causal, int window,
+                                        void* workspace, size_t ws_bytes, void* const* out, int64_t ldo,
+                                        tp_stream_t stream);
+
+/* Bytes of device workspace tp_attention_paged_fp8 needs on the current device (0 for a call that it would
+ * refuse or that enqueues nothing). */
+TP_API size_t tp_attention_paged_workspace_bytes(const tp_paged_cache* cache, const tp_paged_batch* batch, int64_t T,
+                                                 int n_heads);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics                                                               */
 /* ------------------------------------------------------------------------ */
 
@@ -605,8 +750,9 @@ TP_API const char* tp_status_name(tp_status status);
 /*
  * tp_device_status -- synchronise `stream`, then report whether any kernel of
  * this library on the current device gave up on an internal wait (every wait
- * is bounded; a kernel that gives up records it and exits cleanly).  Returns
- * TP_ERR_TIMEOUT and clears the record if so, TP_ERR_CUDA if the stream
+ * is bounded; a kernel that gives up records it and exits cleanly) or met an
+ * index in device memory that it could not use (the paged cache's calls).
+ * Returns TP_ERR_TIMEOUT or TP_ERR_INVALID_ARG and clears the record if so, TP_ERR_CUDA if the stream
  * reported an error, TP_OK otherwise.
  */
 TP_API tp_status tp_device_status(tp_stream_t stream);

@@ -44,6 +44,7 @@ COMBINE_MODES = {"gather": 0, "reduce": 1}
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 FP8_GROUP = 128         # features (or weight rows) that share a scale
 NORM_MAX_D = 32768      # TP_NORM_MAX_D
+ROPE_STYLES = {"half": 0, "pairs": 1}
 MAX_DEGREE = 16
 MAX_SPLITS = 16
 
@@ -77,6 +78,11 @@ _SIGS = {
                                         _i64, _vp, _i64, _vp, _i64, _vp]),
     "tp_linear_rowwise_fp8": (_status, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp,
                                         _i64, _vp]),
+    # (their structures and arrays of pointers are passed as bytes, see PagedCache)
+    "tp_kv_append_fp8": (_status, [_vp, _vp, _vp, _i64, _i64, ctypes.c_int, _vp, _vp, _i64, _vp]),
+    "tp_attention_paged_fp8": (_status, [_vp, _vp, _vp, _i64, _i64, ctypes.c_int, ctypes.c_float, ctypes.c_int,
+                                         ctypes.c_int, _vp, ctypes.c_size_t, _vp, _i64, _vp]),
+    "tp_attention_paged_workspace_bytes": (ctypes.c_size_t, [_vp, _vp, _i64, ctypes.c_int]),
     "tp_last_error": (ctypes.c_char_p, []),
     "tp_status_name": (ctypes.c_char_p, [ctypes.c_int]),
     "tp_device_status": (_status, [_vp]),
@@ -118,6 +124,9 @@ _SIGS["tp_plan_shard_many"] = (_status, [ctypes.POINTER(ShardRequest), ctypes.c_
 _SIGS["tp_residual_norm"] = (_status, [_vp, _vp])
 # The same structure as bytes, in native alignment (q: int64, P: pointer, i: enum).
 _residual_norm_args = struct.Struct("@qq PqPq iPP ff PPP qqq Pq iPP PqPq").pack
+_paged_cache = struct.Struct("@iiii q PPPP qq").pack      # tp_paged_cache
+_paged_batch = struct.Struct("@ii PPP qq").pack           # tp_paged_batch
+_rope = struct.Struct("@iiPqqP").pack                     # tp_rope
 
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -715,6 +724,184 @@ def tp_residual_norm(x: torch.Tensor, y: torch.Tensor | None = None, norm: str =
                                0 if out is None else NORMS[norm], vectors[0], vectors[1], u_at, ldu, s_at, ld_us)
     _check(lib.tp_residual_norm(args, _launch_stream(stream, dev)))
     return h, u, u_scales
+
+
+# ---------------------------------------------------------------------------
+# Paged 8-bit cache of keys and values
+# ---------------------------------------------------------------------------
+
+class PagedCache:
+    """The keys and values of every rank's KV heads: tp_paged_cache (include/tp.h) over the caller's tensors.
+
+    k[r] and v[r] are float8_e4m3fn [n_pages, n_kv_heads, page_size, head_dim], whole but for the
+    stride from page to page; k_scales[r] and v_scales[r] are float8_e8m0fnu (or uint8) [n_pages,
+    n_kv_heads].  The tensors are checked once, here, and kept: a program makes one cache for
+    each layer and passes it to every call."""
+
+    def __init__(self, k: Sequence[torch.Tensor], v: Sequence[torch.Tensor], k_scales: Sequence[torch.Tensor],
+                 v_scales: Sequence[torch.Tensor]):
+        n = len(k)
+        if n < 1 or n > MAX_DEGREE:
+            raise ValueError(f"k must have one entry for each of 1 to {MAX_DEGREE} ranks, got {n}")
+        if not len(v) == len(k_scales) == len(v_scales) == n:
+            raise ValueError(f"every list must have one entry for each of the {n} ranks")
+        if k[0].dim() != 4:
+            raise ValueError(f"k[0] must be [n_pages, n_kv_heads, page_size, head_dim], got {tuple(k[0].shape)}")
+        shape = n_pages, heads, page, d = tuple(k[0].shape)
+        self.device = k[0].device
+        if not k[0].is_cuda:
+            raise ValueError(f"k[0] must be on a CUDA device, got {k[0].device}")
+        ld_page = self._strides("k and v", [*k, *v], (_E4M3,), shape, (page * d, d, 1))
+        ld_scales = self._strides("k_scales and v_scales", [*k_scales, *v_scales], (_E8M0, _U8), (n_pages, heads), (1,))
+        self.k, self.v, self.k_scales, self.v_scales = list(k), list(v), list(k_scales), list(v_scales)
+        self.n_ranks, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n, n_pages, heads, page, d
+        self._arrays = [_ptrs(ts) for ts in (k, v, k_scales, v_scales)]
+        self._struct = _paged_cache(n, heads, d, page, n_pages, *[ctypes.addressof(a) for a in self._arrays], ld_page,
+                                    ld_scales)
+
+    @classmethod
+    def empty(cls, n_ranks: int, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda"):
+        """A cache over new tensors (uninitialised: pages are read only where tokens were appended)."""
+        codes = [[torch.empty((n_pages, n_kv_heads, page_size, head_dim), dtype=_E4M3, device=device)
+                  for _ in range(n_ranks)] for _ in range(2)]
+        scales = [[torch.empty((n_pages, n_kv_heads), dtype=_E8M0, device=device) for _ in range(n_ranks)]
+                  for _ in range(2)]
+        return cls(*codes, *scales)
+
+    def _strides(self, name, ts, dtypes, shape, inner) -> int:
+        """The stride from page to page (0: whole tensors), the same for every tensor."""
+        steps = set()
+        for t in ts:
+            if t.dtype not in dtypes:
+                raise TypeError(f"{name} must be {dtypes[0]}, got {t.dtype}")
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must all have the shape {shape}, got {tuple(t.shape)}")
+            if t.device != self.device:
+                raise ValueError(f"{name} must all be on {self.device}, got {t.device}")
+            if t.is_contiguous():
+                steps.add(shape[1] * inner[0] if len(inner) > 1 else shape[1])
+                continue
+            if any(size > 1 and got != want for size, got, want in zip(shape[1:], t.stride()[1:], inner)):
+                raise ValueError(f"{name} must be whole but for the stride from page to page, got strides {t.stride()}")
+            if t.stride(0) < shape[1] * inner[0]:
+                raise ValueError(f"{name}: a stride of {t.stride(0)} overlaps pages of {shape[1] * inner[0]} elements")
+            steps.add(t.stride(0))
+        if len(steps) > 1:
+            raise ValueError(f"{name} must all have the same stride from page to page")
+        return steps.pop()
+
+
+class PagedBatch:
+    """The sequences of a step and where their tokens are: tp_paged_batch (include/tp.h) over int32 tensors on the GPU.
+
+    seq_start [n_seqs + 1], kv_len [n_seqs] and page_table [n_seqs, max_pages] are read when the
+    kernels run; max_new is at least the new rows of any sequence.  Made once a step, for every layer."""
+
+    def __init__(self, seq_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, max_new: int):
+        if page_table.dim() != 2:
+            raise ValueError(f"page_table must be [n_seqs, max_pages], got {tuple(page_table.shape)}")
+        n, max_pages = page_table.shape
+        self.device = page_table.device
+        if not page_table.is_cuda:
+            raise ValueError(f"page_table must be on a CUDA device, got {page_table.device}")
+        for name, t, shape in (("seq_start", seq_start, (n + 1,)), ("kv_len", kv_len, (n,)),
+                               ("page_table", page_table, (n, max_pages))):
+            if t.dtype is not torch.int32:
+                raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+        ld = [_need(name, t, torch.int32, torch.Size(shape), page_table.get_device())
+              for name, t, shape in (("seq_start", seq_start, (n + 1,)), ("kv_len", kv_len, (n,)),
+                                     ("page_table", page_table, (n, max_pages)))][2]
+        self.seq_start, self.kv_len, self.page_table = seq_start, kv_len, page_table
+        self.n_seqs, self.max_pages, self.max_new = n, max_pages, int(max_new)
+        self._struct = _paged_batch(n, self.max_new, seq_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), ld,
+                                    max_pages)
+
+
+def _paged_device(cache: PagedCache, batch: PagedBatch) -> int:
+    dev = cache.device.index
+    if dev != torch._C._cuda_getDevice() or batch.device.index != dev:
+        raise ValueError(f"cache ({cache.device}) and batch ({batch.device}) must be on the current CUDA device")
+    return dev
+
+
+def tp_kv_append_fp8(qkv: Sequence[torch.Tensor], n_heads: int, cache: PagedCache, batch: PagedBatch,
+                     rope: str | None = None, cos_sin: torch.Tensor | None = None,
+                     positions: torch.Tensor | None = None, q_out: Sequence[torch.Tensor] | None = None,
+                     stream=None) -> list[torch.Tensor]:
+    """Every rank's new keys (rotated) and values into its cache, one launch; returns each rank's Q, rotated.
+
+    qkv[r] is bf16 [T, (n_heads + 2 n_kv_heads) head_dim], rank r's colwise Q, K and V columns.
+    rope names the pairs of the rotation, "half" or "pairs"; cos_sin is then its fp32 table
+    [n_positions, rot_dim], cosines before sines, and positions (int32 [T]) the table row of each
+    token (default: its position in the cache).  q_out[r] may be qkv[r][:, :n_heads * head_dim]."""
+    dev = _paged_device(cache, batch)
+    n = cache.n_ranks
+    if len(qkv) != n or (q_out is not None and len(q_out) != n):
+        raise ValueError(f"qkv and q_out must have one entry for each of the cache's {n} ranks")
+    if qkv[0].dim() != 2:
+        raise ValueError(f"qkv[0] must be 2-D, got {tuple(qkv[0].shape)}")
+    T, wide = qkv[0].shape[0], n_heads * cache.head_dim
+    at, ld = _need_ranks("qkv", qkv, _BF16, (T, wide + 2 * cache.n_kv_heads * cache.head_dim), dev)
+    turn = None
+    if rope is not None:
+        if rope not in ROPE_STYLES:
+            raise ValueError(f'rope must be "half" or "pairs", got {rope!r}')
+        if cos_sin is None or cos_sin.dim() != 2:
+            raise ValueError("a rotation needs cos_sin, [n_positions, rot_dim]")
+        step = _need("cos_sin", cos_sin, torch.float32, cos_sin.shape, dev)
+        if positions is not None:
+            _need("positions", positions, torch.int32, (T,), dev)
+        turn = _rope(ROPE_STYLES[rope], cos_sin.shape[1], cos_sin.data_ptr(), step, cos_sin.shape[0],
+                     0 if positions is None else positions.data_ptr())
+    elif cos_sin is not None or positions is not None:
+        raise ValueError('cos_sin and positions belong to rope="half" or rope="pairs"')
+    if n_heads == 0:
+        q_out, q_at, ld_q = [], None, 0
+    else:
+        if q_out is None:
+            q_out = _alloc(stream, cache.device, _BF16, (T, wide), n)
+        q_at, ld_q = _need_ranks("q_out", q_out, _BF16, (T, wide), dev)
+    _check(lib.tp_kv_append_fp8(cache._struct, batch._struct, at, ld, T, n_heads, turn, q_at, ld_q,
+                                _launch_stream(stream, dev)))
+    return list(q_out)
+
+
+def tp_attention_paged_workspace_bytes(cache: PagedCache, batch: PagedBatch, T: int, n_heads: int) -> int:
+    return int(lib.tp_attention_paged_workspace_bytes(cache._struct, batch._struct, T, n_heads))
+
+
+def tp_attention_paged_fp8(q: Sequence[torch.Tensor], cache: PagedCache, batch: PagedBatch, scale: float | None = None,
+                           causal: bool = True, window: int = 0, outs: Sequence[torch.Tensor] | None = None,
+                           workspace: torch.Tensor | None = None, stream=None) -> list[torch.Tensor]:
+    """softmax(scale Q_h K_g^T) V_g of every rank's new tokens over its cache, g the KV head of query head h.
+
+    q[r] is bf16 [T, n_heads * head_dim]; scale defaults to head_dim ** -0.5.  A token sees the
+    keys of its sequence up to its own position (causal), the last `window` of them where window > 0."""
+    dev = _paged_device(cache, batch)
+    n, d = cache.n_ranks, cache.head_dim
+    if len(q) != n or (outs is not None and len(outs) != n):
+        raise ValueError(f"q and outs must have one entry for each of the cache's {n} ranks")
+    shape = q[0].shape
+    if len(shape) != 2 or shape[1] % d != 0:
+        raise ValueError(f"q[0] must be [T, n_heads * {d}], got {tuple(shape)}")
+    T, n_heads = shape[0], shape[1] // d
+    at, ld = _need_ranks("q", q, _BF16, shape, dev)
+    if outs is None:
+        outs = _alloc(stream, cache.device, _BF16, shape, n)
+    out_at, ldo = _need_ranks("outs", outs, _BF16, shape, dev)
+    if workspace is None:
+        need = tp_attention_paged_workspace_bytes(cache, batch, T, n_heads)
+        if need:
+            workspace, = _alloc(stream, cache.device, _U8, (need,))
+    ws_at, ws_bytes = 0, 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the current CUDA device")
+        ws_at, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib.tp_attention_paged_fp8(cache._struct, batch._struct, at, ld, T, n_heads,
+                                      d ** -0.5 if scale is None else scale, int(causal), window, ws_at, ws_bytes, out_at,
+                                      ldo, _launch_stream(stream, dev)))
+    return list(outs)
 
 
 # ---------------------------------------------------------------------------

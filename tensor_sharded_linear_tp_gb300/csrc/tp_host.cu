@@ -213,7 +213,11 @@ tp_status tp_device_status(tp_stream_t stream) {
     unsigned int zero = 0;
     e = cudaMemcpyToSymbol(tp::tp_kernel_status_word, &zero, sizeof(zero));
     if (e != cudaSuccess) return tp::cuda_fail(e, "clearing the kernel status word");
-    return tp::fail(TP_ERR_TIMEOUT, "a kernel gave up on a bounded wait (status word 0x%x)", word);
+    if (word & TP_DEVSTATUS_TIMEOUT)
+      return tp::fail(TP_ERR_TIMEOUT, "a kernel gave up on a bounded wait (status word 0x%x)", word);
+    return tp::fail(TP_ERR_INVALID_ARG,
+                    "a kernel of the paged cache met a sequence, page or position out of bounds and left it out "
+                    "(status word 0x%x)", word);
   }
   return TP_OK;
 }
@@ -224,6 +228,6 @@ void tp_set_tile_wait_limit_ns(uint64_t ns) {
 
 uint64_t tp_tile_wait_limit_ns(void) { return tp::tile_wait_limit_ns(); }
 
-int tp_abi_version(void) { return 104; }
+int tp_abi_version(void) { return 105; }
 
 }  // extern "C"

@@ -34,7 +34,7 @@ tp_status guarded(Body&& body) {
 int sm_count();
 
 // Device address of the library's kernel status word on the current device
-// (bit 0: a kernel gave up on a bounded wait).  Looked up once per device.
+// (TP_DEVSTATUS_* below).  Looked up once per device.
 unsigned int* status_word();
 
 // Identity of the calling thread's current CUDA context, unique over the process's lifetime
@@ -83,8 +83,9 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 }  // namespace tp
 
-// Bit 0 of the status word: a bounded wait gave up.
+// Bits of the status word: a bounded wait gave up; an index read from device memory was out of bounds.
 #define TP_DEVSTATUS_TIMEOUT 1u
+#define TP_DEVSTATUS_INDEX 2u
 
 namespace tp {
 // Library-internal batched GEMM (tp_gemm.cu): out_g = A_g . B_g^T for up to TP_MAX_DEGREE groups.

@@ -1,0 +1,962 @@
+// Attention over the paged 8-bit cache (tp_paged.h, include/tp.h): few rows a KV head.
+//
+//     S = scale Q K^T,  O = softmax(S) V      one item = the rows of one sequence, KV head and rank
+//
+// What bounds it: the cache's bytes.  With R rows (new tokens x query heads of the KV head) a key
+// costs 2 D bytes and 4 D R FLOP; at R <= 16 that is at most 32 FLOP a byte, a tenth of what the GPU
+// has, so the keys and values stream through the SMs once and everything else has to keep out of
+// their way:
+//
+// * All keys of all items are one line of steps of 32 keys, cut into equal parts: one for each CTA
+//   (one an SM), one of 8 within it for each warp.  Sequences of any lengths load the GPU evenly,
+//   from a batch of short ones to one long one.  An item that lies in one warp is finished by it;
+//   pieces of an item in several warps are joined in shared memory, pieces in several CTAs through the
+//   workspace by a second launch, always in key order (no atomics).
+// * A warp has a ring of steps of its own in shared memory, filled by TMA (one box a page, swizzled
+//   so that the loads below meet no bank twice) and drained by itself: no barrier between warps.
+// * The products are S^T = K Q^T and O^T = V^T P^T on mma.sync m16n8k16 (keys, then head elements,
+//   on M; rows on N), since so few rows would leave most of a tcgen05 tile's 128 empty.  K's
+//   fragments are 32-bit words of the cache, converted two codes an instruction to fp16 (exact); V's need two
+//   keys side by side, a byte permutation first; P^T's come from S^T's by a transposing move.
+// * Scales stay out of the fragments: K's multiplies a score, V's the probability.
+//
+// Q enters as fp16 as well, each row scaled by a power of two to below 2^15, so that what it loses
+// lies 2^-39 below its largest element; its factor goes into the scores.  P is 2^(s - m) (m the running maximum)
+// times 2^(e - E + 14), e the exponent of the key's V page and E the largest so far: at most 2^14, so
+// that fp16 keeps what is up to 2^-38 below the largest.  O is kept in units of 2^(E - 14).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "tp_e4m3.cuh"
+#include "tp_internal.h"
+#include "tp_paged.h"
+#include "tp_ptx.cuh"
+
+namespace tp {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStep = 32;                         // keys of a step
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+struct AttendParams {
+  CUtensorMap map_k[TP_MAX_DEGREE], map_v[TP_MAX_DEGREE];  // [pages][heads][tokens][D] codes, box of one page's tokens (at most 32)
+  BatchView b;
+  const __nv_bfloat16* q[TP_MAX_DEGREE];
+  __nv_bfloat16* out[TP_MAX_DEGREE];
+  const uint8_t *ks[TP_MAX_DEGREE], *vs[TP_MAX_DEGREE];
+  int64_t ld_q, ldo, ld_scales;
+  int n_kv, group;             // KV heads of a rank, query heads of a KV head
+  int heads;                   // n_ranks * n_kv
+  int causal, window;
+  float scale_log2e;
+  int per_item;                // 1: a CTA takes one item whole; 0: equal parts of all steps
+  float* parts;                // workspace: two partial items a CTA (part_floats each)
+  int4* joins;                 // workspace: a CTA's item to be joined {parts, first row, rows, rank and head}
+};
+
+// A piece of an item in shared memory.
+struct Piece {
+  int64_t item_end;     // the step behind the item's last
+  int valid, first, last;
+  int s, h, row0;
+};
+struct Start {          // where a warp's part begins
+  int s, h, tile;
+  int64_t at;           // its first step
+};
+template <int STAGES>
+struct alignas(16) Ctrl {
+  uint64_t full[kWarps][STAGES];
+  uint32_t info[kWarps][STAGES][2];   // scale bytes of a step's two halves (page_info)
+  Piece piece[kWarps][2];
+  Start start[kWarps];
+  int64_t sums[kWarps];
+  int64_t total;
+};
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr uint32_t HALF = kStep * D;     // K's or V's bytes of a step
+  static constexpr uint32_t STAGE = 2 * HALF;
+  static constexpr int STAGES = (NT == 1 ? 3 : 2) * (128 / D);
+  static constexpr uint32_t RING = STAGES * STAGE;                   // of one warp
+  static constexpr uint32_t PIECE = ROWS * (D + 2) * 4;              // O, then (m, l) of each row
+  static constexpr uint32_t OFF_HEAD = kWarps * RING;                // each warp's first piece; its last one takes its ring
+  static constexpr uint32_t OFF_CTRL = OFF_HEAD + kWarps * PIECE;
+  static constexpr size_t SMEM = 1024 + OFF_CTRL + sizeof(Ctrl<STAGES>);
+  static_assert(PIECE <= RING && SMEM <= 232448, "shared memory");
+};
+
+// One item: rows [row0, row0 + rows) of a sequence's n * group rows (token by token), and its steps.
+struct Item {
+  SeqView v;
+  int row0, rows;
+  int tile0, tiles;     // steps tile0 .. tile0 + tiles of the sequence's keys
+  int key_end;          // keys from here on are not seen by any row
+};
+
+template <int ROWS>
+__device__ __forceinline__ Item item_of(const AttendParams& p, const SeqView& v, int block) {
+  Item it;
+  it.v = v;
+  it.row0 = block * ROWS;
+  it.rows = static_cast<int>(min(static_cast<int64_t>(ROWS), static_cast<int64_t>(v.n) * p.group - it.row0));
+  const int first = it.row0 / p.group, last = (it.row0 + max(it.rows, 1) - 1) / p.group;
+  it.key_end = p.causal ? max(min(static_cast<int64_t>(v.len), static_cast<int64_t>(v.pos0) + last + 1), int64_t(0)) : v.len;
+  const int64_t lo = p.window > 0 ? max(static_cast<int64_t>(v.pos0) + first - p.window + 1, int64_t(0)) : 0;
+  it.tile0 = static_cast<int>(min(lo, static_cast<int64_t>(it.key_end))) / kStep;
+  it.tiles = it.rows > 0 ? max(1, (it.key_end + kStep - 1) / kStep - it.tile0) : 0;   // (a row without keys is an item too)
+  return it;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^e, 0 below fp32's normal range.
+__device__ __forceinline__ float pow2(int e) {
+  return e < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(min(e, 127) + 127) << 23);
+}
+// A scale byte's value (NaN for 255).
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7FFFFFFFu) : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+}
+
+// Two codes (the low or high half of a word) as fp16.
+__device__ __forceinline__ uint32_t f16_lo(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16_hi(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w >> 16)));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, uint32_t bar, int token, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(0), "r"(token), "r"(head), "r"(page)
+      : "memory");
+}
+
+// A step's data in shared memory: row `key`, 16-byte chunk c, under the TMA's swizzle (128 or 64 bytes).
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int key, int c) {
+  return static_cast<uint32_t>(key * D + ((c ^ (D == 128 ? key & 7 : (key >> 1) & 3)) << 4));
+}
+
+constexpr uint32_t kPageSeen = 0x10000;   // in a page's info, above its K and V scale bytes: its index is valid
+
+// The steps of a warp's part in the order they are loaded, ahead of the one that is worked on.
+struct Loader {
+  int s, h;
+  int tile, tile_end;          // of the current item
+  int page0;                   // the lanes hold pages page0 .. page0 + 31 of the sequence
+  int my_page;
+  uint32_t my_info;
+  int len;                     // the sequence's keys
+};
+
+template <int D>
+__device__ __forceinline__ void load_pages(const AttendParams& p, Loader& ld, int first, int lane) {
+  ld.page0 = first;
+  const int64_t at = static_cast<int64_t>(first) + lane;
+  const int rank = ld.h / p.n_kv, head = ld.h - rank * p.n_kv;
+  ld.my_info = 0;
+  ld.my_page = 0;
+  if ((at << p.b.page_shift) < ld.len) {
+    ld.my_page = p.b.page_table[ld.s * p.b.ld_table + at];
+    if (ld.my_page >= 0 && ld.my_page < p.b.n_pages) {
+      const int64_t sc = static_cast<int64_t>(ld.my_page) * p.ld_scales + head;
+      ld.my_info = kPageSeen | p.ks[rank][sc] | (static_cast<uint32_t>(p.vs[rank][sc]) << 8);
+    } else {
+      bad_index(p.b);
+    }
+  }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void issue_step(const AttendParams& p, Loader& ld, int stage, uint32_t ring, Ctrl<Cfg<D, NT>::STAGES>* ctl,
+                                           int warp, int lane) {
+  using C = Cfg<D, NT>;
+  if (ld.tile == ld.tile_end) {   // the next item: the next head, or the next sequence's first
+    SeqView v;
+    Item it;
+    if (++ld.h == p.heads) {
+      ld.h = 0;
+      do {
+        v = seq_view(p.b, ++ld.s);
+        it = item_of<C::ROWS>(p, v, 0);
+      } while (it.tiles == 0 && ld.s + 1 < p.b.n_seqs);
+    } else {
+      v = seq_view(p.b, ld.s);
+      it = item_of<C::ROWS>(p, v, 0);
+    }
+    ld.tile = it.tile0;
+    ld.tile_end = it.tile0 + it.tiles;
+    ld.len = v.len;
+    ld.page0 = -64;
+  }
+  const int key0 = ld.tile * kStep;
+  const int page = key0 >> p.b.page_shift;
+  const bool two = p.b.page_size == 16;
+  if (page < ld.page0 || page + (two ? 1 : 0) >= ld.page0 + 32) load_pages<D>(p, ld, page, lane);
+  const int src = page - ld.page0;
+  const uint32_t info0 = __shfl_sync(0xffffffffu, ld.my_info, src);
+  const int page_a = __shfl_sync(0xffffffffu, ld.my_page, src);
+  const uint32_t info1 = two ? __shfl_sync(0xffffffffu, ld.my_info, src + 1) : info0;
+  const int page_b = two ? __shfl_sync(0xffffffffu, ld.my_page, src + 1) : page_a;
+  if (lane == 0) {
+    const uint32_t bar = ptx::smem_addr(&ctl->full[warp][stage]);
+    const int rank = ld.h / p.n_kv, head = ld.h - rank * p.n_kv;
+    const uint32_t box = two ? C::HALF / 2 : C::HALF;
+    const bool a = (info0 & kPageSeen) != 0, b = two && (info1 & kPageSeen) != 0;
+    const uint32_t dst = ring + stage * C::STAGE;
+    ctl->info[warp][stage][0] = info0;
+    ctl->info[warp][stage][1] = info1;
+    ptx::mbar_arrive_expect_tx(bar, ((a ? 2 : 0) + (b ? 2 : 0)) * box);
+    const int token = key0 & (p.b.page_size - 1);
+    if (a) {
+      tma_load_page(dst, &p.map_k[rank], bar, token, head, page_a);
+      tma_load_page(dst + C::HALF, &p.map_v[rank], bar, token, head, page_a);
+    }
+    if (b) {
+      tma_load_page(dst + box, &p.map_k[rank], bar, 0, head, page_b);
+      tma_load_page(dst + C::HALF + box, &p.map_v[rank], bar, 0, head, page_b);
+    }
+  }
+  ++ld.tile;
+}
+
+__device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity, unsigned int* status) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0 && ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicOr(status, TP_DEVSTATUS_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// What a warp knows of its item: Q's fragments, the softmax's state, and per column (row of Q) limits.
+template <int D, int NT>
+struct State {
+  uint32_t q[NT][D / 16][2];
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2], ck[NT][2];   // of the rows 8 nt + 2 t and + 1
+  int hi[NT][2], lo[NT][2];              // keys [lo, hi) are seen
+  int hi_all, lo_all;                    // every row sees [lo_all, hi_all)
+  int e_v;
+};
+
+// Q's rows into fragments: row g of tile nt, elements 32 t .. 32 t + 31 (16 at D 64) in the k order
+// that K's words give (word j: elements 4 j .. 4 j + 3 of them).
+template <int D, int NT>
+__device__ __forceinline__ void load_item(const AttendParams& p, const Item& it, int h, State<D, NT>& st, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const int rank = h / p.n_kv, head = h - rank * p.n_kv;
+  constexpr int W = D / 16;
+  int hi_all = 0x7FFFFFFF, lo_all = 0;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = 8 * nt + g;
+    uint4 raw[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+    if (r < it.rows) {
+      const int token = (it.row0 + r) / p.group, hq = (it.row0 + r) - token * p.group;
+      const __nv_bfloat16* src = p.q[rank] + static_cast<int64_t>(it.v.a + token) * p.ld_q +
+                                 (static_cast<int64_t>(head) * p.group + hq) * D + t * (D / 4);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) raw[i] = reinterpret_cast<const uint4*>(src)[i];
+    }
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // top < 2^(E - 126), E its exponent field: times 2^(141 - E) the row is below 2^15.  (A row of
+    // subnormals has E 0: its least steps are lost, 2^-133.)  A NaN or an infinity makes the row NaN.
+    const int E = static_cast<int>(top >> 7);
+    const float f0 = pow2((141 - E) / 2), f1 = pow2(141 - E - (141 - E) / 2);   // (2^141 itself is no fp32 value)
+    float back = p.scale_log2e * pow2((E - 141) / 2) * pow2(E - 141 - (E - 141) / 2);
+    if (E == 255) back = __uint_as_float(0x7FFFFFFFu);
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t v = E == 255 ? 0u : w[2 * j + i];
+        st.q[nt][j][i] = f16_pair(__uint_as_float(v << 16) * f0 * f1, __uint_as_float(v & 0xFFFF0000u) * f0 * f1);
+      }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      st.ck[nt][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c));
+      const int row = 8 * nt + 2 * t + c;
+      const int pos = it.v.pos0 + (it.row0 + row) / p.group;
+      st.hi[nt][c] = row < it.rows ? (p.causal ? min(it.v.len, pos + 1) : it.v.len) : 0;
+      st.lo[nt][c] = p.window > 0 ? pos - p.window + 1 : 0;
+      st.m[nt][c] = -INFINITY;
+      st.l[nt][c] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) st.o[nt][i][c] = 0.0f;
+  }
+  const int first = it.v.pos0 + it.row0 / p.group, last = it.v.pos0 + (it.row0 + max(it.rows, 1) - 1) / p.group;
+  if (p.causal) hi_all = first + 1;
+  if (p.window > 0) lo_all = last - p.window + 1;
+  st.hi_all = min(hi_all, it.v.len);
+  st.lo_all = lo_all;
+  st.e_v = -1000;
+}
+
+// One step of 32 keys from shared memory.
+template <int D, int NT>
+__device__ __forceinline__ void step(State<D, NT>& st, uint32_t data, uint32_t info0, uint32_t info1, int key0, int key_end, int lane) {
+  using C = Cfg<D, NT>;
+  constexpr int W = D / 16;       // words of K a lane has of a key = 16-element steps of the head
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t info[2] = {info0, info1};
+  const bool partial = key0 < st.lo_all || key0 + kStep > st.hi_all ||
+                       (info0 & info1 & kPageSeen) == 0 || (info0 & 0xFFu) == 255u || (info0 & 0xFF00u) == 0xFF00u ||
+                       (info1 & 0xFFu) == 255u || (info1 & 0xFF00u) == 0xFF00u;   // (warp-uniform)
+  float x[2][NT][4];
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    uint32_t ka[W], kb[W];        // keys 16 mt + g and + 8
+    if constexpr (D == 128) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint4 a = lds128(data + chunk_at<D>(16 * mt + g, 2 * t + c)), b = lds128(data + chunk_at<D>(16 * mt + g + 8, 2 * t + c));
+        ka[4 * c] = a.x, ka[4 * c + 1] = a.y, ka[4 * c + 2] = a.z, ka[4 * c + 3] = a.w;
+        kb[4 * c] = b.x, kb[4 * c + 1] = b.y, kb[4 * c + 2] = b.z, kb[4 * c + 3] = b.w;
+      }
+    } else {
+      const uint4 a = lds128(data + chunk_at<D>(16 * mt + g, t)), b = lds128(data + chunk_at<D>(16 * mt + g + 8, t));
+      ka[0] = a.x, ka[1] = a.y, ka[2] = a.z, ka[3] = a.w;
+      kb[0] = b.x, kb[1] = b.y, kb[2] = b.z, kb[3] = b.w;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[mt][nt][c] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const uint32_t a0 = f16_lo(ka[j]), a1 = f16_lo(kb[j]), a2 = f16_hi(ka[j]), a3 = f16_hi(kb[j]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma(x[mt][nt], a0, a1, a2, a3, st.q[nt][j][0], st.q[nt][j][1]);
+    }
+    // Scores in log2 units.  A page whose K or V is NaN makes its keys' scores NaN (its V enters as 0).
+    const float ks = (info[mt] & 0xFF00u) == 0xFF00u ? __uint_as_float(0x7FFFFFFFu) : e8m0_value(info[mt] & 0xFFu);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[mt][nt][c] *= st.ck[nt][c & 1] * ks;
+    if (partial) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int key = key0 + 16 * mt + g + 8 * (c >> 1);
+          if (key >= st.hi[nt][c & 1] || key < st.lo[nt][c & 1] || (info[mt] & kPageSeen) == 0) x[mt][nt][c] = -INFINITY;
+        }
+    }
+  }
+  // The running maximum of each row, and the largest V exponent.
+  bool grew = false;
+  float alpha[NT][2], ms[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float mx = fmaxf(fmaxf(x[0][nt][c], x[0][nt][c + 2]), fmaxf(x[1][nt][c], x[1][nt][c + 2]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      const float m_new = fmaxf(st.m[nt][c], mx);
+      ms[nt][c] = m_new == -INFINITY ? 0.0f : m_new;
+      grew |= m_new > st.m[nt][c];
+      alpha[nt][c] = ex2(st.m[nt][c] - ms[nt][c]);
+      st.m[nt][c] = m_new;
+    }
+  int e[2], e_new = st.e_v;
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    const int byte = static_cast<int>((info[mt] >> 8) & 0xFFu);
+    e[mt] = byte == 255 || (info[mt] & kPageSeen) == 0 ? -127 : byte - 127;
+    e_new = max(e_new, e[mt]);
+  }
+  if (__any_sync(0xffffffffu, grew) || e_new > st.e_v) {
+    const float f = pow2(max(st.e_v - e_new, -127));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        st.l[nt][c] *= alpha[nt][c];
+        alpha[nt][c] *= f;
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) st.o[nt][i][c] *= alpha[nt][c & 1];
+    }
+    st.e_v = e_new;
+  }
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    // P^T as the B operand: S^T has a key a lane group, B wants a row a lane group.
+    const float f = pow2(e[mt] - e_new + 14);
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float y[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        y[c] = ex2(x[mt][nt][c] - ms[nt][c & 1]);
+        st.l[nt][c & 1] += y[c];
+      }
+      pb[nt][0] = transpose8x8(f16_pair(y[0] * f, y[1] * f));
+      pb[nt][1] = transpose8x8(f16_pair(y[2] * f, y[3] * f));
+    }
+    // V^T: lane (g, t) has elements W g .. of the keys 2 t, 2 t + 1, 2 t + 8 and 2 t + 9.
+    constexpr int VW = D / 32;    // words of a key
+    uint32_t v[4][VW];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int key = 16 * mt + 2 * t + (k & 1) + 8 * (k >> 1);
+      if constexpr (D == 128) {
+        const uint4 w = lds128(data + C::HALF + chunk_at<D>(key, g));
+        v[k][0] = w.x, v[k][1] = w.y, v[k][2] = w.z, v[k][3] = w.w;
+      } else {
+        const uint2 w = lds64(data + C::HALF + chunk_at<D>(key, g >> 1) + 8 * (g & 1));
+        v[k][0] = w.x, v[k][1] = w.y;
+      }
+      // What no row sees may hold anything, a NaN times 0 among it.
+      if (partial && (key0 + key >= key_end || (info[mt] & kPageSeen) == 0 || (info[mt] & 0xFF00u) == 0xFF00u)) {
+#pragma unroll
+        for (int i = 0; i < VW; ++i) v[k][i] = 0;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VW; ++i) {
+      const uint32_t ab = __byte_perm(v[0][i], v[1][i], 0x5140), cd = __byte_perm(v[2][i], v[3][i], 0x5140);
+      const uint32_t ab2 = __byte_perm(v[0][i], v[1][i], 0x7362), cd2 = __byte_perm(v[2][i], v[3][i], 0x7362);
+      const uint32_t a0 = f16_lo(ab), a1 = f16_hi(ab), a2 = f16_lo(cd), a3 = f16_hi(cd);
+      const uint32_t b0 = f16_lo(ab2), b1 = f16_hi(ab2), b2 = f16_lo(cd2), b3 = f16_hi(cd2);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma(st.o[nt][2 * i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        mma(st.o[nt][2 * i + 1], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Ends an item's piece: O / l to the output where the piece is the whole item, else to `piece`
+// (shared memory) with the rows' m and l.
+template <int D, int NT>
+__device__ __forceinline__ void end_piece(const AttendParams& p, const Item& it, int h, State<D, NT>& st, bool whole, uint32_t piece, int lane) {
+  using C = Cfg<D, NT>;
+  const int g = lane >> 2, t = lane & 3;
+  const int rank = h / p.n_kv, head = h - rank * p.n_kv;
+  const float fe = e8m0_value(static_cast<uint32_t>(max(st.e_v, -127) + 127));
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float l = st.l[nt][c];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const float inv = l == 0.0f ? 0.0f : 0x1p-14f / l;
+      float o[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        o[2 * i] = st.o[nt][i][c] * inv * fe;
+        o[2 * i + 1] = st.o[nt][i][c + 2] * inv * fe;
+      }
+      const int row = 8 * nt + 2 * t + c;   // elements D/8 g .. of it
+      if (!whole) {
+        const uint32_t dst = piece + (row * D + g * (D / 8)) * 4;
+#pragma unroll
+        for (int i = 0; i < D / 8; i += 4)
+          ptx::st_shared_v4(dst + 4 * i, __float_as_uint(o[i]), __float_as_uint(o[i + 1]), __float_as_uint(o[i + 2]), __float_as_uint(o[i + 3]));
+        if (g == 0) {
+          const uint32_t ml = piece + (C::ROWS * D + 2 * row) * 4;
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml), "f"(st.m[nt][c]), "f"(l) : "memory");
+        }
+      } else if (row < it.rows) {
+        const int token = (it.row0 + row) / p.group, hq = it.row0 + row - token * p.group;
+        __nv_bfloat16* dst = p.out[rank] + static_cast<int64_t>(it.v.a + token) * p.ldo +
+                             (static_cast<int64_t>(head) * p.group + hq) * D + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < D / 8; i += 8)
+          reinterpret_cast<uint4*>(dst)[i / 8] = make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]),
+                                                            pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7]));
+      }
+    }
+}
+
+// Joins up to `n` pieces of a row: weights l 2^(m - max m); 0 where no piece has seen a key.
+template <typename ML, typename O4>
+__device__ __forceinline__ float4 join_row(int n, ML&& ml, O4&& o4) {
+  float top = -INFINITY;
+  for (int i = 0; i < n; ++i) top = fmaxf(top, ml(i).x);
+  if (top == -INFINITY) top = 0.0f;
+  float sum = 0.0f;
+  float4 acc = make_float4(0, 0, 0, 0);
+  for (int i = 0; i < n; ++i) {
+    const float2 v = ml(i);
+    const float w = v.y * ex2(v.x - top);
+    const float4 o = o4(i);
+    sum += w;
+    acc.x += w * o.x, acc.y += w * o.y, acc.z += w * o.z, acc.w += w * o.w;
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+}
+
+__device__ __forceinline__ void store_row4(const AttendParams& p, int a, int h, int row, int col, int D, const float4& v) {
+  const int rank = h / p.n_kv, head = h - rank * p.n_kv;
+  const int token = row / p.group, hq = row - token * p.group;
+  __nv_bfloat16* dst = p.out[rank] + static_cast<int64_t>(a + token) * p.ldo + (static_cast<int64_t>(head) * p.group + hq) * D + col;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+// Where the steps of all items are cut: CTA c of n has the steps from total * c / n on.
+__device__ __forceinline__ int64_t cut(int64_t total, int64_t c, int64_t n) { return total * c / n; }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_constant__ AttendParams p) {
+  using C = Cfg<D, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  auto* ctl = reinterpret_cast<Ctrl<C::STAGES>*>(base + C::OFF_CTRL);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = ptx::smem_addr(base) + warp * C::RING;
+  const uint32_t head_piece = ptx::smem_addr(base) + C::OFF_HEAD + warp * C::PIECE;
+  pdl_launch_dependents();
+  if (lane == 0) {
+    for (int i = 0; i < C::STAGES; ++i) ptx::mbar_init(ptx::smem_addr(&ctl->full[warp][i]), 1);
+    ctl->piece[warp][0].valid = ctl->piece[warp][1].valid = 0;
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  __syncwarp();
+  pdl_wait();
+
+  // This CTA's steps [u0, u1) of `total`, and the item and step at which this warp's part begins.
+  int64_t u0 = 0, u1 = 0, total = 0, n_cta = 1;
+  Start my{0, 0, 0, 0};
+  int count = 0, block = 0;
+  if (p.per_item) {
+    const int64_t slot = blockIdx.x;
+    my.h = blockIdx.y;
+    my.s = find_sequence(p.b, slot, C::ROWS, p.group, 1, lane);
+    if (my.s < 0) return;
+    const SeqView v = seq_view(p.b, my.s);
+    block = static_cast<int>(slot - (static_cast<int64_t>(v.a) * p.group / C::ROWS + my.s));
+    if (static_cast<int64_t>(block) * C::ROWS >= static_cast<int64_t>(v.n) * p.group) return;
+    const Item it = item_of<C::ROWS>(p, v, block);
+    u1 = total = it.tiles;
+    my.at = u1 * warp / kWarps;
+    my.tile = static_cast<int>(my.at) + it.tile0;
+    count = static_cast<int>(u1 * (warp + 1) / kWarps - my.at);
+  } else {
+    // Sequences are dealt to the threads in runs; a scan of their steps finds the cuts.
+    const int run = (p.b.n_seqs + kThreads - 1) / kThreads;
+    const int s0 = min(static_cast<int>(threadIdx.x) * run, p.b.n_seqs), s1 = min(s0 + run, p.b.n_seqs);
+    int64_t mine = 0;
+    for (int s = s0; s < s1; ++s) mine += item_of<C::ROWS>(p, seq_view(p.b, s), 0).tiles;
+    mine *= p.heads;
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 31) ctl->sums[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+      total += ctl->sums[w];
+      if (w < warp) upto += ctl->sums[w];
+    }
+    // (At least one step a warp, so that no CTA between two others is empty.)
+    n_cta = min(static_cast<int64_t>(gridDim.x), (total + kWarps - 1) / kWarps);
+    if (blockIdx.x < n_cta) {
+      u0 = cut(total, blockIdx.x, n_cta);
+      u1 = cut(total, blockIdx.x + 1, n_cta);
+    }
+    int64_t before = upto - mine;
+    for (int s = s0; s < s1 && before < u1; ++s) {
+      const Item it = item_of<C::ROWS>(p, seq_view(p.b, s), 0);
+      const int64_t after = before + static_cast<int64_t>(it.tiles) * p.heads;
+      if (after > u0) {
+        for (int w = 0; w < kWarps; ++w) {
+          const int64_t at = u0 + (u1 - u0) * w / kWarps;
+          if (at >= before && at < after) {
+            const int h = static_cast<int>((at - before) / it.tiles);
+            ctl->start[w] = {s, h, it.tile0 + static_cast<int>(at - before - static_cast<int64_t>(h) * it.tiles), at};
+          }
+        }
+      }
+      before = after;
+    }
+    __syncthreads();
+    my = ctl->start[warp];
+    count = static_cast<int>((u1 - u0) * (warp + 1) / kWarps - (u1 - u0) * warp / kWarps);
+  }
+
+  if (count > 0) {
+    // The loader and the worker walk the same steps, the loader STAGES ahead.
+    SeqView v = seq_view(p.b, my.s);
+    Item it = item_of<C::ROWS>(p, v, block);
+    Loader ld{my.s, my.h, my.tile, it.tile0 + it.tiles, -64, 0, 0, v.len};
+    int issued = 0;
+    for (; issued < C::STAGES && issued < count; ++issued) issue_step<D, NT>(p, ld, issued, ring, ctl, warp, lane);
+    __syncwarp();
+    int s = my.s, h = my.h, tile = my.tile, stage = 0;
+    uint32_t parity = 0;
+    bool ok = true;
+    State<D, NT> st;
+    for (int k = 0; k < count;) {
+      load_item<D, NT>(p, it, h, st, lane);
+      const int from = tile, end = it.tile0 + it.tiles;
+      const int n = min(end - tile, count - k);
+      if (n <= 0) break;   // (the lengths changed under the kernel)
+      for (int i = 0; i < n; ++i, ++k, ++tile) {
+        ok = __all_sync(0xffffffffu, wait_full(ptx::smem_addr(&ctl->full[warp][stage]), parity, p.b.status)) && ok;
+        const uint32_t info0 = ctl->info[warp][stage][0], info1 = ctl->info[warp][stage][1];
+        step<D, NT>(st, ring + stage * C::STAGE, info0, info1, tile * kStep, it.key_end, lane);
+        __syncwarp();   // every lane has read the stage
+        if (issued < count) {
+          issue_step<D, NT>(p, ld, stage, ring, ctl, warp, lane);
+          ++issued;
+          __syncwarp();
+        }
+        if (++stage == C::STAGES) stage = 0, parity ^= 1;
+      }
+      const bool first = from == it.tile0, last = tile == end, whole = first && last;
+      // A piece that the warp's part cuts: one that began before it goes to the first place, its last to its (drained) ring.
+      const int place = first ? 1 : 0;
+      end_piece<D, NT>(p, it, h, st, whole, place == 0 ? head_piece : ring, lane);
+      if (!whole && lane == 0)
+        ctl->piece[warp][place] = Piece{my.at + k + (end - tile), 1, first, last, s, h, it.row0};
+      if (k < count) {
+        if (++h == p.heads) {
+          h = 0;
+          do {
+            v = seq_view(p.b, ++s);
+            it = item_of<C::ROWS>(p, v, 0);
+          } while (it.tiles == 0 && s + 1 < p.b.n_seqs);
+        }
+        tile = it.tile0;
+      }
+    }
+    if (!ok && lane == 0) atomicOr(p.b.status, TP_DEVSTATUS_TIMEOUT);
+  }
+  __syncthreads();
+
+  // Pieces of one item lie in consecutive warps, in key order.
+  int4 join = make_int4(0, 0, 0, 0);
+  for (int i = 0; i < 2 * kWarps;) {
+    const Piece& lead = ctl->piece[i >> 1][i & 1];
+    if (!lead.valid) {
+      ++i;
+      continue;
+    }
+    int member[kWarps + 1], n = 0;
+    bool last = false;
+    for (; i < 2 * kWarps; ++i) {
+      const Piece& q = ctl->piece[i >> 1][i & 1];
+      if (!q.valid) continue;
+      if (q.s != lead.s || q.h != lead.h) break;
+      if (n <= kWarps) member[n++] = i;
+      last = q.last;
+    }
+    const bool whole = lead.first && last;
+    const SeqView v = seq_view(p.b, lead.s);
+    const int rows = static_cast<int>(min(static_cast<int64_t>(C::ROWS), static_cast<int64_t>(v.n) * p.group - lead.row0));
+    auto piece_at = [&](int m) {
+      return reinterpret_cast<const float*>((m & 1) == 0 ? base + C::OFF_HEAD + (m >> 1) * C::PIECE : base + (m >> 1) * C::RING);
+    };
+    float* part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (lead.first ? 1 : 0)) * (C::PIECE / 4);
+    for (int at = threadIdx.x * 4; at < C::ROWS * D; at += kThreads * 4) {
+      const int row = at / D, col = at - row * D;
+      const float4 o = join_row(
+          n, [&](int m) { return *reinterpret_cast<const float2*>(piece_at(member[m]) + C::ROWS * D + 2 * row); },
+          [&](int m) { return *reinterpret_cast<const float4*>(piece_at(member[m]) + at); });
+      if (whole) {
+        if (row < rows) store_row4(p, v.a, lead.h, lead.row0 + row, col, D, o);
+      } else {
+        *reinterpret_cast<float4*>(part + at) = o;
+        if (col == 0) {
+          float top = -INFINITY, l = 0.0f;
+          for (int m = 0; m < n; ++m) top = fmaxf(top, piece_at(member[m])[C::ROWS * D + 2 * row]);
+          const float ref = top == -INFINITY ? 0.0f : top;
+          for (int m = 0; m < n; ++m)
+            l += piece_at(member[m])[C::ROWS * D + 2 * row + 1] * ex2(piece_at(member[m])[C::ROWS * D + 2 * row] - ref);
+          part[C::ROWS * D + 2 * row] = top;
+          part[C::ROWS * D + 2 * row + 1] = l;
+        }
+      }
+    }
+    if (lead.first && !last) {
+      // CTA c holds step u where c is the largest with cut(c) <= u.
+      const int64_t u = lead.item_end - 1;
+      const int64_t c_last = ((u + 1) * n_cta + total - 1) / total - 1;
+      join = make_int4(static_cast<int>(c_last - blockIdx.x) + 1, v.a, rows, lead.h);
+    }
+  }
+  if (!p.per_item && threadIdx.x == 0) p.joins[blockIdx.x] = join;
+}
+
+// Joins the items that lie in several CTAs: block c the one that begins in CTA c and goes beyond it
+// (its piece in that CTA's second part, the others in the first parts of those behind).
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ AttendParams p) {
+  using C = Cfg<D, NT>;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int4 join = p.joins[blockIdx.x];
+  const int n = join.x;
+  if (n == 0) return;
+  const float* own = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * (C::PIECE / 4);
+  auto part = [&](int i) { return i == 0 ? own : own + (2 * i - 1) * static_cast<int64_t>(C::PIECE / 4); };
+  for (int at = threadIdx.x * 4; at < join.z * D; at += kThreads * 4) {
+    const int row = at / D, col = at - row * D;
+    const float4 o = join_row(
+        n, [&](int i) { return *reinterpret_cast<const float2*>(part(i) + C::ROWS * D + 2 * row); },
+        [&](int i) { return *reinterpret_cast<const float4*>(part(i) + at); });
+    store_row4(p, join.y, join.w, row, col, D, o);
+  }
+}
+
+// The tensor map of a rank's codes: [n_pages][n_kv][page_size][D] bytes, a box of the tokens of one
+// page that a step takes.
+tp_status encode_pages(CUtensorMap* m, const void* codes, const tp_paged_cache& c, int64_t ld_page) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  if (fn == nullptr) return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t D = static_cast<cuuint64_t>(c.head_dim), P = static_cast<cuuint64_t>(c.page_size);
+  const cuuint64_t dims[4] = {D, P, static_cast<cuuint64_t>(c.n_kv_heads), static_cast<cuuint64_t>(c.n_pages)};
+  const cuuint64_t strides[3] = {D, D * P, static_cast<cuuint64_t>(ld_page)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(c.head_dim), static_cast<cuuint32_t>(c.page_size < kStep ? c.page_size : kStep), 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box, ones,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+  return TP_OK;
+}
+
+tp_status current_device(int* dev) {
+  const cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (*dev < 0 || *dev >= 64) return fail(TP_ERR_UNSUPPORTED, "device index %d", *dev);
+  return TP_OK;
+}
+
+struct Plan {
+  bool one_row_tile;     // 8 rows an item, else 16
+  bool per_item;
+  int64_t slots;         // per_item: blocks of rows
+  int ctas;              // else
+  size_t ws_bytes;
+};
+
+Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int64_t T, int group, int sms) {
+  Plan pl{};
+  const int64_t rows = static_cast<int64_t>(b.max_new) * group;
+  pl.one_row_tile = rows <= 8;
+  const int R = pl.one_row_tile ? 8 : 16;
+  pl.slots = T * group / R + b.n_seqs;
+  const int64_t items = static_cast<int64_t>(b.n_seqs) * c.n_ranks * c.n_kv_heads;
+  const int64_t keys = b.max_pages * c.page_size;
+  // Few short items: each by one CTA, no second launch.  Otherwise equal parts.
+  pl.per_item = rows > 16 || (items <= sms && keys <= 1024);
+  pl.ctas = sms;
+  if (!pl.per_item) {
+    const size_t piece = static_cast<size_t>(R) * (c.head_dim + 2) * 4;
+    pl.ws_bytes = static_cast<size_t>(pl.ctas) * (2 * piece + sizeof(int4));
+  }
+  return pl;
+}
+
+template <int D, int NT>
+tp_status launch(const Plan& pl, const AttendParams& p, cudaStream_t stream) {
+  using C = Cfg<D, NT>;
+  struct Raised {
+    std::once_flag once;
+    cudaError_t err = cudaSuccess;
+  };
+  static Raised raised[64];
+  int dev = 0;
+  tp_status st = current_device(&dev);
+  if (st != TP_OK) return st;
+  Raised& r = raised[dev];
+  std::call_once(r.once, [&] {
+    r.err = cudaFuncSetAttribute(paged_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
+  });
+  if (r.err != cudaSuccess) return cuda_fail(r.err, "cudaFuncSetAttribute(max dynamic shared memory)");
+  const dim3 grid = pl.per_item ? dim3(static_cast<unsigned>(pl.slots), static_cast<unsigned>(p.heads))
+                                : dim3(static_cast<unsigned>(pl.ctas));
+  cudaError_t e = launch_pdl(paged_rows_kernel<D, NT>, grid, dim3(kThreads), C::SMEM, stream, p);
+  if (e == cudaSuccess && !pl.per_item)
+    e = launch_pdl(paged_join_kernel<D, NT>, dim3(static_cast<unsigned>(pl.ctas)), dim3(kThreads), 0, stream, p);
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  return TP_OK;
+}
+
+tp_status check_attention(const tp_paged_cache* c, const tp_paged_batch* b, int64_t T, int n_heads, bool* empty) {
+  const tp_status st = check_paged(c, b, T, n_heads, empty);
+  if (st != TP_OK) return st;
+  if (n_heads < 1 || n_heads % c->n_kv_heads != 0)
+    return fail(TP_ERR_INVALID_ARG, "n_heads (%d) must be a multiple of n_kv_heads (%d)", n_heads, c->n_kv_heads);
+  if (static_cast<int64_t>(T) * (n_heads / c->n_kv_heads) + b->n_seqs > 0x7FFFFFFF ||
+      static_cast<int64_t>(c->n_ranks) * c->n_kv_heads > 65535)
+    return fail(TP_ERR_UNSUPPORTED, "more than 2^31-1 rows of a KV head, or 65535 KV heads of all ranks");
+  return TP_OK;
+}
+
+}  // namespace
+}  // namespace tp
+
+extern "C" {
+
+size_t tp_attention_paged_workspace_bytes(const tp_paged_cache* cache, const tp_paged_batch* batch, int64_t T, int n_heads) {
+  using namespace tp;
+  size_t bytes = 0;
+  (void)guarded([&]() -> tp_status {
+    clear_error();
+    bool empty = false;
+    const tp_status st = check_attention(cache, batch, T, n_heads, &empty);
+    if (st != TP_OK || empty) return st;
+    const int sms = sm_count();
+    if (sms <= 0) return fail(TP_ERR_CUDA, "no CUDA device");
+    bytes = make_plan(*cache, *batch, T, n_heads / cache->n_kv_heads, sms).ws_bytes;
+    return TP_OK;
+  });
+  return bytes;
+}
+
+tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_batch* batch, const void* const* q,
+                                 int64_t ld_q, int64_t T, int n_heads, float scale, int causal, int window,
+                                 void* workspace, size_t ws_bytes, void* const* out, int64_t ldo, tp_stream_t stream) {
+  using namespace tp;
+  return guarded([&]() -> tp_status {
+    clear_error();
+    bool empty = false;
+    tp_status st = check_attention(cache, batch, T, n_heads, &empty);
+    if (st != TP_OK) return st;
+    const tp_paged_cache& c = *cache;
+    const int64_t wide = static_cast<int64_t>(n_heads) * c.head_dim;
+    if ((ld_q != 0 && ld_q < wide) || (ldo != 0 && ldo < wide))
+      return fail(TP_ERR_INVALID_ARG, "a row stride (ld_q %lld, ldo %lld) is smaller than its row", (long long)ld_q, (long long)ldo);
+    if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal))
+      return fail(TP_ERR_INVALID_ARG, "causal must be 0 or 1, and window >= 0 and 0 without causal; got %d, %d", causal, window);
+    if (!(scale - scale == 0.0f)) return fail(TP_ERR_INVALID_ARG, "scale must be finite");
+    if (empty) return TP_OK;
+    if (q == nullptr || out == nullptr) return fail(TP_ERR_INVALID_ARG, "q or out is NULL");
+    if (ld_q % 8 != 0 || ldo % 8 != 0)
+      return fail(TP_ERR_ALIGNMENT, "ld_q (%lld) and ldo (%lld) must be multiples of 8", (long long)ld_q, (long long)ldo);
+    AttendParams p{};
+    for (int r = 0; r < c.n_ranks; ++r) {
+      if (q[r] == nullptr || out[r] == nullptr) return fail(TP_ERR_INVALID_ARG, "q[%d] or out[%d] is NULL", r, r);
+      if (!aligned16(q[r]) || !aligned16(out[r]))
+        return fail(TP_ERR_ALIGNMENT, "q[%d] or out[%d] is not 16-byte aligned", r, r);
+      p.q[r] = static_cast<const __nv_bfloat16*>(q[r]);
+      p.out[r] = static_cast<__nv_bfloat16*>(out[r]);
+      p.ks[r] = static_cast<const uint8_t*>(c.k_scales[r]);
+      p.vs[r] = static_cast<const uint8_t*>(c.v_scales[r]);
+    }
+    const int sms = sm_count();
+    if (sms <= 0) return fail(TP_ERR_CUDA, "no CUDA device");
+    const Plan pl = make_plan(c, *batch, T, n_heads / c.n_kv_heads, sms);
+    if (pl.ws_bytes > 0 && (workspace == nullptr || ws_bytes < pl.ws_bytes))
+      return fail(TP_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace == nullptr ? size_t(0) : ws_bytes, pl.ws_bytes);
+    if (pl.ws_bytes > 0 && !aligned16(workspace)) return fail(TP_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+    unsigned int* status = status_word();
+    if (status == nullptr) return fail(TP_ERR_CUDA, "cannot locate the kernel status word");
+    const int64_t ld_page = c.ld_page != 0 ? c.ld_page : static_cast<int64_t>(c.n_kv_heads) * c.page_size * c.head_dim;
+    for (int r = 0; r < c.n_ranks && c.n_pages > 0; ++r) {
+      st = encode_pages(&p.map_k[r], c.k[r], c, ld_page);
+      if (st == TP_OK) st = encode_pages(&p.map_v[r], c.v[r], c, ld_page);
+      if (st != TP_OK) return st;
+    }
+    p.b = batch_view(c, *batch, T, status);
+    p.ld_q = ld_q != 0 ? ld_q : wide;
+    p.ldo = ldo != 0 ? ldo : wide;
+    p.ld_scales = c.ld_scales != 0 ? c.ld_scales : c.n_kv_heads;
+    p.n_kv = c.n_kv_heads;
+    p.group = n_heads / c.n_kv_heads;
+    p.heads = c.n_ranks * c.n_kv_heads;
+    p.causal = causal;
+    p.window = window <= p.b.max_keys ? window : 0;
+    p.scale_log2e = scale * 1.4426950408889634f;
+    p.per_item = pl.per_item ? 1 : 0;
+    if (!pl.per_item) {
+      p.joins = static_cast<int4*>(workspace);
+      p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.ctas * sizeof(int4));
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (c.head_dim == 128) return pl.one_row_tile ? launch<128, 1>(pl, p, s) : launch<128, 2>(pl, p, s);
+    return pl.one_row_tile ? launch<64, 1>(pl, p, s) : launch<64, 2>(pl, p, s);
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,746 @@
+"""The paged 8-bit cache against float64 numpy: appending with rotation, attention, and both as they are used together.
+
+Unrotated keys, values, and rotations by quarter turns (cosines and sines of 0, 1 and -1) have one
+right code and are compared bit for bit.  The rest is held to bounds made of the steps that round:
+
+* a rotated element: two products and a sum in fp32, 3 * 2^-24 of |x1 c| + |x2 s|; stored bf16 2^-8,
+  a code 2^-4 or half the subnormal spacing, 2^-10 times its scale;
+* a score: products are exact in the tensor core, each step of 16 adds into an fp32 accumulator
+  without rounding to nearest, at most 2^-22 of the sum of magnitudes a step, and three more
+  roundings; in log2 units it passes one subtraction and the exponential, 2^-22 relative and 2^-24 of
+  its argument each; a probability moves by the score's error d relative (e^d - 1 <= 1.01 d here);
+* a probability in fp16: 2^-11 relative, or half its least step, 2^-25 / 2^7, times the largest value's scale;
+* the sum over keys: a step of 16 adds without rounding to nearest, 2^-22 of the sum of weights times |v|;
+* the join of parts and the division: 2^-20 relative.
+"""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8_oracle as F
+from oracle import paged_oracle as P
+
+pytestmark = pytest.mark.gpu
+
+tp = pytest.importorskip("tensor_sharded_linear_tp_gb300")
+
+DEV = "cuda"
+E4M3, E8M0, BF16 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.bfloat16
+
+
+@pytest.fixture(autouse=True)
+def _device_status_clean():
+    yield
+    tp.tp_device_status()
+
+
+def f64(t):
+    torch.cuda.synchronize()
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def raw(t):
+    torch.cuda.synchronize()
+    return t.detach().view(torch.uint8).cpu().numpy().copy()
+
+
+def to_bf16(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(BF16).to(DEV)
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+class Case:
+    """A batch of sequences [(cached, new)] over a cache of random pages, on the GPU and as numpy arrays."""
+
+    def __init__(self, seqs, p=1, n_kv=2, group=1, D=128, page=16, seed=0, spare=2, front=0, behind=0, split=False,
+                 fill=None, spread=0.5):
+        rng = self.rng = np.random.default_rng(seed)
+        self.p, self.n_kv, self.group, self.D, self.page = p, n_kv, group, D, page
+        self.heads = n_kv * group
+        self.seqs, row = [], front                    # (first row, new rows, length)
+        for old, new in seqs:
+            self.seqs.append((row, new, old + new))
+            row += new
+        self.T = row + behind
+        need = [-(-n // page) for _, _, n in self.seqs]
+        self.n_pages = sum(need) + spare
+        order = rng.permutation(self.n_pages)
+        self.max_pages = max(need + [1])
+        self.table = np.zeros((len(seqs), self.max_pages), dtype=np.int32)
+        at = 0
+        for s, n in enumerate(need):
+            self.table[s, :n] = order[at:at + n]
+            at += n
+        self.codes, self.scales = [], []              # [rank][k or v]
+        for _ in range(p):
+            x = rng.normal(size=(2, self.n_pages, n_kv, page, D)) * 2.0 ** rng.normal(0, spread, (2, self.n_pages, n_kv, 1, 1))
+            b = P.scale_byte(np.abs(x).max(axis=(3, 4)))
+            self.codes.append(F.f64_to_e4m3(x / F.scale_value(b)[..., None, None]))
+            self.scales.append(b)
+        if fill is not None:                          # slots that hold no token
+            for s, (_, _, n) in enumerate(self.seqs):
+                if n % page:
+                    for c in self.codes:
+                        c[:, self.table[s, n // page], :, n % page:] = fill
+        self.upload(split)
+
+    def upload(self, split=False):
+        def code(c):
+            return torch.from_numpy(c).to(DEV).view(E4M3)
+
+        def byte(b):
+            return torch.from_numpy(b).to(DEV).view(E8M0)
+        if split:   # K and V side by side in one allocation: strides from page to page
+            both = [code(np.ascontiguousarray(c.transpose(1, 0, 2, 3, 4))) for c in self.codes]
+            sc = [byte(np.ascontiguousarray(b.transpose(1, 0, 2))) for b in self.scales]
+            k, v = [c[:, 0] for c in both], [c[:, 1] for c in both]
+            ks, vs = [b[:, 0] for b in sc], [b[:, 1] for b in sc]
+        else:
+            k, v = [code(c[0]) for c in self.codes], [code(c[1]) for c in self.codes]
+            ks, vs = [byte(b[0]) for b in self.scales], [byte(b[1]) for b in self.scales]
+        self.cache = tp.PagedCache(k, v, ks, vs)
+        self.batch = self.make_batch()
+
+    def make_batch(self, max_new=None):
+        starts = [a for a, _, _ in self.seqs] + [self.seqs[-1][0] + self.seqs[-1][1]]
+        return tp.PagedBatch(i32(starts), i32([n for _, _, n in self.seqs]), i32(self.table.tolist()),
+                             max_new if max_new is not None else max(n for _, n, _ in self.seqs))
+
+    def got(self):
+        """The cache's codes and scales as they are on the GPU, [rank][k or v]."""
+        c = self.cache
+        return ([np.stack([raw(c.k[r]), raw(c.v[r])]) for r in range(self.p)],
+                [np.stack([raw(c.k_scales[r]), raw(c.v_scales[r])]) for r in range(self.p)])
+
+    def queries(self, std=1.0):
+        self.q = [to_bf16(self.rng.normal(0, std, (self.T, self.heads * self.D))) for _ in range(self.p)]
+        return self.q
+
+    def check(self, outs, scale=None, causal=True, window=0, before=None, what=""):
+        """Every row against the oracle; rows of no sequence as they were."""
+        scale = self.D ** -0.5 if scale is None else scale
+        for r in range(self.p):
+            got = f64(outs[r]).reshape(self.T, self.heads, self.D)
+            q = f64(self.q[r]).reshape(self.T, self.heads, self.D)
+            owned = np.zeros(self.T, dtype=bool)
+            for s, (a, n, length) in enumerate(self.seqs):
+                owned[a:a + n] = True
+                if n == 0:
+                    continue
+                K, V = (P.values(self.codes[r][i], self.scales[r][i], self.table[s], length) for i in (0, 1))
+                see = P.seen(n, length, causal, window)
+                want, w = P.attention(q[a:a + n], K, V, scale, see)
+                bound = attention_bound(q[a:a + n], K, V, scale, want, w, see)
+                bad = ~(np.abs(got[a:a + n] - want) <= bound)
+                assert not bad.any(), (what, r, s, np.argwhere(bad)[:5], got[a:a + n][bad][:5], want[bad][:5], bound[bad][:5])
+            if before is not None:
+                np.testing.assert_array_equal(got[~owned], f64(before[r]).reshape(got.shape)[~owned])
+
+
+def attention_bound(q, K, V, scale, want, w, see):
+    n, heads, D = q.shape
+    group = heads // K.shape[0]
+    bound = np.zeros_like(want)
+    keys = K.shape[1]
+    if keys == 0:
+        return bound
+    top_v = 2.0 * np.abs(V).max(axis=(1, 2))
+    for h in range(heads):
+        g = h // group
+        mag = abs(scale) * (np.abs(q[:, h]) @ np.abs(K[g]).T)                       # [n, keys]
+        d = mag * ((D // 16) * 2.0 ** -22 + 3 * 2.0 ** -24)
+        x = np.where(see, (q[:, h] @ K[g].T) * scale, 0.0)
+        span = np.abs(x).max(axis=1, keepdims=True) * 2
+        d = d + 2.0 ** -22 + span * 2.0 ** -23
+        wd = 1.01 * w[h] * d
+        total = np.abs(V[g])
+        err = wd @ total + (w[h] @ total) * (2.0 ** -11 + (keys // 16 + 1) * 2.0 ** -22 + 2.0 ** -20)
+        err += wd.sum(axis=1, keepdims=True) * np.abs(want[:, h])
+        err += keys * 2.0 ** -32 * top_v[g] * w[h].max(axis=1, keepdims=True)
+        bound[:, h] = 2.0 ** -8 * (np.abs(want[:, h]) + err) + err
+    return bound
+
+
+def fresh(q):
+    return [torch.full_like(t, 7.0) for t in q]
+
+
+# ----------------------------------------------------------------------------- append
+
+QUARTERS = np.array([[1, 0], [0, 1], [-1, 0], [0, -1]], dtype=np.float32)   # (cos, sin)
+
+
+def quarter_table(rng, rows, rot):
+    turn = QUARTERS[rng.integers(0, 4, (rows, rot // 2))]
+    return np.concatenate([turn[..., 0], turn[..., 1]], 1).astype(np.float32)
+
+
+def qkv_of(c, std=1.0):
+    width = (c.heads + 2 * c.n_kv) * c.D
+    out = []
+    for _ in range(c.p):
+        x = c.rng.normal(0, std, (c.T, width)) * 2.0 ** c.rng.integers(-4, 5, (c.T, 1))
+        out.append(to_bf16(x))
+    return out
+
+
+def split(c, x):
+    x = x.reshape(c.T, c.heads + 2 * c.n_kv, c.D)
+    return x[:, :c.heads], x[:, c.heads:c.heads + c.n_kv], x[:, c.heads + c.n_kv:]
+
+
+BATCHES = [
+    [(0, 1)], [(15, 1)], [(16, 1)], [(0, 0), (3, 2), (7, 0)], [(0, 129)], [(5, 300)],
+    [(0, 1), (31, 1), (63, 1), (127, 1), (128, 1), (1000, 1), (0, 1)], [(100, 17), (0, 40), (129, 1), (64, 64)],
+]
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("D, rot, style", [(128, 128, "half"), (128, 48, "pairs"), (64, 64, "pairs"), (64, 16, "half"),
+                                           (128, 0, None)])
+@pytest.mark.parametrize("seqs", BATCHES, ids=str)
+def test_append_bit_exact(seqs, D, rot, style, page):
+    c = Case(seqs, p=2, n_kv=3, group=2, D=D, page=page, seed=len(seqs) + page, front=2, behind=3, split=page == 32)
+    qkv = qkv_of(c)
+    rows = max(n for _, _, n in c.seqs) + 1
+    cs = quarter_table(c.rng, rows, rot) if rot else None
+    q_out = [torch.full((c.T, c.heads * D), 7.0, dtype=BF16, device=DEV) for _ in range(c.p)]
+    tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch, rope=style, cos_sin=None if cs is None else torch.from_numpy(cs).to(DEV),
+                        q_out=q_out)
+    got_codes, got_scales = c.got()
+    pos = np.concatenate([np.arange(n - new, n) for _, new, n in c.seqs]).astype(int)
+    owned = np.concatenate([np.arange(a, a + n) for a, n, _ in c.seqs]).astype(int)
+    for r in range(c.p):
+        q, k, v = split(c, f64(qkv[r]))
+        if rot:
+            table = np.zeros((c.T, rot))
+            table[owned] = cs[pos]
+            q, k = P.rotate(q, table, style), P.rotate(k, table, style)
+        P.append(c.codes[r][0], c.scales[r][0], k, c.seqs, c.table)
+        P.append(c.codes[r][1], c.scales[r][1], v, c.seqs, c.table)
+        np.testing.assert_array_equal(got_scales[r], c.scales[r])
+        # (a zero's sign is lost where -0 + 0 met)
+        np.testing.assert_array_equal(F.e4m3_to_f64(got_codes[r]), F.e4m3_to_f64(c.codes[r]))
+        want = np.full((c.T, c.heads * D), 7.0)
+        want[owned] = q.reshape(c.T, -1)[owned]
+        np.testing.assert_array_equal(f64(q_out[r]), want)
+
+
+@pytest.mark.parametrize("style", ["half", "pairs"])
+@pytest.mark.parametrize("D, rot", [(128, 128), (64, 32)])
+def test_append_rotates_in_fp32(D, rot, style):
+    c = Case([(0, 50), (700, 33), (11, 1)], p=2, n_kv=2, group=3, D=D, page=16, seed=3, spread=3)
+    angle = np.outer(np.arange(800), 10000.0 ** (-np.arange(rot // 2) * 2 / rot))
+    cs = np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32)
+    qkv = qkv_of(c)
+    q_out = tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch, rope=style, cos_sin=torch.from_numpy(cs).to(DEV))
+    got_codes, got_scales = c.got()
+    pos = np.concatenate([np.arange(n - new, n) for _, new, n in c.seqs])
+    for r in range(c.p):
+        q, k, _ = split(c, f64(qkv[r]))
+        t = cs[pos].astype(np.float64)
+        err = 3 * 2.0 ** -24 * 2 * np.abs(q).max(axis=2, keepdims=True)
+        want = P.rotate(q, t, style)
+        got = f64(q_out[r]).reshape(want.shape)
+        assert np.all(np.abs(got - want) <= 2.0 ** -8 * (np.abs(want) + err) + err)
+        want = P.rotate(k, t, style)
+        err = 3 * 2.0 ** -24 * 2 * np.abs(k).max(axis=2, keepdims=True)
+        for s, (a, n, length) in enumerate(c.seqs):
+            v = P.values(got_codes[r][0], got_scales[r][0], c.table[s], length)[:, length - n:].transpose(1, 0, 2)
+            pages = c.table[s][np.arange(length - n, length) // c.page]
+            size = F.scale_value(got_scales[r][0][pages])[:, :, None]
+            w, e = want[a:a + n], err[a:a + n]
+            assert np.all(np.abs(v - w) <= np.maximum(2.0 ** -4 * (np.abs(w) + e), 2.0 ** -10 * size) + e)
+
+
+def test_append_positions_of_their_own():
+    c = Case([(0, 9), (30, 4)], p=1, n_kv=2, group=1, D=64, page=16, seed=5)
+    cs = quarter_table(c.rng, 50, 64)
+    positions = c.rng.integers(0, 50, c.T)
+    qkv = qkv_of(c)
+    q, = tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch, rope="half", cos_sin=torch.from_numpy(cs).to(DEV),
+                             positions=i32(positions.tolist()))
+    want, k, v = split(c, f64(qkv[0]))
+    np.testing.assert_array_equal(f64(q), P.rotate(want, cs[positions], "half").reshape(c.T, -1))
+    P.append(c.codes[0][0], c.scales[0][0], P.rotate(k, cs[positions], "half"), c.seqs, c.table)
+    np.testing.assert_array_equal(c.got()[1][0][0], c.scales[0][0])
+
+
+def test_append_strides_and_in_place():
+    c = Case([(3, 20), (0, 5)], p=2, n_kv=2, group=2, D=128, page=16, seed=6, split=True)
+    wide = (c.heads + 2 * c.n_kv) * c.D
+    whole = [to_bf16(c.rng.normal(size=(c.T, wide + 64))) for _ in range(2)]
+    qkv = [t[:, 16:16 + wide] for t in whole]
+    cs = torch.from_numpy(quarter_table(c.rng, 40, 128)).to(DEV)
+    wider = torch.zeros((40, 160), device=DEV)
+    wider[:, :128] = cs
+    apart = tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch, rope="half", cos_sin=wider[:, :128])
+    first = c.got()
+    before = [t.clone() for t in whole]
+    there = tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch, rope="half", cos_sin=cs,
+                                q_out=[t[:, :c.heads * c.D] for t in qkv])
+    for r in range(2):
+        assert torch.equal(apart[r], there[r])
+        np.testing.assert_array_equal(c.got()[0][r], first[0][r])           # again: the same cache
+        np.testing.assert_array_equal(c.got()[1][r], first[1][r])
+        keep = torch.ones(whole[r].shape[1], dtype=torch.bool, device=DEV)
+        keep[16:16 + c.heads * c.D] = False
+        assert torch.equal(whole[r][:, keep], before[r][:, keep])
+
+
+@pytest.mark.parametrize("page", [16, 128])
+def test_append_special_values(page):
+    """Zeros never raise a page's scale; a NaN or an infinity makes its page and head NaN; tiny and huge values."""
+    c = Case([(4, 3), (4, 3), (4, 3), (4, 3), (0, 3)], p=1, n_kv=2, group=1, D=64, page=page, seed=7)
+    x = f64(qkv_of(c)[0]).reshape(c.T, 6, 64)
+    x[0:3, 2:] = 0
+    x[3, 2, 5], x[4, 5, 1] = np.nan, np.inf
+    x[6:9, 2:] *= 2.0 ** 110
+    x[9:12, 2:] *= 2.0 ** -120
+    x[12:15, 2:] = 0
+    qkv = [to_bf16(x.reshape(c.T, -1))]
+    q, = tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch)
+    np.testing.assert_array_equal(f64(q), f64(qkv[0])[:, :c.heads * 64])
+    _, k, v = split(c, f64(qkv[0]))
+    P.append(c.codes[0][0], c.scales[0][0], k, c.seqs, c.table)
+    P.append(c.codes[0][1], c.scales[0][1], v, c.seqs, c.table)
+    codes, scales = c.got()
+    np.testing.assert_array_equal(scales[0], c.scales[0])
+    for s, (_, _, length) in enumerate(c.seqs):      # (a NaN's payload means nothing; slots behind stay)
+        np.testing.assert_array_equal(F.e4m3_to_f64(codes[0][:, c.table[s, 0], :, :length]),
+                                      F.e4m3_to_f64(c.codes[0][:, c.table[s, 0], :, :length]))
+        np.testing.assert_array_equal(codes[0][:, c.table[s, 0], :, length:], c.codes[0][:, c.table[s, 0], :, length:])
+
+
+def test_append_token_by_token_equals_the_oracle_and_decays_gently():
+    c = Case([(0, 1)], p=1, n_kv=2, group=1, D=128, page=32, seed=8, spare=4)
+    c.table = np.arange(4, dtype=np.int32)[None, :]
+    x = to_bf16(c.rng.normal(size=(100, 6 * 128)) * 2.0 ** c.rng.integers(-3, 4, (100, 1)))
+    starts, length = i32([0, 1]), i32([0])
+    batch = tp.PagedBatch(starts, length, i32(c.table.tolist()), 1)
+    for t in range(100):
+        length.fill_(t + 1)
+        tp.tp_kv_append_fp8([x[t:t + 1]], 2, c.cache, batch)
+        _, k, v = np.split(f64(x[t:t + 1]).reshape(1, 6, 128), [2, 4], axis=1)
+        P.append(c.codes[0][0], c.scales[0][0], k, [(0, 1, t + 1)], c.table)
+        P.append(c.codes[0][1], c.scales[0][1], v, [(0, 1, t + 1)], c.table)
+    codes, scales = c.got()
+    np.testing.assert_array_equal(scales[0], c.scales[0])
+    np.testing.assert_array_equal(codes[0], c.codes[0])
+
+
+def test_bad_places_are_left_out_and_reported():
+    """A page outside the cache, a length beyond the table, rows beyond max_new and T, more rows than tokens."""
+    c = Case([(10, 3), (10, 3), (10, 3), (0, 4)], p=1, n_kv=1, group=2, D=64, page=16, seed=9, spare=1)
+    qkv = qkv_of(c)
+    c.queries()
+    table = c.table.copy()
+    table[1, 0] = c.n_pages
+    table[2, 0] = -1
+    for lens, starts, max_new in (([13, 13, 13, 2], [0, 3, 6, 9, 13], 4), ([13, 13, 13, 40], [0, 3, 6, 9, 13], 4),
+                                  ([13, 13, 13, 4], [0, 3, 6, 9, 14], 5), ([13, 13, 13, 4], [0, 3, 6, 9, 13], 3),
+                                  ([13, 13, 13, -5], [0, 3, 6, 9, 13], 4), ([13, 13, 13, 4], [0, 3, 2, 9, 13], 4),
+                                  ([13, 13, 13, 2 ** 31 - 1], [0, 3, 6, 9, 13], 4)):
+        c.upload()
+        before = c.got()
+        batch = tp.PagedBatch(i32(starts), i32(lens), i32(table.tolist()), max_new)
+        tp.tp_kv_append_fp8(qkv, 2, c.cache, batch, rope="half", cos_sin=torch.ones((100, 64), device=DEV))
+        with pytest.raises(tp.TPError, match="TP_ERR_INVALID_ARG"):
+            tp.tp_device_status()
+        outs = fresh(c.q)
+        tp.tp_attention_paged_fp8(c.q, c.cache, batch, outs=outs)
+        with pytest.raises(tp.TPError, match="TP_ERR_INVALID_ARG"):
+            tp.tp_device_status()
+        tp.tp_device_status()                                                # the record is cleared
+        got = c.got()
+        for page in range(c.n_pages):
+            if page not in table[[0, 3], 0]:
+                np.testing.assert_array_equal(got[0][0][:, page], before[0][0][:, page])
+        if starts[1:3] == [3, 6]:
+            assert np.all(f64(outs[0])[3:9] == 0)                            # no key of these can be read
+
+
+def test_rotation_outside_its_table_is_nan_and_reported():
+    c = Case([(10, 3)], p=1, n_kv=1, group=1, D=64, page=16, seed=10)
+    qkv = qkv_of(c)
+    q, = tp.tp_kv_append_fp8(qkv, 1, c.cache, c.batch, rope="pairs", cos_sin=torch.ones((12, 32), device=DEV))
+    with pytest.raises(tp.TPError, match="TP_ERR_INVALID_ARG"):
+        tp.tp_device_status()
+    got = f64(q)
+    assert np.all(np.isfinite(got[:2])) and np.all(np.isnan(got[2, :32])) and np.all(np.isfinite(got[2, 32:]))
+    assert c.got()[1][0][0, c.table[0, 0], 0] == 255
+
+
+# ----------------------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("D, group", [(128, 1), (128, 6), (64, 1), (64, 8), (128, 16), (64, 12)])
+@pytest.mark.parametrize("seqs", [
+    [(0, 1)], [(31, 1)], [(32, 1), (0, 1), (15, 1), (16, 1), (127, 1), (128, 1), (500, 1)], [(1000, 1), (0, 0), (7, 1)],
+], ids=str)
+def test_one_token(seqs, D, group, page):
+    c = Case(seqs, p=2, n_kv=2, group=group, D=D, page=page, seed=group + page, front=1, behind=2, split=page == 64, fill=0x7F)
+    q = c.queries()
+    outs = fresh(q)
+    tp.tp_attention_paged_fp8(q, c.cache, c.batch, outs=outs)
+    c.check(outs, before=fresh(q))
+
+
+@pytest.mark.parametrize("causal, window", [(True, 0), (False, 0), (True, 1), (True, 37), (True, 300)])
+@pytest.mark.parametrize("D, group, page", [(128, 1, 16), (128, 3, 32), (64, 5, 64), (64, 2, 128), (128, 8, 128)])
+@pytest.mark.parametrize("seqs", [
+    [(0, 5)], [(100, 2), (3, 5), (0, 1), (40, 4)], [(0, 131)], [(77, 40), (0, 300), (5, 1), (513, 9)], [(200, 70)],
+], ids=str)
+def test_several_tokens(seqs, D, group, page, causal, window):
+    c = Case(seqs, p=2, n_kv=2, group=group, D=D, page=page, seed=group + page, front=3, behind=1, fill=0xFF)
+    q = c.queries()
+    outs = fresh(q)
+    tp.tp_attention_paged_fp8(q, c.cache, c.batch, causal=causal, window=window, outs=outs)
+    c.check(outs, causal=causal, window=window, before=fresh(q))
+
+
+@pytest.mark.parametrize("D, group, n_kv", [(128, 1, 3), (128, 4, 1), (64, 16, 2), (128, 12, 1)])
+@pytest.mark.parametrize("seqs", [[(9000, 1)], [(4000, 1), (2, 1), (6000, 1), (70, 1)], [(5000, 1)] + [(33, 1)] * 40,
+                                  [(11, 1)] * 300, [(0, 0)] * 5 + [(3000, 1)] + [(0, 0)] * 300 + [(2, 1)]], ids=len)
+def test_long_axes_and_many_sequences(seqs, D, group, n_kv):
+    """Items over several warps and CTAs, several items in one, sequences without rows between them."""
+    c = Case(seqs, p=2, n_kv=n_kv, group=group, D=D, page=32, seed=len(seqs))
+    q = c.queries()
+    outs = tp.tp_attention_paged_fp8(q, c.cache, c.batch)
+    c.check(outs)
+
+
+@pytest.mark.parametrize("new", [1, 3, 60, 200])
+def test_rows_that_see_nothing(new):
+    """More rows than tokens: the first rows come before the first key; a sequence of no tokens at all."""
+    c = Case([(0, new), (20, new)], p=1, n_kv=2, group=2, D=128, page=16, seed=new)
+    c.seqs = [(0, new, 0), (new, new, new // 2 + 1)]
+    c.batch = c.make_batch()
+    q = c.queries()
+    outs = fresh(q)
+    tp.tp_attention_paged_fp8(q, c.cache, c.batch, outs=outs)
+    got = f64(outs[0])
+    assert np.all(got[:new] == 0)
+    c.check(outs)
+
+
+@pytest.mark.parametrize("new", [1, 4, 100])
+@pytest.mark.parametrize("page", [16, 64])
+def test_a_nan_page_stays_with_the_rows_that_see_it(new, page):
+    seqs = [(3 * page, new), (2 * page, new)]
+    c = Case(seqs, p=1, n_kv=2, group=2, D=128, page=page, seed=page + new)
+    for which, head, at in ((0, 0, c.table[0, 1]), (1, 1, c.table[1, 0])):
+        c.scales[0][which, at, head] = 255
+        c.codes[0][which, at, head] = 0x7F
+    # the last page of sequence 0: only its rows from there on see it (causal)
+    last = (3 * page + new - 1) // page
+    c.scales[0][1, c.table[0, last], 1] = 255
+    c.codes[0][1, c.table[0, last], 1] = 0xFF
+    c.upload()
+    q = c.queries()
+    out = f64(tp.tp_attention_paged_fp8(q, c.cache, c.batch)[0]).reshape(c.T, 4, 128)
+    for s, (a, n, length) in enumerate(c.seqs):
+        K, V = (P.values(c.codes[0][i], c.scales[0][i], c.table[s], length) for i in (0, 1))
+        want, _ = P.attention(f64(q[0]).reshape(c.T, 4, 128)[a:a + n], K, V, 128 ** -0.5, P.seen(n, length))
+        np.testing.assert_array_equal(np.isnan(out[a:a + n]), np.isnan(want))
+        fine = np.isfinite(want)
+        assert np.all(np.abs(out[a:a + n][fine] - want[fine]) <= 2.0 ** -6 * (np.abs(want[fine]) + 1))
+    assert np.isfinite(out).any()
+
+
+@pytest.mark.parametrize("new", [1, 2, 70])
+def test_special_queries(new):
+    """Zero, tiny and huge queries; a NaN or an infinity makes its row NaN and no other."""
+    c = Case([(100, new), (40, new)], p=1, n_kv=2, group=6, D=128, page=32, seed=11)
+    q = f64(c.queries()[0]).reshape(c.T, 12, 128)
+    q[0, 0] = 0
+    q[0, 1] *= 2.0 ** -100
+    q[0, 2] *= 2.0 ** -130
+    q[0, 3] *= 2.0 ** 3
+    q[0, 4, 7], q[0, 5, 100], q[new, 6, 0] = np.nan, np.inf, -np.inf
+    q[new, 7] = 0
+    q[new, 7, 3] = 1.0
+    q[new, 7, 4] = 2.0 ** -30
+    c.q = [to_bf16(q.reshape(c.T, -1))]
+    out = f64(tp.tp_attention_paged_fp8(c.q, c.cache, c.batch)[0]).reshape(c.T, 12, 128)
+    bad = [(0, 4), (0, 5), (new, 6)]
+    for t, h in bad:
+        assert np.all(np.isnan(out[t, h]))
+        out[t, h] = 0
+    clean = f64(c.q[0]).reshape(c.T, 12, 128)
+    for t, h in bad:
+        clean[t, h] = 0
+    c.q = [to_bf16(clean.reshape(c.T, -1))]
+    again = f64(tp.tp_attention_paged_fp8(c.q, c.cache, c.batch)[0]).reshape(c.T, 12, 128)
+    for t, h in bad:
+        again[t, h] = 0
+    np.testing.assert_array_equal(out, again)
+    c.check(tp.tp_attention_paged_fp8(c.q, c.cache, c.batch))
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_page_scales_far_apart(new):
+    """V pages between 2^-20 and 2^20, K pages between 2^-8 and 2^2, some all zero with the least scale."""
+    c = Case([(300, new), (90, new)], p=1, n_kv=2, group=4, D=128, page=16, seed=12)
+    for which, lo, hi in ((0, -8, 3), (1, -20, 21)):
+        c.scales[0][which] = 121 + c.rng.integers(lo, hi, c.scales[0][which].shape)
+    zero = c.rng.random(c.scales[0].shape) < 0.2
+    c.codes[0][zero] = 0
+    c.scales[0][zero] = 0
+    c.upload()
+    q = c.queries()
+    c.check(tp.tp_attention_paged_fp8(q, c.cache, c.batch))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_scales_of_the_scores(scale):
+    c = Case([(200, 1), (40, 1)], p=1, n_kv=2, group=3, D=64, page=32, seed=13)
+    q = c.queries()
+    c.check(tp.tp_attention_paged_fp8(q, c.cache, c.batch, scale=scale), scale=scale)
+
+
+def test_shared_pages_of_a_prefix():
+    c = Case([(64, 3), (64, 3), (64, 3)], p=1, n_kv=2, group=2, D=128, page=16, seed=14)
+    c.table[1, :4] = c.table[2, :4] = c.table[0, :4]
+    c.batch = c.make_batch()
+    qkv = qkv_of(c)
+    c.q = tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch)
+    c.codes, c.scales = c.got()
+    c.check(tp.tp_attention_paged_fp8(c.q, c.cache, c.batch))
+
+
+# ----------------------------------------------------------------------------- as they are used
+
+def heads_of(w, heads, n_kv, D):
+    return [heads * D, n_kv * D, n_kv * D]
+
+
+@pytest.mark.parametrize("D, page, group", [(128, 16, 2), (64, 64, 4)])
+def test_a_sharded_layer_serving_several_sequences(D, page, group):
+    """Prompts, then tokens one by one: projection, append, attention and out-projection against the oracle, on the
+    stored output of each step before; and the cached path's last token against the whole sequence's attention."""
+    p, hidden, n_kv = 2, 256, 2
+    heads = n_kv * group
+    rng = np.random.default_rng(15)
+    width = p * (heads + 2 * n_kv) * D
+    w_qkv = to_bf16(rng.normal(0, 0.06, (width, hidden)))
+    w_out = to_bf16(rng.normal(0, 0.05, (hidden, p * heads * D)))
+    splits = [p * heads * D, p * n_kv * D, p * n_kv * D]
+    shards = tp.tp_plan_shard_ranks(w_qkv, "colwise", p, fused_splits=splits, num_heads=p * n_kv, head_dim=D)
+    outs = tp.tp_plan_shard_ranks(w_out, "rowwise", p)
+    cache = tp.PagedCache.empty(p, 24, n_kv, page, D)
+    table = rng.permutation(24).reshape(3, 8).astype(np.int32)
+    angle = np.outer(np.arange(512), 10000.0 ** (-np.arange(D // 2) * 2 / D))
+    cs = torch.from_numpy(np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32)).to(DEV)
+    lengths = [0, 0, 0]
+    for step, new in enumerate([(37, 5, 90), (1, 1, 1), (1, 1, 1), (6, 0, 3)]):
+        starts = np.concatenate([[0], np.cumsum(new)])
+        T = int(starts[-1])
+        lengths = [n + m for n, m in zip(lengths, new)]
+        batch = tp.PagedBatch(i32(starts.tolist()), i32(lengths), i32(table.tolist()), max(new))
+        x = to_bf16(rng.normal(size=(T, hidden)))
+        qkv = tp.tp_linear_colwise(x, shards)
+        q = tp.tp_kv_append_fp8(qkv, heads, cache, batch, rope="half", cos_sin=cs)
+        att = tp.tp_attention_paged_fp8(q, cache, batch)
+        y = tp.tp_linear_rowwise(att, outs)
+        assert torch.isfinite(y).all()
+        total = sum(f64(a) @ f64(w).T for a, w in zip(att, outs))
+        assert np.all(np.abs(f64(y) - total) <= 2.0 ** -8 * np.abs(total) + 1e-4 * np.abs(total).max())
+        for r in range(p):
+            codes = [raw(cache.k[r]), raw(cache.v[r])]
+            scales = [raw(cache.k_scales[r]), raw(cache.v_scales[r])]
+            qf = f64(q[r]).reshape(T, heads, D)
+            for s, (a, n) in enumerate(zip(starts, new)):
+                if n == 0:
+                    continue
+                K, V = (P.values(codes[i], scales[i], table[s], lengths[s]) for i in (0, 1))
+                see = P.seen(n, lengths[s])
+                want, w = P.attention(qf[a:a + n], K, V, D ** -0.5, see)
+                bound = attention_bound(qf[a:a + n], K, V, D ** -0.5, want, w, see)
+                got = f64(att[r]).reshape(T, heads, D)[a:a + n]
+                assert np.all(np.abs(got - want) <= bound), (step, r, s)
+                # what was appended: this step's K, rotated, to within a code's rounding
+                kx = f64(qkv[r]).reshape(T, heads + 2 * n_kv, D)[a:a + n, heads:heads + n_kv]
+                want_k = P.rotate(kx, f64(cs)[lengths[s] - n:lengths[s]], "half").transpose(1, 0, 2)
+                pages = table[s][np.arange(lengths[s] - n, lengths[s]) // page]
+                size = F.scale_value(scales[0][pages]).T[:, :, None]
+                assert np.all(np.abs(K[:, lengths[s] - n:] - want_k) <= np.maximum(2.0 ** -4 * np.abs(want_k), 2.0 ** -10 * size) * 1.001)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_same_bits_every_time_and_on_another_stream(new):
+    c = Case([(700, new), (3000, new), (5, new)], p=2, n_kv=2, group=4, D=128, page=16, seed=16)
+    qkv = qkv_of(c)
+    first = tp.tp_attention_paged_fp8(tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch), c.cache, c.batch)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    need = tp.tp_attention_paged_workspace_bytes(c.cache, c.batch, c.T, c.heads)
+    for i in range(4):
+        ws = torch.randint(0, 256, (max(need, 16),), dtype=torch.uint8, device=DEV)      # any content
+        torch.cuda.synchronize()
+        q = tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch, stream=stream)
+        outs = tp.tp_attention_paged_fp8(q, c.cache, c.batch, workspace=ws, stream=stream)
+        stream.synchronize()
+        for a, b in zip(first, outs):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("long", [False, True])
+def test_captured_decode_follows_the_lengths(long):
+    """One captured step, replayed while lengths, pages and tokens change on the device."""
+    top = 4000 if long else 200
+    c = Case([(top, 1)] * 3, p=2, n_kv=2, group=3, D=128, page=16, seed=17)
+    lengths, table = i32([1, 1, 1]), i32(c.table.tolist())
+    batch = tp.PagedBatch(i32([0, 1, 2, 3]), lengths, table, 1)
+    x = [torch.zeros((3, (c.heads + 4) * 128), dtype=BF16, device=DEV) for _ in range(2)]
+    need = tp.tp_attention_paged_workspace_bytes(c.cache, batch, 3, c.heads)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+    tp.tp_attention_paged_fp8(tp.tp_kv_append_fp8(x, c.heads, c.cache, batch), c.cache, batch, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q = tp.tp_kv_append_fp8(x, c.heads, c.cache, batch)
+        outs = tp.tp_attention_paged_fp8(q, c.cache, batch, workspace=ws)
+    for lens in ([1, 2, 3], [16, 17, 33], [top, 5, top // 2], [100, 199, 1], [2, 0, 1]):
+        lengths.copy_(i32(lens))
+        for t in x:
+            t.copy_(to_bf16(c.rng.normal(size=t.shape)))
+        graph.replay()
+        torch.cuda.synchronize()
+        c.q, (c.codes, c.scales) = q, c.got()
+        c.seqs = [(s, 1, n) for s, n in enumerate(lens)]
+        if 0 in lens:      # a row without a token: reported, its output 0
+            assert np.all(f64(outs[0])[lens.index(0)] == 0)
+            with pytest.raises(tp.TPError):
+                tp.tp_device_status()
+        else:
+            c.check(outs, what=lens)
+
+
+def test_calls_on_several_streams_and_from_several_threads():
+    cases = [Case([(400 * i + 50, 1), (3000, 1 + 30 * (i % 2))], p=2, n_kv=2, group=2, D=128, page=32, seed=20 + i) for i in range(4)]
+    results, errors = [None] * 4, []
+    for c in cases:
+        c.queries()
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(10):
+                results[i] = tp.tp_attention_paged_fp8(cases[i].q, cases[i].cache, cases[i].batch, stream=stream)
+            stream.synchronize()
+        except Exception as e:   # pragma: no cover
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for c, outs in zip(cases, results):
+        c.check(outs)
+
+
+def test_one_cache_for_several_ranks():
+    """The same tensors as several ranks' caches (read only): every rank has rank 0's answer."""
+    c = Case([(1500, 1), (33, 1)], p=1, n_kv=2, group=2, D=128, page=16, seed=30)
+    q = c.queries()
+    k = c.cache
+    many = tp.PagedCache(k.k * 3, k.v * 3, k.k_scales * 3, k.v_scales * 3)
+    outs = tp.tp_attention_paged_fp8(q * 3, many, c.batch)
+    c.check(outs[:1])
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_offsets_past_four_gib(new):
+    """Pages whose codes lie beyond 4 GiB, from a stride of 64 KiB a page."""
+    n_pages, n_kv, page, D = 70000, 1, 16, 128
+    free, _ = torch.cuda.mem_get_info()
+    if free < 12 << 30:
+        pytest.skip("needs 12 GB of free device memory")
+    store = torch.zeros((n_pages, 65536), dtype=torch.uint8, device=DEV)
+    size = n_kv * page * D
+    k = store[:, :size].view(E4M3).view(n_pages, n_kv, page, D)
+    v = store[:, size:2 * size].view(E4M3).view(n_pages, n_kv, page, D)
+    scales = torch.zeros((2, n_pages, n_kv), dtype=torch.uint8, device=DEV)
+    cache = tp.PagedCache([k], [v], [scales[0]], [scales[1]])
+    rng = np.random.default_rng(31)
+    length = 100 + new
+    table = (n_pages - 1 - rng.permutation(200)[:-(-length // page)])[None, :].astype(np.int32)
+    qkv = to_bf16(rng.normal(size=(length, 4 * D)))
+    tp.tp_kv_append_fp8([qkv], 2, cache, tp.PagedBatch(i32([0, length]), i32([length]), i32(table.tolist()), length))
+    q = [qkv[length - new:, :2 * D].contiguous()]
+    out, = tp.tp_attention_paged_fp8(q, cache, tp.PagedBatch(i32([0, new]), i32([length]), i32(table.tolist()), new))
+    x = f64(qkv).reshape(length, 4, D)
+    pages = -(-length // page)
+    codes, sc = np.zeros((2, pages, 1, page, D), np.uint8), np.zeros((2, pages, 1), np.uint8)
+    at = np.arange(pages)[None, :]
+    for i in (0, 1):
+        P.append(codes[i], sc[i], x[:, 2 + i:3 + i], [(0, length, length)], at)
+        got = raw((k, v)[i][torch.from_numpy(table[0].astype(np.int64)).to(DEV)].contiguous())
+        lengths = min(page, length)
+        np.testing.assert_array_equal(got.reshape(-1, D)[:length], codes[i].reshape(-1, D)[:length])
+    K, V = (P.values(codes[i], sc[i], at[0], length) for i in (0, 1))
+    see = P.seen(new, length)
+    want, w = P.attention(f64(q[0]).reshape(new, 2, D), K, V, D ** -0.5, see)
+    assert np.all(np.abs(f64(out).reshape(want.shape) - want) <= attention_bound(f64(q[0]).reshape(new, 2, D), K, V, D ** -0.5, want, w, see))
+
+
+def test_empty_calls_write_nothing():
+    c = Case([(5, 2)], p=1, n_kv=1, group=1, D=64, page=16, seed=32)
+    before = c.got()
+    none = tp.PagedBatch(i32([0, 0]), i32([0]), i32([[0]]), 0)
+    q, = tp.tp_kv_append_fp8([torch.zeros((0, 3 * 64), dtype=BF16, device=DEV)], 1, c.cache, c.batch)
+    assert q.shape == (0, 64)
+    tp.tp_kv_append_fp8([torch.zeros((2, 3 * 64), dtype=BF16, device=DEV)], 1, c.cache, none)
+    out = torch.full((2, 64), 7.0, dtype=BF16, device=DEV)
+    tp.tp_attention_paged_fp8([torch.zeros_like(out)], c.cache, none, outs=[out])
+    assert torch.all(out == 7)
+    after = c.got()
+    np.testing.assert_array_equal(before[0][0], after[0][0])
+    np.testing.assert_array_equal(before[1][0], after[1][0])
+
+
+def test_binding_refusals():
+    c = Case([(5, 2)], p=2, n_kv=2, group=1, D=64, page=16, seed=33)
+    q = c.queries()
+    k = c.cache
+    with pytest.raises(TypeError):
+        tp.PagedCache([t.view(torch.uint8) for t in k.k], k.v, k.k_scales, k.v_scales)
+    with pytest.raises(ValueError):
+        tp.PagedCache(k.k, k.v[:1], k.k_scales, k.v_scales)
+    with pytest.raises(ValueError):
+        tp.PagedCache(k.k, [t[:-1] for t in k.v], k.k_scales, k.v_scales)
+    with pytest.raises(ValueError):
+        tp.PagedCache([t.transpose(1, 2).contiguous().transpose(1, 2) for t in k.k], k.v, k.k_scales, k.v_scales)
+    with pytest.raises(TypeError):
+        tp.PagedBatch(c.batch.seq_start.long(), c.batch.kv_len, c.batch.page_table, 2)
+    with pytest.raises(ValueError):
+        tp.PagedBatch(c.batch.kv_len, c.batch.kv_len, c.batch.page_table, 2)
+    with pytest.raises(ValueError):
+        tp.tp_attention_paged_fp8(q[:1], k, c.batch)
+    with pytest.raises(ValueError):
+        tp.tp_attention_paged_fp8([t[:, :100] for t in q], k, c.batch)
+    with pytest.raises(TypeError):
+        tp.tp_attention_paged_fp8([t.float() for t in q], k, c.batch)
+    with pytest.raises(ValueError):
+        tp.tp_attention_paged_fp8([t.cpu() for t in q], k, c.batch)
+    long = Case([(5000, 2)], p=1, n_kv=2, group=1, D=64, page=16, seed=34)
+    with pytest.raises(tp.TPError, match="TP_ERR_WORKSPACE"):
+        tp.tp_attention_paged_fp8(long.queries(), long.cache, long.batch, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    qkv = qkv_of(c)
+    with pytest.raises(ValueError):
+        tp.tp_kv_append_fp8(qkv, c.heads, k, c.batch, rope="half")
+    with pytest.raises(ValueError):
+        tp.tp_kv_append_fp8(qkv, c.heads, k, c.batch, cos_sin=torch.ones((9, 64), device=DEV))
+    with pytest.raises(ValueError):
+        tp.tp_kv_append_fp8(qkv, c.heads + 1, k, c.batch)
+    with pytest.raises(tp.TPError, match="TP_ERR_INVALID_ARG"):
+        tp.tp_kv_append_fp8(qkv, c.heads, k, c.batch, rope="half", cos_sin=torch.ones((9, 20), device=DEV))
