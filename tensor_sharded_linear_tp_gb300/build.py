@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libtp.so")
 SOURCES = ["tp_host.cu", "tp_copy.cu", "tp_gemm.cu", "tp_attention.cu", "tp_flash.cu", "tp_quant.cu", "tp_fp8.cu",
-           "tp_kv_append.cu", "tp_paged_attention.cu", "tp_safetensors.cu"]
+           "tp_kv_append.cu", "tp_paged_attention.cu", "tp_paged_tiles.cu", "tp_safetensors.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

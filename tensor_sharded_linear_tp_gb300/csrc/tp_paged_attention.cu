@@ -34,7 +34,7 @@
 
 #include "tp_e4m3.cuh"
 #include "tp_internal.h"
-#include "tp_paged.h"
+#include "tp_paged_attention.cuh"
 #include "tp_ptx.cuh"
 
 namespace tp {
@@ -44,22 +44,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                         // keys of a step
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-
-struct AttendParams {
-  CUtensorMap map_k[TP_MAX_DEGREE], map_v[TP_MAX_DEGREE];  // [pages][heads][tokens][D] codes, box of one page's tokens (at most 32)
-  BatchView b;
-  const __nv_bfloat16* q[TP_MAX_DEGREE];
-  __nv_bfloat16* out[TP_MAX_DEGREE];
-  const uint8_t *ks[TP_MAX_DEGREE], *vs[TP_MAX_DEGREE];
-  int64_t ld_q, ldo, ld_scales;
-  int n_kv, group;             // KV heads of a rank, query heads of a KV head
-  int heads;                   // n_ranks * n_kv
-  int causal, window;
-  float scale_log2e;
-  int per_item;                // 1: a CTA takes one item whole; 0: equal parts of all steps
-  float* parts;                // workspace: two partial items a CTA (part_floats each)
-  int4* joins;                 // workspace: a CTA's item to be joined {parts, first row, rows, rank and head}
-};
 
 // A piece of an item in shared memory.
 struct Piece {
@@ -94,42 +78,6 @@ struct Cfg {
   static constexpr size_t SMEM = 1024 + OFF_CTRL + sizeof(Ctrl<STAGES>);
   static_assert(PIECE <= RING && SMEM <= 232448, "shared memory");
 };
-
-// One item: rows [row0, row0 + rows) of a sequence's n * group rows (token by token), and its steps.
-struct Item {
-  SeqView v;
-  int row0, rows;
-  int tile0, tiles;     // steps tile0 .. tile0 + tiles of the sequence's keys
-  int key_end;          // keys from here on are not seen by any row
-};
-
-template <int ROWS>
-__device__ __forceinline__ Item item_of(const AttendParams& p, const SeqView& v, int block) {
-  Item it;
-  it.v = v;
-  it.row0 = block * ROWS;
-  it.rows = static_cast<int>(min(static_cast<int64_t>(ROWS), static_cast<int64_t>(v.n) * p.group - it.row0));
-  const int first = it.row0 / p.group, last = (it.row0 + max(it.rows, 1) - 1) / p.group;
-  it.key_end = p.causal ? max(min(static_cast<int64_t>(v.len), static_cast<int64_t>(v.pos0) + last + 1), int64_t(0)) : v.len;
-  const int64_t lo = p.window > 0 ? max(static_cast<int64_t>(v.pos0) + first - p.window + 1, int64_t(0)) : 0;
-  it.tile0 = static_cast<int>(min(lo, static_cast<int64_t>(it.key_end))) / kStep;
-  it.tiles = it.rows > 0 ? max(1, (it.key_end + kStep - 1) / kStep - it.tile0) : 0;   // (a row without keys is an item too)
-  return it;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 2^e, 0 below fp32's normal range.
-__device__ __forceinline__ float pow2(int e) {
-  return e < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(min(e, 127) + 127) << 23);
-}
-// A scale byte's value (NaN for 255).
-__device__ __forceinline__ float e8m0_value(uint32_t byte) {
-  return byte == 255u ? __uint_as_float(0x7FFFFFFFu) : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
-}
 
 // Two codes (the low or high half of a word) as fp16.
 __device__ __forceinline__ uint32_t f16_lo(uint32_t w) {
@@ -222,11 +170,11 @@ __device__ __forceinline__ void issue_step(const AttendParams& p, Loader& ld, in
       ld.h = 0;
       do {
         v = seq_view(p.b, ++ld.s);
-        it = item_of<C::ROWS>(p, v, 0);
+        it = item_of<C::ROWS, kStep>(p, v, 0);
       } while (it.tiles == 0 && ld.s + 1 < p.b.n_seqs);
     } else {
       v = seq_view(p.b, ld.s);
-      it = item_of<C::ROWS>(p, v, 0);
+      it = item_of<C::ROWS, kStep>(p, v, 0);
     }
     ld.tile = it.tile0;
     ld.tile_end = it.tile0 + it.tiles;
@@ -493,11 +441,6 @@ __device__ __forceinline__ void step(State<D, NT>& st, uint32_t data, uint32_t i
   }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // Ends an item's piece: O / l to the output where the piece is the whole item, else to `piece`
 // (shared memory) with the rows' m and l.
 template <int D, int NT>
@@ -543,35 +486,6 @@ __device__ __forceinline__ void end_piece(const AttendParams& p, const Item& it,
     }
 }
 
-// Joins up to `n` pieces of a row: weights l 2^(m - max m); 0 where no piece has seen a key.
-template <typename ML, typename O4>
-__device__ __forceinline__ float4 join_row(int n, ML&& ml, O4&& o4) {
-  float top = -INFINITY;
-  for (int i = 0; i < n; ++i) top = fmaxf(top, ml(i).x);
-  if (top == -INFINITY) top = 0.0f;
-  float sum = 0.0f;
-  float4 acc = make_float4(0, 0, 0, 0);
-  for (int i = 0; i < n; ++i) {
-    const float2 v = ml(i);
-    const float w = v.y * ex2(v.x - top);
-    const float4 o = o4(i);
-    sum += w;
-    acc.x += w * o.x, acc.y += w * o.y, acc.z += w * o.z, acc.w += w * o.w;
-  }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-}
-
-__device__ __forceinline__ void store_row4(const AttendParams& p, int a, int h, int row, int col, int D, const float4& v) {
-  const int rank = h / p.n_kv, head = h - rank * p.n_kv;
-  const int token = row / p.group, hq = row - token * p.group;
-  __nv_bfloat16* dst = p.out[rank] + static_cast<int64_t>(a + token) * p.ldo + (static_cast<int64_t>(head) * p.group + hq) * D + col;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-}
-
-// Where the steps of all items are cut: CTA c of n has the steps from total * c / n on.
-__device__ __forceinline__ int64_t cut(int64_t total, int64_t c, int64_t n) { return total * c / n; }
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_constant__ AttendParams p) {
   using C = Cfg<D, NT>;
@@ -594,16 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   // This CTA's steps [u0, u1) of `total`, and the item and step at which this warp's part begins.
   int64_t u0 = 0, u1 = 0, total = 0, n_cta = 1;
   Start my{0, 0, 0, 0};
-  int count = 0, block = 0;
+  int count = 0;
   if (p.per_item) {
-    const int64_t slot = blockIdx.x;
+    my.s = blockIdx.x;
     my.h = blockIdx.y;
-    my.s = find_sequence(p.b, slot, C::ROWS, p.group, 1, lane);
-    if (my.s < 0) return;
-    const SeqView v = seq_view(p.b, my.s);
-    block = static_cast<int>(slot - (static_cast<int64_t>(v.a) * p.group / C::ROWS + my.s));
-    if (static_cast<int64_t>(block) * C::ROWS >= static_cast<int64_t>(v.n) * p.group) return;
-    const Item it = item_of<C::ROWS>(p, v, block);
+    const Item it = item_of<C::ROWS, kStep>(p, seq_view(p.b, my.s), 0);
     u1 = total = it.tiles;
     my.at = u1 * warp / kWarps;
     my.tile = static_cast<int>(my.at) + it.tile0;
@@ -613,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     const int run = (p.b.n_seqs + kThreads - 1) / kThreads;
     const int s0 = min(static_cast<int>(threadIdx.x) * run, p.b.n_seqs), s1 = min(s0 + run, p.b.n_seqs);
     int64_t mine = 0;
-    for (int s = s0; s < s1; ++s) mine += item_of<C::ROWS>(p, seq_view(p.b, s), 0).tiles;
+    for (int s = s0; s < s1; ++s) mine += item_of<C::ROWS, kStep>(p, seq_view(p.b, s), 0).tiles;
     mine *= p.heads;
     int64_t upto = mine;
 #pragma unroll
@@ -635,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     }
     int64_t before = upto - mine;
     for (int s = s0; s < s1 && before < u1; ++s) {
-      const Item it = item_of<C::ROWS>(p, seq_view(p.b, s), 0);
+      const Item it = item_of<C::ROWS, kStep>(p, seq_view(p.b, s), 0);
       const int64_t after = before + static_cast<int64_t>(it.tiles) * p.heads;
       if (after > u0) {
         for (int w = 0; w < kWarps; ++w) {
@@ -656,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   if (count > 0) {
     // The loader and the worker walk the same steps, the loader STAGES ahead.
     SeqView v = seq_view(p.b, my.s);
-    Item it = item_of<C::ROWS>(p, v, block);
+    Item it = item_of<C::ROWS, kStep>(p, v, 0);
     Loader ld{my.s, my.h, my.tile, it.tile0 + it.tiles, -64, 0, 0, v.len};
     int issued = 0;
     for (; issued < C::STAGES && issued < count; ++issued) issue_step<D, NT>(p, ld, issued, ring, ctl, warp, lane);
@@ -693,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
           h = 0;
           do {
             v = seq_view(p.b, ++s);
-            it = item_of<C::ROWS>(p, v, 0);
+            it = item_of<C::ROWS, kStep>(p, v, 0);
           } while (it.tiles == 0 && s + 1 < p.b.n_seqs);
         }
         tile = it.tile0;
@@ -704,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   __syncthreads();
 
   // Pieces of one item lie in consecutive warps, in key order.
-  int4 join = make_int4(0, 0, 0, 0);
+  Join join{};
   for (int i = 0; i < 2 * kWarps;) {
     const Piece& lead = ctl->piece[i >> 1][i & 1];
     if (!lead.valid) {
@@ -751,31 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       // CTA c holds step u where c is the largest with cut(c) <= u.
       const int64_t u = lead.item_end - 1;
       const int64_t c_last = ((u + 1) * n_cta + total - 1) / total - 1;
-      join = make_int4(static_cast<int>(c_last - blockIdx.x) + 1, v.a, rows, lead.h);
+      join = Join{static_cast<int>(c_last - blockIdx.x) + 1, v.a, lead.row0, rows, lead.h, {}};
     }
   }
   if (!p.per_item && threadIdx.x == 0) p.joins[blockIdx.x] = join;
-}
-
-// Joins the items that lie in several CTAs: block c the one that begins in CTA c and goes beyond it
-// (its piece in that CTA's second part, the others in the first parts of those behind).
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ AttendParams p) {
-  using C = Cfg<D, NT>;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int4 join = p.joins[blockIdx.x];
-  const int n = join.x;
-  if (n == 0) return;
-  const float* own = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * (C::PIECE / 4);
-  auto part = [&](int i) { return i == 0 ? own : own + (2 * i - 1) * static_cast<int64_t>(C::PIECE / 4); };
-  for (int at = threadIdx.x * 4; at < join.z * D; at += kThreads * 4) {
-    const int row = at / D, col = at - row * D;
-    const float4 o = join_row(
-        n, [&](int i) { return *reinterpret_cast<const float2*>(part(i) + C::ROWS * D + 2 * row); },
-        [&](int i) { return *reinterpret_cast<const float4*>(part(i) + at); });
-    store_row4(p, join.y, join.w, row, col, D, o);
-  }
 }
 
 // The tensor map of a rank's codes: [n_pages][n_kv][page_size][D] bytes, a box of the tokens of one
@@ -811,28 +699,29 @@ tp_status current_device(int* dev) {
   return TP_OK;
 }
 
+// Which kernel takes a call, and how.
 struct Plan {
+  bool tiles;            // more than 16 rows a sequence and KV head: paged_tiles_kernel
   bool one_row_tile;     // 8 rows an item, else 16
-  bool per_item;
-  int64_t slots;         // per_item: blocks of rows
-  int ctas;              // else
+  bool per_item;         // a CTA an item, no second launch; else equal parts of all steps
+  int ctas;              // of those parts
   size_t ws_bytes;
 };
 
-Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int64_t T, int group, int sms) {
+Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int group, int sms) {
   Plan pl{};
   const int64_t rows = static_cast<int64_t>(b.max_new) * group;
+  pl.tiles = rows > 16;
   pl.one_row_tile = rows <= 8;
-  const int R = pl.one_row_tile ? 8 : 16;
-  pl.slots = T * group / R + b.n_seqs;
   const int64_t items = static_cast<int64_t>(b.n_seqs) * c.n_ranks * c.n_kv_heads;
   const int64_t keys = b.max_pages * c.page_size;
   // Few short items: each by one CTA, no second launch.  Otherwise equal parts.
-  pl.per_item = rows > 16 || (items <= sms && keys <= 1024);
+  pl.per_item = !pl.tiles && items <= sms && keys <= 1024;
   pl.ctas = sms;
   if (!pl.per_item) {
-    const size_t piece = static_cast<size_t>(R) * (c.head_dim + 2) * 4;
-    pl.ws_bytes = static_cast<size_t>(pl.ctas) * (2 * piece + sizeof(int4));
+    const size_t part = pl.tiles ? paged_tiles_part_floats(c.head_dim) * 4
+                                 : static_cast<size_t>(pl.one_row_tile ? 8 : 16) * (c.head_dim + 2) * 4;
+    pl.ws_bytes = static_cast<size_t>(pl.ctas) * (2 * part + sizeof(Join));
   }
   return pl;
 }
@@ -853,11 +742,12 @@ tp_status launch(const Plan& pl, const AttendParams& p, cudaStream_t stream) {
     r.err = cudaFuncSetAttribute(paged_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
   });
   if (r.err != cudaSuccess) return cuda_fail(r.err, "cudaFuncSetAttribute(max dynamic shared memory)");
-  const dim3 grid = pl.per_item ? dim3(static_cast<unsigned>(pl.slots), static_cast<unsigned>(p.heads))
+  const dim3 grid = pl.per_item ? dim3(static_cast<unsigned>(p.b.n_seqs), static_cast<unsigned>(p.heads))
                                 : dim3(static_cast<unsigned>(pl.ctas));
   cudaError_t e = launch_pdl(paged_rows_kernel<D, NT>, grid, dim3(kThreads), C::SMEM, stream, p);
   if (e == cudaSuccess && !pl.per_item)
-    e = launch_pdl(paged_join_kernel<D, NT>, dim3(static_cast<unsigned>(pl.ctas)), dim3(kThreads), 0, stream, p);
+    e = launch_pdl(paged_join_kernel<D, C::ROWS>, dim3(static_cast<unsigned>(pl.ctas), (C::ROWS + kJoinRows - 1) / kJoinRows),
+                   dim3(kJoinThreads), 0, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return TP_OK;
 }
@@ -888,7 +778,7 @@ size_t tp_attention_paged_workspace_bytes(const tp_paged_cache* cache, const tp_
     if (st != TP_OK || empty) return st;
     const int sms = sm_count();
     if (sms <= 0) return fail(TP_ERR_CUDA, "no CUDA device");
-    bytes = make_plan(*cache, *batch, T, n_heads / cache->n_kv_heads, sms).ws_bytes;
+    bytes = make_plan(*cache, *batch, n_heads / cache->n_kv_heads, sms).ws_bytes;
     return TP_OK;
   });
   return bytes;
@@ -916,6 +806,8 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
       return fail(TP_ERR_ALIGNMENT, "ld_q (%lld) and ldo (%lld) must be multiples of 8", (long long)ld_q, (long long)ldo);
     AttendParams p{};
     for (int r = 0; r < c.n_ranks; ++r) {
+      p.k[r] = static_cast<const uint8_t*>(c.k[r]);
+      p.v[r] = static_cast<const uint8_t*>(c.v[r]);
       if (q[r] == nullptr || out[r] == nullptr) return fail(TP_ERR_INVALID_ARG, "q[%d] or out[%d] is NULL", r, r);
       if (!aligned16(q[r]) || !aligned16(out[r]))
         return fail(TP_ERR_ALIGNMENT, "q[%d] or out[%d] is not 16-byte aligned", r, r);
@@ -926,14 +818,14 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
     }
     const int sms = sm_count();
     if (sms <= 0) return fail(TP_ERR_CUDA, "no CUDA device");
-    const Plan pl = make_plan(c, *batch, T, n_heads / c.n_kv_heads, sms);
+    const Plan pl = make_plan(c, *batch, n_heads / c.n_kv_heads, sms);
     if (pl.ws_bytes > 0 && (workspace == nullptr || ws_bytes < pl.ws_bytes))
       return fail(TP_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace == nullptr ? size_t(0) : ws_bytes, pl.ws_bytes);
     if (pl.ws_bytes > 0 && !aligned16(workspace)) return fail(TP_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
     unsigned int* status = status_word();
     if (status == nullptr) return fail(TP_ERR_CUDA, "cannot locate the kernel status word");
     const int64_t ld_page = c.ld_page != 0 ? c.ld_page : static_cast<int64_t>(c.n_kv_heads) * c.page_size * c.head_dim;
-    for (int r = 0; r < c.n_ranks && c.n_pages > 0; ++r) {
+    for (int r = 0; r < c.n_ranks && c.n_pages > 0 && !pl.tiles; ++r) {
       st = encode_pages(&p.map_k[r], c.k[r], c, ld_page);
       if (st == TP_OK) st = encode_pages(&p.map_v[r], c.v[r], c, ld_page);
       if (st != TP_OK) return st;
@@ -941,6 +833,7 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
     p.b = batch_view(c, *batch, T, status);
     p.ld_q = ld_q != 0 ? ld_q : wide;
     p.ldo = ldo != 0 ? ldo : wide;
+    p.ld_page = ld_page;
     p.ld_scales = c.ld_scales != 0 ? c.ld_scales : c.n_kv_heads;
     p.n_kv = c.n_kv_heads;
     p.group = n_heads / c.n_kv_heads;
@@ -950,10 +843,11 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
     p.scale_log2e = scale * 1.4426950408889634f;
     p.per_item = pl.per_item ? 1 : 0;
     if (!pl.per_item) {
-      p.joins = static_cast<int4*>(workspace);
-      p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.ctas * sizeof(int4));
+      p.joins = static_cast<Join*>(workspace);
+      p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.ctas * sizeof(Join));
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (pl.tiles) return launch_paged_tiles(c.head_dim, pl.ctas, p, s);
     if (c.head_dim == 128) return pl.one_row_tile ? launch<128, 1>(pl, p, s) : launch<128, 2>(pl, p, s);
     return pl.one_row_tile ? launch<64, 1>(pl, p, s) : launch<64, 2>(pl, p, s);
   });

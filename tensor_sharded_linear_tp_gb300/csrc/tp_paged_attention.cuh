@@ -1,0 +1,131 @@
+// What the kernels of the attention over the paged cache share: their parameters, how a sequence's
+// rows are cut into items and an item's keys into steps, and the join of partial results.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "tp_paged.h"
+
+namespace tp {
+
+// An item in `n` CTAs (0: none), whose parts are to be joined.
+struct Join {
+  int n, a, row0, rows, h, pad[3];
+};
+
+struct AttendParams {
+  CUtensorMap map_k[TP_MAX_DEGREE], map_v[TP_MAX_DEGREE];  // [pages][heads][tokens][D] codes, box of one page's tokens (at most 32)
+  BatchView b;
+  const __nv_bfloat16* q[TP_MAX_DEGREE];
+  __nv_bfloat16* out[TP_MAX_DEGREE];
+  const uint8_t *k[TP_MAX_DEGREE], *v[TP_MAX_DEGREE], *ks[TP_MAX_DEGREE], *vs[TP_MAX_DEGREE];
+  int64_t ld_q, ldo, ld_page, ld_scales;
+  int n_kv, group;             // KV heads of a rank, query heads of a KV head
+  int heads;                   // n_ranks * n_kv
+  int causal, window;
+  float scale_log2e;
+  int per_item;                // 1: a CTA takes one item whole; 0: equal parts of all steps
+  float* parts;                // workspace: two partial items a CTA, O and then (m, l) of each row
+  Join* joins;                 // workspace: the item that begins in a CTA and goes beyond it
+};
+
+// One item: rows [row0, row0 + rows) of a sequence's n * group rows (token by token), and its steps.
+struct Item {
+  SeqView v;
+  int row0, rows;
+  int tile0, tiles;     // steps tile0 .. tile0 + tiles of the sequence's keys
+  int key_end;          // keys from here on are not seen by any row
+};
+
+template <int ROWS, int STEP>
+__device__ __forceinline__ Item item_of(const AttendParams& p, const SeqView& v, int block) {
+  Item it;
+  it.v = v;
+  it.row0 = block * ROWS;
+  it.rows = static_cast<int>(min(static_cast<int64_t>(ROWS), static_cast<int64_t>(v.n) * p.group - it.row0));
+  const int first = it.row0 / p.group, last = (it.row0 + max(it.rows, 1) - 1) / p.group;
+  it.key_end = p.causal ? max(min(static_cast<int64_t>(v.len), static_cast<int64_t>(v.pos0) + last + 1), int64_t(0)) : v.len;
+  const int64_t lo = p.window > 0 ? max(static_cast<int64_t>(v.pos0) + first - p.window + 1, int64_t(0)) : 0;
+  it.tile0 = static_cast<int>(min(lo, static_cast<int64_t>(it.key_end))) / STEP;
+  it.tiles = it.rows > 0 ? max(1, (it.key_end + STEP - 1) / STEP - it.tile0) : 0;   // (a row without keys is an item too)
+  return it;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^e, 0 below fp32's normal range.
+__device__ __forceinline__ float pow2(int e) {
+  return e < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(min(e, 127) + 127) << 23);
+}
+// A scale byte's value (NaN for 255).
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7FFFFFFFu) : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Joins up to `n` pieces of a row: weights l 2^(m - max m); 0 where no piece has seen a key.
+template <typename ML, typename O4>
+__device__ __forceinline__ float4 join_row(int n, ML&& ml, O4&& o4) {
+  float top = -INFINITY;
+  for (int i = 0; i < n; ++i) top = fmaxf(top, ml(i).x);
+  if (top == -INFINITY) top = 0.0f;
+  float sum = 0.0f;
+  float4 acc = make_float4(0, 0, 0, 0);
+  for (int i = 0; i < n; ++i) {
+    const float2 v = ml(i);
+    const float w = v.y * ex2(v.x - top);
+    const float4 o = o4(i);
+    sum += w;
+    acc.x += w * o.x, acc.y += w * o.y, acc.z += w * o.z, acc.w += w * o.w;
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+}
+
+__device__ __forceinline__ void store_row4(const AttendParams& p, int a, int h, int row, int col, int D, const float4& v) {
+  const int rank = h / p.n_kv, head = h - rank * p.n_kv;
+  const int token = row / p.group, hq = row - token * p.group;
+  __nv_bfloat16* dst = p.out[rank] + static_cast<int64_t>(a + token) * p.ldo + (static_cast<int64_t>(head) * p.group + hq) * D + col;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+// Where the steps of all items are cut: CTA c of n has the steps from total * c / n on.
+__device__ __forceinline__ int64_t cut(int64_t total, int64_t c, int64_t n) { return total * c / n; }
+
+constexpr int kJoinRows = 8, kJoinThreads = 256;
+
+// Joins the items that lie in several CTAs: blocks (c, .) the one that begins in CTA c and goes beyond
+// it (its piece in that CTA's second part, the others in the first parts of those behind), eight rows a block.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int PART = ROWS * (D + 2);
+  pdl_launch_dependents();
+  pdl_wait();
+  const Join join = p.joins[blockIdx.x];
+  const int end = min(join.rows, static_cast<int>(blockIdx.y + 1) * kJoinRows) * D;
+  if (join.n == 0) return;
+  const float* own = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * PART;
+  auto part = [&](int i) { return i == 0 ? own : own + (2 * i - 1) * static_cast<int64_t>(PART); };
+  for (int at = blockIdx.y * kJoinRows * D + threadIdx.x * 4; at < end; at += kJoinThreads * 4) {
+    const int row = at / D, col = at - row * D;
+    const float4 o = join_row(
+        join.n, [&](int i) { return *reinterpret_cast<const float2*>(part(i) + ROWS * D + 2 * row); },
+        [&](int i) { return *reinterpret_cast<const float4*>(part(i) + at); });
+    store_row4(p, join.a, join.h, join.row0 + row, col, D, o);
+  }
+}
+
+// The kernel for many rows a KV head (tp_paged_tiles.cu).
+size_t paged_tiles_part_floats(int head_dim);
+tp_status launch_paged_tiles(int head_dim, int ctas, const AttendParams& p, cudaStream_t stream);
+
+}  // namespace tp
