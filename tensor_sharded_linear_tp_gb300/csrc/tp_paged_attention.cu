@@ -116,13 +116,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
   return v;
 }
-__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, uint32_t bar, int token, int head, int page) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(map), "r"(bar), "r"(0), "r"(token), "r"(head), "r"(page)
-      : "memory");
-}
-
 // A step's data in shared memory: row `key`, 16-byte chunk c, under the TMA's swizzle (128 or 64 bytes).
 template <int D>
 __device__ __forceinline__ uint32_t chunk_at(int key, int c) {
@@ -825,7 +818,7 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
     unsigned int* status = status_word();
     if (status == nullptr) return fail(TP_ERR_CUDA, "cannot locate the kernel status word");
     const int64_t ld_page = c.ld_page != 0 ? c.ld_page : static_cast<int64_t>(c.n_kv_heads) * c.page_size * c.head_dim;
-    for (int r = 0; r < c.n_ranks && c.n_pages > 0 && !pl.tiles; ++r) {
+    for (int r = 0; r < c.n_ranks && c.n_pages > 0; ++r) {
       st = encode_pages(&p.map_k[r], c.k[r], c, ld_page);
       if (st == TP_OK) st = encode_pages(&p.map_v[r], c.v[r], c, ld_page);
       if (st != TP_OK) return st;

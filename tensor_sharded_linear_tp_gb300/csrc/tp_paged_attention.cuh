@@ -98,6 +98,14 @@ __device__ __forceinline__ void store_row4(const AttendParams& p, int a, int h, 
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
+// Part of a page (tokens from `token` on) and head into shared memory.
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, uint32_t bar, int token, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(0), "r"(token), "r"(head), "r"(page)
+      : "memory");
+}
+
 // Where the steps of all items are cut: CTA c of n has the steps from total * c / n on.
 __device__ __forceinline__ int64_t cut(int64_t total, int64_t c, int64_t n) { return total * c / n; }
 

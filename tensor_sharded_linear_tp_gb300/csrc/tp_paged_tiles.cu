@@ -8,18 +8,20 @@
 // launch (tp_paged_attention.cuh).  So neither the causal triangle nor ragged lengths leave SMs idle.
 //
 // CTA (512 threads):
-//   warps 0..3    the codes' way: 16-byte loads of the pages, a step ahead in registers, two codes an
-//                 instruction to fp16 (exact), times the page's scale relative to the largest one (a
-//                 power of two), into a ring of two K and two V tiles, 128-byte swizzled.  What no row sees is 0.
+//   warps 0..3    the codes' way (two for K, two for V): a step's codes from shared memory, two an
+//                 instruction to fp16 (exact), times the page's scale relative to the largest one (a power
+//                 of two), into a ring of two K and two V tiles, 128-byte swizzled.  What no row sees is 0.
 //   warps 4..7    softmax of stream 0, warps 8..11 of stream 1, a row a thread (its TMEM lane).
-//   warp 12       one thread issues the MMAs.
+//   warp 12       issues the MMAs.
 //   warp 13       one thread finds the pieces, ahead of the others.
+//   warp 14       finds a step's pages and scales, and has its codes loaded by TMA.
+//   warp 15       asks Q's rows of the next piece into L2.
 // The two streams keep the tensor core busy in turn: while one's softmax runs, the other's products
 // do.  With more than 128 rows each stream has 128 of them, over every step; otherwise both have
 // the same rows, stream 0 the even steps and stream 1 the odd ones, and they are joined at the end.
 //
-// Tensor memory: S_g in columns [128 g, 128 g + 128), its P over the first 64 as fp16 pairs; O_g in
-// [256 + D g, + D).  Per turn: S = Q K^T (K-major operands), P.V with P from tensor memory and V
+// Tensor memory: S_g in columns [128 g, 128 g + 128), its P (fp16 pairs) over the first 32 and the
+// last 32 of them; O_g in [256 + D g, + D).  Per turn: S = Q K^T (K-major operands), P.V with P from tensor memory and V
 // as stored (MN-major).  A stream's S of the next turn follows its P.V in the issue order, so that it
 // may overwrite P.
 //
@@ -32,6 +34,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <mutex>
 
 #include "tp_internal.h"
@@ -44,15 +47,18 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kKeys = 128;                        // keys of a step
 constexpr int kRows = 256;                        // rows of an item
-constexpr int kInfos = 4;                         // steps whose Info is kept: those in the ring and the one in the softmax
+constexpr int kInfos = 8;                         // steps whose Info is kept: five are in use (see pages_way)
 constexpr uint32_t SUB = 16384;                   // 128 rows x 64 fp16, 128-byte swizzled
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
-// What the softmax has to know of a step's pages.
-struct Info {
+// A step's pages, by 16 keys.
+struct alignas(16) Info {
   int e_k, e_v;            // exponents that the step's K and V are relative to
-  uint32_t unseen, nan;    // by 16 keys: the page is out of bounds; K or V is NaN
+  uint32_t unseen, nan;    // bits: the page is out of bounds; K or V is NaN
+  uint32_t by[2][8];       // what K's and V's codes are multiplied with, as fp16 twice; kZero where they enter as 0
+  int keys;                // of the step's keys, those that some row sees; the others enter as 0
 };
+constexpr uint32_t kZero = 0xFFFFFFFFu;
 
 // A piece of an item: steps from .. from + n of its sequence's keys (n = 0: no more pieces).
 struct PieceInfo {
@@ -67,13 +73,14 @@ struct PieceInfo {
   __device__ __forceinline__ int turns() const { return split() ? n : 2 * n; }
 };
 constexpr int kPieces = 4;
-constexpr int kPieceReaders = 4 + 8 + 1;   // warps of the codes' way and the softmax, the MMA thread
+constexpr int kPieceReaders = 8 + 1 + 2;   // the warps of the softmax, of the MMAs, of the pages and of the prefetch
 
 struct alignas(16) TilesCtrl {
   uint64_t q_full[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t info_full[kInfos];
+  uint64_t raw_full[2], raw_empty[2];   // K's and V's codes of a step
   uint64_t pair;           // both streams' softmax threads
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t drain;
@@ -86,8 +93,9 @@ struct alignas(16) TilesCtrl {
   struct {
     int s, h, block, tile;
   } start;
-  float ml[128][3];        // stream 1's m, l and exponent of V of each row, for the join of the streams
 };
+
+static_assert(sizeof(Info) % 16 == 0 && offsetof(Info, by) % 16 == 0 && offsetof(TilesCtrl, info) % 16 == 0, "read as uint4");
 
 template <int D>
 struct Dims {
@@ -96,7 +104,9 @@ struct Dims {
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_K = 2 * TILE;
   static constexpr uint32_t OFF_V = OFF_K + 2 * TILE;
-  static constexpr uint32_t DATA = OFF_V + 2 * TILE;
+  static constexpr uint32_t OFF_RAW = OFF_V + 2 * TILE;    // codes of a step: K, then V
+  static constexpr uint32_t RAW = kKeys * D;
+  static constexpr uint32_t DATA = OFF_RAW + 2 * RAW;
   static constexpr size_t SMEM = 1024 + DATA + sizeof(TilesCtrl);
   static_assert(SMEM <= 232448, "shared memory");
 };
@@ -315,16 +325,10 @@ __device__ __forceinline__ void find_part(const AttendParams& p, TilesCtrl* ctl,
 
 // ---------------------------------------------------------------- the codes' way (warps 0..3)
 
-// A warp's rows of a tile: 32 keys, key 32 warp + 8 i + lane / 4, and of it 16-byte chunks lane % 4 and 4 more.
-template <int D>
-struct Raw {
-  uint4 v[4][D / 64];
-};
-
 // Pages of a sequence and head, 32 at a time, a page a lane.
 struct Pages {
   int page0, page;
-  uint32_t info;     // as in the rows kernel: K's and V's scale byte, and that the index is valid
+  uint32_t info;     // K's and V's scale byte, and that the index is valid
 };
 constexpr uint32_t kSeen = 0x10000;
 
@@ -345,261 +349,290 @@ __device__ __forceinline__ void load_pages(const AttendParams& p, Pages& pg, con
   }
 }
 
-// What a warp keeps of a step: where its two groups of 16 keys are, and their scales.
-struct Scales {
-  uint32_t info[2];
-  int e_k, e_v;         // the largest exponents of the step's pages
-  uint32_t unseen, nan;
-};
-struct Step {
-  int64_t off[2];       // of the group's page and head in the codes, -1: not there
-  int key0;
-  Scales scales;
-};
-
 // get_piece for a whole warp: null behind the last.
 __device__ __forceinline__ const PieceInfo* warp_piece(TilesCtrl* ctl, uint32_t k, unsigned int* status) {
   const PieceInfo* w = get_piece(ctl, nullptr, k, status);
   return __all_sync(0xffffffffu, w != nullptr) && w->n > 0 ? w : nullptr;
 }
 
+// The pages' way (warp 14): where a step's keys are and what their scales are, for the others; and
+// their codes into shared memory by TMA, a box a page (of 32 keys at most).
 template <int D>
-__device__ __forceinline__ Step locate(const AttendParams& p, Pages& pg, const PieceInfo& w, int tile, int warp, int lane) {
-  Step st;
-  st.key0 = tile * kKeys;
-  const int shift = p.b.page_shift, first = st.key0 >> shift, pages = max(kKeys >> shift, 1);
-  if (first < pg.page0 || first + pages > pg.page0 + 32) load_pages(p, pg, w, first, lane);
-  const int head = w.h - w.h / p.n_kv * p.n_kv;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int key = st.key0 + 32 * warp + 16 * i, src = (key >> shift) - pg.page0;
-    st.scales.info[i] = __shfl_sync(0xffffffffu, pg.info, src);
-    const int page = __shfl_sync(0xffffffffu, pg.page, src);
-    st.off[i] = (st.scales.info[i] & kSeen) != 0
-                    ? page * p.ld_page + (static_cast<int64_t>(head) * p.b.page_size + (key & (p.b.page_size - 1))) * D
-                    : -1;
-  }
-  // Lane i < 8: the page of the step's i-th 16 keys.
-  const uint32_t mine = __shfl_sync(0xffffffffu, pg.info, ((st.key0 + 16 * (lane & 7)) >> shift) - pg.page0);
-  const uint32_t k = mine & 0xFFu, v = (mine >> 8) & 0xFFu;
-  const bool seen = (mine & kSeen) != 0;
-  // (Keys behind the sequence's last are never seen; their pages are not there either.)
-  const bool there = st.key0 + 16 * (lane & 7) < w.len;
-  st.scales.unseen = __ballot_sync(0xffffffffu, !seen && there) & 0xFFu;
-  st.scales.nan = __ballot_sync(0xffffffffu, seen && (k == 255u || v == 255u)) & 0xFFu;
-  st.scales.e_k = __reduce_max_sync(0xffffffffu, seen && k != 255u ? static_cast<int>(k) - 127 : -127);
-  st.scales.e_v = __reduce_max_sync(0xffffffffu, seen && v != 255u ? static_cast<int>(v) - 127 : -127);
-  return st;
-}
-
-template <int D>
-__device__ __forceinline__ void load_raw(Raw<D>& r, const uint8_t* codes, const Step& st, int key_end, int warp, int lane) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int key = 8 * (i & 1) + (lane >> 2);       // of the group of 16
-    const bool there = st.off[i >> 1] >= 0 && st.key0 + 32 * warp + 16 * (i >> 1) + key < key_end;
-    const uint4* at = reinterpret_cast<const uint4*>(codes + st.off[i >> 1] + key * D) + (lane & 3);
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) r.v[i][c] = there ? at[4 * c] : make_uint4(0, 0, 0, 0);
-  }
-}
-
-// To fp16 in the tile at `tile`: element d of a key is in sub-tile d / 64, 16-byte chunk (d % 64) / 8 of
-// the key's row, swizzled.  Eight lanes store two keys' chunks of one parity each: no bank twice.
-template <int D>
-__device__ __forceinline__ void store_tile(const Raw<D>& r, uint32_t tile, const uint32_t (&by)[2], int warp, int lane) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 32 * warp + 8 * i + (lane >> 2);
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-      const uint32_t w[4] = {r.v[i][c].x, r.v[i][c].y, r.v[i][c].z, r.v[i][c].w};
-      uint32_t h[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        h[2 * k] = scaled_pair(w[k], by[i >> 1]);
-        h[2 * k + 1] = scaled_pair(w[k] >> 16, by[i >> 1]);
-      }
-      const uint32_t dst = tile + c * SUB + row * 128;
-      const int chunk = 2 * (lane & 3), x = row & 7;
-      ptx::st_shared_v4(dst + ((chunk ^ x) << 4), h[0], h[1], h[2], h[3]);
-      ptx::st_shared_v4(dst + (((chunk + 1) ^ x) << 4), h[4], h[5], h[6], h[7]);
-    }
-  }
-}
-
-template <int D>
-__device__ __forceinline__ void codes_way(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, int warp, int lane) {
+__device__ __forceinline__ void pages_way(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, int lane) {
   using M = Dims<D>;
   volatile int* abort_flag = &ctl->abort;
-  uint32_t k = 0;
-  const PieceInfo* w = warp_piece(ctl, k, p.b.status);
-  if (w == nullptr) return;
+  const int shift = p.b.page_shift, boxes = p.b.page_size == 16 ? 8 : 4, box_keys = kKeys / boxes;
   Pages pg{-64, 0, 0};
-  Raw<D> rk, rv;
-  int tile = w->from, end = tile + w->n, key_end = w->key_end, h = w->h, s = w->s;   // of the step that is loaded next
-  int e_run = -1000;                         // V's exponent in the piece so far
-  Step next = locate<D>(p, pg, *w, tile, warp, lane);
-  load_raw<D>(rk, p.k[h / p.n_kv], next, key_end, warp, lane);
-  load_raw<D>(rv, p.v[h / p.n_kv], next, key_end, warp, lane);
-  for (uint32_t t = 0;; ++t) {
-    const Scales st = next.scales;
-    e_run = max(e_run, st.e_v);
-    const int e_now = e_run;
-    // The step behind this one, in this piece or the next.
-    bool more = true;
-    if (++tile == end) {
+  int s = -1, h = -1;
+  uint32_t t = 0;
+  bool ok = true;
+  for (uint32_t k = 0; ok; ++k) {
+    const PieceInfo* piece = warp_piece(ctl, k, p.b.status);
+    if (piece == nullptr) break;
+    const PieceInfo w = *piece;
+    if (w.s != s || w.h != h) pg.page0 = -64, s = w.s, h = w.h;
+    const int rank = w.h / p.n_kv, head = w.h - rank * p.n_kv;
+    int e_run = -127;
+    for (int tile = w.from; tile < w.from + w.n && ok; ++tile, ++t) {
+      const int key0 = tile * kKeys, first = key0 >> shift;
+      if (first < pg.page0 || first + max(kKeys >> shift, 1) > pg.page0 + 32) load_pages(p, pg, w, first, lane);
+      // Lane i < 8: the page of the step's i-th 16 keys (and lanes behind them the same again).
+      const int key16 = key0 + 16 * (lane & 7);
+      const uint32_t mine = __shfl_sync(0xffffffffu, pg.info, (key16 >> shift) - pg.page0);
+      const uint32_t kb = mine & 0xFFu, vb = (mine >> 8) & 0xFFu;
+      const bool seen = (mine & kSeen) != 0, nan = seen && (kb == 255u || vb == 255u);
+      const uint32_t unseen = __ballot_sync(0xffffffffu, !seen && key16 < w.len) & 0xFFu;   // (behind the last key nothing is seen anyway)
+      const uint32_t nans = __ballot_sync(0xffffffffu, nan) & 0xFFu;
+      const int e_k = __reduce_max_sync(0xffffffffu, seen && !nan ? static_cast<int>(kb) - 127 : -127);
+      e_run = max(e_run, __reduce_max_sync(0xffffffffu, seen && !nan ? static_cast<int>(vb) - 127 : -127));
+      // The box of lane i < boxes.
+      const int key_box = key0 + box_keys * (lane & (boxes - 1));
+      const uint32_t box_info = __shfl_sync(0xffffffffu, pg.info, (key_box >> shift) - pg.page0);
+      const int box_page = __shfl_sync(0xffffffffu, pg.page, (key_box >> shift) - pg.page0);
+      const bool load = lane < boxes && (box_info & kSeen) != 0 && key_box < w.key_end;
+      const int n_boxes = __popc(__ballot_sync(0xffffffffu, load));
+      // (The codes of step t - 2 have been taken, so V of step t - 3 is stored, P.V of step t - 5 done and
+      // with it everything that reads that step's Info.)
+      Info& info = ctl->info[t % kInfos];
+      if (lane < 8) {
+        info.by[0][lane] = seen && !nan ? f16_pow2(static_cast<int>(kb) - 127 - e_k + 7) : kZero;
+        info.by[1][lane] = seen && !nan ? f16_pow2(static_cast<int>(vb) - 127 - e_run + 7) : kZero;
+      }
+      if (lane == 0) info.e_k = e_k, info.e_v = e_run, info.unseen = unseen, info.nan = nans, info.keys = w.key_end - key0;
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_empty[k % kPieces]));
-      w = warp_piece(ctl, ++k, p.b.status);
-      more = w != nullptr;
-      if (more) {
-        if (w->s != s || w->h != h) pg.page0 = -64;
-        tile = w->from, end = tile + w->n, key_end = w->key_end, h = w->h, s = w->s;
-        e_run = -1000;
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->info_full[t % kInfos]));
+#pragma unroll 1
+      for (int i = 0; i < 2 && ok; ++i) {
+        const uint32_t full = ptx::smem_addr(&ctl->raw_full[i]);
+        ok = __all_sync(0xffffffffu, wait(ptx::smem_addr(&ctl->raw_empty[i]), (t & 1) ^ 1u, abort_flag, p.b.status));
+        if (!ok) break;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(n_boxes) * box_keys * D);
+        __syncwarp();
+        if (load)
+          tma_load_page(sbase + M::OFF_RAW + i * M::RAW + lane * box_keys * D, i == 0 ? &p.map_k[rank] : &p.map_v[rank], full,
+                        key_box & (p.b.page_size - 1), head, box_page);
       }
     }
-    if (more) next = locate<D>(p, pg, *w, tile, warp, lane);
-    const uint32_t stage = t & 1, parity = ((t >> 1) & 1) ^ 1u;
-    uint32_t by[2];
-    // K: the tile two steps back has been multiplied.
-    if (!__all_sync(0xffffffffu, wait(ptx::smem_addr(&ctl->k_empty[stage]), parity, abort_flag, p.b.status))) return;
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_empty[k % kPieces]));
+  }
+  // The last copies land before the CTA can exit.
+  for (int i = 0; i < 2 && t > 0; ++i) wait(ptx::smem_addr(&ctl->raw_full[i]), (t - 1) & 1, abort_flag, p.b.status, true);
+}
+
+// The codes' way: warps 0 and 1 take K, 2 and 3 V, each 64 keys of every step, from shared memory to fp16
+// in their tile, once the tile two steps back has been multiplied.
+template <int D>
+__device__ __forceinline__ void codes_way(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, int64_t steps, int warp, int lane) {
+  using M = Dims<D>;
+  constexpr int C = D / 64;                  // 16-byte chunks of a key that a lane has: lane % 4 and 4 more
+  volatile int* abort_flag = &ctl->abort;
+  const int is_v = warp >> 1;
+  // Eight lanes have two keys r and r ^ 5 of a group of eight: their chunks meet no bank twice, neither
+  // where they are read (rows of D bytes, swizzled) nor where they are written (rows of 128).
+  const int r8 = (lane >> 3) ^ ((lane & 4) != 0 ? 5 : 0), row0 = 64 * (warp & 1) + r8;   // keys row0 + 8 i
+  const uint32_t full = ptx::smem_addr(is_v ? &ctl->v_full[0] : &ctl->k_full[0]);
+  const uint32_t empty = ptx::smem_addr(is_v ? &ctl->v_empty[0] : &ctl->k_empty[0]);
+  const uint32_t raw_full = ptx::smem_addr(&ctl->raw_full[is_v]), raw_empty = ptx::smem_addr(&ctl->raw_empty[is_v]);
+  const uint32_t src = sbase + M::OFF_RAW + is_v * M::RAW + row0 * D + (((lane & 3) ^ (D == 128 ? r8 : r8 >> 1 & 3)) << 4);
+  // Element d of a key is in sub-tile d / 64, 16-byte chunk (d % 64) / 8 of the key's row, swizzled.
+  const uint32_t dst0 = sbase + (is_v ? M::OFF_V : M::OFF_K) + row0 * 128 + (((2 * (lane & 3)) ^ r8) << 4);
+  for (uint32_t t = 0; t < steps; ++t) {
+    if (!__all_sync(0xffffffffu, wait(raw_full, t & 1, abort_flag, p.b.status))) return;
+    uint4 raw[8][C];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) by[i] = (st.info[i] & 0xFFu) == 255u ? 0u : f16_pow2(static_cast<int>(st.info[i] & 0xFFu) - 127 - st.e_k + 7);
-    if (st.nan != 0) {      // a NaN page's codes are NaN: 0 instead (the softmax knows)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int c = 0; c < C; ++c)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(raw[i][c].x), "=r"(raw[i][c].y), "=r"(raw[i][c].z), "=r"(raw[i][c].w)
+                     : "r"((src ^ (c * 64)) + i * 8 * D) : "memory");
+    const Info& info = ctl->info[t % kInfos];
+    const uint4 by4 = *reinterpret_cast<const uint4*>(&info.by[is_v][4 * (warp & 1)]);
+    const int keys = info.keys - row0;
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(raw_empty);
+    const uint32_t stage = t & 1;
+    if (!__all_sync(0xffffffffu, wait(empty + 8 * stage, ((t >> 1) & 1) ^ 1u, abort_flag, p.b.status))) return;
+    const uint32_t dst = dst0 + stage * M::TILE, by[4] = {by4.x, by4.y, by4.z, by4.w};
+    if (__any_sync(0xffffffffu, by4.x == kZero || by4.y == kZero || by4.z == kZero || by4.w == kZero || keys <= 56)) {
+      // Codes that are not there, of NaN pages or behind the last key that is seen (any content): 0.
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          if ((st.info[i >> 1] & 0xFFu) == 255u) rk.v[i][c] = make_uint4(0, 0, 0, 0);
-          if ((st.info[i >> 1] & 0xFF00u) == 0xFF00u) rv.v[i][c] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (by[i >> 1] == kZero || 8 * i >= keys) raw[i][c] = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t f = by[i >> 1] == kZero ? 0u : by[i >> 1];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint32_t x[4] = {raw[i][c].x, raw[i][c].y, raw[i][c].z, raw[i][c].w};
+        uint32_t h[8];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          h[2 * n] = scaled_pair(x[n], f);
+          h[2 * n + 1] = scaled_pair(x[n] >> 16, f);
         }
-    }
-    store_tile<D>(rk, sbase + M::OFF_K + stage * M::TILE, by, warp, lane);
-    if (warp == 0 && lane == 0) {
-      // (The slot's last reader was done before the tile two steps back could be multiplied.)
-      ctl->info[t % kInfos] = Info{st.e_k, e_now, st.unseen, st.nan};
-      ptx::mbar_arrive(ptx::smem_addr(&ctl->info_full[t % kInfos]));
+        ptx::st_shared_v4(dst + c * SUB + i * 1024, h[0], h[1], h[2], h[3]);
+        ptx::st_shared_v4((dst ^ 16) + c * SUB + i * 1024, h[4], h[5], h[6], h[7]);
+      }
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->k_full[stage]));
-    if (more) load_raw<D>(rk, p.k[h / p.n_kv], next, key_end, warp, lane);
-    // V.
-    if (!__all_sync(0xffffffffu, wait(ptx::smem_addr(&ctl->v_empty[stage]), parity, abort_flag, p.b.status))) return;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      by[i] = (st.info[i] & 0xFF00u) == 0xFF00u ? 0u : f16_pow2(static_cast<int>((st.info[i] >> 8) & 0xFFu) - 127 - e_now + 7);
-    store_tile<D>(rv, sbase + M::OFF_V + stage * M::TILE, by, warp, lane);
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->v_full[stage]));
-    if (!more) return;
-    load_raw<D>(rv, p.v[h / p.n_kv], next, key_end, warp, lane);
+    if (lane == 0) ptx::mbar_arrive(full + 8 * stage);
   }
 }
 
-// ---------------------------------------------------------------- the MMAs (one thread)
+// Asks the next piece's rows of Q into L2 (warp 15), while this piece is worked on.
+template <int D>
+__device__ __forceinline__ void prefetch_q(const AttendParams& p, TilesCtrl* ctl, int lane) {
+  for (uint32_t k = 0;; ++k) {
+    const PieceInfo* piece = warp_piece(ctl, k, p.b.status);
+    if (piece == nullptr) return;
+    const int rank = piece->h / p.n_kv, head = piece->h - rank * p.n_kv;
+    for (int row = lane; row < piece->rows; row += 32) {
+      const int r = piece->row0 + row, token = r / p.group;
+      const __nv_bfloat16* at = p.q[rank] + static_cast<int64_t>(piece->a + token) * p.ld_q +
+                                (static_cast<int64_t>(head) * p.group + (r - token * p.group)) * D;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+      if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 64));
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_empty[k % kPieces]));
+  }
+}
 
+// ---------------------------------------------------------------- the MMAs (warp 12)
+
+// Column of S_g's region in which P's 16 keys kk are: the first 64 keys in columns 0..31, the last 64 in 96..127.
+__host__ __device__ constexpr uint32_t p_column(int kk) { return kk < 4 ? 8u * kk : 64u + 8u * kk; }
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+
+// The whole warp runs the loop, so that addresses stay in uniform registers; one lane issues.
 template <int D>
 __device__ __forceinline__ void issue_mmas(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, uint32_t tmem) {
   using M = Dims<D>;
   volatile int* abort_flag = &ctl->abort;
+  const bool issuer = elect_one();
+  auto wait_all = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity, abort_flag, p.b.status)); };
   // fp16 operands, fp32 accumulators (the operand formats' codes are 0).
   constexpr uint32_t idesc = (1u << 4) | ((kKeys >> 3) << 17) | ((128u >> 4) << 24);
   constexpr uint32_t idesc_pv = (1u << 4) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24) | ptx::kIdescMnMajorB;
+  const uint64_t q0 = ptx::sw128_kmajor_desc(sbase + M::OFF_Q), k0 = ptx::sw128_kmajor_desc(sbase + M::OFF_K);
+  const uint64_t v0 = ptx::sw128_mnmajor_desc(sbase + M::OFF_V, SUB, 1024);
+  const uint32_t k_full = ptx::smem_addr(&ctl->k_full[0]), k_empty = ptx::smem_addr(&ctl->k_empty[0]);
+  const uint32_t v_full = ptx::smem_addr(&ctl->v_full[0]), v_empty = ptx::smem_addr(&ctl->v_empty[0]);
+  const uint32_t s_full = ptx::smem_addr(&ctl->s_full[0]), p_full = ptx::smem_addr(&ctl->p_full[0]);
   uint32_t base = 0;                      // steps before this piece
-  uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+  uint32_t q_uses0 = 0, q_uses1 = 0, p_uses0 = 0, p_uses1 = 0;
   bool ok = true;
   for (uint32_t k = 0; ok; ++k) {
-    const PieceInfo* w = get_piece(ctl, nullptr, k, p.b.status);
-    if (w == nullptr || w->n == 0) break;
+    const PieceInfo* w = warp_piece(ctl, k, p.b.status);
+    if (w == nullptr) break;
     const bool split = w->split();
     const int turns = w->turns(), n = w->n;
-    ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_empty[k % kPieces]));
-    auto issue_s = [&](int u) {
-      const int g = u & 1, step = split ? u : u >> 1;
-      const uint32_t t = base + step;
-      if ((split || g == 0) && !wait(ptx::smem_addr(&ctl->k_full[t & 1]), (t >> 1) & 1, abort_flag, p.b.status)) return false;
-      ptx::tc_fence_after();
-      const uint32_t kb = sbase + M::OFF_K + (t & 1) * M::TILE, qb = sbase + M::OFF_Q + (split ? 0 : g) * M::TILE;
+    __syncwarp();
+    if (issuer) ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_empty[k % kPieces]));
+    ok = wait_all(ptx::smem_addr(&ctl->q_full[0]), q_uses0++ & 1);
+    if (!split) ok = ok && wait_all(ptx::smem_addr(&ctl->q_full[1]), q_uses1++ & 1);
+    // Turn u: P.V of turn u - 2 of the same stream first (none for u < 2), then S of turn u (none behind the last).
+    for (int u = 0; u < turns + 2 && ok; ++u) {
+      const uint32_t g = u & 1;
+      if (u >= 2) {
+        const uint32_t t = base + (split ? u - 2 : (u - 2) >> 1), stage = t & 1;
+        if (split || g == 0) ok = wait_all(v_full + 8 * stage, (t >> 1) & 1);
+        ok = ok && wait_all(p_full + 8 * g, (g != 0 ? p_uses1++ : p_uses0++) & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (issuer) {
+          const uint64_t vdesc = v0 + stage * (M::TILE >> 4);
+          const uint32_t o = tmem + 2 * kKeys + g * D, pr = tmem + g * kKeys;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t sub = (kk >> 2) * SUB, k4 = 2u * (kk & 3);
-        ptx::umma_bf16(tmem + g * kKeys, ptx::sw128_kmajor_desc(qb + sub) + k4, ptx::sw128_kmajor_desc(kb + sub) + k4, idesc, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            ptx::umma_bf16_ts(o, pr + p_column(kk), vdesc + kk * (2048u >> 4), idesc_pv, (u >= 4 || kk > 0) ? 1u : 0u);
+          if (split || g == 1) ptx::umma_commit(v_empty + 8 * stage);
+          if (u >= turns) ptx::umma_commit(ptx::smem_addr(&ctl->o_done[0]) + 8 * g);
+        }
       }
-      ptx::umma_commit(ptx::smem_addr(&ctl->s_full[g]));
-      if (split || g == 1) ptx::umma_commit(ptx::smem_addr(&ctl->k_empty[t & 1]));
-      return true;
-    };
-    for (int g = 0; g < (split ? 1 : 2) && ok; ++g)
-      ok = wait(ptx::smem_addr(&ctl->q_full[g]), q_uses[g]++ & 1, abort_flag, p.b.status);
-    for (int u = 0; u < 2 && u < turns && ok; ++u) ok = issue_s(u);
-    for (int u = 0; u < turns && ok; ++u) {
-      const int g = u & 1, step = split ? u : u >> 1;
-      const uint32_t t = base + step;
-      ok = ((!split && g == 1) || wait(ptx::smem_addr(&ctl->v_full[t & 1]), (t >> 1) & 1, abort_flag, p.b.status)) &&
-           wait(ptx::smem_addr(&ctl->p_full[g]), p_uses[g]++ & 1, abort_flag, p.b.status);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      const uint64_t vdesc = ptx::sw128_mnmajor_desc(sbase + M::OFF_V + (t & 1) * M::TILE, SUB, 1024);
+      if (u < turns) {
+        const uint32_t t = base + (split ? u : u >> 1), stage = t & 1;
+        if (split || g == 0) ok = wait_all(k_full + 8 * stage, (t >> 1) & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (issuer) {
+          const uint64_t qdesc = q0 + (split ? 0u : g * (M::TILE >> 4)), kdesc = k0 + stage * (M::TILE >> 4);
+          const uint32_t to = tmem + g * kKeys;
 #pragma unroll
-      for (int kk = 0; kk < kKeys / 16; ++kk)
-        ptx::umma_bf16_ts(tmem + 2 * kKeys + g * D, tmem + g * kKeys + kk * 8, vdesc + kk * (2048u >> 4), idesc_pv,
-                          (u >= 2 || kk > 0) ? 1u : 0u);
-      if (split || g == 1) ptx::umma_commit(ptx::smem_addr(&ctl->v_empty[t & 1]));
-      if (u + 2 < turns)
-        ok = issue_s(u + 2);
-      else
-        ptx::umma_commit(ptx::smem_addr(&ctl->o_done[g]));
+          for (int kk = 0; kk < D / 16; ++kk)
+            ptx::umma_bf16(to, qdesc + (kk >> 2) * (SUB >> 4) + 2 * (kk & 3), kdesc + (kk >> 2) * (SUB >> 4) + 2 * (kk & 3), idesc,
+                           kk > 0 ? 1u : 0u);
+          ptx::umma_commit(s_full + 8 * g);
+          if (split || g == 1) ptx::umma_commit(k_empty + 8 * stage);
+        }
+      }
+      __syncwarp();
     }
     base += n;
   }
-  ptx::umma_commit(ptx::smem_addr(&ctl->drain));
+  if (issuer) ptx::umma_commit(ptx::smem_addr(&ctl->drain));
   wait(ptx::smem_addr(&ctl->drain), 0, abort_flag, p.b.status, true);
 }
 
 // ---------------------------------------------------------------- softmax (a row a thread)
 
-// The row's Q as fp16 in its tile, times a power of two; returns what the scores have to be multiplied
-// with (log2 units), NaN where the row holds a NaN or an infinity.
+// The warp's 32 rows of Q as fp16 in its tile, each times a power of two.  at: of this lane's row
+// in q, in elements, negative where there is none.  Returns what that row's scores have to be
+// multiplied with (log2 units), NaN where it holds a NaN or an infinity.
 template <int D>
-__device__ __forceinline__ float load_q(const AttendParams& p, const PieceInfo& w, int row, bool sees, uint32_t tile, int lane_row) {
-  uint4 raw[D / 8];
+__device__ __forceinline__ float load_q(const AttendParams& p, const __nv_bfloat16* q, int64_t at, uint32_t tile, int q4, int lane) {
+  constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes, kBatch = 8;   // lanes of a row; rows of a load; loads in flight
+  const int sub = lane % kLanes;
+  const float sign = p.scale_log2e < 0.0f ? -1.0f : 1.0f;   // (so that the largest score is the largest product)
+  int e_mine = 0;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += kBatch * kRowsAtOnce) {
+    uint4 raw[kBatch];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-  if (row < w.rows) {
-    const int r = w.row0 + row, token = r / p.group, hq = r - token * p.group;
-    const int rank = w.h / p.n_kv, head = w.h - rank * p.n_kv;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q[rank] + static_cast<int64_t>(w.a + token) * p.ld_q +
-                                                      (static_cast<int64_t>(head) * p.group + hq) * D);
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) raw[i] = src[i];
-  }
-  uint32_t* words = reinterpret_cast<uint32_t*>(raw);
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < D / 2; ++i) top = __vmaxu2(top, words[i] & 0x7FFF7FFFu);
-  top = max(top & 0xFFFFu, top >> 16);
-  const int E = static_cast<int>(top >> 7);             // top < 2^(E - 126): times 2^(141 - E) below 2^15
-  float f0 = pow2((141 - E) / 2);
-  const float f1 = pow2(141 - E - (141 - E) / 2);
-  float back = fabsf(p.scale_log2e) * pow2((E - 141) / 2) * pow2(E - 141 - (E - 141) / 2);
-  if (p.scale_log2e < 0.0f) f0 = -f0;                   // (so that the largest score is the largest product)
-  const bool zero = E == 255 || p.scale_log2e == 0.0f;
-  if (E == 255) back = __uint_as_float(0x7FFFFFFFu);
-  if (!sees) back = 1.0f;
-#pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = zero ? 0u : words[4 * c + i];
-      h[i] = f16_pair(__uint_as_float(v << 16) * f0 * f1, __uint_as_float(v & 0xFFFF0000u) * f0 * f1);
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t from = __shfl_sync(0xffffffffu, at, r0 + i * kRowsAtOnce + lane / kLanes);
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (from >= 0) raw[i] = *reinterpret_cast<const uint4*>(q + from + sub * 8);
     }
-    ptx::st_shared_v4(tile + (c >> 3) * SUB + lane_row * 128 + (((c & 7) ^ (lane_row & 7)) << 4), h[0], h[1], h[2], h[3]);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r1 = r0 + i * kRowsAtOnce, r = 32 * q4 + r1 + lane / kLanes;
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+      top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+      for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const int E = static_cast<int>(top >> 7);             // top < 2^(E - 126): times 2^(141 - E) below 2^15
+      const int e_row = __shfl_sync(0xffffffffu, E, ((lane - r1) * kLanes) & 31);
+      if (lane >= r1 && lane < r1 + kRowsAtOnce) e_mine = e_row;
+      const bool zero = E == 255 || p.scale_log2e == 0.0f;
+      const float f0 = zero ? 0.0f : pow2((141 - E) / 2) * sign, f1 = pow2(141 - E - (141 - E) / 2);
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t v = zero ? 0u : w[k];
+        h[k] = f16_pair(__uint_as_float(v << 16) * f0 * f1, __uint_as_float(v & 0xFFFF0000u) * f0 * f1);
+      }
+      ptx::st_shared_v4(tile + (sub >> 3) * SUB + r * 128 + (((sub & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+    }
   }
-  return back;
+  return e_mine == 255 ? __uint_as_float(0x7FFFFFFFu)
+                       : fabsf(p.scale_log2e) * pow2((e_mine - 141) / 2) * pow2(e_mine - 141 - (e_mine - 141) / 2);
 }
 
 struct RowState {
@@ -607,34 +640,74 @@ struct RowState {
   int e_v;
 };
 
-// A step of the row: its scores from tensor memory, P over them, O rescaled where m or V's exponent grew.
-template <int D>
-__device__ __forceinline__ void softmax_step(RowState& st, const Info& info, float back, int lo, int hi, uint32_t s_addr, uint32_t o_addr, bool fresh) {
-  uint32_t sv[kKeys];
+// Ones from bit a up to below bit b (both taken into 0 .. 32).
+__device__ __forceinline__ uint32_t bits(int a, int b) {
+  a = min(max(a, 0), 32), b = min(max(b, 0), 32);
+  return b <= a ? 0u : (0xFFFFFFFFu >> (32 - (b - a))) << a;
+}
+// The 32 keys from t0 on of a step that a row sees, and those whose page is NaN.
+struct Seen {
+  uint32_t seen, nan;
+};
+__device__ __forceinline__ Seen seen_chunk(const Info& info, int t0, int lo, int hi) {
+  const uint32_t u = info.unseen >> (t0 >> 4), n = info.nan >> (t0 >> 4);
+  auto spread = [](uint32_t w) { return (w & 1 ? 0xFFFFu : 0u) | (w & 2 ? 0xFFFF0000u : 0u); };
+  return Seen{bits(lo - t0, hi - t0) & ~spread(u), spread(n)};
+}
+__device__ __forceinline__ void mask_chunk(uint32_t (&sv)[32], const Info& info, int t0, int lo, int hi) {
+  Seen s = seen_chunk(info, t0, lo, hi);
+  asm volatile("" : "+r"(s.seen), "+r"(s.nan));   // (the same keys are masked twice: not from 64 results kept meanwhile)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) ptx::tmem_ld_32x32b_x32(s_addr + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * i]));
+  for (int t = 0; t < 32; ++t) {
+    sv[t] = (s.nan >> t) & 1 ? 0x7FFFFFFFu : sv[t];
+    sv[t] = (s.seen >> t) & 1 ? sv[t] : 0xFF800000u;
+  }
+}
+__device__ __forceinline__ float max_chunk(const uint32_t (&sv)[32], float top) {
+  float mx[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int t = 0; t < 32; t += 2) mx[(t >> 1) & 3] = max3(mx[(t >> 1) & 3], __uint_as_float(sv[t]), __uint_as_float(sv[t + 1]));
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+// P of 32 keys, stored as 16 columns.
+__device__ __forceinline__ void exp_chunk(const uint32_t (&sv)[32], uint64_t c2, uint64_t s2, uint64_t (&ls)[2], uint32_t to) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+    const uint64_t x2 = fma2(f2(__uint_as_float(sv[2 * t]), __uint_as_float(sv[2 * t + 1])), c2, s2);
+    float x0, x1;
+    f2_split(x2, x0, x1);
+    const float p0 = ex2(x0), p1 = ex2(x1);
+    ls[t & 1] = add2(ls[t & 1], f2(p0, p1));
+    pk[t] = f16_pair(p0, p1);
+  }
+  ptx::tmem_st_32x32b_x16(to, pk);
+}
+
+// A step of the row: its scores from tensor memory, P over them, O rescaled where m or V's exponent
+// grew.  64 scores at a time, the first of them read twice (a whole row's 128 registers would spill), in
+// rolled loops: with the code of every chunk laid out, the SM's warps fetched their instructions anew each step.
+template <int D>
+__device__ __forceinline__ void softmax_step(RowState& st, const Info& info, float back, int lo, int hi, bool edge, uint32_t s_addr, uint32_t o_addr, bool fresh) {
+  uint32_t x[32], y[32];
   // (c is kept above 0, so that it may multiply the -infinity of a masked key; smaller ones make every score 0.)
   float c = back * pow2(info.e_k - 7);
   if (c < 0x1p-100f) c = 0x1p-100f;
-  ptx::tmem_ld_wait();
-  if (__any_sync(0xffffffffu, lo > 0 || hi < kKeys)) {
-#pragma unroll
-    for (int t = 0; t < kKeys; ++t)
-      if (t < lo || t >= hi) sv[t] = 0xFF800000u;
-  }
-  if ((info.unseen | info.nan) != 0) {
-#pragma unroll
-    for (int t = 0; t < kKeys; ++t) {
-      if ((info.unseen >> (t >> 4)) & 1) sv[t] = 0xFF800000u;
-      else if (((info.nan >> (t >> 4)) & 1) && t >= lo && t < hi) sv[t] = 0x7FFFFFFFu;
+  float mt = -INFINITY;
+#pragma unroll 1
+  for (int t0 = 0; t0 < kKeys; t0 += 64) {
+    ptx::tmem_ld_32x32b_x32(s_addr + t0, x);
+    ptx::tmem_ld_32x32b_x32(s_addr + t0 + 32, y);
+    ptx::tmem_ld_wait();
+    if (edge) {
+      mask_chunk(x, info, t0, lo, hi);
+      mask_chunk(y, info, t0 + 32, lo, hi);
     }
+    mt = max_chunk(y, max_chunk(x, mt));
   }
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int t = 0; t < kKeys; t += 2) mx[(t >> 1) & 3] = max3(mx[(t >> 1) & 3], __uint_as_float(sv[t]), __uint_as_float(sv[t + 1]));
-  const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+  mt *= c;
   float alpha = 1.0f;
-  if (mt > st.m + 8.0f || (st.m == -INFINITY && mt > st.m)) {
+  if (mt > st.m + 8.0f) {      // (m is -infinity at first)
     alpha = ex2(st.m - mt);
     st.m = mt;
     st.l *= alpha;
@@ -646,43 +719,59 @@ __device__ __forceinline__ void softmax_step(RowState& st, const Info& info, flo
   const bool rescale = !fresh && __any_sync(0xffffffffu, alpha != 1.0f);
   const float shift = 7.0f - (st.m == -INFINITY ? 0.0f : st.m);
   const uint64_t c2 = f2(c, c), s2 = f2(shift, shift);
-  uint64_t ls[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    // Packed in place: the pair of column t comes from entries 2 t and 2 t + 1.
-    uint32_t* pk = &sv[32 * half];
-#pragma unroll
-    for (int t = 0; t < 32; ++t) {
-      const uint64_t x2 = fma2(f2(__uint_as_float(sv[64 * half + 2 * t]), __uint_as_float(sv[64 * half + 2 * t + 1])), c2, s2);
-      float x0, x1;
-      f2_split(x2, x0, x1);
-      const float p0 = ex2(x0), p1 = ex2(x1);
-      ls[t & 3] = add2(ls[t & 3], f2(p0, p1));
-      pk[t] = f16_pair(p0, p1);
+  uint64_t ls[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll 1
+  for (int t0 = 64;; t0 = 0) {
+    exp_chunk(y, c2, s2, ls, s_addr + (t0 != 0 ? p_column(6) : p_column(2)));
+    exp_chunk(x, c2, s2, ls, s_addr + (t0 != 0 ? p_column(4) : p_column(0)));
+    if (t0 == 0) break;
+    ptx::tmem_ld_32x32b_x32(s_addr, x);
+    ptx::tmem_ld_32x32b_x32(s_addr + 32, y);
+    ptx::tmem_ld_wait();
+    if (edge) {
+      mask_chunk(x, info, 0, lo, hi);
+      mask_chunk(y, info, 32, lo, hi);
     }
-    ptx::tmem_st_32x32b_x32(s_addr + 32 * half, *reinterpret_cast<uint32_t(*)[32]>(pk));
   }
   if (rescale) {
 #pragma unroll 1
     for (int col = 0; col < D; col += 32) {
-      uint32_t v[32];
-      ptx::tmem_ld_32x32b_x32(o_addr + col, v);
+      ptx::tmem_ld_32x32b_x32(o_addr + col, x);
       ptx::tmem_ld_wait();
 #pragma unroll
-      for (int t = 0; t < 32; ++t) v[t] = __float_as_uint(__uint_as_float(v[t]) * alpha);
-      ptx::tmem_st_32x32b_x32(o_addr + col, v);
+      for (int t = 0; t < 32; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * alpha);
+      ptx::tmem_st_32x32b_x32(o_addr + col, x);
     }
   }
   ptx::tmem_st_wait();
   float a0, a1;
-  f2_split(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), a0, a1);
+  f2_split(add2(ls[0], ls[1]), a0, a1);
   st.l += a0 + a1;
 }
 
+// 32 rows of 128 bytes each in shared memory (a row a lane's, swizzled) to `to` + the rows' offsets (in
+// bytes, negative: left out), four whole rows an instruction.  Warp-collective.
+__device__ __forceinline__ void store_rows(char* to, int64_t offset, uint32_t stage, int lane) {
+  __syncwarp();
+#pragma unroll 2
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "r"(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) : "memory");
+    const int64_t at = __shfl_sync(0xffffffffu, offset, r);
+    if (at >= 0) *reinterpret_cast<uint4*>(to + at + (lane & 7) * 16) = x;
+  }
+  __syncwarp();
+}
+
 template <int D>
-__device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, uint32_t tmem, int g, int warp, int lane) {
+__device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* ctl, uint8_t* smem, uint32_t sbase, uint32_t tmem, int g, int warp, int lane) {
   using M = Dims<D>;
   volatile int* abort_flag = &ctl->abort;
+  // Stream 1's m, l and exponent of V of each row, for the join of the streams: in the second tile of Q,
+  // which is idle where both streams have the same rows.
+  float(*ml)[3] = reinterpret_cast<float(*)[3]>(smem + M::OFF_Q + M::TILE);
   const int q = warp & 3, lane_row = 32 * q + lane;
   const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
   const uint32_t s_addr = tmem + lane_base + g * kKeys, o_addr = tmem + lane_base + 2 * kKeys + g * D;
@@ -706,16 +795,26 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
       hi = p.causal ? min(w.len, pos + 1) : w.len;
       lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
     }
+    // Where the row is in q and out, in elements from the first rank's (negative: nowhere).
+    const int rank = w.h / p.n_kv;
+    int64_t token = -1, column = 0;
+    if (row < w.rows) {
+      const int r = w.row0 + row;
+      token = r / p.group;
+      column = (static_cast<int64_t>(w.h - rank * p.n_kv) * p.group + (r - token * p.group)) * D;
+      token += w.a;
+    }
     float back;
     if (!split || g == 0) {
-      back = load_q<D>(p, w, row, hi > lo, sbase + M::OFF_Q + g * M::TILE, lane_row);
-      if (split) ctl->ml[lane_row][0] = back;
+      back = load_q<D>(p, p.q[rank], token < 0 ? -1 : token * p.ld_q + column, sbase + M::OFF_Q + g * M::TILE, q, lane);
+      if (hi <= lo) back = 1.0f;
+      if (split) ml[lane_row][0] = back;
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(ptx::smem_addr(&ctl->q_full[g]));
     }
     if (split) {
       if (!meet()) return;
-      if (g == 1) back = ctl->ml[lane_row][0];
+      if (g == 1) back = ml[lane_row][0];
     }
     RowState st{-INFINITY, 0.0f, -1000};
     bool fresh = true;
@@ -725,9 +824,11 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
       ptx::tc_fence_after();
       const uint32_t t = base + step;
       if (!__all_sync(0xffffffffu, wait(ptx::smem_addr(&ctl->info_full[t % kInfos]), (t / kInfos) & 1, abort_flag, p.b.status))) return;
-      const Info info = ctl->info[t % kInfos];
+      const Info& info = ctl->info[t % kInfos];
       const int key0 = (from + step) * kKeys;
-      softmax_step<D>(st, info, back, lo - key0, hi - key0, s_addr, o_addr, fresh);
+      // edge: some row does not see every key of the step.
+      const bool edge = __any_sync(0xffffffffu, lo > key0 || hi < key0 + kKeys || (info.unseen | info.nan) != 0);
+      softmax_step<D>(st, info, back, lo - key0, hi - key0, edge, s_addr, o_addr, fresh);
       fresh = false;
       ptx::tc_fence_before();
       ptx::mbar_arrive(ptx::smem_addr(&ctl->p_full[g]));
@@ -737,9 +838,9 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
     const bool whole = w.first && w.last;
     const int n_streams = split ? min(turns, 2) : 1;
     if (split && g == 1) {
-      ctl->ml[lane_row][0] = st.m;
-      ctl->ml[lane_row][1] = st.l;
-      ctl->ml[lane_row][2] = __int_as_float(st.e_v);
+      ml[lane_row][0] = st.m;
+      ml[lane_row][1] = st.l;
+      ml[lane_row][2] = __int_as_float(st.e_v);
     }
     bool ok = true;
     for (int i = 0; i < 2; ++i)
@@ -757,8 +858,8 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
       float m = st.m, l = st.l, w0 = 1.0f, w1 = 0.0f, e0, e1 = 0.0f;
       e0 = e8m0_value(static_cast<uint32_t>(max(st.e_v, -127) + 127));
       if (n_streams == 2) {
-        const float m1 = ctl->ml[lane_row][0], l1 = ctl->ml[lane_row][1];
-        e1 = e8m0_value(static_cast<uint32_t>(max(__float_as_int(ctl->ml[lane_row][2]), -127) + 127));
+        const float m1 = ml[lane_row][0], l1 = ml[lane_row][1];
+        e1 = e8m0_value(static_cast<uint32_t>(max(__float_as_int(ml[lane_row][2]), -127) + 127));
         m = fmaxf(st.m, m1);
         const float ref = m == -INFINITY ? 0.0f : m;
         w0 = ex2(st.m - ref), w1 = ex2(m1 - ref);
@@ -766,36 +867,42 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
       }
       const float inv = l == 0.0f ? 0.0f : 0x1p-7f / l;
       w0 *= inv, w1 *= inv;
-      const int r = w.row0 + row, token = r / p.group, hq = r - token * p.group;
-      const int rank = w.h / p.n_kv, head = w.h - rank * p.n_kv;
-      __nv_bfloat16* dst = p.out[rank] + static_cast<int64_t>(w.a + token) * p.ldo + (static_cast<int64_t>(head) * p.group + hq) * D;
       constexpr int PART = kRows * (D + 2);
       float* part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (w.first ? 1 : 0)) * PART;
+      char* to = whole ? reinterpret_cast<char*>(p.out[rank]) : reinterpret_cast<char*>(part);
+      const int64_t offset = token < 0 ? -1 : whole ? (token * p.ldo + column) * 2 : static_cast<int64_t>(row) * D * 4;
+      // (Q's tile is idle: every S of this piece is done.)
+      const uint32_t stage = sbase + M::OFF_Q + g * M::TILE + q * 4096;
+      const float f0 = w0 * e0, f1 = w1 * e1;
+      const int per = whole ? 64 : 32;     // columns of 128 bytes
 #pragma unroll 1
-      for (int col = 0; col < D; col += 32) {
-        uint32_t v[32];
-        ptx::tmem_ld_32x32b_x32(o_addr + col, v);
+      for (int col = 0; col < D; col += 16) {
+        uint32_t v[16];
+        float o[16];
+        ptx::tmem_ld_32x32b_x16(o_addr + col, v);
         ptx::tmem_ld_wait();
-        float o[32];
 #pragma unroll
-        for (int t = 0; t < 32; ++t) o[t] = __uint_as_float(v[t]) * w0 * e0;
+        for (int t = 0; t < 16; ++t) o[t] = __uint_as_float(v[t]) * f0;
         if (n_streams == 2) {
-          ptx::tmem_ld_32x32b_x32(o_addr + D + col, v);
+          ptx::tmem_ld_32x32b_x16(o_addr + D + col, v);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int t = 0; t < 32; ++t) o[t] += __uint_as_float(v[t]) * w1 * e1;
+          for (int t = 0; t < 16; ++t) o[t] += __uint_as_float(v[t]) * f1;
         }
-        if (row < w.rows) {
-          if (whole) {
+        const int at = col & (per - 1);
+        const uint32_t line = stage + lane * 128;
+        if (whole) {
 #pragma unroll
-            for (int t = 0; t < 32; t += 8)
-              *reinterpret_cast<uint4*>(dst + col + t) = make_uint4(pack_bf16(o[t], o[t + 1]), pack_bf16(o[t + 2], o[t + 3]),
-                                                                    pack_bf16(o[t + 4], o[t + 5]), pack_bf16(o[t + 6], o[t + 7]));
-          } else {
+          for (int i = 0; i < 2; ++i)
+            ptx::st_shared_v4(line + ((((at >> 3) + i) ^ (lane & 7)) << 4), pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                              pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+        } else {
 #pragma unroll
-            for (int t = 0; t < 32; t += 4) *reinterpret_cast<float4*>(part + row * D + col + t) = make_float4(o[t], o[t + 1], o[t + 2], o[t + 3]);
-          }
+          for (int i = 0; i < 4; ++i)
+            ptx::st_shared_v4(line + ((((at >> 2) + i) ^ (lane & 7)) << 4), __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                              __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
         }
+        if (at + 16 == per) store_rows(to + (col - at) * (whole ? 2 : 4), offset, stage, lane);
       }
       if (!whole && row < w.rows) *reinterpret_cast<float2*>(part + kRows * D + 2 * row) = make_float2(m, l);
       ptx::tc_fence_before();
@@ -818,9 +925,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(ptx::smem_addr(&ctl->q_full[i]), 128);
-      ptx::mbar_init(ptx::smem_addr(&ctl->k_full[i]), 4);
+      ptx::mbar_init(ptx::smem_addr(&ctl->raw_full[i]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl->raw_empty[i]), 2);
+      ptx::mbar_init(ptx::smem_addr(&ctl->k_full[i]), 2);
       ptx::mbar_init(ptx::smem_addr(&ctl->k_empty[i]), 1);
-      ptx::mbar_init(ptx::smem_addr(&ctl->v_full[i]), 4);
+      ptx::mbar_init(ptx::smem_addr(&ctl->v_full[i]), 2);
       ptx::mbar_init(ptx::smem_addr(&ctl->v_empty[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->s_full[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->p_full[i]), 128);
@@ -849,19 +958,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
   int64_t u0, u1, total, n_cta;
   find_part(p, ctl, u0, u1, total, n_cta);
 
-  // 512 threads of 128 registers: 104 + 176 + 176 + 56 a warpgroup's thread.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    codes_way<D>(p, ctl, sbase, warp, lane);
+    codes_way<D>(p, ctl, sbase, u1 - u0, warp, lane);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-    softmax_rows<D>(p, ctl, sbase, tmem, (warp - 4) >> 2, warp, lane);
+    softmax_rows<D>(p, ctl, base, sbase, tmem, (warp - 4) >> 2, warp, lane);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 12) {
-      if (lane == 0) issue_mmas<D>(p, ctl, sbase, tmem);
+      issue_mmas<D>(p, ctl, sbase, tmem);
     } else if (warp == 13 && lane == 0) {
       hand_out_pieces(p, ctl, u0, u1, total, n_cta);
+    } else if (warp == 14) {
+      pages_way<D>(p, ctl, sbase, lane);
+    } else if (warp == 15) {
+      prefetch_q<D>(p, ctl, lane);
     }
   }
   __syncwarp();
@@ -887,14 +996,9 @@ tp_status launch(int ctas, const AttendParams& p, cudaStream_t stream) {
   if (dev < 0 || dev >= 64) return fail(TP_ERR_UNSUPPORTED, "device index %d", dev);
   Raised& r = raised[dev];
   std::call_once(r.once, [&] {
-    cudaFuncAttributes a{};
-    r.err = cudaFuncGetAttributes(&a, paged_tiles_kernel<D>);
-    // The warpgroups' shares of registers add up to what the block is launched with, 128 a thread.
-    if (r.err == cudaSuccess && a.numRegs != 128) r.err = cudaErrorInvalidKernelImage;
-    if (r.err == cudaSuccess)
-      r.err = cudaFuncSetAttribute(paged_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(M::SMEM));
+    r.err = cudaFuncSetAttribute(paged_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(M::SMEM));
   });
-  if (r.err != cudaSuccess) return cuda_fail(r.err, "paged_tiles_kernel's attributes");
+  if (r.err != cudaSuccess) return cuda_fail(r.err, "cudaFuncSetAttribute(max dynamic shared memory)");
   e = launch_pdl(paged_tiles_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), M::SMEM, stream, p);
   if (e == cudaSuccess)
     e = launch_pdl(paged_join_kernel<D, kRows>, dim3(static_cast<unsigned>(ctas), kRows / kJoinRows), dim3(kJoinThreads), 0, stream, p);
