@@ -12,10 +12,9 @@
 //                 instruction to fp16 (exact), times the page's scale relative to the largest one (a power
 //                 of two), into a ring of two K and two V tiles, 128-byte swizzled.  What no row sees is 0.
 //   warps 4..7    softmax of stream 0, warps 8..11 of stream 1, a row a thread (its TMEM lane).
-//   warp 12       issues the MMAs.
-//   warp 13       one thread finds the pieces, ahead of the others.
-//   warp 14       finds a step's pages and scales, and has its codes loaded by TMA.
-//   warp 15       asks Q's rows of the next piece into L2.
+//   warps 12, 13  issue the MMAs of a stream each.
+//   warp 14       finds the pieces, ahead of the others, and asks their rows of Q into L2.
+//   warp 15       finds a step's pages and scales, and has its codes loaded by TMA.
 // The two streams keep the tensor core busy in turn: while one's softmax runs, the other's products
 // do.  With more than 128 rows each stream has 128 of them, over every step; otherwise both have
 // the same rows, stream 0 the even steps and stream 1 the odd ones, and they are joined at the end.
@@ -28,8 +27,9 @@
 // Numbers: Q enters as fp16, each row times a power of two to below 2^15 (what that loses lies 2^-39
 // below its largest element).  K's codes enter times 2^(e - E + 7), E the largest exponent of the step's pages,
 // V's likewise with E the largest so far: at most 448 * 2^7 < 65504, and what is 2^-40 below the largest is
-// lost.  P = 2^(s - m + 7) with the running maximum m raised only where a row exceeds it by more than 8, so P
-// is at most 2^15; l sums the unrounded P, O stays in units of 2^(E - 7).
+// lost.  P = 2^(s - m + 5) with the running maximum m raised only where a row exceeds it by more than 10, so P
+// is at most 2^15 and what is 2^-30 below the largest is lost; l sums the unrounded P, O stays in units of
+// 2^(E - 7).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -47,7 +47,8 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kKeys = 128;                        // keys of a step
 constexpr int kRows = 256;                        // rows of an item
-constexpr int kInfos = 8;                         // steps whose Info is kept: five are in use (see pages_way)
+constexpr int kInfos = 8;                         // steps whose Info is kept: seven are in use (see pages_way)
+constexpr float kBias = 5.0f, kSlack = 10.0f;     // P = 2^(s - m + kBias), m raised by scores above m + kSlack
 constexpr uint32_t SUB = 16384;                   // 128 rows x 64 fp16, 128-byte swizzled
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -73,17 +74,17 @@ struct PieceInfo {
   __device__ __forceinline__ int turns() const { return split() ? n : 2 * n; }
 };
 constexpr int kPieces = 4;
-constexpr int kPieceReaders = 8 + 1 + 2;   // the warps of the softmax, of the MMAs, of the pages and of the prefetch
+constexpr int kPieceReaders = 8 + 2 + 1;   // the warps of the softmax, of the MMAs and of the pages
 
 struct alignas(16) TilesCtrl {
   uint64_t q_full[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
   uint64_t info_full[kInfos];
   uint64_t raw_full[2], raw_empty[2];   // K's and V's codes of a step
   uint64_t pair;           // both streams' softmax threads
   uint64_t piece_full[kPieces], piece_empty[kPieces];
-  uint64_t drain;
+  uint64_t drain[2];
   PieceInfo piece[kPieces];
   uint32_t tmem_base;
   int abort;
@@ -170,19 +171,20 @@ __device__ __forceinline__ uint32_t f16_pow2(int e) {
   return h * 0x10001u;
 }
 
-// The pieces of a CTA's part, one after the other, handed to the other warps through ctl->piece; and
-// the item that begins in the part and goes beyond it.  One thread.
-__device__ __forceinline__ void hand_out_pieces(const AttendParams& p, TilesCtrl* ctl, int64_t u0, int64_t u1, int64_t total, int64_t n_cta) {
+// The pieces of a CTA's part, one after the other, handed to the other warps through ctl->piece, their
+// rows of Q asked into L2; and the item that begins in the part and goes beyond it.  Warp 14, every lane
+// the same but for the rows.
+template <int D>
+__device__ __forceinline__ void hand_out_pieces(const AttendParams& p, TilesCtrl* ctl, int64_t u0, int64_t u1, int64_t total, int64_t n_cta, int lane) {
   int s = ctl->start.s, h = ctl->start.h, block = ctl->start.block, from = ctl->start.tile;
   int64_t at = u0;
   Join join{};
   SeqView v{0, 0, 0, 0};
   if (u1 > u0) v = seq_view(p.b, s);
   for (uint32_t k = 0;; ++k) {
-    if (!wait(ptx::smem_addr(&ctl->piece_empty[k % kPieces]), ((k / kPieces) & 1) ^ 1u, &ctl->abort, p.b.status)) break;
-    PieceInfo& out = ctl->piece[k % kPieces];
+    if (!__all_sync(0xffffffffu, wait(ptx::smem_addr(&ctl->piece_empty[k % kPieces]), ((k / kPieces) & 1) ^ 1u, &ctl->abort, p.b.status))) break;
     const bool more = at < u1;
-    out.n = 0;
+    PieceInfo out{};
     if (more) {
       const Item it = item_of<kRows, kKeys>(p, v, block);
       const int left = it.tile0 + it.tiles - from, n = static_cast<int>(min(static_cast<int64_t>(left), u1 - at));
@@ -195,8 +197,20 @@ __device__ __forceinline__ void hand_out_pieces(const AttendParams& p, TilesCtrl
         join = Join{static_cast<int>(c_last - blockIdx.x) + 1, v.a, it.row0, it.rows, h, {}};
       }
     }
-    ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_full[k % kPieces]));
+    if (lane == 0) {
+      ctl->piece[k % kPieces] = out;
+      ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_full[k % kPieces]));
+    }
     if (!more) break;
+    const int rank = h / p.n_kv, head = h - rank * p.n_kv;
+#pragma unroll 1
+    for (int row = lane; row < out.rows; row += 32) {
+      const int r = out.row0 + row, token = r / p.group;
+      const __nv_bfloat16* q = p.q[rank] + static_cast<int64_t>(v.a + token) * p.ld_q +
+                               (static_cast<int64_t>(head) * p.group + (r - token * p.group)) * D;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+      if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+    }
     if (at < u1) {
       if (static_cast<int64_t>(++block) * kRows >= static_cast<int64_t>(v.n) * p.group) {
         block = 0;
@@ -210,7 +224,7 @@ __device__ __forceinline__ void hand_out_pieces(const AttendParams& p, TilesCtrl
       from = item_of<kRows, kKeys>(p, v, block).tile0;
     }
   }
-  p.joins[blockIdx.x] = join;
+  if (lane == 0) p.joins[blockIdx.x] = join;
 }
 
 // The k-th piece (its n is 0 behind the last, or where a wait gave up).  Warp-collective for the warps
@@ -355,7 +369,7 @@ __device__ __forceinline__ const PieceInfo* warp_piece(TilesCtrl* ctl, uint32_t 
   return __all_sync(0xffffffffu, w != nullptr) && w->n > 0 ? w : nullptr;
 }
 
-// The pages' way (warp 14): where a step's keys are and what their scales are, for the others; and
+// The pages' way (warp 15): where a step's keys are and what their scales are, for the others; and
 // their codes into shared memory by TMA, a box a page (of 32 keys at most).
 template <int D>
 __device__ __forceinline__ void pages_way(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, int lane) {
@@ -366,6 +380,23 @@ __device__ __forceinline__ void pages_way(const AttendParams& p, TilesCtrl* ctl,
   int s = -1, h = -1;
   uint32_t t = 0;
   bool ok = true;
+  // This lane's box of a step, and the bytes of all.
+  struct Boxes {
+    bool load;
+    int rank, head, page, token;
+    uint32_t bytes;
+  };
+  auto copy = [&](int i, const Boxes& b, uint32_t step) {
+    const uint32_t full = ptx::smem_addr(&ctl->raw_full[i]);
+    if (!__all_sync(0xffffffffu, wait(ptx::smem_addr(&ctl->raw_empty[i]), (step & 1) ^ 1u, abort_flag, p.b.status))) return false;
+    if (lane == 0) ptx::mbar_arrive_expect_tx(full, b.bytes);
+    __syncwarp();
+    if (b.load)
+      tma_load_page(sbase + M::OFF_RAW + i * M::RAW + lane * box_keys * D, i == 0 ? &p.map_k[b.rank] : &p.map_v[b.rank], full, b.token,
+                    b.head, b.page);
+    return true;
+  };
+  Boxes before{};
   for (uint32_t k = 0; ok; ++k) {
     const PieceInfo* piece = warp_piece(ctl, k, p.b.status);
     if (piece == nullptr) break;
@@ -391,7 +422,7 @@ __device__ __forceinline__ void pages_way(const AttendParams& p, TilesCtrl* ctl,
       const int box_page = __shfl_sync(0xffffffffu, pg.page, (key_box >> shift) - pg.page0);
       const bool load = lane < boxes && (box_info & kSeen) != 0 && key_box < w.key_end;
       const int n_boxes = __popc(__ballot_sync(0xffffffffu, load));
-      // (The codes of step t - 2 have been taken, so V of step t - 3 is stored, P.V of step t - 5 done and
+      // (V's codes of step t - 3 have been taken, so V of step t - 4 is stored, P.V of step t - 6 done and
       // with it everything that reads that step's Info.)
       Info& info = ctl->info[t % kInfos];
       if (lane < 8) {
@@ -401,21 +432,15 @@ __device__ __forceinline__ void pages_way(const AttendParams& p, TilesCtrl* ctl,
       if (lane == 0) info.e_k = e_k, info.e_v = e_run, info.unseen = unseen, info.nan = nans, info.keys = w.key_end - key0;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->info_full[t % kInfos]));
-#pragma unroll 1
-      for (int i = 0; i < 2 && ok; ++i) {
-        const uint32_t full = ptx::smem_addr(&ctl->raw_full[i]);
-        ok = __all_sync(0xffffffffu, wait(ptx::smem_addr(&ctl->raw_empty[i]), (t & 1) ^ 1u, abort_flag, p.b.status));
-        if (!ok) break;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(n_boxes) * box_keys * D);
-        __syncwarp();
-        if (load)
-          tma_load_page(sbase + M::OFF_RAW + i * M::RAW + lane * box_keys * D, i == 0 ? &p.map_k[rank] : &p.map_v[rank], full,
-                        key_box & (p.b.page_size - 1), head, box_page);
-      }
+      // K of this step, V of the one before: K is needed first, and V's place is free late.
+      const Boxes now{load, rank, head, box_page, key_box & (p.b.page_size - 1), static_cast<uint32_t>(n_boxes) * box_keys * D};
+      ok = copy(0, now, t) && (t == 0 || copy(1, before, t - 1));
+      before = now;
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_empty[k % kPieces]));
   }
+  if (ok && t > 0) copy(1, before, t - 1);
   // The last copies land before the CTA can exit.
   for (int i = 0; i < 2 && t > 0; ++i) wait(ptx::smem_addr(&ctl->raw_full[i]), (t - 1) & 1, abort_flag, p.b.status, true);
 }
@@ -439,35 +464,34 @@ __device__ __forceinline__ void codes_way(const AttendParams& p, TilesCtrl* ctl,
   const uint32_t dst0 = sbase + (is_v ? M::OFF_V : M::OFF_K) + row0 * 128 + (((2 * (lane & 3)) ^ r8) << 4);
   for (uint32_t t = 0; t < steps; ++t) {
     if (!__all_sync(0xffffffffu, wait(raw_full, t & 1, abort_flag, p.b.status))) return;
-    uint4 raw[8][C];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(raw[i][c].x), "=r"(raw[i][c].y), "=r"(raw[i][c].z), "=r"(raw[i][c].w)
-                     : "r"((src ^ (c * 64)) + i * 8 * D) : "memory");
+    const uint32_t stage = t & 1;
+    if (!__all_sync(0xffffffffu, wait(empty + 8 * stage, ((t >> 1) & 1) ^ 1u, abort_flag, p.b.status))) return;
     const Info& info = ctl->info[t % kInfos];
     const uint4 by4 = *reinterpret_cast<const uint4*>(&info.by[is_v][4 * (warp & 1)]);
     const int keys = info.keys - row0;
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(raw_empty);
-    const uint32_t stage = t & 1;
-    if (!__all_sync(0xffffffffu, wait(empty + 8 * stage, ((t >> 1) & 1) ^ 1u, abort_flag, p.b.status))) return;
-    const uint32_t dst = dst0 + stage * M::TILE, by[4] = {by4.x, by4.y, by4.z, by4.w};
-    if (__any_sync(0xffffffffu, by4.x == kZero || by4.y == kZero || by4.z == kZero || by4.w == kZero || keys <= 56)) {
-      // Codes that are not there, of NaN pages or behind the last key that is seen (any content): 0.
+    const uint32_t by[4] = {by4.x, by4.y, by4.z, by4.w};
+    const bool zeros = __any_sync(0xffffffffu, by4.x == kZero || by4.y == kZero || by4.z == kZero || by4.w == kZero || keys <= 56);
+    const uint32_t dst = dst0 + stage * M::TILE;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      uint4 raw[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(raw[i].x), "=r"(raw[i].y), "=r"(raw[i].z), "=r"(raw[i].w)
+                     : "r"((src ^ (c * 64)) + i * 8 * D) : "memory");
+      if (c == C - 1) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(raw_empty);
+      }
+      if (zeros) {
+        // Codes that are not there, of NaN pages or behind the last key that is seen (any content): 0.
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-          if (by[i >> 1] == kZero || 8 * i >= keys) raw[i][c] = make_uint4(0, 0, 0, 0);
-    }
+        for (int i = 0; i < 8; ++i)
+          if (by[i >> 1] == kZero || 8 * i >= keys) raw[i] = make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t f = by[i >> 1] == kZero ? 0u : by[i >> 1];
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const uint32_t x[4] = {raw[i][c].x, raw[i][c].y, raw[i][c].z, raw[i][c].w};
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w}, f = by[i >> 1] == kZero ? 0u : by[i >> 1];
         uint32_t h[8];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -484,26 +508,7 @@ __device__ __forceinline__ void codes_way(const AttendParams& p, TilesCtrl* ctl,
   }
 }
 
-// Asks the next piece's rows of Q into L2 (warp 15), while this piece is worked on.
-template <int D>
-__device__ __forceinline__ void prefetch_q(const AttendParams& p, TilesCtrl* ctl, int lane) {
-  for (uint32_t k = 0;; ++k) {
-    const PieceInfo* piece = warp_piece(ctl, k, p.b.status);
-    if (piece == nullptr) return;
-    const int rank = piece->h / p.n_kv, head = piece->h - rank * p.n_kv;
-    for (int row = lane; row < piece->rows; row += 32) {
-      const int r = piece->row0 + row, token = r / p.group;
-      const __nv_bfloat16* at = p.q[rank] + static_cast<int64_t>(piece->a + token) * p.ld_q +
-                                (static_cast<int64_t>(head) * p.group + (r - token * p.group)) * D;
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
-      if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 64));
-    }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_empty[k % kPieces]));
-  }
-}
-
-// ---------------------------------------------------------------- the MMAs (warp 12)
+// ---------------------------------------------------------------- the MMAs (warps 12 and 13)
 
 // Column of S_g's region in which P's 16 keys kk are: the first 64 keys in columns 0..31, the last 64 in 96..127.
 __host__ __device__ constexpr uint32_t p_column(int kk) { return kk < 4 ? 8u * kk : 64u + 8u * kk; }
@@ -519,9 +524,11 @@ __device__ __forceinline__ bool elect_one() {
   return is != 0;
 }
 
-// The whole warp runs the loop, so that addresses stay in uniform registers; one lane issues.
+// One stream's MMAs.  A warp for each stream, since an MMA instruction waits for the tensor core: what
+// one warp spends on barriers and commits is then the other's time there (a warp for both left it idle 880 cycles
+// of 1900 a turn).  The whole warp runs the loop, so that addresses stay in uniform registers; one lane issues.
 template <int D>
-__device__ __forceinline__ void issue_mmas(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, uint32_t tmem) {
+__device__ __forceinline__ void issue_mmas(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, uint32_t tmem, uint32_t g) {
   using M = Dims<D>;
   volatile int* abort_flag = &ctl->abort;
   const bool issuer = elect_one();
@@ -533,106 +540,126 @@ __device__ __forceinline__ void issue_mmas(const AttendParams& p, TilesCtrl* ctl
   const uint64_t v0 = ptx::sw128_mnmajor_desc(sbase + M::OFF_V, SUB, 1024);
   const uint32_t k_full = ptx::smem_addr(&ctl->k_full[0]), k_empty = ptx::smem_addr(&ctl->k_empty[0]);
   const uint32_t v_full = ptx::smem_addr(&ctl->v_full[0]), v_empty = ptx::smem_addr(&ctl->v_empty[0]);
-  const uint32_t s_full = ptx::smem_addr(&ctl->s_full[0]), p_full = ptx::smem_addr(&ctl->p_full[0]);
+  const uint32_t s_full = ptx::smem_addr(&ctl->s_full[g]), p_half = ptx::smem_addr(&ctl->p_half[g]), p_full = ptx::smem_addr(&ctl->p_full[g]);
+  const uint32_t s_tmem = tmem + g * kKeys, o_tmem = tmem + 2 * kKeys + g * D;
   uint32_t base = 0;                      // steps before this piece
-  uint32_t q_uses0 = 0, q_uses1 = 0, p_uses0 = 0, p_uses1 = 0;
+  uint32_t q_uses = 0, p_uses = 0;        // pieces that are not split; turns with P.V
   bool ok = true;
   for (uint32_t k = 0; ok; ++k) {
     const PieceInfo* w = warp_piece(ctl, k, p.b.status);
     if (w == nullptr) break;
     const bool split = w->split();
-    const int turns = w->turns(), n = w->n;
+    const int n = w->n, turns = split ? (n + 1 - static_cast<int>(g)) / 2 : n;   // of this stream
     __syncwarp();
     if (issuer) ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_empty[k % kPieces]));
-    ok = wait_all(ptx::smem_addr(&ctl->q_full[0]), q_uses0++ & 1);
-    if (!split) ok = ok && wait_all(ptx::smem_addr(&ctl->q_full[1]), q_uses1++ & 1);
-    // Turn u: P.V of turn u - 2 of the same stream first (none for u < 2), then S of turn u (none behind the last).
-    for (int u = 0; u < turns + 2 && ok; ++u) {
-      const uint32_t g = u & 1;
-      if (u >= 2) {
-        const uint32_t t = base + (split ? u - 2 : (u - 2) >> 1), stage = t & 1;
-        if (split || g == 0) ok = wait_all(v_full + 8 * stage, (t >> 1) & 1);
-        ok = ok && wait_all(p_full + 8 * g, (g != 0 ? p_uses1++ : p_uses0++) & 1);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        if (issuer) {
-          const uint64_t vdesc = v0 + stage * (M::TILE >> 4);
-          const uint32_t o = tmem + 2 * kKeys + g * D, pr = tmem + g * kKeys;
+    // Q's tiles.  Both streams wait for the first one, also where stream 1 has its own: it is loaded once
+    // stream 0 is done with the piece before (and, where that was split, stream 1 with its half), so
+    // that no barrier below can be two phases behind.
+    ok = wait_all(ptx::smem_addr(&ctl->q_full[0]), k & 1);
+    if (!split && g == 1) ok = ok && wait_all(ptx::smem_addr(&ctl->q_full[1]), q_uses & 1);
+    if (!split) ++q_uses;
+    const uint64_t qdesc = q0 + (split ? 0u : g * (M::TILE >> 4));
+    // A stage is handed back by two arrivals, one of each stream or both of the only one that has it.
+    auto hand_back = [&](uint32_t bar) {
+      ptx::umma_commit(bar);
+      if (split) ptx::umma_commit(bar);
+    };
+    // Turn u of the stream: P.V of turn u - 1 first, then S of turn u (none behind the last).
+    for (int u = 0; u <= turns && ok; ++u) {
+      const uint32_t t = base + (split ? 2 * u + g : u), stage = t & 1;          // S's step
+      const uint32_t tv = split ? t - 2 : t - 1, stage_v = tv & 1;               // P.V's
+      if (u > 0) ok = wait_all(v_full + 8 * stage_v, (tv >> 1) & 1);
+      if (u < turns) ok = ok && wait_all(k_full + 8 * stage, (t >> 1) & 1);
+      if (u > 0) {
+        const uint64_t vdesc = v0 + stage_v * (M::TILE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            ptx::umma_bf16_ts(o, pr + p_column(kk), vdesc + kk * (2048u >> 4), idesc_pv, (u >= 4 || kk > 0) ? 1u : 0u);
-          if (split || g == 1) ptx::umma_commit(v_empty + 8 * stage);
-          if (u >= turns) ptx::umma_commit(ptx::smem_addr(&ctl->o_done[0]) + 8 * g);
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && wait_all(half == 0 ? p_half : p_full, p_uses & 1);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (issuer) {
+#pragma unroll
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              ptx::umma_bf16_ts(o_tmem, s_tmem + p_column(kk), vdesc + kk * (2048u >> 4), idesc_pv, (u > 1 || kk > 0) ? 1u : 0u);
+          }
+          __syncwarp();
         }
+        ++p_uses;
       }
-      if (u < turns) {
-        const uint32_t t = base + (split ? u : u >> 1), stage = t & 1;
-        if (split || g == 0) ok = wait_all(k_full + 8 * stage, (t >> 1) & 1);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        if (issuer) {
-          const uint64_t qdesc = q0 + (split ? 0u : g * (M::TILE >> 4)), kdesc = k0 + stage * (M::TILE >> 4);
-          const uint32_t to = tmem + g * kKeys;
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (issuer) {
+        if (u < turns) {
+          const uint64_t kdesc = k0 + stage * (M::TILE >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            ptx::umma_bf16(to, qdesc + (kk >> 2) * (SUB >> 4) + 2 * (kk & 3), kdesc + (kk >> 2) * (SUB >> 4) + 2 * (kk & 3), idesc,
+            ptx::umma_bf16(s_tmem, qdesc + (kk >> 2) * (SUB >> 4) + 2 * (kk & 3), kdesc + (kk >> 2) * (SUB >> 4) + 2 * (kk & 3), idesc,
                            kk > 0 ? 1u : 0u);
-          ptx::umma_commit(s_full + 8 * g);
-          if (split || g == 1) ptx::umma_commit(k_empty + 8 * stage);
+          ptx::umma_commit(s_full);
+          hand_back(k_empty + 8 * stage);
+        } else if (u > 0) {
+          ptx::umma_commit(ptx::smem_addr(&ctl->o_done[g]));
         }
+        if (u > 0) hand_back(v_empty + 8 * stage_v);
       }
       __syncwarp();
     }
     base += n;
   }
-  if (issuer) ptx::umma_commit(ptx::smem_addr(&ctl->drain));
-  wait(ptx::smem_addr(&ctl->drain), 0, abort_flag, p.b.status, true);
+  if (issuer) ptx::umma_commit(ptx::smem_addr(&ctl->drain[g]));
+  wait(ptx::smem_addr(&ctl->drain[g]), 0, abort_flag, p.b.status, true);
 }
 
 // ---------------------------------------------------------------- softmax (a row a thread)
 
-// The warp's 32 rows of Q as fp16 in its tile, each times a power of two.  at: of this lane's row
-// in q, in elements, negative where there is none.  Returns what that row's scores have to be
-// multiplied with (log2 units), NaN where it holds a NaN or an infinity.
+// The warp's 32 rows of Q as fp16 in its tile, each times a power of two: copied there as they are,
+// then converted in place by the row's thread, in small rolled loops (this runs once a piece: what it costs is
+// mostly the fetch of its instructions).  at: of this lane's row in q, in elements, negative where there is
+// none.  Returns what the row's scores have to be multiplied with (log2 units), NaN where it holds a NaN or
+// an infinity.
 template <int D>
 __device__ __forceinline__ float load_q(const AttendParams& p, const __nv_bfloat16* q, int64_t at, uint32_t tile, int q4, int lane) {
-  constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes, kBatch = 8;   // lanes of a row; rows of a load; loads in flight
+  constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;   // lanes of a row; rows of a copy
   const int sub = lane % kLanes;
-  const float sign = p.scale_log2e < 0.0f ? -1.0f : 1.0f;   // (so that the largest score is the largest product)
-  int e_mine = 0;
-#pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += kBatch * kRowsAtOnce) {
-    uint4 raw[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int64_t from = __shfl_sync(0xffffffffu, at, r0 + i * kRowsAtOnce + lane / kLanes);
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (from >= 0) raw[i] = *reinterpret_cast<const uint4*>(q + from + sub * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r1 = r0 + i * kRowsAtOnce, r = 32 * q4 + r1 + lane / kLanes;
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-      top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-      for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-      const int E = static_cast<int>(top >> 7);             // top < 2^(E - 126): times 2^(141 - E) below 2^15
-      const int e_row = __shfl_sync(0xffffffffu, E, ((lane - r1) * kLanes) & 31);
-      if (lane >= r1 && lane < r1 + kRowsAtOnce) e_mine = e_row;
-      const bool zero = E == 255 || p.scale_log2e == 0.0f;
-      const float f0 = zero ? 0.0f : pow2((141 - E) / 2) * sign, f1 = pow2(141 - E - (141 - E) / 2);
-      uint32_t h[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t v = zero ? 0u : w[k];
-        h[k] = f16_pair(__uint_as_float(v << 16) * f0 * f1, __uint_as_float(v & 0xFFFF0000u) * f0 * f1);
-      }
-      ptx::st_shared_v4(tile + (sub >> 3) * SUB + r * 128 + (((sub & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-    }
+#pragma unroll 2
+  for (int r0 = 0; r0 < 32; r0 += kRowsAtOnce) {
+    const int r = r0 + lane / kLanes;
+    const int64_t from = __shfl_sync(0xffffffffu, at, r);
+    const uint32_t dst = tile + (sub >> 3) * SUB + (32 * q4 + r) * 128 + (((sub & 7) ^ (r & 7)) << 4);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(q + max(from, int64_t(0)) + sub * 8), "r"(from >= 0 ? 16 : 0)
+                 : "memory");     // (a row that is not there: zeros, nothing is read)
   }
-  return e_mine == 255 ? __uint_as_float(0x7FFFFFFFu)
-                       : fabsf(p.scale_log2e) * pow2((e_mine - 141) / 2) * pow2(e_mine - 141 - (e_mine - 141) / 2);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  const uint32_t row = tile + (32 * q4 + lane) * 128;
+  auto chunk = [&](int c) { return row + (c >> 3) * SUB + (((c & 7) ^ (lane & 7)) << 4); };
+  auto load = [&](uint32_t from, uint32_t (&w)[4]) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from) : "memory");
+  };
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    uint32_t w[4];
+    load(chunk(c), w);
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu)));
+  }
+  top = max(top & 0xFFFFu, top >> 16);
+  const int E = static_cast<int>(top >> 7);             // top < 2^(E - 126): times 2^(141 - E) below 2^15
+  const bool zero = E == 255 || p.scale_log2e == 0.0f;
+  // (the sign of scale goes into Q, so that the largest score is the largest product)
+  const float f0 = zero ? 0.0f : copysignf(pow2((141 - E) / 2), p.scale_log2e), f1 = pow2(141 - E - (141 - E) / 2);
+#pragma unroll 2
+  for (int c = 0; c < D / 8; ++c) {
+    uint32_t w[4];
+    load(chunk(c), w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t v = zero ? 0u : w[k];
+      w[k] = f16_pair(__uint_as_float(v << 16) * f0 * f1, __uint_as_float(v & 0xFFFF0000u) * f0 * f1);
+    }
+    ptx::st_shared_v4(chunk(c), w[0], w[1], w[2], w[3]);
+  }
+  return E == 255 ? __uint_as_float(0x7FFFFFFFu) : fabsf(p.scale_log2e) * pow2((E - 141) / 2) * pow2(E - 141 - (E - 141) / 2);
 }
 
 struct RowState {
@@ -685,29 +712,29 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&sv)[32], uint64_t c2,
 }
 
 // A step of the row: its scores from tensor memory, P over them, O rescaled where m or V's exponent
-// grew.  64 scores at a time, the first of them read twice (a whole row's 128 registers would spill), in
-// rolled loops: with the code of every chunk laid out, the SM's warps fetched their instructions anew each step.
+// grew.
 template <int D>
-__device__ __forceinline__ void softmax_step(RowState& st, const Info& info, float back, int lo, int hi, bool edge, uint32_t s_addr, uint32_t o_addr, bool fresh) {
-  uint32_t x[32], y[32];
+__device__ __forceinline__ void softmax_step(RowState& st, const Info& info, float back, int lo, int hi, bool edge, uint32_t s_addr, uint32_t o_addr, bool fresh, uint32_t p_half) {
+  uint32_t x[4][32];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ptx::tmem_ld_32x32b_x32(s_addr + 32 * i, x[i]);
   // (c is kept above 0, so that it may multiply the -infinity of a masked key; smaller ones make every score 0.)
   float c = back * pow2(info.e_k - 7);
   if (c < 0x1p-100f) c = 0x1p-100f;
-  float mt = -INFINITY;
-#pragma unroll 1
-  for (int t0 = 0; t0 < kKeys; t0 += 64) {
-    ptx::tmem_ld_32x32b_x32(s_addr + t0, x);
-    ptx::tmem_ld_32x32b_x32(s_addr + t0 + 32, y);
-    ptx::tmem_ld_wait();
-    if (edge) {
-      mask_chunk(x, info, t0, lo, hi);
-      mask_chunk(y, info, t0 + 32, lo, hi);
-    }
-    mt = max_chunk(y, max_chunk(x, mt));
+  ptx::tmem_ld_wait();
+  if (edge) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mask_chunk(x[i], info, 32 * i, lo, hi);
   }
-  mt *= c;
+  float mt = -INFINITY;
+  {
+    float mx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx[i] = max_chunk(x[i], -INFINITY);
+    mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+  }
   float alpha = 1.0f;
-  if (mt > st.m + 8.0f) {      // (m is -infinity at first)
+  if (mt > st.m + kSlack) {      // (m is -infinity at first)
     alpha = ex2(st.m - mt);
     st.m = mt;
     st.l *= alpha;
@@ -717,30 +744,28 @@ __device__ __forceinline__ void softmax_step(RowState& st, const Info& info, flo
     st.e_v = info.e_v;
   }
   const bool rescale = !fresh && __any_sync(0xffffffffu, alpha != 1.0f);
-  const float shift = 7.0f - (st.m == -INFINITY ? 0.0f : st.m);
+  const float shift = kBias - (st.m == -INFINITY ? 0.0f : st.m);
   const uint64_t c2 = f2(c, c), s2 = f2(shift, shift);
   uint64_t ls[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+  if (rescale) {      // (O is complete up to the step before: S follows its P.V in the tensor core)
 #pragma unroll 1
-  for (int t0 = 64;; t0 = 0) {
-    exp_chunk(y, c2, s2, ls, s_addr + (t0 != 0 ? p_column(6) : p_column(2)));
-    exp_chunk(x, c2, s2, ls, s_addr + (t0 != 0 ? p_column(4) : p_column(0)));
-    if (t0 == 0) break;
-    ptx::tmem_ld_32x32b_x32(s_addr, x);
-    ptx::tmem_ld_32x32b_x32(s_addr + 32, y);
-    ptx::tmem_ld_wait();
-    if (edge) {
-      mask_chunk(x, info, 0, lo, hi);
-      mask_chunk(y, info, 32, lo, hi);
-    }
-  }
-  if (rescale) {
-#pragma unroll 1
-    for (int col = 0; col < D; col += 32) {
-      ptx::tmem_ld_32x32b_x32(o_addr + col, x);
+    for (int col = 0; col < D; col += 16) {
+      uint32_t v[16];
+      ptx::tmem_ld_32x32b_x16(o_addr + col, v);
       ptx::tmem_ld_wait();
 #pragma unroll
-      for (int t = 0; t < 32; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * alpha);
-      ptx::tmem_st_32x32b_x32(o_addr + col, x);
+      for (int t = 0; t < 16; ++t) v[t] = __float_as_uint(__uint_as_float(v[t]) * alpha);
+      ptx::tmem_st_32x32b_x16(o_addr + col, v);
+    }
+  }
+  // P of the first 64 keys is multiplied while that of the others is computed.
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    exp_chunk(x[i], c2, s2, ls, s_addr + p_column(2 * i));
+    if (i == 1) {
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(p_half);
     }
   }
   ptx::tmem_st_wait();
@@ -808,11 +833,12 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
     if (!split || g == 0) {
       back = load_q<D>(p, p.q[rank], token < 0 ? -1 : token * p.ld_q + column, sbase + M::OFF_Q + g * M::TILE, q, lane);
       if (hi <= lo) back = 1.0f;
-      if (split) ml[lane_row][0] = back;
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(ptx::smem_addr(&ctl->q_full[g]));
     }
     if (split) {
+      if (!meet()) return;      // (stream 1 is done with the piece before, which may have used the second tile)
+      if (g == 0) ml[lane_row][0] = back;
       if (!meet()) return;
       if (g == 1) back = ml[lane_row][0];
     }
@@ -828,7 +854,7 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
       const int key0 = (from + step) * kKeys;
       // edge: some row does not see every key of the step.
       const bool edge = __any_sync(0xffffffffu, lo > key0 || hi < key0 + kKeys || (info.unseen | info.nan) != 0);
-      softmax_step<D>(st, info, back, lo - key0, hi - key0, edge, s_addr, o_addr, fresh);
+      softmax_step<D>(st, info, back, lo - key0, hi - key0, edge, s_addr, o_addr, fresh, ptx::smem_addr(&ctl->p_half[g]));
       fresh = false;
       ptx::tc_fence_before();
       ptx::mbar_arrive(ptx::smem_addr(&ctl->p_full[g]));
@@ -928,11 +954,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
       ptx::mbar_init(ptx::smem_addr(&ctl->raw_full[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->raw_empty[i]), 2);
       ptx::mbar_init(ptx::smem_addr(&ctl->k_full[i]), 2);
-      ptx::mbar_init(ptx::smem_addr(&ctl->k_empty[i]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl->k_empty[i]), 2);
       ptx::mbar_init(ptx::smem_addr(&ctl->v_full[i]), 2);
-      ptx::mbar_init(ptx::smem_addr(&ctl->v_empty[i]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl->v_empty[i]), 2);
       ptx::mbar_init(ptx::smem_addr(&ctl->s_full[i]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl->p_half[i]), 128);
       ptx::mbar_init(ptx::smem_addr(&ctl->p_full[i]), 128);
+      ptx::mbar_init(ptx::smem_addr(&ctl->drain[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->o_done[i]), 1);
     }
     for (int i = 0; i < kInfos; ++i) ptx::mbar_init(ptx::smem_addr(&ctl->info_full[i]), 1);
@@ -941,7 +969,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
       ptx::mbar_init(ptx::smem_addr(&ctl->piece_full[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->piece_empty[i]), kPieceReaders);
     }
-    ptx::mbar_init(ptx::smem_addr(&ctl->drain), 1);
     ctl->abort = 0;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
@@ -958,19 +985,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
   int64_t u0, u1, total, n_cta;
   find_part(p, ctl, u0, u1, total, n_cta);
 
+  // 512 threads of 128 registers: 80 + 184 + 184 + 64 a warpgroup's thread.
   if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     codes_way<D>(p, ctl, sbase, u1 - u0, warp, lane);
   } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     softmax_rows<D>(p, ctl, base, sbase, tmem, (warp - 4) >> 2, warp, lane);
   } else {
-    if (warp == 12) {
-      issue_mmas<D>(p, ctl, sbase, tmem);
-    } else if (warp == 13 && lane == 0) {
-      hand_out_pieces(p, ctl, u0, u1, total, n_cta);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp < 14) {
+      issue_mmas<D>(p, ctl, sbase, tmem, warp - 12);
     } else if (warp == 14) {
+      hand_out_pieces<D>(p, ctl, u0, u1, total, n_cta, lane);
+    } else {
       pages_way<D>(p, ctl, sbase, lane);
-    } else if (warp == 15) {
-      prefetch_q<D>(p, ctl, lane);
     }
   }
   __syncwarp();
@@ -996,9 +1025,14 @@ tp_status launch(int ctas, const AttendParams& p, cudaStream_t stream) {
   if (dev < 0 || dev >= 64) return fail(TP_ERR_UNSUPPORTED, "device index %d", dev);
   Raised& r = raised[dev];
   std::call_once(r.once, [&] {
-    r.err = cudaFuncSetAttribute(paged_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(M::SMEM));
+    cudaFuncAttributes a{};
+    r.err = cudaFuncGetAttributes(&a, paged_tiles_kernel<D>);
+    // The warpgroups' shares of registers add up to what the block is launched with, 128 a thread.
+    if (r.err == cudaSuccess && a.numRegs != 128) r.err = cudaErrorInvalidKernelImage;
+    if (r.err == cudaSuccess)
+      r.err = cudaFuncSetAttribute(paged_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(M::SMEM));
   });
-  if (r.err != cudaSuccess) return cuda_fail(r.err, "cudaFuncSetAttribute(max dynamic shared memory)");
+  if (r.err != cudaSuccess) return cuda_fail(r.err, "paged_tiles_kernel's attributes");
   e = launch_pdl(paged_tiles_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), M::SMEM, stream, p);
   if (e == cudaSuccess)
     e = launch_pdl(paged_join_kernel<D, kRows>, dim3(static_cast<unsigned>(ctas), kRows / kJoinRows), dim3(kJoinThreads), 0, stream, p);
