@@ -1,12 +1,12 @@
 // Appending keys and values to the paged 8-bit cache, with the position rotation of Q and K.
 //
 // One launch over every rank.  Its first blocks rotate Q (a warp takes one token and up to four
-// times 32 lanes' worth of its heads); the others each quantise, for one KV head, the new tokens
-// of one page, since these share a scale:
+// times 32 lanes' worth of its heads); the others each quantise the new tokens of one page for
+// 128 / P of all ranks' KV heads, since a page's tokens share a head's scale:
 //     e = max(e_old if the page holds older tokens, least e with max|x| <= 448 * 2^e)
-// A warp holds 16 tokens of the page in registers as fp32 (rotated), a page of P tokens is held by
-// P / 16 warps, and the maximum is joined by one warp reduction and, for larger pages, through
-// shared memory: every element is read once and written once.  Only where e grew are the older
+// A warp holds 16 tokens of a page and head in registers, a page of P tokens is held by P / 16 warps, and
+// the maximum is joined by one warp reduction and, for larger pages, through shared memory: every
+// element is read once and written once.  Only where e grew are the older
 // tokens' codes read and written again, scaled by 2^(e_old - e): exact but for codes that fall
 // among the subnormal ones, since scales are powers of two.
 //
@@ -36,9 +36,10 @@ struct AppendParams {
   const int32_t* positions;
   int64_t ld_rope, n_positions;
   int style, rot;              // rot 0: no rotation
-  int n_heads, n_kv;
-  int q_units, q_blocks;       // units of kQRounds rounds of heads a token; blocks of the Q part
-  int64_t kv_units;
+  int n_ranks, n_heads, n_kv;
+  int first_head;              // one token a sequence: 0, or n_heads where Q is left alone
+  int q_units, q_blocks;       // units of kQRounds rounds of heads a token and rank; blocks of the Q part
+  int kv_groups;               // blocks of a page's K (and as many of its V)
   int slot_per, slot_gap;      // numbering of the pages (find_sequence)
 };
 
@@ -56,76 +57,139 @@ __device__ __forceinline__ Chunks chunks_of(int part, int rot) {
   return {c, c + 1, false};
 }
 
-struct Turn {
-  float c[8], s[8];
-};
-__device__ __forceinline__ void load8(float* dst, const float* src) {
-  *reinterpret_cast<float4*>(dst) = *reinterpret_cast<const float4*>(src);
-  *reinterpret_cast<float4*>(dst + 4) = *reinterpret_cast<const float4*>(src + 4);
+// Pairs of fp32 values for the two-wide instructions (half the instructions: this kernel would issue them
+// longer than it moves its bytes).
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
-// The cosines and sines of a token's two chunks; NaN where its row is outside the table.
-__device__ __forceinline__ void load_turn(Turn& t, const AppendParams& p, int64_t at, const Chunks& ch) {
-  if (at < 0 || at >= p.n_positions) {
-    bad_index(p.b);
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+// The larger magnitude of three, NaN if any is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// A thread's elements in fp32: pair i of chunk 0, then of chunk 1.
+struct Values {
+  uint64_t x[8];
+};
+__device__ __forceinline__ void unpack(Values& v, const uint4 (&raw)[2]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t.c[i] = t.s[i] = __uint_as_float(0x7FFFFFFFu);
-    return;
-  }
-  const float* row = p.cos_sin + at * p.ld_rope;
-  if (p.style == TP_ROPE_HALF) {
-    load8(t.c, row + 8 * ch.c0);
-    load8(t.s, row + p.rot / 2 + 8 * ch.c0);
-  } else {
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 4 * (h == 0 ? ch.c0 : ch.c1);
-      *reinterpret_cast<float4*>(t.c + 4 * h) = *reinterpret_cast<const float4*>(row + i);
-      *reinterpret_cast<float4*>(t.s + 4 * h) = *reinterpret_cast<const float4*>(row + p.rot / 2 + i);
-    }
+    for (int i = 0; i < 4; ++i) v.x[4 * c + i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   }
 }
 
-__device__ __forceinline__ void unpack8(float* x, const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// The cosines and sines of a token's two chunks, from its row of the table: for TP_ROPE_HALF those of the
+// elements of either chunk, for TP_ROPE_PAIRS of the first chunk's pairs, then of the second's.
+struct Turn {
+  uint64_t c[4], s[4];
+};
+__device__ __forceinline__ void load4(uint64_t* dst, const float* src) {
+  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(src);
+  dst[0] = v.x, dst[1] = v.y;
+}
+__device__ __forceinline__ void turn_of(Turn& t, const float* row, int style, int rot, const Chunks& ch) {
+  const int i = style == TP_ROPE_HALF ? 8 * ch.c0 : 4 * ch.c0, j = style == TP_ROPE_HALF ? 8 * ch.c0 + 4 : 4 * ch.c1;
+  load4(t.c, row + i);
+  load4(t.c + 2, row + j);
+  load4(t.s, row + rot / 2 + i);
+  load4(t.s + 2, row + rot / 2 + j);
+}
+// NaN where the row is outside the table.
+__device__ __forceinline__ void load_turn(Turn& t, const AppendParams& p, int64_t at, const Chunks& ch) {
+  if (at >= 0 && at < p.n_positions) {
+    turn_of(t, p.cos_sin + at * p.ld_rope, p.style, p.rot, ch);
+    return;
+  }
+  bad_index(p.b);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  for (int i = 0; i < 4; ++i) t.c[i] = t.s[i] = 0x7FFFFFFF7FFFFFFFull;
+}
+// (x1 c - x2 s, x2 c + x1 s) of each pair.
+__device__ __forceinline__ void rotate(Values& v, const Turn& t, int style) {
+  if (style == TP_ROPE_HALF) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t a = v.x[i], b = v.x[4 + i];
+      v.x[i] = fma2(b, t.s[i] ^ 0x8000000080000000ull, mul2(a, t.c[i]));
+      v.x[4 + i] = fma2(a, t.s[i], mul2(b, t.c[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 c = split2(t.c[i]), s = split2(t.s[i]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 x = split2(v.x[2 * i + k]);
+        const float ck = k == 0 ? c.x : c.y, sk = k == 0 ? s.x : s.y;
+        v.x[2 * i + k] = f2(fmaf(-x.y, sk, x.x * ck), fmaf(x.x, sk, x.y * ck));
+      }
+    }
   }
 }
-__device__ __forceinline__ uint4 pack8(const float* x) {
+__device__ __forceinline__ uint4 pack_bf16x8(const uint64_t* x) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    const float2 v = split2(x[i]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-
-__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
-  const float x = a, y = b;
-  a = x * c - y * s;
-  b = y * c + x * s;
+__device__ __forceinline__ uint2 pack_e4m3x8(const uint64_t* x, uint64_t by) {
+  float2 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = split2(mul2(x[i], by));
+  return make_uint2(e4m3x4(v[0].x, v[0].y, v[1].x, v[1].y), e4m3x4(v[2].x, v[2].y, v[3].x, v[3].y));
 }
-// x: chunk c0 in [0, 8), chunk c1 in [8, 16).
-__device__ __forceinline__ void rotate(float (&x)[16], const Turn& t, int style) {
-  if (style == TP_ROPE_HALF) {
+// Bits of the largest magnitude as fp32 (a NaN's are the largest).
+__device__ __forceinline__ uint32_t amax_bits(const Values& v) {
+  float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) turn_pair(x[i], x[8 + i], t.c[i], t.s[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn_pair(x[2 * i], x[2 * i + 1], t.c[i], t.s[i]);
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = split2(v.x[i]);
+    top = max_abs3(top, x.x, x.y);
   }
+  return __float_as_uint(top) & 0x7FFFFFFFu;
+}
+__device__ __forceinline__ uint32_t amax_bits(const uint4 (&raw)[2]) {
+  const uint32_t m = 0x7FFF7FFFu;
+  uint32_t v = 0;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    v = __vmaxu2(v, __vmaxu2(__vmaxu2(raw[c].x & m, raw[c].y & m), __vmaxu2(raw[c].z & m, raw[c].w & m)));
+  return max(v & 0xFFFFu, v >> 16) << 16;
 }
 
 // Q of one token: kQRounds rounds of 32 / kParts heads, a head held by kParts = D / 16 threads.
 template <int D>
-__device__ __forceinline__ void rotate_q(const AppendParams& p, int rank, int64_t unit, int lane) {
+__device__ __forceinline__ void rotate_q(const AppendParams& p, int64_t unit, int lane) {
   constexpr int kParts = D / 16, kHeads = 32 / kParts;
-  if (unit >= static_cast<int64_t>(p.b.T) * p.q_units) return;
-  const int t = static_cast<int>(unit / p.q_units);
-  const int h0 = static_cast<int>(unit - static_cast<int64_t>(t) * p.q_units) * kQRounds * kHeads + lane / kParts;
+  const int per_token = p.q_units * p.n_ranks;
+  if (unit >= static_cast<int64_t>(p.b.T) * per_token) return;
+  const int t = static_cast<int>(unit / per_token), rest = static_cast<int>(unit - static_cast<int64_t>(t) * per_token);
+  const int rank = rest / p.q_units, h0 = (rest - rank * p.q_units) * kQRounds * kHeads + lane / kParts;
   const Chunks ch = chunks_of(lane % kParts, p.rot);
   const __nv_bfloat16* src = p.qkv[rank] + t * p.ld_qkv;
   uint4 raw[kQRounds][2];
@@ -151,12 +215,11 @@ __device__ __forceinline__ void rotate_q(const AppendParams& p, int rank, int64_
     const int h = h0 + i * kHeads;
     if (h < p.n_heads) {
       if (ch.turned) {
-        float x[16];
-        unpack8(x, raw[i][0]);
-        unpack8(x + 8, raw[i][1]);
+        Values x;
+        unpack(x, raw[i]);
         rotate(x, turn, p.style);
-        raw[i][0] = pack8(x);
-        raw[i][1] = pack8(x + 8);
+        raw[i][0] = pack_bf16x8(x.x);
+        raw[i][1] = pack_bf16x8(x.x + 4);
       }
       *reinterpret_cast<uint4*>(dst + h * D + 8 * ch.c0) = raw[i][0];
       *reinterpret_cast<uint4*>(dst + h * D + 8 * ch.c1) = raw[i][1];
@@ -178,21 +241,29 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
   return e4m3x4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
 }
 
+// The rotation's rows for a page's tokens, where several heads use them.
+constexpr int kTablePages = 32;                  // tokens of the largest page that has them in shared memory
+struct alignas(16) Shared {
+  float cs[kTablePages][128];
+  uint32_t warp_top[kWarps];
+};
+
 template <int D>
-__device__ __forceinline__ void append_page(const AppendParams& p, int rank, int64_t block, uint32_t* warp_top) {
+__device__ __forceinline__ void append_page(const AppendParams& p, int64_t block, Shared& sh) {
   constexpr int kParts = D / 16, kTokens = 32 / kParts, kRounds = 16 / kTokens;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int P = p.b.page_size, warps = P / 16;     // warps of a page
-  const int64_t unit = block * (kWarps / warps) + warp / warps;
-  const int64_t slot = unit / (2 * p.n_kv);
-  const int rest = static_cast<int>(unit - slot * (2 * p.n_kv));
-  const bool is_v = rest >= p.n_kv;
-  const int head = is_v ? rest - p.n_kv : rest;
+  const int P = p.b.page_size, warps = P / 16, heads = kWarps / warps;     // warps of a page and head, heads of a block
+  const int64_t slot = block / (2 * p.kv_groups);
+  const int rest = static_cast<int>(block - slot * (2 * p.kv_groups));
+  const bool is_v = rest >= p.kv_groups;
+  const int h = (is_v ? rest - p.kv_groups : rest) * heads + warp / warps;  // of all ranks'
+  const bool mine = h < p.n_ranks * p.n_kv;
+  const int rank = mine ? h / p.n_kv : 0, head = mine ? h - rank * p.n_kv : 0;
 
-  // Which tokens [j0, j1) of which sequence, in which page.
+  // Which tokens [j0, j1) of which sequence, in which page (the same for the whole block).
   int j0 = 0, j1 = 0, row0 = 0;                    // the row of position j is row0 + j
   int64_t page = -1;
-  const int s = unit < p.kv_units ? find_sequence(p.b, slot, p.slot_per, 1, p.slot_gap, lane) : -1;
+  const int s = find_sequence(p.b, slot, p.slot_per, 1, p.slot_gap, lane);
   if (s >= 0) {
     const SeqView v = seq_view(p.b, s);
     const int64_t local = slot - (v.a / p.slot_per + static_cast<int64_t>(p.slot_gap) * s);
@@ -208,44 +279,79 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int rank, int
         bad_index(p.b);
         page = -1;
       }
-      if (page < 0) j1 = j0;
     }
   }
+  if (page < 0) return;
 
-  // This warp's 16 slots: the new values in fp32, and their largest magnitude.
+  // This warp's 16 slots: the new values as they are.
   const int base = (j0 & ~(P - 1)) + 16 * (warp % warps);
   const int rot = is_v ? 0 : p.rot;
   const Chunks ch = chunks_of(lane % kParts, rot);
   const __nv_bfloat16* src = p.qkv[rank] + (p.n_heads + (is_v ? p.n_kv : 0) + head) * static_cast<int64_t>(D);
-  float x[kRounds][16];
-  uint32_t top = 0;
+  uint4 raw[kRounds][2];
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
     const int j = base + i * kTokens + lane / kParts;
+    raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
+    if (mine && j >= j0 && j < j1) {
+      const uint4* at = reinterpret_cast<const uint4*>(src + (static_cast<int64_t>(row0) + j) * p.ld_qkv);
+      raw[i][0] = at[ch.c0];
+      raw[i][1] = at[ch.c1];
+    }
+  }
+  uint8_t* scale = (is_v ? p.vs : p.ks)[rank] + page * p.ld_scales + head;
+  const bool older = mine && (j0 & (P - 1)) != 0;
+  const uint32_t old_byte = older ? *scale : 0u;
+  const bool shared_table = rot > 0 && P <= kTablePages;
+  if (shared_table) {
+    const int first = j0 & ~(P - 1), quads = rot / 4;
+    for (int i = threadIdx.x; i < (j1 - j0) * quads; i += kThreads) {
+      const int j = j0 + i / quads, c = i % quads;
+      const int64_t at = p.positions != nullptr ? p.positions[row0 + j] : j;
+      float4 v = make_float4(NAN, NAN, NAN, NAN);
+      if (at >= 0 && at < p.n_positions) v = *reinterpret_cast<const float4*>(p.cos_sin + at * p.ld_rope + 4 * c);
+      else bad_index(p.b);
+      *reinterpret_cast<float4*>(&sh.cs[j - first][4 * c]) = v;
+    }
+    __syncthreads();
+  }
+  // Round i's values, rotated.  (Computed twice, for the maximum and for the codes: kept, they would take
+  // half the warps' registers.)
+  auto turned = [&](int i, Values& x) {
+    const int j = base + i * kTokens + lane / kParts;
+    unpack(x, raw[i]);
     if (j >= j0 && j < j1) {
-      const int64_t row = row0 + j;
-      const uint4* at = reinterpret_cast<const uint4*>(src + row * p.ld_qkv);
-      unpack8(x[i], at[ch.c0]);
-      unpack8(x[i] + 8, at[ch.c1]);
-      if (ch.turned) {
-        Turn t;
+      Turn t;
+      if (shared_table) {
+        turn_of(t, sh.cs[j & (P - 1)], p.style, p.rot, ch);
+      } else {
+        const int64_t row = static_cast<int64_t>(row0) + j;
         load_turn(t, p, p.positions != nullptr ? p.positions[row] : j, ch);
-        rotate(x[i], t, p.style);
       }
+      rotate(x, t, p.style);
+    }
+  };
+  uint32_t top = 0;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) top = max(top, abs_bits(x[i][k]));
+  for (int i = 0; i < kRounds; ++i) {
+    if (ch.turned) {
+      Values x;
+      turned(i, x);
+      top = max(top, amax_bits(x));
+    } else {
+      top = max(top, amax_bits(raw[i]));
     }
   }
   top = __reduce_max_sync(0xffffffffu, top);
-  uint8_t* scale = (is_v ? p.vs : p.ks)[rank] + page * p.ld_scales + head;
-  const bool older = page >= 0 && (j0 & (P - 1)) != 0;
-  const uint32_t old_byte = older ? *scale : 0u;
-  if (lane == 0) warp_top[warp] = top;
-  __syncthreads();   // (every warp has read the old scale as well)
-  for (int w = warp / warps * warps, i = 0; i < warps; ++i) top = max(top, warp_top[w + i]);
-  if (page < 0) return;
+  if (warps > 1) {
+    if (lane == 0) sh.warp_top[warp] = top;
+    __syncthreads();
+    for (int w = warp / warps * warps, i = 0; i < warps; ++i) top = max(top, sh.warp_top[w + i]);
+  }
+  if (!mine) return;
   const uint32_t byte = max(old_byte, top == 0u ? 0u : e8m0_of_amax(top));
   uint8_t* codes = (is_v ? p.v : p.k)[rank] + page * p.ld_page + static_cast<int64_t>(head) * P * D;
+  __syncwarp();      // (every lane has the old scale)
   if (warp % warps == 0 && lane == 0) *scale = static_cast<uint8_t>(byte);
   if (byte > old_byte && older) {   // the older tokens' codes at the new scale
     const float f = byte == 255u ? __uint_as_float(0x7FFFFFFFu)
@@ -260,28 +366,126 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int rank, int
   const float inv = e8m0_inverse(byte);
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)      // (so that the compiler computes them again)
+      asm volatile("" : "+r"(raw[i][c].x), "+r"(raw[i][c].y), "+r"(raw[i][c].z), "+r"(raw[i][c].w) : : "memory");
     const int j = base + i * kTokens + lane / kParts;
     if (j >= j0 && j < j1) {
       uint2* to = reinterpret_cast<uint2*>(codes + (j & (P - 1)) * D);
-      float* y = x[i];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) y[k] *= inv;
-      to[ch.c0] = make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
-      to[ch.c1] = make_uint2(e4m3x4(y[8], y[9], y[10], y[11]), e4m3x4(y[12], y[13], y[14], y[15]));
+      Values x;
+      if (ch.turned) turned(i, x);
+      else unpack(x, raw[i]);
+      to[ch.c0] = pack_e4m3x8(x.x, f2(inv, inv));
+      to[ch.c1] = pack_e4m3x8(x.x + 4, f2(inv, inv));
     }
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
-  __shared__ uint32_t warp_top[kWarps];
+__global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_constant__ AppendParams p) {
+  __shared__ Shared sh;
   pdl_launch_dependents();
   pdl_wait();
-  const int rank = blockIdx.y;
   if (static_cast<int>(blockIdx.x) < p.q_blocks)
-    rotate_q<D>(p, rank, static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), threadIdx.x & 31);
+    rotate_q<D>(p, static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), threadIdx.x & 31);
   else
-    append_page<D>(p, rank, static_cast<int64_t>(blockIdx.x) - p.q_blocks, warp_top);
+    append_page<D>(p, static_cast<int64_t>(blockIdx.x) - p.q_blocks, sh);
+}
+
+// One new token a sequence at most (decoding): a warp takes kTokenRounds rounds of a token's heads, Q's,
+// K's and V's alike, a head held by kParts threads.  No page is shared by two tokens here, so no block has
+// to meet.
+constexpr int kTokenWarps = 2, kTokenRounds = 2;
+template <int D>
+__global__ void __launch_bounds__(kTokenWarps * 32) kv_append_token_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kParts = D / 16, kHeads = 32 / kParts;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kTokenWarps + (threadIdx.x >> 5);
+  const int per_token = p.q_units * p.n_ranks;
+  if (unit >= static_cast<int64_t>(p.b.T) * per_token) return;
+  const int t = static_cast<int>(unit / per_token), rest = static_cast<int>(unit - static_cast<int64_t>(t) * per_token);
+  const int rank = rest / p.q_units, h0 = p.first_head + (rest - rank * p.q_units) * kTokenRounds * kHeads + lane / kParts;
+  const Chunks ch = chunks_of(lane % kParts, p.rot);
+  const __nv_bfloat16* src = p.qkv[rank] + t * p.ld_qkv;
+  const int n_all = p.n_heads + 2 * p.n_kv;
+  uint4 raw[kTokenRounds][2];
+#pragma unroll
+  for (int i = 0; i < kTokenRounds; ++i) {
+    const int h = h0 + i * kHeads;
+    raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
+    if (h < n_all) {
+      raw[i][0] = *reinterpret_cast<const uint4*>(src + h * D + 8 * ch.c0);
+      raw[i][1] = *reinterpret_cast<const uint4*>(src + h * D + 8 * ch.c1);
+    }
+  }
+  const int s = find_sequence(p.b, t, 1, 1, 0, lane);
+  if (s < 0) return;
+  const SeqView v = seq_view(p.b, s);
+  if (t - v.a >= v.n) return;            // rows of no sequence are left alone
+  const int pos = v.pos0;
+  Turn turn;
+  if (ch.turned) load_turn(turn, p, p.positions != nullptr ? p.positions[t] : pos, ch);
+  int64_t page = -1;
+  if (pos >= 0 && pos < p.b.max_keys) page = p.b.page_table[s * p.b.ld_table + (pos >> p.b.page_shift)];
+  if (page < 0 || page >= p.b.n_pages) {
+    if (lane == 0) bad_index(p.b);
+    page = -1;
+  }
+  const int slot = pos & (p.b.page_size - 1);
+  uint8_t* scale[kTokenRounds];
+  uint32_t old_byte[kTokenRounds];
+#pragma unroll
+  for (int i = 0; i < kTokenRounds; ++i) {
+    const int g = h0 + i * kHeads - p.n_heads;          // K's heads, then V's
+    scale[i] = nullptr;
+    old_byte[i] = 0;
+    if (g >= 0 && g < 2 * p.n_kv && page >= 0) {
+      scale[i] = g < p.n_kv ? p.ks[rank] + page * p.ld_scales + g : p.vs[rank] + page * p.ld_scales + (g - p.n_kv);
+      if (slot > 0) old_byte[i] = *scale[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kTokenRounds; ++i) {
+    const int h = h0 + i * kHeads, g = h - p.n_heads;
+    Values x;
+    unpack(x, raw[i]);
+    if (ch.turned && g < p.n_kv) rotate(x, turn, p.style);
+    // (V is not rotated, but its threads hold the chunks of a rotated head: any will do)
+    uint32_t top = amax_bits(x);
+#pragma unroll
+    for (int d = 1; d < kParts; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const uint32_t byte = max(old_byte[i], top == 0u ? 0u : e8m0_of_amax(top));
+    uint8_t* codes = nullptr;
+    if (scale[i] != nullptr)
+      codes = g < p.n_kv ? p.k[rank] + page * p.ld_page + static_cast<int64_t>(g) * p.b.page_size * D
+                         : p.v[rank] + page * p.ld_page + static_cast<int64_t>(g - p.n_kv) * p.b.page_size * D;
+    // Older tokens' codes at a larger scale, by the whole warp, one head after the other.
+    const bool grew = codes != nullptr && slot > 0 && byte > old_byte[i];
+    for (uint32_t m = __ballot_sync(0xffffffffu, grew && lane % kParts == 0); m != 0; m &= m - 1) {
+      const int from = __ffs(m) - 1;
+      const uint32_t nb = __shfl_sync(0xffffffffu, byte, from), ob = __shfl_sync(0xffffffffu, old_byte[i], from);
+      uint4* at = reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(codes), from));
+      const float f = nb == 255u ? __uint_as_float(0x7FFFFFFFu) : nb - ob > 126u ? 0.0f : __uint_as_float((127u - (nb - ob)) << 23);
+#pragma unroll 4
+      for (int j = lane; j < slot * (D / 16); j += 32) {
+        const uint4 w = at[j];
+        at[j] = make_uint4(rescale4(w.x, f), rescale4(w.y, f), rescale4(w.z, f), rescale4(w.w, f));
+      }
+    }
+    if (codes != nullptr) {
+      const float inv = e8m0_inverse(byte);
+      uint2* to = reinterpret_cast<uint2*>(codes + slot * D);
+      to[ch.c0] = pack_e4m3x8(x.x, f2(inv, inv));
+      to[ch.c1] = pack_e4m3x8(x.x + 4, f2(inv, inv));
+      if (lane % kParts == 0) *scale[i] = static_cast<uint8_t>(byte);
+    } else if (g < 0) {
+      __nv_bfloat16* dst = p.q_out[rank] + t * p.ld_q + h * D;
+      *reinterpret_cast<uint4*>(dst + 8 * ch.c0) = ch.turned ? pack_bf16x8(x.x) : raw[i][0];
+      *reinterpret_cast<uint4*>(dst + 8 * ch.c1) = ch.turned ? pack_bf16x8(x.x + 4) : raw[i][1];
+    }
+  }
 }
 
 }  // namespace
@@ -411,26 +615,35 @@ tp_status tp_kv_append_fp8(const tp_paged_cache* cache, const tp_paged_batch* ba
       p.style = rope->style;
       p.rot = rope->rot_dim;
     }
+    p.n_ranks = c.n_ranks;
     p.n_heads = n_heads;
     p.n_kv = c.n_kv_heads;
-    const int per_unit = kQRounds * 32 / (c.head_dim / 16);   // heads of one warp
-    p.q_units = (n_heads + per_unit - 1) / per_unit;
-    const int64_t q_blocks = q_out != nullptr ? (T * p.q_units + kWarps - 1) / kWarps : 0;
-    // Pages of sequence s get the slots from seq_start[s] / page_size + 2 s on: n new tokens from any
-    // position touch at most (n - 1) / page_size + 2 pages.  One new token touches one.
-    const bool single = batch->max_new == 1;
-    p.slot_per = single ? 0x7FFFFFFF : c.page_size;
-    p.slot_gap = single ? 1 : 2;
-    const int64_t slots = T / p.slot_per + static_cast<int64_t>(p.slot_gap) * batch->n_seqs;
-    p.kv_units = slots * 2 * c.n_kv_heads;
-    const int units_per_block = kWarps / (c.page_size / 16);
-    const int64_t kv_blocks = (p.kv_units + units_per_block - 1) / units_per_block;
-    if (q_blocks + kv_blocks > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many tokens and heads for one launch");
-    p.q_blocks = static_cast<int>(q_blocks);
-    const cudaError_t e =
-        launch_pdl(c.head_dim == 128 ? kv_append_kernel<128> : kv_append_kernel<64>,
-                   dim3(static_cast<unsigned>(q_blocks + kv_blocks), static_cast<unsigned>(c.n_ranks)), dim3(kThreads), 0,
-                   reinterpret_cast<cudaStream_t>(stream), p);
+    cudaError_t e;
+    if (batch->max_new == 1) {
+      p.first_head = q_out != nullptr ? 0 : n_heads;
+      const int heads = n_heads + 2 * c.n_kv_heads - p.first_head, per_warp = kTokenRounds * 32 / (c.head_dim / 16);
+      p.q_units = (heads + per_warp - 1) / per_warp;
+      const int64_t blocks = (T * p.q_units * c.n_ranks + kTokenWarps - 1) / kTokenWarps;
+      if (blocks > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many tokens and heads for one launch");
+      e = launch_pdl(c.head_dim == 128 ? kv_append_token_kernel<128> : kv_append_token_kernel<64>, dim3(static_cast<unsigned>(blocks)),
+                     dim3(kTokenWarps * 32), 0, reinterpret_cast<cudaStream_t>(stream), p);
+    } else {
+      const int per_unit = kQRounds * 32 / (c.head_dim / 16);   // heads of one warp
+      p.q_units = (n_heads + per_unit - 1) / per_unit;
+      const int64_t q_blocks = q_out != nullptr ? (T * p.q_units * c.n_ranks + kWarps - 1) / kWarps : 0;
+      // Pages of sequence s get the slots from seq_start[s] / page_size + 2 s on: n new tokens from any
+      // position touch at most (n - 1) / page_size + 2 pages.
+      p.slot_per = c.page_size;
+      p.slot_gap = 2;
+      const int64_t slots = T / p.slot_per + static_cast<int64_t>(p.slot_gap) * batch->n_seqs;
+      const int heads = kWarps / (c.page_size / 16);            // of a block
+      p.kv_groups = (c.n_ranks * c.n_kv_heads + heads - 1) / heads;
+      const int64_t kv_blocks = slots * 2 * p.kv_groups;
+      if (q_blocks + kv_blocks > 0x7FFFFFFF) return fail(TP_ERR_UNSUPPORTED, "too many tokens and heads for one launch");
+      p.q_blocks = static_cast<int>(q_blocks);
+      e = launch_pdl(c.head_dim == 128 ? kv_append_kernel<128> : kv_append_kernel<64>,
+                     dim3(static_cast<unsigned>(q_blocks + kv_blocks)), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), p);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
     return TP_OK;
   });

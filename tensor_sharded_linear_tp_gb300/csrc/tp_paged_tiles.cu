@@ -12,9 +12,9 @@
 //                 instruction to fp16 (exact), times the page's scale relative to the largest one (a power
 //                 of two), into a ring of two K and two V tiles, 128-byte swizzled.  What no row sees is 0.
 //   warps 4..7    softmax of stream 0, warps 8..11 of stream 1, a row a thread (its TMEM lane).
-//   warps 12, 13  issue the MMAs of a stream each.
-//   warp 14       finds the pieces, ahead of the others, and asks their rows of Q into L2.
-//   warp 15       finds a step's pages and scales, and has its codes loaded by TMA.
+//   warp 12       issues the MMAs.
+//   warp 13       finds the pieces, ahead of the others, and asks their rows of Q into L2.
+//   warp 14       finds a step's pages and scales, and has its codes loaded by TMA.
 // The two streams keep the tensor core busy in turn: while one's softmax runs, the other's products
 // do.  With more than 128 rows each stream has 128 of them, over every step; otherwise both have
 // the same rows, stream 0 the even steps and stream 1 the odd ones, and they are joined at the end.
@@ -74,7 +74,7 @@ struct PieceInfo {
   __device__ __forceinline__ int turns() const { return split() ? n : 2 * n; }
 };
 constexpr int kPieces = 4;
-constexpr int kPieceReaders = 8 + 2 + 1;   // the warps of the softmax, of the MMAs and of the pages
+constexpr int kPieceReaders = 8 + 1 + 1;   // the warps of the softmax, of the MMAs and of the pages
 
 struct alignas(16) TilesCtrl {
   uint64_t q_full[2];
@@ -84,7 +84,7 @@ struct alignas(16) TilesCtrl {
   uint64_t raw_full[2], raw_empty[2];   // K's and V's codes of a step
   uint64_t pair;           // both streams' softmax threads
   uint64_t piece_full[kPieces], piece_empty[kPieces];
-  uint64_t drain[2];
+  uint64_t drain;
   PieceInfo piece[kPieces];
   uint32_t tmem_base;
   int abort;
@@ -172,7 +172,7 @@ __device__ __forceinline__ uint32_t f16_pow2(int e) {
 }
 
 // The pieces of a CTA's part, one after the other, handed to the other warps through ctl->piece, their
-// rows of Q asked into L2; and the item that begins in the part and goes beyond it.  Warp 14, every lane
+// rows of Q asked into L2; and the item that begins in the part and goes beyond it.  Warp 13, every lane
 // the same but for the rows.
 template <int D>
 __device__ __forceinline__ void hand_out_pieces(const AttendParams& p, TilesCtrl* ctl, int64_t u0, int64_t u1, int64_t total, int64_t n_cta, int lane) {
@@ -369,7 +369,7 @@ __device__ __forceinline__ const PieceInfo* warp_piece(TilesCtrl* ctl, uint32_t 
   return __all_sync(0xffffffffu, w != nullptr) && w->n > 0 ? w : nullptr;
 }
 
-// The pages' way (warp 15): where a step's keys are and what their scales are, for the others; and
+// The pages' way (warp 14): where a step's keys are and what their scales are, for the others; and
 // their codes into shared memory by TMA, a box a page (of 32 keys at most).
 template <int D>
 __device__ __forceinline__ void pages_way(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, int lane) {
@@ -508,7 +508,7 @@ __device__ __forceinline__ void codes_way(const AttendParams& p, TilesCtrl* ctl,
   }
 }
 
-// ---------------------------------------------------------------- the MMAs (warps 12 and 13)
+// ---------------------------------------------------------------- the MMAs (warp 12)
 
 // Column of S_g's region in which P's 16 keys kk are: the first 64 keys in columns 0..31, the last 64 in 96..127.
 __host__ __device__ constexpr uint32_t p_column(int kk) { return kk < 4 ? 8u * kk : 64u + 8u * kk; }
@@ -524,11 +524,11 @@ __device__ __forceinline__ bool elect_one() {
   return is != 0;
 }
 
-// One stream's MMAs.  A warp for each stream, since an MMA instruction waits for the tensor core: what
-// one warp spends on barriers and commits is then the other's time there (a warp for both left it idle 880 cycles
-// of 1900 a turn).  The whole warp runs the loop, so that addresses stay in uniform registers; one lane issues.
+// The two streams' turns alternate, so that one's softmax runs while the other's products do (with a warp for
+// each stream they fell into step, both in the softmax and then both waiting for the tensor core: a step of
+// 5000 cycles, not 4300).  The whole warp runs the loop, so that addresses stay in uniform registers; one lane issues.
 template <int D>
-__device__ __forceinline__ void issue_mmas(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, uint32_t tmem, uint32_t g) {
+__device__ __forceinline__ void issue_mmas(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, uint32_t tmem) {
   using M = Dims<D>;
   volatile int* abort_flag = &ctl->abort;
   const bool issuer = elect_one();
@@ -540,74 +540,68 @@ __device__ __forceinline__ void issue_mmas(const AttendParams& p, TilesCtrl* ctl
   const uint64_t v0 = ptx::sw128_mnmajor_desc(sbase + M::OFF_V, SUB, 1024);
   const uint32_t k_full = ptx::smem_addr(&ctl->k_full[0]), k_empty = ptx::smem_addr(&ctl->k_empty[0]);
   const uint32_t v_full = ptx::smem_addr(&ctl->v_full[0]), v_empty = ptx::smem_addr(&ctl->v_empty[0]);
-  const uint32_t s_full = ptx::smem_addr(&ctl->s_full[g]), p_half = ptx::smem_addr(&ctl->p_half[g]), p_full = ptx::smem_addr(&ctl->p_full[g]);
-  const uint32_t s_tmem = tmem + g * kKeys, o_tmem = tmem + 2 * kKeys + g * D;
+  const uint32_t s_full = ptx::smem_addr(&ctl->s_full[0]), p_half = ptx::smem_addr(&ctl->p_half[0]), p_full = ptx::smem_addr(&ctl->p_full[0]);
   uint32_t base = 0;                      // steps before this piece
-  uint32_t q_uses = 0, p_uses = 0;        // pieces that are not split; turns with P.V
+  uint32_t q_uses1 = 0, p_uses0 = 0, p_uses1 = 0;
   bool ok = true;
   for (uint32_t k = 0; ok; ++k) {
     const PieceInfo* w = warp_piece(ctl, k, p.b.status);
     if (w == nullptr) break;
     const bool split = w->split();
-    const int n = w->n, turns = split ? (n + 1 - static_cast<int>(g)) / 2 : n;   // of this stream
+    const int turns = w->turns(), n = w->n;
     __syncwarp();
     if (issuer) ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_empty[k % kPieces]));
-    // Q's tiles.  Both streams wait for the first one, also where stream 1 has its own: it is loaded once
-    // stream 0 is done with the piece before (and, where that was split, stream 1 with its half), so
-    // that no barrier below can be two phases behind.
-    ok = wait_all(ptx::smem_addr(&ctl->q_full[0]), k & 1);
-    if (!split && g == 1) ok = ok && wait_all(ptx::smem_addr(&ctl->q_full[1]), q_uses & 1);
-    if (!split) ++q_uses;
-    const uint64_t qdesc = q0 + (split ? 0u : g * (M::TILE >> 4));
-    // A stage is handed back by two arrivals, one of each stream or both of the only one that has it.
-    auto hand_back = [&](uint32_t bar) {
-      ptx::umma_commit(bar);
-      if (split) ptx::umma_commit(bar);
-    };
-    // Turn u of the stream: P.V of turn u - 1 first, then S of turn u (none behind the last).
-    for (int u = 0; u <= turns && ok; ++u) {
-      const uint32_t t = base + (split ? 2 * u + g : u), stage = t & 1;          // S's step
-      const uint32_t tv = split ? t - 2 : t - 1, stage_v = tv & 1;               // P.V's
-      if (u > 0) ok = wait_all(v_full + 8 * stage_v, (tv >> 1) & 1);
-      if (u < turns) ok = ok && wait_all(k_full + 8 * stage, (t >> 1) & 1);
-      if (u > 0) {
+    // Turn u: P.V of turn u - 2 of the same stream first (none for u < 2), then S of turn u (none behind the last).
+    for (int u = 0; u < turns + 2 && ok; ++u) {
+      const uint32_t g = u & 1;
+      const uint32_t t = base + (split ? u : u >> 1), stage = t & 1;                       // S's step
+      const uint32_t tv = t - (split ? 2 : 1), stage_v = tv & 1;                           // P.V's
+      if (u < 2) {
+        if (g == 0) ok = wait_all(ptx::smem_addr(&ctl->q_full[0]), k & 1);
+        if (g == 1 && !split) ok = wait_all(ptx::smem_addr(&ctl->q_full[1]), q_uses1++ & 1);
+      }
+      // What is there by now is waited for before P, which is not.
+      if (u >= 2 && (split || g == 0)) ok = ok && wait_all(v_full + 8 * stage_v, (tv >> 1) & 1);
+      if (u < turns && (split || g == 0)) ok = ok && wait_all(k_full + 8 * stage, (t >> 1) & 1);
+      if (u >= 2) {
         const uint64_t vdesc = v0 + stage_v * (M::TILE >> 4);
+        const uint32_t parity = (g != 0 ? p_uses1++ : p_uses0++) & 1, o = tmem + 2 * kKeys + g * D, pr = tmem + g * kKeys;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          ok = ok && wait_all(half == 0 ? p_half : p_full, p_uses & 1);
+          ok = ok && wait_all((half == 0 ? p_half : p_full) + 8 * g, parity);
           if (!ok) break;
           ptx::tc_fence_after();
           if (issuer) {
 #pragma unroll
             for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-              ptx::umma_bf16_ts(o_tmem, s_tmem + p_column(kk), vdesc + kk * (2048u >> 4), idesc_pv, (u > 1 || kk > 0) ? 1u : 0u);
+              ptx::umma_bf16_ts(o, pr + p_column(kk), vdesc + kk * (2048u >> 4), idesc_pv, (u >= 4 || kk > 0) ? 1u : 0u);
           }
           __syncwarp();
         }
-        ++p_uses;
       }
       if (!ok) break;
       ptx::tc_fence_after();
       if (issuer) {
         if (u < turns) {
-          const uint64_t kdesc = k0 + stage * (M::TILE >> 4);
+          const uint64_t qdesc = q0 + (split ? 0u : g * (M::TILE >> 4)), kdesc = k0 + stage * (M::TILE >> 4);
+          const uint32_t to = tmem + g * kKeys;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            ptx::umma_bf16(s_tmem, qdesc + (kk >> 2) * (SUB >> 4) + 2 * (kk & 3), kdesc + (kk >> 2) * (SUB >> 4) + 2 * (kk & 3), idesc,
+            ptx::umma_bf16(to, qdesc + (kk >> 2) * (SUB >> 4) + 2 * (kk & 3), kdesc + (kk >> 2) * (SUB >> 4) + 2 * (kk & 3), idesc,
                            kk > 0 ? 1u : 0u);
-          ptx::umma_commit(s_full);
-          hand_back(k_empty + 8 * stage);
-        } else if (u > 0) {
-          ptx::umma_commit(ptx::smem_addr(&ctl->o_done[g]));
+          ptx::umma_commit(s_full + 8 * g);
+          if (split || g == 1) ptx::umma_commit(k_empty + 8 * stage);
+        } else if (u >= 2) {
+          ptx::umma_commit(ptx::smem_addr(&ctl->o_done[0]) + 8 * g);
         }
-        if (u > 0) hand_back(v_empty + 8 * stage_v);
+        if (u >= 2 && (split || g == 1)) ptx::umma_commit(v_empty + 8 * stage_v);
       }
       __syncwarp();
     }
     base += n;
   }
-  if (issuer) ptx::umma_commit(ptx::smem_addr(&ctl->drain[g]));
-  wait(ptx::smem_addr(&ctl->drain[g]), 0, abort_flag, p.b.status, true);
+  if (issuer) ptx::umma_commit(ptx::smem_addr(&ctl->drain));
+  wait(ptx::smem_addr(&ctl->drain), 0, abort_flag, p.b.status, true);
 }
 
 // ---------------------------------------------------------------- softmax (a row a thread)
@@ -954,16 +948,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
       ptx::mbar_init(ptx::smem_addr(&ctl->raw_full[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->raw_empty[i]), 2);
       ptx::mbar_init(ptx::smem_addr(&ctl->k_full[i]), 2);
-      ptx::mbar_init(ptx::smem_addr(&ctl->k_empty[i]), 2);
+      ptx::mbar_init(ptx::smem_addr(&ctl->k_empty[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->v_full[i]), 2);
-      ptx::mbar_init(ptx::smem_addr(&ctl->v_empty[i]), 2);
+      ptx::mbar_init(ptx::smem_addr(&ctl->v_empty[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->s_full[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->p_half[i]), 128);
       ptx::mbar_init(ptx::smem_addr(&ctl->p_full[i]), 128);
-      ptx::mbar_init(ptx::smem_addr(&ctl->drain[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl->o_done[i]), 1);
     }
     for (int i = 0; i < kInfos; ++i) ptx::mbar_init(ptx::smem_addr(&ctl->info_full[i]), 1);
+    ptx::mbar_init(ptx::smem_addr(&ctl->drain), 1);
     ptx::mbar_init(ptx::smem_addr(&ctl->pair), 256);
     for (int i = 0; i < kPieces; ++i) {
       ptx::mbar_init(ptx::smem_addr(&ctl->piece_full[i]), 1);
@@ -994,11 +988,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
     softmax_rows<D>(p, ctl, base, sbase, tmem, (warp - 4) >> 2, warp, lane);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp < 14) {
-      issue_mmas<D>(p, ctl, sbase, tmem, warp - 12);
-    } else if (warp == 14) {
+    if (warp == 12) {
+      issue_mmas<D>(p, ctl, sbase, tmem);
+    } else if (warp == 13) {
       hand_out_pieces<D>(p, ctl, u0, u1, total, n_cta, lane);
-    } else {
+    } else if (warp == 14) {
       pages_way<D>(p, ctl, sbase, lane);
     }
   }
