@@ -7,13 +7,16 @@
 // has, so the keys and values stream through the SMs once and everything else has to keep out of
 // their way:
 //
-// * All keys of all items are one line of steps of 32 keys, cut into equal parts: one for each CTA
-//   (one an SM), one of 8 within it for each warp.  Sequences of any lengths load the GPU evenly,
+// * All keys of all items are one line of steps of 32 keys, cut into equal parts for the CTAs, and each
+//   of them into equal parts for its warps.  Sequences of any lengths load the GPU evenly,
 //   from a batch of short ones to one long one.  An item that lies in one warp is finished by it;
 //   pieces of an item in several warps are joined in shared memory, pieces in several CTAs through the
 //   workspace by a second launch, always in key order (no atomics).
-// * A warp has a ring of steps of its own in shared memory, filled by TMA (one box a page, swizzled
-//   so that the loads below meet no bank twice) and drained by itself: no barrier between warps.
+// * A warp has a ring of steps of its own in shared memory, filled by its own asynchronous copies (swizzled so
+//   that the loads below meet no bank twice; TMA's boxes of a page each took its issuing lane 700 to 1400
+//   cycles a step) and drained by itself: no barrier between warps.  What bounds a warp is
+//   the latency of its own instructions (a step's 8 KB are there 200 cycles after it asks, its arithmetic takes
+//   1700), so an SM has as many as their registers and rings allow.
 // * The products are S^T = K Q^T and O^T = V^T P^T on mma.sync m16n8k16 (keys, then head elements,
 //   on M; rows on N), since so few rows would leave most of a tcgen05 tile's 128 empty.  K's
 //   fragments are 32-bit words of the cache, converted two codes an instruction to fp16 (exact); V's need two
@@ -40,43 +43,60 @@
 namespace tp {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                         // keys of a step
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr int kCtasPerSm = 2;
 
 // A piece of an item in shared memory.
 struct Piece {
   int64_t item_end;     // the step behind the item's last
   int valid, first, last;
-  int s, h, row0;
+  int early;            // in the workspace, since the warp went on to the next item; else in its (drained) ring
+  int s, h, a, rows;
 };
 struct Start {          // where a warp's part begins
   int s, h, tile;
   int64_t at;           // its first step
 };
-template <int STAGES>
-struct alignas(16) Ctrl {
-  uint64_t full[kWarps][STAGES];
-  uint32_t info[kWarps][STAGES][2];   // scale bytes of a step's two halves (page_info)
-  Piece piece[kWarps][2];
-  Start start[kWarps];
-  int64_t sums[kWarps];
-  int64_t total;
+// An item: the rows of a sequence (n new tokens x group) and KV head h of all ranks', and its steps.
+struct RowsItem {
+  int s, h, a, len, pos0;
+  int rows, tile0, tiles, key_end;
 };
+template <int WARPS, int STAGES>
+struct alignas(16) Ctrl {
+  static constexpr int ITEMS = STAGES < 4 ? 4 : 8;   // more than are in the ring of steps at once
+  uint32_t info[WARPS][STAGES][2];   // scale bytes of a step's two halves (load_pages)
+  RowsItem item[WARPS][ITEMS];
+  Piece piece[WARPS][2];
+  Start start[WARPS];
+  int64_t sums[WARPS];
+};
+__device__ __forceinline__ RowsItem rows_item(const AttendParams& p, int s, int h, const SeqView& v) {
+  RowsItem it;
+  it.s = s, it.h = h, it.a = v.a, it.len = v.len, it.pos0 = v.pos0;
+  it.rows = v.n * p.group;
+  const int64_t end = static_cast<int64_t>(v.pos0) + v.n;     // behind the last row's position
+  it.key_end = p.causal ? static_cast<int>(max(min(static_cast<int64_t>(v.len), end), int64_t(0))) : v.len;
+  const int lo = p.window > 0 ? max(v.pos0 - p.window + 1, 0) : 0;
+  it.tile0 = min(lo, it.key_end) / kStep;
+  it.tiles = it.rows > 0 ? max(1, (it.key_end + kStep - 1) / kStep - it.tile0) : 0;   // (a row without keys is an item too)
+  return it;
+}
 
 template <int D, int NT>
 struct Cfg {
+  // Two CTAs an SM (kCtasPerSm): 12 warps of 168 registers, or 8 of 255 for two row tiles.
+  static constexpr int WARPS = NT == 1 ? 6 : 4;
+  static constexpr int THREADS = WARPS * 32;
   static constexpr int ROWS = 8 * NT;
   static constexpr uint32_t HALF = kStep * D;     // K's or V's bytes of a step
   static constexpr uint32_t STAGE = 2 * HALF;
-  static constexpr int STAGES = (NT == 1 ? 3 : 2) * (128 / D);
+  static constexpr int STAGES = (NT == 1 ? 2 : 3) * (128 / D);
   static constexpr uint32_t RING = STAGES * STAGE;                   // of one warp
   static constexpr uint32_t PIECE = ROWS * (D + 2) * 4;              // O, then (m, l) of each row
-  static constexpr uint32_t OFF_HEAD = kWarps * RING;                // each warp's first piece; its last one takes its ring
-  static constexpr uint32_t OFF_CTRL = OFF_HEAD + kWarps * PIECE;
-  static constexpr size_t SMEM = 1024 + OFF_CTRL + sizeof(Ctrl<STAGES>);
-  static_assert(PIECE <= RING && SMEM <= 232448, "shared memory");
+  static constexpr uint32_t OFF_CTRL = WARPS * RING;
+  static constexpr size_t SMEM = 1024 + OFF_CTRL + sizeof(Ctrl<WARPS, STAGES>);
+  static_assert(PIECE <= RING && kCtasPerSm * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
 
 // Two codes (the low or high half of a word) as fp16.
@@ -116,7 +136,7 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
   return v;
 }
-// A step's data in shared memory: row `key`, 16-byte chunk c, under the TMA's swizzle (128 or 64 bytes).
+// A step's data in shared memory: row `key`, 16-byte chunk c, swizzled.
 template <int D>
 __device__ __forceinline__ uint32_t chunk_at(int key, int c) {
   return static_cast<uint32_t>(key * D + ((c ^ (D == 128 ? key & 7 : (key >> 1) & 3)) << 4));
@@ -126,26 +146,37 @@ constexpr uint32_t kPageSeen = 0x10000;   // in a page's info, above its K and V
 
 // The steps of a warp's part in the order they are loaded, ahead of the one that is worked on.
 struct Loader {
-  int s, h;
+  int s, h, rank, head;        // h = rank * n_kv + head
+  uint32_t items;              // that it has begun
   int tile, tile_end;          // of the current item
   int page0;                   // the lanes hold pages page0 .. page0 + 31 of the sequence
   int my_page;
   uint32_t my_info;
   int len;                     // the sequence's keys
+  const uint8_t *k, *v;        // the rank's codes
 };
+
+// 16 bytes into shared memory, or zeros (size 0), by the asynchronous copy of the calling thread.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, uint32_t size) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 template <int D>
 __device__ __forceinline__ void load_pages(const AttendParams& p, Loader& ld, int first, int lane) {
   ld.page0 = first;
   const int64_t at = static_cast<int64_t>(first) + lane;
-  const int rank = ld.h / p.n_kv, head = ld.h - rank * p.n_kv;
   ld.my_info = 0;
   ld.my_page = 0;
   if ((at << p.b.page_shift) < ld.len) {
     ld.my_page = p.b.page_table[ld.s * p.b.ld_table + at];
     if (ld.my_page >= 0 && ld.my_page < p.b.n_pages) {
-      const int64_t sc = static_cast<int64_t>(ld.my_page) * p.ld_scales + head;
-      ld.my_info = kPageSeen | p.ks[rank][sc] | (static_cast<uint32_t>(p.vs[rank][sc]) << 8);
+      const int64_t sc = static_cast<int64_t>(ld.my_page) * p.ld_scales + ld.head;
+      ld.my_info = kPageSeen | p.ks[ld.rank][sc] | (static_cast<uint32_t>(p.vs[ld.rank][sc]) << 8);
     } else {
       bad_index(p.b);
     }
@@ -153,68 +184,59 @@ __device__ __forceinline__ void load_pages(const AttendParams& p, Loader& ld, in
 }
 
 template <int D, int NT>
-__device__ __forceinline__ void issue_step(const AttendParams& p, Loader& ld, int stage, uint32_t ring, Ctrl<Cfg<D, NT>::STAGES>* ctl,
-                                           int warp, int lane) {
+__device__ __forceinline__ void issue_step(const AttendParams& p, Loader& ld, int stage, uint32_t ring, Ctrl<Cfg<D, NT>::WARPS, Cfg<D, NT>::STAGES>* ctl,
+                                           int first_tile, int warp, int lane) {
   using C = Cfg<D, NT>;
   if (ld.tile == ld.tile_end) {   // the next item: the next head, or the next sequence's first
-    SeqView v;
-    Item it;
-    if (++ld.h == p.heads) {
-      ld.h = 0;
-      do {
-        v = seq_view(p.b, ++ld.s);
-        it = item_of<C::ROWS, kStep>(p, v, 0);
-      } while (it.tiles == 0 && ld.s + 1 < p.b.n_seqs);
-    } else {
-      v = seq_view(p.b, ld.s);
-      it = item_of<C::ROWS, kStep>(p, v, 0);
+    if (++ld.h == p.heads) ld.h = 0, ++ld.s;
+    RowsItem it;
+    for (;; ++ld.s) {
+      it = rows_item(p, ld.s, ld.h, seq_view(p.b, ld.s));
+      if (it.tiles > 0 || ld.s + 1 >= p.b.n_seqs) break;
     }
-    ld.tile = it.tile0;
+    if (lane == 0) ctl->item[warp][ld.items % Ctrl<C::WARPS, C::STAGES>::ITEMS] = it;
+    ld.tile = ld.items == 0 ? first_tile : it.tile0;
     ld.tile_end = it.tile0 + it.tiles;
-    ld.len = v.len;
+    ld.len = it.len;
     ld.page0 = -64;
+    ld.rank = p.by_kv(ld.h);
+    ld.head = ld.h - ld.rank * p.n_kv;
+    ld.k = p.k[ld.rank];
+    ld.v = p.v[ld.rank];
+    ++ld.items;
+    // Its rows of Q into L2: they are read when the step before is done.
+    if (lane < it.rows * (D / 64)) {
+      const int r = lane / (D / 64), token = p.by_group(r);
+      const __nv_bfloat16* q = p.q[ld.rank] + static_cast<int64_t>(it.a + token) * p.ld_q +
+                               (static_cast<int64_t>(ld.head) * p.group + (r - token * p.group)) * D + (lane % (D / 64)) * 64;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+    }
   }
-  const int key0 = ld.tile * kStep;
-  const int page = key0 >> p.b.page_shift;
+  const int key0 = ld.tile * kStep, page = key0 >> p.b.page_shift;
   const bool two = p.b.page_size == 16;
   if (page < ld.page0 || page + (two ? 1 : 0) >= ld.page0 + 32) load_pages<D>(p, ld, page, lane);
-  const int src = page - ld.page0;
-  const uint32_t info0 = __shfl_sync(0xffffffffu, ld.my_info, src);
-  const int page_a = __shfl_sync(0xffffffffu, ld.my_page, src);
-  const uint32_t info1 = two ? __shfl_sync(0xffffffffu, ld.my_info, src + 1) : info0;
-  const int page_b = two ? __shfl_sync(0xffffffffu, ld.my_page, src + 1) : page_a;
-  if (lane == 0) {
-    const uint32_t bar = ptx::smem_addr(&ctl->full[warp][stage]);
-    const int rank = ld.h / p.n_kv, head = ld.h - rank * p.n_kv;
-    const uint32_t box = two ? C::HALF / 2 : C::HALF;
-    const bool a = (info0 & kPageSeen) != 0, b = two && (info1 & kPageSeen) != 0;
-    const uint32_t dst = ring + stage * C::STAGE;
-    ctl->info[warp][stage][0] = info0;
-    ctl->info[warp][stage][1] = info1;
-    ptx::mbar_arrive_expect_tx(bar, ((a ? 2 : 0) + (b ? 2 : 0)) * box);
-    const int token = key0 & (p.b.page_size - 1);
-    if (a) {
-      tma_load_page(dst, &p.map_k[rank], bar, token, head, page_a);
-      tma_load_page(dst + C::HALF, &p.map_v[rank], bar, token, head, page_a);
+  constexpr int kChunks = D / 16, kKeysAtOnce = 32 / kChunks;   // 16-byte chunks of a key; keys of a copy
+  const int chunk = lane % kChunks, row = lane / kChunks;
+  const uint32_t dst = ring + stage * C::STAGE;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int src = page - ld.page0 + (two ? i : 0), key = key0 + 16 * i;
+    const uint32_t info = __shfl_sync(0xffffffffu, ld.my_info, src);
+    const int at = __shfl_sync(0xffffffffu, ld.my_page, src);
+    // (A page that is not there: zeros, nothing is read.)
+    const uint32_t size = (info & kPageSeen) != 0 ? 16 : 0;
+    const int64_t off = at * p.ld_page + (static_cast<int64_t>(ld.head) * p.b.page_size + (key & (p.b.page_size - 1)) + row) * D + chunk * 16;
+    const uint8_t* none = reinterpret_cast<const uint8_t*>(p.q[0]);
+    const uint8_t *k = ld.k + off, *v = ld.v + off;
+#pragma unroll
+    for (int j = 0; j < 16; j += kKeysAtOnce) {
+      const uint32_t to = dst + chunk_at<D>(16 * i + j + row, chunk);
+      copy16(to, size != 0 ? k + j * D : none, size);
+      copy16(to + C::HALF, size != 0 ? v + j * D : none, size);
     }
-    if (b) {
-      tma_load_page(dst + box, &p.map_k[rank], bar, 0, head, page_b);
-      tma_load_page(dst + C::HALF + box, &p.map_v[rank], bar, 0, head, page_b);
-    }
+    if (lane == 0) ctl->info[warp][stage][i] = info;
   }
   ++ld.tile;
-}
-
-__device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity, unsigned int* status) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0 && ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
-      atomicOr(status, TP_DEVSTATUS_TIMEOUT);
-      return false;
-    }
-  }
 }
 
 // What a warp knows of its item: Q's fragments, the softmax's state, and per column (row of Q) limits.
@@ -231,9 +253,9 @@ struct State {
 // Q's rows into fragments: row g of tile nt, elements 32 t .. 32 t + 31 (16 at D 64) in the k order
 // that K's words give (word j: elements 4 j .. 4 j + 3 of them).
 template <int D, int NT>
-__device__ __forceinline__ void load_item(const AttendParams& p, const Item& it, int h, State<D, NT>& st, int lane) {
+__device__ __forceinline__ void load_item(const AttendParams& p, const RowsItem& it, State<D, NT>& st, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const int rank = h / p.n_kv, head = h - rank * p.n_kv;
+  const int rank = p.by_kv(it.h), head = it.h - rank * p.n_kv;
   constexpr int W = D / 16;
   int hi_all = 0x7FFFFFFF, lo_all = 0;
 #pragma unroll
@@ -243,8 +265,8 @@ __device__ __forceinline__ void load_item(const AttendParams& p, const Item& it,
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
     if (r < it.rows) {
-      const int token = (it.row0 + r) / p.group, hq = (it.row0 + r) - token * p.group;
-      const __nv_bfloat16* src = p.q[rank] + static_cast<int64_t>(it.v.a + token) * p.ld_q +
+      const int token = p.by_group(r), hq = r - token * p.group;
+      const __nv_bfloat16* src = p.q[rank] + static_cast<int64_t>(it.a + token) * p.ld_q +
                                  (static_cast<int64_t>(head) * p.group + hq) * D + t * (D / 4);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) raw[i] = reinterpret_cast<const uint4*>(src)[i];
@@ -273,8 +295,8 @@ __device__ __forceinline__ void load_item(const AttendParams& p, const Item& it,
     for (int c = 0; c < 2; ++c) {
       st.ck[nt][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c));
       const int row = 8 * nt + 2 * t + c;
-      const int pos = it.v.pos0 + (it.row0 + row) / p.group;
-      st.hi[nt][c] = row < it.rows ? (p.causal ? min(it.v.len, pos + 1) : it.v.len) : 0;
+      const int pos = it.pos0 + p.by_group(row);
+      st.hi[nt][c] = row < it.rows ? (p.causal ? min(it.len, pos + 1) : it.len) : 0;
       st.lo[nt][c] = p.window > 0 ? pos - p.window + 1 : 0;
       st.m[nt][c] = -INFINITY;
       st.l[nt][c] = 0.0f;
@@ -284,10 +306,10 @@ __device__ __forceinline__ void load_item(const AttendParams& p, const Item& it,
 #pragma unroll
       for (int c = 0; c < 4; ++c) st.o[nt][i][c] = 0.0f;
   }
-  const int first = it.v.pos0 + it.row0 / p.group, last = it.v.pos0 + (it.row0 + max(it.rows, 1) - 1) / p.group;
+  const int first = it.pos0, last = it.pos0 + p.by_group(max(it.rows, 1) - 1);
   if (p.causal) hi_all = first + 1;
   if (p.window > 0) lo_all = last - p.window + 1;
-  st.hi_all = min(hi_all, it.v.len);
+  st.hi_all = min(hi_all, it.len);
   st.lo_all = lo_all;
   st.e_v = -1000;
 }
@@ -303,31 +325,32 @@ __device__ __forceinline__ void step(State<D, NT>& st, uint32_t data, uint32_t i
                        (info0 & info1 & kPageSeen) == 0 || (info0 & 0xFFu) == 255u || (info0 & 0xFF00u) == 0xFF00u ||
                        (info1 & 0xFFu) == 255u || (info1 & 0xFF00u) == 0xFF00u;   // (warp-uniform)
   float x[2][NT][4];
+  uint32_t ka[2][W], kb[2][W];    // keys 16 mt + g and + 8
 #pragma unroll
-  for (int mt = 0; mt < 2; ++mt) {
-    uint32_t ka[W], kb[W];        // keys 16 mt + g and + 8
-    if constexpr (D == 128) {
+  for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint4 a = lds128(data + chunk_at<D>(16 * mt + g, 2 * t + c)), b = lds128(data + chunk_at<D>(16 * mt + g + 8, 2 * t + c));
-        ka[4 * c] = a.x, ka[4 * c + 1] = a.y, ka[4 * c + 2] = a.z, ka[4 * c + 3] = a.w;
-        kb[4 * c] = b.x, kb[4 * c + 1] = b.y, kb[4 * c + 2] = b.z, kb[4 * c + 3] = b.w;
-      }
-    } else {
-      const uint4 a = lds128(data + chunk_at<D>(16 * mt + g, t)), b = lds128(data + chunk_at<D>(16 * mt + g + 8, t));
-      ka[0] = a.x, ka[1] = a.y, ka[2] = a.z, ka[3] = a.w;
-      kb[0] = b.x, kb[1] = b.y, kb[2] = b.z, kb[3] = b.w;
+    for (int c = 0; c < D / 64; ++c) {
+      const int at = D == 128 ? 2 * t + c : t;
+      const uint4 a = lds128(data + chunk_at<D>(16 * mt + g, at)), b = lds128(data + chunk_at<D>(16 * mt + g + 8, at));
+      ka[mt][4 * c] = a.x, ka[mt][4 * c + 1] = a.y, ka[mt][4 * c + 2] = a.z, ka[mt][4 * c + 3] = a.w;
+      kb[mt][4 * c] = b.x, kb[mt][4 * c + 1] = b.y, kb[mt][4 * c + 2] = b.z, kb[mt][4 * c + 3] = b.w;
     }
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[mt][nt][c] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      const uint32_t a0 = f16_lo(ka[j]), a1 = f16_lo(kb[j]), a2 = f16_hi(ka[j]), a3 = f16_hi(kb[j]);
+  for (int j = 0; j < W; ++j)
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      const uint32_t a0 = f16_lo(ka[mt][j]), a1 = f16_lo(kb[mt][j]), a2 = f16_hi(ka[mt][j]), a3 = f16_hi(kb[mt][j]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mma(x[mt][nt], a0, a1, a2, a3, st.q[nt][j][0], st.q[nt][j][1]);
     }
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
     // Scores in log2 units.  A page whose K or V is NaN makes its keys' scores NaN (its V enters as 0).
     const float ks = (info[mt] & 0xFF00u) == 0xFF00u ? __uint_as_float(0x7FFFFFFFu) : e8m0_value(info[mt] & 0xFFu);
 #pragma unroll
@@ -435,12 +458,12 @@ __device__ __forceinline__ void step(State<D, NT>& st, uint32_t data, uint32_t i
 }
 
 // Ends an item's piece: O / l to the output where the piece is the whole item, else to `piece`
-// (shared memory) with the rows' m and l.
+// with the rows' m and l.
 template <int D, int NT>
-__device__ __forceinline__ void end_piece(const AttendParams& p, const Item& it, int h, State<D, NT>& st, bool whole, uint32_t piece, int lane) {
+__device__ __forceinline__ void end_piece(const AttendParams& p, const RowsItem& it, State<D, NT>& st, bool whole, float* piece, int lane) {
   using C = Cfg<D, NT>;
   const int g = lane >> 2, t = lane & 3;
-  const int rank = h / p.n_kv, head = h - rank * p.n_kv;
+  const int rank = p.by_kv(it.h), head = it.h - rank * p.n_kv;
   const float fe = e8m0_value(static_cast<uint32_t>(max(st.e_v, -127) + 127));
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -459,17 +482,13 @@ __device__ __forceinline__ void end_piece(const AttendParams& p, const Item& it,
       }
       const int row = 8 * nt + 2 * t + c;   // elements D/8 g .. of it
       if (!whole) {
-        const uint32_t dst = piece + (row * D + g * (D / 8)) * 4;
+        float* dst = piece + row * D + g * (D / 8);
 #pragma unroll
-        for (int i = 0; i < D / 8; i += 4)
-          ptx::st_shared_v4(dst + 4 * i, __float_as_uint(o[i]), __float_as_uint(o[i + 1]), __float_as_uint(o[i + 2]), __float_as_uint(o[i + 3]));
-        if (g == 0) {
-          const uint32_t ml = piece + (C::ROWS * D + 2 * row) * 4;
-          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml), "f"(st.m[nt][c]), "f"(l) : "memory");
-        }
+        for (int i = 0; i < D / 8; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        if (g == 0) *reinterpret_cast<float2*>(piece + C::ROWS * D + 2 * row) = make_float2(st.m[nt][c], l);
       } else if (row < it.rows) {
-        const int token = (it.row0 + row) / p.group, hq = it.row0 + row - token * p.group;
-        __nv_bfloat16* dst = p.out[rank] + static_cast<int64_t>(it.v.a + token) * p.ldo +
+        const int token = p.by_group(row), hq = row - token * p.group;
+        __nv_bfloat16* dst = p.out[rank] + static_cast<int64_t>(it.a + token) * p.ldo +
                              (static_cast<int64_t>(head) * p.group + hq) * D + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < D / 8; i += 8)
@@ -480,21 +499,16 @@ __device__ __forceinline__ void end_piece(const AttendParams& p, const Item& it,
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(Cfg<D, NT>::THREADS, kCtasPerSm) paged_rows_kernel(const __grid_constant__ AttendParams p) {
   using C = Cfg<D, NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  auto* ctl = reinterpret_cast<Ctrl<C::STAGES>*>(base + C::OFF_CTRL);
+  auto* ctl = reinterpret_cast<Ctrl<C::WARPS, C::STAGES>*>(base + C::OFF_CTRL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = ptx::smem_addr(base) + warp * C::RING;
-  const uint32_t head_piece = ptx::smem_addr(base) + C::OFF_HEAD + warp * C::PIECE;
+  float* early_piece = p.early + (static_cast<int64_t>(blockIdx.x) * C::WARPS + warp) * (C::PIECE / 4);
   pdl_launch_dependents();
-  if (lane == 0) {
-    for (int i = 0; i < C::STAGES; ++i) ptx::mbar_init(ptx::smem_addr(&ctl->full[warp][i]), 1);
-    ctl->piece[warp][0].valid = ctl->piece[warp][1].valid = 0;
-    ptx::fence_mbar_init();
-    ptx::fence_proxy_async_smem();
-  }
+  if (lane == 0) ctl->piece[warp][0].valid = ctl->piece[warp][1].valid = 0;
   __syncwarp();
   pdl_wait();
 
@@ -505,156 +519,167 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   if (p.per_item) {
     my.s = blockIdx.x;
     my.h = blockIdx.y;
-    const Item it = item_of<C::ROWS, kStep>(p, seq_view(p.b, my.s), 0);
+    const RowsItem it = rows_item(p, my.s, my.h, seq_view(p.b, my.s));
     u1 = total = it.tiles;
-    my.at = u1 * warp / kWarps;
-    my.tile = static_cast<int>(my.at) + it.tile0;
-    count = static_cast<int>(u1 * (warp + 1) / kWarps - my.at);
+    const int from = it.tiles * warp / C::WARPS;
+    my.at = from;
+    my.tile = from + it.tile0;
+    count = it.tiles * (warp + 1) / C::WARPS - from;
   } else {
     // Sequences are dealt to the threads in runs; a scan of their steps finds the cuts.
-    const int run = (p.b.n_seqs + kThreads - 1) / kThreads;
+    const int run = (p.b.n_seqs + C::THREADS - 1) / C::THREADS;
     const int s0 = min(static_cast<int>(threadIdx.x) * run, p.b.n_seqs), s1 = min(s0 + run, p.b.n_seqs);
-    int64_t mine = 0;
-    for (int s = s0; s < s1; ++s) mine += item_of<C::ROWS, kStep>(p, seq_view(p.b, s), 0).tiles;
-    mine *= p.heads;
-    int64_t upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += o;
-    }
-    if (lane == 31) ctl->sums[warp] = upto;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) {
-      total += ctl->sums[w];
-      if (w < warp) upto += ctl->sums[w];
-    }
-    // (At least one step a warp, so that no CTA between two others is empty.)
-    n_cta = min(static_cast<int64_t>(gridDim.x), (total + kWarps - 1) / kWarps);
-    if (blockIdx.x < n_cta) {
-      u0 = cut(total, blockIdx.x, n_cta);
-      u1 = cut(total, blockIdx.x + 1, n_cta);
-    }
-    int64_t before = upto - mine;
-    for (int s = s0; s < s1 && before < u1; ++s) {
-      const Item it = item_of<C::ROWS, kStep>(p, seq_view(p.b, s), 0);
-      const int64_t after = before + static_cast<int64_t>(it.tiles) * p.heads;
-      if (after > u0) {
-        for (int w = 0; w < kWarps; ++w) {
-          const int64_t at = u0 + (u1 - u0) * w / kWarps;
-          if (at >= before && at < after) {
-            const int h = static_cast<int>((at - before) / it.tiles);
-            ctl->start[w] = {s, h, it.tile0 + static_cast<int>(at - before - static_cast<int64_t>(h) * it.tiles), at};
+    int64_t mine = 0, upto = 0, before = 0;
+    // (First the sums, then the sequence in which each warp's part begins.)
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+      for (int s = s0; s < s1 && (pass == 0 || before < u1); ++s) {
+        const RowsItem it = rows_item(p, s, 0, seq_view(p.b, s));
+        const int64_t steps = static_cast<int64_t>(it.tiles) * p.heads;
+        if (pass == 0) {
+          mine += steps;
+          continue;
+        }
+        const int64_t after = before + steps;
+        if (after > u0) {
+#pragma unroll 1
+          for (int w = 0; w < C::WARPS; ++w) {
+            const int64_t at = u0 + static_cast<int>(u1 - u0) * w / C::WARPS;
+            if (at >= before && at < after) {
+              const int64_t off = at - before;
+              const int h = off <= 0x7FFFFFFF ? static_cast<int>(off) / it.tiles : static_cast<int>(off / it.tiles);
+              ctl->start[w] = {s, h, it.tile0 + static_cast<int>(off - static_cast<int64_t>(h) * it.tiles), at};
+            }
           }
         }
+        before = after;
       }
-      before = after;
+      if (pass == 1) break;
+      upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      if (lane == 31) ctl->sums[warp] = upto;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) {
+        total += ctl->sums[w];
+        if (w < warp) upto += ctl->sums[w];
+      }
+      before = upto - mine;
+      // (At least one step a warp, so that no CTA between two others is empty.)
+      n_cta = min(static_cast<int64_t>(gridDim.x), (total + C::WARPS - 1) / C::WARPS);
+      if (blockIdx.x < n_cta) {
+        const Cuts cuts(total, n_cta);
+        u0 = cuts.at(blockIdx.x);
+        u1 = cuts.at(blockIdx.x + 1);
+      }
     }
     __syncthreads();
     my = ctl->start[warp];
-    count = static_cast<int>((u1 - u0) * (warp + 1) / kWarps - (u1 - u0) * warp / kWarps);
+    count = static_cast<int>(u1 - u0) * (warp + 1) / C::WARPS - static_cast<int>(u1 - u0) * warp / C::WARPS;
   }
 
+  // The loader and the worker walk the same steps, the loader STAGES ahead; it leaves the items for the
+  // worker in ctl->item.  (One loop with one copy of either's code: what a call costs before its first step is
+  // mostly the fetch of its instructions.)
   if (count > 0) {
-    // The loader and the worker walk the same steps, the loader STAGES ahead.
-    SeqView v = seq_view(p.b, my.s);
-    Item it = item_of<C::ROWS, kStep>(p, v, 0);
-    Loader ld{my.s, my.h, my.tile, it.tile0 + it.tiles, -64, 0, 0, v.len};
-    int issued = 0;
-    for (; issued < C::STAGES && issued < count; ++issued) issue_step<D, NT>(p, ld, issued, ring, ctl, warp, lane);
-    __syncwarp();
-    int s = my.s, h = my.h, tile = my.tile, stage = 0;
-    uint32_t parity = 0;
-    bool ok = true;
+    Loader ld{};
+    ld.s = my.s, ld.h = my.h - 1;      // (the first step begins an item for it)
+    int stage = 0, tile = my.tile, from = 0;
+    uint32_t items = 0;
+    bool begin = true;
+    RowsItem it{};
     State<D, NT> st;
-    for (int k = 0; k < count;) {
-      load_item<D, NT>(p, it, h, st, lane);
-      const int from = tile, end = it.tile0 + it.tiles;
-      const int n = min(end - tile, count - k);
-      if (n <= 0) break;   // (the lengths changed under the kernel)
-      for (int i = 0; i < n; ++i, ++k, ++tile) {
-        ok = __all_sync(0xffffffffu, wait_full(ptx::smem_addr(&ctl->full[warp][stage]), parity, p.b.status)) && ok;
+#pragma unroll 1
+    for (int k = -C::STAGES; k < count; ++k) {
+      if (k >= 0) {
+        if (begin) {
+          it = ctl->item[warp][items % Ctrl<C::WARPS, C::STAGES>::ITEMS];
+          if (items > 0) tile = it.tile0;
+          ++items;
+          from = tile;
+          begin = false;
+          load_item<D, NT>(p, it, st, lane);
+        }
+        copies_wait<C::STAGES - 1>();
+        __syncwarp();   // every lane's copies of the step are there
         const uint32_t info0 = ctl->info[warp][stage][0], info1 = ctl->info[warp][stage][1];
         step<D, NT>(st, ring + stage * C::STAGE, info0, info1, tile * kStep, it.key_end, lane);
+        ++tile;
         __syncwarp();   // every lane has read the stage
-        if (issued < count) {
-          issue_step<D, NT>(p, ld, stage, ring, ctl, warp, lane);
-          ++issued;
-          __syncwarp();
+        const int end = it.tile0 + it.tiles;
+        if (tile == end || k + 1 == count) {
+          const bool first = from == it.tile0, last = tile == end, whole = first && last;
+          // A piece that the warp's part cuts: its first (0) or its last (1).
+          const int place = first ? 1 : 0, early = k + 1 < count;
+          end_piece<D, NT>(p, it, st, whole, early ? early_piece : reinterpret_cast<float*>(base + warp * C::RING), lane);
+          if (!whole && lane == 0)
+            ctl->piece[warp][place] = Piece{my.at + k + 1 + (end - tile), 1, first, last, early, it.s, it.h, it.a, it.rows};
+          begin = true;
         }
-        if (++stage == C::STAGES) stage = 0, parity ^= 1;
       }
-      const bool first = from == it.tile0, last = tile == end, whole = first && last;
-      // A piece that the warp's part cuts: one that began before it goes to the first place, its last to its (drained) ring.
-      const int place = first ? 1 : 0;
-      end_piece<D, NT>(p, it, h, st, whole, place == 0 ? head_piece : ring, lane);
-      if (!whole && lane == 0)
-        ctl->piece[warp][place] = Piece{my.at + k + (end - tile), 1, first, last, s, h, it.row0};
-      if (k < count) {
-        if (++h == p.heads) {
-          h = 0;
-          do {
-            v = seq_view(p.b, ++s);
-            it = item_of<C::ROWS, kStep>(p, v, 0);
-          } while (it.tiles == 0 && s + 1 < p.b.n_seqs);
-        }
-        tile = it.tile0;
-      }
+      if (k + C::STAGES < count) issue_step<D, NT>(p, ld, stage, ring, ctl, my.tile, warp, lane);
+      copies_commit();   // (a group a step, empty ones behind the last, so that all but the newest STAGES - 1 are step k's)
+      __syncwarp();      // (what lane 0 has written down of items and steps)
+      if (++stage == C::STAGES) stage = 0;
     }
-    if (!ok && lane == 0) atomicOr(p.b.status, TP_DEVSTATUS_TIMEOUT);
   }
   __syncthreads();
 
   // Pieces of one item lie in consecutive warps, in key order.
   Join join{};
-  for (int i = 0; i < 2 * kWarps;) {
-    const Piece& lead = ctl->piece[i >> 1][i & 1];
+#pragma unroll 1
+  for (int i = 0; i < 2 * C::WARPS;) {
+    const Piece lead = ctl->piece[i >> 1][i & 1];
     if (!lead.valid) {
       ++i;
       continue;
     }
-    int member[kWarps + 1], n = 0;
+    // Its pieces: `members` (bits) up to i.
+    uint32_t members = 0;
     bool last = false;
-    for (; i < 2 * kWarps; ++i) {
+#pragma unroll 1
+    for (; i < 2 * C::WARPS; ++i) {
       const Piece& q = ctl->piece[i >> 1][i & 1];
       if (!q.valid) continue;
       if (q.s != lead.s || q.h != lead.h) break;
-      if (n <= kWarps) member[n++] = i;
+      members |= 1u << i;
       last = q.last;
     }
     const bool whole = lead.first && last;
-    const SeqView v = seq_view(p.b, lead.s);
-    const int rows = static_cast<int>(min(static_cast<int64_t>(C::ROWS), static_cast<int64_t>(v.n) * p.group - lead.row0));
-    auto piece_at = [&](int m) {
-      return reinterpret_cast<const float*>((m & 1) == 0 ? base + C::OFF_HEAD + (m >> 1) * C::PIECE : base + (m >> 1) * C::RING);
-    };
     float* part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (lead.first ? 1 : 0)) * (C::PIECE / 4);
-    for (int at = threadIdx.x * 4; at < C::ROWS * D; at += kThreads * 4) {
+#pragma unroll 1
+    for (int at = threadIdx.x * 4; at < C::ROWS * D; at += C::THREADS * 4) {
       const int row = at / D, col = at - row * D;
-      const float4 o = join_row(
-          n, [&](int m) { return *reinterpret_cast<const float2*>(piece_at(member[m]) + C::ROWS * D + 2 * row); },
-          [&](int m) { return *reinterpret_cast<const float4*>(piece_at(member[m]) + at); });
+      float top = -INFINITY, sum = 0.0f;
+      float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll 1
+      for (uint32_t m = members; m != 0; m &= m - 1) {
+        const int w = (__ffs(m) - 1) >> 1, place = (__ffs(m) - 1) & 1;
+        const float* piece = ctl->piece[w][place].early ? p.early + (static_cast<int64_t>(blockIdx.x) * C::WARPS + w) * (C::PIECE / 4)
+                                                        : reinterpret_cast<const float*>(base + w * C::RING);
+        const float2 ml = *reinterpret_cast<const float2*>(piece + C::ROWS * D + 2 * row);
+        const float4 o = *reinterpret_cast<const float4*>(piece + at);
+        const float mx = fmaxf(top, ml.x), ref = mx == -INFINITY ? 0.0f : mx, keep = ex2(top - ref), add = ml.y * ex2(ml.x - ref);
+        top = mx;
+        sum = sum * keep + add;
+        acc.x = acc.x * keep + add * o.x, acc.y = acc.y * keep + add * o.y, acc.z = acc.z * keep + add * o.z, acc.w = acc.w * keep + add * o.w;
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       if (whole) {
-        if (row < rows) store_row4(p, v.a, lead.h, lead.row0 + row, col, D, o);
+        if (row < lead.rows) store_row4(p, lead.a, lead.h, row, col, D, o);
       } else {
         *reinterpret_cast<float4*>(part + at) = o;
-        if (col == 0) {
-          float top = -INFINITY, l = 0.0f;
-          for (int m = 0; m < n; ++m) top = fmaxf(top, piece_at(member[m])[C::ROWS * D + 2 * row]);
-          const float ref = top == -INFINITY ? 0.0f : top;
-          for (int m = 0; m < n; ++m)
-            l += piece_at(member[m])[C::ROWS * D + 2 * row + 1] * ex2(piece_at(member[m])[C::ROWS * D + 2 * row] - ref);
-          part[C::ROWS * D + 2 * row] = top;
-          part[C::ROWS * D + 2 * row + 1] = l;
-        }
+        if (col == 0) *reinterpret_cast<float2*>(part + C::ROWS * D + 2 * row) = make_float2(top, sum);
       }
     }
-    if (lead.first && !last) {
-      // CTA c holds step u where c is the largest with cut(c) <= u.
-      const int64_t u = lead.item_end - 1;
-      const int64_t c_last = ((u + 1) * n_cta + total - 1) / total - 1;
-      join = Join{static_cast<int>(c_last - blockIdx.x) + 1, v.a, lead.row0, rows, lead.h, {}};
-    }
+    if (lead.first && !last)
+      join = Join{static_cast<int>(Cuts(total, n_cta).part(lead.item_end - 1) - blockIdx.x) + 1, lead.a, 0, lead.rows, lead.h, {}};
   }
   if (!p.per_item && threadIdx.x == 0) p.joins[blockIdx.x] = join;
 }
@@ -698,7 +723,7 @@ struct Plan {
   bool one_row_tile;     // 8 rows an item, else 16
   bool per_item;         // a CTA an item, no second launch; else equal parts of all steps
   int ctas;              // of those parts
-  size_t ws_bytes;
+  size_t part_bytes, ws_bytes;
 };
 
 Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int group, int sms) {
@@ -710,11 +735,13 @@ Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int group, int 
   const int64_t keys = b.max_pages * c.page_size;
   // Few short items: each by one CTA, no second launch.  Otherwise equal parts.
   pl.per_item = !pl.tiles && items <= sms && keys <= 1024;
-  pl.ctas = sms;
+  pl.ctas = pl.tiles ? sms : sms * kCtasPerSm;
   if (!pl.per_item) {
-    const size_t part = pl.tiles ? paged_tiles_part_floats(c.head_dim) * 4
-                                 : static_cast<size_t>(pl.one_row_tile ? 8 : 16) * (c.head_dim + 2) * 4;
-    pl.ws_bytes = static_cast<size_t>(pl.ctas) * (2 * part + sizeof(Join));
+    // A CTA's Join, its two partial items and (paged_rows_kernel) a piece of each warp.
+    pl.part_bytes = pl.tiles ? paged_tiles_part_floats(c.head_dim) * 4
+                             : static_cast<size_t>(pl.one_row_tile ? 8 : 16) * (c.head_dim + 2) * 4;
+    const int pieces = pl.tiles ? 0 : pl.one_row_tile ? Cfg<128, 1>::WARPS : Cfg<128, 2>::WARPS;
+    pl.ws_bytes = static_cast<size_t>(pl.ctas) * ((2 + pieces) * pl.part_bytes + sizeof(Join));
   }
   return pl;
 }
@@ -737,7 +764,7 @@ tp_status launch(const Plan& pl, const AttendParams& p, cudaStream_t stream) {
   if (r.err != cudaSuccess) return cuda_fail(r.err, "cudaFuncSetAttribute(max dynamic shared memory)");
   const dim3 grid = pl.per_item ? dim3(static_cast<unsigned>(p.b.n_seqs), static_cast<unsigned>(p.heads))
                                 : dim3(static_cast<unsigned>(pl.ctas));
-  cudaError_t e = launch_pdl(paged_rows_kernel<D, NT>, grid, dim3(kThreads), C::SMEM, stream, p);
+  cudaError_t e = launch_pdl(paged_rows_kernel<D, NT>, grid, dim3(C::THREADS), C::SMEM, stream, p);
   if (e == cudaSuccess && !pl.per_item)
     e = launch_pdl(paged_join_kernel<D, C::ROWS>, dim3(static_cast<unsigned>(pl.ctas), (C::ROWS + kJoinRows - 1) / kJoinRows),
                    dim3(kJoinThreads), 0, stream, p);
@@ -818,7 +845,7 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
     unsigned int* status = status_word();
     if (status == nullptr) return fail(TP_ERR_CUDA, "cannot locate the kernel status word");
     const int64_t ld_page = c.ld_page != 0 ? c.ld_page : static_cast<int64_t>(c.n_kv_heads) * c.page_size * c.head_dim;
-    for (int r = 0; r < c.n_ranks && c.n_pages > 0; ++r) {
+    for (int r = 0; r < c.n_ranks && c.n_pages > 0 && pl.tiles; ++r) {
       st = encode_pages(&p.map_k[r], c.k[r], c, ld_page);
       if (st == TP_OK) st = encode_pages(&p.map_v[r], c.v[r], c, ld_page);
       if (st != TP_OK) return st;
@@ -831,6 +858,8 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
     p.n_kv = c.n_kv_heads;
     p.group = n_heads / c.n_kv_heads;
     p.heads = c.n_ranks * c.n_kv_heads;
+    p.by_kv = div_by(static_cast<uint32_t>(p.n_kv));
+    p.by_group = div_by(static_cast<uint32_t>(p.group));
     p.causal = causal;
     p.window = window <= p.b.max_keys ? window : 0;
     p.scale_log2e = scale * 1.4426950408889634f;
@@ -838,6 +867,7 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
     if (!pl.per_item) {
       p.joins = static_cast<Join*>(workspace);
       p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.ctas * sizeof(Join));
+      p.early = reinterpret_cast<float*>(reinterpret_cast<char*>(p.parts) + 2 * pl.ctas * pl.part_bytes);
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (pl.tiles) return launch_paged_tiles(c.head_dim, pl.ctas, p, s);

@@ -15,6 +15,23 @@ struct Join {
   int n, a, row0, rows, h, pad[3];
 };
 
+// Division by a number that the host knows, of n < 2^31: m = ceil(2^(31 + s) / d), s = ceil(log2 d), is less than
+// 2^32 and off by less than d / 2^(31 + s) relative, so n m / 2^(31 + s) has the quotient's whole part.
+struct Div {
+  uint32_t m;
+  int s;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * m) >> (31 + s));
+  }
+#endif
+};
+inline Div div_by(uint32_t d) {
+  int s = 0;
+  while ((uint64_t(1) << s) < d) ++s;
+  return {static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + d - 1) / d), s};
+}
+
 struct AttendParams {
   CUtensorMap map_k[TP_MAX_DEGREE], map_v[TP_MAX_DEGREE];  // [pages][heads][tokens][D] codes, box of one page's tokens (at most 32)
   BatchView b;
@@ -24,10 +41,12 @@ struct AttendParams {
   int64_t ld_q, ldo, ld_page, ld_scales;
   int n_kv, group;             // KV heads of a rank, query heads of a KV head
   int heads;                   // n_ranks * n_kv
+  Div by_kv, by_group;
   int causal, window;
   float scale_log2e;
   int per_item;                // 1: a CTA takes one item whole; 0: equal parts of all steps
   float* parts;                // workspace: two partial items a CTA, O and then (m, l) of each row
+  float* early;                // workspace (paged_rows_kernel): a piece of each warp that it leaves behind
   Join* joins;                 // workspace: the item that begins in a CTA and goes beyond it
 };
 
@@ -45,7 +64,7 @@ __device__ __forceinline__ Item item_of(const AttendParams& p, const SeqView& v,
   it.v = v;
   it.row0 = block * ROWS;
   it.rows = static_cast<int>(min(static_cast<int64_t>(ROWS), static_cast<int64_t>(v.n) * p.group - it.row0));
-  const int first = it.row0 / p.group, last = (it.row0 + max(it.rows, 1) - 1) / p.group;
+  const int first = p.by_group(it.row0), last = p.by_group(it.row0 + max(it.rows, 1) - 1);
   it.key_end = p.causal ? max(min(static_cast<int64_t>(v.len), static_cast<int64_t>(v.pos0) + last + 1), int64_t(0)) : v.len;
   const int64_t lo = p.window > 0 ? max(static_cast<int64_t>(v.pos0) + first - p.window + 1, int64_t(0)) : 0;
   it.tile0 = static_cast<int>(min(lo, static_cast<int64_t>(it.key_end))) / STEP;
@@ -72,28 +91,41 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Joins up to `n` pieces of a row: weights l 2^(m - max m); 0 where no piece has seen a key.
+// Joins `n` pieces of a row in their order: weights l 2^(m - max m); 0 where no piece has seen a key.
+// Eight pieces are read at once, and what was joined before them is scaled where the maximum grew.
 template <typename ML, typename O4>
 __device__ __forceinline__ float4 join_row(int n, ML&& ml, O4&& o4) {
-  float top = -INFINITY;
-  for (int i = 0; i < n; ++i) top = fmaxf(top, ml(i).x);
-  if (top == -INFINITY) top = 0.0f;
-  float sum = 0.0f;
+  float top = -INFINITY, sum = 0.0f;
   float4 acc = make_float4(0, 0, 0, 0);
-  for (int i = 0; i < n; ++i) {
-    const float2 v = ml(i);
-    const float w = v.y * ex2(v.x - top);
-    const float4 o = o4(i);
-    sum += w;
-    acc.x += w * o.x, acc.y += w * o.y, acc.z += w * o.z, acc.w += w * o.w;
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    float2 v[8];
+    float4 o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k < n) v[k] = ml(i0 + k), o[k] = o4(i0 + k);
+    float m = top;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k < n) m = fmaxf(m, v[k].x);
+    const float ref = m == -INFINITY ? 0.0f : m, keep = ex2(top - ref);
+    top = m;
+    sum *= keep;
+    acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k < n) {
+        const float w = v[k].y * ex2(v[k].x - ref);
+        sum += w;
+        acc.x += w * o[k].x, acc.y += w * o[k].y, acc.z += w * o[k].z, acc.w += w * o[k].w;
+      }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
 __device__ __forceinline__ void store_row4(const AttendParams& p, int a, int h, int row, int col, int D, const float4& v) {
-  const int rank = h / p.n_kv, head = h - rank * p.n_kv;
-  const int token = row / p.group, hq = row - token * p.group;
+  const int rank = p.by_kv(h), head = h - rank * p.n_kv;
+  const int token = p.by_group(row), hq = row - token * p.group;
   __nv_bfloat16* dst = p.out[rank] + static_cast<int64_t>(a + token) * p.ldo + (static_cast<int64_t>(head) * p.group + hq) * D + col;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
@@ -106,8 +138,15 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-// Where the steps of all items are cut: CTA c of n has the steps from total * c / n on.
-__device__ __forceinline__ int64_t cut(int64_t total, int64_t c, int64_t n) { return total * c / n; }
+// Where the steps of all items are cut: into n parts of q or q + 1 steps, the longer ones first.
+struct Cuts {
+  int64_t q, r;
+  __device__ __forceinline__ Cuts(int64_t total, int64_t n) : q(total / n), r(total - q * n) {}
+  __device__ __forceinline__ int64_t at(int64_t c) const { return c * q + min(c, r); }      // the first step of part c
+  __device__ __forceinline__ int64_t part(int64_t u) const {                                // of step u
+    return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q;
+  }
+};
 
 constexpr int kJoinRows = 8, kJoinThreads = 256;
 

@@ -191,9 +191,7 @@ __device__ __forceinline__ void hand_out_pieces(const AttendParams& p, TilesCtrl
       out = PieceInfo{s, h, v.a, v.len, v.pos0, it.row0, it.rows, it.key_end, from, n, from == it.tile0, n == left};
       at += n;
       if (out.first && !out.last) {
-        // CTA c holds step u where c is the largest with cut(c) <= u.
-        const int64_t u = at + left - n - 1;
-        const int64_t c_last = ((u + 1) * n_cta + total - 1) / total - 1;
+        const int64_t c_last = Cuts(total, n_cta).part(at + left - n - 1);
         join = Join{static_cast<int>(c_last - blockIdx.x) + 1, v.a, it.row0, it.rows, h, {}};
       }
     }
@@ -202,10 +200,10 @@ __device__ __forceinline__ void hand_out_pieces(const AttendParams& p, TilesCtrl
       ptx::mbar_arrive(ptx::smem_addr(&ctl->piece_full[k % kPieces]));
     }
     if (!more) break;
-    const int rank = h / p.n_kv, head = h - rank * p.n_kv;
+    const int rank = p.by_kv(h), head = h - rank * p.n_kv;
 #pragma unroll 1
     for (int row = lane; row < out.rows; row += 32) {
-      const int r = out.row0 + row, token = r / p.group;
+      const int r = out.row0 + row, token = p.by_group(r);
       const __nv_bfloat16* q = p.q[rank] + static_cast<int64_t>(v.a + token) * p.ld_q +
                                (static_cast<int64_t>(head) * p.group + (r - token * p.group)) * D;
       asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
@@ -286,8 +284,9 @@ __device__ __forceinline__ void find_part(const AttendParams& p, TilesCtrl* ctl,
   n_cta = min(static_cast<int64_t>(gridDim.x), total);
   u0 = u1 = 0;
   if (blockIdx.x < n_cta) {
-    u0 = cut(total, blockIdx.x, n_cta);
-    u1 = cut(total, blockIdx.x + 1, n_cta);
+    const Cuts cuts(total, n_cta);
+    u0 = cuts.at(blockIdx.x);
+    u1 = cuts.at(blockIdx.x + 1);
   }
   if (u1 > u0 && u0 >= before && u0 < before + sum) {    // (one warp)
     for (int b = b0; b < b1; ++b) {
@@ -354,7 +353,7 @@ __device__ __forceinline__ void load_pages(const AttendParams& p, Pages& pg, con
   if ((at << p.b.page_shift) < w.len) {
     pg.page = p.b.page_table[w.s * p.b.ld_table + at];
     if (pg.page >= 0 && pg.page < p.b.n_pages) {
-      const int rank = w.h / p.n_kv, head = w.h - rank * p.n_kv;
+      const int rank = p.by_kv(w.h), head = w.h - rank * p.n_kv;
       const int64_t sc = static_cast<int64_t>(pg.page) * p.ld_scales + head;
       pg.info = kSeen | p.ks[rank][sc] | (static_cast<uint32_t>(p.vs[rank][sc]) << 8);
     } else {
@@ -402,7 +401,7 @@ __device__ __forceinline__ void pages_way(const AttendParams& p, TilesCtrl* ctl,
     if (piece == nullptr) break;
     const PieceInfo w = *piece;
     if (w.s != s || w.h != h) pg.page0 = -64, s = w.s, h = w.h;
-    const int rank = w.h / p.n_kv, head = w.h - rank * p.n_kv;
+    const int rank = p.by_kv(w.h), head = w.h - rank * p.n_kv;
     int e_run = -127;
     for (int tile = w.from; tile < w.from + w.n && ok; ++tile, ++t) {
       const int key0 = tile * kKeys, first = key0 >> shift;
@@ -808,18 +807,18 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
     const bool split = w.split();
     const int turns = w.turns(), from = w.from, n = w.n;
     const int row = (split ? 0 : 128 * g) + lane_row;
-    const int pos = w.pos0 + (w.row0 + row) / p.group;
+    const int pos = w.pos0 + p.by_group(w.row0 + row);
     int lo = 0, hi = 0x40000000;          // keys [lo, hi) are seen (by the row; what none needs is not masked)
     if (row < w.rows) {
       hi = p.causal ? min(w.len, pos + 1) : w.len;
       lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
     }
     // Where the row is in q and out, in elements from the first rank's (negative: nowhere).
-    const int rank = w.h / p.n_kv;
+    const int rank = p.by_kv(w.h);
     int64_t token = -1, column = 0;
     if (row < w.rows) {
       const int r = w.row0 + row;
-      token = r / p.group;
+      token = p.by_group(r);
       column = (static_cast<int64_t>(w.h - rank * p.n_kv) * p.group + (r - token * p.group)) * D;
       token += w.a;
     }
