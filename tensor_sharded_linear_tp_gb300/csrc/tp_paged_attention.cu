@@ -766,8 +766,8 @@ tp_status launch(const Plan& pl, const AttendParams& p, cudaStream_t stream) {
                                 : dim3(static_cast<unsigned>(pl.ctas));
   cudaError_t e = launch_pdl(paged_rows_kernel<D, NT>, grid, dim3(C::THREADS), C::SMEM, stream, p);
   if (e == cudaSuccess && !pl.per_item)
-    e = launch_pdl(paged_join_kernel<D, C::ROWS>, dim3(static_cast<unsigned>(pl.ctas), (C::ROWS + kJoinRows - 1) / kJoinRows),
-                   dim3(kJoinThreads), 0, stream, p);
+    e = launch_pdl(paged_join_kernel<D, C::ROWS, 8>, dim3(static_cast<unsigned>(pl.ctas), C::ROWS / kJoinRows<D, 8>), dim3(kJoinThreads), 0,
+                   stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return TP_OK;
 }

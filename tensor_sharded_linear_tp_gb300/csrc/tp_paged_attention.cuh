@@ -91,36 +91,39 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Joins `n` pieces of a row in their order: weights l 2^(m - max m); 0 where no piece has seen a key.
-// Eight pieces are read at once, and what was joined before them is scaled where the maximum grew.
+// Some pieces of a row joined: the largest m, the sum of l 2^(m_i - m) and the sum of these times O.
+struct Joined {
+  float m, l;
+  float4 o;
+};
+// Pieces first, first + step, ... below n in this order, eight of them read at once.
 template <typename ML, typename O4>
-__device__ __forceinline__ float4 join_row(int n, ML&& ml, O4&& o4) {
-  float top = -INFINITY, sum = 0.0f;
-  float4 acc = make_float4(0, 0, 0, 0);
-  for (int i0 = 0; i0 < n; i0 += 8) {
+__device__ __forceinline__ Joined join_pieces(int first, int step, int n, ML&& ml, O4&& o4) {
+  Joined j{-INFINITY, 0.0f, make_float4(0, 0, 0, 0)};
+#pragma unroll 1
+  for (int i0 = first; i0 < n; i0 += 8 * step) {
     float2 v[8];
     float4 o[8];
+    float m = j.m;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i0 + k < n) v[k] = ml(i0 + k), o[k] = o4(i0 + k);
-    float m = top;
+    for (int k = 0; k < 8; ++k) {
+      v[k] = make_float2(-INFINITY, 0.0f), o[k] = make_float4(0, 0, 0, 0);
+      if (i0 + k * step < n) v[k] = ml(i0 + k * step), o[k] = o4(i0 + k * step);
+    }
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i0 + k < n) m = fmaxf(m, v[k].x);
-    const float ref = m == -INFINITY ? 0.0f : m, keep = ex2(top - ref);
-    top = m;
-    sum *= keep;
-    acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, v[k].x);
+    const float ref = m == -INFINITY ? 0.0f : m, keep = ex2(j.m - ref);
+    j.m = m;
+    j.l *= keep;
+    j.o.x *= keep, j.o.y *= keep, j.o.z *= keep, j.o.w *= keep;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i0 + k < n) {
-        const float w = v[k].y * ex2(v[k].x - ref);
-        sum += w;
-        acc.x += w * o[k].x, acc.y += w * o[k].y, acc.z += w * o[k].z, acc.w += w * o[k].w;
-      }
+    for (int k = 0; k < 8; ++k) {
+      const float w = v[k].y * ex2(v[k].x - ref);
+      j.l += w;
+      j.o.x += w * o[k].x, j.o.y += w * o[k].y, j.o.z += w * o[k].z, j.o.w += w * o[k].w;
+    }
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  return j;
 }
 
 __device__ __forceinline__ void store_row4(const AttendParams& p, int a, int h, int row, int col, int D, const float4& v) {
@@ -148,27 +151,43 @@ struct Cuts {
   }
 };
 
-constexpr int kJoinRows = 8, kJoinThreads = 256;
+constexpr int kJoinThreads = 256;
+template <int D, int GROUPS>
+constexpr int kJoinRows = kJoinThreads / GROUPS / (D / 4);   // of a block
 
 // Joins the items that lie in several CTAs: blocks (c, .) the one that begins in CTA c and goes beyond
-// it (its piece in that CTA's second part, the others in the first parts of those behind), eight rows a block.
-template <int D, int ROWS>
+// it (its piece in that CTA's second part, the others in the first parts of those behind).  GROUPS
+// groups of threads take every GROUPS-th piece of a row each: a long item of few rows lies in many CTAs.
+template <int D, int ROWS, int GROUPS>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttendParams p) {
-  constexpr int PART = ROWS * (D + 2);
+  constexpr int PART = ROWS * (D + 2), QUADS = D / 4, PER = kJoinThreads / GROUPS;
+  __shared__ Joined found[GROUPS > 1 ? kJoinThreads : 1];
   pdl_launch_dependents();
   pdl_wait();
   const Join join = p.joins[blockIdx.x];
-  const int end = min(join.rows, static_cast<int>(blockIdx.y + 1) * kJoinRows) * D;
-  if (join.n == 0) return;
+  if (join.n == 0 || static_cast<int>(blockIdx.y) * kJoinRows<D, GROUPS> >= join.rows) return;
+  const int group = threadIdx.x / PER, in = threadIdx.x % PER;
+  const int row = blockIdx.y * kJoinRows<D, GROUPS> + in / QUADS, at = row * D + in % QUADS * 4;
   const float* own = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * PART;
   auto part = [&](int i) { return i == 0 ? own : own + (2 * i - 1) * static_cast<int64_t>(PART); };
-  for (int at = blockIdx.y * kJoinRows * D + threadIdx.x * 4; at < end; at += kJoinThreads * 4) {
-    const int row = at / D, col = at - row * D;
-    const float4 o = join_row(
-        join.n, [&](int i) { return *reinterpret_cast<const float2*>(part(i) + ROWS * D + 2 * row); },
-        [&](int i) { return *reinterpret_cast<const float4*>(part(i) + at); });
-    store_row4(p, join.a, join.h, join.row0 + row, col, D, o);
+  Joined j{-INFINITY, 0.0f, make_float4(0, 0, 0, 0)};
+  if (row < join.rows)
+    j = join_pieces(group, GROUPS, join.n, [&](int i) { return *reinterpret_cast<const float2*>(part(i) + ROWS * D + 2 * row); },
+                    [&](int i) { return *reinterpret_cast<const float4*>(part(i) + at); });
+  if constexpr (GROUPS > 1) {
+    found[threadIdx.x] = j;
+    __syncthreads();
+    if (group > 0) return;
+    j = join_pieces(0, 1, GROUPS, [&](int i) { return make_float2(found[i * PER + in].m, found[i * PER + in].l); },
+                    [&](int i) {
+                      const Joined& f = found[i * PER + in];
+                      const float inv = f.l == 0.0f ? 0.0f : 1.0f / f.l;
+                      return make_float4(f.o.x * inv, f.o.y * inv, f.o.z * inv, f.o.w * inv);
+                    });
   }
+  if (row >= join.rows) return;
+  const float inv = j.l == 0.0f ? 0.0f : 1.0f / j.l;
+  store_row4(p, join.a, join.h, join.row0 + row, in % QUADS * 4, D, make_float4(j.o.x * inv, j.o.y * inv, j.o.z * inv, j.o.w * inv));
 }
 
 // The kernel for many rows a KV head (tp_paged_tiles.cu).

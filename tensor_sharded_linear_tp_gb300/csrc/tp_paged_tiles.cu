@@ -1028,7 +1028,7 @@ tp_status launch(int ctas, const AttendParams& p, cudaStream_t stream) {
   if (r.err != cudaSuccess) return cuda_fail(r.err, "paged_tiles_kernel's attributes");
   e = launch_pdl(paged_tiles_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), M::SMEM, stream, p);
   if (e == cudaSuccess)
-    e = launch_pdl(paged_join_kernel<D, kRows>, dim3(static_cast<unsigned>(ctas), kRows / kJoinRows), dim3(kJoinThreads), 0, stream, p);
+    e = launch_pdl(paged_join_kernel<D, kRows, 1>, dim3(static_cast<unsigned>(ctas), kRows / kJoinRows<D, 1>), dim3(kJoinThreads), 0, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return TP_OK;
 }
