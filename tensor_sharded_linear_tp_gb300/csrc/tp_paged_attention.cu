@@ -278,18 +278,18 @@ __device__ __forceinline__ void load_item(const AttendParams& p, const RowsItem&
     top = max(top & 0xFFFFu, top >> 16);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // top < 2^(E - 126), E its exponent field: times 2^(141 - E) the row is below 2^15.  (A row of
-    // subnormals has E 0: its least steps are lost, 2^-133.)  A NaN or an infinity makes the row NaN.
-    const int E = static_cast<int>(top >> 7);
-    const float f0 = pow2((141 - E) / 2), f1 = pow2(141 - E - (141 - E) / 2);   // (2^141 itself is no fp32 value)
-    float back = p.scale_log2e * pow2((E - 141) / 2) * pow2(E - 141 - (E - 141) / 2);
+    // top < 2^(E - 126), E its exponent field: times 2^(141 - E) the row is below 2^15.  (2^127 at most, which
+    // is enough for rows below 2^-112.)  A NaN or an infinity makes the row NaN.
+    const int E = static_cast<int>(top >> 7), up = min(141 - E, 127);
+    const float f = E == 255 ? 0.0f : pow2(up);
+    float back = p.scale_log2e * pow2(-(up / 2)) * pow2(up / 2 - up);
     if (E == 255) back = __uint_as_float(0x7FFFFFFFu);
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t v = E == 255 ? 0u : w[2 * j + i];
-        st.q[nt][j][i] = f16_pair(__uint_as_float(v << 16) * f0 * f1, __uint_as_float(v & 0xFFFF0000u) * f0 * f1);
+        st.q[nt][j][i] = f16_pair(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
       }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -845,11 +845,6 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
     unsigned int* status = status_word();
     if (status == nullptr) return fail(TP_ERR_CUDA, "cannot locate the kernel status word");
     const int64_t ld_page = c.ld_page != 0 ? c.ld_page : static_cast<int64_t>(c.n_kv_heads) * c.page_size * c.head_dim;
-    for (int r = 0; r < c.n_ranks && c.n_pages > 0 && pl.tiles; ++r) {
-      st = encode_pages(&p.map_k[r], c.k[r], c, ld_page);
-      if (st == TP_OK) st = encode_pages(&p.map_v[r], c.v[r], c, ld_page);
-      if (st != TP_OK) return st;
-    }
     p.b = batch_view(c, *batch, T, status);
     p.ld_q = ld_q != 0 ? ld_q : wide;
     p.ldo = ldo != 0 ? ldo : wide;
@@ -870,7 +865,15 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
       p.early = reinterpret_cast<float*>(reinterpret_cast<char*>(p.parts) + 2 * pl.ctas * pl.part_bytes);
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (pl.tiles) return launch_paged_tiles(c.head_dim, pl.ctas, p, s);
+    if (pl.tiles) {
+      CodeMaps maps{};
+      for (int r = 0; r < c.n_ranks && c.n_pages > 0; ++r) {
+        st = encode_pages(&maps.k[r], c.k[r], c, ld_page);
+        if (st == TP_OK) st = encode_pages(&maps.v[r], c.v[r], c, ld_page);
+        if (st != TP_OK) return st;
+      }
+      return launch_paged_tiles(c.head_dim, pl.ctas, p, maps, s);
+    }
     if (c.head_dim == 128) return pl.one_row_tile ? launch<128, 1>(pl, p, s) : launch<128, 2>(pl, p, s);
     return pl.one_row_tile ? launch<64, 1>(pl, p, s) : launch<64, 2>(pl, p, s);
   });

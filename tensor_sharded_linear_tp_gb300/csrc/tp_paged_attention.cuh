@@ -33,11 +33,7 @@ inline Div div_by(uint32_t d) {
 }
 
 struct AttendParams {
-  CUtensorMap map_k[TP_MAX_DEGREE], map_v[TP_MAX_DEGREE];  // [pages][heads][tokens][D] codes, box of one page's tokens (at most 32)
   BatchView b;
-  const __nv_bfloat16* q[TP_MAX_DEGREE];
-  __nv_bfloat16* out[TP_MAX_DEGREE];
-  const uint8_t *k[TP_MAX_DEGREE], *v[TP_MAX_DEGREE], *ks[TP_MAX_DEGREE], *vs[TP_MAX_DEGREE];
   int64_t ld_q, ldo, ld_page, ld_scales;
   int n_kv, group;             // KV heads of a rank, query heads of a KV head
   int heads;                   // n_ranks * n_kv
@@ -48,6 +44,13 @@ struct AttendParams {
   float* parts;                // workspace: two partial items a CTA, O and then (m, l) of each row
   float* early;                // workspace (paged_rows_kernel): a piece of each warp that it leaves behind
   Join* joins;                 // workspace: the item that begins in a CTA and goes beyond it
+  const __nv_bfloat16* q[TP_MAX_DEGREE];
+  __nv_bfloat16* out[TP_MAX_DEGREE];
+  const uint8_t *k[TP_MAX_DEGREE], *v[TP_MAX_DEGREE], *ks[TP_MAX_DEGREE], *vs[TP_MAX_DEGREE];
+};
+// The tensor maps of the codes, [pages][heads][tokens][D], boxes of one page's tokens (at most 32).
+struct CodeMaps {
+  CUtensorMap k[TP_MAX_DEGREE], v[TP_MAX_DEGREE];
 };
 
 // One item: rows [row0, row0 + rows) of a sequence's n * group rows (token by token), and its steps.
@@ -192,6 +195,6 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 
 // The kernel for many rows a KV head (tp_paged_tiles.cu).
 size_t paged_tiles_part_floats(int head_dim);
-tp_status launch_paged_tiles(int head_dim, int ctas, const AttendParams& p, cudaStream_t stream);
+tp_status launch_paged_tiles(int head_dim, int ctas, const AttendParams& p, const CodeMaps& maps, cudaStream_t stream);
 
 }  // namespace tp

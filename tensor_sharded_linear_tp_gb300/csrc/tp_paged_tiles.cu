@@ -371,7 +371,7 @@ __device__ __forceinline__ const PieceInfo* warp_piece(TilesCtrl* ctl, uint32_t 
 // The pages' way (warp 14): where a step's keys are and what their scales are, for the others; and
 // their codes into shared memory by TMA, a box a page (of 32 keys at most).
 template <int D>
-__device__ __forceinline__ void pages_way(const AttendParams& p, TilesCtrl* ctl, uint32_t sbase, int lane) {
+__device__ __forceinline__ void pages_way(const AttendParams& p, const CodeMaps& maps, TilesCtrl* ctl, uint32_t sbase, int lane) {
   using M = Dims<D>;
   volatile int* abort_flag = &ctl->abort;
   const int shift = p.b.page_shift, boxes = p.b.page_size == 16 ? 8 : 4, box_keys = kKeys / boxes;
@@ -391,7 +391,7 @@ __device__ __forceinline__ void pages_way(const AttendParams& p, TilesCtrl* ctl,
     if (lane == 0) ptx::mbar_arrive_expect_tx(full, b.bytes);
     __syncwarp();
     if (b.load)
-      tma_load_page(sbase + M::OFF_RAW + i * M::RAW + lane * box_keys * D, i == 0 ? &p.map_k[b.rank] : &p.map_v[b.rank], full, b.token,
+      tma_load_page(sbase + M::OFF_RAW + i * M::RAW + lane * box_keys * D, i == 0 ? &maps.k[b.rank] : &maps.v[b.rank], full, b.token,
                     b.head, b.page);
     return true;
   };
@@ -933,7 +933,7 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CodeMaps maps) {
   using M = Dims<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -992,7 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
     } else if (warp == 13) {
       hand_out_pieces<D>(p, ctl, u0, u1, total, n_cta, lane);
     } else if (warp == 14) {
-      pages_way<D>(p, ctl, sbase, lane);
+      pages_way<D>(p, maps, ctl, sbase, lane);
     }
   }
   __syncwarp();
@@ -1005,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
 }
 
 template <int D>
-tp_status launch(int ctas, const AttendParams& p, cudaStream_t stream) {
+tp_status launch(int ctas, const AttendParams& p, const CodeMaps& maps, cudaStream_t stream) {
   using M = Dims<D>;
   struct Raised {
     std::once_flag once;
@@ -1026,7 +1026,7 @@ tp_status launch(int ctas, const AttendParams& p, cudaStream_t stream) {
       r.err = cudaFuncSetAttribute(paged_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(M::SMEM));
   });
   if (r.err != cudaSuccess) return cuda_fail(r.err, "paged_tiles_kernel's attributes");
-  e = launch_pdl(paged_tiles_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), M::SMEM, stream, p);
+  e = launch_pdl(paged_tiles_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), M::SMEM, stream, p, maps);
   if (e == cudaSuccess)
     e = launch_pdl(paged_join_kernel<D, kRows, 1>, dim3(static_cast<unsigned>(ctas), kRows / kJoinRows<D, 1>), dim3(kJoinThreads), 0, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
@@ -1037,8 +1037,8 @@ tp_status launch(int ctas, const AttendParams& p, cudaStream_t stream) {
 
 size_t paged_tiles_part_floats(int head_dim) { return static_cast<size_t>(kRows) * (head_dim + 2); }
 
-tp_status launch_paged_tiles(int head_dim, int ctas, const AttendParams& p, cudaStream_t stream) {
-  return head_dim == 128 ? launch<128>(ctas, p, stream) : launch<64>(ctas, p, stream);
+tp_status launch_paged_tiles(int head_dim, int ctas, const AttendParams& p, const CodeMaps& maps, cudaStream_t stream) {
+  return head_dim == 128 ? launch<128>(ctas, p, maps, stream) : launch<64>(ctas, p, maps, stream);
 }
 
 }  // namespace tp
