@@ -3,7 +3,7 @@
 //     S = scale Q K^T,  O = softmax(S) V      one item = the rows of one sequence, KV head and rank
 //
 // What bounds it: the cache's bytes.  With R rows (new tokens x query heads of the KV head) a key
-// costs 2 D bytes and 4 D R FLOP; at R <= 16 that is at most 32 FLOP a byte, a tenth of what the GPU
+// costs 2 D bytes and 4 D R FLOP; at R <= 32 that is at most 64 FLOP a byte, a quarter of what the GPU
 // has, so the keys and values stream through the SMs once and everything else has to keep out of
 // their way:
 //
@@ -22,6 +22,8 @@
 //   fragments are 32-bit words of the cache, converted two codes an instruction to fp16 (exact); V's need two
 //   keys side by side, a byte permutation first; P^T's come from S^T's by a transposing move.
 // * Scales stay out of the fragments: K's multiplies a score, V's the probability.
+// * Up to 32 rows, 8 on N at a time.  (Beyond, mma.sync's rate would bound it: at 32 rows its products take
+//   270 cycles for a step's 8 KB, which the memory delivers in 350.)
 //
 // Q enters as fp16 as well, each row scaled by a power of two to below 2^15, so that what it loses
 // lies 2^-39 below its largest element; its factor goes into the scores.  P is 2^(s - m) (m the running maximum)
@@ -85,18 +87,21 @@ __device__ __forceinline__ RowsItem rows_item(const AttendParams& p, int s, int 
 
 template <int D, int NT>
 struct Cfg {
-  // Two CTAs an SM (kCtasPerSm): 12 warps of 168 registers, or 8 of 255 for two row tiles.
+  // Two CTAs an SM (kCtasPerSm): 12 warps of 168 registers, or 8 of 255 for more row tiles.
   static constexpr int WARPS = NT == 1 ? 6 : 4;
+  static constexpr bool Q_SHARED = NT > 2;        // Q's fragments in shared memory, for want of registers
   static constexpr int THREADS = WARPS * 32;
   static constexpr int ROWS = 8 * NT;
   static constexpr uint32_t HALF = kStep * D;     // K's or V's bytes of a step
   static constexpr uint32_t STAGE = 2 * HALF;
-  static constexpr int STAGES = (NT == 1 ? 2 : 3) * (128 / D);
+  static constexpr int STAGES = (NT == 2 ? 3 : 2) * (128 / D);
   static constexpr uint32_t RING = STAGES * STAGE;                   // of one warp
   static constexpr uint32_t PIECE = ROWS * (D + 2) * 4;              // O, then (m, l) of each row
-  static constexpr uint32_t OFF_CTRL = WARPS * RING;
+  static constexpr uint32_t OFF_Q = RING;                            // in a warp's own part
+  static constexpr uint32_t OWN = RING + (Q_SHARED ? NT * (D / 16) * 32 * 8 : 0);
+  static constexpr uint32_t OFF_CTRL = WARPS * OWN;
   static constexpr size_t SMEM = 1024 + OFF_CTRL + sizeof(Ctrl<WARPS, STAGES>);
-  static_assert(PIECE <= RING && kCtasPerSm * (SMEM + 1024) <= 228 * 1024, "shared memory");
+  static_assert(PIECE <= OWN && kCtasPerSm * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
 
 // Two codes (the low or high half of a word) as fp16.
@@ -205,10 +210,11 @@ __device__ __forceinline__ void issue_step(const AttendParams& p, Loader& ld, in
     ld.v = p.v[ld.rank];
     ++ld.items;
     // Its rows of Q into L2: they are read when the step before is done.
-    if (lane < it.rows * (D / 64)) {
-      const int r = lane / (D / 64), token = p.by_group(r);
+#pragma unroll 1
+    for (int i = lane; i < it.rows * (D / 64); i += 32) {
+      const int r = i / (D / 64), token = p.by_group(r);
       const __nv_bfloat16* q = p.q[ld.rank] + static_cast<int64_t>(it.a + token) * p.ld_q +
-                               (static_cast<int64_t>(ld.head) * p.group + (r - token * p.group)) * D + (lane % (D / 64)) * 64;
+                               (static_cast<int64_t>(ld.head) * p.group + (r - token * p.group)) * D + (i % (D / 64)) * 64;
       asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
     }
   }
@@ -239,13 +245,12 @@ __device__ __forceinline__ void issue_step(const AttendParams& p, Loader& ld, in
   ++ld.tile;
 }
 
-// What a warp knows of its item: Q's fragments, the softmax's state, and per column (row of Q) limits.
+// What a warp knows of its item: Q's fragments (unless in shared memory), the softmax's state.
 template <int D, int NT>
 struct State {
-  uint32_t q[NT][D / 16][2];
+  uint32_t q[Cfg<D, NT>::Q_SHARED ? 1 : NT][D / 16][2];
   float o[NT][D / 16][4];
   float m[NT][2], l[NT][2], ck[NT][2];   // of the rows 8 nt + 2 t and + 1
-  int hi[NT][2], lo[NT][2];              // keys [lo, hi) are seen
   int hi_all, lo_all;                    // every row sees [lo_all, hi_all)
   int e_v;
 };
@@ -253,7 +258,7 @@ struct State {
 // Q's rows into fragments: row g of tile nt, elements 32 t .. 32 t + 31 (16 at D 64) in the k order
 // that K's words give (word j: elements 4 j .. 4 j + 3 of them).
 template <int D, int NT>
-__device__ __forceinline__ void load_item(const AttendParams& p, const RowsItem& it, State<D, NT>& st, int lane) {
+__device__ __forceinline__ void load_item(const AttendParams& p, const RowsItem& it, State<D, NT>& st, uint32_t q_at, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const int rank = p.by_kv(it.h), head = it.h - rank * p.n_kv;
   constexpr int W = D / 16;
@@ -285,19 +290,21 @@ __device__ __forceinline__ void load_item(const AttendParams& p, const RowsItem&
     float back = p.scale_log2e * pow2(-(up / 2)) * pow2(up / 2 - up);
     if (E == 255) back = __uint_as_float(0x7FFFFFFFu);
 #pragma unroll
-    for (int j = 0; j < W; ++j)
+    for (int j = 0; j < W; ++j) {
+      uint32_t q[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t v = E == 255 ? 0u : w[2 * j + i];
-        st.q[nt][j][i] = f16_pair(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
+        q[i] = f16_pair(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
       }
+      if constexpr (Cfg<D, NT>::Q_SHARED)
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_at + ((j * NT + nt) * 32 + lane) * 8), "r"(q[0]), "r"(q[1]) : "memory");
+      else
+        st.q[nt][j][0] = q[0], st.q[nt][j][1] = q[1];
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       st.ck[nt][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c));
-      const int row = 8 * nt + 2 * t + c;
-      const int pos = it.pos0 + p.by_group(row);
-      st.hi[nt][c] = row < it.rows ? (p.causal ? min(it.len, pos + 1) : it.len) : 0;
-      st.lo[nt][c] = p.window > 0 ? pos - p.window + 1 : 0;
       st.m[nt][c] = -INFINITY;
       st.l[nt][c] = 0.0f;
     }
@@ -316,7 +323,8 @@ __device__ __forceinline__ void load_item(const AttendParams& p, const RowsItem&
 
 // One step of 32 keys from shared memory.
 template <int D, int NT>
-__device__ __forceinline__ void step(State<D, NT>& st, uint32_t data, uint32_t info0, uint32_t info1, int key0, int key_end, int lane) {
+__device__ __forceinline__ void step(const AttendParams& p, const RowsItem& it, State<D, NT>& st, uint32_t data, uint32_t q_at, uint32_t info0, uint32_t info1, int key0,
+                                     int lane) {
   using C = Cfg<D, NT>;
   constexpr int W = D / 16;       // words of K a lane has of a key = 16-element steps of the head
   const int g = lane >> 2, t = lane & 3;
@@ -342,13 +350,19 @@ __device__ __forceinline__ void step(State<D, NT>& st, uint32_t data, uint32_t i
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[mt][nt][c] = 0.0f;
 #pragma unroll
-  for (int j = 0; j < W; ++j)
+  for (int j = 0; j < W; ++j) {
+    uint32_t a[2][4];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const uint32_t a0 = f16_lo(ka[mt][j]), a1 = f16_lo(kb[mt][j]), a2 = f16_hi(ka[mt][j]), a3 = f16_hi(kb[mt][j]);
+    for (int mt = 0; mt < 2; ++mt) a[mt][0] = f16_lo(ka[mt][j]), a[mt][1] = f16_lo(kb[mt][j]), a[mt][2] = f16_hi(ka[mt][j]), a[mt][3] = f16_hi(kb[mt][j]);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma(x[mt][nt], a0, a1, a2, a3, st.q[nt][j][0], st.q[nt][j][1]);
+    for (int nt = 0; nt < NT; ++nt) {
+      uint2 q;
+      if constexpr (C::Q_SHARED) q = lds64(q_at + ((j * NT + nt) * 32 + lane) * 8);
+      else q = make_uint2(st.q[nt][j][0], st.q[nt][j][1]);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) mma(x[mt][nt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], q.x, q.y);
     }
+  }
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
     // Scores in log2 units.  A page whose K or V is NaN makes its keys' scores NaN (its V enters as 0).
@@ -361,9 +375,15 @@ __device__ __forceinline__ void step(State<D, NT>& st, uint32_t data, uint32_t i
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int key = key0 + 16 * mt + g + 8 * (c >> 1);
-          if (key >= st.hi[nt][c & 1] || key < st.lo[nt][c & 1] || (info[mt] & kPageSeen) == 0) x[mt][nt][c] = -INFINITY;
+        for (int c = 0; c < 2; ++c) {
+          const int row = 8 * nt + 2 * t + c, pos = it.pos0 + p.by_group(row);      // keys [lo, hi) are seen
+          const int hi = row < it.rows && (info[mt] & kPageSeen) != 0 ? (p.causal ? min(it.len, pos + 1) : it.len) : 0;
+          const int lo = p.window > 0 ? pos - p.window + 1 : 0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int key = key0 + 16 * mt + g + 8 * i;
+            if (key >= hi || key < lo) x[mt][nt][c + 2 * i] = -INFINITY;
+          }
         }
     }
   }
@@ -437,7 +457,7 @@ __device__ __forceinline__ void step(State<D, NT>& st, uint32_t data, uint32_t i
         v[k][0] = w.x, v[k][1] = w.y;
       }
       // What no row sees may hold anything, a NaN times 0 among it.
-      if (partial && (key0 + key >= key_end || (info[mt] & kPageSeen) == 0 || (info[mt] & 0xFF00u) == 0xFF00u)) {
+      if (partial && (key0 + key >= it.key_end || (info[mt] & kPageSeen) == 0 || (info[mt] & 0xFF00u) == 0xFF00u)) {
 #pragma unroll
         for (int i = 0; i < VW; ++i) v[k][i] = 0;
       }
@@ -505,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, kCtasPerSm) paged_rows_ke
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto* ctl = reinterpret_cast<Ctrl<C::WARPS, C::STAGES>*>(base + C::OFF_CTRL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ring = ptx::smem_addr(base) + warp * C::RING;
+  const uint32_t ring = ptx::smem_addr(base) + warp * C::OWN, q_at = ring + C::OFF_Q;
   float* early_piece = p.early + (static_cast<int64_t>(blockIdx.x) * C::WARPS + warp) * (C::PIECE / 4);
   pdl_launch_dependents();
   if (lane == 0) ctl->piece[warp][0].valid = ctl->piece[warp][1].valid = 0;
@@ -603,12 +623,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, kCtasPerSm) paged_rows_ke
           ++items;
           from = tile;
           begin = false;
-          load_item<D, NT>(p, it, st, lane);
+          load_item<D, NT>(p, it, st, q_at, lane);
         }
         copies_wait<C::STAGES - 1>();
         __syncwarp();   // every lane's copies of the step are there
         const uint32_t info0 = ctl->info[warp][stage][0], info1 = ctl->info[warp][stage][1];
-        step<D, NT>(st, ring + stage * C::STAGE, info0, info1, tile * kStep, it.key_end, lane);
+        step<D, NT>(p, it, st, ring + stage * C::STAGE, q_at, info0, info1, tile * kStep, lane);
         ++tile;
         __syncwarp();   // every lane has read the stage
         const int end = it.tile0 + it.tiles;
@@ -616,7 +636,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, kCtasPerSm) paged_rows_ke
           const bool first = from == it.tile0, last = tile == end, whole = first && last;
           // A piece that the warp's part cuts: its first (0) or its last (1).
           const int place = first ? 1 : 0, early = k + 1 < count;
-          end_piece<D, NT>(p, it, st, whole, early ? early_piece : reinterpret_cast<float*>(base + warp * C::RING), lane);
+          end_piece<D, NT>(p, it, st, whole, early ? early_piece : reinterpret_cast<float*>(base + warp * C::OWN), lane);
           if (!whole && lane == 0)
             ctl->piece[warp][place] = Piece{my.at + k + 1 + (end - tile), 1, first, last, early, it.s, it.h, it.a, it.rows};
           begin = true;
@@ -661,7 +681,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, kCtasPerSm) paged_rows_ke
       for (uint32_t m = members; m != 0; m &= m - 1) {
         const int w = (__ffs(m) - 1) >> 1, place = (__ffs(m) - 1) & 1;
         const float* piece = ctl->piece[w][place].early ? p.early + (static_cast<int64_t>(blockIdx.x) * C::WARPS + w) * (C::PIECE / 4)
-                                                        : reinterpret_cast<const float*>(base + w * C::RING);
+                                                        : reinterpret_cast<const float*>(base + w * C::OWN);
         const float2 ml = *reinterpret_cast<const float2*>(piece + C::ROWS * D + 2 * row);
         const float4 o = *reinterpret_cast<const float4*>(piece + at);
         const float mx = fmaxf(top, ml.x), ref = mx == -INFINITY ? 0.0f : mx, keep = ex2(top - ref), add = ml.y * ex2(ml.x - ref);
@@ -719,8 +739,8 @@ tp_status current_device(int* dev) {
 
 // Which kernel takes a call, and how.
 struct Plan {
-  bool tiles;            // more than 16 rows a sequence and KV head: paged_tiles_kernel
-  bool one_row_tile;     // 8 rows an item, else 16
+  bool tiles;            // more than 32 rows a sequence and KV head: paged_tiles_kernel
+  int row_tiles;         // of 8 rows, else
   bool per_item;         // a CTA an item, no second launch; else equal parts of all steps
   int ctas;              // of those parts
   size_t part_bytes, ws_bytes;
@@ -729,8 +749,8 @@ struct Plan {
 Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int group, int sms) {
   Plan pl{};
   const int64_t rows = static_cast<int64_t>(b.max_new) * group;
-  pl.tiles = rows > 16;
-  pl.one_row_tile = rows <= 8;
+  pl.tiles = rows > 32;
+  pl.row_tiles = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   const int64_t items = static_cast<int64_t>(b.n_seqs) * c.n_ranks * c.n_kv_heads;
   const int64_t keys = b.max_pages * c.page_size;
   // Few short items: each by one CTA, no second launch.  Otherwise equal parts.
@@ -739,8 +759,8 @@ Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int group, int 
   if (!pl.per_item) {
     // A CTA's Join, its two partial items and (paged_rows_kernel) a piece of each warp.
     pl.part_bytes = pl.tiles ? paged_tiles_part_floats(c.head_dim) * 4
-                             : static_cast<size_t>(pl.one_row_tile ? 8 : 16) * (c.head_dim + 2) * 4;
-    const int pieces = pl.tiles ? 0 : pl.one_row_tile ? Cfg<128, 1>::WARPS : Cfg<128, 2>::WARPS;
+                             : static_cast<size_t>(8 * pl.row_tiles) * (c.head_dim + 2) * 4;
+    const int pieces = pl.tiles ? 0 : pl.row_tiles == 1 ? Cfg<128, 1>::WARPS : Cfg<128, 2>::WARPS;
     pl.ws_bytes = static_cast<size_t>(pl.ctas) * ((2 + pieces) * pl.part_bytes + sizeof(Join));
   }
   return pl;
@@ -766,7 +786,7 @@ tp_status launch(const Plan& pl, const AttendParams& p, cudaStream_t stream) {
                                 : dim3(static_cast<unsigned>(pl.ctas));
   cudaError_t e = launch_pdl(paged_rows_kernel<D, NT>, grid, dim3(C::THREADS), C::SMEM, stream, p);
   if (e == cudaSuccess && !pl.per_item)
-    e = launch_pdl(paged_join_kernel<D, C::ROWS, 8>, dim3(static_cast<unsigned>(pl.ctas), C::ROWS / kJoinRows<D, 8>), dim3(kJoinThreads), 0,
+    e = launch_pdl(paged_join_kernel<D, C::ROWS, 64 / C::ROWS>, dim3(static_cast<unsigned>(pl.ctas), C::ROWS / kJoinRows<D, 64 / C::ROWS>), dim3(kJoinThreads), 0,
                    stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return TP_OK;
@@ -874,8 +894,9 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
       }
       return launch_paged_tiles(c.head_dim, pl.ctas, p, maps, s);
     }
-    if (c.head_dim == 128) return pl.one_row_tile ? launch<128, 1>(pl, p, s) : launch<128, 2>(pl, p, s);
-    return pl.one_row_tile ? launch<64, 1>(pl, p, s) : launch<64, 2>(pl, p, s);
+    if (c.head_dim == 128)
+      return pl.row_tiles == 1 ? launch<128, 1>(pl, p, s) : pl.row_tiles == 2 ? launch<128, 2>(pl, p, s) : launch<128, 4>(pl, p, s);
+    return pl.row_tiles == 1 ? launch<64, 1>(pl, p, s) : pl.row_tiles == 2 ? launch<64, 2>(pl, p, s) : launch<64, 4>(pl, p, s);
   });
 }
 
