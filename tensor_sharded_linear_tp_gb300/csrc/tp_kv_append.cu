@@ -202,7 +202,7 @@ __device__ __forceinline__ void rotate_q(const AppendParams& p, int64_t unit, in
     }
   }
   // The row's position; rows of no sequence are left alone.
-  const int s = find_sequence(p.b, t, 1, 1, 0, lane);
+  const int s = find_sequence(p.b, t, 1, 0, lane);
   if (s < 0) return;
   const SeqView v = seq_view(p.b, s);
   const int i_new = t - v.a;
@@ -263,7 +263,7 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int64_t block
   // Which tokens [j0, j1) of which sequence, in which page (the same for the whole block).
   int j0 = 0, j1 = 0, row0 = 0;                    // the row of position j is row0 + j
   int64_t page = -1;
-  const int s = find_sequence(p.b, slot, p.slot_per, 1, p.slot_gap, lane);
+  const int s = find_sequence(p.b, slot, p.slot_per, p.slot_gap, lane);
   if (s >= 0) {
     const SeqView v = seq_view(p.b, s);
     const int64_t local = slot - (v.a / p.slot_per + static_cast<int64_t>(p.slot_gap) * s);
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_append_token_kernel(const
       raw[i][1] = *reinterpret_cast<const uint4*>(src + h * D + 8 * ch.c1);
     }
   }
-  const int s = find_sequence(p.b, t, 1, 1, 0, lane);
+  const int s = find_sequence(p.b, t, 1, 0, lane);
   if (s < 0) return;
   const SeqView v = seq_view(p.b, s);
   if (t - v.a >= v.n) return;            // rows of no sequence are left alone

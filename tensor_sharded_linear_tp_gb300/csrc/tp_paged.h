@@ -64,13 +64,13 @@ __device__ __forceinline__ SeqView seq_view(const BatchView& b, int s) {
 // sequence s never need more than base(s + 1) - base(s) blocks for gap large enough), and
 // no prefix sum over the sequences is needed.  Warp-collective: 32 sequences are probed at once.
 // Returns -1 where u lies before the first sequence; a u behind the last belongs to the last.
-__device__ __forceinline__ int find_sequence(const BatchView& b, int64_t u, int per, int mul, int gap, int lane) {
+__device__ __forceinline__ int find_sequence(const BatchView& b, int64_t u, int per, int gap, int lane) {
   int lo = -1, hi = b.n_seqs;   // base(lo) <= u (or lo = -1), base(hi) > u or hi = n_seqs
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;   // probes lo + step, lo + 2 step, ... below hi
     const int64_t s = static_cast<int64_t>(lo) + static_cast<int64_t>(step) * (lane + 1);
     bool below = false;
-    if (s < hi) below = static_cast<int64_t>(max(b.seq_start[s], 0)) * mul / per + static_cast<int64_t>(gap) * s <= u;
+    if (s < hi) below = static_cast<int64_t>(max(b.seq_start[s], 0)) / per + static_cast<int64_t>(gap) * s <= u;
     const int n = __popc(__ballot_sync(0xffffffffu, below));   // starts ascend: the lanes below form a prefix
     hi = static_cast<int>(min(static_cast<int64_t>(hi), static_cast<int64_t>(lo) + static_cast<int64_t>(step) * (n + 1)));
     lo += step * n;

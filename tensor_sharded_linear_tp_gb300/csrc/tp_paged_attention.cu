@@ -750,7 +750,7 @@ Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int group, int 
   Plan pl{};
   const int64_t rows = static_cast<int64_t>(b.max_new) * group;
   pl.tiles = rows > 32;
-  pl.row_tiles = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  pl.row_tiles = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
   const int64_t items = static_cast<int64_t>(b.n_seqs) * c.n_ranks * c.n_kv_heads;
   const int64_t keys = b.max_pages * c.page_size;
   // Few short items: each by one CTA, no second launch.  Otherwise equal parts.
@@ -790,6 +790,16 @@ tp_status launch(const Plan& pl, const AttendParams& p, cudaStream_t stream) {
                    stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   return TP_OK;
+}
+
+template <int D>
+tp_status launch_rows(const Plan& pl, const AttendParams& p, cudaStream_t stream) {
+  switch (pl.row_tiles) {
+    case 1: return launch<D, 1>(pl, p, stream);
+    case 2: return launch<D, 2>(pl, p, stream);
+    case 3: return launch<D, 3>(pl, p, stream);
+    default: return launch<D, 4>(pl, p, stream);
+  }
 }
 
 tp_status check_attention(const tp_paged_cache* c, const tp_paged_batch* b, int64_t T, int n_heads, bool* empty) {
@@ -894,9 +904,7 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
       }
       return launch_paged_tiles(c.head_dim, pl.ctas, p, maps, s);
     }
-    if (c.head_dim == 128)
-      return pl.row_tiles == 1 ? launch<128, 1>(pl, p, s) : pl.row_tiles == 2 ? launch<128, 2>(pl, p, s) : launch<128, 4>(pl, p, s);
-    return pl.row_tiles == 1 ? launch<64, 1>(pl, p, s) : pl.row_tiles == 2 ? launch<64, 2>(pl, p, s) : launch<64, 4>(pl, p, s);
+    return c.head_dim == 128 ? launch_rows<128>(pl, p, s) : launch_rows<64>(pl, p, s);
   });
 }
 

@@ -27,8 +27,8 @@
 // Numbers: Q enters as fp16, each row times a power of two to below 2^15 (what that loses lies 2^-39
 // below its largest element).  K's codes enter times 2^(e - E + 7), E the largest exponent of the step's pages,
 // V's likewise with E the largest so far: at most 448 * 2^7 < 65504, and what is 2^-40 below the largest is
-// lost.  P = 2^(s - m + 5) with the running maximum m raised only where a row exceeds it by more than 10, so P
-// is at most 2^15 and what is 2^-30 below the largest is lost; l sums the unrounded P, O stays in units of
+// lost.  P = 2^(s - m + 6) with the running maximum m raised only where a row exceeds it by more than 9, so P
+// is at most 2^15 and what is 2^-31 below the largest is lost; l sums the unrounded P, O stays in units of
 // 2^(E - 7).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -48,7 +48,7 @@ constexpr int kThreads = 512;
 constexpr int kKeys = 128;                        // keys of a step
 constexpr int kRows = 256;                        // rows of an item
 constexpr int kInfos = 8;                         // steps whose Info is kept: seven are in use (see pages_way)
-constexpr float kBias = 5.0f, kSlack = 10.0f;     // P = 2^(s - m + kBias), m raised by scores above m + kSlack
+constexpr float kBias = 6.0f, kSlack = 9.0f;     // P = 2^(s - m + kBias), m raised by scores above m + kSlack
 constexpr uint32_t SUB = 16384;                   // 128 rows x 64 fp16, 128-byte swizzled
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -90,7 +90,6 @@ struct alignas(16) TilesCtrl {
   int abort;
   Info info[kInfos];
   int64_t sums[kThreads / 32];
-  int64_t total;
   struct {
     int s, h, block, tile;
   } start;
@@ -978,12 +977,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
   int64_t u0, u1, total, n_cta;
   find_part(p, ctl, u0, u1, total, n_cta);
 
-  // 512 threads of 128 registers: 80 + 184 + 184 + 64 a warpgroup's thread.
+  // 512 threads of 128 registers: 64 + 192 + 192 + 64 a warpgroup's thread.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     codes_way<D>(p, ctl, sbase, u1 - u0, warp, lane);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     softmax_rows<D>(p, ctl, base, sbase, tmem, (warp - 4) >> 2, warp, lane);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");

@@ -404,6 +404,18 @@ def test_several_tokens(seqs, D, group, page, causal, window):
     c.check(outs, causal=causal, window=window, before=fresh(q))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group, new", [(8, 1), (3, 3), (8, 2), (17, 1), (6, 4), (5, 5), (8, 4), (11, 3)])
+@pytest.mark.parametrize("olds", [[300], [700, 3, 2500, 0, 65, 4000]], ids=len)
+def test_row_counts_on_either_side_of_a_variant(olds, group, new, D):
+    """8, 9, 16, 17, 24, 25, 32 and 33 rows a KV head; items of one CTA and items cut between them."""
+    c = Case([(old, new) for old in olds], p=2, n_kv=2, group=group, D=D, page=16, seed=group + new, behind=1)
+    q = c.queries()
+    outs = fresh(q)
+    tp.tp_attention_paged_fp8(q, c.cache, c.batch, outs=outs)
+    c.check(outs, before=fresh(q))
+
+
 @pytest.mark.parametrize("D, group, n_kv", [(128, 1, 3), (128, 4, 1), (64, 16, 2), (128, 12, 1)])
 @pytest.mark.parametrize("seqs", [[(9000, 1)], [(4000, 1), (2, 1), (6000, 1), (70, 1)], [(5000, 1)] + [(33, 1)] * 40,
                                   [(11, 1)] * 300, [(0, 0)] * 5 + [(3000, 1)] + [(0, 0)] * 300 + [(2, 1)]], ids=len)
