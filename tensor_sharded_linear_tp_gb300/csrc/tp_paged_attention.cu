@@ -333,16 +333,6 @@ __device__ __forceinline__ void step(const AttendParams& p, const RowsItem& it, 
                        (info0 & info1 & kPageSeen) == 0 || (info0 & 0xFFu) == 255u || (info0 & 0xFF00u) == 0xFF00u ||
                        (info1 & 0xFFu) == 255u || (info1 & 0xFF00u) == 0xFF00u;   // (warp-uniform)
   float x[2][NT][4];
-  uint32_t ka[2][W], kb[2][W];    // keys 16 mt + g and + 8
-#pragma unroll
-  for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-      const int at = D == 128 ? 2 * t + c : t;
-      const uint4 a = lds128(data + chunk_at<D>(16 * mt + g, at)), b = lds128(data + chunk_at<D>(16 * mt + g + 8, at));
-      ka[mt][4 * c] = a.x, ka[mt][4 * c + 1] = a.y, ka[mt][4 * c + 2] = a.z, ka[mt][4 * c + 3] = a.w;
-      kb[mt][4 * c] = b.x, kb[mt][4 * c + 1] = b.y, kb[mt][4 * c + 2] = b.z, kb[mt][4 * c + 3] = b.w;
-    }
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -350,17 +340,29 @@ __device__ __forceinline__ void step(const AttendParams& p, const RowsItem& it, 
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[mt][nt][c] = 0.0f;
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
-    uint32_t a[2][4];
+  for (int c = 0; c < D / 64; ++c) {
+    uint32_t ka[2][4], kb[2][4];    // keys 16 mt + g and + 8, four words of a lane
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) a[mt][0] = f16_lo(ka[mt][j]), a[mt][1] = f16_lo(kb[mt][j]), a[mt][2] = f16_hi(ka[mt][j]), a[mt][3] = f16_hi(kb[mt][j]);
+    for (int mt = 0; mt < 2; ++mt) {
+      const int at = D == 128 ? 2 * t + c : t;
+      const uint4 a = lds128(data + chunk_at<D>(16 * mt + g, at)), b = lds128(data + chunk_at<D>(16 * mt + g + 8, at));
+      ka[mt][0] = a.x, ka[mt][1] = a.y, ka[mt][2] = a.z, ka[mt][3] = a.w;
+      kb[mt][0] = b.x, kb[mt][1] = b.y, kb[mt][2] = b.z, kb[mt][3] = b.w;
+    }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      uint2 q;
-      if constexpr (C::Q_SHARED) q = lds64(q_at + ((j * NT + nt) * 32 + lane) * 8);
-      else q = make_uint2(st.q[nt][j][0], st.q[nt][j][1]);
+    for (int i = 0; i < 4; ++i) {
+      const int j = 4 * c + i;
+      uint32_t a[2][4];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) mma(x[mt][nt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], q.x, q.y);
+      for (int mt = 0; mt < 2; ++mt) a[mt][0] = f16_lo(ka[mt][i]), a[mt][1] = f16_lo(kb[mt][i]), a[mt][2] = f16_hi(ka[mt][i]), a[mt][3] = f16_hi(kb[mt][i]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint2 q;
+        if constexpr (C::Q_SHARED) q = lds64(q_at + ((j * NT + nt) * 32 + lane) * 8);
+        else q = make_uint2(st.q[nt][j][0], st.q[nt][j][1]);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) mma(x[mt][nt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], q.x, q.y);
+      }
     }
   }
 #pragma unroll
