@@ -627,13 +627,18 @@ TP_API tp_status tp_residual_norm(const tp_residual_norm_args* args, tp_stream_t
  * position j is slot j % page_size of page page_table[s][j / page_size].  Rows
  * of T outside every sequence (padding) are neither read nor written.  A page
  * may be in several sequences' tables (a shared prefix), but not be appended
- * to by two in one call.
+ * to by two in one call.  Table entries of pages that no row of the call sees
+ * (behind kv_len, or before every row's window) may hold anything.
  *
  * What only the device can see is checked there: a token without a place (a
  * negative position, a page outside the table or the cache) is not cached, a
  * key in such a page is not seen, a token whose rotation is outside its table
  * is NaN, and rows beyond max_new or T are left out.  Nothing is read or
  * written out of bounds, and tp_device_status reports TP_ERR_INVALID_ARG.
+ *
+ * Sizes (TP_ERR_UNSUPPORTED beyond): 2^30 rows, pages, and keys of a sequence,
+ * 65535 heads of a rank, 2^24 sequences; for the attention also 65535 KV heads
+ * of all ranks, and page tables of 2^40 keys over all of them.
  */
 typedef struct {
   int n_ranks;                  /* 1 .. TP_MAX_DEGREE */
@@ -719,11 +724,13 @@ TP_API tp_status tp_kv_append_fp8(const tp_paged_cache* cache, const tp_paged_ba
  * workspace: device buffer of tp_attention_paged_workspace_bytes(...) bytes,
  *       16-byte aligned, owned by the caller, of any content.  Calls that share one must not
  *       overlap on the GPU.
- * Codes and Q enter the tensor cores exactly (as fp16, scaled by powers of
- * two); products, softmax and sums are fp32, the probabilities enter P.V as
- * fp16 (2^-12 relative, a sixteenth of the output's own rounding step).  A key or value
- * page that is NaN makes the rows that see it NaN, and no others.  The same
- * call gives the same bits every time.
+ * Codes and Q enter the tensor cores as fp16, scaled by powers of two: exactly
+ * but for what lies 2^-39 below the largest element of a row of Q or 2^-40 below the
+ * largest page scale in use.  Products, softmax and sums are fp32, the probabilities
+ * enter P.V as fp16 (2^-11 relative, an eighth of the output's own 2^-8).  A
+ * page whose K or V is NaN (scale byte 255, as tp_kv_append_fp8 leaves it) makes the rows that see
+ * it NaN and no others; NaN codes in a page with another scale byte may make any row of
+ * the sequence NaN.  The same call gives the same bits every time.
  * Alignment (TP_ERR_ALIGNMENT): ld_q and ldo % 8 == 0, q and out 16-byte.
  * T == 0, n_seqs == 0 or max_new == 0 enqueues nothing.
  */

@@ -812,6 +812,8 @@ class PagedBatch:
               for name, t, shape in (("seq_start", seq_start, (n + 1,)), ("kv_len", kv_len, (n,)),
                                      ("page_table", page_table, (n, max_pages)))][2]
         self.seq_start, self.kv_len, self.page_table = seq_start, kv_len, page_table
+        if not 0 <= max_new < 2 ** 31:
+            raise ValueError(f"max_new must be in 0 .. 2**31 - 1, got {max_new}")
         self.n_seqs, self.max_pages, self.max_new = n, max_pages, int(max_new)
         self._struct = _paged_batch(n, self.max_new, seq_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), ld,
                                     max_pages)
@@ -899,7 +901,7 @@ def tp_attention_paged_fp8(q: Sequence[torch.Tensor], cache: PagedCache, batch: 
             raise ValueError("workspace must be contiguous, on the current CUDA device")
         ws_at, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(lib.tp_attention_paged_fp8(cache._struct, batch._struct, at, ld, T, n_heads,
-                                      d ** -0.5 if scale is None else scale, int(causal), window, ws_at, ws_bytes, out_at,
+                                      d ** -0.5 if scale is None else scale, int(causal), min(window, 2 ** 31 - 1), ws_at, ws_bytes, out_at,
                                       ldo, _launch_stream(stream, dev)))
     return list(outs)
 
@@ -917,7 +919,7 @@ def tp_status_name(status: int) -> str:
 
 
 def tp_device_status(stream=None) -> None:
-    """Synchronise the stream; raise TPError if a kernel gave up on a bounded wait."""
+    """Synchronise the stream; raise TPError if a kernel gave up on a bounded wait or met a bad index (paged cache)."""
     _check(lib.tp_device_status(_stream(stream)))
 
 

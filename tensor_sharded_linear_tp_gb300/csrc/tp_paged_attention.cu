@@ -182,8 +182,8 @@ __device__ __forceinline__ void load_pages(const AttendParams& p, Loader& ld, in
     if (ld.my_page >= 0 && ld.my_page < p.b.n_pages) {
       const int64_t sc = static_cast<int64_t>(ld.my_page) * p.ld_scales + ld.head;
       ld.my_info = kPageSeen | p.ks[ld.rank][sc] | (static_cast<uint32_t>(p.vs[ld.rank][sc]) << 8);
-    } else {
-      bad_index(p.b);
+    } else if (p.window == 0 || ((at + 1) << p.b.page_shift) > seq_view(p.b, ld.s).pos0 - p.window + 1) {
+      bad_index(p.b);      // (a page before every row's window may be gone)
     }
   }
 }
@@ -812,6 +812,8 @@ tp_status check_attention(const tp_paged_cache* c, const tp_paged_batch* b, int6
   if (static_cast<int64_t>(T) * (n_heads / c->n_kv_heads) + b->n_seqs > 0x7FFFFFFF ||
       static_cast<int64_t>(c->n_ranks) * c->n_kv_heads > 65535)
     return fail(TP_ERR_UNSUPPORTED, "more than 2^31-1 rows of a KV head, or 65535 KV heads of all ranks");
+  if (static_cast<double>(b->n_seqs) * c->n_ranks * c->n_kv_heads * (static_cast<double>(b->max_pages) * c->page_size) > 0x1p40)
+    return fail(TP_ERR_UNSUPPORTED, "page tables of more than 2^40 keys, over all KV heads");   // (a CTA counts its steps in 32 bits)
   return TP_OK;
 }
 
@@ -851,7 +853,8 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
       return fail(TP_ERR_INVALID_ARG, "a row stride (ld_q %lld, ldo %lld) is smaller than its row", (long long)ld_q, (long long)ldo);
     if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal))
       return fail(TP_ERR_INVALID_ARG, "causal must be 0 or 1, and window >= 0 and 0 without causal; got %d, %d", causal, window);
-    if (!(scale - scale == 0.0f)) return fail(TP_ERR_INVALID_ARG, "scale must be finite");
+    const float scale_log2e = scale * 1.4426950408889634f;
+    if (!(scale_log2e - scale_log2e == 0.0f)) return fail(TP_ERR_INVALID_ARG, "scale must be finite, and below 2^127");
     if (empty) return TP_OK;
     if (q == nullptr || out == nullptr) return fail(TP_ERR_INVALID_ARG, "q or out is NULL");
     if (ld_q % 8 != 0 || ldo % 8 != 0)
@@ -889,7 +892,7 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
     p.by_group = div_by(static_cast<uint32_t>(p.group));
     p.causal = causal;
     p.window = window <= p.b.max_keys ? window : 0;
-    p.scale_log2e = scale * 1.4426950408889634f;
+    p.scale_log2e = scale_log2e;
     p.per_item = pl.per_item ? 1 : 0;
     if (!pl.per_item) {
       p.joins = static_cast<Join*>(workspace);

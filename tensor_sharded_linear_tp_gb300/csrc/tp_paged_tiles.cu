@@ -355,8 +355,8 @@ __device__ __forceinline__ void load_pages(const AttendParams& p, Pages& pg, con
       const int rank = p.by_kv(w.h), head = w.h - rank * p.n_kv;
       const int64_t sc = static_cast<int64_t>(pg.page) * p.ld_scales + head;
       pg.info = kSeen | p.ks[rank][sc] | (static_cast<uint32_t>(p.vs[rank][sc]) << 8);
-    } else {
-      bad_index(p.b);
+    } else if (p.window == 0 || ((at + 1) << p.b.page_shift) > w.pos0 + p.by_group(w.row0) - p.window + 1) {
+      bad_index(p.b);      // (a page before every row's window may be gone)
     }
   }
 }

@@ -441,6 +441,21 @@ def test_rows_that_see_nothing(new):
     c.check(outs)
 
 
+@pytest.mark.parametrize("new", [1, 20, 200])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("window", [1, 50, 333])
+def test_pages_before_every_window_may_be_gone(new, page, window):
+    c = Case([(1000, new), (70, new), (345, new)], p=1, n_kv=2, group=3, D=128, page=page, seed=window + new)
+    q = c.queries()
+    table = c.table.copy()
+    for s, (_, n, length) in enumerate(c.seqs):
+        table[s, :max(length - n - window + 1, 0) // page] = (-1, c.n_pages, 2 ** 31 - 1)[s]
+    batch = tp.PagedBatch(c.batch.seq_start, c.batch.kv_len, i32(table.tolist()), new)
+    outs = tp.tp_attention_paged_fp8(q, c.cache, batch, window=window)
+    tp.tp_device_status()
+    c.check(outs, window=window)
+
+
 @pytest.mark.parametrize("new", [1, 4, 100])
 @pytest.mark.parametrize("page", [16, 64])
 def test_a_nan_page_stays_with_the_rows_that_see_it(new, page):

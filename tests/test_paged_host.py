@@ -185,6 +185,8 @@ def _attend(kw):
     (dict(ldo=1028), "TP_ERR_ALIGNMENT"), (dict(q=None), "TP_ERR_INVALID_ARG"), (dict(q=FAKE + 8), "TP_ERR_ALIGNMENT"),
     (dict(out=None), "TP_ERR_INVALID_ARG"), (dict(out=FAKE + 2), "TP_ERR_ALIGNMENT"), (dict(causal=2), "TP_ERR_INVALID_ARG"),
     (dict(window=-1), "TP_ERR_INVALID_ARG"), (dict(window=5, causal=0), "TP_ERR_INVALID_ARG"),
+    (dict(scale=3e38), "TP_ERR_INVALID_ARG"),
+    (dict(n_seqs=1 << 20, max_pages=1 << 16, n_kv_heads=2, n_heads=2), "TP_ERR_UNSUPPORTED"),
     (dict(scale=float("nan")), "TP_ERR_INVALID_ARG"), (dict(scale=float("inf")), "TP_ERR_INVALID_ARG"),
     (dict(no_cache=True), "TP_ERR_INVALID_ARG"), (dict(n_kv_heads=40000, n_heads=40000), "TP_ERR_UNSUPPORTED"),
 ])
