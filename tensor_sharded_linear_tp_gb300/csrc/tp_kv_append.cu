@@ -10,6 +10,12 @@
 // tokens' codes read and written again, scaled by 2^(e_old - e): exact but for codes that fall
 // among the subnormal ones, since scales are powers of two.
 //
+// What bounds it: the bytes (Q, K and V read once as bf16, Q written, K and V as bytes), and close behind them the
+// instructions: 14 an element of K and V.  A prompt of 4608 tokens, 4 ranks of 12 heads and 12 KV heads of 128
+// (283 MB) takes 76 us, 0.55 of the copy rate (the pages' part 58 us, Q's 21; a warp loads its 16 tokens, waits, and needs
+// their maximum before it can write: three CTAs an SM hide part of that).  Small calls are a launch: one token of 4
+// ranks 3.3 us, a batch of 61 3.6 us, 7 chunks of odd lengths (21 MB) 10.2 us, against 3.1 of their bytes.
+//
 // Which sequence and page a block has comes from the device's seq_start without a prefix sum
 // (find_sequence), so that lengths may change between the replays of a graph.
 #include <cuda_bf16.h>
@@ -241,7 +247,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
   return e4m3x4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
 }
 
-// The rotation's rows for a page's tokens, where several heads use them.
+// The rotation's rows for a page's tokens, where several heads of a block use them (a larger page has fewer in one).
 constexpr int kTablePages = 32;                  // tokens of the largest page that has them in shared memory
 struct alignas(16) Shared {
   float cs[kTablePages][128];
@@ -392,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_con
     append_page<D>(p, static_cast<int64_t>(blockIdx.x) - p.q_blocks, sh);
 }
 
-// One new token a sequence at most (decoding): a warp takes kTokenRounds rounds of a token's heads, Q's,
+// One new token a sequence at most (decoding; 61 sequences 3.6 us, 6.7 by the kernel above, whose blocks are for 16
+// tokens and more): a warp takes kTokenRounds rounds of a token's heads, Q's,
 // K's and V's alike, a head held by kParts threads.  No page is shared by two tokens here, so no block has
 // to meet.
 constexpr int kTokenWarps = 2, kTokenRounds = 2;

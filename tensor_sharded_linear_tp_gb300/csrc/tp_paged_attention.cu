@@ -5,7 +5,10 @@
 // What bounds it: the cache's bytes.  With R rows (new tokens x query heads of the KV head) a key
 // costs 2 D bytes and 4 D R FLOP; at R <= 32 that is at most 64 FLOP a byte, a quarter of what the GPU
 // has, so the keys and values stream through the SMs once and everything else has to keep out of
-// their way:
+// their way.  Measured: 64 sequences of 50 to 8000 tokens, 8 KV heads of 6 query heads (569 MB) in 116 us, 0.72 of the
+// copy rate (queueing and prologues take some 10 us, the last CTAs 10, the join 6); one sequence of 131000
+// tokens 59 us, 0.67.  From 17 rows on it is the warps' own latency that bounds (eight of them an SM):
+// 16 sequences 57 us with 12 rows, 65 with 18, 88 with 30, where the bytes take 24.
 //
 // * All keys of all items are one line of steps of 32 keys, cut into equal parts for the CTAs, and each
 //   of them into equal parts for its warps.  Sequences of any lengths load the GPU evenly,
@@ -14,16 +17,15 @@
 //   workspace by a second launch, always in key order (no atomics).
 // * A warp has a ring of steps of its own in shared memory, filled by its own asynchronous copies (swizzled so
 //   that the loads below meet no bank twice; TMA's boxes of a page each took its issuing lane 700 to 1400
-//   cycles a step) and drained by itself: no barrier between warps.  What bounds a warp is
-//   the latency of its own instructions (a step's 8 KB are there 200 cycles after it asks, its arithmetic takes
-//   1700), so an SM has as many as their registers and rings allow.
+//   cycles a step: 128 us for the 64 sequences, not 109 to 116) and drained by itself: no barrier between warps.  What
+//   bounds a warp is the latency of its own instructions (some 1700 cycles a step at 8 rows), so an SM has as
+//   many as their registers and rings allow.
 // * The products are S^T = K Q^T and O^T = V^T P^T on mma.sync m16n8k16 (keys, then head elements,
 //   on M; rows on N), since so few rows would leave most of a tcgen05 tile's 128 empty.  K's
 //   fragments are 32-bit words of the cache, converted two codes an instruction to fp16 (exact); V's need two
 //   keys side by side, a byte permutation first; P^T's come from S^T's by a transposing move.
 // * Scales stay out of the fragments: K's multiplies a score, V's the probability.
-// * Up to 32 rows, 8 on N at a time.  (Beyond, mma.sync's rate would bound it: at 32 rows its products take
-//   270 cycles for a step's 8 KB, which the memory delivers in 350.)
+// * Up to 32 rows, 8 on N at a time, and a kernel for each 8 more (make_plan).
 //
 // Q enters as fp16 as well, each row scaled by a power of two to below 2^15, so that what it loses
 // lies 2^-39 below its largest element; its factor goes into the scores.  P is 2^(s - m) (m the running maximum)
@@ -87,7 +89,8 @@ __device__ __forceinline__ RowsItem rows_item(const AttendParams& p, int s, int 
 
 template <int D, int NT>
 struct Cfg {
-  // Two CTAs an SM (kCtasPerSm): 12 warps of 168 registers, or 8 of 255 for more row tiles.
+  // Two CTAs an SM (kCtasPerSm): 12 warps of 168 registers, or 8 of 255 for more row tiles, whose O alone is
+  // 32 registers each at D 128.
   static constexpr int WARPS = NT == 1 ? 6 : 4;
   static constexpr bool Q_SHARED = NT > 2;        // Q's fragments in shared memory, for want of registers
   static constexpr int THREADS = WARPS * 32;
@@ -751,11 +754,17 @@ struct Plan {
 Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int group, int sms) {
   Plan pl{};
   const int64_t rows = static_cast<int64_t>(b.max_new) * group;
+  // The fewest row tiles that hold them: one tile on the kernel for two takes 138 us, not 116 (64 sequences of 6 rows),
+  // 12 rows on four 261, not 152, and 18 on four 90, not 65 (16 sequences).  The other kernel, whose time does not
+  // depend on the rows, takes 101 us where 30 rows of 16 sequences take 88, 319 for 273 of 64, 104 for 107 of 2 of
+  // 60000 keys, but 40 for 46 of 4 of up to 9000.
   pl.tiles = rows > 32;
   pl.row_tiles = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
   const int64_t items = static_cast<int64_t>(b.n_seqs) * c.n_ranks * c.n_kv_heads;
   const int64_t keys = b.max_pages * c.page_size;
-  // Few short items: each by one CTA, no second launch.  Otherwise equal parts.
+  // Few short items: each by one CTA, no second launch.  Otherwise equal parts.  (One token, 8 KV heads over
+  // 200 keys: 8.9 us so, 14.5 in parts; 500: 10.8 and 14.4; 1000: 14.9 and 14.3; 2000: 22.6 and 14.2.  Of 12
+  // sequences of 500: 12.2 and 16.6; 1000: 17.4 and 20.0; 2000: 27.9 and 27.5.)
   pl.per_item = !pl.tiles && items <= sms && keys <= 1024;
   pl.ctas = pl.tiles ? sms : sms * kCtasPerSm;
   if (!pl.per_item) {
