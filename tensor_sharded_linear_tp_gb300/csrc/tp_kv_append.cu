@@ -1,8 +1,8 @@
 // Appending keys and values to the paged 8-bit cache, with the position rotation of Q and K.
 //
-// One launch over every rank.  Its first blocks rotate Q (a warp takes one token and up to four
-// times 32 lanes' worth of its heads); the others each quantise the new tokens of one page for
-// 128 / P of all ranks' KV heads, since a page's tokens share a head's scale:
+// One launch over every rank.  Its first blocks each quantise the new tokens of one page for
+// 128 / P of all ranks' KV heads, since a page's tokens share a head's scale; the others rotate Q (a warp takes one
+// token and up to four times 32 lanes' worth of its heads):
 //     e = max(e_old if the page holds older tokens, least e with max|x| <= 448 * 2^e)
 // A warp holds 16 tokens of a page and head in registers, a page of P tokens is held by P / 16 warps, and
 // the maximum is joined by one warp reduction and, for larger pages, through shared memory: every
@@ -12,9 +12,9 @@
 //
 // What bounds it: the bytes (Q, K and V read once as bf16, Q written, K and V as bytes), and close behind them the
 // instructions: 14 an element of K and V.  A prompt of 4608 tokens, 4 ranks of 12 heads and 12 KV heads of 128
-// (283 MB) takes 76 us, 0.55 of the copy rate (the pages' part 58 us, Q's 21; a warp loads its 16 tokens, waits, and needs
+// (283 MB) takes 67 us, 0.63 of the copy rate (the pages' part 58 us alone, Q's 21; a warp loads its 16 tokens, waits, and needs
 // their maximum before it can write: three CTAs an SM hide part of that).  Small calls are a launch: one token of 4
-// ranks 3.3 us, a batch of 61 3.6 us, 7 chunks of odd lengths (21 MB) 10.2 us, against 3.1 of their bytes.
+// ranks 3.3 us, a batch of 61 3.6 us, 7 chunks of odd lengths (21 MB) 8.5 us, against 3.1 of their bytes.
 //
 // Which sequence and page a block has comes from the device's seq_start without a prefix sum
 // (find_sequence), so that lengths may change between the replays of a graph.
@@ -392,10 +392,13 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_con
   __shared__ Shared sh;
   pdl_launch_dependents();
   pdl_wait();
-  if (static_cast<int>(blockIdx.x) < p.q_blocks)
-    rotate_q<D>(p, static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), threadIdx.x & 31);
+  // The pages first: their blocks take longest, and Q's fill the SMs that they leave.  (Prompt of 4608 tokens: 67 us,
+  // Q first 76, evenly mixed 75.)
+  const int pages = static_cast<int>(gridDim.x) - p.q_blocks, block = static_cast<int>(blockIdx.x);
+  if (block < pages)
+    append_page<D>(p, block, sh);
   else
-    append_page<D>(p, static_cast<int64_t>(blockIdx.x) - p.q_blocks, sh);
+    rotate_q<D>(p, static_cast<int64_t>(block - pages) * kWarps + (threadIdx.x >> 5), threadIdx.x & 31);
 }
 
 // One new token a sequence at most (decoding; 61 sequences 3.6 us, 6.7 by the kernel above, whose blocks are for 16
