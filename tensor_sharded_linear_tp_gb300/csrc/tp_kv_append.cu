@@ -1,14 +1,14 @@
 // Appending keys and values to the paged 8-bit cache, with the position rotation of Q and K.
 //
 // One launch over every rank.  Its first blocks each quantise the new tokens of one page for
-// 128 / P of all ranks' KV heads, since a page's tokens share a head's scale; the others rotate Q (a warp takes one
-// token and up to four times 32 lanes' worth of its heads):
+// 128 / P of all ranks' KV heads, since a page's tokens share a head's scale:
 //     e = max(e_old if the page holds older tokens, least e with max|x| <= 448 * 2^e)
 // A warp holds 16 tokens of a page and head in registers, a page of P tokens is held by P / 16 warps, and
 // the maximum is joined by one warp reduction and, for larger pages, through shared memory: every
 // element is read once and written once.  Only where e grew are the older
 // tokens' codes read and written again, scaled by 2^(e_old - e): exact but for codes that fall
-// among the subnormal ones, since scales are powers of two.
+// among the subnormal ones, since scales are powers of two.  The other blocks rotate Q (a warp takes one
+// token and up to four times 32 lanes' worth of its heads).
 //
 // What bounds it: the bytes (Q, K and V read once as bf16, Q written, K and V as bytes), and close behind them the
 // instructions: 14 an element of K and V.  A prompt of 4608 tokens, 4 ranks of 12 heads and 12 KV heads of 128

@@ -34,12 +34,10 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <mutex>
 
-#include "tp_e4m3.cuh"
 #include "tp_internal.h"
 #include "tp_paged_attention.cuh"
 #include "tp_ptx.cuh"
