@@ -795,9 +795,14 @@ class PagedBatch:
     """The sequences of a step and where their tokens are: tp_paged_batch (include/tp.h) over int32 tensors on the GPU.
 
     seq_start [n_seqs + 1], kv_len [n_seqs] and page_table [n_seqs, max_pages] are read when the
-    kernels run; max_new is at least the new rows of any sequence.  Made once a step, for every layer."""
+    kernels run; max_new (or max_q, its other name: the rows of Q) is at least the new rows of any
+    sequence.  Made once a step, for every layer."""
 
-    def __init__(self, seq_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, max_new: int):
+    def __init__(self, seq_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+                 max_new: int | None = None, max_q: int | None = None):
+        if (max_new is None) == (max_q is None):
+            raise TypeError("one of max_new and max_q, its other name, is needed")
+        max_new = max_q if max_new is None else max_new
         if page_table.dim() != 2:
             raise ValueError(f"page_table must be [n_seqs, max_pages], got {tuple(page_table.shape)}")
         n, max_pages = page_table.shape

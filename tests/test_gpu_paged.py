@@ -771,3 +771,14 @@ def test_binding_refusals():
         tp.tp_kv_append_fp8(qkv, c.heads + 1, k, c.batch)
     with pytest.raises(tp.TPError, match="TP_ERR_INVALID_ARG"):
         tp.tp_kv_append_fp8(qkv, c.heads, k, c.batch, rope="half", cos_sin=torch.ones((9, 20), device=DEV))
+
+
+def test_a_batchs_rows_by_either_name():
+    c = Case([(40, 3), (7, 5)], p=1, n_kv=2, group=2, D=64, page=16, seed=35)
+    q = c.queries()
+    b = c.batch
+    same = tp.PagedBatch(b.seq_start, b.kv_len, b.page_table, max_q=5)
+    assert same.max_new == b.max_new == 5
+    outs = tp.tp_attention_paged_fp8(q, c.cache, same)
+    assert torch.equal(outs[0], tp.tp_attention_paged_fp8(q, c.cache, b)[0])
+    c.check(outs)

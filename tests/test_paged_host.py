@@ -222,3 +222,14 @@ def test_binding_wants_device_tensors():
         tp.PagedBatch(i32[0], i32[0, :1], i32, 1)
     with pytest.raises(ValueError):
         tp.PagedCache([], [], [], [])
+
+
+def test_a_batchs_rows_have_two_names():
+    """max_new and max_q name the same argument; one of them has to be there (the tensors are checked after it)."""
+    i32 = torch.zeros((1, 2), dtype=torch.int32)
+    for kw in (dict(max_new=1), dict(max_q=1)):
+        with pytest.raises(ValueError, match="CUDA"):
+            tp.PagedBatch(i32[0], i32[0, :1], i32, **kw)
+    for args, kw in (((), {}), ((1,), dict(max_q=1)), ((), dict(max_new=1, max_q=1))):
+        with pytest.raises(TypeError, match="max_q"):
+            tp.PagedBatch(i32[0], i32[0, :1], i32, *args, **kw)
