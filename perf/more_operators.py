@@ -157,7 +157,7 @@ def prepare(case, seed):
         starts.append(starts[-1] + new)
     T = starts[-1]
     i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
-    s = dict(case=c, op=c["op"], starts=starts, total=total, T=T, table=table, max_new=max(new for _, new in at),
+    s = dict(case=c, op=c["op"], starts=starts, total=total, T=T, table=table, max_q=max(new for _, new in at),
              seq_start=i32(starts), kv_len=i32(total))
     k = [_pages(g, n_pages, c["kv"], c["page"], c["D"], 1.5) for _ in range(c["p"])]
     v = [_pages(g, n_pages, c["kv"], c["page"], c["D"], 0.8) for _ in range(c["p"])]
@@ -173,7 +173,7 @@ def prepare(case, seed):
     if own:
         import tensor_sharded_linear_tp_gb300 as tp
         s["cache"] = tp.PagedCache(s["k"], s["v"], s["ks"], s["vs"])
-        s["batch"] = tp.PagedBatch(s["seq_start"], s["kv_len"], table, max_new=s["max_new"])
+        s["batch"] = tp.PagedBatch(s["seq_start"], s["kv_len"], table, max_q=s["max_q"])
         if c["op"] == "attend":
             need = tp.tp_attention_paged_workspace_bytes(s["cache"], s["batch"], T, c["heads"])
             s["workspace"] = torch.empty(need, dtype=torch.uint8, device=DEV)
