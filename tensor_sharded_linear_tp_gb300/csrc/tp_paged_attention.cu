@@ -148,7 +148,7 @@ __device__ __forceinline__ uint32_t chunk_at(int key, int c) {
   return static_cast<uint32_t>(key * D + ((c ^ (D == 128 ? key & 7 : (key >> 1) & 3)) << 4));
 }
 
-constexpr uint32_t kPageSeen = 0x10000;   // in a page's info, above its K and V scale bytes: its index is valid
+constexpr uint32_t kPageSeen = 0x10000;   // in a page's info, above its K and V scale bytes: some row sees it, and its index is valid
 
 // The steps of a warp's part in the order they are loaded, ahead of the one that is worked on.
 struct Loader {
@@ -178,13 +178,16 @@ __device__ __forceinline__ void load_pages(const AttendParams& p, Loader& ld, in
   const int64_t at = static_cast<int64_t>(first) + lane;
   ld.my_info = 0;
   ld.my_page = 0;
-  if ((at << p.b.page_shift) < ld.len) {
+  // A page before every row's window may be gone, or another sequence's by now: its codes and scales take no part.
+  // (The window's first key is read again here, once for 32 pages: kept by the loader, it would spill.)
+  const int lo = p.window > 0 ? seq_view(p.b, ld.s).pos0 - p.window + 1 : 0;
+  if ((at << p.b.page_shift) < ld.len && ((at + 1) << p.b.page_shift) > lo) {
     ld.my_page = p.b.page_table[ld.s * p.b.ld_table + at];
     if (ld.my_page >= 0 && ld.my_page < p.b.n_pages) {
       const int64_t sc = static_cast<int64_t>(ld.my_page) * p.ld_scales + ld.head;
       ld.my_info = kPageSeen | p.ks[ld.rank][sc] | (static_cast<uint32_t>(p.vs[ld.rank][sc]) << 8);
-    } else if (p.window == 0 || ((at + 1) << p.b.page_shift) > seq_view(p.b, ld.s).pos0 - p.window + 1) {
-      bad_index(p.b);      // (a page before every row's window may be gone)
+    } else {
+      bad_index(p.b);
     }
   }
 }
@@ -230,7 +233,7 @@ __device__ __forceinline__ void issue_step(const AttendParams& p, Loader& ld, in
     const int src = page - ld.page0 + (two ? i : 0), key = key0 + 16 * i;
     const uint32_t info = __shfl_sync(0xffffffffu, ld.my_info, src);
     const int at = __shfl_sync(0xffffffffu, ld.my_page, src);
-    // (A page that is not there: zeros, nothing is read.)
+    // (A page that is not there, or that no row sees: zeros, nothing is read.)
     const uint32_t size = (info & kPageSeen) != 0 ? 16 : 0;
     const int64_t off = at * p.ld_page + (static_cast<int64_t>(ld.head) * p.b.page_size + (key & (p.b.page_size - 1)) + row) * D + chunk * 16;
     const uint8_t* none = reinterpret_cast<const uint8_t*>(p.q[0]);

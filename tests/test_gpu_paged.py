@@ -782,3 +782,35 @@ def test_a_batchs_rows_by_either_name():
     outs = tp.tp_attention_paged_fp8(q, c.cache, same)
     assert torch.equal(outs[0], tp.tp_attention_paged_fp8(q, c.cache, b)[0])
     c.check(outs)
+
+
+STALE = {"nan codes": (127, 0x7F), "a larger scale": (167, None), "the largest scale": (254, None), "a nan page": (255, 0xFF)}
+
+
+def stale_pages(c, content, window):
+    """c's batch with every table entry before all of a sequence's windows naming a page that holds something else."""
+    z = sorted(set(range(c.n_pages)) - {p for s, (_, _, n) in enumerate(c.seqs) for p in c.table[s, :-(-n // c.page)]})[0]
+    byte, code = STALE[content]
+    for r in range(c.p):
+        c.scales[r][:, z] = byte
+        if code is not None:
+            c.codes[r][:, z] = code
+    c.upload()
+    table = c.table.copy()
+    for s, (_, n, length) in enumerate(c.seqs):
+        table[s, :max(length - n - window + 1, 0) // c.page] = z
+    return tp.PagedBatch(c.batch.seq_start, c.batch.kv_len, i32(table.tolist()), c.batch.max_new)
+
+
+WINDOW_STARTS = [(600 + 16 * i + 3) for i in range(8)]     # in each 16 keys of a step of 128
+
+
+@pytest.mark.parametrize("content", STALE)
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("D, new", [(128, 1), (64, 1), (128, 4), (64, 10)])
+def test_few_rows_pages_before_every_window_may_hold_anything(D, new, page, content):
+    c = Case([(old, new) for old in WINDOW_STARTS], p=1, n_kv=2, group=3, D=D, page=page, seed=page + new)
+    batch = stale_pages(c, content, 200)
+    outs = tp.tp_attention_paged_fp8(c.queries(), c.cache, batch, window=200)
+    tp.tp_device_status()
+    c.check(outs, window=200)
