@@ -58,7 +58,7 @@ struct Item {
   SeqView v;
   int row0, rows;
   int tile0, tiles;     // steps tile0 .. tile0 + tiles of the sequence's keys
-  int key_end;          // keys from here on are not seen by any row
+  int key_lo, key_end;  // some row sees key_lo; none sees an earlier key, nor one from key_end on
 };
 
 template <int ROWS, int STEP>
@@ -69,8 +69,8 @@ __device__ __forceinline__ Item item_of(const AttendParams& p, const SeqView& v,
   it.rows = static_cast<int>(min(static_cast<int64_t>(ROWS), static_cast<int64_t>(v.n) * p.group - it.row0));
   const int first = p.by_group(it.row0), last = p.by_group(it.row0 + max(it.rows, 1) - 1);
   it.key_end = p.causal ? max(min(static_cast<int64_t>(v.len), static_cast<int64_t>(v.pos0) + last + 1), int64_t(0)) : v.len;
-  const int64_t lo = p.window > 0 ? max(static_cast<int64_t>(v.pos0) + first - p.window + 1, int64_t(0)) : 0;
-  it.tile0 = static_cast<int>(min(lo, static_cast<int64_t>(it.key_end))) / STEP;
+  it.key_lo = p.window > 0 ? static_cast<int>(max(static_cast<int64_t>(v.pos0) + first - p.window + 1, int64_t(0))) : 0;
+  it.tile0 = min(it.key_lo, it.key_end) / STEP;
   it.tiles = it.rows > 0 ? max(1, (it.key_end + STEP - 1) / STEP - it.tile0) : 0;   // (a row without keys is an item too)
   return it;
 }

@@ -63,7 +63,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // A step's pages, by 16 keys.
 struct alignas(16) Info {
   int e_k, e_v;            // exponents that the step's K and V are relative to
-  uint32_t unseen, nan;    // bits: the page is out of bounds; K or V is NaN
+  uint32_t unseen, nan;    // bits: the page is out of bounds, or before every row's window; K or V is NaN
   uint32_t by[2][8];       // what K's and V's codes are multiplied with, as fp16 twice; kZero where they enter as 0
   int keys;                // of the step's keys, those that some row sees; the others enter as 0
 };
@@ -74,7 +74,8 @@ struct PieceInfo {
   int s, h;               // sequence; rank and KV head
   int a, len, pos0;       // SeqView
   int row0, rows;         // the item's rows
-  int key_end, from, n;
+  int key_lo, key_end;    // some row sees key_lo; none sees an earlier key, nor one from key_end on
+  int from, n;
   int first, last;        // does it hold the item's first and last step
 
   // Turns of the two streams: with both on the same rows (split) turn u is step u, else step u / 2; stream u % 2.
@@ -195,7 +196,7 @@ __device__ __forceinline__ void hand_out_pieces(const AttendParams& p, TilesCtrl
     if (more) {
       const Item it = item_of<kRows, kKeys>(p, v, block);
       const int left = it.tile0 + it.tiles - from, n = static_cast<int>(min(static_cast<int64_t>(left), u1 - at));
-      out = PieceInfo{s, h, v.a, v.len, v.pos0, it.row0, it.rows, it.key_end, from, n, from == it.tile0, n == left};
+      out = PieceInfo{s, h, v.a, v.len, v.pos0, it.row0, it.rows, it.key_lo, it.key_end, from, n, from == it.tile0, n == left};
       at += n;
       if (out.first && !out.last) {
         const int64_t c_last = Cuts(total, n_cta).part(at + left - n - 1);
@@ -357,14 +358,16 @@ __device__ __forceinline__ void load_pages(const AttendParams& p, Pages& pg, con
   pg.page = 0;
   pg.info = 0;
   const int64_t at = static_cast<int64_t>(first) + lane;
-  if ((at << p.b.page_shift) < w.len) {
+  // (The pages before every row's window may be gone, or have become another sequence's.  What is left out here no later
+  // item of the sequence needs: their windows begin further on.)
+  if ((at << p.b.page_shift) < w.len && ((at + 1) << p.b.page_shift) > w.key_lo) {
     pg.page = p.b.page_table[w.s * p.b.ld_table + at];
     if (pg.page >= 0 && pg.page < p.b.n_pages) {
       const int rank = p.by_kv(w.h), head = w.h - rank * p.n_kv;
       const int64_t sc = static_cast<int64_t>(pg.page) * p.ld_scales + head;
       pg.info = kSeen | p.ks[rank][sc] | (static_cast<uint32_t>(p.vs[rank][sc]) << 8);
-    } else if (p.window == 0 || ((at + 1) << p.b.page_shift) > w.pos0 + p.by_group(w.row0) - p.window + 1) {
-      bad_index(p.b);      // (a page before every row's window may be gone)
+    } else {
+      bad_index(p.b);
     }
   }
 }
@@ -417,7 +420,8 @@ __device__ __forceinline__ void pages_way(const AttendParams& p, const CodeMaps&
       const int key16 = key0 + 16 * (lane & 7);
       const uint32_t mine = __shfl_sync(0xffffffffu, pg.info, (key16 >> shift) - pg.page0);
       const uint32_t kb = mine & 0xFFu, vb = (mine >> 8) & 0xFFu;
-      const bool seen = (mine & kSeen) != 0, nan = seen && (kb == 255u || vb == 255u);
+      // (A page that an item before this one saw may lie before this one's windows.)
+      const bool seen = (mine & kSeen) != 0 && ((key16 >> shift) + 1) << shift > w.key_lo, nan = seen && (kb == 255u || vb == 255u);
       const uint32_t unseen = __ballot_sync(0xffffffffu, !seen && key16 < w.len) & 0xFFu;   // (behind the last key nothing is seen anyway)
       const uint32_t nans = __ballot_sync(0xffffffffu, nan) & 0xFFu;
       const int e_k = __reduce_max_sync(0xffffffffu, seen && !nan ? static_cast<int>(kb) - 127 : -127);
@@ -426,7 +430,7 @@ __device__ __forceinline__ void pages_way(const AttendParams& p, const CodeMaps&
       const int key_box = key0 + box_keys * (lane & (boxes - 1));
       const uint32_t box_info = __shfl_sync(0xffffffffu, pg.info, (key_box >> shift) - pg.page0);
       const int box_page = __shfl_sync(0xffffffffu, pg.page, (key_box >> shift) - pg.page0);
-      const bool load = lane < boxes && (box_info & kSeen) != 0 && key_box < w.key_end;
+      const bool load = lane < boxes && (box_info & kSeen) != 0 && key_box < w.key_end && ((key_box >> shift) + 1) << shift > w.key_lo;
       const int n_boxes = __popc(__ballot_sync(0xffffffffu, load));
       // (V's codes of step t - 3 have been taken, so V of step t - 4 is stored, P.V of step t - 6 done and
       // with it everything that reads that step's Info.)

@@ -814,3 +814,15 @@ def test_few_rows_pages_before_every_window_may_hold_anything(D, new, page, cont
     outs = tp.tp_attention_paged_fp8(c.queries(), c.cache, batch, window=200)
     tp.tp_device_status()
     c.check(outs, window=200)
+
+
+@pytest.mark.parametrize("content", STALE)
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("D, new", [(128, 20), (64, 20), (128, 100), (64, 200)])
+def test_many_rows_pages_before_every_window_may_hold_anything(D, new, page, content):
+    """Items of up to 128 and of 256 rows; several items of a sequence, whose windows begin in different pages."""
+    c = Case([(old, new) for old in WINDOW_STARTS], p=1, n_kv=2, group=3, D=D, page=page, seed=page + new)
+    batch = stale_pages(c, content, 200)
+    outs = tp.tp_attention_paged_fp8(c.queries(), c.cache, batch, window=200)
+    tp.tp_device_status()
+    c.check(outs, window=200)
