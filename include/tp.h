@@ -724,10 +724,13 @@ TP_API tp_status tp_kv_append_fp8(const tp_paged_cache* cache, const tp_paged_ba
  * workspace: device buffer of tp_attention_paged_workspace_bytes(...) bytes,
  *       16-byte aligned, owned by the caller, of any content.  Calls that share one must not
  *       overlap on the GPU.
- * Codes and Q enter the tensor cores as fp16, scaled by powers of two: exactly
- * but for what lies 2^-39 below the largest element of a row of Q or 2^-40 below the
- * largest page scale in use.  Products, softmax and sums are fp32, the probabilities
- * enter P.V as fp16 (2^-11 relative, an eighth of the output's own 2^-8).  A
+ * Codes and Q enter the tensor cores as fp16, scaled by powers of two.  Of a row of Q, what lies 2^-39 below its
+ * largest element is lost.  With up to 32 rows a KV head (max_new * n_heads / n_kv_heads) K enters exactly, and a key's
+ * probability times value is off by at most 2^-30 of the largest V scale met so far.  With more rows K enters relative to
+ * the largest K scale among 128 keys and V to the largest V scale so far, those of keys that a row does not see
+ * among them: an element is off by at most 2^-32 of that scale, a page whose scale is 2^32 or more below it enters as
+ * 0, and a probability is off by 2^-31 of the row's largest.  Products, softmax and sums are fp32, the probabilities
+ * enter P.V as fp16 (besides the above 2^-11 relative, an eighth of the output's own 2^-8).  A
  * page whose K or V is NaN (scale byte 255, as tp_kv_append_fp8 leaves it) makes the rows that see
  * it NaN and no others; NaN codes in a page with another scale byte may make any row of
  * the sequence NaN.  The same call gives the same bits every time.

@@ -26,10 +26,12 @@
 //
 // Numbers: Q enters as fp16, each row times a power of two to below 2^15 (what that loses lies 2^-39
 // below its largest element).  K's codes enter times 2^(e - E + 7), E the largest exponent of the step's pages,
-// V's likewise with E the largest so far: at most 448 * 2^7 < 65504, and what is 2^-40 below the largest is
-// lost.  P = 2^(s - m + 6) with the running maximum m raised only where a row exceeds it by more than 9, so P
-// is at most 2^15 and what is 2^-31 below the largest is lost; l sums the unrounded P, O stays in units of
-// 2^(E - 7).
+// V's likewise with E the largest so far: at most 448 * 2^7 < 65504, and off by at most half of fp16's least step, 2^-25 in
+// units of 2^(E - 7), so 2^(E - 32); but from e = E - 32 down the factor itself is 0 and with it the page, which is at
+// most 448 * 2^(E - 32).  (Factors in two parts would keep those pages: the codes' warps have no registers left for them,
+// and a prompt of 4608 tokens took 340 us, not 331.)  P = 2^(s - m + 6) with the running maximum m raised only
+// where a row exceeds it by more than 9, so P is at most 2^15 and what is 2^-31 below the largest is lost; l sums the
+// unrounded P, O stays in units of 2^(E - 7).
 //
 // What bounds it: at 256 rows a key costs 2 D bytes of the cache, 4 D 256 FLOP and 256 exponentials; a step's
 // products take 2048 cycles of the tensor core, its exponentials 1024 of an SM's rate, and measured it takes

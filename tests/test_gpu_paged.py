@@ -826,3 +826,39 @@ def test_many_rows_pages_before_every_window_may_hold_anything(D, new, page, con
     outs = tp.tp_attention_paged_fp8(c.queries(), c.cache, batch, window=200)
     tp.tp_device_status()
     c.check(outs, window=200)
+
+
+@pytest.mark.parametrize("gap", [20, 24, 30, 32, 34, 38, 45, 80])
+@pytest.mark.parametrize("D, group, new", [(128, 2, 40), (64, 8, 40), (128, 1, 24), (64, 1, 30)])
+def test_rows_that_see_only_a_page_of_small_scale(D, group, new, gap):
+    """The first page's scales 2^-gap of the next one's, which its own rows do not see.  Many rows: an element of K or V
+    is off by at most 2^-32 of the largest scale of a step, half the least step of fp16 in units of 2^-7 of it, and from a
+    gap of 32 on the page enters as 0.  Few rows: a probability is off by 2^-25 in units of 2^(E_v - 14), times a code
+    of up to 448, so a key by 2^-30 of V's largest."""
+    c = Case([(0, new)], p=1, n_kv=2, group=group, D=D, page=16, seed=gap)
+    few = new * group <= 32
+    big = {0: 147, 1: 137}                       # the other pages' bytes: K 2^20, V 2^10
+    for which in (0, 1):
+        c.scales[0][which] = big[which]
+        c.scales[0][which, c.table[0, 0]] = big[which] - gap
+    c.upload()
+    q = np.zeros((c.T, c.heads, D))              # (one element each, so that scores of that page are about 1)
+    q[np.arange(c.T)[:, None], np.arange(c.heads)[None, :], c.rng.integers(0, D, (c.T, c.heads))] = 2.0 ** min(gap - 25, 9)
+    c.q = [to_bf16(q.reshape(c.T, -1))]
+    out = f64(tp.tp_attention_paged_fp8(c.q, c.cache, c.batch)[0]).reshape(c.T, c.heads, D)[:16]
+    q = f64(c.q[0]).reshape(c.T, c.heads, D)[:16]
+    K, V = (P.values(c.codes[0][i], c.scales[0][i], c.table[0], 16) for i in (0, 1))
+    see = P.seen(16, 16)
+    want, w = P.attention(q, K, V, D ** -0.5, see)
+    bound = attention_bound(q, K, V, D ** -0.5, want, w, see)
+    off = [2.0 ** (big[i] - 127 - 32) if gap < 32 else np.abs(x).max() for i, x in ((0, K), (1, V))]
+    d = 1.01 * D ** -0.5 * np.abs(q).sum(axis=2) * off[0]                                # of a score [16, heads]
+    for h in range(c.heads):
+        g = h // group
+        if few:
+            err = np.arange(1, 17)[:, None] * 2.0 ** (big[1] - 127 - 30)
+        else:
+            err = np.expm1(2 * d[:, h])[:, None] * (w[h] @ np.abs(V[g])) + off[1]
+        bound[:, h] += (1 + 2.0 ** -8) * err
+    bad = ~(np.abs(out - want) <= bound)
+    assert not bad.any(), (np.argwhere(bad)[:5], out[bad][:5], want[bad][:5], bound[bad][:5])
