@@ -729,7 +729,8 @@ TP_API tp_status tp_kv_append_fp8(const tp_paged_cache* cache, const tp_paged_ba
  * probability times value is off by at most 2^-30 of the largest V scale met so far.  With more rows K enters relative to
  * the largest K scale among 128 keys and V to the largest V scale so far, those of keys that a row does not see
  * among them: an element is off by at most 2^-32 of that scale, a page whose scale is 2^32 or more below it enters as
- * 0, and a probability is off by 2^-31 of the row's largest.  Products, softmax and sums are fp32, the probabilities
+ * 0, and a probability is off by 2^-31 of the row's largest.  Products, softmax and sums are fp32 (in the tensor core
+ * without rounding to nearest, in pieces of at most 2^19 keys), the probabilities
  * enter P.V as fp16 (besides the above 2^-11 relative, an eighth of the output's own 2^-8).  A
  * page whose K or V is NaN (scale byte 255, as tp_kv_append_fp8 leaves it) makes the rows that see
  * it NaN and no others; NaN codes in a page with another scale byte may make any row of

@@ -47,6 +47,7 @@ namespace {
 
 constexpr int kStep = 32;                         // keys of a step
 constexpr int kCtasPerSm = 2;
+constexpr int kMaxSteps = kLongestPiece / kStep;  // of a piece
 
 // A piece of an item in shared memory.
 struct Piece {
@@ -524,6 +525,32 @@ __device__ __forceinline__ void end_piece(const AttendParams& p, const RowsItem&
     }
 }
 
+// Joins two pieces of an item, the second of which continues the first: to the output where `to` is NULL, else to `to`, which may be
+// the first.  (A small rolled loop: only items of more than kMaxSteps steps in a warp come here.)  Warp-collective.
+template <int D, int NT>
+__device__ __forceinline__ void join_two(const AttendParams& p, const RowsItem& it, const float* a, const float* b, float* to, int lane) {
+  using C = Cfg<D, NT>;
+  auto ml = [&](const float* piece, int row) { return *reinterpret_cast<const float2*>(piece + C::ROWS * D + 2 * row); };
+  __syncwarp();
+#pragma unroll 1
+  for (int i = lane * 4; i < C::ROWS * D; i += 128) {
+    const int row = i / D;
+    const Joined j = join_pieces(0, 1, 2, [&](int k) { return ml(k == 0 ? a : b, row); },
+                                 [&](int k) { return *reinterpret_cast<const float4*>((k == 0 ? a : b) + i); });
+    const float inv = j.l == 0.0f ? 0.0f : 1.0f / j.l;
+    const float4 o = make_float4(j.o.x * inv, j.o.y * inv, j.o.z * inv, j.o.w * inv);
+    if (to != nullptr) *reinterpret_cast<float4*>(to + i) = o;
+    else if (row < it.rows) store_row4(p, it.a, it.h, row, i - row * D, D, o);
+  }
+  __syncwarp();
+  if (to != nullptr && lane < C::ROWS) {
+    const float2 x = ml(a, lane), y = ml(b, lane);
+    const float m = fmaxf(x.x, y.x), ref = m == -INFINITY ? 0.0f : m;
+    *reinterpret_cast<float2*>(to + C::ROWS * D + 2 * lane) = make_float2(m, x.y * ex2(x.x - ref) + y.y * ex2(y.x - ref));
+  }
+  __syncwarp();
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, kCtasPerSm) paged_rows_kernel(const __grid_constant__ AttendParams p) {
   using C = Cfg<D, NT>;
@@ -532,7 +559,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, kCtasPerSm) paged_rows_ke
   auto* ctl = reinterpret_cast<Ctrl<C::WARPS, C::STAGES>*>(base + C::OFF_CTRL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = ptx::smem_addr(base) + warp * C::OWN, q_at = ring + C::OFF_Q;
-  float* early_piece = p.early + (static_cast<int64_t>(blockIdx.x) * C::WARPS + warp) * (C::PIECE / 4);
   pdl_launch_dependents();
   if (lane == 0) ctl->piece[warp][0].valid = ctl->piece[warp][1].valid = 0;
   __syncwarp();
@@ -617,18 +643,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, kCtasPerSm) paged_rows_ke
     ld.s = my.s, ld.h = my.h - 1;      // (the first step begins an item for it)
     int stage = 0, tile = my.tile, from = 0;
     uint32_t items = 0;
-    bool begin = true;
+    enum { kNothing, kItem, kSameItem } begin = kItem;     // what begins: another item, or another piece of the item
     RowsItem it{};
     State<D, NT> st;
 #pragma unroll 1
     for (int k = -C::STAGES; k < count; ++k) {
       if (k >= 0) {
-        if (begin) {
-          it = ctl->item[warp][items % Ctrl<C::WARPS, C::STAGES>::ITEMS];
-          if (items > 0) tile = it.tile0;
-          ++items;
-          from = tile;
-          begin = false;
+        if (begin != kNothing) {
+          if (begin == kItem) {
+            it = ctl->item[warp][items % Ctrl<C::WARPS, C::STAGES>::ITEMS];
+            if (items > 0) tile = it.tile0;
+            ++items;
+            from = tile;
+          }
+          begin = kNothing;
           load_item<D, NT>(p, it, st, q_at, lane);
         }
         copies_wait<C::STAGES - 1>();
@@ -638,14 +666,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::THREADS, kCtasPerSm) paged_rows_ke
         ++tile;
         __syncwarp();   // every lane has read the stage
         const int end = it.tile0 + it.tiles;
-        if (tile == end || k + 1 == count) {
+        const bool go_on = tile != end && k + 1 != count;
+        if (!go_on || (tile - from) % kMaxSteps == 0) {
           const bool first = from == it.tile0, last = tile == end, whole = first && last;
           // A piece that the warp's part cuts: its first (0) or its last (1).
           const int place = first ? 1 : 0, early = k + 1 < count;
-          end_piece<D, NT>(p, it, st, whole, early ? early_piece : reinterpret_cast<float*>(base + warp * C::OWN), lane);
-          if (!whole && lane == 0)
+          const int64_t my_piece = static_cast<int64_t>(blockIdx.x) * C::WARPS + warp;
+          float *carry = p.carry + my_piece * 2 * (C::PIECE / 4), *early_piece = p.early + my_piece * (C::PIECE / 4);
+          float* to = go_on ? carry : early ? early_piece : reinterpret_cast<float*>(base + warp * C::OWN);
+          const bool cont = tile - from > kMaxSteps;     // another piece of the item, in `carry`, was before
+          end_piece<D, NT>(p, it, st, whole && !cont, cont ? carry + C::PIECE / 4 : to, lane);
+          if (cont) join_two<D, NT>(p, it, carry, carry + C::PIECE / 4, whole ? nullptr : to, lane);
+          if (!whole && !go_on && lane == 0)
             ctl->piece[warp][place] = Piece{my.at + k + 1 + (end - tile), 1, first, last, early, it.s, it.h, it.a, it.rows};
-          begin = true;
+          begin = go_on ? kSameItem : kItem;
         }
       }
       if (k + C::STAGES < count) issue_step<D, NT>(p, ld, stage, ring, ctl, my.tile, warp, lane);
@@ -749,7 +783,9 @@ struct Plan {
   int row_tiles;         // of 8 rows, else
   bool per_item;         // a CTA an item, no second launch; else equal parts of all steps
   int ctas;              // of those parts
+  int pieces;            // that a CTA leaves behind (AttendParams::early)
   size_t part_bytes, ws_bytes;
+  bool carry;            // an item may be longer than a piece: workspace to go on from
 };
 
 Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int group, int sms) {
@@ -769,11 +805,14 @@ Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int group, int 
   pl.per_item = !pl.tiles && items <= sms && keys <= 1024;
   pl.ctas = pl.tiles ? sms : sms * kCtasPerSm;
   if (!pl.per_item) {
-    // A CTA's Join, its two partial items and (paged_rows_kernel) a piece of each warp.
+    // A CTA's Join, its two partial items and (paged_rows_kernel) a piece of each warp; where there can be longer items
+    // than a piece is, a piece to go on from (paged_rows_kernel: of each warp, and its next one).
     pl.part_bytes = pl.tiles ? paged_tiles_part_floats(c.head_dim) * 4
                              : static_cast<size_t>(8 * pl.row_tiles) * (c.head_dim + 2) * 4;
-    const int pieces = pl.tiles ? 0 : pl.row_tiles == 1 ? Cfg<128, 1>::WARPS : Cfg<128, 2>::WARPS;
-    pl.ws_bytes = static_cast<size_t>(pl.ctas) * ((2 + pieces) * pl.part_bytes + sizeof(Join));
+    pl.pieces = pl.tiles ? 0 : pl.row_tiles == 1 ? Cfg<128, 1>::WARPS : Cfg<128, 2>::WARPS;
+    pl.carry = keys > kLongestPiece;
+    const int carried = !pl.carry ? 0 : pl.tiles ? 1 : 2 * pl.pieces;
+    pl.ws_bytes = static_cast<size_t>(pl.ctas) * ((2 + pl.pieces + carried) * pl.part_bytes + sizeof(Join));
   }
   return pl;
 }
@@ -908,6 +947,7 @@ tp_status tp_attention_paged_fp8(const tp_paged_cache* cache, const tp_paged_bat
       p.joins = static_cast<Join*>(workspace);
       p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.ctas * sizeof(Join));
       p.early = reinterpret_cast<float*>(reinterpret_cast<char*>(p.parts) + 2 * pl.ctas * pl.part_bytes);
+      p.carry = reinterpret_cast<float*>(reinterpret_cast<char*>(p.early) + static_cast<size_t>(pl.ctas) * pl.pieces * pl.part_bytes);
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (pl.tiles) {

@@ -43,6 +43,7 @@ struct AttendParams {
   int per_item;                // 1: a CTA takes one item whole; 0: equal parts of all steps
   float* parts;                // workspace: two partial items a CTA, O and then (m, l) of each row
   float* early;                // workspace (paged_rows_kernel): a piece of each warp that it leaves behind
+  float* carry;                // workspace: the piece that another one continues, of a CTA (paged_rows_kernel: of a warp, and the other)
   Join* joins;                 // workspace: the item that begins in a CTA and goes beyond it
   const __nv_bfloat16* q[TP_MAX_DEGREE];
   __nv_bfloat16* out[TP_MAX_DEGREE];
@@ -52,6 +53,12 @@ struct AttendParams {
 struct CodeMaps {
   CUtensorMap k[TP_MAX_DEGREE], v[TP_MAX_DEGREE];
 };
+
+// The keys of a piece, at most.  The tensor core's accumulators are fp32, but what a product has below the sum's last
+// places is cut off, not rounded, so that a long sum falls short: by 0.05 % over 2^19 keys of equal weight (measured,
+// either kernel), 0.1 % over 2^20, 0.3 over 2^21, 0.7 over 2^22, 2 over 2^23, and from some 2^26 on nothing is added any
+// more.  Pieces are joined by sums that round.
+constexpr int kLongestPiece = 1 << 19;
 
 // One item: rows [row0, row0 + rows) of a sequence's n * group rows (token by token), and its steps.
 struct Item {

@@ -60,6 +60,7 @@ constexpr int kRows = 256;                        // rows of an item
 constexpr int kInfos = 8;                         // steps whose Info is kept: seven are in use (see pages_way)
 constexpr float kBias = 6.0f, kSlack = 9.0f;     // P = 2^(s - m + kBias), m raised by scores above m + kSlack
 constexpr uint32_t SUB = 16384;                   // 128 rows x 64 fp16, 128-byte swizzled
+constexpr int kMaxSteps = kLongestPiece / kKeys;  // of a piece
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // A step's pages, by 16 keys.
@@ -78,7 +79,8 @@ struct PieceInfo {
   int row0, rows;         // the item's rows
   int key_lo, key_end;    // some row sees key_lo; none sees an earlier key, nor one from key_end on
   int from, n;
-  int first, last;        // does it hold the item's first and last step
+  int first, last;        // does it, with what it continues, hold the item's first step; does it hold the last one
+  int cont, cut;          // it continues the piece before, and is continued by the next, for kMaxSteps: through p.carry
 
   // Turns of the two streams: with both on the same rows (split) turn u is step u, else step u / 2; stream u % 2.
   __device__ __forceinline__ bool split() const { return rows <= 128; }
@@ -188,6 +190,7 @@ template <int D>
 __device__ __forceinline__ void hand_out_pieces(const AttendParams& p, TilesCtrl* ctl, int64_t u0, int64_t u1, int64_t total, int64_t n_cta, int lane) {
   int s = ctl->start.s, h = ctl->start.h, block = ctl->start.block, from = ctl->start.tile;
   int64_t at = u0;
+  bool first = false, cont = false;
   Join join{};
   SeqView v{0, 0, 0, 0};
   if (u1 > u0) v = seq_view(p.b, s);
@@ -197,10 +200,13 @@ __device__ __forceinline__ void hand_out_pieces(const AttendParams& p, TilesCtrl
     PieceInfo out{};
     if (more) {
       const Item it = item_of<kRows, kKeys>(p, v, block);
-      const int left = it.tile0 + it.tiles - from, n = static_cast<int>(min(static_cast<int64_t>(left), u1 - at));
-      out = PieceInfo{s, h, v.a, v.len, v.pos0, it.row0, it.rows, it.key_lo, it.key_end, from, n, from == it.tile0, n == left};
+      const int left = it.tile0 + it.tiles - from, most = static_cast<int>(min(static_cast<int64_t>(left), u1 - at)), n = min(most, kMaxSteps);
+      if (!cont) first = from == it.tile0;
+      out = PieceInfo{s, h, v.a, v.len, v.pos0, it.row0, it.rows, it.key_lo, it.key_end, from, n, first, n == left, cont, n < most};
       at += n;
-      if (out.first && !out.last) {
+      cont = n < most;
+      from += n;
+      if (first && n == most && n < left) {
         const int64_t c_last = Cuts(total, n_cta).part(at + left - n - 1);
         join = Join{static_cast<int>(c_last - blockIdx.x) + 1, v.a, it.row0, it.rows, h, {}};
       }
@@ -219,7 +225,7 @@ __device__ __forceinline__ void hand_out_pieces(const AttendParams& p, TilesCtrl
       asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
       if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
     }
-    if (at < u1) {
+    if (at < u1 && !cont) {
       if (static_cast<int64_t>(++block) * kRows >= static_cast<int64_t>(v.n) * p.group) {
         block = 0;
         if (++h == p.heads) {
@@ -867,7 +873,7 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
     }
     base += n;
     // O of this stream (and where both have the same rows of the other one) is complete.
-    const bool whole = w.first && w.last;
+    const bool whole = w.first && w.last, cont = w.cont;
     const int n_streams = split ? min(turns, 2) : 1;
     if (split && g == 1) {
       ml[lane_row][0] = st.m;
@@ -897,10 +903,21 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
         w0 = ex2(st.m - ref), w1 = ex2(m1 - ref);
         l = st.l * w0 + l1 * w1;
       }
-      const float inv = l == 0.0f ? 0.0f : 0x1p-7f / l;
-      w0 *= inv, w1 *= inv;
       constexpr int PART = kRows * (D + 2);
-      float* part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (w.first ? 1 : 0)) * PART;
+      float* carry = p.carry + static_cast<int64_t>(blockIdx.x) * PART;
+      float f2 = 0.0f;      // of the piece that this one continues, an O / l
+      if (cont && row < w.rows) {
+        const float2 c = *reinterpret_cast<const float2*>(carry + kRows * D + 2 * row);
+        const float m1 = m;
+        m = fmaxf(m1, c.x);
+        const float ref = m == -INFINITY ? 0.0f : m, by = ex2(m1 - ref);
+        f2 = c.y * ex2(c.x - ref);
+        w0 *= by, w1 *= by;
+        l = l * by + f2;
+      }
+      const float inv = l == 0.0f ? 0.0f : 0x1p-7f / l;
+      w0 *= inv, w1 *= inv, f2 *= inv * 0x1p7f;
+      float* part = w.cut ? carry : p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (w.first ? 1 : 0)) * PART;
       char* to = whole ? reinterpret_cast<char*>(p.out[rank]) : reinterpret_cast<char*>(part);
       const int64_t offset = token < 0 ? -1 : whole ? (token * p.ldo + column) * 2 : static_cast<int64_t>(row) * D * 4;
       // (Q's tile is idle: every S of this piece is done.)
@@ -920,6 +937,13 @@ __device__ __forceinline__ void softmax_rows(const AttendParams& p, TilesCtrl* c
           ptx::tmem_ld_wait();
 #pragma unroll
           for (int t = 0; t < 16; ++t) o[t] += __uint_as_float(v[t]) * f1;
+        }
+        if (cont && row < w.rows) {
+#pragma unroll
+          for (int t = 0; t < 16; t += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(carry + row * D + col + t);
+            o[t] += c.x * f2, o[t + 1] += c.y * f2, o[t + 2] += c.z * f2, o[t + 3] += c.w * f2;
+          }
         }
         const int at = col & (per - 1);
         const uint32_t line = stage + lane * 128;

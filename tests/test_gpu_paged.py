@@ -862,3 +862,62 @@ def test_rows_that_see_only_a_page_of_small_scale(D, group, new, gap):
         bound[:, h] += (1 + 2.0 ** -8) * err
     bad = ~(np.abs(out - want) <= bound)
     assert not bad.any(), (np.argwhere(bad)[:5], out[bad][:5], want[bad][:5], bound[bad][:5])
+
+
+@pytest.mark.parametrize("rows, D, keys", [(1, 128, 2 ** 21 + 77), (12, 64, 2 ** 21 + 77), (20, 128, 2 ** 21 + 77), (32, 128, 2 ** 21 + 77),
+                                           (100, 64, 2 ** 21 + 77), (300, 128, 2 ** 21 + 77), (1, 64, 2 ** 23), (256, 64, 2 ** 23)])
+def test_millions_of_keys(rows, D, keys):
+    """Sums over more keys than a piece has: a warp (up to 32 rows) or a CTA has whole sequences, of a few pages again
+    and again, so that the oracle needs only their tokens and how often they occur.  Later pages have larger scales.
+
+    A piece of 2^19 keys adds 2^15 times to its accumulators, each time without rounding to nearest (2^-22 of the sum); V
+    is positive, so that this is 2^-7 of the output."""
+    few = rows <= 32
+    p, n_kv = (16, 114) if few else (4, 38)
+    page, pool, pages = 128, 16, -(-keys // 128)
+    rng = np.random.default_rng(rows)
+    kc = F.f64_to_e4m3(rng.normal(0, 64, (pool, n_kv, page, D)))
+    vc = F.f64_to_e4m3(rng.uniform(1, 448, (pool, n_kv, page, D)))
+    step = np.repeat(np.arange(pool)[:, None], n_kv, 1)
+    ks, vs = (118 + step // 5).astype(np.uint8), (118 + (step * 3 + np.arange(n_kv)) % 9).astype(np.uint8)
+    dev = [torch.from_numpy(a).to(DEV) for a in (kc, vc, ks, vs)]
+    cache = tp.PagedCache([dev[0].view(E4M3)] * p, [dev[1].view(E4M3)] * p, [dev[2]] * p, [dev[3]] * p)
+    table = np.concatenate([rng.integers(0, pool // 2, pages // 2), rng.integers(0, pool, pages - pages // 2)]).astype(np.int32)
+    batch = tp.PagedBatch(i32([0, 1]), i32([keys]), torch.from_numpy(table[None]).to(DEV), 1)
+    q = to_bf16(rng.normal(size=(1, n_kv * rows * D)))
+    outs = tp.tp_attention_paged_fp8([q] * p, cache, batch, causal=False)
+    tp.tp_device_status()
+    assert all(torch.equal(outs[0], o) for o in outs)
+
+    count = np.bincount(table, minlength=pool)[:, None] * np.ones(page)
+    count[table[-1], keys - (pages - 1) * page:] -= 1
+    count = torch.from_numpy(count.reshape(1, -1)).to(DEV)
+    qf = q.double().view(n_kv, rows, D)
+    K, V = (torch.from_numpy(F.e4m3_to_f64(c) * F.scale_value(s)[:, :, None, None]).to(DEV).transpose(0, 1).reshape(n_kv, -1, D)
+            for c, s in ((kc, ks), (vc, vs)))
+    x = qf @ K.transpose(1, 2) * D ** -0.5                                             # [n_kv, rows, pool * page]
+    d = (qf.abs() @ K.abs().transpose(1, 2) * D ** -0.5) * ((D // 16) * 2.0 ** -22 + 3 * 2.0 ** -24)
+    d = d + 2.0 ** -22 + x.abs().amax(2, keepdim=True) * 2.0 ** -22
+    w = torch.exp(x - x.amax(2, keepdim=True)) * count
+    w = w / w.sum(2, keepdim=True)
+    want = w @ V
+    err = (1.01 * w * d) @ V + want * (2.0 ** -11 + 2.0 ** -7 + 2.0 ** -18) + (1.01 * w * d).sum(2, keepdim=True) * want
+    got = outs[0].double().view(n_kv, rows, D)
+    bad = ~((got - want).abs() <= 2.0 ** -8 * (want + err) + err)
+    assert not bad.any(), (int(bad.sum()), ((got - want) / want)[bad][:5], (got / want - 1).mean())
+
+
+def test_a_part_of_more_than_two_seconds():
+    """A CTA's part of some two and a half seconds in one item, and short items behind it: no wait gives up."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows, pages, page, D = 256 * sms, 1_250_000, 128, 128
+    k = torch.zeros((1, 1, page, D), dtype=torch.uint8, device=DEV).view(E4M3)
+    v = torch.full((1, 1, page, D), 0x38, dtype=torch.uint8, device=DEV).view(E4M3)
+    one = torch.full((1, 1), 127, dtype=torch.uint8, device=DEV)
+    cache = tp.PagedCache([k], [v], [one], [one])
+    batch = tp.PagedBatch(i32([0] + [rows + i for i in range(9)]), i32([pages * page] + [1] * 8),
+                          torch.zeros((9, pages), dtype=torch.int32, device=DEV), rows)
+    q = [torch.ones((rows + 8, D), dtype=BF16, device=DEV)]
+    out, = tp.tp_attention_paged_fp8(q, cache, batch, causal=False)
+    tp.tp_device_status()
+    assert torch.all(out == 1)                   # (every key is worth 1)
