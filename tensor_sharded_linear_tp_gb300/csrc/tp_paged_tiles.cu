@@ -497,10 +497,6 @@ __device__ __forceinline__ void codes_way(const AttendParams& p, TilesCtrl* ctl,
       for (int i = 0; i < 8; ++i)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(raw[i].x), "=r"(raw[i].y), "=r"(raw[i].z), "=r"(raw[i].w)
                      : "r"((src ^ (c * 64)) + i * 8 * D) : "memory");
-      if (c == C - 1) {
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(raw_empty);
-      }
       if (zeros) {
         // Codes that are not there, of NaN pages or behind the last key that is seen (any content): 0.
 #pragma unroll
@@ -522,7 +518,12 @@ __device__ __forceinline__ void codes_way(const AttendParams& p, TilesCtrl* ctl,
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(full + 8 * stage);
+    // The codes are handed back only now that every lane's loads have arrived (the stores needed them).  Handed back when the
+    // loads had been issued, they were overtaken by the next step's box: the MMAs' operands keep loads waiting that long.
+    if (lane == 0) {
+      ptx::mbar_arrive(raw_empty);
+      ptx::mbar_arrive(full + 8 * stage);
+    }
   }
 }
 

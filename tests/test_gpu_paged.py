@@ -921,3 +921,26 @@ def test_a_part_of_more_than_two_seconds():
     out, = tp.tp_attention_paged_fp8(q, cache, batch, causal=False)
     tp.tp_device_status()
     assert torch.all(out == 1)                   # (every key is worth 1)
+
+
+@pytest.mark.parametrize("seqs, p, n_kv, group, D, page", [
+    ([(0, 4608)], 2, 12, 1, 128, 16), ([(20011, 300)], 2, 2, 6, 128, 64), ([(0, 3000)], 2, 12, 1, 64, 32),
+    ([(300 * i, 8) for i in range(1, 17)], 2, 2, 6, 128, 16), ([(200 * i, 1) for i in range(1, 33)], 2, 2, 6, 128, 16),
+    ([(200 * i, 5) for i in range(1, 17)], 2, 2, 6, 128, 16)], ids=["prompt", "chunk", "prompt64", "rows48", "rows6", "rows30"])
+def test_calls_one_after_another(seqs, p, n_kv, group, D, page):
+    """Calls that follow each other without a wait, each with outputs of its own: the bits of a call by itself."""
+    c = Case(seqs, p=p, n_kv=n_kv, group=group, D=D, page=page, seed=41)
+    q = c.queries()
+    alone = tp.tp_attention_paged_fp8(q, c.cache, c.batch)
+    torch.cuda.synchronize()
+    need = tp.tp_attention_paged_workspace_bytes(c.cache, c.batch, c.T, c.heads)
+    spaces = [torch.empty(max(need, 16), dtype=torch.uint8, device=DEV) for _ in range(6)]
+    for _ in range(10):
+        outs = [fresh(q) for _ in spaces]
+        torch.cuda.synchronize()
+        for o, ws in zip(outs, spaces):
+            tp.tp_attention_paged_fp8(q, c.cache, c.batch, outs=o, workspace=ws)
+        torch.cuda.synchronize()
+        for k, o in enumerate(outs):
+            for r in range(p):
+                assert torch.equal(o[r], alone[r]), (k, r, int((o[r] != alone[r]).sum()))
