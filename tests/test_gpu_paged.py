@@ -13,6 +13,7 @@ right code and are compared bit for bit.  The rest is held to bounds made of the
 * the sum over keys: a step of 16 adds without rounding to nearest, 2^-22 of the sum of weights times |v|;
 * the join of parts and the division: 2^-20 relative.
 """
+import ctypes
 import threading
 
 import numpy as np
@@ -944,3 +945,136 @@ def test_calls_one_after_another(seqs, p, n_kv, group, D, page):
         for k, o in enumerate(outs):
             for r in range(p):
                 assert torch.equal(o[r], alone[r]), (k, r, int((o[r] != alone[r]).sum()))
+
+
+@pytest.mark.parametrize("seqs", [[(15, 1), (40, 1), (0, 1)], [(3, 20), (0, 5)]], ids=len)
+def test_append_leaves_queries_alone(seqs):
+    """q_out NULL: K and V are cached, Q is neither read for it nor written."""
+    c = Case(seqs, p=2, n_kv=2, group=3, D=64, page=16, seed=36)
+    qkv = qkv_of(c)
+    before = [t.clone() for t in qkv]
+    cs = torch.from_numpy(quarter_table(c.rng, 60, 32)).to(DEV)
+    at = (ctypes.c_void_p * 2)(*[t.data_ptr() for t in qkv])
+    rope = tp._rope(0, 32, cs.data_ptr(), 0, 60, 0)
+    tp._check(tp.lib.tp_kv_append_fp8(c.cache._struct, c.batch._struct, at, 0, c.T, c.heads, rope, None, 0,
+                                      torch.cuda.current_stream().cuda_stream))
+    codes, scales = c.got()
+    assert all(torch.equal(a, b) for a, b in zip(qkv, before))
+    c.upload()
+    tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch, rope="half", cos_sin=cs)
+    want_codes, want_scales = c.got()
+    for r in range(2):
+        np.testing.assert_array_equal(codes[r], want_codes[r])
+        np.testing.assert_array_equal(scales[r], want_scales[r])
+
+
+@pytest.mark.parametrize("style", ["half", "pairs"])
+def test_append_one_token_at_positions_of_its_own(style):
+    c = Case([(15, 1), (30, 1), (0, 1), (17, 1)], p=2, n_kv=3, group=2, D=64, page=16, seed=37, front=1, behind=1)
+    cs = quarter_table(c.rng, 50, 48)
+    positions = c.rng.integers(0, 50, c.T)
+    positions[0] = positions[-1] = -1            # (rows of no sequence)
+    qkv = qkv_of(c)
+    q_out = [torch.full((c.T, c.heads * c.D), 7.0, dtype=BF16, device=DEV) for _ in range(2)]
+    tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch, rope=style, cos_sin=torch.from_numpy(cs).to(DEV),
+                        positions=i32(positions.tolist()), q_out=q_out)
+    codes, scales = c.got()
+    for r in range(2):
+        q, k, v = split(c, f64(qkv[r]))
+        q, k = P.rotate(q, cs[positions], style), P.rotate(k, cs[positions], style)
+        want = q.reshape(c.T, -1)
+        want[[0, -1]] = 7.0
+        np.testing.assert_array_equal(f64(q_out[r]), want)
+        P.append(c.codes[r][0], c.scales[r][0], k, c.seqs, c.table)
+        P.append(c.codes[r][1], c.scales[r][1], v, c.seqs, c.table)
+        np.testing.assert_array_equal(scales[r], c.scales[r])
+        np.testing.assert_array_equal(F.e4m3_to_f64(codes[r]), F.e4m3_to_f64(c.codes[r]))
+
+
+def test_captured_chunks_follow_the_lengths():
+    """One captured step of up to 40 tokens a sequence (many rows a KV head), replayed with other counts, lengths and pages."""
+    c = Case([(300, 40), (500, 40), (90, 40)], p=2, n_kv=2, group=2, D=64, page=32, seed=38, behind=7)
+    starts, lengths, table = i32([0, 0, 0, 0]), i32([0, 0, 0]), i32(c.table.tolist())
+    batch = tp.PagedBatch(starts, lengths, table, 40)
+    x = [torch.zeros((c.T, (c.heads + 4) * c.D), dtype=BF16, device=DEV) for _ in range(2)]
+    q = [torch.empty((c.T, c.heads * c.D), dtype=BF16, device=DEV) for _ in range(2)]
+    outs = [torch.empty_like(t) for t in q]
+    ws = torch.empty(tp.tp_attention_paged_workspace_bytes(c.cache, batch, c.T, c.heads), dtype=torch.uint8, device=DEV)
+
+    def call():
+        tp.tp_kv_append_fp8(x, c.heads, c.cache, batch, q_out=q)
+        tp.tp_attention_paged_fp8(q, c.cache, batch, outs=outs, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for seqs in ([(0, 3), (17, 40), (80, 1)], [(300, 40), (500, 40), (90, 40)], [(5, 0), (100, 39), (0, 0)]):
+        table.copy_(table[[1, 2, 0]])
+        order = table.cpu().numpy()
+        room = [int((row > 0).sum()) + 1 for row in order]
+        at, new = 2, []
+        for s, (old, n) in enumerate(seqs):
+            old = min(old, 32 * 3 - n) if room[s] < 16 else old
+            new.append((at, n, old + n))
+            at += n
+        c.seqs, c.table = new, order
+        starts.copy_(i32([a for a, _, _ in new] + [at]))
+        lengths.copy_(i32([n for _, _, n in new]))
+        for t in x:
+            t.copy_(to_bf16(c.rng.normal(size=t.shape)))
+        for t in q + outs:
+            t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        tp.tp_device_status()
+        c.q, (c.codes, c.scales) = q, c.got()
+        for r in range(2):
+            owned = np.concatenate([np.arange(a, a + n) for a, n, _ in new]).astype(int)
+            want = np.full((c.T, c.heads * c.D), 7.0)
+            want[owned] = f64(x[r])[owned, :c.heads * c.D]
+            np.testing.assert_array_equal(f64(q[r]), want)
+        c.check(outs, before=fresh(q), what=seqs)
+
+
+def test_no_pages_at_all():
+    """An empty page table, and a cache without pages: no row sees a key; a length that claims some is reported."""
+    c = Case([(0, 3), (0, 50)], p=1, n_kv=2, group=2, D=64, page=16, seed=39)
+    q = c.queries()
+    none = tp.PagedBatch(c.batch.seq_start, i32([0, 0]), torch.empty((2, 0), dtype=torch.int32, device=DEV), 50)
+    small = tp.PagedBatch(i32([0, 3, 3]), i32([0, 0]), torch.empty((2, 0), dtype=torch.int32, device=DEV), 3)
+    for batch, rows in ((none, 53), (small, 3)):
+        outs = fresh(q)
+        tp.tp_attention_paged_fp8(q, c.cache, batch, outs=outs, window=5)
+        tp.tp_device_status()
+        assert torch.all(outs[0][:rows] == 0) and torch.all(outs[0][rows:] == 7)
+    k = torch.empty((0, 2, 16, 64), dtype=E4M3, device=DEV)
+    s = torch.empty((0, 2), dtype=E8M0, device=DEV)
+    empty = tp.PagedCache([k], [k], [s], [s])
+    for batch in (c.batch, tp.PagedBatch(i32([0, 3, 3]), i32([3, 0]), c.batch.page_table, 3)):
+        outs = tp.tp_attention_paged_fp8(q, empty, batch)
+        with pytest.raises(tp.TPError, match="TP_ERR_INVALID_ARG"):
+            tp.tp_device_status()
+        assert torch.all(outs[0][:3] == 0)
+        tp.tp_kv_append_fp8(qkv_of(c), c.heads, empty, batch)
+        with pytest.raises(tp.TPError, match="TP_ERR_INVALID_ARG"):
+            tp.tp_device_status()
+
+
+@pytest.mark.parametrize("max_new", [2, 5, 17, 200])
+def test_more_rows_allowed_than_there_are(max_new):
+    """max_new chooses the kernel; any bound has the same answers."""
+    c = Case([(700, 1), (33, 2), (0, 1), (2000, 1)], p=2, n_kv=2, group=3, D=128, page=16, seed=40, behind=2)
+    c.batch = c.make_batch(max_new)
+    qkv = qkv_of(c)
+    q = tp.tp_kv_append_fp8(qkv, c.heads, c.cache, c.batch)
+    c.q, (codes, scales) = q, c.got()
+    for r in range(2):
+        _, k, v = split(c, f64(qkv[r]))
+        P.append(c.codes[r][0], c.scales[r][0], k, c.seqs, c.table)
+        P.append(c.codes[r][1], c.scales[r][1], v, c.seqs, c.table)
+        np.testing.assert_array_equal(scales[r], c.scales[r])
+        np.testing.assert_array_equal(F.e4m3_to_f64(codes[r]), F.e4m3_to_f64(c.codes[r]))
+    outs = fresh(q)
+    tp.tp_attention_paged_fp8(q, c.cache, c.batch, outs=outs)
+    c.check(outs, before=fresh(q))
