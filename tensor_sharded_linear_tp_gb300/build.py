@@ -11,6 +11,7 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -24,6 +25,8 @@ LIB_PATH = os.path.join(HERE, "libtp.so")
 SOURCES = ["tp_host.cu", "tp_copy.cu", "tp_gemm.cu", "tp_attention.cu", "tp_flash.cu", "tp_quant.cu", "tp_fp8.cu",
            "tp_kv_append.cu", "tp_paged_attention.cu", "tp_paged_tiles.cu", "tp_safetensors.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+# Kernels whose warpgroups share the block's registers out among themselves: the launch has to have this many a thread.
+REGISTERS = {"tp_paged_tiles.cu": ("paged_tiles_kernel", 128)}
 
 
 def nvcc_path() -> str:
@@ -51,6 +54,16 @@ def up_to_date() -> bool:
     return os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= _newest_input_mtime()
 
 
+def check_registers(src: str, log: str) -> None:
+    """Raise unless ptxas gave every instance of the source's kernel the registers that its split adds up to."""
+    if src not in REGISTERS:
+        return
+    kernel, want = REGISTERS[src]
+    used = re.findall(r"Compiling entry function '[^']*" + kernel + r"[^']*'.*?Used (\d+) registers", log, re.S)
+    if not used or any(int(n) != want for n in used):
+        raise RuntimeError(f"{src}: {kernel} needs {want} registers a thread, ptxas gave {used or 'no report'}")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libtp.so if any source is newer than it; return its path."""
     if not force and up_to_date():
@@ -61,10 +74,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_one(src: str) -> tuple[str, str]:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
-        cmd = [nvcc, *flags, "-c", os.path.join(CSRC, src), "-o", obj]
+        report = [] if verbose or src not in REGISTERS else ["-Xptxas", "-v"]
+        cmd = [nvcc, *flags, *report, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        check_registers(src, r.stdout + r.stderr)
         return obj, r.stdout + r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:

@@ -233,3 +233,18 @@ def test_a_batchs_rows_have_two_names():
     for args, kw in (((), {}), ((1,), dict(max_q=1)), ((), dict(max_new=1, max_q=1))):
         with pytest.raises(TypeError, match="max_q"):
             tp.PagedBatch(i32[0], i32[0, :1], i32, *args, **kw)
+
+
+def test_the_build_checks_the_registers_of_a_split_kernel():
+    """The many-rows kernel's warpgroups share 128 registers a thread out; a build that has others is refused."""
+    from tensor_sharded_linear_tp_gb300 import build
+
+    def log(n, m):
+        entry = ("ptxas info    : Compiling entry function '_ZN2tp18paged_tiles_kernelILi{}EEEv' for 'sm_103a'\n    0 bytes stack frame\n"
+                 "ptxas info    : Used {} registers, used 1 barriers\n")
+        return entry.format(64, n) + entry.format(128, m) + entry.replace("tiles", "join").format(64, 60)
+    build.check_registers("tp_paged_tiles.cu", log(128, 128))
+    build.check_registers("tp_gemm.cu", log(40, 40))
+    for text in (log(128, 120), log(96, 128), ""):
+        with pytest.raises(RuntimeError, match="128 registers"):
+            build.check_registers("tp_paged_tiles.cu", text)
