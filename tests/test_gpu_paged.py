@@ -1078,3 +1078,46 @@ def test_more_rows_allowed_than_there_are(max_new):
     outs = fresh(q)
     tp.tp_attention_paged_fp8(q, c.cache, c.batch, outs=outs)
     c.check(outs, before=fresh(q))
+
+
+@pytest.mark.parametrize("seqs, new, p, n_kv, group, D, page", [
+    ([90 + 7 * i for i in range(40)], 1, 2, 4, 3, 128, 16), ([700, 0, 33], 70, 2, 4, 2, 128, 64), ([900, 5], 40, 2, 4, 2, 64, 32)],
+    ids=["tokens", "chunks", "chunks64"])
+def test_steps_one_after_another(seqs, new, p, n_kv, group, D, page):
+    """Appends and attentions that follow each other without a wait, tokens growing so that scales change at every step: the
+    bits of the same steps with a wait after each call."""
+    steps = 24
+    c = Case([(old, new) for old in seqs], p=p, n_kv=n_kv, group=group, D=D, page=page, seed=42, spare=sum(-(-new * steps // page) + 1 for _ in seqs))
+    used = c.table.copy()
+    free = sorted(set(range(c.n_pages)) - {int(x) for s, (_, _, n) in enumerate(c.seqs) for x in used[s, :-(-n // page)]})
+    need = [-(-(old + new * steps) // page) for old in seqs]
+    c.table = np.zeros((len(seqs), max(need)), dtype=np.int32)
+    for s, (_, _, n) in enumerate(c.seqs):
+        have = -(-n // page)
+        c.table[s, :have] = used[s, :have]
+        for i in range(have, need[s]):
+            c.table[s, i] = free.pop()
+    x = [[to_bf16(c.rng.normal(size=(c.T, (c.heads + 2 * n_kv) * D)) * 1.3 ** k) for _ in range(p)] for k in range(steps)]
+    cs = torch.from_numpy(quarter_table(c.rng, max(seqs) + new * steps + 1, D)).to(DEV)
+    starts, table = i32([new * s for s in range(len(seqs) + 1)]), i32(c.table.tolist())
+    batches = [tp.PagedBatch(starts, i32([old + new * (k + 1) for old in seqs]), table, new) for k in range(steps)]
+    results = []
+    for wait in (True, False, False, False):
+        c.upload()
+        torch.cuda.synchronize()
+        outs = []
+        for k in range(steps):
+            q = tp.tp_kv_append_fp8(x[k], c.heads, c.cache, batches[k], rope="half", cos_sin=cs)
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(tp.tp_attention_paged_fp8(q, c.cache, batches[k]))
+            if wait:
+                torch.cuda.synchronize()
+        codes, scales = c.got()
+        results.append(([t for o in outs for t in o], codes, scales))
+    for got in results[1:]:
+        for i, (a, b) in enumerate(zip(results[0][0], got[0])):
+            assert torch.equal(a, b), (i // p, i % p, int((a != b).sum()))
+        for r in range(p):
+            np.testing.assert_array_equal(results[0][1][r], got[1][r])
+            np.testing.assert_array_equal(results[0][2][r], got[2][r])
