@@ -12,9 +12,9 @@
 //
 // What bounds it: the bytes (Q, K and V read once as bf16, Q written, K and V as bytes), and close behind them the
 // instructions: 14 an element of K and V.  A prompt of 4608 tokens, 4 ranks of 12 heads and 12 KV heads of 128
-// (283 MB) takes 67 us, 0.63 of the copy rate (the pages' part 58 us alone, Q's 21; a warp loads its 16 tokens, waits, and needs
+// (283 MB) takes 66 us, 0.64 of the copy rate (the pages' part 58 us alone, Q's 21; a warp loads its 16 tokens, waits, and needs
 // their maximum before it can write: three CTAs an SM hide part of that).  Small calls are a launch: one token of 4
-// ranks 3.3 us, a batch of 61 3.6 us, 7 chunks of odd lengths (21 MB) 8.5 us, against 3.1 of their bytes.
+// ranks 3.1 us, a batch of 61 3.5 us, 7 chunks of odd lengths (21 MB) 8.6 us, against 3.1 of their bytes.
 //
 // Which sequence and page a block has comes from the device's seq_start without a prefix sum
 // (find_sequence), so that lengths may change between the replays of a graph.
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_con
     rotate_q<D>(p, static_cast<int64_t>(block - pages) * kWarps + (threadIdx.x >> 5), threadIdx.x & 31);
 }
 
-// One new token a sequence at most (decoding; 61 sequences 3.6 us, 6.7 by the kernel above, whose blocks are for 16
+// One new token a sequence at most (decoding; 61 sequences 3.5 us, 6.7 by the kernel above, whose blocks are for 16
 // tokens and more): a warp takes kTokenRounds rounds of a token's heads, Q's,
 // K's and V's alike, a head held by kParts threads.  No page is shared by two tokens here, so no block has
 // to meet.

@@ -8,7 +8,7 @@
 // their way.  Measured: 64 sequences of 50 to 8000 tokens, 8 KV heads of 6 query heads (569 MB) in 116 us, 0.72 of the
 // copy rate (queueing and prologues take some 10 us, the last CTAs 10, the join 6); one sequence of 131000
 // tokens 59 us, 0.67.  From 17 rows on it is the warps' own latency that bounds (eight of them an SM):
-// 16 sequences 57 us with 12 rows, 65 with 18, 88 with 30, where the bytes take 24.
+// 16 sequences 57 us with 12 rows, 67 with 18, 90 with 30, where the bytes take 24.
 //
 // * All keys of all items are one line of steps of 32 keys, cut into equal parts for the CTAs, and each
 //   of them into equal parts for its warps.  Sequences of any lengths load the GPU evenly,
@@ -17,7 +17,7 @@
 //   workspace by a second launch, always in key order (no atomics).
 // * A warp has a ring of steps of its own in shared memory, filled by its own asynchronous copies (swizzled so
 //   that the loads below meet no bank twice; TMA's boxes of a page each took its issuing lane 700 to 1400
-//   cycles a step: 128 us for the 64 sequences, not 109 to 116) and drained by itself: no barrier between warps.  What
+//   cycles a step: 128 us for the 64 sequences, not 116) and drained by itself: no barrier between warps.  What
 //   bounds a warp is the latency of its own instructions (some 1700 cycles a step at 8 rows), so an SM has as
 //   many as their registers and rings allow.
 // * The products are S^T = K Q^T and O^T = V^T P^T on mma.sync m16n8k16 (keys, then head elements,
@@ -792,9 +792,9 @@ Plan make_plan(const tp_paged_cache& c, const tp_paged_batch& b, int group, int 
   Plan pl{};
   const int64_t rows = static_cast<int64_t>(b.max_new) * group;
   // The fewest row tiles that hold them: one tile on the kernel for two takes 138 us, not 116 (64 sequences of 6 rows),
-  // 12 rows on four 261, not 152, and 18 on four 90, not 65 (16 sequences).  The other kernel, whose time does not
-  // depend on the rows, takes 101 us where 30 rows of 16 sequences take 88, 319 for 273 of 64, 104 for 107 of 2 of
-  // 60000 keys, but 40 for 46 of 4 of up to 9000.
+  // 12 rows on four 261, not 152, and 18 on four 90, not 67 (16 sequences).  The other kernel, whose time hardly
+  // depends on the rows, takes 104 us where 30 rows of 16 sequences take 90, 102 for 67 with 18 rows and 57 with 12,
+  // 300 for 116 of the 64 sequences, but 40 for 46 with 30 rows of 4 sequences of up to 9000.
   pl.tiles = rows > 32;
   pl.row_tiles = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4;
   const int64_t items = static_cast<int64_t>(b.n_seqs) * c.n_ranks * c.n_kv_heads;

@@ -37,9 +37,10 @@
 // products take 2048 cycles of the tensor core, its exponentials 1024 of an SM's rate, and measured it takes
 // 4300 (D 128): a stream's softmax is some 1700 cycles from S to P, in turn with the other's, on schedulers that also
 // convert the codes (without the softmax's arithmetic a chunk took 158 us, not 222; the epilogue and Q's loads are 3 and 5 %).  A
-// prompt of 4608 tokens, 48 heads: 331 us, 788 TFLOP/s, 0.41 of the measured bf16 rate (135 us); a chunk of 300 tokens,
+// prompt of 4608 tokens, 48 heads: 330 us, 790 TFLOP/s, 0.41 of the measured bf16 rate (135 us); a chunk of 300 tokens,
 // 48 query on 8 KV heads, over 30011: 222 us, 0.52 (115 us).  With at most 128 rows each stream has steps of its own, and what bounds them
-// is the one step of codes that fits beside the fp16 tiles: 2.6 us for 128 keys.
+// is the one step of codes that fits beside the fp16 tiles: 2.6 us for 128 keys (48 rows of 16 sequences 104 us, where the
+// bytes take 24).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
